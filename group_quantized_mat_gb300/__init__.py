@@ -27,15 +27,20 @@ F32_OUT = 0x1
 FORCE_M1_PER_COLUMN = 0x2
 PDL = 0x4
 SB_INTERLEAVED = 0x8
+MOE_GELU = 0x10
+MOE_SOFTMAX_ALL = 0x20
+VERIFY_F32_LOGITS = 0x40
 
 STATUS = {
     0: "QMV_OK", 1: "QMV_ERR_NULL", 2: "QMV_ERR_BITS", 3: "QMV_ERR_GROUP", 4: "QMV_ERR_SHAPE",
     5: "QMV_ERR_M_RANGE", 6: "QMV_ERR_ALIGN", 7: "QMV_ERR_CUDA", 8: "QMV_ERR_WORKSPACE",
     9: "QMV_ERR_VALUE", 10: "QMV_ERR_FLAGS",
+    11: "QMV_ERR_COUNT",
 }
 
 EXPORTED = ("qmv_packed_words", "qmv_pack", "qmv_unpack", "qmv_pack_sb", "qmv_split_count", "qmv_workspace_size",
-            "qmv_run", "qmv_run_ex", "qmv_run_noalloc", "qmv_mxfp4_run", "qmv_workspace_init", "qmv_device_error", "qmv_last_cuda_error",
+            "qmv_run", "qmv_run_ex", "qmv_run_noalloc", "qmv_mxfp4_run", "qmv_workspace_init", "qmv_lora_workspace_size", "qmv_lora_run",
+            "qmv_moe_workspace_size", "qmv_moe_run", "qmv_verify_workspace_size", "qmv_verify_run", "qmv_device_error", "qmv_last_cuda_error",
             "qmv_status_string")
 
 
@@ -83,6 +88,18 @@ def load(path: str | None = None) -> ctypes.CDLL:
         lib.qmv_run_noalloc.argtypes = [P, P, P, P, P, I, I, I, I, I, P]
         lib.qmv_mxfp4_run.restype = I
         lib.qmv_mxfp4_run.argtypes = [P, P, P, P, I, I, I, U, P]
+        lib.qmv_lora_workspace_size.restype = SZ
+        lib.qmv_lora_workspace_size.argtypes = [I] * 6
+        lib.qmv_lora_run.restype = I
+        lib.qmv_lora_run.argtypes = [P] * 9 + [I] * 7 + [P, SZ, U, P]
+        lib.qmv_moe_workspace_size.restype = SZ
+        lib.qmv_moe_workspace_size.argtypes = [I] * 7
+        lib.qmv_moe_run.restype = I
+        lib.qmv_moe_run.argtypes = [P] * 11 + [I] * 7 + [P, SZ, U, P]
+        lib.qmv_verify_workspace_size.restype = SZ
+        lib.qmv_verify_workspace_size.argtypes = [I] * 3
+        lib.qmv_verify_run.restype = I
+        lib.qmv_verify_run.argtypes = [P] * 10 + [I] * 3 + [I64] * 3 + [P, SZ, U, P]
         lib.qmv_workspace_init.restype = I
         lib.qmv_workspace_init.argtypes = [P, SZ, P]
         lib.qmv_device_error.restype = I
@@ -203,6 +220,54 @@ def qmv_mxfp4_run(w_q, scales, x, y, M: int, N: int, K: int, flags: int = 0, str
     uint8 E8M0 scales [N, K/32]); see include/qmv.h."""
     code = load().qmv_mxfp4_run(_ptr(w_q), _ptr(scales), _ptr(x), _ptr(y), M, N, K, int(flags), _stream(stream))
     _check(code, "qmv_mxfp4_run")
+
+
+# ------------------------------------------- operators of a decode step --
+def qmv_lora_workspace_size(M: int, N: int, K: int, bits: int, group_size: int, rank: int) -> int:
+    return int(load().qmv_lora_workspace_size(M, N, K, bits, group_size, rank))
+
+
+def qmv_lora_run(w_q, scales, biases, x, lora_a, lora_b, adapter, lora_scale, y, M: int, N: int, K: int, bits: int,
+                 group_size: int, adapters: int, rank: int, workspace=None, workspace_bytes: int = 0, flags: int = 0,
+                 stream=None) -> None:
+    """y[M, N] = W x + scale_a B_a (A_a x) with each vector's own adapter a, enqueued on ``stream``; see include/qmv.h."""
+    code = load().qmv_lora_run(_ptr(w_q), _ptr(scales), _ptr(biases), _ptr(x), _ptr(lora_a), _ptr(lora_b),
+                               _ptr(adapter), _ptr(lora_scale), _ptr(y), M, N, K, bits, group_size, adapters, rank,
+                               _ptr(workspace), workspace_bytes, flags, _stream(stream))
+    _check(code, "qmv_lora_run")
+
+
+def qmv_moe_workspace_size(M: int, K: int, inter: int, experts: int, top_k: int, bits: int, group_size: int) -> int:
+    return int(load().qmv_moe_workspace_size(M, K, inter, experts, top_k, bits, group_size))
+
+
+def qmv_moe_run(x, router, gu_w, gu_scales, gu_biases, dn_w, dn_scales, dn_biases, y, topk_ids, topk_weights, M: int,
+                K: int, inter: int, experts: int, top_k: int, bits: int, group_size: int, workspace=None,
+                workspace_bytes: int = 0, flags: int = 0, stream=None) -> None:
+    """y[M, K] of a whole mixture-of-experts layer, and the routing if ``topk_ids`` / ``topk_weights`` are given."""
+    code = load().qmv_moe_run(_ptr(x), _ptr(router), _ptr(gu_w), _ptr(gu_scales), _ptr(gu_biases), _ptr(dn_w),
+                              _ptr(dn_scales), _ptr(dn_biases), _ptr(y), _ptr(topk_ids), _ptr(topk_weights), M, K,
+                              inter, experts, top_k, bits, group_size, _ptr(workspace), workspace_bytes, flags,
+                              _stream(stream))
+    _check(code, "qmv_moe_run")
+
+
+def qmv_verify_workspace_size(B: int, S: int, V: int) -> int:
+    return int(load().qmv_verify_workspace_size(B, S, V))
+
+
+def qmv_verify_run(target, draft, draft_tokens, draft_len, temperature, uniform, noise, tokens, accepted, logprob,
+                   B: int, S: int, V: int, ld_target: int | None = None, ld_draft: int | None = None,
+                   ld_noise: int | None = None, workspace=None, workspace_bytes: int = 0, flags: int = 0,
+                   stream=None) -> None:
+    """Accepted prefix of the drafted tokens, the token after it and their log-probabilities; see include/qmv.h.
+    The row strides default to V."""
+    code = load().qmv_verify_run(_ptr(target), _ptr(draft), _ptr(draft_tokens), _ptr(draft_len), _ptr(temperature),
+                                 _ptr(uniform), _ptr(noise), _ptr(tokens), _ptr(accepted), _ptr(logprob), B, S, V,
+                                 V if ld_target is None else ld_target, V if ld_draft is None else ld_draft,
+                                 V if ld_noise is None else ld_noise, _ptr(workspace), workspace_bytes, flags,
+                                 _stream(stream))
+    _check(code, "qmv_verify_run")
 
 
 def qmv_workspace_init(workspace, nbytes: int, stream=None) -> None:

@@ -513,6 +513,28 @@ qmv_status check_run_args(const void *w_q, const void *scales, const void *biase
 
 qmv_status record_cuda_failure(const char *what, cudaError_t e) { return cuda_fail(what, e); }
 
+qmv_status check_weights(int M, int N, int K, int bits, int gs) { return check_shape(M, N, K, bits, gs, true); }
+
+qmv_status current_device(DeviceInfo *out)
+{
+    cudaError_t ce = cudaGetDevice(&out->dev);
+    if (ce != cudaSuccess) return cuda_fail("cudaGetDevice", ce);
+    if (out->dev >= kMaxDevices) return cuda_fail("device index >= 64", cudaErrorInvalidDevice);
+    qmv_status st = sm_count(out->dev, &out->sms);
+    if (st != QMV_OK) return st;
+    return device_error_ptr(out->dev, &out->err);
+}
+
+qmv_status scratch(const DeviceInfo &d, size_t need, void *given, size_t given_bytes, void **out)
+{
+    if (given) {
+        if (given_bytes < need) return QMV_ERR_WORKSPACE;
+        *out = given;
+        return QMV_OK;
+    }
+    return library_workspace(d.dev, need, out);
+}
+
 }  // namespace qmv
 
 namespace {
@@ -712,6 +734,7 @@ extern "C" const char *qmv_status_string(qmv_status s)
         case QMV_ERR_WORKSPACE: return "QMV_ERR_WORKSPACE: workspace smaller than qmv_workspace_size()";
         case QMV_ERR_VALUE: return "QMV_ERR_VALUE: a quantized value does not fit in `bits` bits";
         case QMV_ERR_FLAGS: return "QMV_ERR_FLAGS: unknown flag bits";
+        case QMV_ERR_COUNT: return "QMV_ERR_COUNT: a count (adapters, rank, experts, top_k, batch, drafts) out of range";
     }
     return "unknown qmv_status";
 }

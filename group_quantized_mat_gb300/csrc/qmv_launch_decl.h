@@ -47,6 +47,17 @@ qmv_status check_run_args(const void *w_q, const void *scales, const void *biase
                           int M, int N, int K, int bits, int gs, const void *workspace, unsigned flags);
 qmv_status record_cuda_failure(const char *what, cudaError_t e);
 
+// What the operators' host sides share with the mat-vec's: the checks of a
+// packed matrix and M, the current device with its SM count and error word,
+// and a call's scratch (the caller's if given, else the library workspace).
+struct DeviceInfo {
+    int dev = 0, sms = 0;
+    unsigned *err = nullptr;
+};
+qmv_status check_weights(int M, int N, int K, int bits, int gs);
+qmv_status current_device(DeviceInfo *out);
+qmv_status scratch(const DeviceInfo &d, size_t need, void *given, size_t given_bytes, void **out);
+
 // One launch for V = 1..16 vectors (qmv_mx.cu).
 cudaError_t launch_mxfp4(int V, const MxParams &p, cudaStream_t stream);
 

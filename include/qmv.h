@@ -58,7 +58,9 @@ typedef enum qmv_status {
     QMV_ERR_CUDA = 7,       /* a CUDA runtime call failed (launch, device query, encode)   */
     QMV_ERR_WORKSPACE = 8,  /* workspace is smaller than qmv_workspace_size()              */
     QMV_ERR_VALUE = 9,      /* qmv_pack: an input value does not fit in `bits` bits        */
-    QMV_ERR_FLAGS = 10      /* unknown bits set in `flags`                                 */
+    QMV_ERR_FLAGS = 10,     /* unknown bits set in `flags`                                 */
+    QMV_ERR_COUNT = 11      /* a count (adapters, rank, experts, top_k, batch, drafted
+                               tokens) is outside its range                               */
 } qmv_status;
 
 /* The CUDA stream type (identical to cudaStream_t; 0 is the legacy default stream). */
@@ -274,6 +276,150 @@ QMV_API qmv_status qmv_run_noalloc(const uint32_t *w_q, const uint16_t *scales, 
  * The host checks run before anything is launched. */
 QMV_API qmv_status qmv_mxfp4_run(const uint32_t *w_q, const uint8_t *scales, const uint16_t *x, void *y,
                                  int M, int N, int K, unsigned flags, qmv_stream_t stream);
+
+/* ------------------------------------------- operators of a decode step -- */
+
+/* The operators below stand next to the mat-vec in one step of speculative
+ * decoding, where a few drafted tokens go through a model at once: a projection
+ * with each request's own low-rank adapter, a whole mixture-of-experts layer,
+ * and the verification of the drafted tokens. They share these rules:
+ *
+ *  workspace        device, 16-byte aligned, at least the operator's
+ *                   ..._workspace_size() bytes, or NULL to use the library
+ *                   workspace of qmv_run (grown in the same way, with the same
+ *                   warning about stream capture and overlapping calls).
+ *                   Scratch only: no particular contents are needed or kept.
+ *  workspace_bytes  its size (ignored when workspace is NULL).
+ *  flags            bitwise OR of the flags each operator names.
+ *
+ * A call returns after enqueueing on `stream`. All checks of arguments run on
+ * the host before anything is launched. Outputs must not overlap inputs. */
+
+/* Low-rank adapters of many requests at once beside a shared projection:
+ *
+ *   y[m, n] = sum_i ( s[n, i/gs] q[n, i] + b[n, i/gs] ) x[m, i]
+ *             + c[a] sum_r B[a, n, r] ( sum_i A[a, r, i] x[m, i] ),   a = adapter[m]
+ *
+ *  w_q, scales, biases, x, y, M, N, K, bits, group_size   as for qmv_run.
+ *  lora_a      device, bf16 [adapters, rank, K], 16-byte aligned.
+ *  lora_b      device, bf16 [adapters, N, rank], 16-byte aligned.
+ *  adapter     device, int32 [M]: the adapter of each vector. A value outside
+ *              [0, adapters) means none: that vector gets the projection alone.
+ *  lora_scale  device, float [adapters]: c.
+ *  adapters    1 .. QMV_MAX_ADAPTERS.  rank 1 .. QMV_MAX_RANK (adapters of lower
+ *              rank are padded with zeros).
+ *  flags       QMV_F32_OUT.
+ *
+ * Arithmetic: the products and sums of both terms are fp32 (the group's
+ * factored form, as for qmv_run, but summed by the tensor cores in another fixed
+ * order), the inner vector A x is kept in fp32, and the sum of the two terms is
+ * rounded once. A vector's result does not depend on the other vectors of the
+ * call: it is bit-identical to an M = 1 call on that vector.
+ *
+ * Errors: QMV_ERR_NULL, QMV_ERR_BITS, QMV_ERR_GROUP, QMV_ERR_SHAPE,
+ * QMV_ERR_M_RANGE, QMV_ERR_COUNT, QMV_ERR_FLAGS, QMV_ERR_ALIGN (also for
+ * adapter and lora_scale off their 4 bytes), QMV_ERR_WORKSPACE, QMV_ERR_CUDA. */
+#define QMV_MAX_ADAPTERS 65536
+#define QMV_MAX_RANK 256
+QMV_API size_t qmv_lora_workspace_size(int M, int N, int K, int bits, int group_size, int rank);
+QMV_API qmv_status qmv_lora_run(const uint32_t *w_q, const uint16_t *scales, const uint16_t *biases, const uint16_t *x,
+                                const uint16_t *lora_a, const uint16_t *lora_b, const int32_t *adapter,
+                                const float *lora_scale, void *y, int M, int N, int K, int bits, int group_size,
+                                int adapters, int rank, void *workspace, size_t workspace_bytes, unsigned flags,
+                                qmv_stream_t stream);
+
+/* A whole mixture-of-experts layer for a few tokens. With l = router x:
+ *
+ *   ids     = the top_k experts of largest l (the lower index first among equals),
+ *   weights = softmax of l over those top_k (or, with QMV_MOE_SOFTMAX_ALL, over all experts),
+ *   h_e     = act(gate_e x) * (up_e x),
+ *   y       = sum over e in ids of weights_e down_e h_e
+ *
+ * where act is silu, or gelu in its tanh form with QMV_MOE_GELU, and gate_e,
+ * up_e and down_e are group-quantized as for qmv_run.
+ *
+ *  x                 device, bf16 [M, K], 16-byte aligned.
+ *  router            device, bf16 [experts, K], 16-byte aligned.
+ *  gu_w              device, uint32 [experts, 2 inter, K*bits/32]: rows 0 .. inter-1 of
+ *                    an expert are gate_e, rows inter .. 2 inter-1 are up_e.
+ *  gu_scales/biases  device, bf16 [experts, 2 inter, K/group_size].
+ *  dn_w              device, uint32 [experts, K, inter*bits/32]: down_e.
+ *  dn_scales/biases  device, bf16 [experts, K, inter/group_size].
+ *                    All six 16-byte aligned.
+ *  y                 device, bf16 [M, K] (fp32 with QMV_F32_OUT).
+ *  topk_ids          device, int32 [M, top_k], or NULL: ids, the largest first.
+ *  topk_weights      device, float [M, top_k], or NULL: weights, in the same order.
+ *  M                 1 .. QMV_MAX_M.  K and inter multiples of group_size.
+ *  experts           1 .. QMV_MAX_EXPERTS.  top_k 1 .. min(experts, QMV_MAX_TOP_K).
+ *  flags             QMV_F32_OUT, QMV_MOE_GELU, QMV_MOE_SOFTMAX_ALL.
+ *
+ * A NaN router logit counts as -inf. Arithmetic: fp32 sums throughout; h is
+ * rounded to the nearest 16 bits of significand between the two products; y is
+ * rounded once. A token's result does not depend on the other tokens of the call.
+ *
+ * Errors: as for qmv_lora_run; QMV_ERR_SHAPE also when inter is not a multiple of
+ * group_size or experts x rows x groups reaches 2^31. */
+#define QMV_MAX_EXPERTS 1024
+#define QMV_MAX_TOP_K 32
+#define QMV_MOE_GELU 0x10u
+#define QMV_MOE_SOFTMAX_ALL 0x20u
+QMV_API size_t qmv_moe_workspace_size(int M, int K, int inter, int experts, int top_k, int bits, int group_size);
+QMV_API qmv_status qmv_moe_run(const uint16_t *x, const uint16_t *router, const uint32_t *gu_w,
+                               const uint16_t *gu_scales, const uint16_t *gu_biases, const uint32_t *dn_w,
+                               const uint16_t *dn_scales, const uint16_t *dn_biases, void *y, int32_t *topk_ids,
+                               float *topk_weights, int M, int K, int inter, int experts, int top_k, int bits,
+                               int group_size, void *workspace, size_t workspace_bytes, unsigned flags,
+                               qmv_stream_t stream);
+
+/* Verification of drafted tokens against the target's probabilities, from given
+ * random numbers (speculative sampling: what is emitted is distributed as the
+ * target's own samples). For a sequence b with L = draft_len[b] drafted tokens x_i,
+ * and p_i, q_i the softmax of target row i and draft row i over temperature[b]:
+ *
+ *   drafted token i is accepted while  uniform[b, i] q_i(x_i) < p_i(x_i);
+ *   after n accepted tokens one more is emitted, the v that maximises
+ *     max(p_n(v) - q_n(v), 0) / noise[b, v]   if n < L (p_n where that is 0 for every v),
+ *     p_n(v) / noise[b, v]                    if n = L,
+ *   the lowest v among equals.
+ *
+ * With noise from the exponential distribution that v is a sample of the
+ * normalised numerator. Where temperature[b] is not above 0, a drafted token is
+ * accepted while it is the argmax of its target row, and the argmax of row n is
+ * emitted (the lowest index among equals); uniform, noise and draft are not used.
+ *
+ *  target        device, bf16 logits (fp32 with QMV_VERIFY_F32_LOGITS) [B, S+1, ld_target].
+ *  draft         device, logits of the same type [B, S, ld_draft], or NULL where the
+ *                drafts were not sampled: q_i is then 1 at x_i and 0 elsewhere.
+ *  draft_tokens  device, int32 [B, S]. One outside [0, V) is never accepted.
+ *  draft_len     device, int32 [B], or NULL (S for all); taken into [0, S].
+ *  temperature   device, float [B], or NULL (1 for all).
+ *  uniform       device, float [B, S], in [0, 1).
+ *  noise         device, float [B, ld_noise], positive; below the smallest normal
+ *                number it counts as that.
+ *  tokens        device, int32 [B, S+1]: the accepted tokens, the one after them, then -1.
+ *  accepted      device, int32 [B]: n.
+ *  logprob       device, float [B, S+1], or NULL: the log of each emitted token's p
+ *                (at temperature 1 where argmax is taken), 0 where tokens holds -1.
+ *  B             1 .. QMV_MAX_BATCH.  S 0 .. QMV_MAX_DRAFT (with S = 0 the pointers
+ *                draft, draft_tokens and uniform are not used).  V 1 .. 2^24.
+ *  ld_*          elements from row to row, at least V.
+ *  flags         QMV_VERIFY_F32_LOGITS.
+ *
+ * A logit of -inf or NaN is never emitted or accepted; +inf counts as the type's
+ * largest finite value. A row with no other logits emits -1, with logprob -inf.
+ * Pointers need their element's alignment only.
+ *
+ * Errors: QMV_ERR_NULL, QMV_ERR_COUNT, QMV_ERR_SHAPE (V or an ld), QMV_ERR_FLAGS,
+ * QMV_ERR_ALIGN, QMV_ERR_WORKSPACE, QMV_ERR_CUDA. */
+#define QMV_MAX_BATCH 65535
+#define QMV_MAX_DRAFT 63
+#define QMV_VERIFY_F32_LOGITS 0x40u
+QMV_API size_t qmv_verify_workspace_size(int B, int S, int V);
+QMV_API qmv_status qmv_verify_run(const void *target, const void *draft, const int32_t *draft_tokens,
+                                  const int32_t *draft_len, const float *temperature, const float *uniform,
+                                  const float *noise, int32_t *tokens, int32_t *accepted, float *logprob, int B,
+                                  int S, int V, int64_t ld_target, int64_t ld_draft, int64_t ld_noise,
+                                  void *workspace, size_t workspace_bytes, unsigned flags, qmv_stream_t stream);
 
 /* Zero-fills `bytes` of a caller workspace on `stream` (cudaMemsetAsync). Calls
  * do not need it (a workspace holds no state between calls); kept as a
