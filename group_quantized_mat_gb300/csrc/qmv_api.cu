@@ -525,6 +525,26 @@ qmv_status current_device(DeviceInfo *out)
     return device_error_ptr(out->dev, &out->err);
 }
 
+qmv_status encode_rows(CUtensorMap *map, const void *w, long long row_bytes, long long rows, int box_elems,
+                       int box_rows)
+{
+    auto fn = encode_fn();
+    int r = -1;
+    if (fn) {
+        const cuuint64_t dims[2] = {cuuint64_t(row_bytes / 8), cuuint64_t(rows)};
+        const cuuint64_t strides[1] = {cuuint64_t(row_bytes)};
+        const cuuint32_t box[2] = {cuuint32_t(box_elems), cuuint32_t(box_rows)};
+        const cuuint32_t estr[2] = {1, 1};
+        r = int(fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT64, 2, const_cast<void *>(w), dims, strides, box, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE));
+    }
+    if (r == 0) return QMV_OK;
+    snprintf(g_last_error, sizeof g_last_error, "cuTensorMapEncodeTiled returned %d%s", r,
+             r < 0 ? " (driver entry point not found)" : "");
+    return QMV_ERR_CUDA;
+}
+
 qmv_status scratch(const DeviceInfo &d, size_t need, void *given, size_t given_bytes, void **out)
 {
     if (given) {
