@@ -8,29 +8,23 @@
 //     vectors A_a x[m] in fp32, both into the workspace.
 //  2. lora_project streams W once per 16 vectors. It starts under the first
 //     kernel (programmatic launch): its weights are on their way while x is
-//     staged, and the inner vectors are needed only by its epilogue, so the
-//     adapters' first half costs no time of its own.
+//     staged, and the inner vectors are needed only at the end of a tile.
 //
-// lora_project, one CTA per SM: a producer warp brings weights through a ring of
-// shared-memory slots (boxes of 8 rows x cs subgroups by tensor map, scales and
-// biases by 4-byte copies), eight consumer warps run the tiles, four epilogue
-// warps join the consumers' sums, add the adapters' second half and store.
-//  - Rows go to CTAs in eights (1920 of them for 15360 rows: 13 at most to an
-//    SM where 12.6 would be even; in sixteens it would be 7 for 6.3).
-//  - A block is up to 32 rows; consumer w takes the subgroups l with l % 8 = w
-//    of the CTA's range of K, so an operand read of x serves two 16-row tiles
-//    and all warps finish a block together.
-//  - cs is odd: rows then start 32 (or 96) bytes apart modulo 128, and the eight
-//    rows x four words of a tile's read cover all banks.
+// lora_project, one CTA per SM: a producer thread brings 128 bytes of each row of
+// a tile to a ring of shared-memory slots (one tensor-map box, 128-byte swizzle),
+// four groups of worker warps run the tiles, four tensor warps multiply. A
+// worker thread owns a row: it reads the row's scales and biases into registers a
+// slot ahead, and in the end adds the adapters' second half to the sums it holds.
+//  - Rows go to CTAs in tiles of equal height (a multiple of 8, at most 128): 104
+//    for 15360 rows on 152 SMs.
 //  - K goes to CTAs in ranges of at most 64 subgroups (4096), whose cells of 16
 //    vectors are 128 KB. Several ranges meet in the workspace: the CTA that
-//    finishes a block last adds them in their order.
-// The order of every sum depends on K alone, so a vector's result does not
+//    finishes a tile last adds them in their order.
+// The order of every sum depends on N and K alone, so a vector's result does not
 // depend on the batch it is in.
 #include <cuda_bf16.h>
 
 #include <cstdint>
-#include <cstdio>
 #include <mutex>
 
 #include "qmv.h"
@@ -40,55 +34,57 @@
 namespace qmv {
 namespace {
 
-constexpr int kConsumers = 8, kEpilogue = 4;
-constexpr int kThreads = 32 * (kConsumers + 1 + kEpilogue);
-constexpr int kBlock = 32;        // rows of a block
 constexpr int kPrepareThreads = 256;
-constexpr int kMaxSlotsLora = 16;
+constexpr int kMaxSlotsLora = 12;
 constexpr int kSmem = 227 * 1024 - 1024;
-constexpr int kMaxK = 1 << 18;
+constexpr int kMaxK = 1 << 16;
+constexpr int kRangeSubs = 64;  // subgroups of a range of K at most
+constexpr int kPass = 16;       // vectors that one read of the weights serves
 
 struct LoraParams {
     const uint16_t *scales, *biases, *x, *a, *b;
     const int32_t *adapter;
     const float *c;
     void *y;
-    uint8_t *cells;      // [pass][S][tp][128]
-    uint8_t *meta;       // [pass][S][nt][64]
+    uint8_t *cells;      // [pass][subs][cell_bytes]
+    uint8_t *meta;       // [pass][subs][meta_bytes]
     float *inner;        // [M][R]
-    float *partials;     // [pass][nseg][N][8 nt], with nseg > 1
-    unsigned *counters;  // [pass][NO], with nseg > 1
+    float *partials;     // [pass][nseg][nc][N], with nseg > 1
+    unsigned *counters;  // [pass][tiles], with nseg > 1
     unsigned *err;
-    int M, N, K, G, L, R, f32_out;
-    int S, cs, chunks, nseg, tp, nt, NO, grid_rows, slots, nsub_max, sbw, sbp, wbytes, ksplit, stage_blocks;
+    int M, N, K, G, gs, L, R, f32_out;
+    int S;       // subgroups of a row
+    int NS;      // slots of a row
+    int subs;    // NS slots' subgroups (those past S are staged as zeros)
+    int nseg;    // ranges of K
+    int range;   // slots of the longest range
+    int rows, tiles, grid_rows;
+    int nc, slots, ksplit, stage_blocks;
 };
 
-// Vectors of pass z.
-__device__ __forceinline__ int pass_vectors(const LoraParams &p, int z) { return min(p.tp, p.M - z * p.tp); }
-
-template <int BITS>
+template <int BITS, int NC>
 __global__ void __launch_bounds__(kPrepareThreads) lora_prepare(const LoraParams p)
 {
     grid_dependency_wait();
     grid_launch_dependents();
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, passes = (p.M + kPass - 1) / kPass;
     if (p.counters)
-        for (int i = blockIdx.x * kPrepareThreads + tid; i < p.NO * ((p.M + p.tp - 1) / p.tp);
-             i += gridDim.x * kPrepareThreads)
+        for (int i = blockIdx.x * kPrepareThreads + tid; i < p.tiles * passes; i += gridDim.x * kPrepareThreads)
             p.counters[i] = 0u;
     if (int(blockIdx.x) < p.stage_blocks) {
         // eight threads for each (vector, subgroup), the subgroups of a vector in a row
         const long long at = (long long)blockIdx.x * kPrepareThreads + tid;
         const int o = int(at & 7);
         long long cell = at >> 3;
-        const bool live = cell < (long long)p.M * p.S;
-        if (!live) cell = (long long)p.M * p.S - 1;
-        const int m = int(cell / p.S), sub = int(cell - (long long)m * p.S), z = m / p.tp, tok = m - z * p.tp;
-        const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p.x + size_t(m) * p.K + sub * 64 + o * 8));
-        uint8_t *c = p.cells + (size_t(z) * p.tp * p.S + size_t(sub) * pass_vectors(p, z) + tok) * tile::kCell;
-        float *meta = reinterpret_cast<float *>(p.meta + ((size_t(z) * p.S + sub) * p.nt + tok / 8) * tile::kMeta);
         // threads past the end repeat the last cell's values (the warp's exchanges need them)
-        tile::stage_octet<BITS>(v, o, tok, c, meta);
+        if (cell >= (long long)p.M * p.subs) cell = (long long)p.M * p.subs - 1;
+        const int m = int(cell / p.subs), sub = int(cell - (long long)m * p.subs), z = m / kPass;
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (sub < p.S) v = __ldg(reinterpret_cast<const uint4 *>(p.x + size_t(m) * p.K + sub * 64 + o * 8));
+        float x[8];
+        tile::widen8(v, x);
+        const size_t s = size_t(z) * p.subs + sub;
+        tile::stage_octet<BITS>(x, o, m - z * kPass, p.cells + s * tile::cell_bytes(NC), p.meta + s * tile::meta_bytes(NC));
         return;
     }
     // inner vectors: ksplit warps for each (vector, row of A), each an even share of K
@@ -129,20 +125,23 @@ __global__ void __launch_bounds__(kPrepareThreads) lora_prepare(const LoraParams
 }
 
 struct Layout {
-    int x, meta, slots, slot, sb, partial, bars, total;
+    int slots, slot, x, meta, bars, total;
 };
 
-__host__ __device__ inline Layout layout(const LoraParams &p, int nt)
+__host__ __device__ inline Layout layout(const LoraParams &p, int bits, int nc)
 {
+    const int subs = p.range * tile::slot_subs(bits);
     Layout l;
-    l.x = 0;
-    l.meta = l.x + p.nsub_max * p.tp * tile::kCell;
-    l.slots = (l.meta + p.nsub_max * nt * tile::kMeta + 127) & ~127;
-    l.sb = (p.wbytes + 127) & ~127;  // scales and biases of a slot, after its weights
-    l.slot = (l.sb + 2 * kBlock * p.sbp * 4 + 127) & ~127;
-    l.partial = l.slots + p.slots * l.slot;
-    l.bars = l.partial + 2 * kConsumers * nt * kBlock * 8 * 4;
-    l.total = l.bars + (2 * p.slots + 5) * 8 + 16;
+    l.slots = 0;
+    l.slot = p.rows * tile::kSlotBytes;
+    // a tile of fewer than 128 rows reads on past its slot's end
+    l.x = p.slots * l.slot;
+    if (l.x < (p.slots - 1) * l.slot + tile::kTileRows * tile::kSlotBytes)
+        l.x = (p.slots - 1) * l.slot + tile::kTileRows * tile::kSlotBytes;
+    l.x = (l.x + 1023) & ~1023;
+    l.meta = l.x + subs * tile::cell_bytes(nc);
+    l.bars = l.meta + subs * tile::meta_bytes(nc);
+    l.total = l.bars + (2 * p.slots + 4 * tile::kGroups + 1) * 8;
     return l;
 }
 
@@ -173,241 +172,165 @@ __device__ __forceinline__ float adapter_term(const LoraParams &p, int ad, int m
     return __fmul_rn(__ldg(p.c + ad), d);
 }
 
-template <int BITS, int NT>
-__global__ void __launch_bounds__(kThreads, 1) lora_project(const __grid_constant__ CUtensorMap map, const LoraParams p)
+template <int BITS, int NC>
+__global__ void __launch_bounds__(tile::kThreads, 1) lora_project(const __grid_constant__ CUtensorMap map,
+                                                                  const LoraParams p)
 {
-    extern __shared__ __align__(128) uint8_t smem[];
+    using namespace tile;
+    extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ int s_abort, s_last;
-    const Layout L = layout(p, NT);
+    __shared__ uint32_t s_tmem;
+    constexpr int SUBS = slot_subs(BITS);
+    const Layout L = layout(p, BITS, NC);
     const uint32_t base = smem_u32(smem), full0 = base + L.bars, empty0 = full0 + 8 * p.slots;
-    const uint32_t xbar = empty0 + 8 * p.slots, pfull0 = xbar + 8, pempty0 = pfull0 + 16;
+    const uint32_t stored0 = empty0 + 8 * p.slots, ready0 = stored0 + 16 * kGroups, xbar = ready0 + 16 * kGroups;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-    const int cta = blockIdx.x, seg = blockIdx.y, z = blockIdx.z;
+    const int seg = blockIdx.y, z = blockIdx.z;
     if (tid == 0) {
         for (int i = 0; i < p.slots; ++i) {
-            mbar_init(full0 + 8 * i, 1 + 32);
-            mbar_init(empty0 + 8 * i, kConsumers);
+            mbar_init(full0 + 8 * i, 1);
+            mbar_init(empty0 + 8 * i, 4);
+        }
+        for (int i = 0; i < 2 * kGroups; ++i) {
+            mbar_init(stored0 + 8 * i, 4);
+            mbar_init(ready0 + 8 * i, 1);
         }
         mbar_init(xbar, 1);
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(pfull0 + 8 * i, kConsumers);
-            mbar_init(pempty0 + 8 * i, kEpilogue);
-        }
         fence_mbar_init();
         s_abort = 0;
     }
+    if (warp == kWorkers) tmem_alloc(smem_u32(&s_tmem), tmem_columns(NC));
+    tmem_fence_before();
     __syncthreads();
+    tmem_fence_after();
+    const uint32_t tm = s_tmem;
+    const Waits wait{&s_abort, p.err};
+    const int lo = int((long long)p.NS * seg / p.nseg), ns = int((long long)p.NS * (seg + 1) / p.nseg) - lo;
 
-    const int oct_lo = int((long long)p.NO * cta / p.grid_rows), oct_hi = int((long long)p.NO * (cta + 1) / p.grid_rows);
-    const int ch_lo = int((long long)p.chunks * seg / p.nseg), ch_hi = int((long long)p.chunks * (seg + 1) / p.nseg);
-    const int sub_lo = ch_lo * p.cs, sub_hi = min(ch_hi * p.cs, p.S), nsub = sub_hi - sub_lo;
-    const int nblocks = (oct_hi - oct_lo + kBlock / 8 - 1) / (kBlock / 8);
-    const int nv = pass_vectors(p, z);
-    const int gs_subs = p.S / p.G;  // subgroups in a group: 1 or 2
-    const uint32_t pitch = uint32_t(p.cs) * (8 * BITS);
-    // A wait that ran out: the error word is set and every warp stops.
-    auto give_up = [&]() {
-        atomicOr(p.err, 1u);
-        *reinterpret_cast<volatile int *>(&s_abort) = 1;
-    };
-    auto wait = [&](uint32_t bar, uint32_t parity) {
-        if (mbar_wait_bounded(bar, parity)) return *reinterpret_cast<volatile int *>(&s_abort) == 0;
-        give_up();
-        return false;
-    };
-
-    if (warp == kConsumers) {
+    if (warp == kThreads / 32 - 1) {
         // ---------------------------------------------------------- producer
-        int it = 0;
-        bool ok = true;
-        for (int bl = 0; bl < nblocks && ok; ++bl) {
-            const int oct = oct_lo + bl * (kBlock / 8), nbox = min(kBlock / 8, oct_hi - oct), row0 = oct * 8;
-            for (int c = ch_lo; c < ch_hi && ok; ++c, ++it) {
-                const int slot = it % p.slots, lap = it / p.slots;
-                const uint32_t full = full0 + 8 * slot, dst = base + L.slots + slot * L.slot;
-                if (lap > 0) ok = wait(empty0 + 8 * slot, (lap - 1) & 1);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-                if (lane == 0) mbar_arrive_expect_tx(full, uint32_t(nbox) * 8u * pitch);
-                __syncwarp();
-                if (lane < nbox) tma_load_2d(dst + lane * 8 * pitch, &map, c * p.cs * BITS, row0 + lane * 8, full);
-                // scales and biases: the words that hold groups g0 .. of each row
-                const int g0 = c * p.cs / gs_subs;
-                const long long all = (long long)p.N * p.G;
-                for (int i = lane; i < nbox * 8 * 16; i += 32) {
-                    const int r = i >> 4, wd = i & 15;
-                    if (wd >= p.sbw) continue;
-                    const int n = row0 + r;
-                    long long e = ((long long)n * p.G + g0) / 2 * 2 + 2 * wd;
-                    uint32_t bytes = 0;
-                    if (n < p.N && e < all) bytes = e + 1 < all ? 4 : 2;
-                    if (!bytes) e = 0;
-                    const uint32_t d = dst + L.sb + (r * p.sbp + wd) * 4;
-                    tile::copy_word(d, p.scales + e, bytes);
-                    tile::copy_word(d + kBlock * p.sbp * 4, p.biases + e, bytes);
+        if (lane == 0) {
+            int it = 0;
+            const uint32_t bytes = uint32_t(p.rows) * kSlotBytes;
+            for (int tl = blockIdx.x; tl < p.tiles && !*wait.abort; tl += p.grid_rows)
+                for (int i = 0; i < ns; ++i, ++it) {
+                    const int s = it % p.slots, lap = it / p.slots;
+                    if (lap > 0 && !wait(empty0 + 8 * s, (lap - 1) & 1)) break;
+                    mbar_arrive_expect_tx(full0 + 8 * s, bytes);
+                    tma_load_2d(base + s * L.slot, &map, (lo + i) * (kSlotBytes / 8), tl * p.rows, full0 + 8 * s);
                 }
-                tile::copy_arrive(full);
-            }
+            if (*wait.abort)  // copies in flight end before the CTA does
+                for (int j = max(0, it - p.slots); j < it; ++j)
+                    (void)mbar_wait_bounded(full0 + 8 * (j % p.slots), (j / p.slots) & 1);
         }
-        asm volatile("cp.async.wait_all;" ::: "memory");
-        if (!ok)  // copies in flight end before the CTA does
-            for (int j = max(0, it - p.slots); j < it; ++j) (void)mbar_wait_bounded(full0 + 8 * (j % p.slots), (j / p.slots) & 1);
-        return;
-    }
-
-    grid_launch_dependents();
-    grid_dependency_wait();  // x cells and inner vectors
-    if (warp < kConsumers) {
-        // --------------------------------------------------------- consumers
+    } else if (warp >= kWorkers) {
+        // ------------------------------------------------------ tensor warps
+        const int group = warp - kWorkers;
+        if (lane == 0) {
+            wait(xbar, 0);
+            const uint32_t ta = tm + group * 32, td = tm + kGroups * 32 + group * 2 * acc_columns(NC);
+            for (int tl = blockIdx.x; tl < p.tiles; tl += p.grid_rows)
+                for (int i = group; i < ns; i += kGroups)
+                    multiply_slot<BITS, NC>(wait, base + L.x + i * SUBS * cell_bytes(NC), stored0 + 16 * group,
+                                            ready0 + 16 * group, ta, td);
+        }
+    } else {
+        // ----------------------------------------------------------- workers
+        const int group = warp / 4, row = (warp & 3) * 32 + lane, nv = min(kPass, p.M - z * kPass);
+        const bool vec = p.G % (SUBS * 64 / p.gs) == 0;
+        const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
+        const uint32_t ta = tm + lanes + group * 32, td = tm + lanes + kGroups * 32 + group * 2 * acc_columns(NC);
+        const uint32_t stored = stored0 + 16 * group, ready = ready0 + 16 * group;
+        const uint32_t wrow = base + row * kSlotBytes + ((row & 7) << 4);
+        Affine<BITS> next;
+        {
+            const int n = blockIdx.x * p.rows + row;
+            next.clear();
+            if (row < p.rows && n < p.N && group < ns) next.load(p.scales, p.biases, n, p.G, p.gs, lo + group, vec);
+        }
+        grid_launch_dependents();
+        grid_dependency_wait();  // x cells and inner vectors
         if (tid == 0) {
             asm volatile("fence.proxy.async;" ::: "memory");
-            const uint32_t cb = uint32_t(nsub) * nv * tile::kCell, mb = uint32_t(nsub) * NT * tile::kMeta;
+            const uint32_t cb = uint32_t(ns) * SUBS * cell_bytes(NC), mb = uint32_t(ns) * SUBS * meta_bytes(NC);
             mbar_arrive_expect_tx(xbar, cb + mb);
-            bulk_load_plain(base + L.x, p.cells + (size_t(z) * p.tp * p.S + size_t(sub_lo) * nv) * tile::kCell, cb, xbar);
-            bulk_load_plain(base + L.meta, p.meta + (size_t(z) * p.S + sub_lo) * NT * tile::kMeta, mb, xbar);
+            const size_t sub = size_t(z) * p.subs + size_t(lo) * SUBS;
+            bulk_load_plain(base + L.x, p.cells + sub * cell_bytes(NC), cb, xbar);
+            bulk_load_plain(base + L.meta, p.meta + sub * meta_bytes(NC), mb, xbar);
         }
-        bool ok = __all_sync(0xffffffffu, wait(xbar, 0));
-        const int g = lane / 4, t = lane % 4;
-        uint32_t xcol[NT], odd[NT];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const int tok = min(n * 8 + g, nv - 1);
-            xcol[n] = base + L.x + tok * tile::kCell + t * 32;
-            odd[n] = (tok & 1) * 16;
-        }
+        wait(xbar, 0);
         int it = 0;
-        for (int bl = 0; bl < nblocks && ok; ++bl) {
-            const int oct = oct_lo + bl * (kBlock / 8);
-            const bool two = oct_hi - oct > 2;
-            const long long rowg = (long long)(oct * 8 + g) * p.G;
-            uint64_t y[2][NT][2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                for (int n = 0; n < NT; ++n) y[i][n][0] = y[i][n][1] = 0ull;
-            for (int c = ch_lo; c < ch_hi && ok; ++c, ++it) {
-                const int slot = it % p.slots, lap = it / p.slots;
-                ok = wait(full0 + 8 * slot, lap & 1);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-                const uint32_t src = base + L.slots + slot * L.slot;
-                const int l0 = c * p.cs - sub_lo, l1 = min(l0 + p.cs, nsub), g0 = c * p.cs / gs_subs;
-                const uint32_t sb = src + L.sb + g * p.sbp * 4 + uint32_t((rowg + g0) & 1) * 2;
-#pragma unroll 2
-                for (int l = l0 + ((warp - l0) & (kConsumers - 1)); l < l1; l += kConsumers) {
-                    const uint32_t w = src + g * pitch + (l - l0) * (8 * BITS) + t * (2 * BITS);
-                    const uint32_t s = sb + ((sub_lo + l) / gs_subs - g0) * 2;
-                    uint32_t x[NT];
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) x[n] = xcol[n] + l * nv * tile::kCell;
-                    const uint32_t meta = base + L.meta + l * NT * tile::kMeta + t * 16;
-                    if (two)
-                        tile::add_subgroup<BITS, 2, NT>(y, w, pitch, s, s + kBlock * p.sbp * 4, p.sbp * 4, x, odd, meta);
-                    else
-                        tile::add_subgroup<BITS, 1, NT>(y, w, pitch, s, s + kBlock * p.sbp * 4, p.sbp * 4, x, odd, meta);
-                }
+        for (int tl = blockIdx.x; tl < p.tiles; tl += p.grid_rows, it += ns) {
+            const int n = tl * p.rows + row;
+            const bool live = row < p.rows && n < p.N;
+            Row<BITS, NC> acc;
+            acc.start();
+            uint32_t last = 0;
+            for (int i = group; i < ns; i += kGroups) {
+                const int s = (it + i) % p.slots, lap = (it + i) / p.slots;
+                const Affine<BITS> now = next;
+                // the next slot's, of this tile or of the next
+                const int ni = i + kGroups < ns ? i + kGroups : group, nn = i + kGroups < ns ? n : n + p.grid_rows * p.rows;
+                next.clear();
+                if (row < p.rows && nn < p.N) next.load(p.scales, p.biases, nn, p.G, p.gs, lo + ni, vec);
+                wait(full0 + 8 * s, lap & 1);
+                const uint32_t meta = base + L.meta + i * SUBS * meta_bytes(NC);
+                acc.slot(wait, wrow + s * L.slot, now, meta, last, stored, ready, ta, td, lane);
+                last = meta + (SUBS - 2) * meta_bytes(NC);
                 __syncwarp();
-                if (lane == 0) mbar_arrive(empty0 + 8 * slot);
+                if (lane == 0) mbar_arrive(empty0 + 8 * s);
             }
-            if (!ok) break;
-            if (bl >= 2) ok = __all_sync(0xffffffffu, wait(pempty0 + 8 * (bl & 1), (bl / 2 - 1) & 1));
-            if (!ok) break;
-            uint64_t *out = reinterpret_cast<uint64_t *>(smem + L.partial) + ((bl & 1) * kConsumers + warp) * NT * kBlock * 4;
+            acc.finish(wait, last, ready, td);
+            float sums[Row<BITS, NC>::kOwn];
+            acc.join(tm + lanes, group, sums);
+            bool mine = true;
+            if (p.nseg > 1) {
+                const size_t plane = size_t(p.N), seg_stride = plane * NC;
+                float *part = p.partials + size_t(z) * p.nseg * seg_stride + n;
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) out[(n * kBlock + 16 * i + 8 * h + g) * 4 + t] = y[i][n][h];
-            __syncwarp();
-            if (lane == 0) mbar_arrive(pfull0 + 8 * (bl & 1));
-        }
-        if (!ok && tid == 0) (void)mbar_wait_bounded(xbar, 0);
-        return;
-    }
-
-    // ------------------------------------------------------------- epilogue
-    const int et = tid - 32 * (kConsumers + 1);
-    constexpr int kVals = NT * kBlock * 8;  // sums of a block
-    for (int bl = 0; bl < nblocks; ++bl) {
-        const int oct = oct_lo + bl * (kBlock / 8), row0 = oct * 8, rows = min(kBlock, (oct_hi - oct) * 8);
-        if (!__all_sync(0xffffffffu, wait(pfull0 + 8 * (bl & 1), (bl / 2) & 1))) break;
-        const float *in = reinterpret_cast<const float *>(smem + L.partial) + (bl & 1) * kConsumers * kVals;
-        float v[kVals / (32 * kEpilogue)];
-#pragma unroll
-        for (int j = 0; j < kVals / (32 * kEpilogue); ++j) {
-            float s = in[j * 32 * kEpilogue + et];
-#pragma unroll
-            for (int w = 1; w < kConsumers; ++w) s = __fadd_rn(s, in[w * kVals + j * 32 * kEpilogue + et]);
-            v[j] = s;
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(pempty0 + 8 * (bl & 1));
-        bool mine = true;
-        if (p.nseg > 1) {
-            float *part = p.partials + (size_t(z) * p.nseg + seg) * p.N * (8 * NT);
-#pragma unroll
-            for (int j = 0; j < kVals / (32 * kEpilogue); ++j) {
-                const int e = j * 32 * kEpilogue + et, r = e / 8 % kBlock, col = e / (8 * kBlock) * 8 + e % 8;
-                if (r < rows && row0 + r < p.N) __stcg(part + size_t(row0 + r) * (8 * NT) + col, v[j]);
-            }
-            __threadfence();
-            tile::named_sync(1, 32 * kEpilogue);
-            if (et == 0) s_last = atomicAdd(p.counters + size_t(z) * p.NO + oct, 1u) == unsigned(p.nseg - 1);
-            tile::named_sync(1, 32 * kEpilogue);
-            mine = s_last != 0;
-            if (mine) {
+                for (int i = 0; i < Row<BITS, NC>::kOwn; ++i) {
+                    const int t = group + 4 * i;
+                    if (live && t < nv) __stcg(part + seg * seg_stride + t * plane, sums[i]);
+                }
                 __threadfence();
-                part = p.partials + size_t(z) * p.nseg * p.N * (8 * NT);
+                named_sync(1, 32 * kWorkers);
+                if (tid == 0) s_last = atomicAdd(p.counters + size_t(z) * p.tiles + tl, 1u) == unsigned(p.nseg - 1);
+                named_sync(1, 32 * kWorkers);
+                mine = s_last != 0;
+                if (mine) {
+                    __threadfence();
 #pragma unroll
-                for (int j = 0; j < kVals / (32 * kEpilogue); ++j) {
-                    const int e = j * 32 * kEpilogue + et, r = e / 8 % kBlock, col = e / (8 * kBlock) * 8 + e % 8;
-                    if (r >= rows || row0 + r >= p.N) continue;
-                    const float *q = part + size_t(row0 + r) * (8 * NT) + col;
-                    float s = __ldcg(q);
-                    for (int k = 1; k < p.nseg; ++k) s = __fadd_rn(s, __ldcg(q + size_t(k) * p.N * (8 * NT)));
-                    v[j] = s;
+                    for (int i = 0; i < Row<BITS, NC>::kOwn; ++i) {
+                        const int t = group + 4 * i;
+                        if (!live || t >= nv) continue;
+                        float s = __ldcg(part + t * plane);
+                        for (int k = 1; k < p.nseg; ++k) s = __fadd_rn(s, __ldcg(part + k * seg_stride + t * plane));
+                        sums[i] = s;
+                    }
                 }
             }
-        }
-        if (!mine) continue;
+            if (!mine || !live) continue;
 #pragma unroll
-        for (int j = 0; j < kVals / (32 * kEpilogue); ++j) {
-            const int e = j * 32 * kEpilogue + et, n = row0 + e / 8 % kBlock, col = e / (8 * kBlock) * 8 + e % 8;
-            if (e / 8 % kBlock >= rows || n >= p.N || col >= nv) continue;
-            const int m = z * p.tp + col, ad = __ldg(p.adapter + m);
-            float s = v[j];
-            if (ad >= 0 && ad < p.L) s = __fadd_rn(s, adapter_term(p, ad, m, n));
-            const size_t at = size_t(m) * p.N + n;
-            if (p.f32_out) static_cast<float *>(p.y)[at] = s;
-            else static_cast<__nv_bfloat16 *>(p.y)[at] = __float2bfloat16_rn(s);
+            for (int i = 0; i < Row<BITS, NC>::kOwn; ++i) {
+                const int t = group + 4 * i;
+                if (t >= nv) continue;
+                const int m = z * kPass + t, ad = __ldg(p.adapter + m);
+                float s = sums[i];
+                if (ad >= 0 && ad < p.L) s = __fadd_rn(s, adapter_term(p, ad, m, n));
+                const size_t at = size_t(m) * p.N + n;
+                if (p.f32_out) static_cast<float *>(p.y)[at] = s;
+                else static_cast<__nv_bfloat16 *>(p.y)[at] = __float2bfloat16_rn(s);
+            }
         }
     }
+    __syncwarp();
+    tmem_fence_before();
+    __syncthreads();
+    tmem_fence_after();
+    if (warp == kWorkers) tmem_free(tm, tmem_columns(NC));
 }
 
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
-// Chunks (cs subgroups, odd) and ranges of K: at least ceil(S / 64) ranges (at
-// most 8), and of the chunk sizes the one that leaves the longest range the
-// shortest, the larger among equals. A function of S and bits alone.
-void split_k(int S, int bits, int &cs, int &chunks, int &nseg)
-{
-    const int most = bits == 4 ? 15 : 31;
-    nseg = (S + 63) / 64;
-    if (nseg > 8) nseg = 8;
-    int best = 1 << 30;
-    cs = 1;
-    for (int c = most; c >= 1; c -= 2) {
-        if (c < 9 && S >= 9) break;
-        const int n = (S + c - 1) / c, longest = (n + nseg - 1) / nseg * c;
-        if (longest < best) {
-            best = longest;
-            cs = c;
-        }
-    }
-    chunks = (S + cs - 1) / cs;
-    if (nseg > chunks) nseg = chunks;
-}
 
 struct Sizes {
     size_t cells, meta, inner, counters, partials, total;
@@ -415,58 +338,67 @@ struct Sizes {
 
 size_t up256(size_t b) { return (b + 255) & ~size_t(255); }
 
-LoraParams plan(int M, int N, int K, int bits, int gs, int R, Sizes &sz)
+// What a call needs; `sms` only shapes the grid (tiles), never an order of sums
+// or a size.
+LoraParams plan(int M, int N, int K, int bits, int gs, int R, int sms, Sizes &sz)
 {
+    const int slot_subs = tile::slot_subs(bits);
     LoraParams p{};
-    p.M = M; p.N = N; p.K = K; p.G = K / gs; p.R = R;
+    p.M = M; p.N = N; p.K = K; p.G = K / gs; p.gs = gs; p.R = R;
     p.S = K / 64;
-    split_k(p.S, bits, p.cs, p.chunks, p.nseg);
-    p.nsub_max = (p.chunks + p.nseg - 1) / p.nseg * p.cs;
-    p.tp = 16;
-    while (p.tp > 1 && p.tp * p.nsub_max > 1024) p.tp /= 2;
-    p.nt = M > 8 && p.tp > 8 ? 2 : 1;
-    if (p.nt == 1 && p.tp > 8) p.tp = 8;
-    p.NO = (N + 7) / 8;
-    const int groups = gs == 64 ? p.cs : p.cs / 2 + 1;  // groups that a chunk can touch
-    p.sbw = (groups + 2) / 2;                           // words that hold them, from an even element on
-    p.sbp = p.sbw | 1;
-    p.wbytes = kBlock * p.cs * 8 * bits;
+    p.NS = (p.S + slot_subs - 1) / slot_subs;
+    p.subs = p.NS * slot_subs;
+    p.nseg = (p.NS * slot_subs + kRangeSubs - 1) / kRangeSubs;
+    p.range = (p.NS + p.nseg - 1) / p.nseg;
+    p.nc = M <= 2 ? 2 : M <= 4 ? 4 : M <= 8 ? 8 : 16;
+    // tiles of equal height: as many rounds of the grid as 128 rows need
+    p.grid_rows = sms / p.nseg > 0 ? sms / p.nseg : 1;
+    const int rounds = (N + tile::kTileRows * p.grid_rows - 1) / (tile::kTileRows * p.grid_rows);
+    p.rows = ((N + p.grid_rows * rounds - 1) / (p.grid_rows * rounds) + 7) / 8 * 8;
+    p.tiles = (N + p.rows - 1) / p.rows;
+    if (p.grid_rows > p.tiles) p.grid_rows = p.tiles;
     p.ksplit = K <= 4096 ? 1 : K <= 8192 ? 2 : K <= 16384 ? 4 : 8;
-    const size_t passes = (M + p.tp - 1) / p.tp;
-    sz.cells = up256(size_t(M) * p.S * tile::kCell);
-    sz.meta = up256(passes * p.S * p.nt * tile::kMeta);
+    const size_t passes = (M + kPass - 1) / kPass;
+    sz.cells = up256(passes * p.subs * tile::cell_bytes(p.nc));
+    sz.meta = up256(passes * p.subs * tile::meta_bytes(p.nc));
     sz.inner = up256(size_t(M) * R * 4);
-    sz.counters = p.nseg > 1 ? up256(passes * p.NO * 4) : 0;
-    sz.partials = p.nseg > 1 ? up256(passes * p.nseg * size_t(N) * 8 * p.nt * 4) : 0;
+    sz.counters = p.nseg > 1 ? up256(passes * ((N + 7) / 8) * 4) : 0;
+    sz.partials = p.nseg > 1 ? up256(passes * p.nseg * size_t(N) * p.nc * 4) : 0;
     sz.total = sz.cells + sz.meta + sz.inner + sz.counters + sz.partials;
     return p;
 }
 
-template <int BITS, int NT>
-cudaError_t launch_project(const CUtensorMap &map, const LoraParams &p, int passes, cudaStream_t stream)
+template <int BITS, int NC>
+cudaError_t launch_lora(const CUtensorMap &map, LoraParams &p, cudaStream_t stream)
 {
-    static std::atomic<int> configured[64] = {};
-    Launch l;
-    l.grid = dim3(p.grid_rows, p.nseg, passes);
-    l.threads = kThreads;
-    l.smem = size_t(layout(p, NT).total);
-    l.pdl = true;
-    return launch_one(lora_project<BITS, NT>, configured, l, stream, map, p);
-}
-
-template <int BITS>
-cudaError_t launch_lora(const CUtensorMap &map, const LoraParams &p, int passes, cudaStream_t stream)
-{
-    static std::atomic<int> configured[64] = {};
+    static std::atomic<int> configured[2][64] = {};
     Launch l;
     const int per = kPrepareThreads / 32 / p.ksplit;
     l.grid = dim3(p.stage_blocks + (p.M * p.R + per - 1) / per);
     l.threads = kPrepareThreads;
     l.smem = 0;
     l.pdl = true;
-    const cudaError_t e = launch_one(lora_prepare<BITS>, configured, l, stream, p);
+    const cudaError_t e = launch_one(lora_prepare<BITS, NC>, configured[0], l, stream, p);
     if (e != cudaSuccess) return e;
-    return p.nt == 2 ? launch_project<BITS, 2>(map, p, passes, stream) : launch_project<BITS, 1>(map, p, passes, stream);
+    l.grid = dim3(p.grid_rows, p.nseg, (p.M + kPass - 1) / kPass);
+    l.threads = tile::kThreads;
+    l.smem = size_t(layout(p, BITS, NC).total);
+    return launch_one(lora_project<BITS, NC>, configured[1], l, stream, map, p);
+}
+
+template <int BITS>
+cudaError_t launch_lora(const CUtensorMap &map, LoraParams &p, cudaStream_t stream)
+{
+    // as many slots as fit
+    p.slots = kMaxSlotsLora;
+    while (p.slots > 2 && layout(p, BITS, p.nc).total > kSmem) --p.slots;
+    if (layout(p, BITS, p.nc).total > kSmem) return cudaErrorInvalidConfiguration;
+    switch (p.nc) {
+        case 2: return launch_lora<BITS, 2>(map, p, stream);
+        case 4: return launch_lora<BITS, 4>(map, p, stream);
+        case 8: return launch_lora<BITS, 8>(map, p, stream);
+        default: return launch_lora<BITS, 16>(map, p, stream);
+    }
 }
 
 }  // namespace
@@ -477,7 +409,7 @@ extern "C" size_t qmv_lora_workspace_size(int M, int N, int K, int bits, int gro
     if (qmv::check_weights(M, N, K, bits, group_size) != QMV_OK || K > qmv::kMaxK || rank < 1 || rank > QMV_MAX_RANK)
         return 0;
     qmv::Sizes sz;
-    qmv::plan(M, N, K, bits, group_size, rank, sz);
+    qmv::plan(M, N, K, bits, group_size, rank, 1, sz);
     return sz.total;
 }
 
@@ -502,7 +434,7 @@ extern "C" qmv_status qmv_lora_run(const uint32_t *w_q, const uint16_t *scales, 
     st = current_device(&dev);
     if (st != QMV_OK) return st;
     Sizes sz;
-    LoraParams p = plan(M, N, K, bits, group_size, rank, sz);
+    LoraParams p = plan(M, N, K, bits, group_size, rank, dev.sms, sz);
     void *ws = nullptr;
     st = scratch(dev, sz.total, workspace, workspace_bytes, &ws);
     if (st != QMV_OK) return st;
@@ -517,26 +449,11 @@ extern "C" qmv_status qmv_lora_run(const uint32_t *w_q, const uint16_t *scales, 
     p.inner = reinterpret_cast<float *>(at); at += sz.inner;
     p.counters = p.nseg > 1 ? reinterpret_cast<unsigned *>(at) : nullptr; at += sz.counters;
     p.partials = p.nseg > 1 ? reinterpret_cast<float *>(at) : nullptr;
-    p.stage_blocks = int(((long long)M * p.S * 8 + kPrepareThreads - 1) / kPrepareThreads);
-    p.grid_rows = dev.sms / p.nseg;
-    if (p.grid_rows < 1) p.grid_rows = 1;
-    if (p.grid_rows > p.NO) p.grid_rows = p.NO;
-    const int passes = (M + p.tp - 1) / p.tp;
-    // as many slots as fit
-    p.slots = 2;
-    while (p.slots < kMaxSlotsLora) {
-        ++p.slots;
-        if (layout(p, p.nt).total > kSmem) {
-            --p.slots;
-            break;
-        }
-    }
-    if (layout(p, p.nt).total > kSmem) return record_cuda_failure("lora launch plan", cudaErrorInvalidConfiguration);
-
+    p.stage_blocks = int(((long long)M * p.subs * 8 + kPrepareThreads - 1) / kPrepareThreads);
     CUtensorMap map;
-    st = encode_rows(&map, w_q, (long long)K * bits / 8, N, p.cs * bits, 8);
+    st = encode_rows(&map, w_q, (long long)K * bits / 8, N, tile::kSlotBytes / 8, p.rows);
     if (st != QMV_OK) return st;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const cudaError_t e = bits == 4 ? launch_lora<4>(map, p, passes, s) : launch_lora<2>(map, p, passes, s);
+    const cudaError_t e = bits == 4 ? launch_lora<4>(map, p, s) : launch_lora<2>(map, p, s);
     return e == cudaSuccess ? QMV_OK : record_cuda_failure("lora kernel launch", e);
 }

@@ -6,37 +6,36 @@
 //
 //   s * sum_k q_k x_k  +  b * sum_k x_k                    (fp32)
 //
-// and the first sum is a product of small integers with bf16 values: one
-// m16n8k16 bf16 instruction covers 16 rows, 16 of the k and 8 vectors. A row's
-// 64 packed fields need no conversion to become bf16 operands: the bf16 whose
-// low byte is n and whose high byte is zero is exactly n * 2^-133 (n < 128 is
-// subnormal, 128 <= n < 256 is the first normal binade; the formula is the
-// same), and the tensor core takes subnormal operands exactly. So one mask
-// isolates two fields (one in each half word), wherever in the half word's low
-// byte they lie, and a shift by 8 serves the high bytes: a 4-bit word's eight
-// fields cost five instructions, a 2-bit word's sixteen cost nine. The factor
-// 2^(field position) goes into x, whose staged form is
+// and the first sum is formed by tcgen05, 128 rows and up to 16 vectors at a
+// time, on 8-bit operands that are exact:
+//  - A byte 0x00..0x0f read as e4m3 is exactly its value times 2^-9 (up to 7 it
+//    is subnormal, from 8 on it is the first normal binade; the formula is the
+//    same). So a packed word becomes operand registers by masks alone: a 4-bit
+//    word's eight fields by v & 0x0f0f0f0f and (v >> 4) & 0x0f0f0f0f; a 2-bit
+//    word's sixteen by four masks and a shift, two of the masks leaving 4 q.
+//  - x is brought to a largest magnitude of 2^7 .. 2^8 in the subgroup by a power
+//    of two, and split into two e4m3 of 4 significant bits each, x' = hi + lo/32.
+//    bf16 has 8 bits, so the split is exact down to 2^-14 of the subgroup's
+//    largest |x| (2^-12 for a 2-bit matrix's odd fields); below that an element
+//    is rounded to 2^-22 (2^-20) of that largest. hi and lo are two rows of the B
+//    operand, their sums two accumulators, joined as (hi + lo/32) * f.
+// The accumulators are fp32 (checked: sums of exact products come out exact).
 //
-//   x'_k = x_k * 2^(p - position),  p = 240 - E (at least 6),
+// The tile. A thread owns a row (a lane of tensor memory). For each subgroup it
+// reads its 32 (2-bit: 16) bytes from the ring, masks them into 16 registers,
+// stores those as its 16 columns of the A operand in tensor memory, and two
+// subgroups later reads the accumulator's columns back and adds s * (..) + b *
+// sum x to its sums, which stay in registers over all of K. What bounds it is the
+// integer pipe (one instruction in two cycles): the masks, 24 for a 4-bit
+// subgroup. Measured with everything resident: 36 bytes of weights a cycle of an
+// SM up to 2 vectors, 32 at 8, 26 at 16 (4-bit), where 6.8 TB/s over 152 SMs are
+// 23.5. Before it, on the same card: bf16 operands (the masks of a low byte are
+// exact there too, 40 for a subgroup) through tcgen05 25, 24 and 21; through
+// mma.sync, whose instruction holds the issue slot for 8 cycles, 27 and 19.
 //
-// E being the largest exponent field of the subgroup's x. All factors are
-// powers of two and exact, so sum q x = acc * f with f = 2^(133 - p). (For x of
-// 2^122 and above, infinities and NaN, the vector's own result is unspecified.)
-//
-// What it costs: per 16 rows x 64 k (512 bytes of 4-bit weights) and 8 vectors
-// about 45 instructions and four tensor instructions (8 cycles of an SM at the
-// measured 0.51 a cycle), against 22 cycles that the bytes take at 6.8 TB/s
-// over 152 SMs. The fp32 cores would need 32 fused multiply-adds of a warp for
-// each vector. tcgen05 would need the fields written out as bf16 to shared or
-// tensor memory first (four times the weight bytes) and its accumulators read
-// back for every group.
-//
-// Staged x. A cell is one subgroup of one vector: 64 bf16 in operand order, 128
-// bytes. The thread with index t of a quad holds k = 16 t .. 16 t + 15, 32
-// bytes: operand registers in the order of the masks. The two 16-byte halves of
-// the 32 bytes are exchanged in odd vectors, so that a quarter warp's 16-byte
-// reads of two vectors cover all banks. Beside the cells lie, for each subgroup
-// and pair of vectors, (sum x, sum x, f, f).
+// Order. Slot i of a row's range of K belongs to worker group i % 4, which adds
+// its subgroups in order; the four groups' sums are added in order. Nothing
+// depends on how many vectors there are.
 #pragma once
 
 #include "qmv_kernel.cuh"
@@ -44,8 +43,21 @@
 namespace qmv {
 namespace tile {
 
-constexpr int kCell = 128;  // bytes of a staged cell
-constexpr int kMeta = 64;   // bytes of a subgroup's (sum, f) of 8 vectors
+constexpr int kGroups = 4;                   // worker groups of four warps
+constexpr int kWorkers = 4 * kGroups;        // worker warps; then a tensor warp for each group
+constexpr int kThreads = 32 * (kWorkers + kGroups + 1);  // and the producer
+constexpr int kTileRows = 128;
+constexpr int kSlotBytes = 128;              // bytes of a row in a ring slot
+
+__host__ __device__ constexpr int slot_subs(int bits) { return kSlotBytes * 8 / bits / 64; }  // 4 or 8
+// Bytes of a subgroup's B operand for up to nc vectors: atoms of 8 rows x 64 bytes.
+__host__ __device__ constexpr int cell_bytes(int nc) { return nc <= 4 ? 512 : nc <= 8 ? 1024 : 2048; }
+// Bytes of a subgroup's (sum, sum, f, f), for each pair of vectors.
+__host__ __device__ constexpr int meta_bytes(int nc) { return nc / 2 * 16; }
+// Columns of an accumulator (the instruction's N; up to 4 vectors its second
+// eight rows are the first again).
+__host__ __device__ constexpr int acc_columns(int nc) { return nc <= 8 ? 16 : 32; }
+__host__ __device__ constexpr int tmem_columns(int nc) { return nc <= 8 ? 256 : 512; }
 
 __device__ __forceinline__ uint64_t pack2(float lo, float hi)
 {
@@ -70,212 +82,469 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
     return d;
 }
 
-__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                         uint32_t b0, uint32_t b1)
-{
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
 __device__ __forceinline__ uint4 lds_128(uint32_t addr)
 {
     uint4 v;
     asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
     return v;
 }
-__device__ __forceinline__ uint2 lds_64(uint32_t addr)
-{
-    uint2 v;
-    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
-    return v;
-}
-__device__ __forceinline__ uint32_t lds_32(uint32_t addr)
-{
-    uint32_t v;
-    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
-    return v;
-}
-// A bf16 of shared memory as fp32.
-__device__ __forceinline__ float lds_bf16(uint32_t addr)
-{
-    uint16_t v;
-    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr));
-    return __uint_as_float(uint32_t(v) << 16);
-}
 
 // 2^e for -126 <= e <= 127.
 __device__ __forceinline__ float exp2i(int e) { return __uint_as_float(uint32_t(e + 127) << 23); }
 
-// Stages eight elements of a vector: octet o (0..7) of a subgroup, by the
-// eight consecutive threads of a warp that hold its octets. `v` holds the bf16
-// of elements 8 o .. 8 o + 7; `tok` is the vector's index in its block, `cell`
-// the subgroup's cell of it, `meta` the subgroup's meta of its eight vectors.
-template <int BITS>
-__device__ __forceinline__ void stage_octet(uint4 v, int o, int tok, uint8_t *cell, float *meta)
+// Two floats as e4m3 (a in the low byte), and back.
+__device__ __forceinline__ uint32_t to_e4m3x2(float a, float b)
 {
-    const uint32_t in[4] = {v.x, v.y, v.z, v.w};
-    float x[8], sum = 0.0f;
+    uint16_t v;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %2, %1;" : "=h"(v) : "f"(a), "f"(b));
+    return v;
+}
+__device__ __forceinline__ void from_e4m3x2(uint32_t v, float &a, float &b)
+{
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(uint16_t(v)));
+    asm("{\n\t.reg .f16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\tcvt.f32.f16 %0, lo;\n\tcvt.f32.f16 %1, hi;\n\t}"
+        : "=f"(a), "=f"(b)
+        : "r"(h));
+}
+
+// Row of the B operand that holds term h (hi, lo) of vector tok: pairs of
+// vectors together, so that their sums are adjacent accumulator columns.
+__device__ __forceinline__ int operand_index(int tok, int h) { return (tok >> 1) * 4 + h * 2 + (tok & 1); }
+// Byte of 16-byte piece c of that row in a subgroup's cell (64-byte swizzle).
+__device__ __forceinline__ int operand_offset(int r, int c) { return (r >> 3) * 512 + (r & 7) * 64 + ((c ^ (r >> 1)) & 3) * 16; }
+
+// Stages eight elements of a vector: octet o (0..7) of a subgroup, by the eight
+// consecutive threads of a warp that hold its octets. x: elements 8 o .. 8 o + 7;
+// tok: the vector's index in its block; cell, meta: the subgroup's.
+template <int BITS>
+__device__ __forceinline__ void stage_octet(const float (&x)[8], int o, int tok, uint8_t *cell, uint8_t *meta)
+{
+    float sum = 0.0f;
     uint32_t E = 1;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        x[2 * i] = __uint_as_float(in[i] << 16);
-        x[2 * i + 1] = __uint_as_float(in[i] & 0xffff0000u);
-        E = max(E, max((in[i] >> 7) & 0xffu, (in[i] >> 23) & 0xffu));
+    for (int i = 0; i < 8; ++i) {
+        sum = __fadd_rn(sum, x[i]);
+        E = max(E, (__float_as_uint(x[i]) >> 23) & 0xffu);
     }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) sum = __fadd_rn(sum, x[i]);
 #pragma unroll
     for (int d = 1; d < 8; d *= 2) {
         sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, d));
         E = max(E, __shfl_xor_sync(0xffffffffu, E, d));
     }
-    const int p = max(240 - int(E), 6);  // 6 .. 239
-    // x * 2^(p - position) in two exact steps; what would come out below the
-    // least normal bf16 is more than 2^200 times smaller than the largest x
+    const int p = 134 - int(E);  // the largest |x| becomes 2^7 .. 2^8
     const float p1 = exp2i(p / 2), p2 = exp2i(p - p / 2);
-    uint32_t y[8];
+    uint32_t hi[4], lo[4];  // elements (2i, 2i + 1) as bytes
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int pos = BITS == 4 ? 4 * (i & 1) : 2 * (i & 3);
-        const float s = __fmul_rn(__fmul_rn(__fmul_rn(x[i], p1), p2), exp2i(-pos));
-        y[i] = __float_as_uint(fabsf(s) < 1.17549435e-38f ? 0.0f : s) >> 16;
+    for (int i = 0; i < 4; ++i) {
+        // a 2-bit matrix's odd fields come out of the masks as 4 q
+        const float a = __fmul_rn(__fmul_rn(x[2 * i], p1), p2);
+        const float b = __fmul_rn(__fmul_rn(__fmul_rn(x[2 * i + 1], p1), p2), BITS == 2 ? 0.25f : 1.0f);
+        float ah, bh;
+        hi[i] = to_e4m3x2(a, b);
+        from_e4m3x2(hi[i], ah, bh);
+        lo[i] = to_e4m3x2(__fmul_rn(__fsub_rn(a, ah), 32.0f), __fmul_rn(__fsub_rn(b, bh), 32.0f));
     }
-    uint4 out;
-    if (BITS == 4) {
-        // masks of a word: fields (0,4), (1,5), then of the word >> 8: (2,6), (3,7)
-        out = make_uint4(y[0] | y[4] << 16, y[1] | y[5] << 16, y[2] | y[6] << 16, y[3] | y[7] << 16);
-    } else {
-        // a word spans two octets: (0,8) .. (3,11), then (4,12) .. (7,15)
-        const uint32_t a = y[0] | y[1] << 16, b = y[2] | y[3] << 16, c = y[4] | y[5] << 16, d = y[6] | y[7] << 16;
-        const bool odd = o & 1;
-        const uint32_t r0 = __shfl_xor_sync(0xffffffffu, odd ? a : c, 1);
-        const uint32_t r1 = __shfl_xor_sync(0xffffffffu, odd ? b : d, 1);
-        const uint32_t lo0 = odd ? r0 : a, lo1 = odd ? r1 : b, hi0 = odd ? c : r0, hi1 = odd ? d : r1;
-        out = make_uint4((lo0 & 0xffffu) | hi0 << 16, lo0 >> 16 | (hi0 & 0xffff0000u), (lo1 & 0xffffu) | hi1 << 16,
-                         lo1 >> 16 | (hi1 & 0xffff0000u));
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const uint32_t *v = h ? lo : hi;
+        uint8_t *out = cell + operand_offset(operand_index(tok, h), o >> 1);
+        // bytes of even elements and of odd ones, in order
+        const uint32_t even = __byte_perm(__byte_perm(v[0], v[1], 0x0040), __byte_perm(v[2], v[3], 0x0040), 0x5410);
+        const uint32_t odd = __byte_perm(__byte_perm(v[0], v[1], 0x0051), __byte_perm(v[2], v[3], 0x0051), 0x5410);
+        if (BITS == 4) {
+            // a word's fields 0 2 4 6, then 1 3 5 7
+            *reinterpret_cast<uint2 *>(out + (o & 1) * 8) = make_uint2(even, odd);
+        } else {
+            // a word spans two octets: fields 0 4 8 12, then 1 5 9 13, 2 6 10 14, 3 7 11 15
+            uint16_t *w = reinterpret_cast<uint16_t *>(out) + (o & 1);
+            w[0] = uint16_t(__byte_perm(even, 0, 0x0020));
+            w[2] = uint16_t(__byte_perm(odd, 0, 0x0020));
+            w[4] = uint16_t(__byte_perm(even, 0, 0x0031));
+            w[6] = uint16_t(__byte_perm(odd, 0, 0x0031));
+        }
     }
-    *reinterpret_cast<uint4 *>(cell + (o >> 1) * 32 + ((o ^ tok) & 1) * 16) = out;
     if (o == 0) {
-        float *m = meta + ((tok & 7) >> 1) * 4 + (tok & 1);
+        float *m = reinterpret_cast<float *>(meta + (tok >> 1) * 16) + (tok & 1);
         m[0] = sum;
-        m[2] = exp2i(min(int(E) - 107, 127));
+        m[2] = exp2i(min(int(E) - 125, 127));  // 2^9 / 2^p
     }
 }
 
-// The operand words of one subgroup and row: two for 4 bits, one for 2.
+// Eight bf16 of a 16-byte load as floats.
+__device__ __forceinline__ void widen8(uint4 v, float (&x)[8])
+{
+    const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        x[2 * i] = __uint_as_float(in[i] << 16);
+        x[2 * i + 1] = __uint_as_float(in[i] & 0xffff0000u);
+    }
+}
+
+// A row's 64 packed fields as 16 operand registers, in the order of staged x.
 template <int BITS>
-struct Words {
-    uint32_t w[BITS / 2];
-    __device__ __forceinline__ void load(uint32_t addr)
-    {
-        if (BITS == 4) {
-            const uint2 v = lds_64(addr);
-            w[0] = v.x;
-            w[BITS / 2 - 1] = v.y;
-        } else {
-            w[0] = lds_32(addr);
-        }
-    }
-    // The two operand registers of step q = 0..3.
-    __device__ __forceinline__ void fields(int q, uint32_t &lo, uint32_t &hi) const
-    {
-        if (BITS == 4) {
-            const uint32_t v = q & 1 ? w[q >> 1] >> 8 : w[q >> 1];
-            lo = v & 0x000f000fu;
-            hi = v & 0x00f000f0u;
-        } else {
-            const uint32_t v = q & 2 ? w[0] >> 8 : w[0];
-            lo = v & (q & 1 ? 0x00300030u : 0x00030003u);
-            hi = v & (q & 1 ? 0x00c000c0u : 0x000c000cu);
-        }
-    }
-};
-
-// Adds one subgroup of MT x 16 rows and NT x 8 vectors to y (y[i][n][h]: rows
-// 16 i + 8 h + lane / 4, vectors 8 n + 2 (lane % 4) and the next).
-//  w      shared address of the lane's words in row lane / 4 of the block
-//  pitch  bytes from row to row
-//  s, b   shared addresses of that row's scale and bias; sp bytes from row to row
-//  x[n]   shared address of the lane's 32 bytes in the cell of vector 8 n + lane / 4
-//  odd[n] 16 where that vector's halves are exchanged
-//  meta   shared address of the lane's (sum, sum, f, f) of vectors 0..7
-template <int BITS, int MT, int NT>
-__device__ __forceinline__ void add_subgroup(uint64_t (&y)[2][NT][2], uint32_t w, uint32_t pitch, uint32_t s,
-                                             uint32_t b, uint32_t sp, const uint32_t (&x)[NT], const uint32_t (&odd)[NT],
-                                             uint32_t meta)
+__device__ __forceinline__ void operand_row(const uint32_t (&w)[2 * BITS], uint32_t (&r)[16])
 {
-    Words<BITS> wr[MT][2];
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) wr[i][h].load(w + (16 * i + 8 * h) * pitch);
-    uint4 xa[NT], xb[NT], m[NT];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        xa[n] = lds_128(x[n] + odd[n]);
-        xb[n] = lds_128(x[n] + (odd[n] ^ 16u));
-        m[n] = lds_128(meta + n * kMeta);
-    }
-    float sv[MT][2], bv[MT][2];
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            sv[i][h] = lds_bf16(s + (16 * i + 8 * h) * sp);
-            bv[i][h] = lds_bf16(b + (16 * i + 8 * h) * sp);
-        }
-    float acc[MT][NT][4];
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) acc[i][n][j] = 0.0f;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-#pragma unroll
-        for (int i = 0; i < MT; ++i) {
-            uint32_t a0, a1, a2, a3;
-            wr[i][0].fields(q, a0, a2);
-            wr[i][1].fields(q, a1, a3);
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                const uint4 &v = q < 2 ? xa[n] : xb[n];
-                mma_bf16(acc[i][n], a0, a1, a2, a3, q & 1 ? v.z : v.x, q & 1 ? v.w : v.y);
-            }
+    for (int i = 0; i < 2 * BITS; ++i) {
+        const uint32_t v = w[i], u = v >> 4;
+        if (BITS == 4) {
+            r[(2 * i) & 15] = v & 0x0f0f0f0fu;
+            r[(2 * i + 1) & 15] = u & 0x0f0f0f0fu;
+        } else {
+            r[(4 * i) & 15] = v & 0x03030303u;
+            r[(4 * i + 1) & 15] = v & 0x0c0c0c0cu;
+            r[(4 * i + 2) & 15] = u & 0x03030303u;
+            r[(4 * i + 3) & 15] = u & 0x0c0c0c0cu;
         }
     }
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const uint64_t ss = pack2(sv[i][h], sv[i][h]), bb = pack2(bv[i][h], bv[i][h]);
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                const uint64_t sum = pack2(__uint_as_float(m[n].x), __uint_as_float(m[n].y));
-                const uint64_t f = pack2(__uint_as_float(m[n].z), __uint_as_float(m[n].w));
-                const uint64_t d = mul2(pack2(acc[i][n][2 * h], acc[i][n][2 * h + 1]), f);
-                y[i][n][h] = fma2(ss, d, fma2(bb, sum, y[i][n][h]));
-            }
-        }
 }
 
-// 4-byte asynchronous copy global -> shared of which `bytes` (0, 2 or 4) are
-// read and the rest are zeros.
-__device__ __forceinline__ void copy_word(uint32_t dst, const void *src, uint32_t bytes)
+// ------------------------------------------------------------ tensor memory --
+
+__device__ __forceinline__ void tmem_alloc(uint32_t out, uint32_t columns)
 {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(out), "r"(columns) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
 }
-// An arrival on `bar` when this thread's earlier copies have landed.
-__device__ __forceinline__ void copy_arrive(uint32_t bar)
+__device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t columns)
 {
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(columns) : "memory");
+}
+__device__ __forceinline__ void tmem_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tmem_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+
+// N columns of the warp's 32 lanes.
+__device__ __forceinline__ void tmem_st(uint32_t a, const uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(a),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st1(uint32_t a, float v)
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(a), "f"(v) : "memory");
+}
+__device__ __forceinline__ float tmem_ld1(uint32_t a)
+{
+    float v;
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=f"(v) : "r"(a));
+    return v;
+}
+template <int N>
+__device__ __forceinline__ void tmem_ld(uint32_t a, float (&v)[N])
+{
+    static_assert(N == 4 || N == 8 || N == 16 || N == 32, "columns");
+    if constexpr (N == 4)
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
+                     : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
+                     : "r"(a));
+    else if constexpr (N == 8)
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                     : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
+                     : "r"(a));
+    else if constexpr (N == 16)
+        asm volatile(
+            "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+            : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+              "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+            : "r"(a));
+    else {
+        float lo[16], hi[16];
+        tmem_ld<16>(a, lo);
+        tmem_ld<16>(a + 16, hi);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            v[i] = lo[i];
+            v[16 + i] = hi[i];
+        }
+    }
+}
+
+// Orders what follows after the wait that made `v` valid.
+template <int N>
+__device__ __forceinline__ void settle(float (&v)[N])
+{
+#pragma unroll
+    for (int i = 0; i < N; ++i) asm volatile("" : "+f"(v[i])::"memory");
+}
+
+// D (128 x ND fp32) (+)= A (128 x 32 e4m3, tensor memory) B^T (ND x 32 e4m3, shared memory).
+template <int ND>
+__device__ __forceinline__ void tmem_mma(uint32_t d, uint32_t a, uint64_t b, bool add)
+{
+    // fp32 accumulator, e4m3 operands, both K-major, N = ND, M = 128
+    constexpr uint32_t kind = 1u << 4 | uint32_t(ND >> 3) << 17 | (128u >> 4) << 24;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(kind), "r"(uint32_t(add))
+        : "memory");
+}
+
+// Descriptor of a B operand: rows of 64 bytes under the 64-byte swizzle, eight
+// rows to an atom, `stride` bytes from atom to atom. 32 bytes further along a
+// row is an address 2 units further.
+__device__ __forceinline__ uint64_t b_descriptor(uint32_t addr, uint32_t stride)
+{
+    return uint64_t((addr >> 4) & 0x3fffu) | uint64_t(1) << 16 | uint64_t(stride >> 4) << 32 | uint64_t(1) << 46 |
+           uint64_t(4) << 61;
+}
+
+// An arrival on `bar` when the thread's earlier tensor instructions are done.
+__device__ __forceinline__ void tmem_commit(uint32_t bar)
+{
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
 
 __device__ __forceinline__ void named_sync(int id, int threads)
 {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+// A bounded wait that all of a CTA's roles share: one that runs out sets the
+// device error word and a flag in shared memory, from then on every wait
+// returns at once and the roles run to their ends without computing anything
+// useful (the output of that launch is invalid).
+struct Waits {
+    volatile int *abort;
+    unsigned *err;
+    __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity) const
+    {
+        if (mbar_try_wait(bar, parity)) return true;
+        return slow(bar, parity);
+    }
+    __device__ __noinline__ bool slow(uint32_t bar, uint32_t parity) const
+    {
+        // the global timer is slow to read: left alone at first
+        for (int i = 0; i < 4096; ++i) {
+            if (mbar_try_wait(bar, parity)) return true;
+            if (*abort) return false;
+        }
+        if (mbar_wait_bounded(bar, parity)) return true;
+        atomicOr(err, 1u);
+        *abort = 1;
+        return false;
+    }
+};
+
+// Scales and biases of a thread's row for the subgroups of one slot, as packed
+// pairs of bf16 (subgroups 2i and 2i + 1).
+template <int BITS>
+struct Affine {
+    static constexpr int kSubs = slot_subs(BITS);
+    uint32_t s[kSubs / 2], b[kSubs / 2];
+
+    __device__ __forceinline__ void clear()
+    {
+#pragma unroll
+        for (int i = 0; i < kSubs / 2; ++i) s[i] = b[i] = 0u;
+    }
+    // Row `row` (an index of the whole array), slot index `slot` of the row.
+    // `vec`: G is a multiple of the slot's groups, whose loads are then one
+    // aligned vector.
+    __device__ __forceinline__ void load(const uint16_t *sc, const uint16_t *bi, long long row, int G, int gs, int slot,
+                                         bool vec)
+    {
+        const int per = kSubs * 64 / gs, g0 = slot * per;
+        const uint16_t *ps = sc + row * G + g0, *pb = bi + row * G + g0;
+        if (vec) {
+            if (gs == 64) {
+                get(ps, s);
+                get(pb, b);
+            } else {
+                uint32_t hs[kSubs / 4], hb[kSubs / 4];
+                get(ps, hs);
+                get(pb, hb);
+#pragma unroll
+                for (int i = 0; i < kSubs / 4; ++i) {
+                    s[2 * i] = __byte_perm(hs[i], 0, 0x1010);
+                    s[2 * i + 1] = __byte_perm(hs[i], 0, 0x3232);
+                    b[2 * i] = __byte_perm(hb[i], 0, 0x1010);
+                    b[2 * i + 1] = __byte_perm(hb[i], 0, 0x3232);
+                }
+            }
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < kSubs; ++i) {
+            const int g = i * 64 / gs;
+            uint32_t sv = 0, bv = 0;
+            if (g0 + g < G) {
+                sv = __ldg(ps + g);
+                bv = __ldg(pb + g);
+            }
+            s[i / 2] = i & 1 ? s[i / 2] | sv << 16 : sv;
+            b[i / 2] = i & 1 ? b[i / 2] | bv << 16 : bv;
+        }
+    }
+
+private:
+    template <int N>
+    static __device__ __forceinline__ void get(const uint16_t *p, uint32_t (&v)[N])
+    {
+        if constexpr (N == 1) {
+            v[0] = __ldg(reinterpret_cast<const uint32_t *>(p));
+        } else if constexpr (N == 2) {
+            const uint2 u = __ldg(reinterpret_cast<const uint2 *>(p));
+            v[0] = u.x;
+            v[1] = u.y;
+        } else {
+            const uint4 u = __ldg(reinterpret_cast<const uint4 *>(p));
+            v[0] = u.x;
+            v[1] = u.y;
+            v[2] = u.z;
+            v[3] = u.w;
+        }
+    }
+};
+
+// A worker thread's row of a tile: sums of NC vectors over the slots it is given.
+// Two subgroups are in flight: the accumulator of one is read two subgroups
+// later, when its A columns are needed again.
+template <int BITS, int NC>
+struct Row {
+    static constexpr int kSubs = slot_subs(BITS);
+    uint64_t y[NC / 2];
+    uint32_t last_s, last_b;  // of the previous slot's last two subgroups
+    bool primed;
+
+    __device__ __forceinline__ void start()
+    {
+#pragma unroll
+        for (int i = 0; i < NC / 2; ++i) y[i] = 0ull;
+        last_s = last_b = 0u;
+        primed = false;
+    }
+
+    __device__ __forceinline__ void add(const float (&v)[2 * NC], uint32_t s2, uint32_t b2, int half, uint32_t meta)
+    {
+        const float s = __uint_as_float(half ? s2 & 0xffff0000u : s2 << 16);
+        const float b = __uint_as_float(half ? b2 & 0xffff0000u : b2 << 16);
+        const uint64_t ss = pack2(s, s), bb = pack2(b, b), r32 = pack2(0.03125f, 0.03125f);
+#pragma unroll
+        for (int c = 0; c < NC / 2; ++c) {
+            const uint4 m = lds_128(meta + c * 16);
+            const uint64_t sum = pack2(__uint_as_float(m.x), __uint_as_float(m.y));
+            const uint64_t f = pack2(__uint_as_float(m.z), __uint_as_float(m.w));
+            const uint64_t d = mul2(fma2(pack2(v[4 * c + 2], v[4 * c + 3]), r32, pack2(v[4 * c], v[4 * c + 1])), f);
+            y[c] = fma2(ss, d, fma2(bb, sum, y[c]));
+        }
+    }
+
+    // One slot: `w` is the row's address in it with its swizzle bits, `meta` the
+    // address of the slot's first subgroup's meta and `last_meta` that of the
+    // previous slot's last but one. af, df: the group's barriers (A stored,
+    // accumulator ready), ta, td: its tensor memory.
+    __device__ __forceinline__ void slot(const Waits &wait, uint32_t w, const Affine<BITS> &a, uint32_t meta,
+                                         uint32_t last_meta, uint32_t af, uint32_t df, uint32_t ta, uint32_t td, int lane)
+    {
+        constexpr int MB = meta_bytes(NC), ND = acc_columns(NC);
+#pragma unroll
+        for (int j = 0; j < kSubs; ++j) {
+            uint32_t words[2 * BITS];
+#pragma unroll
+            for (int h = 0; h < BITS / 2; ++h) {
+                const uint4 v = lds_128(w ^ uint32_t((j * (BITS / 2) + h) << 4));
+                words[4 * h] = v.x;
+                words[4 * h + 1] = v.y;
+                words[4 * h + 2] = v.z;
+                words[4 * h + 3] = v.w;
+            }
+            const bool take = j >= 2 || primed;
+            if (take) wait(df + 8 * (j & 1), ((j >> 1) & 1) ^ 1);
+            tmem_fence_after();
+            float v[2 * NC];
+            tmem_ld<2 * NC>(td + (j & 1) * ND, v);
+            uint32_t r[16];
+            operand_row<BITS>(words, r);
+            tmem_st(ta + (j & 1) * 16, r);
+            tmem_wait_ld();
+            settle(v);
+            tmem_wait_st();
+            tmem_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(af + 8 * (j & 1));
+            if (take) {
+                if (j < 2) add(v, last_s, last_b, j, last_meta + j * MB);
+                else add(v, a.s[(j - 2) / 2], a.b[(j - 2) / 2], j & 1, meta + (j - 2) * MB);
+            }
+        }
+        last_s = a.s[kSubs / 2 - 1];
+        last_b = a.b[kSubs / 2 - 1];
+        primed = true;
+    }
+
+    // The four groups' sums of the tile's rows meet in tensor memory (each group
+    // its own A columns, `tm`: the warp's lanes): sums[i] becomes the total of
+    // vector group + 4 i, the groups' sums added in order.
+    static constexpr int kOwn = (NC + 3) / 4;
+    __device__ __forceinline__ void join(uint32_t tm, int group, float (&sums)[kOwn])
+    {
+#pragma unroll
+        for (int c = 0; c < NC / 2; ++c) {
+            float lo, hi;
+            unpack2(y[c], lo, hi);
+            tmem_st1(tm + group * 32 + 2 * c, lo);
+            tmem_st1(tm + group * 32 + 2 * c + 1, hi);
+        }
+        tmem_wait_st();
+        tmem_fence_before();
+        named_sync(1, 32 * kWorkers);
+        tmem_fence_after();
+#pragma unroll
+        for (int i = 0; i < kOwn; ++i) {
+            float v[kGroups];
+            const int t = min(group + 4 * i, NC - 1);
+#pragma unroll
+            for (int g = 0; g < kGroups; ++g) v[g] = tmem_ld1(tm + g * 32 + t);
+            tmem_wait_ld();
+            settle(v);
+            sums[i] = __fadd_rn(__fadd_rn(__fadd_rn(v[0], v[1]), v[2]), v[3]);
+        }
+        tmem_fence_before();
+        named_sync(1, 32 * kWorkers);
+        tmem_fence_after();
+    }
+
+    // The last slot's last two subgroups.
+    __device__ __forceinline__ void finish(const Waits &wait, uint32_t last_meta, uint32_t df, uint32_t td)
+    {
+        if (!primed) return;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            wait(df + 8 * j, 1);
+            tmem_fence_after();
+            float v[2 * NC];
+            tmem_ld<2 * NC>(td + j * acc_columns(NC), v);
+            tmem_wait_ld();
+            settle(v);
+            add(v, last_s, last_b, j, last_meta + j * meta_bytes(NC));
+        }
+    }
+};
+
+// The tensor warp's part of one slot: waits for each subgroup's A operand and
+// multiplies it with the subgroup's cell. `cell` is the first subgroup's.
+template <int BITS, int NC>
+__device__ __forceinline__ void multiply_slot(const Waits &wait, uint32_t cell, uint32_t af, uint32_t df, uint32_t ta,
+                                              uint32_t td)
+{
+    constexpr int ND = acc_columns(NC), CB = cell_bytes(NC);
+#pragma unroll
+    for (int j = 0; j < slot_subs(BITS); ++j) {
+        wait(af + 8 * (j & 1), (j >> 1) & 1);
+        tmem_fence_after();
+        const uint64_t b = b_descriptor(cell + j * CB, NC <= 4 ? 0 : 512);
+        tmem_mma<ND>(td + (j & 1) * ND, ta + (j & 1) * 16, b, false);
+        tmem_mma<ND>(td + (j & 1) * ND, ta + (j & 1) * 16 + 8, b + 2, true);
+        tmem_commit(df + 8 * (j & 1));
+    }
 }
 
 }  // namespace tile

@@ -300,7 +300,8 @@ QMV_API qmv_status qmv_mxfp4_run(const uint32_t *w_q, const uint8_t *scales, con
  *   y[m, n] = sum_i ( s[n, i/gs] q[n, i] + b[n, i/gs] ) x[m, i]
  *             + c[a] sum_r B[a, n, r] ( sum_i A[a, r, i] x[m, i] ),   a = adapter[m]
  *
- *  w_q, scales, biases, x, y, M, N, K, bits, group_size   as for qmv_run.
+ *  w_q, scales, biases, x, y, M, N, K, bits, group_size   as for qmv_run, with
+ *              K at most 65536.
  *  lora_a      device, bf16 [adapters, rank, K], 16-byte aligned.
  *  lora_b      device, bf16 [adapters, N, rank], 16-byte aligned.
  *  adapter     device, int32 [M]: the adapter of each vector. A value outside
