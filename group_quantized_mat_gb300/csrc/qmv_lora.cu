@@ -4,11 +4,14 @@
 //   y[m] = W x[m] + c_a B_a (A_a x[m]),   a = adapter[m].
 //
 // Two kernels.
-//  1. lora_prepare stages x as operand cells (qmv_tile.cuh) and forms the inner
-//     vectors A_a x[m] in fp32, both into the workspace.
+//  1. lora_prepare forms the inner vectors A_a x[m] in fp32, and for more than
+//     kStageHere vectors stages x as operand cells (qmv_tile.cuh), into the
+//     workspace.
 //  2. lora_project streams W once per 16 vectors. It starts under the first
-//     kernel (programmatic launch): its weights are on their way while x is
-//     staged, and the inner vectors are needed only at the end of a tile.
+//     kernel (programmatic launch): its weights are on their way meanwhile, and
+//     the inner vectors are needed only at the end of a tile. Up to kStageHere
+//     vectors every CTA stages x itself, which takes less time than the first
+//     kernel takes to end and be seen to have ended.
 //
 // lora_project, one CTA per SM: a producer thread brings 128 bytes of each row of
 // a tile to a ring of shared-memory slots (one tensor-map box, 128-byte swizzle),
@@ -40,6 +43,7 @@ constexpr int kSmem = 227 * 1024 - 1024;
 constexpr int kMaxK = 1 << 16;
 constexpr int kRangeSubs = 64;  // subgroups of a range of K at most
 constexpr int kPass = 16;       // vectors that one read of the weights serves
+constexpr int kStageHere = 4;   // vectors that lora_project stages itself
 
 struct LoraParams {
     const uint16_t *scales, *biases, *x, *a, *b;
@@ -59,7 +63,7 @@ struct LoraParams {
     int nseg;    // ranges of K
     int range;   // slots of the longest range
     int rows, tiles, grid_rows;
-    int nc, slots, ksplit, stage_blocks;
+    int nc, slots, stage_blocks;
 };
 
 template <int BITS, int NC>
@@ -87,39 +91,28 @@ __global__ void __launch_bounds__(kPrepareThreads) lora_prepare(const LoraParams
         tile::stage_octet<BITS>(x, o, m - z * kPass, p.cells + s * tile::cell_bytes(NC), p.meta + s * tile::meta_bytes(NC));
         return;
     }
-    // inner vectors: ksplit warps for each (vector, row of A), each an even share of K
+    // inner vectors: a block for each (vector, row of A), its warps sharing K
     __shared__ float part[kPrepareThreads / 32];
-    const int warp = tid / 32, lane = tid % 32, per = kPrepareThreads / 32 / p.ksplit;
-    const long long item = (long long)(int(blockIdx.x) - p.stage_blocks) * per + warp / p.ksplit;
+    const int item = int(blockIdx.x) - p.stage_blocks, m = item / p.R, r = item - m * p.R;
+    const int ad = __ldg(p.adapter + m);
+    if (ad < 0 || ad >= p.L) return;
+    const uint4 *a = reinterpret_cast<const uint4 *>(p.a + (size_t(ad) * p.R + r) * p.K);
+    const uint4 *x = reinterpret_cast<const uint4 *>(p.x + size_t(m) * p.K);
     float s = 0.0f;
-    int m = 0, r = 0, ad = -1;
-    if (item < (long long)p.M * p.R) {
-        m = int(item / p.R);
-        r = int(item - (long long)m * p.R);
-        ad = __ldg(p.adapter + m);
-        if (ad >= 0 && ad < p.L) {
-            const uint4 *a = reinterpret_cast<const uint4 *>(p.a + (size_t(ad) * p.R + r) * p.K);
-            const uint4 *x = reinterpret_cast<const uint4 *>(p.x + size_t(m) * p.K);
-            const int n8 = p.K / 8, kw = warp % p.ksplit;
-            const int lo = int((long long)n8 * kw / p.ksplit), hi = int((long long)n8 * (kw + 1) / p.ksplit);
 #pragma unroll 4
-            for (int i = lo + lane; i < hi; i += 32) {
-                const uint4 av = __ldg(a + i), xv = __ldg(x + i);
-                const uint32_t aw[4] = {av.x, av.y, av.z, av.w}, xw[4] = {xv.x, xv.y, xv.z, xv.w};
+    for (int i = tid; i < p.K / 8; i += kPrepareThreads) {
+        float av[8], xv[8];
+        tile::widen8(__ldg(a + i), av);
+        tile::widen8(__ldg(x + i), xv);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    s = __fmaf_rn(__uint_as_float(aw[j] << 16), __uint_as_float(xw[j] << 16), s);
-                    s = __fmaf_rn(__uint_as_float(aw[j] & 0xffff0000u), __uint_as_float(xw[j] & 0xffff0000u), s);
-                }
-            }
-        }
+        for (int j = 0; j < 8; ++j) s = __fmaf_rn(av[j], xv[j], s);
     }
 #pragma unroll
     for (int d = 16; d; d >>= 1) s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, d));
-    if (lane == 0) part[warp] = s;
+    if (tid % 32 == 0) part[tid / 32] = s;
     __syncthreads();
-    if (lane == 0 && warp % p.ksplit == 0 && ad >= 0 && ad < p.L) {
-        for (int j = 1; j < p.ksplit; ++j) s = __fadd_rn(s, part[warp + j]);
+    if (tid == 0) {
+        for (int j = 1; j < kPrepareThreads / 32; ++j) s = __fadd_rn(s, part[j]);
         p.inner[size_t(m) * p.R + r] = s;
     }
 }
@@ -195,11 +188,11 @@ __global__ void __launch_bounds__(tile::kThreads, 1) lora_project(const __grid_c
             mbar_init(stored0 + 8 * i, 4);
             mbar_init(ready0 + 8 * i, 1);
         }
-        mbar_init(xbar, 1);
+        mbar_init(xbar, p.cells ? 1 : kWorkers);
         fence_mbar_init();
         s_abort = 0;
     }
-    if (warp == kWorkers) tmem_alloc(smem_u32(&s_tmem), tmem_columns(NC));
+    if (warp == kWorkers) tmem_alloc(smem_u32(&s_tmem), kTmemColumns);
     tmem_fence_before();
     __syncthreads();
     tmem_fence_after();
@@ -228,19 +221,17 @@ __global__ void __launch_bounds__(tile::kThreads, 1) lora_project(const __grid_c
         const int group = warp - kWorkers;
         if (lane == 0) {
             wait(xbar, 0);
-            const uint32_t ta = tm + group * 32, td = tm + kGroups * 32 + group * 2 * acc_columns(NC);
+            Pipe pipe = Pipe::make<NC>(tm, 0, stored0, ready0, group);
             for (int tl = blockIdx.x; tl < p.tiles; tl += p.grid_rows)
                 for (int i = group; i < ns; i += kGroups)
-                    multiply_slot<BITS, NC>(wait, base + L.x + i * SUBS * cell_bytes(NC), stored0 + 16 * group,
-                                            ready0 + 16 * group, ta, td);
+                    multiply_slot<BITS, NC>(wait, pipe, base + L.x + i * SUBS * cell_bytes(NC));
         }
     } else {
         // ----------------------------------------------------------- workers
         const int group = warp / 4, row = (warp & 3) * 32 + lane, nv = min(kPass, p.M - z * kPass);
         const bool vec = p.G % (SUBS * 64 / p.gs) == 0;
         const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
-        const uint32_t ta = tm + lanes + group * 32, td = tm + lanes + kGroups * 32 + group * 2 * acc_columns(NC);
-        const uint32_t stored = stored0 + 16 * group, ready = ready0 + 16 * group;
+        Pipe pipe = Pipe::make<NC>(tm, lanes, stored0, ready0, group);
         const uint32_t wrow = base + row * kSlotBytes + ((row & 7) << 4);
         Affine<BITS> next;
         {
@@ -249,14 +240,32 @@ __global__ void __launch_bounds__(tile::kThreads, 1) lora_project(const __grid_c
             if (row < p.rows && n < p.N && group < ns) next.load(p.scales, p.biases, n, p.G, p.gs, lo + group, vec);
         }
         grid_launch_dependents();
-        grid_dependency_wait();  // x cells and inner vectors
-        if (tid == 0) {
-            asm volatile("fence.proxy.async;" ::: "memory");
-            const uint32_t cb = uint32_t(ns) * SUBS * cell_bytes(NC), mb = uint32_t(ns) * SUBS * meta_bytes(NC);
-            mbar_arrive_expect_tx(xbar, cb + mb);
-            const size_t sub = size_t(z) * p.subs + size_t(lo) * SUBS;
-            bulk_load_plain(base + L.x, p.cells + sub * cell_bytes(NC), cb, xbar);
-            bulk_load_plain(base + L.meta, p.meta + sub * meta_bytes(NC), mb, xbar);
+        if (p.cells) {
+            grid_dependency_wait();
+            if (tid == 0) {
+                asm volatile("fence.proxy.async;" ::: "memory");
+                const uint32_t cb = uint32_t(ns) * SUBS * cell_bytes(NC), mb = uint32_t(ns) * SUBS * meta_bytes(NC);
+                mbar_arrive_expect_tx(xbar, cb + mb);
+                const size_t sub = size_t(z) * p.subs + size_t(lo) * SUBS;
+                bulk_load_plain(base + L.x, p.cells + sub * cell_bytes(NC), cb, xbar);
+                bulk_load_plain(base + L.meta, p.meta + sub * meta_bytes(NC), mb, xbar);
+            }
+        } else {
+            // eight threads for each (subgroup, vector), the vectors of a
+            // subgroup in a row; whole warps take part (their exchanges need it)
+            const int items = ns * SUBS * nv * 8;
+            for (int i0 = warp * 32; i0 < items; i0 += 32 * kWorkers) {
+                const int i = min(i0 + lane, items - 8 + (lane & 7)), cell = i >> 3, sub = cell / nv, tok = cell - sub * nv;
+                uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                if (lo * SUBS + sub < p.S)
+                    v = __ldg(reinterpret_cast<const uint4 *>(p.x + size_t(tok) * p.K + (lo * SUBS + sub) * 64 + (i & 7) * 8));
+                float x[8];
+                widen8(v, x);
+                stage_octet<BITS>(x, i & 7, tok, smem + L.x + sub * cell_bytes(NC), smem + L.meta + sub * meta_bytes(NC));
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(xbar);
         }
         wait(xbar, 0);
         int it = 0;
@@ -266,6 +275,13 @@ __global__ void __launch_bounds__(tile::kThreads, 1) lora_project(const __grid_c
             Row<BITS, NC> acc;
             acc.start();
             uint32_t last = 0;
+            // the adapters' rows of this tile are on their way to L2 meanwhile
+            for (int t = group; live && t < nv; t += kGroups) {
+                const int ad = __ldg(p.adapter + z * kPass + t);
+                if (ad < 0 || ad >= p.L) continue;
+                const uint16_t *b = p.b + (size_t(ad) * p.N + n) * p.R;
+                for (int r = 0; r < p.R; r += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(b + r));
+            }
             for (int i = group; i < ns; i += kGroups) {
                 const int s = (it + i) % p.slots, lap = (it + i) / p.slots;
                 const Affine<BITS> now = next;
@@ -275,21 +291,22 @@ __global__ void __launch_bounds__(tile::kThreads, 1) lora_project(const __grid_c
                 if (row < p.rows && nn < p.N) next.load(p.scales, p.biases, nn, p.G, p.gs, lo + ni, vec);
                 wait(full0 + 8 * s, lap & 1);
                 const uint32_t meta = base + L.meta + i * SUBS * meta_bytes(NC);
-                acc.slot(wait, wrow + s * L.slot, now, meta, last, stored, ready, ta, td, lane);
-                last = meta + (SUBS - 2) * meta_bytes(NC);
+                acc.slot(wait, pipe, wrow + s * L.slot, now, meta, last, lane);
+                last = meta + (SUBS - 2 * step_subs(NC)) * meta_bytes(NC);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(empty0 + 8 * s);
             }
-            acc.finish(wait, last, ready, td);
+            acc.finish(wait, pipe, last);
             float sums[Row<BITS, NC>::kOwn];
             acc.join(tm + lanes, group, sums);
+            grid_dependency_wait();  // inner vectors, cleared tickets
             bool mine = true;
             if (p.nseg > 1) {
                 const size_t plane = size_t(p.N), seg_stride = plane * NC;
                 float *part = p.partials + size_t(z) * p.nseg * seg_stride + n;
 #pragma unroll
                 for (int i = 0; i < Row<BITS, NC>::kOwn; ++i) {
-                    const int t = group + 4 * i;
+                    const int t = group + kGroups * i;
                     if (live && t < nv) __stcg(part + seg * seg_stride + t * plane, sums[i]);
                 }
                 __threadfence();
@@ -301,7 +318,7 @@ __global__ void __launch_bounds__(tile::kThreads, 1) lora_project(const __grid_c
                     __threadfence();
 #pragma unroll
                     for (int i = 0; i < Row<BITS, NC>::kOwn; ++i) {
-                        const int t = group + 4 * i;
+                        const int t = group + kGroups * i;
                         if (!live || t >= nv) continue;
                         float s = __ldcg(part + t * plane);
                         for (int k = 1; k < p.nseg; ++k) s = __fadd_rn(s, __ldcg(part + k * seg_stride + t * plane));
@@ -312,7 +329,7 @@ __global__ void __launch_bounds__(tile::kThreads, 1) lora_project(const __grid_c
             if (!mine || !live) continue;
 #pragma unroll
             for (int i = 0; i < Row<BITS, NC>::kOwn; ++i) {
-                const int t = group + 4 * i;
+                const int t = group + kGroups * i;
                 if (t >= nv) continue;
                 const int m = z * kPass + t, ad = __ldg(p.adapter + m);
                 float s = sums[i];
@@ -327,7 +344,7 @@ __global__ void __launch_bounds__(tile::kThreads, 1) lora_project(const __grid_c
     tmem_fence_before();
     __syncthreads();
     tmem_fence_after();
-    if (warp == kWorkers) tmem_free(tm, tmem_columns(NC));
+    if (warp == kWorkers) tmem_free(tm, kTmemColumns);
 }
 
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
@@ -357,10 +374,9 @@ LoraParams plan(int M, int N, int K, int bits, int gs, int R, int sms, Sizes &sz
     p.rows = ((N + p.grid_rows * rounds - 1) / (p.grid_rows * rounds) + 7) / 8 * 8;
     p.tiles = (N + p.rows - 1) / p.rows;
     if (p.grid_rows > p.tiles) p.grid_rows = p.tiles;
-    p.ksplit = K <= 4096 ? 1 : K <= 8192 ? 2 : K <= 16384 ? 4 : 8;
     const size_t passes = (M + kPass - 1) / kPass;
-    sz.cells = up256(passes * p.subs * tile::cell_bytes(p.nc));
-    sz.meta = up256(passes * p.subs * tile::meta_bytes(p.nc));
+    sz.cells = M > kStageHere ? up256(passes * p.subs * tile::cell_bytes(p.nc)) : 0;
+    sz.meta = M > kStageHere ? up256(passes * p.subs * tile::meta_bytes(p.nc)) : 0;
     sz.inner = up256(size_t(M) * R * 4);
     sz.counters = p.nseg > 1 ? up256(passes * ((N + 7) / 8) * 4) : 0;
     sz.partials = p.nseg > 1 ? up256(passes * p.nseg * size_t(N) * p.nc * 4) : 0;
@@ -373,8 +389,7 @@ cudaError_t launch_lora(const CUtensorMap &map, LoraParams &p, cudaStream_t stre
 {
     static std::atomic<int> configured[2][64] = {};
     Launch l;
-    const int per = kPrepareThreads / 32 / p.ksplit;
-    l.grid = dim3(p.stage_blocks + (p.M * p.R + per - 1) / per);
+    l.grid = dim3(p.stage_blocks + p.M * p.R);
     l.threads = kPrepareThreads;
     l.smem = 0;
     l.pdl = true;
@@ -444,12 +459,12 @@ extern "C" qmv_status qmv_lora_run(const uint32_t *w_q, const uint16_t *scales, 
     p.L = adapters;
     p.f32_out = (flags & QMV_F32_OUT) != 0;
     uint8_t *at = static_cast<uint8_t *>(ws);
-    p.cells = at; at += sz.cells;
+    p.cells = sz.cells ? at : nullptr; at += sz.cells;
     p.meta = at; at += sz.meta;
     p.inner = reinterpret_cast<float *>(at); at += sz.inner;
     p.counters = p.nseg > 1 ? reinterpret_cast<unsigned *>(at) : nullptr; at += sz.counters;
     p.partials = p.nseg > 1 ? reinterpret_cast<float *>(at) : nullptr;
-    p.stage_blocks = int(((long long)M * p.subs * 8 + kPrepareThreads - 1) / kPrepareThreads);
+    p.stage_blocks = !p.cells ? 0 : int(((long long)M * p.subs * 8 + kPrepareThreads - 1) / kPrepareThreads);
     CUtensorMap map;
     st = encode_rows(&map, w_q, (long long)K * bits / 8, N, tile::kSlotBytes / 8, p.rows);
     if (st != QMV_OK) return st;

@@ -24,17 +24,21 @@
 // The tile. A thread owns a row (a lane of tensor memory). For each subgroup it
 // reads its 32 (2-bit: 16) bytes from the ring, masks them into 16 registers,
 // stores those as its 16 columns of the A operand in tensor memory, and two
-// subgroups later reads the accumulator's columns back and adds s * (..) + b *
-// sum x to its sums, which stay in registers over all of K. What bounds it is the
-// integer pipe (one instruction in two cycles): the masks, 24 for a 4-bit
-// subgroup. Measured with everything resident: 36 bytes of weights a cycle of an
-// SM up to 2 vectors, 32 at 8, 26 at 16 (4-bit), where 6.8 TB/s over 152 SMs are
-// 23.5. Before it, on the same card: bf16 operands (the masks of a low byte are
+// steps (of two subgroups, or of one where 16 vectors need the columns) later
+// reads the accumulator's columns back and adds s * (..) + b * sum x to its sums,
+// which stay in registers over all of K. What bounds it is the integer pipe (one
+// instruction in two cycles), of which the masks are 24 instructions for a 4-bit
+// subgroup, and the latency of a step, which three warps on each scheduler cover.
+// Measured with everything resident, in bytes of 4-bit weights a cycle of an SM
+// (6.8 TB/s over 152 SMs are 23.5): 35 up to 4 vectors, 32 at 8, 24 at 16; with
+// four worker groups, whose warps have 80 registers instead of 128, 40, 36 and 25,
+// but they hold more of the ring while they work; with steps of one subgroup 31
+// and 28. Before it, on the same card: bf16 operands (the masks of a low byte are
 // exact there too, 40 for a subgroup) through tcgen05 25, 24 and 21; through
 // mma.sync, whose instruction holds the issue slot for 8 cycles, 27 and 19.
 //
-// Order. Slot i of a row's range of K belongs to worker group i % 4, which adds
-// its subgroups in order; the four groups' sums are added in order. Nothing
+// Order. Slot i of a row's range of K belongs to worker group i % 3, which adds
+// its subgroups in order; the three groups' sums are added in order. Nothing
 // depends on how many vectors there are.
 #pragma once
 
@@ -43,7 +47,7 @@
 namespace qmv {
 namespace tile {
 
-constexpr int kGroups = 4;                   // worker groups of four warps
+constexpr int kGroups = 3;                   // worker groups of four warps
 constexpr int kWorkers = 4 * kGroups;        // worker warps; then a tensor warp for each group
 constexpr int kThreads = 32 * (kWorkers + kGroups + 1);  // and the producer
 constexpr int kTileRows = 128;
@@ -57,7 +61,11 @@ __host__ __device__ constexpr int meta_bytes(int nc) { return nc / 2 * 16; }
 // Columns of an accumulator (the instruction's N; up to 4 vectors its second
 // eight rows are the first again).
 __host__ __device__ constexpr int acc_columns(int nc) { return nc <= 8 ? 16 : 32; }
-__host__ __device__ constexpr int tmem_columns(int nc) { return nc <= 8 ? 256 : 512; }
+// Subgroups of a step, and a group's columns of A (two steps) and of accumulators.
+__host__ __device__ constexpr int step_subs(int nc) { return nc <= 8 ? 2 : 1; }
+__host__ __device__ constexpr int a_columns(int nc) { return 2 * step_subs(nc) * 16; }
+__host__ __device__ constexpr int d_columns(int nc) { return 2 * step_subs(nc) * acc_columns(nc); }
+constexpr int kTmemColumns = 512;
 
 __device__ __forceinline__ uint64_t pack2(float lo, float hi)
 {
@@ -404,21 +412,38 @@ private:
     }
 };
 
+// A group's barriers (A stored, accumulators ready) and tensor memory; `lanes`
+// is the warp's part of it for workers, 0 for the tensor warp. `steps` counts the
+// group's steps from the launch's start, the same in workers and tensor warp.
+struct Pipe {
+    uint32_t stored, ready, a, d;
+    uint32_t steps;
+
+    template <int NC>
+    __device__ __forceinline__ static Pipe make(uint32_t tm, uint32_t lanes, uint32_t stored0, uint32_t ready0, int group)
+    {
+        return {stored0 + 16 * group, ready0 + 16 * group, tm + lanes + group * a_columns(NC),
+                tm + lanes + kGroups * a_columns(NC) + group * d_columns(NC), 0u};
+    }
+};
+
 // A worker thread's row of a tile: sums of NC vectors over the slots it is given.
-// Two subgroups are in flight: the accumulator of one is read two subgroups
-// later, when its A columns are needed again.
+// Two steps are in flight: the accumulators of one are read two steps later, when
+// its A columns are needed again.
 template <int BITS, int NC>
 struct Row {
-    static constexpr int kSubs = slot_subs(BITS);
+    static constexpr int kSubs = slot_subs(BITS), kStep = step_subs(NC), kSteps = kSubs / kStep;
+    static_assert(kSteps % 2 == 0, "a slot's steps use the two buffers alike");
     uint64_t y[NC / 2];
-    uint32_t last_s, last_b;  // of the previous slot's last two subgroups
+    uint32_t last_s[kStep], last_b[kStep];  // of the previous slot's last two steps, packed pairs
     bool primed;
 
     __device__ __forceinline__ void start()
     {
 #pragma unroll
         for (int i = 0; i < NC / 2; ++i) y[i] = 0ull;
-        last_s = last_b = 0u;
+#pragma unroll
+        for (int i = 0; i < kStep; ++i) last_s[i] = last_b[i] = 0u;
         primed = false;
     }
 
@@ -439,112 +464,136 @@ struct Row {
 
     // One slot: `w` is the row's address in it with its swizzle bits, `meta` the
     // address of the slot's first subgroup's meta and `last_meta` that of the
-    // previous slot's last but one. af, df: the group's barriers (A stored,
-    // accumulator ready), ta, td: its tensor memory.
-    __device__ __forceinline__ void slot(const Waits &wait, uint32_t w, const Affine<BITS> &a, uint32_t meta,
-                                         uint32_t last_meta, uint32_t af, uint32_t df, uint32_t ta, uint32_t td, int lane)
+    // first subgroup of the previous slot's last two steps.
+    __device__ __forceinline__ void slot(const Waits &wait, Pipe &p, uint32_t w, const Affine<BITS> &aff, uint32_t meta,
+                                         uint32_t last_meta, int lane)
     {
         constexpr int MB = meta_bytes(NC), ND = acc_columns(NC);
 #pragma unroll
-        for (int j = 0; j < kSubs; ++j) {
-            uint32_t words[2 * BITS];
+        for (int j = 0; j < kSteps; ++j) {
+            uint32_t words[kStep][2 * BITS];
 #pragma unroll
-            for (int h = 0; h < BITS / 2; ++h) {
-                const uint4 v = lds_128(w ^ uint32_t((j * (BITS / 2) + h) << 4));
-                words[4 * h] = v.x;
-                words[4 * h + 1] = v.y;
-                words[4 * h + 2] = v.z;
-                words[4 * h + 3] = v.w;
-            }
+            for (int u = 0; u < kStep; ++u)
+#pragma unroll
+                for (int h = 0; h < BITS / 2; ++h) {
+                    const uint4 v = lds_128(w ^ uint32_t(((j * kStep + u) * (BITS / 2) + h) << 4));
+                    words[u][4 * h] = v.x;
+                    words[u][4 * h + 1] = v.y;
+                    words[u][4 * h + 2] = v.z;
+                    words[u][4 * h + 3] = v.w;
+                }
             const bool take = j >= 2 || primed;
-            if (take) wait(df + 8 * (j & 1), ((j >> 1) & 1) ^ 1);
+            if (take) wait(p.ready + 8 * (j & 1), ((p.steps + j) / 2 + 1) & 1);
             tmem_fence_after();
-            float v[2 * NC];
-            tmem_ld<2 * NC>(td + (j & 1) * ND, v);
-            uint32_t r[16];
-            operand_row<BITS>(words, r);
-            tmem_st(ta + (j & 1) * 16, r);
+            float v[kStep][2 * NC];
+#pragma unroll
+            for (int u = 0; u < kStep; ++u) tmem_ld<2 * NC>(p.d + ((j & 1) * kStep + u) * ND, v[u]);
+#pragma unroll
+            for (int u = 0; u < kStep; ++u) {
+                uint32_t r[16];
+                operand_row<BITS>(words[u], r);
+                tmem_st(p.a + ((j & 1) * kStep + u) * 16, r);
+            }
             tmem_wait_ld();
-            settle(v);
+#pragma unroll
+            for (int u = 0; u < kStep; ++u) settle(v[u]);
             tmem_wait_st();
             tmem_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(af + 8 * (j & 1));
+            if (lane == 0) mbar_arrive(p.stored + 8 * (j & 1));
             if (take) {
-                if (j < 2) add(v, last_s, last_b, j, last_meta + j * MB);
-                else add(v, a.s[(j - 2) / 2], a.b[(j - 2) / 2], j & 1, meta + (j - 2) * MB);
+#pragma unroll
+                for (int u = 0; u < kStep; ++u) {
+                    const int sub = (j - 2) * kStep + u;  // below 0: of the previous slot
+                    if (j < 2) add(v[u], last_s[(sub + 2 * kStep) / 2], last_b[(sub + 2 * kStep) / 2], sub & 1, last_meta + (sub + 2 * kStep) * MB);
+                    else add(v[u], aff.s[(sub & (kSubs - 1)) / 2], aff.b[(sub & (kSubs - 1)) / 2], sub & 1, meta + sub * MB);
+                }
             }
         }
-        last_s = a.s[kSubs / 2 - 1];
-        last_b = a.b[kSubs / 2 - 1];
+#pragma unroll
+        for (int i = 0; i < kStep; ++i) {
+            last_s[i] = aff.s[kSubs / 2 - kStep + i];
+            last_b[i] = aff.b[kSubs / 2 - kStep + i];
+        }
+        p.steps += kSteps;
         primed = true;
     }
 
-    // The four groups' sums of the tile's rows meet in tensor memory (each group
-    // its own A columns, `tm`: the warp's lanes): sums[i] becomes the total of
-    // vector group + 4 i, the groups' sums added in order.
-    static constexpr int kOwn = (NC + 3) / 4;
+    // The last slot's last two steps.
+    __device__ __forceinline__ void finish(const Waits &wait, const Pipe &p, uint32_t last_meta)
+    {
+        if (!primed) return;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            wait(p.ready + 8 * j, (p.steps / 2 + 1) & 1);
+            tmem_fence_after();
+            float v[kStep][2 * NC];
+#pragma unroll
+            for (int u = 0; u < kStep; ++u) tmem_ld<2 * NC>(p.d + (j * kStep + u) * acc_columns(NC), v[u]);
+            tmem_wait_ld();
+#pragma unroll
+            for (int u = 0; u < kStep; ++u) {
+                settle(v[u]);
+                add(v[u], last_s[(j * kStep + u) / 2], last_b[(j * kStep + u) / 2], (j * kStep + u) & 1,
+                    last_meta + (j * kStep + u) * meta_bytes(NC));
+            }
+        }
+    }
+
+    // The three groups' sums of the tile's rows meet in tensor memory (each group
+    // its own A columns, `tm` being the first with the warp's lanes): sums[i]
+    // becomes the total of vector group + 3 i, the groups' sums added in order.
+    static constexpr int kOwn = (NC + kGroups - 1) / kGroups;
     __device__ __forceinline__ void join(uint32_t tm, int group, float (&sums)[kOwn])
     {
 #pragma unroll
         for (int c = 0; c < NC / 2; ++c) {
             float lo, hi;
             unpack2(y[c], lo, hi);
-            tmem_st1(tm + group * 32 + 2 * c, lo);
-            tmem_st1(tm + group * 32 + 2 * c + 1, hi);
+            tmem_st1(tm + group * a_columns(NC) + 2 * c, lo);
+            tmem_st1(tm + group * a_columns(NC) + 2 * c + 1, hi);
         }
         tmem_wait_st();
         tmem_fence_before();
         named_sync(1, 32 * kWorkers);
         tmem_fence_after();
+        float v[kOwn][kGroups];
+#pragma unroll
+        for (int i = 0; i < kOwn; ++i)
+#pragma unroll
+            for (int g = 0; g < kGroups; ++g) v[i][g] = tmem_ld1(tm + g * a_columns(NC) + min(group + kGroups * i, NC - 1));
+        tmem_wait_ld();
 #pragma unroll
         for (int i = 0; i < kOwn; ++i) {
-            float v[kGroups];
-            const int t = min(group + 4 * i, NC - 1);
-#pragma unroll
-            for (int g = 0; g < kGroups; ++g) v[g] = tmem_ld1(tm + g * 32 + t);
-            tmem_wait_ld();
-            settle(v);
-            sums[i] = __fadd_rn(__fadd_rn(__fadd_rn(v[0], v[1]), v[2]), v[3]);
+            settle(v[i]);
+            sums[i] = __fadd_rn(__fadd_rn(v[i][0], v[i][1]), v[i][2]);
         }
         tmem_fence_before();
         named_sync(1, 32 * kWorkers);
         tmem_fence_after();
     }
-
-    // The last slot's last two subgroups.
-    __device__ __forceinline__ void finish(const Waits &wait, uint32_t last_meta, uint32_t df, uint32_t td)
-    {
-        if (!primed) return;
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            wait(df + 8 * j, 1);
-            tmem_fence_after();
-            float v[2 * NC];
-            tmem_ld<2 * NC>(td + j * acc_columns(NC), v);
-            tmem_wait_ld();
-            settle(v);
-            add(v, last_s, last_b, j, last_meta + j * meta_bytes(NC));
-        }
-    }
 };
 
-// The tensor warp's part of one slot: waits for each subgroup's A operand and
-// multiplies it with the subgroup's cell. `cell` is the first subgroup's.
+// The tensor warp's part of one slot: waits for each step's A operands and
+// multiplies them with the subgroups' cells. `cell` is the slot's first.
 template <int BITS, int NC>
-__device__ __forceinline__ void multiply_slot(const Waits &wait, uint32_t cell, uint32_t af, uint32_t df, uint32_t ta,
-                                              uint32_t td)
+__device__ __forceinline__ void multiply_slot(const Waits &wait, Pipe &p, uint32_t cell)
 {
-    constexpr int ND = acc_columns(NC), CB = cell_bytes(NC);
+    constexpr int ND = acc_columns(NC), CB = cell_bytes(NC), U = step_subs(NC), STEPS = slot_subs(BITS) / U;
 #pragma unroll
-    for (int j = 0; j < slot_subs(BITS); ++j) {
-        wait(af + 8 * (j & 1), (j >> 1) & 1);
+    for (int j = 0; j < STEPS; ++j) {
+        wait(p.stored + 8 * (j & 1), ((p.steps + j) / 2) & 1);
         tmem_fence_after();
-        const uint64_t b = b_descriptor(cell + j * CB, NC <= 4 ? 0 : 512);
-        tmem_mma<ND>(td + (j & 1) * ND, ta + (j & 1) * 16, b, false);
-        tmem_mma<ND>(td + (j & 1) * ND, ta + (j & 1) * 16 + 8, b + 2, true);
-        tmem_commit(df + 8 * (j & 1));
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const uint64_t b = b_descriptor(cell + (j * U + u) * CB, NC <= 4 ? 0 : 512);
+            const uint32_t a = p.a + ((j & 1) * U + u) * 16, d = p.d + ((j & 1) * U + u) * ND;
+            tmem_mma<ND>(d, a, b, false);
+            tmem_mma<ND>(d, a + 8, b + 2, true);
+        }
+        tmem_commit(p.ready + 8 * (j & 1));
     }
+    p.steps += STEPS;
 }
 
 }  // namespace tile
