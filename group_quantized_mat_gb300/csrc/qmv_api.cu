@@ -526,7 +526,7 @@ qmv_status current_device(DeviceInfo *out)
 }
 
 qmv_status encode_rows(CUtensorMap *map, const void *w, long long row_bytes, long long rows, int box_elems,
-                       int box_rows)
+                       int box_rows, bool swizzle)
 {
     auto fn = encode_fn();
     int r = -1;
@@ -536,7 +536,7 @@ qmv_status encode_rows(CUtensorMap *map, const void *w, long long row_bytes, lon
         const cuuint32_t box[2] = {cuuint32_t(box_elems), cuuint32_t(box_rows)};
         const cuuint32_t estr[2] = {1, 1};
         r = int(fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT64, 2, const_cast<void *>(w), dims, strides, box, estr,
-                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE));
     }
     if (r == 0) return QMV_OK;

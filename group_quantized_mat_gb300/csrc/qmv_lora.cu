@@ -4,20 +4,20 @@
 //   y[m] = W x[m] + c_a B_a (A_a x[m]),   a = adapter[m].
 //
 // Two kernels.
-//  1. lora_prepare forms the inner vectors A_a x[m] in fp32, and for more than
-//     kStageHere vectors stages x as operand cells (qmv_tile.cuh), into the
-//     workspace.
+//  1. lora_prepare stages x as operand cells (qmv_tile.cuh) and forms the inner
+//     vectors A_a x[m] in fp32, both into the workspace. (Every CTA of the second
+//     kernel staging x for itself took 3 us for 4 vectors, where the first kernel
+//     and a copy take 1.7.)
 //  2. lora_project streams W once per 16 vectors. It starts under the first
-//     kernel (programmatic launch): its weights are on their way meanwhile, and
-//     the inner vectors are needed only at the end of a tile. Up to kStageHere
-//     vectors every CTA stages x itself, which takes less time than the first
-//     kernel takes to end and be seen to have ended.
+//     kernel (programmatic launch) and asks for its first weights meanwhile; the
+//     rest, which fills the memory system for microseconds, it asks for after the
+//     staged x.
 //
-// lora_project, one CTA per SM: a producer thread brings 128 bytes of each row of
-// a tile to a ring of shared-memory slots (one tensor-map box, 128-byte swizzle),
-// four groups of worker warps run the tiles, four tensor warps multiply. A
-// worker thread owns a row: it reads the row's scales and biases into registers a
-// slot ahead, and in the end adds the adapters' second half to the sums it holds.
+// lora_project, one CTA per SM: a producer warp brings 128 bytes of each row of
+// a tile, with their scales and biases, to a ring of shared-memory slots (one
+// tensor-map box, 128-byte swizzle), three groups of worker warps run the tiles,
+// three tensor warps multiply. A worker thread owns a row, and in the end adds
+// the adapters' second half to the sums it holds.
 //  - Rows go to CTAs in tiles of equal height (a multiple of 8, at most 128): 104
 //    for 15360 rows on 152 SMs.
 //  - K goes to CTAs in ranges of at most 64 subgroups (4096), whose cells of 16
@@ -43,7 +43,7 @@ constexpr int kSmem = 227 * 1024 - 1024;
 constexpr int kMaxK = 1 << 16;
 constexpr int kRangeSubs = 64;  // subgroups of a range of K at most
 constexpr int kPass = 16;       // vectors that one read of the weights serves
-constexpr int kStageHere = 4;   // vectors that lora_project stages itself
+constexpr int kBefore = 3;      // slots of weights asked for before staged x
 
 struct LoraParams {
     const uint16_t *scales, *biases, *x, *a, *b;
@@ -63,14 +63,14 @@ struct LoraParams {
     int nseg;    // ranges of K
     int range;   // slots of the longest range
     int rows, tiles, grid_rows;
-    int nc, slots, stage_blocks;
+    int nc, slots, stage_blocks, sb_buffers;
+    tile::Affines sb;
 };
 
 template <int BITS, int NC>
 __global__ void __launch_bounds__(kPrepareThreads) lora_prepare(const LoraParams p)
 {
     grid_dependency_wait();
-    grid_launch_dependents();
     const int tid = threadIdx.x, passes = (p.M + kPass - 1) / kPass;
     if (p.counters)
         for (int i = blockIdx.x * kPrepareThreads + tid; i < p.tiles * passes; i += gridDim.x * kPrepareThreads)
@@ -85,6 +85,7 @@ __global__ void __launch_bounds__(kPrepareThreads) lora_prepare(const LoraParams
         const int m = int(cell / p.subs), sub = int(cell - (long long)m * p.subs), z = m / kPass;
         uint4 v = make_uint4(0u, 0u, 0u, 0u);
         if (sub < p.S) v = __ldg(reinterpret_cast<const uint4 *>(p.x + size_t(m) * p.K + sub * 64 + o * 8));
+        grid_launch_dependents();
         float x[8];
         tile::widen8(v, x);
         const size_t s = size_t(z) * p.subs + sub;
@@ -95,10 +96,11 @@ __global__ void __launch_bounds__(kPrepareThreads) lora_prepare(const LoraParams
     __shared__ float part[kPrepareThreads / 32];
     const int item = int(blockIdx.x) - p.stage_blocks, m = item / p.R, r = item - m * p.R;
     const int ad = __ldg(p.adapter + m);
-    if (ad < 0 || ad >= p.L) return;
+    if (ad < 0 || ad >= p.L) return;  // which also lets the next kernel start
     const uint4 *a = reinterpret_cast<const uint4 *>(p.a + (size_t(ad) * p.R + r) * p.K);
     const uint4 *x = reinterpret_cast<const uint4 *>(p.x + size_t(m) * p.K);
     float s = 0.0f;
+    grid_launch_dependents();
 #pragma unroll 4
     for (int i = tid; i < p.K / 8; i += kPrepareThreads) {
         float av[8], xv[8];
@@ -118,7 +120,7 @@ __global__ void __launch_bounds__(kPrepareThreads) lora_prepare(const LoraParams
 }
 
 struct Layout {
-    int slots, slot, x, meta, bars, total;
+    int slots, slot, x, meta, sb, inner, bars, total;
 };
 
 __host__ __device__ inline Layout layout(const LoraParams &p, int bits, int nc)
@@ -133,52 +135,91 @@ __host__ __device__ inline Layout layout(const LoraParams &p, int bits, int nc)
         l.x = (p.slots - 1) * l.slot + tile::kTileRows * tile::kSlotBytes;
     l.x = (l.x + 1023) & ~1023;
     l.meta = l.x + subs * tile::cell_bytes(nc);
-    l.bars = l.meta + subs * tile::meta_bytes(nc);
-    l.total = l.bars + (2 * p.slots + 4 * tile::kGroups + 1) * 8;
+    l.sb = (l.meta + subs * tile::meta_bytes(nc) + 127) & ~127;
+    l.inner = l.sb + p.sb_buffers * 2 * p.sb.block;
+    l.bars = l.inner + nc * p.R * 4;
+    l.bars = (l.bars + 15) & ~15;
+    l.total = l.bars + (2 * p.slots + 4 * tile::kGroups + 5) * 8;
     return l;
 }
 
-// c * (B v) of one output: row n of the adapter's B with the vector's inner.
-__device__ __forceinline__ float adapter_term(const LoraParams &p, int ad, int m, int n)
+// Adds c * (B v) to sums[i] for the thread's vectors (ads[i] their adapters, -1:
+// none) in row n of the adapters' B, v(i) being the address of vector i's inner
+// vector in shared memory: 16 of the rank at a time, so that the loads of all
+// vectors are in flight together.
+template <int OWN>
+__device__ __forceinline__ void add_adapters(const LoraParams &p, const int (&ads)[OWN], const float *inner, int n,
+                                             float (&sums)[OWN])
 {
-    const uint16_t *b = p.b + (size_t(ad) * p.N + n) * p.R;
-    const float *v = p.inner + size_t(m) * p.R;
-    float d = 0.0f;
+    float d[OWN];
+#pragma unroll
+    for (int i = 0; i < OWN; ++i) d[i] = 0.0f;
     if (p.R % 8 == 0) {
-#pragma unroll 2
-        for (int r = 0; r < p.R; r += 8) {
-            const uint4 bw = __ldg(reinterpret_cast<const uint4 *>(b + r));
-            const float4 v0 = *reinterpret_cast<const float4 *>(v + r), v1 = *reinterpret_cast<const float4 *>(v + r + 4);
-            d = __fmaf_rn(__uint_as_float(bw.x << 16), v0.x, d);
-            d = __fmaf_rn(__uint_as_float(bw.x & 0xffff0000u), v0.y, d);
-            d = __fmaf_rn(__uint_as_float(bw.y << 16), v0.z, d);
-            d = __fmaf_rn(__uint_as_float(bw.y & 0xffff0000u), v0.w, d);
-            d = __fmaf_rn(__uint_as_float(bw.z << 16), v1.x, d);
-            d = __fmaf_rn(__uint_as_float(bw.z & 0xffff0000u), v1.y, d);
-            d = __fmaf_rn(__uint_as_float(bw.w << 16), v1.z, d);
-            d = __fmaf_rn(__uint_as_float(bw.w & 0xffff0000u), v1.w, d);
+#pragma unroll 1
+        for (int r = 0; r < p.R; r += 16) {
+            const bool two = r + 8 < p.R;
+            uint4 b[OWN][2];
+#pragma unroll
+            for (int i = 0; i < OWN; ++i)
+                if (ads[i] >= 0) {
+                    const uint4 *q = reinterpret_cast<const uint4 *>(p.b + (size_t(ads[i]) * p.N + n) * p.R + r);
+                    b[i][0] = __ldg(q);
+                    if (two) b[i][1] = __ldg(q + 1);
+                }
+#pragma unroll
+            for (int i = 0; i < OWN; ++i)
+                if (ads[i] >= 0) {
+                    const float4 *v = reinterpret_cast<const float4 *>(inner + (tile::kGroups * i) * p.R + r);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        if (h && !two) break;
+                        float x[8];
+                        tile::widen8(b[i][h], x);
+                        const float4 v0 = v[2 * h], v1 = v[2 * h + 1];
+                        const float w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) d[i] = __fmaf_rn(x[j], w[j], d[i]);
+                    }
+                }
         }
     } else {
 #pragma unroll 4
-        for (int r = 0; r < p.R; ++r) d = __fmaf_rn(__uint_as_float(uint32_t(__ldg(b + r)) << 16), v[r], d);
+        for (int r = 0; r < p.R; ++r)
+#pragma unroll
+            for (int i = 0; i < OWN; ++i)
+                if (ads[i] >= 0)
+                    d[i] = __fmaf_rn(__uint_as_float(uint32_t(__ldg(p.b + (size_t(ads[i]) * p.N + n) * p.R + r)) << 16),
+                                     inner[(tile::kGroups * i) * p.R + r], d[i]);
     }
-    return __fmul_rn(__ldg(p.c + ad), d);
+#pragma unroll
+    for (int i = 0; i < OWN; ++i)
+        if (ads[i] >= 0) sums[i] = __fadd_rn(sums[i], __fmul_rn(__ldg(p.c + ads[i]), d[i]));
 }
 
-template <int BITS, int NC>
+template <int BITS, int GS, int NC>
 __global__ void __launch_bounds__(tile::kThreads, 1) lora_project(const __grid_constant__ CUtensorMap map,
+                                                                  const __grid_constant__ CUtensorMap smap,
+                                                                  const __grid_constant__ CUtensorMap bmap,
                                                                   const LoraParams p)
 {
     using namespace tile;
     extern __shared__ __align__(1024) uint8_t smem[];
-    __shared__ int s_abort, s_last;
+    __shared__ int s_abort, s_last, s_ad[kPass];
     __shared__ uint32_t s_tmem;
     constexpr int SUBS = slot_subs(BITS);
     const Layout L = layout(p, BITS, NC);
     const uint32_t base = smem_u32(smem), full0 = base + L.bars, empty0 = full0 + 8 * p.slots;
     const uint32_t stored0 = empty0 + 8 * p.slots, ready0 = stored0 + 16 * kGroups, xbar = ready0 + 16 * kGroups;
+    const uint32_t sfull0 = xbar + 8, sempty0 = sfull0 + 16;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-    const int seg = blockIdx.y, z = blockIdx.z;
+    const int seg = blockIdx.y, z = blockIdx.z, nv = min(kPass, p.M - z * kPass);
+    const int lo = int((long long)p.NS * seg / p.nseg), ns = int((long long)p.NS * (seg + 1) / p.nseg) - lo;
+    const int g0 = lo * SUBS * 64 / GS, groups = min(ns * SUBS * 64 / GS, p.G - g0);
+    if (tid >= 64 && tid < 64 + kPass) {
+        // the adapters of this pass's vectors, -1: none
+        const int t = tid - 64, ad = t < nv ? __ldg(p.adapter + z * kPass + t) : -1;
+        s_ad[t] = ad < p.L ? ad : -1;
+    }
     if (tid == 0) {
         for (int i = 0; i < p.slots; ++i) {
             mbar_init(full0 + 8 * i, 1);
@@ -188,7 +229,11 @@ __global__ void __launch_bounds__(tile::kThreads, 1) lora_project(const __grid_c
             mbar_init(stored0 + 8 * i, 4);
             mbar_init(ready0 + 8 * i, 1);
         }
-        mbar_init(xbar, p.cells ? 1 : kWorkers);
+        mbar_init(xbar, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(sfull0 + 8 * i, p.sb.arrivals());
+            mbar_init(sempty0 + 8 * i, kWorkers);
+        }
         fence_mbar_init();
         s_abort = 0;
     }
@@ -198,23 +243,52 @@ __global__ void __launch_bounds__(tile::kThreads, 1) lora_project(const __grid_c
     tmem_fence_after();
     const uint32_t tm = s_tmem;
     const Waits wait{&s_abort, p.err};
-    const int lo = int((long long)p.NS * seg / p.nseg), ns = int((long long)p.NS * (seg + 1) / p.nseg) - lo;
+
+    // staged x by bulk copies, once the first kernel has ended
+    auto fetch_x = [&]() {
+        grid_dependency_wait();
+        asm volatile("fence.proxy.async;" ::: "memory");
+        const uint32_t cb = uint32_t(ns) * SUBS * cell_bytes(NC), mb = uint32_t(ns) * SUBS * meta_bytes(NC);
+        mbar_arrive_expect_tx(xbar, cb + mb);
+        const size_t sub = size_t(z) * p.subs + size_t(lo) * SUBS;
+        bulk_load_plain(base + L.x, p.cells + sub * cell_bytes(NC), cb, xbar);
+        bulk_load_plain(base + L.meta, p.meta + sub * meta_bytes(NC), mb, xbar);
+    };
 
     if (warp == kThreads / 32 - 1) {
         // ---------------------------------------------------------- producer
-        if (lane == 0) {
-            int it = 0;
-            const uint32_t bytes = uint32_t(p.rows) * kSlotBytes;
-            for (int tl = blockIdx.x; tl < p.tiles && !*wait.abort; tl += p.grid_rows)
+        int it = 0, tiles = 0;
+        bool staged = false, ok = true;
+        const uint32_t bytes = uint32_t(p.rows) * kSlotBytes;
+        for (int tl = blockIdx.x; tl < p.tiles && ok; tl += p.grid_rows, ++tiles) {
+            const int buf = tiles % p.sb_buffers, turn = tiles / p.sb_buffers;
+            ok = __all_sync(0xffffffffu, turn == 0 || wait(sempty0 + 8 * buf, (turn - 1) & 1));
+            if (!ok) break;
+            p.sb.fetch(base + L.sb + buf * 2 * p.sb.block, smem + L.sb + buf * 2 * p.sb.block, p.scales, p.biases, &smap, &bmap,
+                       (long long)tl * p.rows, p.rows, p.N, p.G, g0, groups, sfull0 + 8 * buf, lane);
+            if (lane == 0)
                 for (int i = 0; i < ns; ++i, ++it) {
+                    if (!staged && it == min(kBefore, ns)) {
+                        staged = true;
+                        fetch_x();
+                    }
                     const int s = it % p.slots, lap = it / p.slots;
-                    if (lap > 0 && !wait(empty0 + 8 * s, (lap - 1) & 1)) break;
+                    ok = lap == 0 || wait(empty0 + 8 * s, (lap - 1) & 1);
+                    if (!ok) break;
                     mbar_arrive_expect_tx(full0 + 8 * s, bytes);
                     tma_load_2d(base + s * L.slot, &map, (lo + i) * (kSlotBytes / 8), tl * p.rows, full0 + 8 * s);
                 }
-            if (*wait.abort)  // copies in flight end before the CTA does
+            ok = __all_sync(0xffffffffu, ok);
+        }
+        if (lane == 0) {
+            if (!staged) fetch_x();
+            if (!ok) {  // copies in flight end before the CTA does
                 for (int j = max(0, it - p.slots); j < it; ++j)
                     (void)mbar_wait_bounded(full0 + 8 * (j % p.slots), (j / p.slots) & 1);
+                for (int j = max(0, tiles - p.sb_buffers); j < tiles; ++j)
+                    (void)mbar_wait_bounded(sfull0 + 8 * (j % p.sb_buffers), (j / p.sb_buffers) & 1);
+                (void)mbar_wait_bounded(xbar, 0);
+            }
         }
     } else if (warp >= kWorkers) {
         // ------------------------------------------------------ tensor warps
@@ -228,84 +302,59 @@ __global__ void __launch_bounds__(tile::kThreads, 1) lora_project(const __grid_c
         }
     } else {
         // ----------------------------------------------------------- workers
-        const int group = warp / 4, row = (warp & 3) * 32 + lane, nv = min(kPass, p.M - z * kPass);
-        const bool vec = p.G % (SUBS * 64 / p.gs) == 0;
+        const int group = warp / 4, row = (warp & 3) * 32 + lane;
         const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
         Pipe pipe = Pipe::make<NC>(tm, lanes, stored0, ready0, group);
         const uint32_t wrow = base + row * kSlotBytes + ((row & 7) << 4);
-        Affine<BITS> next;
-        {
-            const int n = blockIdx.x * p.rows + row;
-            next.clear();
-            if (row < p.rows && n < p.N && group < ns) next.load(p.scales, p.biases, n, p.G, p.gs, lo + group, vec);
-        }
         grid_launch_dependents();
-        if (p.cells) {
-            grid_dependency_wait();
-            if (tid == 0) {
-                asm volatile("fence.proxy.async;" ::: "memory");
-                const uint32_t cb = uint32_t(ns) * SUBS * cell_bytes(NC), mb = uint32_t(ns) * SUBS * meta_bytes(NC);
-                mbar_arrive_expect_tx(xbar, cb + mb);
-                const size_t sub = size_t(z) * p.subs + size_t(lo) * SUBS;
-                bulk_load_plain(base + L.x, p.cells + sub * cell_bytes(NC), cb, xbar);
-                bulk_load_plain(base + L.meta, p.meta + sub * meta_bytes(NC), mb, xbar);
-            }
-        } else {
-            // eight threads for each (subgroup, vector), the vectors of a
-            // subgroup in a row; whole warps take part (their exchanges need it)
-            const int items = ns * SUBS * nv * 8;
-            for (int i0 = warp * 32; i0 < items; i0 += 32 * kWorkers) {
-                const int i = min(i0 + lane, items - 8 + (lane & 7)), cell = i >> 3, sub = cell / nv, tok = cell - sub * nv;
-                uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                if (lo * SUBS + sub < p.S)
-                    v = __ldg(reinterpret_cast<const uint4 *>(p.x + size_t(tok) * p.K + (lo * SUBS + sub) * 64 + (i & 7) * 8));
-                float x[8];
-                widen8(v, x);
-                stage_octet<BITS>(x, i & 7, tok, smem + L.x + sub * cell_bytes(NC), smem + L.meta + sub * meta_bytes(NC));
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(xbar);
-        }
         wait(xbar, 0);
-        int it = 0;
-        for (int tl = blockIdx.x; tl < p.tiles; tl += p.grid_rows, it += ns) {
+        int it = 0, tiles = 0;
+        const int align = p.sb.alignment(p.G);
+        for (int tl = blockIdx.x; tl < p.tiles; tl += p.grid_rows, it += ns, ++tiles) {
             const int n = tl * p.rows + row;
             const bool live = row < p.rows && n < p.N;
-            Row<BITS, NC> acc;
+            Row<BITS, GS, NC> acc;
             acc.start();
             uint32_t last = 0;
             // the adapters' rows of this tile are on their way to L2 meanwhile
-            for (int t = group; live && t < nv; t += kGroups) {
-                const int ad = __ldg(p.adapter + z * kPass + t);
-                if (ad < 0 || ad >= p.L) continue;
-                const uint16_t *b = p.b + (size_t(ad) * p.N + n) * p.R;
-                for (int r = 0; r < p.R; r += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(b + r));
-            }
+            if (live)
+                for (int t = group; t < nv; t += kGroups) {
+                    if (s_ad[t] < 0) continue;
+                    const uint16_t *b = p.b + (size_t(s_ad[t]) * p.N + n) * p.R;
+                    for (int r = 0; r < p.R; r += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(b + r));
+                }
+            const int buf = tiles % p.sb_buffers;
+            wait(sfull0 + 8 * buf, (tiles / p.sb_buffers) & 1);
+            const uint32_t sb = base + L.sb + buf * 2 * p.sb.block + min(row, p.rows - 1) * p.sb.pitch + p.sb.offset(n, p.G, g0);
+#pragma unroll 1
             for (int i = group; i < ns; i += kGroups) {
                 const int s = (it + i) % p.slots, lap = (it + i) / p.slots;
-                const Affine<BITS> now = next;
-                // the next slot's, of this tile or of the next
-                const int ni = i + kGroups < ns ? i + kGroups : group, nn = i + kGroups < ns ? n : n + p.grid_rows * p.rows;
-                next.clear();
-                if (row < p.rows && nn < p.N) next.load(p.scales, p.biases, nn, p.G, p.gs, lo + ni, vec);
                 wait(full0 + 8 * s, lap & 1);
                 const uint32_t meta = base + L.meta + i * SUBS * meta_bytes(NC);
-                acc.slot(wait, pipe, wrow + s * L.slot, now, meta, last, lane);
+                Affine<BITS, GS> aff;
+                aff.read(sb + i * Affine<BITS, GS>::kGroupsPerSlot * 2, p.sb.block, align,
+                         groups - i * Affine<BITS, GS>::kGroupsPerSlot);
+                acc.slot(wait, pipe, wrow + s * L.slot, aff, meta, last, lane);
                 last = meta + (SUBS - 2 * step_subs(NC)) * meta_bytes(NC);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(empty0 + 8 * s);
             }
+            if (lane == 0) mbar_arrive(sempty0 + 8 * buf);
             acc.finish(wait, pipe, last);
-            float sums[Row<BITS, NC>::kOwn];
-            acc.join(tm + lanes, group, sums);
-            grid_dependency_wait();  // inner vectors, cleared tickets
+            if (tiles == 0) {
+                // the inner vectors (of vectors without an adapter: whatever is there)
+                grid_dependency_wait();
+                for (int i = tid; i < nv * p.R; i += 32 * kWorkers)
+                    reinterpret_cast<float *>(smem + L.inner)[i] = __ldcg(p.inner + size_t(z) * kPass * p.R + i);
+            }
+            float sums[Row<BITS, GS, NC>::kOwn];
+            acc.join(tm + lanes, group, sums);  // its barriers also publish the inner vectors
             bool mine = true;
             if (p.nseg > 1) {
                 const size_t plane = size_t(p.N), seg_stride = plane * NC;
                 float *part = p.partials + size_t(z) * p.nseg * seg_stride + n;
 #pragma unroll
-                for (int i = 0; i < Row<BITS, NC>::kOwn; ++i) {
+                for (int i = 0; i < Row<BITS, GS, NC>::kOwn; ++i) {
                     const int t = group + kGroups * i;
                     if (live && t < nv) __stcg(part + seg * seg_stride + t * plane, sums[i]);
                 }
@@ -317,7 +366,7 @@ __global__ void __launch_bounds__(tile::kThreads, 1) lora_project(const __grid_c
                 if (mine) {
                     __threadfence();
 #pragma unroll
-                    for (int i = 0; i < Row<BITS, NC>::kOwn; ++i) {
+                    for (int i = 0; i < Row<BITS, GS, NC>::kOwn; ++i) {
                         const int t = group + kGroups * i;
                         if (!live || t >= nv) continue;
                         float s = __ldcg(part + t * plane);
@@ -327,16 +376,17 @@ __global__ void __launch_bounds__(tile::kThreads, 1) lora_project(const __grid_c
                 }
             }
             if (!mine || !live) continue;
+            int ads[Row<BITS, GS, NC>::kOwn];
 #pragma unroll
-            for (int i = 0; i < Row<BITS, NC>::kOwn; ++i) {
+            for (int i = 0; i < Row<BITS, GS, NC>::kOwn; ++i) ads[i] = group + kGroups * i < nv ? s_ad[group + kGroups * i] : -1;
+            add_adapters(p, ads, reinterpret_cast<const float *>(smem + L.inner) + group * p.R, n, sums);
+#pragma unroll
+            for (int i = 0; i < Row<BITS, GS, NC>::kOwn; ++i) {
                 const int t = group + kGroups * i;
                 if (t >= nv) continue;
-                const int m = z * kPass + t, ad = __ldg(p.adapter + m);
-                float s = sums[i];
-                if (ad >= 0 && ad < p.L) s = __fadd_rn(s, adapter_term(p, ad, m, n));
-                const size_t at = size_t(m) * p.N + n;
-                if (p.f32_out) static_cast<float *>(p.y)[at] = s;
-                else static_cast<__nv_bfloat16 *>(p.y)[at] = __float2bfloat16_rn(s);
+                const size_t at = size_t(z * kPass + t) * p.N + n;
+                if (p.f32_out) static_cast<float *>(p.y)[at] = sums[i];
+                else static_cast<__nv_bfloat16 *>(p.y)[at] = __float2bfloat16_rn(sums[i]);
             }
         }
     }
@@ -374,9 +424,11 @@ LoraParams plan(int M, int N, int K, int bits, int gs, int R, int sms, Sizes &sz
     p.rows = ((N + p.grid_rows * rounds - 1) / (p.grid_rows * rounds) + 7) / 8 * 8;
     p.tiles = (N + p.rows - 1) / p.rows;
     if (p.grid_rows > p.tiles) p.grid_rows = p.tiles;
+    p.sb = tile::Affines::plan(p.G, p.range * slot_subs * 64 / gs, p.rows);
+    p.sb_buffers = rounds > 1 ? 2 : 1;
     const size_t passes = (M + kPass - 1) / kPass;
-    sz.cells = M > kStageHere ? up256(passes * p.subs * tile::cell_bytes(p.nc)) : 0;
-    sz.meta = M > kStageHere ? up256(passes * p.subs * tile::meta_bytes(p.nc)) : 0;
+    sz.cells = up256(passes * p.subs * tile::cell_bytes(p.nc));
+    sz.meta = up256(passes * p.subs * tile::meta_bytes(p.nc));
     sz.inner = up256(size_t(M) * R * 4);
     sz.counters = p.nseg > 1 ? up256(passes * ((N + 7) / 8) * 4) : 0;
     sz.partials = p.nseg > 1 ? up256(passes * p.nseg * size_t(N) * p.nc * 4) : 0;
@@ -385,9 +437,9 @@ LoraParams plan(int M, int N, int K, int bits, int gs, int R, int sms, Sizes &sz
 }
 
 template <int BITS, int NC>
-cudaError_t launch_lora(const CUtensorMap &map, LoraParams &p, cudaStream_t stream)
+cudaError_t launch_lora(const RingMaps &maps, LoraParams &p, cudaStream_t stream)
 {
-    static std::atomic<int> configured[2][64] = {};
+    static std::atomic<int> configured[3][64] = {};
     Launch l;
     l.grid = dim3(p.stage_blocks + p.M * p.R);
     l.threads = kPrepareThreads;
@@ -398,21 +450,24 @@ cudaError_t launch_lora(const CUtensorMap &map, LoraParams &p, cudaStream_t stre
     l.grid = dim3(p.grid_rows, p.nseg, (p.M + kPass - 1) / kPass);
     l.threads = tile::kThreads;
     l.smem = size_t(layout(p, BITS, NC).total);
-    return launch_one(lora_project<BITS, NC>, configured[1], l, stream, map, p);
+    if (p.gs == 64) return launch_one(lora_project<BITS, 64, NC>, configured[1], l, stream, maps.w, maps.s, maps.b, p);
+    return launch_one(lora_project<BITS, 128, NC>, configured[2], l, stream, maps.w, maps.s, maps.b, p);
 }
 
 template <int BITS>
-cudaError_t launch_lora(const CUtensorMap &map, LoraParams &p, cudaStream_t stream)
+cudaError_t launch_lora(const RingMaps &maps, LoraParams &p, cudaStream_t stream)
 {
     // as many slots as fit
+    p.slots = 4;
+    if (layout(p, BITS, p.nc).total > kSmem) p.sb_buffers = 1;
     p.slots = kMaxSlotsLora;
     while (p.slots > 2 && layout(p, BITS, p.nc).total > kSmem) --p.slots;
     if (layout(p, BITS, p.nc).total > kSmem) return cudaErrorInvalidConfiguration;
     switch (p.nc) {
-        case 2: return launch_lora<BITS, 2>(map, p, stream);
-        case 4: return launch_lora<BITS, 4>(map, p, stream);
-        case 8: return launch_lora<BITS, 8>(map, p, stream);
-        default: return launch_lora<BITS, 16>(map, p, stream);
+        case 2: return launch_lora<BITS, 2>(maps, p, stream);
+        case 4: return launch_lora<BITS, 4>(maps, p, stream);
+        case 8: return launch_lora<BITS, 8>(maps, p, stream);
+        default: return launch_lora<BITS, 16>(maps, p, stream);
     }
 }
 
@@ -459,16 +514,18 @@ extern "C" qmv_status qmv_lora_run(const uint32_t *w_q, const uint16_t *scales, 
     p.L = adapters;
     p.f32_out = (flags & QMV_F32_OUT) != 0;
     uint8_t *at = static_cast<uint8_t *>(ws);
-    p.cells = sz.cells ? at : nullptr; at += sz.cells;
+    p.cells = at; at += sz.cells;
     p.meta = at; at += sz.meta;
     p.inner = reinterpret_cast<float *>(at); at += sz.inner;
     p.counters = p.nseg > 1 ? reinterpret_cast<unsigned *>(at) : nullptr; at += sz.counters;
     p.partials = p.nseg > 1 ? reinterpret_cast<float *>(at) : nullptr;
-    p.stage_blocks = !p.cells ? 0 : int(((long long)M * p.subs * 8 + kPrepareThreads - 1) / kPrepareThreads);
-    CUtensorMap map;
-    st = encode_rows(&map, w_q, (long long)K * bits / 8, N, tile::kSlotBytes / 8, p.rows);
+    p.stage_blocks = int(((long long)M * p.subs * 8 + kPrepareThreads - 1) / kPrepareThreads);
+    RingMaps maps{};
+    st = encode_rows(&maps.w, w_q, (long long)K * bits / 8, N, tile::kSlotBytes / 8, p.rows, true);
+    if (st == QMV_OK && p.sb.mode == tile::kSbBoxes) st = encode_rows(&maps.s, scales, p.G * 2ll, N, p.sb.pitch / 8, p.rows, false);
+    if (st == QMV_OK && p.sb.mode == tile::kSbBoxes) st = encode_rows(&maps.b, biases, p.G * 2ll, N, p.sb.pitch / 8, p.rows, false);
     if (st != QMV_OK) return st;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const cudaError_t e = bits == 4 ? launch_lora<4>(map, p, s) : launch_lora<2>(map, p, s);
+    const cudaError_t e = bits == 4 ? launch_lora<4>(maps, p, s) : launch_lora<2>(maps, p, s);
     return e == cudaSuccess ? QMV_OK : record_cuda_failure("lora kernel launch", e);
 }

@@ -135,11 +135,9 @@ __device__ __forceinline__ void stage_octet(const float (&x)[8], int o, int tok,
         sum = __fadd_rn(sum, x[i]);
         E = max(E, (__float_as_uint(x[i]) >> 23) & 0xffu);
     }
+    E = __reduce_max_sync(0xffu << (threadIdx.x & 24), E);
 #pragma unroll
-    for (int d = 1; d < 8; d *= 2) {
-        sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, d));
-        E = max(E, __shfl_xor_sync(0xffffffffu, E, d));
-    }
+    for (int d = 1; d < 8; d *= 2) sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, d));
     const int p = 134 - int(E);  // the largest |x| becomes 2^7 .. 2^8
     const float p1 = exp2i(p / 2), p2 = exp2i(p - p / 2);
     uint32_t hi[4], lo[4];  // elements (2i, 2i + 1) as bytes
@@ -324,90 +322,144 @@ struct Waits {
     unsigned *err;
     __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity) const
     {
-        if (mbar_try_wait(bar, parity)) return true;
-        return slow(bar, parity);
-    }
-    __device__ __noinline__ bool slow(uint32_t bar, uint32_t parity) const
-    {
-        // the global timer is slow to read: left alone at first
-        for (int i = 0; i < 4096; ++i) {
+        // bounded by attempts alone (tens of milliseconds at least): the global
+        // timer takes longer to read than most waits last
+#pragma unroll 1
+        for (int i = 1; i < 1 << 22; ++i) {
             if (mbar_try_wait(bar, parity)) return true;
-            if (*abort) return false;
+            if ((i & 63) == 0 && *abort) return false;
         }
-        if (mbar_wait_bounded(bar, parity)) return true;
         atomicOr(err, 1u);
         *abort = 1;
         return false;
     }
 };
 
-// Scales and biases of a thread's row for the subgroups of one slot, as packed
-// pairs of bf16 (subgroups 2i and 2i + 1).
-template <int BITS>
-struct Affine {
-    static constexpr int kSubs = slot_subs(BITS);
-    uint32_t s[kSubs / 2], b[kSubs / 2];
+// How a tile's scales and biases come to shared memory, once for its range of K:
+// by tensor map where rows start on 16 bytes (boxes an odd number of 16 bytes
+// wide, so that 32 rows' reads spread over the banks), else whole rows in one
+// piece where that is small, else row by row. What was tried instead: a thread
+// reading its own row's from global memory, up to three slots ahead, waited for
+// microseconds behind the stream of weights; copies of 8 bytes a row and slot by
+// the producer warp kept it busy for twice the time of a slot.
+enum { kSbBoxes, kSbWhole, kSbRows };
 
-    __device__ __forceinline__ void clear()
+struct Affines {
+    int mode, pitch, block;  // bytes from row to row, and of each of the two arrays
+
+    __host__ __device__ static Affines plan(int G, int groups, int rows)
     {
-#pragma unroll
-        for (int i = 0; i < kSubs / 2; ++i) s[i] = b[i] = 0u;
+        Affines a;
+        a.mode = G % 8 == 0 ? kSbBoxes : G <= 96 ? kSbWhole : kSbRows;
+        a.pitch = a.mode == kSbWhole ? 2 * G : (((2 * groups + 30) / 16) | 1) * 16;
+        a.block = (rows * a.pitch + 127) & ~127;
+        return a;
     }
-    // Row `row` (an index of the whole array), slot index `slot` of the row.
-    // `vec`: G is a multiple of the slot's groups, whose loads are then one
-    // aligned vector.
-    __device__ __forceinline__ void load(const uint16_t *sc, const uint16_t *bi, long long row, int G, int gs, int slot,
-                                         bool vec)
+    // Arrivals that one fetch makes on its barrier.
+    __device__ __forceinline__ int arrivals() const { return mode == kSbRows ? 32 : 1; }
+
+    // By the whole producer warp: rows row0 .. row0 + rows - 1 of `all`, groups g0 ..
+    // g0 + groups - 1 of G, into dst (generic address `gen`). smap, bmap: tensor
+    // maps for kSbBoxes, at row `mrow0` of the map.
+    __device__ __forceinline__ void fetch(uint32_t dst, uint8_t *gen, const uint16_t *sc, const uint16_t *bi,
+                                          const CUtensorMap *smap, const CUtensorMap *bmap, long long row0, int rows,
+                                          long long all, int G, int g0, int groups, uint32_t bar, int lane) const
     {
-        const int per = kSubs * 64 / gs, g0 = slot * per;
-        const uint16_t *ps = sc + row * G + g0, *pb = bi + row * G + g0;
-        if (vec) {
-            if (gs == 64) {
-                get(ps, s);
-                get(pb, b);
-            } else {
-                uint32_t hs[kSubs / 4], hb[kSubs / 4];
-                get(ps, hs);
-                get(pb, hb);
-#pragma unroll
-                for (int i = 0; i < kSubs / 4; ++i) {
-                    s[2 * i] = __byte_perm(hs[i], 0, 0x1010);
-                    s[2 * i + 1] = __byte_perm(hs[i], 0, 0x3232);
-                    b[2 * i] = __byte_perm(hb[i], 0, 0x1010);
-                    b[2 * i + 1] = __byte_perm(hb[i], 0, 0x3232);
-                }
+        if (mode == kSbBoxes) {
+            if (lane == 0) {
+                mbar_arrive_expect_tx(bar, uint32_t(2 * rows * pitch));
+                tma_load_2d(dst, smap, g0 / 8 * 2, int(row0), bar);  // eight groups are two elements
+                tma_load_2d(dst + block, bmap, g0 / 8 * 2, int(row0), bar);
             }
             return;
         }
-#pragma unroll
-        for (int i = 0; i < kSubs; ++i) {
-            const int g = i * 64 / gs;
-            uint32_t sv = 0, bv = 0;
-            if (g0 + g < G) {
-                sv = __ldg(ps + g);
-                bv = __ldg(pb + g);
+        // from the 16-byte boundary before the first; the last bytes of the
+        // arrays, where they fill no 16, go one by one
+        const long long end = all * G * 2;
+        const int step = mode == kSbWhole ? rows : 1;
+        uint32_t total = 0;
+        for (int pass = 0; pass < 2; ++pass) {
+            for (int r = mode == kSbWhole ? (lane == 0 ? 0 : rows) : lane; r < rows; r += mode == kSbWhole ? rows : 32) {
+                const long long n = row0 + r;
+                if (n >= all) break;
+                const long long first = mode == kSbWhole ? n * G * 2 : (n * G + g0) * 2, from = first & ~15ll;
+                const long long to = mode == kSbWhole ? min(first + (long long)step * G * 2, end) : first + 2 * groups;
+                const long long whole = min((to + 15) & ~15ll, end & ~15ll);
+                const uint32_t bytes = whole > from ? uint32_t(whole - from) : 0u, d = uint32_t(r * pitch);
+                if (pass == 0) {
+                    total += 2 * bytes;
+                    for (long long e = max(whole, from); e < to; e += 2) {
+                        *reinterpret_cast<uint16_t *>(gen + d + (e - from)) = __ldg(sc + e / 2);
+                        *reinterpret_cast<uint16_t *>(gen + d + block + (e - from)) = __ldg(bi + e / 2);
+                    }
+                } else if (bytes) {
+                    bulk_load_plain(dst + d, reinterpret_cast<const uint8_t *>(sc) + from, bytes, bar);
+                    bulk_load_plain(dst + d + block, reinterpret_cast<const uint8_t *>(bi) + from, bytes, bar);
+                }
             }
-            s[i / 2] = i & 1 ? s[i / 2] | sv << 16 : sv;
-            b[i / 2] = i & 1 ? b[i / 2] | bv << 16 : bv;
+            if (pass == 0 && (mode == kSbRows || lane == 0)) mbar_arrive_expect_tx(bar, total);
         }
     }
+    // Offset of group g0 of a row in its bytes there.
+    __device__ __forceinline__ uint32_t offset(long long row, int G, int g0) const
+    {
+        return mode == kSbBoxes ? (g0 & 7) * 2u : mode == kSbWhole ? g0 * 2u : uint32_t((row * G + g0) * 2) & 15u;
+    }
+    // Bytes by which a row's groups of a slot are aligned there, at most 8.
+    __device__ __forceinline__ int alignment(int G) const
+    {
+        return mode == kSbRows ? 2 : mode == kSbBoxes || G % 4 == 0 ? 8 : G % 2 == 0 ? 4 : 2;
+    }
+};
+
+// Scales and biases of a row for the groups of one slot.
+template <int BITS, int GS>
+struct Affine {
+    static constexpr int kSubs = slot_subs(BITS), kGroupsPerSlot = kSubs * 64 / GS, kWords = kGroupsPerSlot / 2;
+    uint32_t s[kWords], b[kWords];
+
+    // At shared address `addr`, the biases `block` bytes further; `left` groups of
+    // the row from there on, those past them being zeros.
+    __device__ __forceinline__ void read(uint32_t addr, uint32_t block, int align, int left)
+    {
+        get(addr, align, s);
+        get(addr + block, align, b);
+        if (left < kGroupsPerSlot) {
+#pragma unroll
+            for (int g = 0; g < kGroupsPerSlot; ++g)
+                if (g >= left) {
+                    s[g / 2] &= g & 1 ? 0x0000ffffu : 0u;
+                    b[g / 2] &= g & 1 ? 0x0000ffffu : 0u;
+                }
+        }
+    }
+    // Of subgroup j of the slot.
+    __device__ __forceinline__ float scale(int j) const { return half(s, j); }
+    __device__ __forceinline__ float bias(int j) const { return half(b, j); }
 
 private:
-    template <int N>
-    static __device__ __forceinline__ void get(const uint16_t *p, uint32_t (&v)[N])
+    static __device__ __forceinline__ float half(const uint32_t (&v)[kWords], int j)
     {
-        if constexpr (N == 1) {
-            v[0] = __ldg(reinterpret_cast<const uint32_t *>(p));
-        } else if constexpr (N == 2) {
-            const uint2 u = __ldg(reinterpret_cast<const uint2 *>(p));
-            v[0] = u.x;
-            v[1] = u.y;
+        const int g = j * 64 / GS;
+        return __uint_as_float(g & 1 ? v[g / 2] & 0xffff0000u : v[g / 2] << 16);
+    }
+    static __device__ __forceinline__ void get(uint32_t addr, int align, uint32_t (&v)[kWords])
+    {
+        if (align == 8 && kWords > 1) {
+#pragma unroll
+            for (int i = 0; i + 1 < kWords; i += 2)
+                asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v[i]), "=r"(v[i + 1]) : "r"(addr + 4 * i));
+        } else if (align >= 4) {
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v[i]) : "r"(addr + 4 * i));
         } else {
-            const uint4 u = __ldg(reinterpret_cast<const uint4 *>(p));
-            v[0] = u.x;
-            v[1] = u.y;
-            v[2] = u.z;
-            v[3] = u.w;
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) {
+                uint16_t lo, hi;
+                asm volatile("ld.shared.u16 %0, [%1];" : "=h"(lo) : "r"(addr + 4 * i));
+                asm volatile("ld.shared.u16 %0, [%1];" : "=h"(hi) : "r"(addr + 4 * i + 2));
+                v[i] = uint32_t(lo) | uint32_t(hi) << 16;
+            }
         }
     }
 };
@@ -430,12 +482,12 @@ struct Pipe {
 // A worker thread's row of a tile: sums of NC vectors over the slots it is given.
 // Two steps are in flight: the accumulators of one are read two steps later, when
 // its A columns are needed again.
-template <int BITS, int NC>
+template <int BITS, int GS, int NC>
 struct Row {
     static constexpr int kSubs = slot_subs(BITS), kStep = step_subs(NC), kSteps = kSubs / kStep;
     static_assert(kSteps % 2 == 0, "a slot's steps use the two buffers alike");
     uint64_t y[NC / 2];
-    uint32_t last_s[kStep], last_b[kStep];  // of the previous slot's last two steps, packed pairs
+    float last_s[2 * kStep], last_b[2 * kStep];  // of the previous slot's last two steps
     bool primed;
 
     __device__ __forceinline__ void start()
@@ -443,14 +495,12 @@ struct Row {
 #pragma unroll
         for (int i = 0; i < NC / 2; ++i) y[i] = 0ull;
 #pragma unroll
-        for (int i = 0; i < kStep; ++i) last_s[i] = last_b[i] = 0u;
+        for (int i = 0; i < 2 * kStep; ++i) last_s[i] = last_b[i] = 0.0f;
         primed = false;
     }
 
-    __device__ __forceinline__ void add(const float (&v)[2 * NC], uint32_t s2, uint32_t b2, int half, uint32_t meta)
+    __device__ __forceinline__ void add(const float (&v)[2 * NC], float s, float b, uint32_t meta)
     {
-        const float s = __uint_as_float(half ? s2 & 0xffff0000u : s2 << 16);
-        const float b = __uint_as_float(half ? b2 & 0xffff0000u : b2 << 16);
         const uint64_t ss = pack2(s, s), bb = pack2(b, b), r32 = pack2(0.03125f, 0.03125f);
 #pragma unroll
         for (int c = 0; c < NC / 2; ++c) {
@@ -459,13 +509,16 @@ struct Row {
             const uint64_t f = pack2(__uint_as_float(m.z), __uint_as_float(m.w));
             const uint64_t d = mul2(fma2(pack2(v[4 * c + 2], v[4 * c + 3]), r32, pack2(v[4 * c], v[4 * c + 1])), f);
             y[c] = fma2(ss, d, fma2(bb, sum, y[c]));
+            // (keeps the loads of the next pairs from being hoisted into registers
+            // that are not there)
+            if (c % 4 == 3) asm volatile("" : "+l"(y[c]), "+l"(y[c - 1]), "+l"(y[c - 2]), "+l"(y[c - 3]));
         }
     }
 
     // One slot: `w` is the row's address in it with its swizzle bits, `meta` the
     // address of the slot's first subgroup's meta and `last_meta` that of the
     // first subgroup of the previous slot's last two steps.
-    __device__ __forceinline__ void slot(const Waits &wait, Pipe &p, uint32_t w, const Affine<BITS> &aff, uint32_t meta,
+    __device__ __forceinline__ void slot(const Waits &wait, Pipe &p, uint32_t w, const Affine<BITS, GS> &aff, uint32_t meta,
                                          uint32_t last_meta, int lane)
     {
         constexpr int MB = meta_bytes(NC), ND = acc_columns(NC);
@@ -505,15 +558,15 @@ struct Row {
 #pragma unroll
                 for (int u = 0; u < kStep; ++u) {
                     const int sub = (j - 2) * kStep + u;  // below 0: of the previous slot
-                    if (j < 2) add(v[u], last_s[(sub + 2 * kStep) / 2], last_b[(sub + 2 * kStep) / 2], sub & 1, last_meta + (sub + 2 * kStep) * MB);
-                    else add(v[u], aff.s[(sub & (kSubs - 1)) / 2], aff.b[(sub & (kSubs - 1)) / 2], sub & 1, meta + sub * MB);
+                    if (j < 2) add(v[u], last_s[sub + 2 * kStep], last_b[sub + 2 * kStep], last_meta + (sub + 2 * kStep) * MB);
+                    else add(v[u], aff.scale(sub), aff.bias(sub), meta + sub * MB);
                 }
             }
         }
 #pragma unroll
-        for (int i = 0; i < kStep; ++i) {
-            last_s[i] = aff.s[kSubs / 2 - kStep + i];
-            last_b[i] = aff.b[kSubs / 2 - kStep + i];
+        for (int i = 0; i < 2 * kStep; ++i) {
+            last_s[i] = aff.scale(kSubs - 2 * kStep + i);
+            last_b[i] = aff.bias(kSubs - 2 * kStep + i);
         }
         p.steps += kSteps;
         primed = true;
@@ -534,8 +587,7 @@ struct Row {
 #pragma unroll
             for (int u = 0; u < kStep; ++u) {
                 settle(v[u]);
-                add(v[u], last_s[(j * kStep + u) / 2], last_b[(j * kStep + u) / 2], (j * kStep + u) & 1,
-                    last_meta + (j * kStep + u) * meta_bytes(NC));
+                add(v[u], last_s[j * kStep + u], last_b[j * kStep + u], last_meta + (j * kStep + u) * meta_bytes(NC));
             }
         }
     }
