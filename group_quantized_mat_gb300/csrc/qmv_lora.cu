@@ -89,7 +89,15 @@ __global__ void __launch_bounds__(kPrepareThreads) lora_prepare(const LoraParams
         float x[8];
         tile::widen8(v, x);
         const size_t s = size_t(z) * p.subs + sub;
-        tile::stage_octet<BITS>(x, o, m - z * kPass, p.cells + s * tile::cell_bytes(NC), p.meta + s * tile::meta_bytes(NC));
+        const int tok = m - z * kPass;
+        tile::stage_octet<BITS>(
+            x, o,
+            [&](int h) { return p.cells + s * tile::cell_bytes(NC) + tile::operand_offset(tile::operand_index(tok, h), o >> 1); },
+            [&](float sum, float f) {
+                float *q = reinterpret_cast<float *>(p.meta + s * tile::meta_bytes(NC) + (tok >> 1) * 16) + (tok & 1);
+                q[0] = sum;
+                q[2] = f;
+            });
         return;
     }
     // inner vectors: a block for each (vector, row of A), its warps sharing K
@@ -231,7 +239,7 @@ __global__ void __launch_bounds__(tile::kThreads, 1) lora_project(const __grid_c
         }
         mbar_init(xbar, 1);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(sfull0 + 8 * i, p.sb.arrivals());
+            mbar_init(sfull0 + 8 * i, 32);
             mbar_init(sempty0 + 8 * i, kWorkers);
         }
         fence_mbar_init();
@@ -424,7 +432,7 @@ LoraParams plan(int M, int N, int K, int bits, int gs, int R, int sms, Sizes &sz
     p.rows = ((N + p.grid_rows * rounds - 1) / (p.grid_rows * rounds) + 7) / 8 * 8;
     p.tiles = (N + p.rows - 1) / p.rows;
     if (p.grid_rows > p.tiles) p.grid_rows = p.tiles;
-    p.sb = tile::Affines::plan(p.G, p.range * slot_subs * 64 / gs, p.rows);
+    p.sb = tile::Affines::plan(p.G, p.range * slot_subs * 64 / gs, p.rows, 96);
     p.sb_buffers = rounds > 1 ? 2 : 1;
     const size_t passes = (M + kPass - 1) / kPass;
     sz.cells = up256(passes * p.subs * tile::cell_bytes(p.nc));

@@ -1,154 +1,744 @@
 // qmv_moe_run: a whole mixture-of-experts layer for a few tokens,
 //
-//   l = router x;  ids = top-k of l;  w = softmax;  y = sum_e w_e down_e (act(gate_e x) * (up_e x)).
+//   l = router x;  ids = top-k of l;  w = softmax;  y = sum_e w_e down_e (act(gate_e x) * (up_e x)),
 //
-// Three kernels: moe_route, moe_hidden (gate, up and activation of every
-// (token, choice)) and moe_down (down product and weighted sum).
+// in two kernels.
+//  1. moe_logits forms the router's logits and stages x (qmv_tile.cuh): rows of
+//     operand bytes for each token, which the second kernel gathers.
+//  2. moe_experts, one CTA per SM, all resident (a cooperative launch). Every CTA
+//     picks the experts from the logits for itself (a few thousand numbers) and
+//     lists the tokens of each; then it takes its share of two kinds of items:
+//       A. 64 rows of an expert's gate and the 64 of its up product, for up to NC
+//          of its tokens: activation, and h as operand bytes to the workspace;
+//       B. 128 rows of an expert's down product: sums to the workspace; the CTA
+//          that finishes a tile of rows last adds the experts' sums with the
+//          tokens' weights, in the order of their choices.
+//     Between A and B all CTAs meet (one counter); the weights of the first B
+//     items are on their way to the ring meanwhile.
+//
+// An expert with no token costs nothing, one with several reads its weights once
+// for up to NC of them. What bounds it is the weights' stream while there are
+// many experts, and for one token the chain logits - experts - meeting - sums.
+//
+// The inner pipeline is qmv_tile.cuh's. A ring slot holds 128 bytes of 128 rows
+// and the slot's subgroups of the item's tokens. h enters the down product with
+// four e4m3 terms (17 bits), x with two (its 8 bits).
+//
+// Orders: a token's logits, its sums over K and inter, and the sum over its
+// choices do not depend on the other tokens of the call.
 #include <cuda_bf16.h>
-#include <cuda_runtime.h>
 
 #include <cstdint>
+#include <mutex>
 
 #include "qmv.h"
-#include "qmv_launch_decl.h"
+#include "qmv_launch.cuh"
+#include "qmv_tile.cuh"
 
+namespace qmv {
 namespace {
 
+constexpr int kLogitThreads = 256;
+constexpr int kSmemMoe = 227 * 1024 - 1024;
+constexpr int kMaxSlotsMoe = 12;
+constexpr int kHalf = 64;        // rows of a box: an item is two
+constexpr int kChunkGroups = 32; // groups of scales and biases that are fetched at a time
+constexpr int kTermsH = 4;
+
 struct MoeParams {
-    const uint16_t *x, *router;
-    const uint32_t *gu_w, *dn_w;
-    const uint16_t *gu_s, *gu_b, *dn_s, *dn_b;
+    const uint16_t *x, *router, *gu_s, *gu_b, *dn_s, *dn_b;
     void *y;
-    int32_t *ids;      // [M][k]
-    float *weights;    // [M][k]
-    float *h;          // [M][k][I]
-    int32_t *ids_out;  // the caller's, or NULL
+    int32_t *ids_out;
     float *weights_out;
-    int M, K, I, E, k, bits, gs, f32_out, gelu, softmax_all;
+    float *logits;      // [M][E]
+    uint8_t *rows;      // staged x: [M][subs_a][hi 64, lo 64]
+    float2 *xmeta;      // [M][subs_a] (sum, f)
+    uint8_t *hcells;    // [entry][subs_b][cell_bytes(NC, 4)]
+    uint8_t *hmeta;     // [entry][subs_b][meta_bytes(NC)]
+    float *partials;    // [pair][K]
+    unsigned *counters; // [0]: CTAs done with A; then one for each tile of rows of B
+    unsigned *err;
+    int M, K, I, E, k, gs, f32_out, gelu, softmax_all;
+    int Sa, NSa, Ga, Sb, NSb, Gb;  // subgroups, slots and groups of a row of A and of B
+    int tiles_a, tiles_b, words, max_entries, slots, stage_blocks;
+    tile::Affines sba, sbb;
+    int cha, chb;  // slots whose scales and biases are fetched at a time
+    int sb_block;
 };
 
-__device__ __forceinline__ float bf(uint16_t u) { return __uint_as_float(uint32_t(u) << 16); }
-
-__device__ __forceinline__ float warp_sum(float v)
+template <int BITS>
+__global__ void __launch_bounds__(kLogitThreads) moe_logits(const MoeParams p)
 {
-    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    if (blockIdx.x == 0)
+        for (int i = tid; i < 1 + p.tiles_b; i += kLogitThreads) p.counters[i] = 0u;
+    if (int(blockIdx.x) < p.stage_blocks) {
+        // eight threads for each (token, subgroup)
+        const int subs = p.NSa * tile::slot_subs(BITS);
+        const long long at = (long long)blockIdx.x * kLogitThreads + tid;
+        const int o = int(at & 7);
+        long long cell = at >> 3;
+        // threads past the end repeat the last cell's values (the warp's exchanges need them)
+        if (cell >= (long long)p.M * subs) cell = (long long)p.M * subs - 1;
+        const int m = int(cell / subs), sub = int(cell - (long long)m * subs);
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (sub < p.Sa) v = __ldg(reinterpret_cast<const uint4 *>(p.x + size_t(m) * p.K + sub * 64 + o * 8));
+        float x[8];
+        tile::widen8(v, x);
+        tile::stage_octet<BITS>(
+            x, o, [&](int h) { return p.rows + cell * 128 + h * 64 + (o >> 1) * 16; },
+            [&](float sum, float f) { p.xmeta[cell] = make_float2(sum, f); });
+        return;
+    }
+    // logits: a block for each expert, its warps sharing K, for all tokens
+    __shared__ float part[kLogitThreads / 32][32];
+    const int e = int(blockIdx.x) - p.stage_blocks, n8 = p.K / 8;
+    const int lo = n8 * warp / (kLogitThreads / 32), hi = n8 * (warp + 1) / (kLogitThreads / 32);
+    const uint4 *r = reinterpret_cast<const uint4 *>(p.router + size_t(e) * p.K);
+    for (int m0 = 0; m0 < p.M; m0 += 32) {
+        const int tokens = min(32, p.M - m0);
+        for (int t = 0; t < tokens; ++t) {
+            const uint4 *x = reinterpret_cast<const uint4 *>(p.x + size_t(m0 + t) * p.K);
+            float s = 0.0f;
+#pragma unroll 4
+            for (int i = lo + lane; i < hi; i += 32) {
+                float rv[8], xv[8];
+                tile::widen8(__ldg(r + i), rv);
+                tile::widen8(__ldg(x + i), xv);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) s = __fmaf_rn(rv[j], xv[j], s);
+            }
+#pragma unroll
+            for (int d = 16; d; d >>= 1) s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, d));
+            if (lane == 0) part[warp][t] = s;
+        }
+        __syncthreads();
+        if (tid < tokens) {
+            float s = part[0][tid];
+            for (int w = 1; w < kLogitThreads / 32; ++w) s = __fadd_rn(s, part[w][tid]);
+            p.logits[size_t(m0 + tid) * p.E + e] = s == s ? s : -INFINITY;
+        }
+        __syncthreads();
+    }
 }
 
-// One block per token.
-__global__ void moe_route(const MoeParams p)
+struct MoeLayout {
+    int slot, cells, meta, sb, xs, lists, total;
+    // within lists
+    int w, ids, pos, tok, base, entry, mask, bars;
+};
+
+template <int BITS, int NC>
+__host__ __device__ inline MoeLayout moe_layout(const MoeParams &p)
 {
-    __shared__ float l[QMV_MAX_EXPERTS];
-    const int m = blockIdx.x, lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-    const uint16_t *x = p.x + size_t(m) * p.K;
-    for (int e = warp; e < p.E; e += blockDim.x / 32) {
-        float s = 0.0f;
-        for (int i = lane; i < p.K; i += 32) s = fmaf(bf(p.router[size_t(e) * p.K + i]), bf(x[i]), s);
-        s = warp_sum(s);
-        if (lane == 0) l[e] = s == s ? s : -INFINITY;
+    constexpr int SUBS = tile::slot_subs(BITS), CB = tile::cell_bytes(NC, kTermsH);
+    const int pairs = p.M * p.k;
+    MoeLayout l;
+    l.cells = tile::kTileRows * tile::kSlotBytes;
+    l.meta = l.cells + SUBS * CB;
+    l.slot = (l.meta + SUBS * tile::meta_bytes(NC) + 1023) & ~1023;
+    l.sb = p.slots * l.slot;
+    l.xs = l.sb + 2 * 2 * p.sb_block;
+    l.lists = l.xs + NC * kHalf * 4 + tile::kGroups * 16;
+    l.w = l.lists;
+    l.ids = l.w + pairs * 4;
+    l.pos = l.ids + ((pairs * 2 + 3) & ~3);
+    l.tok = l.pos + ((pairs * 2 + 3) & ~3);
+    l.base = l.tok + ((pairs * 2 + 3) & ~3);
+    l.entry = l.base + (p.E + 1) * 4;
+    l.bars = (l.entry + p.max_entries * 4 + 7) & ~7;
+    // scratch of the routing, in the ring: a row of logits for each warp, the masks
+    l.mask = tile::kThreads / 32 * p.E * 4;
+    l.total = l.bars + (2 * p.slots + 4 * tile::kGroups + 4) * 8;
+    return l;
+}
+
+// The expert choice of token t by one warp: `l` is scratch for the E logits.
+__device__ __forceinline__ void choose(const MoeParams &p, int t, float *l, float *w, uint16_t *ids, uint32_t *mask, int lane)
+{
+    for (int e = lane; e < p.E; e += 32) l[e] = __ldcg(p.logits + size_t(t) * p.E + e);
+    __syncwarp();
+    float top = 0.0f, sum = 0.0f, mine = 0.0f;
+    for (int j = 0; j < p.k; ++j) {
+        float best = -INFINITY;
+        int arg = 0x7fffffff;
+        for (int e = lane; e < p.E; e += 32) {
+            const float v = l[e];  // NaN: already chosen
+            if (v > best || (v == best && e < arg)) {
+                best = v;
+                arg = e;
+            }
+        }
+#pragma unroll
+        for (int d = 16; d; d >>= 1) {
+            const float v = __shfl_xor_sync(0xffffffffu, best, d);
+            const int a = __shfl_xor_sync(0xffffffffu, arg, d);
+            if (v > best || (v == best && a < arg)) {
+                best = v;
+                arg = a;
+            }
+        }
+        if (j == 0) {
+            top = best;
+            if (p.softmax_all) {
+                // over all experts, each lane's in order, then across the lanes
+                for (int e = lane; e < p.E; e += 32) sum = __fadd_rn(sum, top > -INFINITY ? expf(__fsub_rn(l[e], top)) : 1.0f);
+#pragma unroll
+                for (int d = 16; d; d >>= 1) sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, d));
+            }
+        }
+        __syncwarp();
+        // (all logits -inf: equal weights)
+        const float mass = top > -INFINITY ? expf(__fsub_rn(best, top)) : 1.0f;
+        if (lane == j) mine = mass;
+        if (!p.softmax_all) sum = __fadd_rn(sum, mass);
+        if (lane == 0) {
+            l[arg] = __uint_as_float(0x7fc00000u);
+            ids[t * p.k + j] = uint16_t(arg);
+            atomicOr(mask + arg * p.words + t / 32, 1u << (t & 31));
+        }
+        __syncwarp();
+    }
+    if (lane < p.k) w[t * p.k + lane] = __fdiv_rn(mine, sum);
+}
+
+__device__ __forceinline__ float activation(float g, bool gelu)
+{
+    if (gelu) {
+        const float c = __fmul_rn(0.7978845608028654f, __fmaf_rn(__fmul_rn(__fmul_rn(0.044715f, g), g), g, g));
+        return __fmul_rn(__fmul_rn(0.5f, g), __fadd_rn(1.0f, tanhf(c)));
+    }
+    return __fdiv_rn(g, __fadd_rn(1.0f, expf(-g)));
+}
+
+template <int BITS, int GS, int NC>
+__global__ void __launch_bounds__(tile::kThreads, 1)
+    moe_experts(const __grid_constant__ CUtensorMap wa, const __grid_constant__ CUtensorMap sa,
+                const __grid_constant__ CUtensorMap ba, const __grid_constant__ CUtensorMap wb,
+                const __grid_constant__ CUtensorMap sbm, const __grid_constant__ CUtensorMap bb, const MoeParams p)
+{
+    using namespace tile;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    __shared__ int s_abort, s_last, s_entries;
+    __shared__ uint32_t s_tmem;
+    constexpr int SUBS = slot_subs(BITS), CA = cell_bytes(NC, 2), CB = cell_bytes(NC, kTermsH), MB = meta_bytes(NC);
+    const MoeLayout L = moe_layout<BITS, NC>(p);
+    const uint32_t base = smem_u32(smem), full0 = base + L.bars, empty0 = full0 + 8 * p.slots;
+    const uint32_t stored0 = empty0 + 8 * p.slots, ready0 = stored0 + 16 * kGroups, sfull0 = ready0 + 16 * kGroups;
+    const uint32_t sempty0 = sfull0 + 16;
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, grid = gridDim.x;
+    float *s_w = reinterpret_cast<float *>(smem + L.w);
+    uint16_t *s_ids = reinterpret_cast<uint16_t *>(smem + L.ids), *s_pos = reinterpret_cast<uint16_t *>(smem + L.pos);
+    uint16_t *s_tok = reinterpret_cast<uint16_t *>(smem + L.tok);
+    int *s_base = reinterpret_cast<int *>(smem + L.base);
+    uint32_t *s_entry = reinterpret_cast<uint32_t *>(smem + L.entry), *s_mask = reinterpret_cast<uint32_t *>(smem + L.mask);
+
+    if (tid == 0) {
+        for (int i = 0; i < p.slots; ++i) {
+            mbar_init(full0 + 8 * i, 1 + 32);
+            mbar_init(empty0 + 8 * i, 4);
+        }
+        for (int i = 0; i < 2 * kGroups; ++i) {
+            mbar_init(stored0 + 8 * i, 4);
+            mbar_init(ready0 + 8 * i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(sfull0 + 8 * i, 2 * 32);
+            mbar_init(sempty0 + 8 * i, kWorkers);
+        }
+        fence_mbar_init();
+        s_abort = 0;
+    }
+    if (warp == kWorkers) tmem_alloc(smem_u32(&s_tmem), kTmemColumns);
+    for (int i = tid; i < p.E * p.words; i += kThreads) s_mask[i] = 0u;
+    grid_dependency_wait();
+    __syncthreads();
+
+    // ------------------------------------------------------------- routing
+    for (int t = warp; t < p.M; t += kThreads / 32)
+        choose(p, t, reinterpret_cast<float *>(smem) + warp * p.E, s_w, s_ids, s_mask, lane);
+    __syncthreads();
+    if (warp == 0) {
+        // each lane a run of experts: tokens and entries before it
+        const int run = (p.E + 31) / 32, e0 = min(lane * run, p.E), e1 = min(e0 + run, p.E);
+        int pairs = 0, entries = 0;
+        for (int e = e0; e < e1; ++e) {
+            int n = 0;
+            for (int i = 0; i < p.words; ++i) n += __popc(s_mask[e * p.words + i]);
+            pairs += n;
+            entries += (n + NC - 1) / NC;
+        }
+        int pb = pairs, eb = entries;
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+            const int a = __shfl_up_sync(0xffffffffu, pb, d), b = __shfl_up_sync(0xffffffffu, eb, d);
+            if (lane >= d) {
+                pb += a;
+                eb += b;
+            }
+        }
+        if (lane == 31) {
+            s_entries = eb;
+            s_base[p.E] = pb;
+        }
+        pb -= pairs;
+        eb -= entries;
+        for (int e = e0; e < e1; ++e) {
+            int n = 0;
+            for (int i = 0; i < p.words; ++i) n += __popc(s_mask[e * p.words + i]);
+            s_base[e] = pb;
+            for (int f = 0; f < n; f += NC) s_entry[eb++] = uint32_t(e) | uint32_t(f) << 16;
+            pb += n;
+        }
     }
     __syncthreads();
-    if (threadIdx.x) return;
-    float top = -INFINITY, all = 0.0f, some = 0.0f;
-    for (int e = 0; e < p.E; ++e) top = fmaxf(top, l[e]);
-    for (int e = 0; e < p.E; ++e) all += expf(l[e] - top);
-    float val[QMV_MAX_TOP_K];
-    int id[QMV_MAX_TOP_K];
-    for (int j = 0; j < p.k; ++j) {
-        int best = -1;
-        for (int e = 0; e < p.E; ++e) {
-            bool used = false;
-            for (int i = 0; i < j; ++i) used |= id[i] == e;
-            if (!used && (best < 0 || l[e] > l[best])) best = e;
+    for (int i = tid; i < p.M * p.k; i += kThreads) {
+        const int t = i / p.k, e = s_ids[i];
+        int before = __popc(s_mask[e * p.words + t / 32] & ((1u << (t & 31)) - 1u));
+        for (int j = 0; j < t / 32; ++j) before += __popc(s_mask[e * p.words + j]);
+        s_pos[i] = uint16_t(s_base[e] + before);
+        s_tok[s_base[e] + before] = uint16_t(t);
+        if (blockIdx.x == 0 && p.ids_out) p.ids_out[i] = e;
+        if (blockIdx.x == 0 && p.weights_out) p.weights_out[i] = s_w[i];
+    }
+    fence_proxy_async_smem();  // the ring was scratch until here
+    tmem_fence_before();
+    __syncthreads();
+    tmem_fence_after();
+    const uint32_t tm = s_tmem;
+    const Waits wait{&s_abort, p.err};
+    const int entries = s_entries, na = entries * p.tiles_a, nb = entries * p.tiles_b;
+    // entry, its expert, first pair, tokens; the item's tile
+    struct Item {
+        int entry, e, pair, count, tl;
+    };
+    auto item_of = [&](int q, int tiles) {
+        Item it;
+        it.entry = q / tiles;
+        it.tl = q - it.entry * tiles;
+        const uint32_t v = s_entry[it.entry];
+        it.e = int(v & 0xffffu);
+        it.pair = s_base[it.e] + int(v >> 16);
+        it.count = min(NC, s_base[it.e + 1] - it.pair);
+        return it;
+    };
+
+    if (warp == kThreads / 32 - 1) {
+        // ---------------------------------------------------------- producer
+        int it = 0, chunk = 0;
+        bool ok = true;
+        // scales and biases of groups of an item's two halves
+        auto fetch = [&](const Affines &a, const uint16_t *sc, const uint16_t *bi, const CUtensorMap *sm, const CUtensorMap *bm,
+                         long long r0, long long r1, bool two, long long all, int G, int i) {
+            const int buf = chunk & 1, turn = chunk >> 1;
+            ok = __all_sync(0xffffffffu, turn == 0 || wait(sempty0 + 8 * buf, (turn - 1) & 1));
+            if (!ok) return;
+            const int g0 = i * SUBS * 64 / GS, groups = min(kChunkGroups, G - g0);  // (of kSbRows)
+            const int off = L.sb + buf * 2 * p.sb_block;
+            Affines b = a;
+            b.block = p.sb_block;
+            b.fetch(base + off, smem + off, sc, bi, sm, bm, r0, kHalf, all, G, g0, groups, sfull0 + 8 * buf, lane);
+            if (two) b.fetch(base + off + kHalf * a.pitch, smem + off + kHalf * a.pitch, sc, bi, sm, bm, r1, kHalf, all, G, g0, groups, sfull0 + 8 * buf, lane);
+            else mbar_arrive(sfull0 + 8 * buf);
+            ++chunk;
+        };
+        for (int q = blockIdx.x; q < na && ok; q += grid) {
+            const Item im = item_of(q, p.tiles_a);
+            const long long r0 = (long long)im.e * 2 * p.I + im.tl * kHalf, r1 = r0 + p.I;
+            for (int i = 0; i < p.NSa && ok; ++i, ++it) {
+                if (i % p.cha == 0) fetch(p.sba, p.gu_s, p.gu_b, &sa, &ba, r0, r1, true, (long long)p.E * 2 * p.I, p.Ga, i);
+                if (!ok) break;
+                const int s = it % p.slots, lap = it / p.slots;
+                ok = __all_sync(0xffffffffu, lap == 0 || wait(empty0 + 8 * s, (lap - 1) & 1));
+                if (!ok) break;
+                const uint32_t full = full0 + 8 * s, dst = base + s * L.slot;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(full, kTileRows * kSlotBytes);
+                    tma_load_2d(dst, &wa, i * (kSlotBytes / 8), int(r0), full);
+                    tma_load_2d(dst + kHalf * kSlotBytes, &wa, i * (kSlotBytes / 8), int(r1), full);
+                }
+                __syncwarp();
+                // the tokens' operand bytes, 16 at a time, and their sums
+                for (int c = lane; c < im.count * SUBS * 8; c += 32) {
+                    const int j = c / (SUBS * 8), sub = c / 8 % SUBS, h = c / 4 & 1, pc = c & 3;
+                    const uint8_t *src = p.rows + (size_t(s_tok[im.pair + j]) * p.NSa * SUBS + i * SUBS + sub) * 128 + h * 64 + pc * 16;
+                    const uint32_t d = dst + L.cells + sub * CA + operand_offset(operand_index(j, h), pc);
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src) : "memory");
+                }
+                for (int c = lane; c < im.count * SUBS * 2; c += 32) {
+                    const int j = c / (SUBS * 2), sub = c / 2 % SUBS, f = c & 1;
+                    const float *src = reinterpret_cast<const float *>(p.xmeta + size_t(s_tok[im.pair + j]) * p.NSa * SUBS + i * SUBS + sub) + f;
+                    const uint32_t d = dst + L.meta + sub * MB + (j >> 1) * 16 + (j & 1) * 4 + f * 8;
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(d), "l"(src) : "memory");
+                }
+                asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(full) : "memory");
+            }
         }
-        id[j] = best;
-        val[j] = expf(l[best] - top);
-        some += val[j];
-    }
-    for (int j = 0; j < p.k; ++j) {
-        const float w = val[j] / (p.softmax_all ? all : some);
-        p.ids[m * p.k + j] = id[j];
-        p.weights[m * p.k + j] = w;
-        if (p.ids_out) p.ids_out[m * p.k + j] = id[j];
-        if (p.weights_out) p.weights_out[m * p.k + j] = w;
-    }
-}
-
-// A warp's dot of packed row `row` of an [.., K] matrix with v(i), fp32.
-template <typename V>
-__device__ float packed_dot(const uint32_t *w, const uint16_t *sc, const uint16_t *bi, size_t row, int K, int bits,
-                            int gs, int lane, V v)
-{
-    const int per = 32 / bits, words = K / per, G = K / gs;
-    float y = 0.0f;
-    for (int j = lane; j < words; j += 32) {
-        const uint32_t word = w[row * words + j];
-        float qx = 0.0f, sx = 0.0f;
-        for (int f = 0; f < per; ++f) {
-            const float xv = v(j * per + f);
-            qx = fmaf(float((word >> (f * bits)) & ((1u << bits) - 1u)), xv, qx);
-            sx += xv;
+        // B: weights of the first slots before the meeting (as many as are free and
+        // as the two buffers of scales serve), h after it
+        int ahead = 0;
+        auto b_slots = [&](int from, bool weights, bool cells, int most) {
+            int n = 0;
+            for (int q = blockIdx.x; q < nb && ok; q += grid) {
+                const Item im = item_of(q, p.tiles_b);
+                const long long r0 = (long long)im.e * p.K + im.tl * kTileRows, r1 = r0 + kHalf;
+                const bool two = im.tl * kTileRows + kHalf < p.K;
+                for (int i = 0; i < p.NSb && ok; ++i, ++n) {
+                    if (n >= most) return n;
+                    if (n < from) continue;
+                    const int s = (it + n) % p.slots, lap = (it + n) / p.slots;
+                    const uint32_t full = full0 + 8 * s, dst = base + s * L.slot;
+                    if (weights) {
+                        if (i % p.chb == 0) fetch(p.sbb, p.dn_s, p.dn_b, &sbm, &bb, r0, r1, two, (long long)p.E * p.K, p.Gb, i);
+                        if (!ok) break;
+                        ok = __all_sync(0xffffffffu, lap == 0 || wait(empty0 + 8 * s, (lap - 1) & 1));
+                        if (!ok) break;
+                        if (lane == 0) {
+                            mbar_arrive_expect_tx(full, (two ? 2 : 1) * kHalf * kSlotBytes + SUBS * (CB + MB));
+                            tma_load_2d(dst, &wb, i * (kSlotBytes / 8), int(r0), full);
+                            if (two) tma_load_2d(dst + kHalf * kSlotBytes, &wb, i * (kSlotBytes / 8), int(r1), full);
+                        }
+                        __syncwarp();
+                        mbar_arrive(full);
+                    }
+                    if (cells && lane == 0) {
+                        const size_t sub = (size_t(im.entry) * p.NSb + i) * SUBS;
+                        bulk_load_plain(dst + L.cells, p.hcells + sub * CB, SUBS * CB, full);
+                        bulk_load_plain(dst + L.meta, p.hmeta + sub * MB, SUBS * MB, full);
+                    }
+                }
+            }
+            return n;
+        };
+        if (ok) ahead = b_slots(0, true, false, min(p.slots, p.chb >= p.NSb ? 2 * p.NSb : min(2 * p.chb, p.NSb)));
+        if (ok && lane == 0) {
+            // the meeting: bounded like every wait
+            bool met = false;
+            for (int i = 0; i < (1 << 21) && !met; ++i) {
+                unsigned v;
+                asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p.counters) : "memory");
+                met = v >= unsigned(grid);
+                if (!met && (i & 63) == 63 && *wait.abort) break;
+            }
+            if (!met) {
+                atomicOr(p.err, 1u);
+                *wait.abort = 1;
+                ok = false;
+            }
+            asm volatile("fence.proxy.async;" ::: "memory");
         }
-        const size_t g = row * G + j * per / gs;
-        y = fmaf(bf(sc[g]), qx, fmaf(bf(bi[g]), sx, y));
-    }
-    return warp_sum(y);
-}
+        ok = __all_sync(0xffffffffu, ok);
+        if (ok) {
+            (void)b_slots(0, false, true, ahead);
+            (void)b_slots(ahead, true, true, 0x7fffffff);
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        if (!ok && lane == 0) {
+            // copies in flight end before the CTA does; none is longer on its way than this
+            const uint64_t t0 = global_timer_ns();
+            while (global_timer_ns() - t0 < 1000000ull) {}
+        }
+    } else if (warp >= kWorkers) {
+        // ------------------------------------------------------ tensor warps
+        const int group = warp - kWorkers;
+        if (lane == 0) {
+            int it = 0;
+            Pipe pipe = Pipe::make<NC, 2>(tm, 0, stored0, ready0, group);
+            for (int q = blockIdx.x; q < na; q += grid, it += p.NSa)
+                for (int i = group; i < p.NSa; i += kGroups)
+                    multiply_slot<BITS, NC, 2, true>(wait, pipe, base + (it + i) % p.slots * L.slot + L.cells);
+            Pipe pb = Pipe::make<NC, kTermsH>(tm, 0, stored0, ready0, group);
+            pb.steps = pipe.steps;
+            for (int q = blockIdx.x; q < nb; q += grid, it += p.NSb)
+                for (int i = group; i < p.NSb; i += kGroups)
+                    multiply_slot<BITS, NC, kTermsH>(wait, pb, base + (it + i) % p.slots * L.slot + L.cells);
+        }
+    } else {
+        // ----------------------------------------------------------- workers
+        const int group = warp / 4, row = (warp & 3) * 32 + lane;
+        const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
+        const uint32_t wrow = base + row * kSlotBytes + ((row & 7) << 4);
+        int it = 0, chunk = 0;
+        uint32_t held = 0;  // the barrier of the slot whose last steps are still to be taken
+        // all slots of an item's rows into acc
+        auto run = [&](auto &acc, Pipe &pipe, const Affines &a, int ch, int NS, int G, long long grow) {
+            const int align = a.alignment(G);
+            constexpr int STEP = std::remove_reference_t<decltype(acc)>::kStep;
+            uint32_t last = 0;
+            held = 0;
+            acc.start();
+            for (int c0 = 0; c0 < NS; c0 += ch, ++chunk) {
+                const int buf = chunk & 1, c1 = min(c0 + ch, NS), g0 = c0 * SUBS * 64 / GS;
+                wait(sfull0 + 8 * buf, (chunk >> 1) & 1);
+                const uint32_t sb = base + L.sb + buf * 2 * p.sb_block + row * a.pitch + a.offset(grow, G, g0);
+#pragma unroll 1
+                for (int i = c0 + (group + kGroups - c0 % kGroups) % kGroups; i < c1; i += kGroups) {
+                    const int s = (it + i) % p.slots, lap = (it + i) / p.slots;
+                    wait(full0 + 8 * s, lap & 1);
+                    Affine<BITS, GS> aff;
+                    constexpr int GP = Affine<BITS, GS>::kGroupsPerSlot;
+                    aff.read(sb + (i - c0) * GP * 2, p.sb_block, align, G - i * GP);
+                    const uint32_t meta = base + s * L.slot + L.meta;
+                    acc.slot(wait, pipe, wrow + s * L.slot, aff, meta, last, lane);
+                    last = meta + (SUBS - 2 * STEP) * MB;
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (held) mbar_arrive(held);
+                    }
+                    held = empty0 + 8 * s;
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(sempty0 + 8 * buf);
+            }
+            acc.finish(wait, pipe, last);
+            __syncwarp();
+            if (lane == 0 && held) mbar_arrive(held);
+        };
 
-// One warp per (token, choice, element of h).
-__global__ void moe_hidden(const MoeParams p)
-{
-    const int i = blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32, lane = threadIdx.x % 32, pair = blockIdx.y;
-    if (i >= p.I) return;
-    const uint16_t *x = p.x + size_t(pair / p.k) * p.K;
-    const size_t row = size_t(p.ids[pair]) * 2 * p.I + i;
-    auto v = [&](int j) { return bf(x[j]); };
-    const float g = packed_dot(p.gu_w, p.gu_s, p.gu_b, row, p.K, p.bits, p.gs, lane, v);
-    const float u = packed_dot(p.gu_w, p.gu_s, p.gu_b, row + p.I, p.K, p.bits, p.gs, lane, v);
-    const float act = p.gelu ? 0.5f * g * (1.0f + tanhf(0.7978845608028654f * (g + 0.044715f * g * g * g)))
-                             : g / (1.0f + expf(-g));
-    if (lane == 0) p.h[size_t(pair) * p.I + i] = act * u;
-}
+        Pipe pipe = Pipe::make<NC, 2>(tm, lanes, stored0, ready0, group);
+        float *xs = reinterpret_cast<float *>(smem + L.xs), *red = xs + NC * kHalf + group * 4;
+        for (int q = blockIdx.x; q < na; q += grid, it += p.NSa) {
+            const Item im = item_of(q, p.tiles_a);
+            Row<BITS, GS, NC, 2> acc;
+            run(acc, pipe, p.sba, p.cha, p.NSa, p.Ga, (long long)im.e * 2 * p.I + (row < kHalf ? 0 : p.I - kHalf) + im.tl * kHalf + row);
+            constexpr int OWN = Row<BITS, GS, NC, 2>::kOwn;
+            float sums[OWN];
+            acc.join(tm + lanes, group, sums);
+            // rows 64.. (up) hand theirs to rows 0.. (gate), which form h
+#pragma unroll
+            for (int i = 0; i < OWN; ++i)
+                if (row >= kHalf && group + kGroups * i < NC) xs[(group + kGroups * i) * kHalf + row - kHalf] = sums[i];
+            named_sync(2 + group, 128);
+            const size_t cell0 = (size_t(im.entry) * p.NSb * SUBS + im.tl) * CB;
+            if (row < kHalf) {
+#pragma unroll
+                for (int i = 0; i < OWN; ++i) {
+                    const int j = group + kGroups * i;
+                    if (j >= im.count) break;
+                    float h = __fmul_rn(activation(sums[i], p.gelu), xs[j * kHalf + row]);
+                    // sum and largest exponent of the 64
+                    uint32_t E = max(1u, (__float_as_uint(h) >> 23) & 0xffu);
+                    float sum = h;
+                    E = __reduce_max_sync(0xffffffffu, E);
+#pragma unroll
+                    for (int d = 16; d; d >>= 1) sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, d));
+                    if (lane == 0) {
+                        red[(warp & 1) * 2] = sum;
+                        red[(warp & 1) * 2 + 1] = __uint_as_float(E);
+                    }
+                    named_sync(2 + kGroups + group, 64);
+                    sum = __fadd_rn(red[0], red[2]);
+                    E = max(__float_as_uint(red[1]), __float_as_uint(red[3]));
+                    named_sync(2 + kGroups + group, 64);
+                    const int pw = 134 - int(E);
+                    float v = __fmul_rn(__fmul_rn(h, exp2i(pw / 2)), exp2i(pw - pw / 2));
+                    // the element's byte of its row, in the order of the masks
+                    const int pc = row >> 4, e = row & 15;
+                    const int at = BITS == 4 ? (e >> 3) * 8 + (e & 1) * 4 + ((e & 7) >> 1) : (e & 3) * 4 + (e >> 2);
+                    if (BITS == 2 && (e & 1)) v = __fmul_rn(v, 0.25f);
+#pragma unroll
+                    for (int t = 0; t < kTermsH; ++t) {
+                        const uint32_t b = to_e4m3x2(v, 0.0f);
+                        float back, none;
+                        from_e4m3x2(b, back, none);
+                        v = __fmul_rn(__fsub_rn(v, back), 32.0f);
+                        p.hcells[cell0 + operand_offset(operand_index(j, t, kTermsH), pc) + at] = uint8_t(b);
+                    }
+                    if (row == 0) {
+                        float *m = reinterpret_cast<float *>(p.hmeta + (size_t(im.entry) * p.NSb * SUBS + im.tl) * MB + (j >> 1) * 16) + (j & 1);
+                        m[0] = sum;
+                        m[2] = exp2i(min(int(E) - 125, 127));
+                    }
+                }
+            }
+            // subgroups that fill the last slot
+            if (im.tl == p.tiles_a - 1)
+                for (int sub = p.Sb; sub < p.NSb * SUBS; ++sub) {
+                    const size_t cell = size_t(im.entry) * p.NSb * SUBS + sub;
+                    for (int i = tid; i < CB / 4; i += 32 * kWorkers) reinterpret_cast<uint32_t *>(p.hcells + cell * CB)[i] = 0u;
+                    for (int i = tid; i < MB / 4; i += 32 * kWorkers) reinterpret_cast<uint32_t *>(p.hmeta + cell * MB)[i] = 0u;
+                }
+        }
+        asm volatile("fence.proxy.async;" ::: "memory");
+        __threadfence();
+        named_sync(1, 32 * kWorkers);
+        if (tid == 0) asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(p.counters) : "memory");
 
-// One warp per (token, element of y).
-__global__ void moe_down(const MoeParams p)
-{
-    const int n = blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32, lane = threadIdx.x % 32, m = blockIdx.y;
-    if (n >= p.K) return;
-    float y = 0.0f;
-    for (int j = 0; j < p.k; ++j) {
-        const int pair = m * p.k + j;
-        const float *h = p.h + size_t(pair) * p.I;
-        const float d = packed_dot(p.dn_w, p.dn_s, p.dn_b, size_t(p.ids[pair]) * p.K + n, p.I, p.bits, p.gs, lane,
-                                   [&](int i) { return h[i]; });
-        y = fmaf(p.weights[pair], d, y);
+        Pipe pb = Pipe::make<NC, kTermsH>(tm, lanes, stored0, ready0, group);
+        pb.steps = pipe.steps;
+        for (int q = blockIdx.x; q < nb; q += grid, it += p.NSb) {
+            const Item im = item_of(q, p.tiles_b);
+            const int n = im.tl * kTileRows + row;
+            Row<BITS, GS, NC, kTermsH> acc;
+            run(acc, pb, p.sbb, p.chb, p.NSb, p.Gb, (long long)im.e * p.K + n);
+            constexpr int OWN = Row<BITS, GS, NC, kTermsH>::kOwn;
+            float sums[OWN];
+            acc.join(tm + lanes, group, sums);
+#pragma unroll
+            for (int i = 0; i < OWN; ++i) {
+                const int j = group + kGroups * i;
+                if (j < im.count && n < p.K) __stcg(p.partials + size_t(im.pair + j) * p.K + n, sums[i]);
+            }
+            __threadfence();
+            named_sync(1, 32 * kWorkers);
+            if (tid == 0) s_last = atomicAdd(p.counters + 1 + im.tl, 1u) == unsigned(entries - 1);
+            named_sync(1, 32 * kWorkers);
+            if (!s_last) continue;
+            __threadfence();
+            if (n < p.K)
+                for (int t = group; t < p.M; t += kGroups) {
+                    float s = 0.0f;
+                    for (int j0 = 0; j0 < p.k; j0 += 4) {
+                        float v[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) v[j] = j0 + j < p.k ? __ldcg(p.partials + size_t(s_pos[t * p.k + j0 + j]) * p.K + n) : 0.0f;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            if (j0 + j < p.k) s = __fmaf_rn(s_w[t * p.k + j0 + j], v[j], s);
+                    }
+                    const size_t at = size_t(t) * p.K + n;
+                    if (p.f32_out) static_cast<float *>(p.y)[at] = s;
+                    else static_cast<__nv_bfloat16 *>(p.y)[at] = __float2bfloat16_rn(s);
+                }
+        }
     }
-    if (lane) return;
-    const size_t at = size_t(m) * p.K + n;
-    if (p.f32_out) static_cast<float *>(p.y)[at] = y;
-    else static_cast<__nv_bfloat16 *>(p.y)[at] = __float2bfloat16_rn(y);
+    __syncwarp();
+    tmem_fence_before();
+    __syncthreads();
+    tmem_fence_after();
+    if (warp == kWorkers) tmem_free(tm, kTmemColumns);
 }
 
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 qmv_status check_moe(int M, int K, int I, int E, int k, int bits, int gs)
 {
-    qmv_status st = qmv::check_weights(M, 1, K, bits, gs);
+    qmv_status st = check_weights(M, 1, K, bits, gs);
     if (st != QMV_OK) return st;
-    if (I < 1 || I > (1 << 24) || I % gs) return QMV_ERR_SHAPE;
-    if (E < 1 || E > QMV_MAX_EXPERTS || k < 1 || k > E || k > QMV_MAX_TOP_K) return QMV_ERR_COUNT;
+    if (K > (1 << 16) || I < 1 || I > (1 << 16) || I % gs) return QMV_ERR_SHAPE;
+    if (E < 1 || E > QMV_MAX_EXPERTS || k < 1 || k > E || k > QMV_MAX_TOP_K || M * k > QMV_MAX_CHOICES) return QMV_ERR_COUNT;
     if ((long long)E * 2 * I * (K / gs) >= (1ll << 31) || (long long)E * K * (I / gs) >= (1ll << 31) ||
         (long long)E * 2 * I > (1 << 30) || (long long)E * K > (1 << 30))
         return QMV_ERR_SHAPE;
     return QMV_OK;
 }
 
+size_t up256(size_t b) { return (b + 255) & ~size_t(255); }
+
+struct MoeSizes {
+    size_t logits, rows, xmeta, hcells, hmeta, partials, counters, total;
+};
+
+// Tokens of an expert that one read of its weights serves: 2, 4 or 8, so that
+// the mean number and some spread fit.
+int columns(int M, int E, int k)
+{
+    const double mean = double(M) * k / E;
+    if (M <= 2 || mean <= 0.3) return 2;
+    return M <= 4 || mean <= 1.5 ? 4 : 8;
+}
+
+MoeParams plan_moe(int M, int K, int I, int E, int k, int bits, int gs, int nc, MoeSizes &z)
+{
+    const int subs = tile::slot_subs(bits);
+    MoeParams p{};
+    p.M = M; p.K = K; p.I = I; p.E = E; p.k = k; p.gs = gs;
+    p.Sa = K / 64; p.NSa = (p.Sa + subs - 1) / subs; p.Ga = K / gs;
+    p.Sb = I / 64; p.NSb = (p.Sb + subs - 1) / subs; p.Gb = I / gs;
+    p.tiles_a = I / kHalf;
+    p.tiles_b = (K + tile::kTileRows - 1) / tile::kTileRows;
+    p.words = (M + 31) / 32;
+    const int pairs = M * k;
+    p.max_entries = pairs < E + pairs / nc ? pairs : E + pairs / nc;
+    p.sba = tile::Affines::plan(p.Ga, p.Ga < kChunkGroups ? p.Ga : kChunkGroups, tile::kTileRows, 64);
+    p.sbb = tile::Affines::plan(p.Gb, p.Gb < kChunkGroups ? p.Gb : kChunkGroups, tile::kTileRows, 64);
+    p.cha = p.sba.mode == tile::kSbWhole ? p.NSa : kChunkGroups * gs / 64 / subs;
+    p.chb = p.sbb.mode == tile::kSbWhole ? p.NSb : kChunkGroups * gs / 64 / subs;
+    p.sb_block = p.sba.block > p.sbb.block ? p.sba.block : p.sbb.block;
+    const size_t hs = size_t(p.max_entries) * p.NSb * subs;
+    z.logits = up256(size_t(M) * E * 4);
+    z.rows = up256(size_t(M) * p.NSa * subs * 128);
+    z.xmeta = up256(size_t(M) * p.NSa * subs * 8);
+    z.hcells = up256(hs * tile::cell_bytes(nc, kTermsH));
+    z.hmeta = up256(hs * tile::meta_bytes(nc));
+    z.partials = up256(size_t(pairs) * K * 4);
+    z.counters = up256(size_t(1 + p.tiles_b) * 4);
+    z.total = z.logits + z.rows + z.xmeta + z.hcells + z.hmeta + z.partials + z.counters;
+    return p;
+}
+
+struct MoeMaps {
+    CUtensorMap wa, sa, ba, wb, sb, bb;
+};
+
+template <int BITS, int GS, int NC>
+cudaError_t launch_experts(const MoeMaps &m, MoeParams &p, int sms, cudaStream_t stream)
+{
+    static std::atomic<int> configured[64] = {};
+    p.slots = kMaxSlotsMoe;
+    // (four at least: a group waits for its next slot while it holds one)
+    while (p.slots > 4 && moe_layout<BITS, NC>(p).total > kSmemMoe) --p.slots;
+    const int smem = moe_layout<BITS, NC>(p).total;
+    if (smem > kSmemMoe) return cudaErrorInvalidConfiguration;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    static std::mutex lock;
+    if (configured[dev].load() < smem) {
+        std::lock_guard<std::mutex> hold(lock);
+        if (configured[dev].load() < smem) {
+            e = cudaFuncSetAttribute(moe_experts<BITS, GS, NC>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+            if (e != cudaSuccess) return e;
+            configured[dev].store(smem);
+        }
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(sms);
+    cfg.blockDim = dim3(tile::kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeCooperative;
+    attr[0].val.cooperative = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, moe_experts<BITS, GS, NC>, m.wa, m.sa, m.ba, m.wb, m.sb, m.bb, p);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <int BITS, int GS>
+cudaError_t launch_experts_nc(int nc, const MoeMaps &m, MoeParams &p, int sms, cudaStream_t stream)
+{
+    if (nc == 2) return launch_experts<BITS, GS, 2>(m, p, sms, stream);
+    if (nc == 4) return launch_experts<BITS, GS, 4>(m, p, sms, stream);
+    return launch_experts<BITS, GS, 8>(m, p, sms, stream);
+}
+
+template <int BITS>
+cudaError_t launch_moe(int nc, const MoeMaps &m, MoeParams &p, int sms, cudaStream_t stream)
+{
+    static std::atomic<int> configured[64] = {};
+    Launch l;
+    l.grid = dim3(p.stage_blocks + p.E);
+    l.threads = kLogitThreads;
+    l.smem = 0;
+    l.pdl = true;
+    const cudaError_t e = launch_one(moe_logits<BITS>, configured, l, stream, p);
+    if (e != cudaSuccess) return e;
+    return p.gs == 64 ? launch_experts_nc<BITS, 64>(nc, m, p, sms, stream) : launch_experts_nc<BITS, 128>(nc, m, p, sms, stream);
+}
+
 }  // namespace
+}  // namespace qmv
 
 extern "C" size_t qmv_moe_workspace_size(int M, int K, int inter, int experts, int top_k, int bits, int group_size)
 {
-    if (check_moe(M, K, inter, experts, top_k, bits, group_size) != QMV_OK) return 0;
-    return size_t(M) * top_k * (size_t(inter) + 2) * 4;
+    if (qmv::check_moe(M, K, inter, experts, top_k, bits, group_size) != QMV_OK) return 0;
+    qmv::MoeSizes z;
+    qmv::plan_moe(M, K, inter, experts, top_k, bits, group_size, qmv::columns(M, experts, top_k), z);
+    return z.total;
 }
 
 extern "C" qmv_status qmv_moe_run(const uint16_t *x, const uint16_t *router, const uint32_t *gu_w,
@@ -158,6 +748,7 @@ extern "C" qmv_status qmv_moe_run(const uint16_t *x, const uint16_t *router, con
                                   int group_size, void *workspace, size_t workspace_bytes, unsigned flags,
                                   qmv_stream_t stream)
 {
+    using namespace qmv;
     if (!x || !router || !gu_w || !gu_scales || !gu_biases || !dn_w || !dn_scales || !dn_biases || !y)
         return QMV_ERR_NULL;
     qmv_status st = check_moe(M, K, inter, experts, top_k, bits, group_size);
@@ -169,31 +760,47 @@ extern "C" qmv_status qmv_moe_run(const uint16_t *x, const uint16_t *router, con
         if (!aligned(ptr, 16)) return QMV_ERR_ALIGN;
     if (!aligned(y, flags & QMV_F32_OUT ? 4 : 2) || !aligned(topk_ids, 4) || !aligned(topk_weights, 4))
         return QMV_ERR_ALIGN;
-    qmv::DeviceInfo dev;
-    st = qmv::current_device(&dev);
+    DeviceInfo dev;
+    st = current_device(&dev);
     if (st != QMV_OK) return st;
+    const int nc = columns(M, experts, top_k);
+    MoeSizes z;
+    MoeParams p = plan_moe(M, K, inter, experts, top_k, bits, group_size, nc, z);
     void *ws = nullptr;
-    st = qmv::scratch(dev, qmv_moe_workspace_size(M, K, inter, experts, top_k, bits, group_size), workspace,
-                      workspace_bytes, &ws);
+    st = scratch(dev, z.total, workspace, workspace_bytes, &ws);
     if (st != QMV_OK) return st;
 
-    const size_t pairs = size_t(M) * top_k;
-    MoeParams p{};
     p.x = x; p.router = router;
-    p.gu_w = gu_w; p.gu_s = gu_scales; p.gu_b = gu_biases;
-    p.dn_w = dn_w; p.dn_s = dn_scales; p.dn_b = dn_biases;
+    p.gu_s = gu_scales; p.gu_b = gu_biases; p.dn_s = dn_scales; p.dn_b = dn_biases;
     p.y = y; p.ids_out = topk_ids; p.weights_out = topk_weights;
-    p.h = static_cast<float *>(ws);
-    p.ids = reinterpret_cast<int32_t *>(p.h + pairs * inter);
-    p.weights = reinterpret_cast<float *>(p.ids + pairs);
-    p.M = M; p.K = K; p.I = inter; p.E = experts; p.k = top_k; p.bits = bits; p.gs = group_size;
+    p.err = dev.err;
     p.f32_out = (flags & QMV_F32_OUT) != 0;
     p.gelu = (flags & QMV_MOE_GELU) != 0;
     p.softmax_all = (flags & QMV_MOE_SOFTMAX_ALL) != 0;
+    uint8_t *at = static_cast<uint8_t *>(ws);
+    p.logits = reinterpret_cast<float *>(at); at += z.logits;
+    p.rows = at; at += z.rows;
+    p.xmeta = reinterpret_cast<float2 *>(at); at += z.xmeta;
+    p.hcells = at; at += z.hcells;
+    p.hmeta = at; at += z.hmeta;
+    p.partials = reinterpret_cast<float *>(at); at += z.partials;
+    p.counters = reinterpret_cast<unsigned *>(at);
+    p.stage_blocks = int(((long long)M * p.NSa * tile::slot_subs(bits) * 8 + kLogitThreads - 1) / kLogitThreads);
+
+    MoeMaps m{};
+    const long long ra = (long long)experts * 2 * inter, rb = (long long)experts * K;
+    st = encode_rows(&m.wa, gu_w, (long long)K * bits / 8, ra, tile::kSlotBytes / 8, kHalf, true);
+    if (st == QMV_OK) st = encode_rows(&m.wb, dn_w, (long long)inter * bits / 8, rb, tile::kSlotBytes / 8, kHalf, true);
+    if (p.sba.mode == tile::kSbBoxes) {
+        if (st == QMV_OK) st = encode_rows(&m.sa, gu_scales, p.Ga * 2ll, ra, p.sba.pitch / 8, kHalf, false);
+        if (st == QMV_OK) st = encode_rows(&m.ba, gu_biases, p.Ga * 2ll, ra, p.sba.pitch / 8, kHalf, false);
+    }
+    if (p.sbb.mode == tile::kSbBoxes) {
+        if (st == QMV_OK) st = encode_rows(&m.sb, dn_scales, p.Gb * 2ll, rb, p.sbb.pitch / 8, kHalf, false);
+        if (st == QMV_OK) st = encode_rows(&m.bb, dn_biases, p.Gb * 2ll, rb, p.sbb.pitch / 8, kHalf, false);
+    }
+    if (st != QMV_OK) return st;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    moe_route<<<M, 256, 0, s>>>(p);
-    moe_hidden<<<dim3((inter + 7) / 8, unsigned(pairs)), 256, 0, s>>>(p);
-    moe_down<<<dim3((K + 7) / 8, M), 256, 0, s>>>(p);
-    const cudaError_t e = cudaGetLastError();
-    return e == cudaSuccess ? QMV_OK : qmv::record_cuda_failure("moe kernel launch", e);
+    const cudaError_t e = bits == 4 ? launch_moe<4>(nc, m, p, dev.sms, s) : launch_moe<2>(nc, m, p, dev.sms, s);
+    return e == cudaSuccess ? QMV_OK : record_cuda_failure("moe kernel launch", e);
 }

@@ -54,17 +54,19 @@ constexpr int kTileRows = 128;
 constexpr int kSlotBytes = 128;              // bytes of a row in a ring slot
 
 __host__ __device__ constexpr int slot_subs(int bits) { return kSlotBytes * 8 / bits / 64; }  // 4 or 8
-// Bytes of a subgroup's B operand for up to nc vectors: atoms of 8 rows x 64 bytes.
-__host__ __device__ constexpr int cell_bytes(int nc) { return nc <= 4 ? 512 : nc <= 8 ? 1024 : 2048; }
+// nc vectors of `terms` e4m3 each are the rows of a subgroup's B operand: atoms of
+// 8 rows x 64 bytes. The instruction's N is 16 at least; where there are only 8
+// rows its second eight are the first again.
+__host__ __device__ constexpr int operand_rows(int nc, int terms = 2) { return nc * terms; }
+__host__ __device__ constexpr int cell_bytes(int nc, int terms = 2) { return operand_rows(nc, terms) <= 8 ? 512 : operand_rows(nc, terms) * 64; }
 // Bytes of a subgroup's (sum, sum, f, f), for each pair of vectors.
 __host__ __device__ constexpr int meta_bytes(int nc) { return nc / 2 * 16; }
-// Columns of an accumulator (the instruction's N; up to 4 vectors its second
-// eight rows are the first again).
-__host__ __device__ constexpr int acc_columns(int nc) { return nc <= 8 ? 16 : 32; }
+// Columns of an accumulator: the instruction's N.
+__host__ __device__ constexpr int acc_columns(int nc, int terms = 2) { return operand_rows(nc, terms) <= 16 ? 16 : operand_rows(nc, terms); }
 // Subgroups of a step, and a group's columns of A (two steps) and of accumulators.
-__host__ __device__ constexpr int step_subs(int nc) { return nc <= 8 ? 2 : 1; }
-__host__ __device__ constexpr int a_columns(int nc) { return 2 * step_subs(nc) * 16; }
-__host__ __device__ constexpr int d_columns(int nc) { return 2 * step_subs(nc) * acc_columns(nc); }
+__host__ __device__ constexpr int step_subs(int nc, int terms = 2) { return operand_rows(nc, terms) <= 16 ? 2 : 1; }
+__host__ __device__ constexpr int a_columns(int nc, int terms = 2) { return 2 * step_subs(nc, terms) * 16; }
+__host__ __device__ constexpr int d_columns(int nc, int terms = 2) { return 2 * step_subs(nc, terms) * acc_columns(nc, terms); }
 constexpr int kTmemColumns = 512;
 
 __device__ __forceinline__ uint64_t pack2(float lo, float hi)
@@ -116,17 +118,18 @@ __device__ __forceinline__ void from_e4m3x2(uint32_t v, float &a, float &b)
         : "r"(h));
 }
 
-// Row of the B operand that holds term h (hi, lo) of vector tok: pairs of
-// vectors together, so that their sums are adjacent accumulator columns.
-__device__ __forceinline__ int operand_index(int tok, int h) { return (tok >> 1) * 4 + h * 2 + (tok & 1); }
+// Row of the B operand that holds term h of vector tok: pairs of vectors
+// together, so that their sums are adjacent accumulator columns.
+__device__ __forceinline__ int operand_index(int tok, int h, int terms = 2) { return (tok >> 1) * 2 * terms + h * 2 + (tok & 1); }
 // Byte of 16-byte piece c of that row in a subgroup's cell (64-byte swizzle).
 __device__ __forceinline__ int operand_offset(int r, int c) { return (r >> 3) * 512 + (r & 7) * 64 + ((c ^ (r >> 1)) & 3) * 16; }
 
 // Stages eight elements of a vector: octet o (0..7) of a subgroup, by the eight
 // consecutive threads of a warp that hold its octets. x: elements 8 o .. 8 o + 7;
-// tok: the vector's index in its block; cell, meta: the subgroup's.
-template <int BITS>
-__device__ __forceinline__ void stage_octet(const float (&x)[8], int o, int tok, uint8_t *cell, uint8_t *meta)
+// piece(h): where the 16-byte piece o / 2 of term h goes; keep(sum, f) is called
+// by one of the eight.
+template <int BITS, typename Piece, typename Keep>
+__device__ __forceinline__ void stage_octet(const float (&x)[8], int o, Piece piece, Keep keep)
 {
     float sum = 0.0f;
     uint32_t E = 1;
@@ -154,7 +157,7 @@ __device__ __forceinline__ void stage_octet(const float (&x)[8], int o, int tok,
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         const uint32_t *v = h ? lo : hi;
-        uint8_t *out = cell + operand_offset(operand_index(tok, h), o >> 1);
+        uint8_t *out = piece(h);
         // bytes of even elements and of odd ones, in order
         const uint32_t even = __byte_perm(__byte_perm(v[0], v[1], 0x0040), __byte_perm(v[2], v[3], 0x0040), 0x5410);
         const uint32_t odd = __byte_perm(__byte_perm(v[0], v[1], 0x0051), __byte_perm(v[2], v[3], 0x0051), 0x5410);
@@ -170,11 +173,7 @@ __device__ __forceinline__ void stage_octet(const float (&x)[8], int o, int tok,
             w[6] = uint16_t(__byte_perm(odd, 0, 0x0031));
         }
     }
-    if (o == 0) {
-        float *m = reinterpret_cast<float *>(meta + (tok >> 1) * 16) + (tok & 1);
-        m[0] = sum;
-        m[2] = exp2i(min(int(E) - 125, 127));  // 2^9 / 2^p
-    }
+    if (o == 0) keep(sum, exp2i(min(int(E) - 125, 127)));  // 2^9 / 2^p
 }
 
 // Eight bf16 of a 16-byte load as floats.
@@ -245,7 +244,7 @@ __device__ __forceinline__ float tmem_ld1(uint32_t a)
 template <int N>
 __device__ __forceinline__ void tmem_ld(uint32_t a, float (&v)[N])
 {
-    static_assert(N == 4 || N == 8 || N == 16 || N == 32, "columns");
+    static_assert(N == 4 || N == 8 || N == 16 || N == 32 || N == 64, "columns");
     if constexpr (N == 4)
         asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
                      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
@@ -261,13 +260,12 @@ __device__ __forceinline__ void tmem_ld(uint32_t a, float (&v)[N])
               "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
             : "r"(a));
     else {
-        float lo[16], hi[16];
-        tmem_ld<16>(a, lo);
-        tmem_ld<16>(a + 16, hi);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            v[i] = lo[i];
-            v[16 + i] = hi[i];
+        for (int k = 0; k < N / 16; ++k) {
+            float part[16];
+            tmem_ld<16>(a + 16 * k, part);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[16 * k + i] = part[i];
         }
     }
 }
@@ -347,18 +345,16 @@ enum { kSbBoxes, kSbWhole, kSbRows };
 struct Affines {
     int mode, pitch, block;  // bytes from row to row, and of each of the two arrays
 
-    __host__ __device__ static Affines plan(int G, int groups, int rows)
+    // `whole`: most groups of a row that are fetched as whole rows.
+    __host__ __device__ static Affines plan(int G, int groups, int rows, int whole)
     {
         Affines a;
-        a.mode = G % 8 == 0 ? kSbBoxes : G <= 96 ? kSbWhole : kSbRows;
+        a.mode = G % 8 == 0 ? kSbBoxes : G <= whole ? kSbWhole : kSbRows;
         a.pitch = a.mode == kSbWhole ? 2 * G : (((2 * groups + 30) / 16) | 1) * 16;
         a.block = (rows * a.pitch + 127) & ~127;
         return a;
     }
-    // Arrivals that one fetch makes on its barrier.
-    __device__ __forceinline__ int arrivals() const { return mode == kSbRows ? 32 : 1; }
-
-    // By the whole producer warp: rows row0 .. row0 + rows - 1 of `all`, groups g0 ..
+    // By the whole producer warp, each lane arriving once on `bar`: rows row0 .. row0 + rows - 1 of `all`, groups g0 ..
     // g0 + groups - 1 of G, into dst (generic address `gen`). smap, bmap: tensor
     // maps for kSbBoxes, at row `mrow0` of the map.
     __device__ __forceinline__ void fetch(uint32_t dst, uint8_t *gen, const uint16_t *sc, const uint16_t *bi,
@@ -370,6 +366,8 @@ struct Affines {
                 mbar_arrive_expect_tx(bar, uint32_t(2 * rows * pitch));
                 tma_load_2d(dst, smap, g0 / 8 * 2, int(row0), bar);  // eight groups are two elements
                 tma_load_2d(dst + block, bmap, g0 / 8 * 2, int(row0), bar);
+            } else {
+                mbar_arrive(bar);
             }
             return;
         }
@@ -397,7 +395,7 @@ struct Affines {
                     bulk_load_plain(dst + d + block, reinterpret_cast<const uint8_t *>(bi) + from, bytes, bar);
                 }
             }
-            if (pass == 0 && (mode == kSbRows || lane == 0)) mbar_arrive_expect_tx(bar, total);
+            if (pass == 0) mbar_arrive_expect_tx(bar, total);
         }
     }
     // Offset of group g0 of a row in its bytes there.
@@ -471,20 +469,21 @@ struct Pipe {
     uint32_t stored, ready, a, d;
     uint32_t steps;
 
-    template <int NC>
+    template <int NC, int TERMS = 2>
     __device__ __forceinline__ static Pipe make(uint32_t tm, uint32_t lanes, uint32_t stored0, uint32_t ready0, int group)
     {
-        return {stored0 + 16 * group, ready0 + 16 * group, tm + lanes + group * a_columns(NC),
-                tm + lanes + kGroups * a_columns(NC) + group * d_columns(NC), 0u};
+        return {stored0 + 16 * group, ready0 + 16 * group, tm + lanes + group * a_columns(NC, TERMS),
+                tm + lanes + kGroups * a_columns(NC, TERMS) + group * d_columns(NC, TERMS), 0u};
     }
 };
 
 // A worker thread's row of a tile: sums of NC vectors over the slots it is given.
 // Two steps are in flight: the accumulators of one are read two steps later, when
 // its A columns are needed again.
-template <int BITS, int GS, int NC>
+template <int BITS, int GS, int NC, int TERMS = 2>
 struct Row {
-    static constexpr int kSubs = slot_subs(BITS), kStep = step_subs(NC), kSteps = kSubs / kStep;
+    static constexpr int kSubs = slot_subs(BITS), kStep = step_subs(NC, TERMS), kSteps = kSubs / kStep;
+    static constexpr int kVals = TERMS * NC;
     static_assert(kSteps % 2 == 0, "a slot's steps use the two buffers alike");
     uint64_t y[NC / 2];
     float last_s[2 * kStep], last_b[2 * kStep];  // of the previous slot's last two steps
@@ -499,7 +498,7 @@ struct Row {
         primed = false;
     }
 
-    __device__ __forceinline__ void add(const float (&v)[2 * NC], float s, float b, uint32_t meta)
+    __device__ __forceinline__ void add(const float (&v)[kVals], float s, float b, uint32_t meta)
     {
         const uint64_t ss = pack2(s, s), bb = pack2(b, b), r32 = pack2(0.03125f, 0.03125f);
 #pragma unroll
@@ -507,7 +506,11 @@ struct Row {
             const uint4 m = lds_128(meta + c * 16);
             const uint64_t sum = pack2(__uint_as_float(m.x), __uint_as_float(m.y));
             const uint64_t f = pack2(__uint_as_float(m.z), __uint_as_float(m.w));
-            const uint64_t d = mul2(fma2(pack2(v[4 * c + 2], v[4 * c + 3]), r32, pack2(v[4 * c], v[4 * c + 1])), f);
+            // terms from the last, each 1/32 of the one before
+            uint64_t d = pack2(v[2 * TERMS * c + 2 * TERMS - 2], v[2 * TERMS * c + 2 * TERMS - 1]);
+#pragma unroll
+            for (int h = TERMS - 2; h >= 0; --h) d = fma2(d, r32, pack2(v[2 * TERMS * c + 2 * h], v[2 * TERMS * c + 2 * h + 1]));
+            d = mul2(d, f);
             y[c] = fma2(ss, d, fma2(bb, sum, y[c]));
             // (keeps the loads of the next pairs from being hoisted into registers
             // that are not there)
@@ -521,7 +524,7 @@ struct Row {
     __device__ __forceinline__ void slot(const Waits &wait, Pipe &p, uint32_t w, const Affine<BITS, GS> &aff, uint32_t meta,
                                          uint32_t last_meta, int lane)
     {
-        constexpr int MB = meta_bytes(NC), ND = acc_columns(NC);
+        constexpr int MB = meta_bytes(NC), ND = acc_columns(NC, TERMS);
 #pragma unroll
         for (int j = 0; j < kSteps; ++j) {
             uint32_t words[kStep][2 * BITS];
@@ -538,9 +541,9 @@ struct Row {
             const bool take = j >= 2 || primed;
             if (take) wait(p.ready + 8 * (j & 1), ((p.steps + j) / 2 + 1) & 1);
             tmem_fence_after();
-            float v[kStep][2 * NC];
+            float v[kStep][kVals];
 #pragma unroll
-            for (int u = 0; u < kStep; ++u) tmem_ld<2 * NC>(p.d + ((j & 1) * kStep + u) * ND, v[u]);
+            for (int u = 0; u < kStep; ++u) tmem_ld<kVals>(p.d + ((j & 1) * kStep + u) * ND, v[u]);
 #pragma unroll
             for (int u = 0; u < kStep; ++u) {
                 uint32_t r[16];
@@ -580,9 +583,9 @@ struct Row {
         for (int j = 0; j < 2; ++j) {
             wait(p.ready + 8 * j, (p.steps / 2 + 1) & 1);
             tmem_fence_after();
-            float v[kStep][2 * NC];
+            float v[kStep][kVals];
 #pragma unroll
-            for (int u = 0; u < kStep; ++u) tmem_ld<2 * NC>(p.d + (j * kStep + u) * acc_columns(NC), v[u]);
+            for (int u = 0; u < kStep; ++u) tmem_ld<kVals>(p.d + (j * kStep + u) * acc_columns(NC, TERMS), v[u]);
             tmem_wait_ld();
 #pragma unroll
             for (int u = 0; u < kStep; ++u) {
@@ -602,8 +605,8 @@ struct Row {
         for (int c = 0; c < NC / 2; ++c) {
             float lo, hi;
             unpack2(y[c], lo, hi);
-            tmem_st1(tm + group * a_columns(NC) + 2 * c, lo);
-            tmem_st1(tm + group * a_columns(NC) + 2 * c + 1, hi);
+            tmem_st1(tm + group * a_columns(NC, TERMS) + 2 * c, lo);
+            tmem_st1(tm + group * a_columns(NC, TERMS) + 2 * c + 1, hi);
         }
         tmem_wait_st();
         tmem_fence_before();
@@ -613,7 +616,7 @@ struct Row {
 #pragma unroll
         for (int i = 0; i < kOwn; ++i)
 #pragma unroll
-            for (int g = 0; g < kGroups; ++g) v[i][g] = tmem_ld1(tm + g * a_columns(NC) + min(group + kGroups * i, NC - 1));
+            for (int g = 0; g < kGroups; ++g) v[i][g] = tmem_ld1(tm + g * a_columns(NC, TERMS) + min(group + kGroups * i, NC - 1));
         tmem_wait_ld();
 #pragma unroll
         for (int i = 0; i < kOwn; ++i) {
@@ -628,17 +631,20 @@ struct Row {
 
 // The tensor warp's part of one slot: waits for each step's A operands and
 // multiplies them with the subgroups' cells. `cell` is the slot's first.
-template <int BITS, int NC>
+// FENCE: the cells were written by threads, not by bulk copies.
+template <int BITS, int NC, int TERMS = 2, bool FENCE = false>
 __device__ __forceinline__ void multiply_slot(const Waits &wait, Pipe &p, uint32_t cell)
 {
-    constexpr int ND = acc_columns(NC), CB = cell_bytes(NC), U = step_subs(NC), STEPS = slot_subs(BITS) / U;
+    constexpr int ND = acc_columns(NC, TERMS), CB = cell_bytes(NC, TERMS), U = step_subs(NC, TERMS);
+    constexpr int STEPS = slot_subs(BITS) / U;
 #pragma unroll
     for (int j = 0; j < STEPS; ++j) {
         wait(p.stored + 8 * (j & 1), ((p.steps + j) / 2) & 1);
+        if (FENCE && j == 0) fence_proxy_async_smem();
         tmem_fence_after();
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const uint64_t b = b_descriptor(cell + (j * U + u) * CB, NC <= 4 ? 0 : 512);
+            const uint64_t b = b_descriptor(cell + (j * U + u) * CB, operand_rows(NC, TERMS) <= 8 ? 0 : 512);
             const uint32_t a = p.a + ((j & 1) * U + u) * 16, d = p.d + ((j & 1) * U + u) * ND;
             tmem_mma<ND>(d, a, b, false);
             tmem_mma<ND>(d, a + 8, b + 2, true);

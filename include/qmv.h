@@ -350,8 +350,9 @@ QMV_API qmv_status qmv_lora_run(const uint32_t *w_q, const uint16_t *scales, con
  *  y                 device, bf16 [M, K] (fp32 with QMV_F32_OUT).
  *  topk_ids          device, int32 [M, top_k], or NULL: ids, the largest first.
  *  topk_weights      device, float [M, top_k], or NULL: weights, in the same order.
- *  M                 1 .. QMV_MAX_M.  K and inter multiples of group_size.
- *  experts           1 .. QMV_MAX_EXPERTS.  top_k 1 .. min(experts, QMV_MAX_TOP_K).
+ *  M                 1 .. QMV_MAX_M.  K and inter multiples of group_size, at most 65536.
+ *  experts           1 .. QMV_MAX_EXPERTS.  top_k 1 .. min(experts, QMV_MAX_TOP_K), M * top_k
+ *                    at most QMV_MAX_CHOICES.
  *  flags             QMV_F32_OUT, QMV_MOE_GELU, QMV_MOE_SOFTMAX_ALL.
  *
  * A NaN router logit counts as -inf. Arithmetic: fp32 sums throughout; h is
@@ -362,6 +363,7 @@ QMV_API qmv_status qmv_lora_run(const uint32_t *w_q, const uint16_t *scales, con
  * group_size or experts x rows x groups reaches 2^31. */
 #define QMV_MAX_EXPERTS 1024
 #define QMV_MAX_TOP_K 32
+#define QMV_MAX_CHOICES 4096
 #define QMV_MOE_GELU 0x10u
 #define QMV_MOE_SOFTMAX_ALL 0x20u
 QMV_API size_t qmv_moe_workspace_size(int M, int K, int inter, int experts, int top_k, int bits, int group_size);

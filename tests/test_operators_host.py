@@ -49,7 +49,7 @@ MOE = (["x", "router", "gu_w", "gu_s", "gu_b", "dn_w", "dn_s", "dn_b", "y", "ids
     *[({p: None}, 1) for p in MOE[0][:9]],
     (dict(bits=8), 2), (dict(gs=96), 3), (dict(K=100), 4), (dict(inter=100), 4), (dict(inter=0), 4), (dict(K=0), 4),
     (dict(inter=192, gs=128), 4), (dict(M=0), 5), (dict(M=257), 5), (dict(E=0), 11), (dict(E=1025), 11), (dict(k=0), 11),
-    (dict(k=9), 11), (dict(E=64, k=33), 11), (dict(K=1 << 20, inter=1 << 20), 4), (dict(flags=2), 10), (dict(flags=0x40), 10),
+    (dict(k=9), 11), (dict(E=64, k=33), 11), (dict(M=256, E=64, k=17), 11), (dict(K=1 << 20, inter=1 << 20), 4), (dict(flags=2), 10), (dict(flags=0x40), 10),
     *[({p: FAKE + 8}, 6) for p in MOE[0][:8] + ["workspace"]],
     (dict(y=FAKE + 1), 6), (dict(y=FAKE + 2, flags=1), 6), (dict(ids=FAKE + 2), 6), (dict(weights=FAKE + 2), 6),
 ])
