@@ -8,12 +8,13 @@
 // argmax r(v) / e(v), r = max(p - q, 0) or p, which joins from parts too.
 //
 // Two kernels.
-//  1. verify_rows reads the logits once, 16 bytes at a time, a part of a row to a
-//     block: all of a part is in flight before any of it is used, and stays in
-//     registers from the maximum to the sum. Rows that no outcome needs (past a
-//     sequence's drafts; draft rows where the argmax decides) are not read. It is
-//     bound by memory, with the integer pipe and the exponentials close behind (5
-//     instructions an element).
+//  1. verify_rows reads the logits once, 16 bytes at a time. A warp takes parts of
+//     rows in turn and goes through each in pieces of 4 KB: a piece stays in
+//     registers from its maximum to its sum while the next one's loads, of the
+//     same part or of the next, are in flight; warps never wait for one another.
+//     Rows that no outcome needs (past a sequence's drafts; draft rows where the
+//     argmax decides) are not read. It is bound by memory, with the integer pipe
+//     and the exponentials close behind (5 instructions an element).
 //  2. verify_emit, several blocks to a sequence: each joins the parts of the
 //     sequence's rows, decides how many tokens are accepted and runs its share of
 //     the race on the one row that matters; the last of a sequence's blocks joins
@@ -31,7 +32,10 @@ namespace {
 
 constexpr int kVerifyThreads = 256;
 constexpr int kVerifyWarps = kVerifyThreads / 32;
+constexpr int kRowThreads = 128, kRowBlocks = 4;  // of verify_rows, and blocks on an SM
+constexpr int kMaxParts = 16;                     // of a row at most
 constexpr int kNone = 0x7fffffff;
+constexpr int kRace = 8 * kVerifyThreads;  // tokens of a block of verify_emit
 constexpr int kMaxRows = 2 * QMV_MAX_DRAFT + 1;
 
 // A part of a row: maximum, sum of exponentials relative to it, index of the
@@ -129,12 +133,19 @@ __device__ __forceinline__ uint32_t clean(uint32_t w)
     asm("{\n\t.reg .b32 t;\n\tmax.bf16x2 t, %1, %2;\n\tmin.bf16x2 %0, t, %3;\n\t}" : "=r"(d) : "r"(w), "r"(0xff80ff80u), "r"(0x7f7f7f7fu));
     return d;
 }
+// The larger, NaN where one is NaN.
 template <bool F32>
 __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b)
 {
-    if (F32) return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
     uint32_t d;
-    asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    if (F32) asm("max.NaN.f32 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    else asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+__device__ __forceinline__ float larger(float a, float b)
+{
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
     return d;
 }
 
@@ -168,73 +179,126 @@ __device__ __forceinline__ uint4 shifted(uint4 a, uint4 b, int bytes)
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// The 16 bytes of a row from element v0 on, elements past V as -inf. Inside the
-// row one aligned load, or two that are shifted; at the ends of a row that lies
-// off a 16-byte boundary (nothing beside the row is read) element by element.
+// The 16 bytes of a row from element v0 on, element by element, those past V as
+// -inf (nothing beside the row is read).
 template <bool F32>
-__device__ __forceinline__ uint4 load16(const uint8_t *base, long long v0, int V, int off)
+__device__ __noinline__ uint4 load16_apart(const uint8_t *base, long long v0, int V)
 {
-    constexpr int EV = F32 ? 4 : 8, SIZE = F32 ? 4 : 2;
+    constexpr int EV = F32 ? 4 : 8;
     const uint32_t none = F32 ? 0xff800000u : 0xff80ff80u;
-    uint4 x = make_uint4(none, none, none, none);
-    if (v0 >= V) return x;
-    const uint8_t *at = base + v0 * SIZE;
-    if (off == 0 && v0 + EV <= V) return __ldcs(reinterpret_cast<const uint4 *>(at));
-    if (off != 0 && v0 > 0 && v0 + 2 * EV <= V) {
-        const uint4 *q = reinterpret_cast<const uint4 *>(at - off);
-        return shifted(__ldg(q), __ldg(q + 1), off);
-    }
     uint32_t w[4] = {none, none, none, none};
 #pragma unroll
     for (int i = 0; i < EV; ++i) {
         if (v0 + i >= V) break;
-        if (F32) w[i & 3] = __ldg(reinterpret_cast<const uint32_t *>(at) + i);
+        if (F32) w[i & 3] = __ldg(reinterpret_cast<const uint32_t *>(base) + v0 + i);
         else {
-            const uint32_t h = __ldg(reinterpret_cast<const uint16_t *>(at) + i);
+            const uint32_t h = __ldg(reinterpret_cast<const uint16_t *>(base) + v0 + i);
             w[i / 2 & 3] = i & 1 ? (w[i / 2 & 3] & 0xffffu) | h << 16 : (w[i / 2 & 3] & 0xffff0000u) | h;
         }
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// One part of one row: NV vectors of 16 bytes to a thread, by the elements'
-// indexes alone, so that equal rows have equal sums wherever they lie.
-template <bool F32, int NV>
-__global__ void __launch_bounds__(kVerifyThreads, 4) verify_rows(const VerifyParams p)
+// N vectors of 16 bytes of a row, from element v0 on and `step` elements apart.
+// Inside the row one aligned load each, or where the row lies off a 16-byte
+// boundary (`off` bytes) two that are shifted; at its ends apart.
+template <bool F32, int N>
+__device__ __forceinline__ void load16(uint4 (&x)[N], const uint8_t *base, long long v0, int step, int V, int off)
 {
-    constexpr int EV = F32 ? 4 : 8;
-    __shared__ float scratch[kVerifyWarps];
-    __shared__ int s_arg;
-    const int tid = threadIdx.x;
-    const int part = blockIdx.x % p.nparts, row = blockIdx.x / p.nparts, b = row / p.rows, r = row - b * p.rows;
-    grid_dependency_wait();
-    grid_launch_dependents();
-    if (r == 0 && part == 0 && tid == 0) p.finished[b] = 0u;
-    const Mode m = mode_of(p, b);
-    if (r <= p.S ? r > m.len : m.greedy || r - p.S - 1 >= m.len) return;
-    const uint8_t *base = static_cast<const uint8_t *>(row_of<F32>(p, b, r));
-    const int off = int(reinterpret_cast<uintptr_t>(base) & 15);
-    const uint32_t none = F32 ? 0xff800000u : 0xff80ff80u;
-    const int v0 = part * kVerifyThreads * NV + tid;
-    uint4 x[NV];
+    constexpr int EV = F32 ? 4 : 8, SIZE = F32 ? 4 : 2;
+    const uint8_t *at = base + v0 * SIZE;
+    if (off == 0 && v0 + (N - 1) * step + EV <= V) {
 #pragma unroll
-    for (int k = 0; k < NV; ++k) x[k] = load16<F32>(base, (long long)(v0 + k * kVerifyThreads) * EV, p.V, off);
-    uint32_t top2 = none;
+        for (int k = 0; k < N; ++k) x[k] = __ldcs(reinterpret_cast<const uint4 *>(at + k * step * SIZE));
+    } else if (off != 0 && v0 > 0 && v0 + (N - 1) * step + 2 * EV <= V) {
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-        x[k] = make_uint4(clean<F32>(x[k].x), clean<F32>(x[k].y), clean<F32>(x[k].z), clean<F32>(x[k].w));
-        top2 = larger<F32>(top2, larger<F32>(larger<F32>(x[k].x, x[k].y), larger<F32>(x[k].z, x[k].w)));
+        for (int k = 0; k < N; ++k) {
+            const uint4 *q = reinterpret_cast<const uint4 *>(at + k * step * SIZE - off);
+            x[k] = shifted(__ldg(q), __ldg(q + 1), off);
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < N; ++k) x[k] = load16_apart<F32>(base, v0 + k * step, V);
     }
-    float top = F32 ? __uint_as_float(top2) : fmaxf(__uint_as_float(top2 << 16), __uint_as_float(top2 & 0xffff0000u));
-    top = block_max(top, scratch);
-    float sum = 0.0f;
-    int arg = kNone;
-    if (top > -INFINITY) {
-        const float c = __fmul_rn(m.inv, 1.4426950408889634f);
-        const uint64_t neg = pair_of(-top, -top), cc = pair_of(c, c);
-        uint64_t s2 = 0ull;
+}
+
+// Eight elements of a row from v0 on (a multiple of eight) as they count, those
+// past V as -inf.
+template <bool F32>
+__device__ __forceinline__ void load8(const uint8_t *base, long long v0, int V, int off, float (&x)[8])
+{
+    uint4 a[F32 ? 2 : 1];
+    load16<F32, F32 ? 2 : 1>(a, base, v0, F32 ? 4 : 8, V, off);
+    const uint32_t w[4] = {clean<F32>(a[0].x), clean<F32>(a[0].y), clean<F32>(a[0].z), clean<F32>(a[0].w)};
+    if (F32) {
+        const uint4 &b = a[F32 ? 1 : 0];
+        const uint32_t u[4] = {clean<F32>(b.x), clean<F32>(b.y), clean<F32>(b.z), clean<F32>(b.w)};
 #pragma unroll
-        for (int k = 0; k < NV; ++k) {
+        for (int i = 0; i < 4; ++i) {
+            x[i] = __uint_as_float(w[i]);
+            x[4 + i] = __uint_as_float(u[i]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[2 * i] = __uint_as_float(w[i] << 16);
+            x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    }
+}
+
+// Maximum, sum and first argmax of the pieces that a warp has seen.
+template <bool F32>
+struct Seen {
+    static constexpr int EV = F32 ? 4 : 8, kVecs = 8, kElems = kVecs * 32 * EV;
+    float top = -INFINITY, sum = 0.0f;  // the sum is the lane's own
+    int arg = kNone;
+
+    static __device__ __forceinline__ void load(uint4 (&x)[kVecs], const uint8_t *base, int piece, int V, int off, int lane)
+    {
+        load16<F32, kVecs>(x, base, (long long)piece * kElems + lane * EV, 32 * EV, V, off);
+    }
+
+    // By elements' indexes alone, so that equal rows have equal sums wherever they lie.
+    __device__ __forceinline__ void add(uint4 (&x)[kVecs], int piece, float c, bool greedy, int lane)
+    {
+        float here;
+        for (int pass = 0; pass < 2; ++pass) {
+            uint32_t top2 = F32 ? 0xff800000u : 0xff80ff80u;
+#pragma unroll
+            for (int k = 0; k < kVecs; ++k) top2 = larger<F32>(top2, larger<F32>(larger<F32>(x[k].x, x[k].y), larger<F32>(x[k].z, x[k].w)));
+            here = F32 ? __uint_as_float(top2) : larger(__uint_as_float(top2 << 16), __uint_as_float(top2 & 0xffff0000u));
+#pragma unroll
+            for (int d = 16; d; d >>= 1) here = larger(here, __shfl_xor_sync(0xffffffffu, here, d));
+            if (here < INFINITY) break;
+            // a NaN or +inf among them, seldom: what they count as
+#pragma unroll
+            for (int k = 0; k < kVecs; ++k) x[k] = make_uint4(clean<F32>(x[k].x), clean<F32>(x[k].y), clean<F32>(x[k].z), clean<F32>(x[k].w));
+        }
+        if (!(here > -INFINITY)) return;
+        if (greedy && here > top) {
+            // the first place of a new maximum
+            arg = kNone;
+#pragma unroll
+            for (int k = 0; k < kVecs; ++k) {
+                const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+#pragma unroll
+                for (int i = 0; i < EV; ++i) {
+                    const float l = F32 ? __uint_as_float(w[i & 3])
+                                        : __uint_as_float(i & 1 ? w[i / 2 & 3] & 0xffff0000u : w[i / 2 & 3] << 16);
+                    if (l == here) arg = min(arg, piece * kElems + (k * 32 + lane) * EV + i);
+                }
+            }
+            arg = __reduce_min_sync(0xffffffffu, arg);
+        }
+        if (here > top) {
+            sum = top > -INFINITY ? __fmul_rn(sum, ex2(__fmul_rn(__fsub_rn(top, here), c))) : 0.0f;
+            top = here;
+        }
+        const uint64_t neg = pair_of(-top, -top), cc = pair_of(c, c);
+        uint64_t s2 = pair_of(sum, 0.0f);
+#pragma unroll
+        for (int k = 0; k < kVecs; ++k) {
             const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
 #pragma unroll
             for (int i = 0; i < (F32 ? 2 : 4); ++i) {
@@ -248,40 +312,86 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) verify_rows(const VerifyPar
         float lo, hi;
         unpair(s2, lo, hi);
         sum = __fadd_rn(lo, hi);
-        if (m.greedy) {
-            // the first place of the maximum
-#pragma unroll
-            for (int k = 0; k < NV; ++k) {
-                const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
-                const int at = (v0 + k * kVerifyThreads) * EV;
-#pragma unroll
-                for (int i = 0; i < EV; ++i) {
-                    const float l = F32 ? __uint_as_float(w[i & 3]) : __uint_as_float(i & 1 ? w[i / 2 & 3] & 0xffff0000u : w[i / 2 & 3] << 16);
-                    if (l == top && at + i < arg) arg = at + i;
-                }
-            }
-        }
     }
+};
+
+// Where a warp is in its parts of rows.
+template <bool F32>
+struct Place {
+    int item, piece, end;  // row of all rows * nparts + part, -1: none left
+    const uint8_t *base;
+    float c;
+    bool greedy;
+
+    // The first part from `from` on, in steps of `step`, that an outcome needs.
+    __device__ __forceinline__ void find(const VerifyParams &p, long long from, int step, int items, int pieces)
+    {
+        for (; from < items; from += step) {
+            item = int(from);
+            const int row = item / p.nparts, part = item - row * p.nparts, b = row / p.rows, r = row - b * p.rows;
+            const Mode m = mode_of(p, b);
+            if (r <= p.S ? r > m.len : m.greedy || r - p.S - 1 >= m.len) continue;
+            base = static_cast<const uint8_t *>(row_of<F32>(p, b, r));
+            piece = int((long long)pieces * part / p.nparts);
+            end = int((long long)pieces * (part + 1) / p.nparts);
+            c = __fmul_rn(m.inv, 1.4426950408889634f);
+            greedy = m.greedy;
+            return;
+        }
+        item = -1;
+    }
+    __device__ __forceinline__ void advance(const VerifyParams &p, int step, int items, int pieces)
+    {
+        if (++piece >= end) find(p, (long long)item + step, step, items, pieces);
+    }
+};
+
+template <bool F32>
+__global__ void __launch_bounds__(kRowThreads, kRowBlocks) verify_rows(const VerifyParams p)
+{
+    using See = Seen<F32>;
+    const int lane = threadIdx.x % 32, step = gridDim.x * (kRowThreads / 32), items = p.B * p.rows * p.nparts;
+    const int pieces = (p.V + See::kElems - 1) / See::kElems;
+    grid_dependency_wait();
+    grid_launch_dependents();
+    for (int i = blockIdx.x * kRowThreads + threadIdx.x; i < p.B; i += gridDim.x * kRowThreads) p.finished[i] = 0u;
+    auto load = [&](uint4(&x)[See::kVecs], const Place<F32> &at) {
+        See::load(x, at.base, at.piece, p.V, int(reinterpret_cast<uintptr_t>(at.base) & 15), lane);
+    };
+    See seen;
+    // adds the piece at `at`; where `next` is of another part, the part is done
+    auto take = [&](uint4(&x)[See::kVecs], const Place<F32> &at, const Place<F32> &next) {
+        seen.add(x, at.piece, at.c, at.greedy, lane);
+        if (next.item == at.item) return;
+        float sum = seen.sum;
 #pragma unroll
-    for (int d = 16; d; d >>= 1) sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, d));
-    if (tid == 0) s_arg = kNone;
-    __syncthreads();
-    if (tid % 32 == 0) scratch[tid / 32] = sum;
-    if (arg != kNone) atomicMin(&s_arg, arg);
-    __syncthreads();
-    if (tid) return;
-    sum = scratch[0];
-#pragma unroll
-    for (int w = 1; w < kVerifyWarps; ++w) sum = __fadd_rn(sum, scratch[w]);
-    p.parts[(size_t)row * p.nparts + part] = {top, sum, s_arg, 0};
+        for (int d = 16; d; d >>= 1) sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, d));
+        if (lane == 0) p.parts[at.item] = {seen.top, sum, seen.arg, 0};
+        seen = See();
+    };
+    // two sets of registers take turns
+    Place<F32> a, b;
+    uint4 x[See::kVecs], y[See::kVecs];
+    a.find(p, (long long)blockIdx.x * (kRowThreads / 32) + threadIdx.x / 32, step, items, pieces);
+    if (a.item >= 0) load(x, a);
+    while (a.item >= 0) {
+        b = a;
+        b.advance(p, step, items, pieces);
+        if (b.item >= 0) load(y, b);
+        take(x, a, b);
+        if (b.item < 0) break;
+        a = b;
+        a.advance(p, step, items, pieces);
+        if (a.item >= 0) load(x, a);
+        take(y, b, a);
+    }
 }
 
-// p or q of token v in a row, 0 where it is no token or the row has none.
-template <bool F32>
-__device__ __forceinline__ float prob(const VerifyParams &p, const void *row, float top, float sum, int v, float inv)
+// p or q of a logit (-inf: no token) in a row, 0 where the row has none.
+__device__ __forceinline__ float prob(float l, float top, float sum, float inv)
 {
-    if (v < 0 || v >= p.V || !(top > -INFINITY)) return 0.0f;
-    return __fdiv_rn(expf(__fmul_rn(__fsub_rn(logit<F32>(row, v), top), inv)), sum);
+    if (!(l > -INFINITY)) return 0.0f;
+    return __fdiv_rn(expf(__fmul_rn(__fsub_rn(l, top), inv)), sum);
 }
 
 // The block's best (ratio, token), in all threads.
@@ -311,45 +421,44 @@ __device__ __forceinline__ void block_best(float &v, int &i, float *sv, int *si)
 }
 
 template <bool F32>
-__global__ void __launch_bounds__(kVerifyThreads) verify_emit(const VerifyParams p)
+__global__ void __launch_bounds__(kVerifyThreads, 2) verify_emit(const VerifyParams p)
 {
     __shared__ float s_max[kMaxRows], s_sum[kMaxRows], sv[kVerifyWarps];
     __shared__ int s_arg[kMaxRows], s_ok[QMV_MAX_DRAFT + 1], si[kVerifyWarps], s_last;
-    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, b = blockIdx.x / p.races, race = blockIdx.x - b * p.races;
+    const int tid = threadIdx.x, b = blockIdx.x / p.races, race = blockIdx.x - b * p.races;
     // (none of these is written by the first kernel)
     const Mode m = mode_of(p, b);
     int drafted = -1;
-    float u = 0.0f;
+    float u = 0.0f, lt = -INFINITY, ld = -INFINITY;
     if (tid < m.len) {
         drafted = __ldg(p.draft_tokens + size_t(b) * p.S + tid);
         u = __ldg(p.uniform + size_t(b) * p.S + tid);
+        if (drafted >= 0 && drafted < p.V) {
+            lt = logit<F32>(row_of<F32>(p, b, tid), drafted);
+            if (p.draft) ld = logit<F32>(row_of<F32>(p, b, p.S + 1 + tid), drafted);
+        }
     }
     grid_dependency_wait();
     grid_launch_dependents();
     const Part *parts = p.parts + (size_t)b * p.rows * p.nparts;
-    for (int r = warp; r < p.rows; r += kVerifyWarps) {
-        if (r <= p.S ? r > m.len : m.greedy || r - p.S - 1 >= m.len) continue;
+    if (tid < p.rows && !(tid <= p.S ? tid > m.len : m.greedy || tid - p.S - 1 >= m.len)) {
+        // a row to a thread, its few parts in order
         float top = -INFINITY, sum = 0.0f;
         int arg = kNone;
-        for (int k = lane; k < p.nparts; k += 32) top = fmaxf(top, __ldcg(&parts[(size_t)r * p.nparts + k].max));
+        const Part *q = parts + (size_t)tid * p.nparts;
 #pragma unroll
-        for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-        for (int k = lane; k < p.nparts; k += 32) {
-            const int4 raw = __ldcg(reinterpret_cast<const int4 *>(parts + (size_t)r * p.nparts + k));
+        for (int k = 0; k < kMaxParts; ++k)
+            if (k < p.nparts) top = fmaxf(top, __ldcg(&q[k].max));
+#pragma unroll 4
+        for (int k = 0; k < p.nparts; ++k) {
+            const int4 raw = __ldcg(reinterpret_cast<const int4 *>(q + k));
             const float pm = __int_as_float(raw.x);
             if (pm > -INFINITY) sum = __fmaf_rn(__int_as_float(raw.y), expf(__fmul_rn(__fsub_rn(pm, top), m.inv)), sum);
             if (pm == top) arg = min(arg, raw.z);
         }
-#pragma unroll
-        for (int d = 16; d; d >>= 1) {
-            sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, d));
-            arg = min(arg, __shfl_xor_sync(0xffffffffu, arg, d));
-        }
-        if (lane == 0) {
-            s_max[r] = top;
-            s_sum[r] = sum;
-            s_arg[r] = arg;
-        }
+        s_max[tid] = top;
+        s_sum[tid] = sum;
+        s_arg[tid] = arg;
     }
     __syncthreads();
     if (tid <= m.len) {
@@ -358,8 +467,8 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_emit(const VerifyParams
             if (m.greedy) ok = s_max[tid] > -INFINITY && drafted == s_arg[tid];
             else {
                 const int d = p.S + 1 + tid;
-                const float q = p.draft ? prob<F32>(p, row_of<F32>(p, b, d), s_max[d], s_sum[d], drafted, m.inv) : 1.0f;
-                ok = __fmul_rn(u, q) < prob<F32>(p, row_of<F32>(p, b, tid), s_max[tid], s_sum[tid], drafted, m.inv);
+                const float q = p.draft ? prob(ld, s_max[d], s_sum[d], m.inv) : 1.0f;
+                ok = __fmul_rn(u, q) < prob(lt, s_max[tid], s_sum[tid], m.inv);
             }
         }
         s_ok[tid] = ok;
@@ -378,49 +487,81 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_emit(const VerifyParams
         const float dtop = drow ? s_max[p.S + 1 + n] : -INFINITY, dsum = drow ? s_sum[p.S + 1 + n] : 1.0f;
         const int cut = n < m.len && !p.draft ? __ldg(p.draft_tokens + size_t(b) * p.S + n) : -1;
         const float *noise = p.noise + (size_t)b * p.ld_noise;
-        // the share of this block, then (in a sequence's last block, where nothing
-        // had a positive remainder) all of p
-        const int lo = int((long long)p.V * race / p.races), hi = int((long long)p.V * (race + 1) / p.races);
-        // A token enters the race by its exact ratio, two divisions and two
-        // exponentials; whether it can beat the thread's best so far is seen
-        // without them, from approximations good to 1e-5 of p.
-        constexpr int U = 8;
-        const float c = __fmul_rn(m.inv, 1.4426950408889634f), itotal = __fdiv_rn(1.0f, total), idsum = dtop > -INFINITY ? __fdiv_rn(1.0f, dsum) : 0.0f;
-        const auto run = [&](int from, int to, bool rest) {
-            best = -1.0f;
-            token = kNone;
-            for (int v0 = from + tid; v0 < to; v0 += U * kVerifyThreads) {
-                float l[U], d[U], e[U];
+        // A token enters the race by its exact ratio: two exponentials and two
+        // divisions. Most are ruled out before, by approximations that are good to
+        // 1e-5 of p: the warp's best lower bound of a ratio so far against the
+        // token's upper bound. Eight tokens to a lane at a time.
+        const float c = __fmul_rn(m.inv, 1.4426950408889634f), itotal = __fdiv_rn(1.0f, total);
+        const float idsum = dtop > -INFINITY ? __fdiv_rn(1.0f, dsum) : 0.0f, dref = dtop > -INFINITY ? dtop : 0.0f;
+        const uint8_t *rowb = static_cast<const uint8_t *>(row), *drowb = static_cast<const uint8_t *>(drow);
+        const uint8_t *noiseb = reinterpret_cast<const uint8_t *>(noise);
+        const int roff = int(reinterpret_cast<uintptr_t>(rowb) & 15), doff = int(reinterpret_cast<uintptr_t>(drowb) & 15);
+        const int noff = int(reinterpret_cast<uintptr_t>(noiseb) & 15), lane = tid % 32;
+        float bound = 0.0f;
+        struct Eight {
+            float l[8], d[8], e[8];
+        };
+        const auto fetch = [&](Eight &t, int share, bool rest) {
+            const long long v0 = (long long)share * 256 + lane * 8;
+            load8<F32>(rowb, v0, p.V, roff, t.l);
+            load8<true>(noiseb, v0, p.V, noff, t.e);
+            if (rest && dtop > -INFINITY) load8<F32>(drowb, v0, p.V, doff, t.d);
+            else
 #pragma unroll
-                for (int k = 0; k < U; ++k) {
-                    const int v = v0 + k * kVerifyThreads;
-                    const bool in = v < to;
-                    l[k] = in ? logit<F32>(row, v) : -INFINITY;
-                    d[k] = in && rest && dtop > -INFINITY ? logit<F32>(drow, v) : -INFINITY;
-                    e[k] = in ? __ldcs(noise + v) : 1.0f;
-                }
+                for (int k = 0; k < 8; ++k) t.d[k] = -INFINITY;
+        };
+        const auto race8 = [&](Eight &t, int share, bool rest) {
+            const int v0 = share * 256 + lane * 8;
+            if (rest && (cut & ~7) == v0 && cut >= 0)  // the refused token, its draft being certain, has nothing left
 #pragma unroll
-                for (int k = 0; k < U; ++k) {
-                    const int v = v0 + k * kVerifyThreads;
-                    const float pa = __fmul_rn(ex2(__fmul_rn(__fsub_rn(l[k], top), c)), itotal);
-                    const float qa = d[k] > -INFINITY ? __fmul_rn(ex2(__fmul_rn(__fsub_rn(d[k], dtop), c)), idsum) : 0.0f;
-                    const float hope = __fmaf_rn(1e-5f, pa, __fsub_rn(pa, qa));
-                    if (!(hope > 0.0f) || hope < __fmul_rn(0.9999f, __fmul_rn(best, e[k])) || v >= to) continue;
-                    float w = __fdiv_rn(expf(__fmul_rn(__fsub_rn(l[k], top), m.inv)), total);
-                    if (d[k] > -INFINITY) w = __fsub_rn(w, __fdiv_rn(expf(__fmul_rn(__fsub_rn(d[k], dtop), m.inv)), dsum));
-                    if (rest && v == cut) w = 0.0f;
-                    if (w > 0.0f) {
-                        const float ratio = __fdiv_rn(w, fmaxf(e[k], FLT_MIN));
-                        if (better(ratio, v, best, token)) {
-                            best = ratio;
-                            token = v;
-                        }
+                for (int k = 0; k < 8; ++k)
+                    if (v0 + k == cut) t.l[k] = -INFINITY;
+            float upper[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const float pa = __fmul_rn(ex2(__fmul_rn(__fsub_rn(t.l[k], top), c)), itotal);
+                const float qa = __fmul_rn(ex2(__fmul_rn(__fsub_rn(t.d[k], dref), c)), idsum);
+                const float w = __fsub_rn(pa, qa);
+                t.e[k] = fmaxf(t.e[k], FLT_MIN);
+                // (a reciprocal of more than 2^126 comes out as 0)
+                const float ea = fminf(t.e[k], 8e37f);
+                float r;
+                asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(ea));
+                upper[k] = __fmul_rn(__fmaf_rn(1e-5f, pa, w), __fmul_rn(r, 1.0001f));
+                const float lower = __fmul_rn(__fmaf_rn(-1e-5f, pa, w), __fmul_rn(r, 0.9999f));
+                if (t.e[k] == ea) bound = fmaxf(bound, lower);
+            }
+#pragma unroll
+            for (int d = 16; d; d >>= 1) bound = fmaxf(bound, __shfl_xor_sync(0xffffffffu, bound, d));
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                if (!(upper[k] > 0.0f) || upper[k] < bound) continue;
+                float w = __fdiv_rn(expf(__fmul_rn(__fsub_rn(t.l[k], top), m.inv)), total);
+                if (t.d[k] > -INFINITY) w = __fsub_rn(w, __fdiv_rn(expf(__fmul_rn(__fsub_rn(t.d[k], dtop), m.inv)), dsum));
+                if (w > 0.0f) {
+                    const float ratio = __fdiv_rn(w, t.e[k]);
+                    if (better(ratio, v0 + k, best, token)) {
+                        best = ratio;
+                        token = v0 + k;
                     }
                 }
             }
-            block_best(best, token, sv, si);
         };
-        run(lo, hi, true);
+        const int shares = (p.V + 255) / 256;
+        const auto run = [&](int from, int step, bool rest) {
+            // two sets of registers take turns
+            Eight t, u;
+            if (from < shares) fetch(t, from, rest);
+            for (int share = from; share < shares; share += 2 * step) {
+                if (share + step < shares) fetch(u, share + step, rest);
+                race8(t, share, rest);
+                if (share + step >= shares) break;
+                if (share + 2 * step < shares) fetch(t, share + 2 * step, rest);
+                race8(u, share + step, rest);
+            }
+        };
+        run(race * kVerifyWarps + tid / 32, p.races * kVerifyWarps, true);
+        block_best(best, token, sv, si);
         if (p.races > 1) {
             if (tid == 0) {
                 __stcg(reinterpret_cast<float2 *>(p.winners + (size_t)b * p.races + race), make_float2(best, __int_as_float(token)));
@@ -441,7 +582,13 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_emit(const VerifyParams
             }
             block_best(best, token, sv, si);
         }
-        if (token == kNone) run(0, p.V, false);
+        if (token == kNone) {
+            // p has nothing that q has not: p itself
+            bound = 0.0f;
+            best = -1.0f;
+            run(tid / 32, kVerifyWarps, false);
+            block_best(best, token, sv, si);
+        }
     }
     if ((m.greedy || none) && race != 0) return;
     for (int i = tid; i <= p.S; i += kVerifyThreads) {
@@ -456,43 +603,43 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_emit(const VerifyParams
     if (tid == 0) p.accepted[b] = n;
 }
 
-// Vectors of 16 bytes to a thread of verify_rows, and parts of a row, as large as
-// still gives the SMs several blocks each: 2 for small calls (3 x 32000: 14 blocks
-// would be one part each), 8 otherwise.
+// Parts of a row: at least a piece each. Blocks of the race: at most two for each
+// of 152 SMs (one wave), each at least kRace tokens (every block joins the parts of
+// its sequence's rows for itself: with 4096 blocks for 64 x 131072 the race took
+// 85 us, with 1216 50).
 struct Split {
-    int nv, nparts, races;
+    int nparts, races;
 };
 
-Split split(int B, int S, int V)
+Split split(int B, int V, bool f32)
 {
     Split s;
-    const long long all = (long long)B * (2 * S + 1) * V;
-    s.nv = all < (4ll << 20) ? 2 : 8;
-    // for the narrower type's vectors; the wider type takes twice as many
-    s.nparts = ((V + 3) / 4 + kVerifyThreads * s.nv - 1) / (kVerifyThreads * s.nv);
-    // blocks of the race: about 4096 tokens each, fewer where sequences fill the GPU
-    s.races = (V + 4095) / 4096;
-    const int most = B >= 304 ? 1 : (1216 + B - 1) / B;
-    if (s.races > most) s.races = most;
+    const int elems = f32 ? Seen<true>::kElems : Seen<false>::kElems;
+    s.nparts = (V + elems - 1) / elems;
+    if (s.nparts > kMaxParts) s.nparts = kMaxParts;
+    s.races = (V + kRace - 1) / kRace;
+    const int blocks = B < 304 ? 304 / B : 1;
+    if (s.races > blocks) s.races = blocks;
     return s;
 }
 
 size_t up256(size_t b) { return (b + 255) & ~size_t(255); }
 
 template <bool F32>
-cudaError_t launch_verify(const VerifyParams &p, int nv, cudaStream_t stream)
+cudaError_t launch_verify(const VerifyParams &p, int sms, cudaStream_t stream)
 {
-    static std::atomic<int> configured[3][64] = {};
+    static std::atomic<int> configured[2][64] = {};
     Launch l;
-    l.grid = dim3(unsigned((long long)p.B * p.rows * p.nparts));
-    l.threads = kVerifyThreads;
+    const int blocks = (p.B * p.rows * p.nparts + kRowThreads / 32 - 1) / (kRowThreads / 32);
+    l.grid = dim3(blocks < kRowBlocks * sms ? blocks : kRowBlocks * sms);
+    l.threads = kRowThreads;
     l.smem = 0;
     l.pdl = true;
-    const cudaError_t e = nv == 2 ? launch_one(verify_rows<F32, 2>, configured[0], l, stream, p)
-                                  : launch_one(verify_rows<F32, 8>, configured[1], l, stream, p);
+    const cudaError_t e = launch_one(verify_rows<F32>, configured[0], l, stream, p);
     if (e != cudaSuccess) return e;
     l.grid = dim3(unsigned(p.B * p.races));
-    return launch_one(verify_emit<F32>, configured[2], l, stream, p);
+    l.threads = kVerifyThreads;
+    return launch_one(verify_emit<F32>, configured[1], l, stream, p);
 }
 
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
@@ -503,7 +650,7 @@ bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 extern "C" size_t qmv_verify_workspace_size(int B, int S, int V)
 {
     if (B < 1 || B > QMV_MAX_BATCH || S < 0 || S > QMV_MAX_DRAFT || V < 1 || V > (1 << 24)) return 0;
-    const qmv::Split s = qmv::split(B, S, V);
+    const qmv::Split s = qmv::split(B, V, true);  // the wider type has more parts
     return qmv::up256(size_t(B) * (2 * S + 1) * s.nparts * sizeof(qmv::Part)) +
            qmv::up256(size_t(B) * s.races * sizeof(qmv::Winner)) + qmv::up256(size_t(B) * 4);
 }
@@ -523,8 +670,6 @@ extern "C" qmv_status qmv_verify_run(const void *target, const void *draft, cons
     if (V < 1 || V > (1 << 24) || ld_target < V || ld_target > most || (draft && (ld_draft < V || ld_draft > most)) ||
         ld_noise < V || ld_noise > most)
         return QMV_ERR_SHAPE;
-    // blocks of the first kernel
-    if ((long long)B * (2 * S + 1) * split(B, S, V).nparts > 0x7fffffffll) return QMV_ERR_SHAPE;
     if (flags & ~QMV_VERIFY_F32_LOGITS) return QMV_ERR_FLAGS;
     const bool f32 = (flags & QMV_VERIFY_F32_LOGITS) != 0;
     if (!aligned(target, f32 ? 4 : 2) || !aligned(draft, f32 ? 4 : 2) || (workspace && !aligned(workspace, 16)))
@@ -540,16 +685,14 @@ extern "C" qmv_status qmv_verify_run(const void *target, const void *draft, cons
     st = scratch(dev, qmv_verify_workspace_size(B, S, V), workspace, workspace_bytes, &ws);
     if (st != QMV_OK) return st;
 
-    const Split sp = split(B, S, V);
+    const Split sp = split(B, V, f32);
     VerifyParams p{};
     p.target = target; p.draft = draft; p.draft_tokens = draft_tokens; p.draft_len = draft_len;
     p.temperature = temperature; p.uniform = uniform; p.noise = noise;
     p.tokens = tokens; p.accepted = accepted; p.logprob = logprob;
     p.B = B; p.S = S; p.V = V;
     p.rows = draft ? 2 * S + 1 : S + 1;
-    // a part is kVerifyThreads * nv vectors of 16 bytes, the last of a row short
-    const int ev = f32 ? 4 : 8;
-    p.nparts = ((V + ev - 1) / ev + kVerifyThreads * sp.nv - 1) / (kVerifyThreads * sp.nv);
+    p.nparts = sp.nparts;
     p.races = sp.races;
     p.ld_target = ld_target; p.ld_draft = ld_draft; p.ld_noise = ld_noise;
     uint8_t *at = static_cast<uint8_t *>(ws);
@@ -557,6 +700,6 @@ extern "C" qmv_status qmv_verify_run(const void *target, const void *draft, cons
     p.winners = reinterpret_cast<Winner *>(at); at += up256(size_t(B) * sp.races * sizeof(Winner));
     p.finished = reinterpret_cast<unsigned *>(at);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const cudaError_t e = f32 ? launch_verify<true>(p, sp.nv, s) : launch_verify<false>(p, sp.nv, s);
+    const cudaError_t e = f32 ? launch_verify<true>(p, dev.sms, s) : launch_verify<false>(p, dev.sms, s);
     return e == cudaSuccess ? QMV_OK : record_cuda_failure("verify kernel launch", e);
 }

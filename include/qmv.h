@@ -405,7 +405,7 @@ QMV_API qmv_status qmv_moe_run(const uint16_t *x, const uint16_t *router, const 
  *                (at temperature 1 where argmax is taken), 0 where tokens holds -1.
  *  B             1 .. QMV_MAX_BATCH.  S 0 .. QMV_MAX_DRAFT (with S = 0 the pointers
  *                draft, draft_tokens and uniform are not used).  V 1 .. 2^24.
- *  ld_*          elements from row to row, at least V. B x (2 S + 1) x V at most 2^43.
+ *  ld_*          elements from row to row, at least V.
  *  flags         QMV_VERIFY_F32_LOGITS.
  *
  * A logit of -inf or NaN is never emitted or accepted; +inf counts as the type's
