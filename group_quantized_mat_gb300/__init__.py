@@ -60,6 +60,8 @@ _lib = None
 def load(path: str | None = None) -> ctypes.CDLL:
     """Load libqmv.so (built by ``python -m group_quantized_mat_gb300.build``)."""
     global _lib
+    if path is None and _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None and path is None:
             return _lib
@@ -116,17 +118,20 @@ def load(path: str | None = None) -> ctypes.CDLL:
 def _ptr(a) -> int | None:
     if a is None:
         return None
-    if isinstance(a, int):
-        return a
-    if isinstance(a, np.ndarray):
-        return a.ctypes.data
-    return int(a.data_ptr())  # torch.Tensor
+    try:
+        return a.data_ptr()  # torch.Tensor
+    except AttributeError:
+        return a.ctypes.data if isinstance(a, np.ndarray) else int(a)
 
 
 def _stream(s) -> int | None:
     if s is None:
         import torch
-        return int(torch.cuda.current_stream().cuda_stream)
+        try:
+            # the handle that torch.cuda.current_stream() wraps, in a tenth of its 3 us
+            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        except AttributeError:
+            return int(torch.cuda.current_stream().cuda_stream)
     if isinstance(s, int):
         return s
     return int(s.cuda_stream)
