@@ -526,16 +526,16 @@ qmv_status current_device(DeviceInfo *out)
 }
 
 qmv_status encode_rows(CUtensorMap *map, const void *w, long long row_bytes, long long rows, int box_elems,
-                       int box_rows, bool swizzle)
+                       int box_rows, bool swizzle, long long blocks, int box_blocks)
 {
     auto fn = encode_fn();
     int r = -1;
     if (fn) {
-        const cuuint64_t dims[2] = {cuuint64_t(row_bytes / 8), cuuint64_t(rows)};
-        const cuuint64_t strides[1] = {cuuint64_t(row_bytes)};
-        const cuuint32_t box[2] = {cuuint32_t(box_elems), cuuint32_t(box_rows)};
-        const cuuint32_t estr[2] = {1, 1};
-        r = int(fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT64, 2, const_cast<void *>(w), dims, strides, box, estr,
+        const cuuint64_t dims[3] = {cuuint64_t(row_bytes / 8), cuuint64_t(rows), cuuint64_t(blocks)};
+        const cuuint64_t strides[2] = {cuuint64_t(row_bytes), cuuint64_t(row_bytes) * cuuint64_t(rows)};
+        const cuuint32_t box[3] = {cuuint32_t(box_elems), cuuint32_t(box_rows), cuuint32_t(box_blocks)};
+        const cuuint32_t estr[3] = {1, 1, 1};
+        r = int(fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT64, blocks > 1 ? 3 : 2, const_cast<void *>(w), dims, strides, box, estr,
                    CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE));
     }

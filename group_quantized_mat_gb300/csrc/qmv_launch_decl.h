@@ -58,9 +58,10 @@ qmv_status check_weights(int M, int N, int K, int bits, int gs);
 qmv_status current_device(DeviceInfo *out);
 // A tensor map of a row-major array as a 2-D tensor [rows][row_bytes / 8] of
 // 8-byte elements, box `box_rows` x `box_elems`, `swizzle` for the 128-byte
-// swizzle; zeros outside the tensor.
+// swizzle; zeros outside the tensor. With several `blocks` of `rows` a 3-D tensor,
+// `box_blocks` of them to a box.
 qmv_status encode_rows(CUtensorMap *map, const void *w, long long row_bytes, long long rows, int box_elems,
-                       int box_rows, bool swizzle);
+                       int box_rows, bool swizzle, long long blocks = 1, int box_blocks = 1);
 qmv_status scratch(const DeviceInfo &d, size_t need, void *given, size_t given_bytes, void **out);
 
 // One launch for V = 1..16 vectors (qmv_mx.cu).

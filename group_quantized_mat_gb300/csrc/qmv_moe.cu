@@ -10,11 +10,11 @@
 //     lists the tokens of each; then it takes its share of two kinds of items:
 //       A. 64 rows of an expert's gate and the 64 of its up product, for up to NC
 //          of its tokens: activation, and h as operand bytes to the workspace;
-//       B. 128 rows of an expert's down product: sums to the workspace; the CTA
-//          that finishes a tile of rows last adds the experts' sums with the
-//          tokens' weights, in the order of their choices.
+//       B. 128 rows of an expert's down product, sums to the workspace.
 //     Between A and B all CTAs meet (one counter); the weights of the first B
-//     items are on their way to the ring meanwhile.
+//     items are on their way to the ring meanwhile. After B they meet again, and
+//     share the sums over each token's choices, in their order. (A ticket for each
+//     tile of rows, the last CTA adding its sums, cost 2 us an item.)
 //
 // An expert with no token costs nothing, one with several reads its weights once
 // for up to NC of them. What bounds it is the weights' stream while there are
@@ -56,7 +56,7 @@ struct MoeParams {
     uint8_t *hcells;    // [entry][subs_b][cell_bytes(NC, 4)]
     uint8_t *hmeta;     // [entry][subs_b][meta_bytes(NC)]
     float *partials;    // [pair][K]
-    unsigned *counters; // [0]: CTAs done with A; then one for each tile of rows of B
+    unsigned *counters; // CTAs done with A, and with B
     unsigned *err;
     int M, K, I, E, k, gs, f32_out, gelu, softmax_all;
     int Sa, NSa, Ga, Sb, NSb, Gb;  // subgroups, slots and groups of a row of A and of B
@@ -73,7 +73,7 @@ __global__ void __launch_bounds__(kLogitThreads) moe_logits(const MoeParams p)
     grid_launch_dependents();
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     if (blockIdx.x == 0)
-        for (int i = tid; i < 1 + p.tiles_b; i += kLogitThreads) p.counters[i] = 0u;
+        for (int i = tid; i < 2; i += kLogitThreads) p.counters[i] = 0u;
     if (int(blockIdx.x) < p.stage_blocks) {
         // eight threads for each (token, subgroup)
         const int subs = p.NSa * tile::slot_subs(BITS);
@@ -155,51 +155,66 @@ __host__ __device__ inline MoeLayout moe_layout(const MoeParams &p)
     return l;
 }
 
-// The expert choice of token t by one warp: `l` is scratch for the E logits.
-__device__ __forceinline__ void choose(const MoeParams &p, int t, float *l, float *w, uint16_t *ids, uint32_t *mask, int lane)
+// A logit as a number that orders as it does (-0 as +0, nothing chosen as 0).
+__device__ __forceinline__ uint32_t order_of(float v)
 {
-    for (int e = lane; e < p.E; e += 32) l[e] = __ldcg(p.logits + size_t(t) * p.E + e);
-    __syncwarp();
+    const uint32_t u = __float_as_uint(__fadd_rn(v, 0.0f));
+    return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+
+// The expert choice of token t by one warp, whose lane holds every 32nd logit:
+// N of them in registers, or for more than 32 N experts in shared memory (l).
+template <int N>
+__device__ __forceinline__ void choose(const MoeParams &p, int t, uint32_t *l, float *w, uint16_t *ids, uint32_t *mask, int lane)
+{
+    uint32_t key[N];
+    const float *logits = p.logits + size_t(t) * p.E;
+    const bool many = p.E > 32 * N;
+#pragma unroll
+    for (int i = 0; i < N; ++i) key[i] = !many && i * 32 + lane < p.E ? order_of(__ldcg(logits + i * 32 + lane)) : 0u;
+    if (many)
+        for (int e = lane; e < p.E; e += 32) l[e] = order_of(__ldcg(logits + e));
     float top = 0.0f, sum = 0.0f, mine = 0.0f;
     for (int j = 0; j < p.k; ++j) {
-        float best = -INFINITY;
-        int arg = 0x7fffffff;
-        for (int e = lane; e < p.E; e += 32) {
-            const float v = l[e];  // NaN: already chosen
-            if (v > best || (v == best && e < arg)) {
-                best = v;
-                arg = e;
-            }
-        }
+        uint32_t best = 0;
 #pragma unroll
-        for (int d = 16; d; d >>= 1) {
-            const float v = __shfl_xor_sync(0xffffffffu, best, d);
-            const int a = __shfl_xor_sync(0xffffffffu, arg, d);
-            if (v > best || (v == best && a < arg)) {
-                best = v;
-                arg = a;
-            }
-        }
+        for (int i = 0; i < N; ++i) best = max(best, key[i]);
+        if (many)
+            for (int e = lane; e < p.E; e += 32) best = max(best, l[e]);
+        best = __reduce_max_sync(0xffffffffu, best);
+        uint32_t arg = 0xffffffffu;
+#pragma unroll
+        for (int i = N - 1; i >= 0; --i)
+            if (key[i] == best) arg = i * 32 + lane;
+        if (many)
+            for (int e = lane; e < p.E; e += 32)
+                if (l[e] == best) {
+                    arg = e;
+                    break;
+                }
+        arg = __reduce_min_sync(0xffffffffu, arg);
+        const float v = __uint_as_float(best & 0x80000000u ? best & 0x7fffffffu : ~best);
         if (j == 0) {
-            top = best;
+            top = v;
             if (p.softmax_all) {
                 // over all experts, each lane's in order, then across the lanes
-                for (int e = lane; e < p.E; e += 32) sum = __fadd_rn(sum, top > -INFINITY ? expf(__fsub_rn(l[e], top)) : 1.0f);
+                for (int e = lane; e < p.E; e += 32) sum = __fadd_rn(sum, top > -INFINITY ? expf(__fsub_rn(__ldcg(logits + e), top)) : 1.0f);
 #pragma unroll
                 for (int d = 16; d; d >>= 1) sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, d));
             }
         }
-        __syncwarp();
         // (all logits -inf: equal weights)
-        const float mass = top > -INFINITY ? expf(__fsub_rn(best, top)) : 1.0f;
+        const float mass = top > -INFINITY ? expf(__fsub_rn(v, top)) : 1.0f;
         if (lane == j) mine = mass;
         if (!p.softmax_all) sum = __fadd_rn(sum, mass);
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (!many && arg == uint32_t(i * 32 + lane)) key[i] = 0u;
+        if (many && lane == int(arg % 32)) l[arg] = 0u;
         if (lane == 0) {
-            l[arg] = __uint_as_float(0x7fc00000u);
             ids[t * p.k + j] = uint16_t(arg);
             atomicOr(mask + arg * p.words + t / 32, 1u << (t & 31));
         }
-        __syncwarp();
     }
     if (lane < p.k) w[t * p.k + lane] = __fdiv_rn(mine, sum);
 }
@@ -221,7 +236,7 @@ __global__ void __launch_bounds__(tile::kThreads, 1)
 {
     using namespace tile;
     extern __shared__ __align__(1024) uint8_t smem[];
-    __shared__ int s_abort, s_last, s_entries;
+    __shared__ int s_abort, s_entries;
     __shared__ uint32_t s_tmem;
     constexpr int SUBS = slot_subs(BITS), CA = cell_bytes(NC, 2), CB = cell_bytes(NC, kTermsH), MB = meta_bytes(NC);
     const MoeLayout L = moe_layout<BITS, NC>(p);
@@ -258,7 +273,7 @@ __global__ void __launch_bounds__(tile::kThreads, 1)
 
     // ------------------------------------------------------------- routing
     for (int t = warp; t < p.M; t += kThreads / 32)
-        choose(p, t, reinterpret_cast<float *>(smem) + warp * p.E, s_w, s_ids, s_mask, lane);
+        choose<4>(p, t, reinterpret_cast<uint32_t *>(smem) + warp * p.E, s_w, s_ids, s_mask, lane);
     __syncthreads();
     if (warp == 0) {
         // each lane a run of experts: tokens and entries before it
@@ -325,82 +340,115 @@ __global__ void __launch_bounds__(tile::kThreads, 1)
         return it;
     };
 
+    // Waits until all CTAs are done with a part: bounded like every wait.
+    auto meet = [&](const unsigned *counter) {
+        for (int i = 0; i < (1 << 21); ++i) {
+            unsigned v;
+            asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(counter) : "memory");
+            if (v >= unsigned(grid)) return true;
+            if ((i & 63) == 63 && *wait.abort) return false;
+        }
+        atomicOr(p.err, 1u);
+        *wait.abort = 1;
+        return false;
+    };
+
     if (warp == kThreads / 32 - 1) {
         // ---------------------------------------------------------- producer
-        int it = 0, chunk = 0;
+        int chunk = 0;
+        Turn turn;
         bool ok = true;
-        // scales and biases of groups of an item's two halves
-        auto fetch = [&](const Affines &a, const uint16_t *sc, const uint16_t *bi, const CUtensorMap *sm, const CUtensorMap *bm,
-                         long long r0, long long r1, bool two, long long all, int G, int i) {
-            const int buf = chunk & 1, turn = chunk >> 1;
-            ok = __all_sync(0xffffffffu, turn == 0 || wait(sempty0 + 8 * buf, (turn - 1) & 1));
+        // scales and biases of an item's rows from slot i on: of A the rows r0 of
+        // gate and up, of B 128 rows from r0 (`rows` of them the expert's)
+        auto fetch = [&](bool part_a, const Affines &a, const uint16_t *sc, const uint16_t *bi, const CUtensorMap *sm,
+                         const CUtensorMap *bm, int e, int row, int rows, int G, int i) {
+            const int buf = chunk & 1, round = chunk >> 1;
+            ok = __all_sync(0xffffffffu, round == 0 || wait(sempty0 + 8 * buf, (round - 1) & 1));
             if (!ok) return;
             const int g0 = i * SUBS * 64 / GS, groups = min(kChunkGroups, G - g0);  // (of kSbRows)
             const int off = L.sb + buf * 2 * p.sb_block;
+            const uint32_t bar = sfull0 + 8 * buf;
+            ++chunk;
+            if (a.mode == kSbBoxes) {
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(bar, uint32_t(2 * kTileRows * a.pitch));
+                    if (part_a) {
+                        tma_load_3d(base + off, sm, g0 / 8 * 2, row, 2 * e, bar);
+                        tma_load_3d(base + off + p.sb_block, bm, g0 / 8 * 2, row, 2 * e, bar);
+                    } else {
+                        tma_load_2d(base + off, sm, g0 / 8 * 2, e * p.K + row, bar);
+                        tma_load_2d(base + off + p.sb_block, bm, g0 / 8 * 2, e * p.K + row, bar);
+                    }
+                } else {
+                    mbar_arrive(bar);
+                }
+                mbar_arrive(bar);
+                return;
+            }
             Affines b = a;
             b.block = p.sb_block;
-            b.fetch(base + off, smem + off, sc, bi, sm, bm, r0, kHalf, all, G, g0, groups, sfull0 + 8 * buf, lane);
-            if (two) b.fetch(base + off + kHalf * a.pitch, smem + off + kHalf * a.pitch, sc, bi, sm, bm, r1, kHalf, all, G, g0, groups, sfull0 + 8 * buf, lane);
-            else mbar_arrive(sfull0 + 8 * buf);
-            ++chunk;
+            const long long r0 = part_a ? (long long)e * 2 * p.I + row : (long long)e * p.K + row, r1 = r0 + (part_a ? p.I : kHalf);
+            const long long all = part_a ? (long long)p.E * 2 * p.I : (long long)p.E * p.K;
+            b.fetch(base + off, smem + off, sc, bi, sm, bm, r0, kHalf, all, G, g0, groups, bar, lane);
+            if (rows > kHalf) b.fetch(base + off + kHalf * a.pitch, smem + off + kHalf * a.pitch, sc, bi, sm, bm, r1, kHalf, all, G, g0, groups, bar, lane);
+            else mbar_arrive(bar);
         };
+        // the lane's 16 bytes of each token's: subgroup, term and piece
+        const int gsub = lane >> 3, gh = lane >> 2 & 1, gpc = lane & 3;
         for (int q = blockIdx.x; q < na && ok; q += grid) {
             const Item im = item_of(q, p.tiles_a);
-            const long long r0 = (long long)im.e * 2 * p.I + im.tl * kHalf, r1 = r0 + p.I;
-            for (int i = 0; i < p.NSa && ok; ++i, ++it) {
-                if (i % p.cha == 0) fetch(p.sba, p.gu_s, p.gu_b, &sa, &ba, r0, r1, true, (long long)p.E * 2 * p.I, p.Ga, i);
+            for (int i = 0; i < p.NSa && ok; ++i) {
+                if (i % p.cha == 0) fetch(true, p.sba, p.gu_s, p.gu_b, &sa, &ba, im.e, im.tl * kHalf, kTileRows, p.Ga, i);
                 if (!ok) break;
-                const int s = it % p.slots, lap = it / p.slots;
-                ok = __all_sync(0xffffffffu, lap == 0 || wait(empty0 + 8 * s, (lap - 1) & 1));
+                ok = __all_sync(0xffffffffu, turn.lap == 0 || wait(empty0 + 8 * turn.slot, (turn.lap - 1) & 1));
                 if (!ok) break;
-                const uint32_t full = full0 + 8 * s, dst = base + s * L.slot;
+                const uint32_t full = full0 + 8 * turn.slot, dst = base + turn.slot * L.slot;
                 if (lane == 0) {
                     mbar_arrive_expect_tx(full, kTileRows * kSlotBytes);
-                    tma_load_2d(dst, &wa, i * (kSlotBytes / 8), int(r0), full);
-                    tma_load_2d(dst + kHalf * kSlotBytes, &wa, i * (kSlotBytes / 8), int(r1), full);
+                    tma_load_3d(dst, &wa, i * (kSlotBytes / 8), im.tl * kHalf, 2 * im.e, full);
                 }
-                __syncwarp();
-                // the tokens' operand bytes, 16 at a time, and their sums
-                for (int c = lane; c < im.count * SUBS * 8; c += 32) {
-                    const int j = c / (SUBS * 8), sub = c / 8 % SUBS, h = c / 4 & 1, pc = c & 3;
-                    const uint8_t *src = p.rows + (size_t(s_tok[im.pair + j]) * p.NSa * SUBS + i * SUBS + sub) * 128 + h * 64 + pc * 16;
-                    const uint32_t d = dst + L.cells + sub * CA + operand_offset(operand_index(j, h), pc);
-                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src) : "memory");
+                // the tokens' operand bytes, 512 a time, and their sums
+                const uint8_t *src = p.rows + (size_t(i) * SUBS * 128 + lane * 16);
+                for (int j = 0; j < im.count; ++j) {
+                    const uint8_t *from = src + size_t(s_tok[im.pair + j]) * p.NSa * (SUBS * 128);
+                    const uint32_t d = dst + L.cells + gsub * CA + operand_offset(operand_index(j, gh), gpc);
+#pragma unroll
+                    for (int s = 0; s < SUBS / 4; ++s)
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d + s * 4 * CA), "l"(from + s * 512) : "memory");
                 }
-                for (int c = lane; c < im.count * SUBS * 2; c += 32) {
-                    const int j = c / (SUBS * 2), sub = c / 2 % SUBS, f = c & 1;
-                    const float *src = reinterpret_cast<const float *>(p.xmeta + size_t(s_tok[im.pair + j]) * p.NSa * SUBS + i * SUBS + sub) + f;
+                const int sub = lane / 2 % SUBS, f = lane & 1;
+                for (int j = lane / (2 * SUBS); j < im.count; j += 16 / SUBS) {
+                    const float *from = reinterpret_cast<const float *>(p.xmeta + (size_t(s_tok[im.pair + j]) * p.NSa + i) * SUBS + sub) + f;
                     const uint32_t d = dst + L.meta + sub * MB + (j >> 1) * 16 + (j & 1) * 4 + f * 8;
-                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(d), "l"(src) : "memory");
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(d), "l"(from) : "memory");
                 }
                 asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(full) : "memory");
+                turn.step(1, p.slots);
             }
         }
         // B: weights of the first slots before the meeting (as many as are free and
         // as the two buffers of scales serve), h after it
         int ahead = 0;
+        const Turn turn0 = turn;
         auto b_slots = [&](int from, bool weights, bool cells, int most) {
             int n = 0;
+            Turn at = turn0;
             for (int q = blockIdx.x; q < nb && ok; q += grid) {
                 const Item im = item_of(q, p.tiles_b);
-                const long long r0 = (long long)im.e * p.K + im.tl * kTileRows, r1 = r0 + kHalf;
-                const bool two = im.tl * kTileRows + kHalf < p.K;
-                for (int i = 0; i < p.NSb && ok; ++i, ++n) {
+                const int row = im.tl * kTileRows;
+                for (int i = 0; i < p.NSb && ok; ++i, ++n, at.step(1, p.slots)) {
                     if (n >= most) return n;
                     if (n < from) continue;
-                    const int s = (it + n) % p.slots, lap = (it + n) / p.slots;
-                    const uint32_t full = full0 + 8 * s, dst = base + s * L.slot;
+                    const uint32_t full = full0 + 8 * at.slot, dst = base + at.slot * L.slot;
                     if (weights) {
-                        if (i % p.chb == 0) fetch(p.sbb, p.dn_s, p.dn_b, &sbm, &bb, r0, r1, two, (long long)p.E * p.K, p.Gb, i);
+                        if (i % p.chb == 0) fetch(false, p.sbb, p.dn_s, p.dn_b, &sbm, &bb, im.e, row, min(p.K - row, kTileRows), p.Gb, i);
                         if (!ok) break;
-                        ok = __all_sync(0xffffffffu, lap == 0 || wait(empty0 + 8 * s, (lap - 1) & 1));
+                        ok = __all_sync(0xffffffffu, at.lap == 0 || wait(empty0 + 8 * at.slot, (at.lap - 1) & 1));
                         if (!ok) break;
                         if (lane == 0) {
-                            mbar_arrive_expect_tx(full, (two ? 2 : 1) * kHalf * kSlotBytes + SUBS * (CB + MB));
-                            tma_load_2d(dst, &wb, i * (kSlotBytes / 8), int(r0), full);
-                            if (two) tma_load_2d(dst + kHalf * kSlotBytes, &wb, i * (kSlotBytes / 8), int(r1), full);
+                            mbar_arrive_expect_tx(full, kTileRows * kSlotBytes + SUBS * (CB + MB));
+                            tma_load_2d(dst, &wb, i * (kSlotBytes / 8), im.e * p.K + row, full);
                         }
-                        __syncwarp();
                         mbar_arrive(full);
                     }
                     if (cells && lane == 0) {
@@ -414,19 +462,7 @@ __global__ void __launch_bounds__(tile::kThreads, 1)
         };
         if (ok) ahead = b_slots(0, true, false, min(p.slots, p.chb >= p.NSb ? 2 * p.NSb : min(2 * p.chb, p.NSb)));
         if (ok && lane == 0) {
-            // the meeting: bounded like every wait
-            bool met = false;
-            for (int i = 0; i < (1 << 21) && !met; ++i) {
-                unsigned v;
-                asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p.counters) : "memory");
-                met = v >= unsigned(grid);
-                if (!met && (i & 63) == 63 && *wait.abort) break;
-            }
-            if (!met) {
-                atomicOr(p.err, 1u);
-                *wait.abort = 1;
-                ok = false;
-            }
+            ok = meet(p.counters);
             asm volatile("fence.proxy.async;" ::: "memory");
         }
         ok = __all_sync(0xffffffffu, ok);
@@ -444,23 +480,31 @@ __global__ void __launch_bounds__(tile::kThreads, 1)
         // ------------------------------------------------------ tensor warps
         const int group = warp - kWorkers;
         if (lane == 0) {
-            int it = 0;
+            // turn: of the item's first slot
+            Turn turn;
             Pipe pipe = Pipe::make<NC, 2>(tm, 0, stored0, ready0, group);
-            for (int q = blockIdx.x; q < na; q += grid, it += p.NSa)
-                for (int i = group; i < p.NSa; i += kGroups)
-                    multiply_slot<BITS, NC, 2, true>(wait, pipe, base + (it + i) % p.slots * L.slot + L.cells);
+            for (int q = blockIdx.x; q < na; q += grid, turn.step(p.NSa, p.slots)) {
+                Turn at = turn;
+                at.step(group, p.slots);
+                for (int i = group; i < p.NSa; i += kGroups, at.step(kGroups, p.slots))
+                    multiply_slot<BITS, NC, 2, true>(wait, pipe, base + at.slot * L.slot + L.cells);
+            }
             Pipe pb = Pipe::make<NC, kTermsH>(tm, 0, stored0, ready0, group);
             pb.steps = pipe.steps;
-            for (int q = blockIdx.x; q < nb; q += grid, it += p.NSb)
-                for (int i = group; i < p.NSb; i += kGroups)
-                    multiply_slot<BITS, NC, kTermsH>(wait, pb, base + (it + i) % p.slots * L.slot + L.cells);
+            for (int q = blockIdx.x; q < nb; q += grid, turn.step(p.NSb, p.slots)) {
+                Turn at = turn;
+                at.step(group, p.slots);
+                for (int i = group; i < p.NSb; i += kGroups, at.step(kGroups, p.slots))
+                    multiply_slot<BITS, NC, kTermsH>(wait, pb, base + at.slot * L.slot + L.cells);
+            }
         }
     } else {
         // ----------------------------------------------------------- workers
         const int group = warp / 4, row = (warp & 3) * 32 + lane;
         const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
         const uint32_t wrow = base + row * kSlotBytes + ((row & 7) << 4);
-        int it = 0, chunk = 0;
+        Turn turn;  // of the item's first slot
+        int chunk = 0;
         uint32_t held = 0;  // the barrier of the slot whose last steps are still to be taken
         // all slots of an item's rows into acc
         auto run = [&](auto &acc, Pipe &pipe, const Affines &a, int ch, int NS, int G, long long grow) {
@@ -469,14 +513,16 @@ __global__ void __launch_bounds__(tile::kThreads, 1)
             uint32_t last = 0;
             held = 0;
             acc.start();
+            Turn at = turn;
+            at.step(group, p.slots);
             for (int c0 = 0; c0 < NS; c0 += ch, ++chunk) {
                 const int buf = chunk & 1, c1 = min(c0 + ch, NS), g0 = c0 * SUBS * 64 / GS;
                 wait(sfull0 + 8 * buf, (chunk >> 1) & 1);
                 const uint32_t sb = base + L.sb + buf * 2 * p.sb_block + row * a.pitch + a.offset(grow, G, g0);
 #pragma unroll 1
-                for (int i = c0 + (group + kGroups - c0 % kGroups) % kGroups; i < c1; i += kGroups) {
-                    const int s = (it + i) % p.slots, lap = (it + i) / p.slots;
-                    wait(full0 + 8 * s, lap & 1);
+                for (int i = c0 + (group + kGroups - c0 % kGroups) % kGroups; i < c1; i += kGroups, at.step(kGroups, p.slots)) {
+                    const int s = at.slot;
+                    wait(full0 + 8 * s, at.lap & 1);
                     Affine<BITS, GS> aff;
                     constexpr int GP = Affine<BITS, GS>::kGroupsPerSlot;
                     aff.read(sb + (i - c0) * GP * 2, p.sb_block, align, G - i * GP);
@@ -495,11 +541,12 @@ __global__ void __launch_bounds__(tile::kThreads, 1)
             acc.finish(wait, pipe, last);
             __syncwarp();
             if (lane == 0 && held) mbar_arrive(held);
+            turn.step(NS, p.slots);
         };
 
         Pipe pipe = Pipe::make<NC, 2>(tm, lanes, stored0, ready0, group);
         float *xs = reinterpret_cast<float *>(smem + L.xs), *red = xs + NC * kHalf + group * 4;
-        for (int q = blockIdx.x; q < na; q += grid, it += p.NSa) {
+        for (int q = blockIdx.x; q < na; q += grid) {
             const Item im = item_of(q, p.tiles_a);
             Row<BITS, GS, NC, 2> acc;
             run(acc, pipe, p.sba, p.cha, p.NSa, p.Ga, (long long)im.e * 2 * p.I + (row < kHalf ? 0 : p.I - kHalf) + im.tl * kHalf + row);
@@ -568,7 +615,7 @@ __global__ void __launch_bounds__(tile::kThreads, 1)
 
         Pipe pb = Pipe::make<NC, kTermsH>(tm, lanes, stored0, ready0, group);
         pb.steps = pipe.steps;
-        for (int q = blockIdx.x; q < nb; q += grid, it += p.NSb) {
+        for (int q = blockIdx.x; q < nb; q += grid) {
             const Item im = item_of(q, p.tiles_b);
             const int n = im.tl * kTileRows + row;
             Row<BITS, GS, NC, kTermsH> acc;
@@ -581,27 +628,41 @@ __global__ void __launch_bounds__(tile::kThreads, 1)
                 const int j = group + kGroups * i;
                 if (j < im.count && n < p.K) __stcg(p.partials + size_t(im.pair + j) * p.K + n, sums[i]);
             }
-            __threadfence();
-            named_sync(1, 32 * kWorkers);
-            if (tid == 0) s_last = atomicAdd(p.counters + 1 + im.tl, 1u) == unsigned(entries - 1);
-            named_sync(1, 32 * kWorkers);
-            if (!s_last) continue;
-            __threadfence();
-            if (n < p.K)
-                for (int t = group; t < p.M; t += kGroups) {
-                    float s = 0.0f;
-                    for (int j0 = 0; j0 < p.k; j0 += 4) {
-                        float v[4];
+        }
+        __threadfence();
+        named_sync(1, 32 * kWorkers);
+        if (tid == 0) {
+            asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(p.counters + 1) : "memory");
+            (void)meet(p.counters + 1);
+        }
+        named_sync(1, 32 * kWorkers);
+        __threadfence();
+        // y, four elements at a time (K is a multiple of 64)
+        const int quads = p.M * p.K / 4;
+        for (int i = blockIdx.x * 32 * kWorkers + tid; i < quads; i += grid * 32 * kWorkers) {
+            const int t = i / (p.K / 4), n = (i - t * (p.K / 4)) * 4;
+            float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            for (int j0 = 0; j0 < p.k; j0 += 4) {
+                float4 v[4];
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) v[j] = j0 + j < p.k ? __ldcg(p.partials + size_t(s_pos[t * p.k + j0 + j]) * p.K + n) : 0.0f;
+                for (int j = 0; j < 4; ++j)
+                    if (j0 + j < p.k) v[j] = __ldcg(reinterpret_cast<const float4 *>(p.partials + size_t(s_pos[t * p.k + j0 + j]) * p.K + n));
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            if (j0 + j < p.k) s = __fmaf_rn(s_w[t * p.k + j0 + j], v[j], s);
+                for (int j = 0; j < 4; ++j)
+                    if (j0 + j < p.k) {
+                        const float w = s_w[t * p.k + j0 + j];
+                        s.x = __fmaf_rn(w, v[j].x, s.x);
+                        s.y = __fmaf_rn(w, v[j].y, s.y);
+                        s.z = __fmaf_rn(w, v[j].z, s.z);
+                        s.w = __fmaf_rn(w, v[j].w, s.w);
                     }
-                    const size_t at = size_t(t) * p.K + n;
-                    if (p.f32_out) static_cast<float *>(p.y)[at] = s;
-                    else static_cast<__nv_bfloat16 *>(p.y)[at] = __float2bfloat16_rn(s);
-                }
+            }
+            const size_t at = size_t(t) * p.K + n;
+            const float o[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (p.f32_out) static_cast<float *>(p.y)[at + j] = o[j];
+                else static_cast<__nv_bfloat16 *>(p.y)[at + j] = __float2bfloat16_rn(o[j]);
         }
     }
     __syncwarp();
@@ -664,7 +725,7 @@ MoeParams plan_moe(int M, int K, int I, int E, int k, int bits, int gs, int nc, 
     z.hcells = up256(hs * tile::cell_bytes(nc, kTermsH));
     z.hmeta = up256(hs * tile::meta_bytes(nc));
     z.partials = up256(size_t(pairs) * K * 4);
-    z.counters = up256(size_t(1 + p.tiles_b) * 4);
+    z.counters = up256(2 * 4);
     z.total = z.logits + z.rows + z.xmeta + z.hcells + z.hmeta + z.partials + z.counters;
     return p;
 }
@@ -788,16 +849,17 @@ extern "C" qmv_status qmv_moe_run(const uint16_t *x, const uint16_t *router, con
     p.stage_blocks = int(((long long)M * p.NSa * tile::slot_subs(bits) * 8 + kLogitThreads - 1) / kLogitThreads);
 
     MoeMaps m{};
-    const long long ra = (long long)experts * 2 * inter, rb = (long long)experts * K;
-    st = encode_rows(&m.wa, gu_w, (long long)K * bits / 8, ra, tile::kSlotBytes / 8, kHalf, true);
-    if (st == QMV_OK) st = encode_rows(&m.wb, dn_w, (long long)inter * bits / 8, rb, tile::kSlotBytes / 8, kHalf, true);
+    const long long rb = (long long)experts * K;
+    const long long two_e = 2ll * experts;
+    st = encode_rows(&m.wa, gu_w, (long long)K * bits / 8, inter, tile::kSlotBytes / 8, kHalf, true, two_e, 2);
+    if (st == QMV_OK) st = encode_rows(&m.wb, dn_w, (long long)inter * bits / 8, rb, tile::kSlotBytes / 8, tile::kTileRows, true);
     if (p.sba.mode == tile::kSbBoxes) {
-        if (st == QMV_OK) st = encode_rows(&m.sa, gu_scales, p.Ga * 2ll, ra, p.sba.pitch / 8, kHalf, false);
-        if (st == QMV_OK) st = encode_rows(&m.ba, gu_biases, p.Ga * 2ll, ra, p.sba.pitch / 8, kHalf, false);
+        if (st == QMV_OK) st = encode_rows(&m.sa, gu_scales, p.Ga * 2ll, inter, p.sba.pitch / 8, kHalf, false, two_e, 2);
+        if (st == QMV_OK) st = encode_rows(&m.ba, gu_biases, p.Ga * 2ll, inter, p.sba.pitch / 8, kHalf, false, two_e, 2);
     }
     if (p.sbb.mode == tile::kSbBoxes) {
-        if (st == QMV_OK) st = encode_rows(&m.sb, dn_scales, p.Gb * 2ll, rb, p.sbb.pitch / 8, kHalf, false);
-        if (st == QMV_OK) st = encode_rows(&m.bb, dn_biases, p.Gb * 2ll, rb, p.sbb.pitch / 8, kHalf, false);
+        if (st == QMV_OK) st = encode_rows(&m.sb, dn_scales, p.Gb * 2ll, rb, p.sbb.pitch / 8, tile::kTileRows, false);
+        if (st == QMV_OK) st = encode_rows(&m.bb, dn_biases, p.Gb * 2ll, rb, p.sbb.pitch / 8, tile::kTileRows, false);
     }
     if (st != QMV_OK) return st;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

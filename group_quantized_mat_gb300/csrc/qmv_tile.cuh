@@ -99,6 +99,28 @@ __device__ __forceinline__ uint4 lds_128(uint32_t addr)
     return v;
 }
 
+// 3-D tensor-map box load (see tma_load_2d).
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+
+// A place in a ring of `slots`: index and parity of the lap, kept without divisions.
+struct Turn {
+    int slot = 0, lap = 0;
+    __device__ __forceinline__ void step(int n, int slots)
+    {
+        slot += n;
+        while (slot >= slots) {
+            slot -= slots;
+            ++lap;
+        }
+    }
+};
+
 // 2^e for -126 <= e <= 127.
 __device__ __forceinline__ float exp2i(int e) { return __uint_as_float(uint32_t(e + 127) << 23); }
 
