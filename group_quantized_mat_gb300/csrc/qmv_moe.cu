@@ -53,8 +53,7 @@ struct MoeParams {
     float *logits;      // [M][E]
     uint8_t *rows;      // staged x: [M][subs_a][hi 64, lo 64]
     float2 *xmeta;      // [M][subs_a] (sum, f)
-    uint8_t *hcells;    // [entry][subs_b][cell_bytes(NC, 4)]
-    uint8_t *hmeta;     // [entry][subs_b][meta_bytes(NC)]
+    uint8_t *h;         // [entry][slot of B][subgroups' cells, subgroups' meta]
     float *partials;    // [pair][K]
     unsigned *counters; // CTAs done with A, and with B
     unsigned *err;
@@ -324,15 +323,36 @@ __global__ void __launch_bounds__(tile::kThreads, 1)
     tmem_fence_after();
     const uint32_t tm = s_tmem;
     const Waits wait{&s_abort, p.err};
-    const int entries = s_entries, na = entries * p.tiles_a, nb = entries * p.tiles_b;
     // entry, its expert, first pair, tokens; the item's tile
     struct Item {
         int entry, e, pair, count, tl;
     };
-    auto item_of = [&](int q, int tiles) {
+    // this CTA's items of `tiles` to an entry: from blockIdx.x on in steps of the grid
+    struct Items {
+        int entry, tl, entries, tiles, dentry, dtl;
+    };
+    auto items_of = [&](int tiles) {
+        Items s;
+        s.entries = s_entries;
+        s.tiles = tiles;
+        s.entry = int(blockIdx.x) / tiles;
+        s.tl = int(blockIdx.x) - s.entry * tiles;
+        s.dentry = grid / tiles;
+        s.dtl = grid - s.dentry * tiles;
+        return s;
+    };
+    auto advance = [](Items &s) {
+        s.entry += s.dentry;
+        s.tl += s.dtl;
+        if (s.tl >= s.tiles) {
+            s.tl -= s.tiles;
+            ++s.entry;
+        }
+    };
+    auto item_of = [&](const Items &s) {
         Item it;
-        it.entry = q / tiles;
-        it.tl = q - it.entry * tiles;
+        it.entry = s.entry;
+        it.tl = s.tl;
         const uint32_t v = s_entry[it.entry];
         it.e = int(v & 0xffffu);
         it.pair = s_base[it.e] + int(v >> 16);
@@ -395,12 +415,28 @@ __global__ void __launch_bounds__(tile::kThreads, 1)
         };
         // the lane's 16 bytes of each token's: subgroup, term and piece
         const int gsub = lane >> 3, gh = lane >> 2 & 1, gpc = lane & 3;
-        for (int q = blockIdx.x; q < na && ok; q += grid) {
-            const Item im = item_of(q, p.tiles_a);
-            for (int i = 0; i < p.NSa && ok; ++i) {
-                if (i % p.cha == 0) fetch(true, p.sba, p.gu_s, p.gu_b, &sa, &ba, im.e, im.tl * kHalf, kTileRows, p.Ga, i);
+        const int msub = lane / 2 % SUBS, mf = lane & 1, mtok = lane / (2 * SUBS);
+        for (Items is = items_of(p.tiles_a); is.entry < is.entries && ok; advance(is)) {
+            const Item im = item_of(is);
+            // where each token's bytes come from, slot by slot
+            const uint8_t *from[NC];
+            const float *mfrom[(NC * SUBS + 15) / 16];
+#pragma unroll
+            for (int j = 0; j < NC; ++j)
+                from[j] = p.rows + size_t(s_tok[im.pair + min(j, im.count - 1)]) * p.NSa * (SUBS * 128) + lane * 16;
+#pragma unroll
+            for (int j = 0; j < (NC * SUBS + 15) / 16; ++j)
+                mfrom[j] = reinterpret_cast<const float *>(
+                               p.xmeta + size_t(s_tok[im.pair + min(j * (16 / SUBS) + mtok, im.count - 1)]) * p.NSa * SUBS + msub) + mf;
+            int left = 0;  // slots until the next scales and biases
+            for (int i = 0; i < p.NSa && ok; ++i, --left) {
+                if (left == 0) {
+                    left = p.cha;
+                    fetch(true, p.sba, p.gu_s, p.gu_b, &sa, &ba, im.e, im.tl * kHalf, kTileRows, p.Ga, i);
+                }
                 if (!ok) break;
-                ok = __all_sync(0xffffffffu, turn.lap == 0 || wait(empty0 + 8 * turn.slot, (turn.lap - 1) & 1));
+                ok = turn.lap == 0 || wait(empty0 + 8 * turn.slot, (turn.lap - 1) & 1);
+                ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 const uint32_t full = full0 + 8 * turn.slot, dst = base + turn.slot * L.slot;
                 if (lane == 0) {
@@ -408,19 +444,23 @@ __global__ void __launch_bounds__(tile::kThreads, 1)
                     tma_load_3d(dst, &wa, i * (kSlotBytes / 8), im.tl * kHalf, 2 * im.e, full);
                 }
                 // the tokens' operand bytes, 512 a time, and their sums
-                const uint8_t *src = p.rows + (size_t(i) * SUBS * 128 + lane * 16);
-                for (int j = 0; j < im.count; ++j) {
-                    const uint8_t *from = src + size_t(s_tok[im.pair + j]) * p.NSa * (SUBS * 128);
+#pragma unroll
+                for (int j = 0; j < NC; ++j) {
+                    if (j >= im.count) break;
                     const uint32_t d = dst + L.cells + gsub * CA + operand_offset(operand_index(j, gh), gpc);
 #pragma unroll
                     for (int s = 0; s < SUBS / 4; ++s)
-                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d + s * 4 * CA), "l"(from + s * 512) : "memory");
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d + s * 4 * CA), "l"(from[j] + s * 512) : "memory");
+                    from[j] += SUBS * 128;
                 }
-                const int sub = lane / 2 % SUBS, f = lane & 1;
-                for (int j = lane / (2 * SUBS); j < im.count; j += 16 / SUBS) {
-                    const float *from = reinterpret_cast<const float *>(p.xmeta + (size_t(s_tok[im.pair + j]) * p.NSa + i) * SUBS + sub) + f;
-                    const uint32_t d = dst + L.meta + sub * MB + (j >> 1) * 16 + (j & 1) * 4 + f * 8;
-                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(d), "l"(from) : "memory");
+#pragma unroll
+                for (int j = 0; j < (NC * SUBS + 15) / 16; ++j) {
+                    const int tk = j * (16 / SUBS) + mtok;
+                    if (tk < im.count)
+                        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst + L.meta + msub * MB + (tk >> 1) * 16 + (tk & 1) * 4 + mf * 8),
+                                     "l"(mfrom[j])
+                                     : "memory");
+                    mfrom[j] += SUBS * 2;
                 }
                 asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(full) : "memory");
                 turn.step(1, p.slots);
@@ -430,32 +470,34 @@ __global__ void __launch_bounds__(tile::kThreads, 1)
         // as the two buffers of scales serve), h after it
         int ahead = 0;
         const Turn turn0 = turn;
-        auto b_slots = [&](int from, bool weights, bool cells, int most) {
+        auto b_slots = [&](int first, bool weights, bool cells, int most) {
             int n = 0;
             Turn at = turn0;
-            for (int q = blockIdx.x; q < nb && ok; q += grid) {
-                const Item im = item_of(q, p.tiles_b);
+            for (Items is = items_of(p.tiles_b); is.entry < is.entries && ok; advance(is)) {
+                const Item im = item_of(is);
                 const int row = im.tl * kTileRows;
-                for (int i = 0; i < p.NSb && ok; ++i, ++n, at.step(1, p.slots)) {
+                const uint8_t *h = p.h + size_t(im.entry) * p.NSb * (SUBS * (CB + MB));
+                int left = 0;
+                for (int i = 0; i < p.NSb && ok; ++i, ++n, --left, h += SUBS * (CB + MB), at.step(1, p.slots)) {
                     if (n >= most) return n;
-                    if (n < from) continue;
+                    const bool fetched = left == 0;
+                    if (fetched) left = p.chb;
+                    if (n < first) continue;
                     const uint32_t full = full0 + 8 * at.slot, dst = base + at.slot * L.slot;
                     if (weights) {
-                        if (i % p.chb == 0) fetch(false, p.sbb, p.dn_s, p.dn_b, &sbm, &bb, im.e, row, min(p.K - row, kTileRows), p.Gb, i);
+                        if (fetched) fetch(false, p.sbb, p.dn_s, p.dn_b, &sbm, &bb, im.e, row, min(p.K - row, kTileRows), p.Gb, i);
                         if (!ok) break;
-                        ok = __all_sync(0xffffffffu, at.lap == 0 || wait(empty0 + 8 * at.slot, (at.lap - 1) & 1));
+                        ok = at.lap == 0 || wait(empty0 + 8 * at.slot, (at.lap - 1) & 1);
+                        ok = __all_sync(0xffffffffu, ok);
                         if (!ok) break;
                         if (lane == 0) {
                             mbar_arrive_expect_tx(full, kTileRows * kSlotBytes + SUBS * (CB + MB));
                             tma_load_2d(dst, &wb, i * (kSlotBytes / 8), im.e * p.K + row, full);
+                            // for the lanes that arrive of their own in A
+                            asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], 32;" ::"r"(full) : "memory");
                         }
-                        mbar_arrive(full);
                     }
-                    if (cells && lane == 0) {
-                        const size_t sub = (size_t(im.entry) * p.NSb + i) * SUBS;
-                        bulk_load_plain(dst + L.cells, p.hcells + sub * CB, SUBS * CB, full);
-                        bulk_load_plain(dst + L.meta, p.hmeta + sub * MB, SUBS * MB, full);
-                    }
+                    if (cells && lane == 0) bulk_load_plain(dst + L.cells, h, SUBS * (CB + MB), full);
                 }
             }
             return n;
@@ -483,7 +525,7 @@ __global__ void __launch_bounds__(tile::kThreads, 1)
             // turn: of the item's first slot
             Turn turn;
             Pipe pipe = Pipe::make<NC, 2>(tm, 0, stored0, ready0, group);
-            for (int q = blockIdx.x; q < na; q += grid, turn.step(p.NSa, p.slots)) {
+            for (Items is = items_of(p.tiles_a); is.entry < is.entries; advance(is), turn.step(p.NSa, p.slots)) {
                 Turn at = turn;
                 at.step(group, p.slots);
                 for (int i = group; i < p.NSa; i += kGroups, at.step(kGroups, p.slots))
@@ -491,7 +533,7 @@ __global__ void __launch_bounds__(tile::kThreads, 1)
             }
             Pipe pb = Pipe::make<NC, kTermsH>(tm, 0, stored0, ready0, group);
             pb.steps = pipe.steps;
-            for (int q = blockIdx.x; q < nb; q += grid, turn.step(p.NSb, p.slots)) {
+            for (Items is = items_of(p.tiles_b); is.entry < is.entries; advance(is), turn.step(p.NSb, p.slots)) {
                 Turn at = turn;
                 at.step(group, p.slots);
                 for (int i = group; i < p.NSb; i += kGroups, at.step(kGroups, p.slots))
@@ -546,8 +588,8 @@ __global__ void __launch_bounds__(tile::kThreads, 1)
 
         Pipe pipe = Pipe::make<NC, 2>(tm, lanes, stored0, ready0, group);
         float *xs = reinterpret_cast<float *>(smem + L.xs), *red = xs + NC * kHalf + group * 4;
-        for (int q = blockIdx.x; q < na; q += grid) {
-            const Item im = item_of(q, p.tiles_a);
+        for (Items is = items_of(p.tiles_a); is.entry < is.entries; advance(is)) {
+            const Item im = item_of(is);
             Row<BITS, GS, NC, 2> acc;
             run(acc, pipe, p.sba, p.cha, p.NSa, p.Ga, (long long)im.e * 2 * p.I + (row < kHalf ? 0 : p.I - kHalf) + im.tl * kHalf + row);
             constexpr int OWN = Row<BITS, GS, NC, 2>::kOwn;
@@ -558,7 +600,8 @@ __global__ void __launch_bounds__(tile::kThreads, 1)
             for (int i = 0; i < OWN; ++i)
                 if (row >= kHalf && group + kGroups * i < NC) xs[(group + kGroups * i) * kHalf + row - kHalf] = sums[i];
             named_sync(2 + group, 128);
-            const size_t cell0 = (size_t(im.entry) * p.NSb * SUBS + im.tl) * CB;
+            uint8_t *slot_h = p.h + (size_t(im.entry) * p.NSb + im.tl / SUBS) * (SUBS * (CB + MB));
+            uint8_t *cell = slot_h + im.tl % SUBS * CB, *meta = slot_h + SUBS * CB + im.tl % SUBS * MB;
             if (row < kHalf) {
 #pragma unroll
                 for (int i = 0; i < OWN; ++i) {
@@ -591,10 +634,10 @@ __global__ void __launch_bounds__(tile::kThreads, 1)
                         float back, none;
                         from_e4m3x2(b, back, none);
                         v = __fmul_rn(__fsub_rn(v, back), 32.0f);
-                        p.hcells[cell0 + operand_offset(operand_index(j, t, kTermsH), pc) + at] = uint8_t(b);
+                        cell[operand_offset(operand_index(j, t, kTermsH), pc) + at] = uint8_t(b);
                     }
                     if (row == 0) {
-                        float *m = reinterpret_cast<float *>(p.hmeta + (size_t(im.entry) * p.NSb * SUBS + im.tl) * MB + (j >> 1) * 16) + (j & 1);
+                        float *m = reinterpret_cast<float *>(meta + (j >> 1) * 16) + (j & 1);
                         m[0] = sum;
                         m[2] = exp2i(min(int(E) - 125, 127));
                     }
@@ -602,10 +645,10 @@ __global__ void __launch_bounds__(tile::kThreads, 1)
             }
             // subgroups that fill the last slot
             if (im.tl == p.tiles_a - 1)
-                for (int sub = p.Sb; sub < p.NSb * SUBS; ++sub) {
-                    const size_t cell = size_t(im.entry) * p.NSb * SUBS + sub;
-                    for (int i = tid; i < CB / 4; i += 32 * kWorkers) reinterpret_cast<uint32_t *>(p.hcells + cell * CB)[i] = 0u;
-                    for (int i = tid; i < MB / 4; i += 32 * kWorkers) reinterpret_cast<uint32_t *>(p.hmeta + cell * MB)[i] = 0u;
+                for (int sub = p.Sb % SUBS; sub > 0 && sub < SUBS; ++sub) {
+                    uint32_t *c = reinterpret_cast<uint32_t *>(slot_h + sub * CB), *m = reinterpret_cast<uint32_t *>(slot_h + SUBS * CB + sub * MB);
+                    for (int i = tid; i < CB / 4; i += 32 * kWorkers) c[i] = 0u;
+                    for (int i = tid; i < MB / 4; i += 32 * kWorkers) m[i] = 0u;
                 }
         }
         asm volatile("fence.proxy.async;" ::: "memory");
@@ -615,8 +658,8 @@ __global__ void __launch_bounds__(tile::kThreads, 1)
 
         Pipe pb = Pipe::make<NC, kTermsH>(tm, lanes, stored0, ready0, group);
         pb.steps = pipe.steps;
-        for (int q = blockIdx.x; q < nb; q += grid) {
-            const Item im = item_of(q, p.tiles_b);
+        for (Items is = items_of(p.tiles_b); is.entry < is.entries; advance(is)) {
+            const Item im = item_of(is);
             const int n = im.tl * kTileRows + row;
             Row<BITS, GS, NC, kTermsH> acc;
             run(acc, pb, p.sbb, p.chb, p.NSb, p.Gb, (long long)im.e * p.K + n);
@@ -689,7 +732,7 @@ qmv_status check_moe(int M, int K, int I, int E, int k, int bits, int gs)
 size_t up256(size_t b) { return (b + 255) & ~size_t(255); }
 
 struct MoeSizes {
-    size_t logits, rows, xmeta, hcells, hmeta, partials, counters, total;
+    size_t logits, rows, xmeta, h, partials, counters, total;
 };
 
 // Tokens of an expert that one read of its weights serves: 2, 4 or 8, so that
@@ -722,11 +765,10 @@ MoeParams plan_moe(int M, int K, int I, int E, int k, int bits, int gs, int nc, 
     z.logits = up256(size_t(M) * E * 4);
     z.rows = up256(size_t(M) * p.NSa * subs * 128);
     z.xmeta = up256(size_t(M) * p.NSa * subs * 8);
-    z.hcells = up256(hs * tile::cell_bytes(nc, kTermsH));
-    z.hmeta = up256(hs * tile::meta_bytes(nc));
+    z.h = up256(hs * (tile::cell_bytes(nc, kTermsH) + tile::meta_bytes(nc)));
     z.partials = up256(size_t(pairs) * K * 4);
     z.counters = up256(2 * 4);
-    z.total = z.logits + z.rows + z.xmeta + z.hcells + z.hmeta + z.partials + z.counters;
+    z.total = z.logits + z.rows + z.xmeta + z.h + z.partials + z.counters;
     return p;
 }
 
@@ -842,8 +884,7 @@ extern "C" qmv_status qmv_moe_run(const uint16_t *x, const uint16_t *router, con
     p.logits = reinterpret_cast<float *>(at); at += z.logits;
     p.rows = at; at += z.rows;
     p.xmeta = reinterpret_cast<float2 *>(at); at += z.xmeta;
-    p.hcells = at; at += z.hcells;
-    p.hmeta = at; at += z.hmeta;
+    p.h = at; at += z.h;
     p.partials = reinterpret_cast<float *>(at); at += z.partials;
     p.counters = reinterpret_cast<unsigned *>(at);
     p.stage_blocks = int(((long long)M * p.NSa * tile::slot_subs(bits) * 8 + kLogitThreads - 1) / kLogitThreads);
