@@ -16,14 +16,18 @@
 // lora_project, one CTA per SM: a producer warp brings 128 bytes of each row of
 // a tile, with their scales and biases, to a ring of shared-memory slots (one
 // tensor-map box, 128-byte swizzle), three groups of worker warps run the tiles,
-// three tensor warps multiply. A worker thread owns a row, and in the end adds
-// the adapters' second half to the sums it holds.
+// three tensor warps multiply. A worker thread owns a row. The rows of the pass's
+// adapters follow a tile's weights through the ring, each adapter once however
+// many vectors have it, and each thread adds their products with the inner
+// vectors to the sums it holds. (Threads reading their rows from global memory,
+// 16 bytes at a time, took 16 of a tile's 47 thousand cycles at 16 vectors of
+// rank 64: 168 us for 64 vectors.)
 //  - Rows go to CTAs in tiles of equal height (a multiple of 8, at most 128): 104
 //    for 15360 rows on 152 SMs.
 //  - K goes to CTAs in ranges of at most 64 subgroups (4096), whose cells of 16
-//    vectors are 128 KB. Several ranges meet in the workspace: the CTA that
+//    vectors are 128 KB (48 at ranks above 88). Several ranges meet in the workspace: the CTA that
 //    finishes a tile last adds them in their order.
-// The order of every sum depends on N and K alone, so a vector's result does not
+// The order of every sum depends on N, K and the rank alone, so a vector's result does not
 // depend on the batch it is in.
 #include <cuda_bf16.h>
 
@@ -41,9 +45,11 @@ constexpr int kPrepareThreads = 256;
 constexpr int kMaxSlotsLora = 12;
 constexpr int kSmem = 227 * 1024 - 1024;
 constexpr int kMaxK = 1 << 16;
-constexpr int kRangeSubs = 64;  // subgroups of a range of K at most
+// Subgroups of a range of K at most. The ring's three slots, a range's cells of 16
+// vectors, its scales and biases and the inner vectors have to fit at 128 rows.
+__host__ __device__ constexpr int range_subs(int rank) { return rank <= 88 ? 64 : 48; }
 constexpr int kPass = 16;       // vectors that one read of the weights serves
-constexpr int kBefore = 3;      // slots of weights asked for before staged x
+constexpr int kBefore = 3;      // slots of weights asked for before staged x (no more than a ring has)
 
 struct LoraParams {
     const uint16_t *scales, *biases, *x, *a, *b;
@@ -63,6 +69,7 @@ struct LoraParams {
     int nseg;    // ranges of K
     int range;   // slots of the longest range
     int rows, tiles, grid_rows;
+    int piece;   // rows of an adapter's B that a ring slot holds
     int nc, slots, stage_blocks, sb_buffers;
     tile::Affines sb;
 };
@@ -145,63 +152,73 @@ __host__ __device__ inline Layout layout(const LoraParams &p, int bits, int nc)
     l.meta = l.x + subs * tile::cell_bytes(nc);
     l.sb = (l.meta + subs * tile::meta_bytes(nc) + 127) & ~127;
     l.inner = l.sb + p.sb_buffers * 2 * p.sb.block;
-    l.bars = l.inner + nc * p.R * 4;
-    l.bars = (l.bars + 15) & ~15;
+    l.bars = l.inner + nc * ((p.R + 7) & ~7) * 4;
     l.total = l.bars + (2 * p.slots + 4 * tile::kGroups + 5) * 8;
     return l;
 }
 
-// Adds c * (B v) to sums[i] for the thread's vectors (ads[i] their adapters, -1:
-// none) in row n of the adapters' B, v(i) being the address of vector i's inner
-// vector in shared memory: 16 of the rank at a time, so that the loads of all
-// vectors are in flight together.
-template <int OWN>
-__device__ __forceinline__ void add_adapters(const LoraParams &p, const int (&ads)[OWN], const float *inner, int n,
-                                             float (&sums)[OWN])
+// The product of a row of an adapter's B (R elements at shared address `addr`)
+// with an inner vector v (padded to a multiple of eight floats).
+__device__ __forceinline__ float adapter_dot(uint32_t addr, const float *v, int R, int row)
 {
-    float d[OWN];
-#pragma unroll
-    for (int i = 0; i < OWN; ++i) d[i] = 0.0f;
-    if (p.R % 8 == 0) {
-#pragma unroll 1
-        for (int r = 0; r < p.R; r += 16) {
-            const bool two = r + 8 < p.R;
-            uint4 b[OWN][2];
-#pragma unroll
-            for (int i = 0; i < OWN; ++i)
-                if (ads[i] >= 0) {
-                    const uint4 *q = reinterpret_cast<const uint4 *>(p.b + (size_t(ads[i]) * p.N + n) * p.R + r);
-                    b[i][0] = __ldg(q);
-                    if (two) b[i][1] = __ldg(q + 1);
-                }
-#pragma unroll
-            for (int i = 0; i < OWN; ++i)
-                if (ads[i] >= 0) {
-                    const float4 *v = reinterpret_cast<const float4 *>(inner + (tile::kGroups * i) * p.R + r);
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        if (h && !two) break;
-                        float x[8];
-                        tile::widen8(b[i][h], x);
-                        const float4 v0 = v[2 * h], v1 = v[2 * h + 1];
-                        const float w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) d[i] = __fmaf_rn(x[j], w[j], d[i]);
-                    }
-                }
+    float d0 = 0.0f, d1 = 0.0f;
+    if (R % 8 == 0) {
+        // Rows lie R/8 pieces of 16 bytes apart: each starts at another piece, so
+        // that neighbours' reads fall on different banks.
+        const int C = R / 8;
+        int c = (C >= 8 ? row : row * C >> 3) % C;
+#pragma unroll 2
+        for (int i = 0; i < C; ++i) {
+            float x[8];
+            tile::widen8(tile::lds_128(addr + c * 16), x);
+            const float4 v0 = *reinterpret_cast<const float4 *>(v + c * 8), v1 = *reinterpret_cast<const float4 *>(v + c * 8 + 4);
+            d0 = __fmaf_rn(x[0], v0.x, d0);
+            d1 = __fmaf_rn(x[1], v0.y, d1);
+            d0 = __fmaf_rn(x[2], v0.z, d0);
+            d1 = __fmaf_rn(x[3], v0.w, d1);
+            d0 = __fmaf_rn(x[4], v1.x, d0);
+            d1 = __fmaf_rn(x[5], v1.y, d1);
+            d0 = __fmaf_rn(x[6], v1.z, d0);
+            d1 = __fmaf_rn(x[7], v1.w, d1);
+            c = c + 1 == C ? 0 : c + 1;
         }
     } else {
-#pragma unroll 4
-        for (int r = 0; r < p.R; ++r)
-#pragma unroll
-            for (int i = 0; i < OWN; ++i)
-                if (ads[i] >= 0)
-                    d[i] = __fmaf_rn(__uint_as_float(uint32_t(__ldg(p.b + (size_t(ads[i]) * p.N + n) * p.R + r)) << 16),
-                                     inner[(tile::kGroups * i) * p.R + r], d[i]);
+        // words, shifted by an element where the row starts inside one
+        const bool odd = addr & 2;
+        const uint32_t word = addr & ~3u;
+        uint32_t next = 0;
+        auto lds_32 = [](uint32_t a) {
+            uint32_t w;
+            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w) : "r"(a));
+            return w;
+        };
+        if (odd) next = lds_32(word);
+        int r = 0;
+#pragma unroll 2
+        for (; r + 4 <= R; r += 4) {
+            uint32_t a, b;
+            if (odd) {
+                const uint32_t w1 = lds_32(word + 2 * r + 4), w2 = lds_32(word + 2 * r + 8);
+                a = __byte_perm(next, w1, 0x5432);
+                b = __byte_perm(w1, w2, 0x5432);
+                next = w2;
+            } else {
+                a = lds_32(word + 2 * r);
+                b = lds_32(word + 2 * r + 4);
+            }
+            const float4 w = *reinterpret_cast<const float4 *>(v + r);
+            d0 = __fmaf_rn(__uint_as_float(a << 16), w.x, d0);
+            d1 = __fmaf_rn(__uint_as_float(a & 0xffff0000u), w.y, d1);
+            d0 = __fmaf_rn(__uint_as_float(b << 16), w.z, d0);
+            d1 = __fmaf_rn(__uint_as_float(b & 0xffff0000u), w.w, d1);
+        }
+        for (; r < R; ++r) {
+            uint16_t e;
+            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(e) : "r"(addr + 2 * r));
+            d0 = __fmaf_rn(__uint_as_float(uint32_t(e) << 16), v[r], d0);
+        }
     }
-#pragma unroll
-    for (int i = 0; i < OWN; ++i)
-        if (ads[i] >= 0) sums[i] = __fadd_rn(sums[i], __fmul_rn(__ldg(p.c + ads[i]), d[i]));
+    return __fadd_rn(d0, d1);
 }
 
 template <int BITS, int GS, int NC>
@@ -212,7 +229,7 @@ __global__ void __launch_bounds__(tile::kThreads, 1) lora_project(const __grid_c
 {
     using namespace tile;
     extern __shared__ __align__(1024) uint8_t smem[];
-    __shared__ int s_abort, s_last, s_ad[kPass];
+    __shared__ int s_abort, s_last, s_ad[kPass], s_which[kPass], s_ads;
     __shared__ uint32_t s_tmem;
     constexpr int SUBS = slot_subs(BITS);
     const Layout L = layout(p, BITS, NC);
@@ -223,15 +240,24 @@ __global__ void __launch_bounds__(tile::kThreads, 1) lora_project(const __grid_c
     const int seg = blockIdx.y, z = blockIdx.z, nv = min(kPass, p.M - z * kPass);
     const int lo = int((long long)p.NS * seg / p.nseg), ns = int((long long)p.NS * (seg + 1) / p.nseg) - lo;
     const int g0 = lo * SUBS * 64 / GS, groups = min(ns * SUBS * 64 / GS, p.G - g0);
-    if (tid >= 64 && tid < 64 + kPass) {
-        // the adapters of this pass's vectors, -1: none
-        const int t = tid - 64, ad = t < nv ? __ldg(p.adapter + z * kPass + t) : -1;
-        s_ad[t] = ad < p.L ? ad : -1;
+    if (warp == 2) {
+        // This range's adapters among those of the pass's vectors, each once, in
+        // their order, and each vector's place among them (-1: none here). An
+        // adapter belongs to the range of its number modulo the ranges.
+        int ad = lane < nv ? __ldg(p.adapter + z * kPass + lane) : -1;
+        if (ad < 0 || ad >= p.L || ad % p.nseg != seg) ad = -1;
+        const uint32_t same = __match_any_sync(0xffffffffu, ad);
+        const bool first = ad >= 0 && __ffs(same) - 1 == lane;
+        const uint32_t firsts = __ballot_sync(0xffffffffu, first);
+        const int at = __shfl_sync(0xffffffffu, __popc(firsts & ((1u << lane) - 1u)), __ffs(same) - 1);
+        if (first) s_ad[at] = ad;
+        if (lane < kPass) s_which[lane] = ad >= 0 ? at : -1;
+        if (lane == 0) s_ads = __popc(firsts);
     }
     if (tid == 0) {
         for (int i = 0; i < p.slots; ++i) {
             mbar_init(full0 + 8 * i, 1);
-            mbar_init(empty0 + 8 * i, 4);
+            mbar_init(empty0 + 8 * i, kWorkers);
         }
         for (int i = 0; i < 2 * kGroups; ++i) {
             mbar_init(stored0 + 8 * i, 4);
@@ -251,6 +277,7 @@ __global__ void __launch_bounds__(tile::kThreads, 1) lora_project(const __grid_c
     tmem_fence_after();
     const uint32_t tm = s_tmem;
     const Waits wait{&s_abort, p.err};
+    const int ads = s_ads, pieces = (p.rows + p.piece - 1) / p.piece;
 
     // staged x by bulk copies, once the first kernel has ended
     auto fetch_x = [&]() {
@@ -286,6 +313,30 @@ __global__ void __launch_bounds__(tile::kThreads, 1) lora_project(const __grid_c
                     mbar_arrive_expect_tx(full0 + 8 * s, bytes);
                     tma_load_2d(base + s * L.slot, &map, (lo + i) * (kSlotBytes / 8), tl * p.rows, full0 + 8 * s);
                 }
+            if (lane == 0 && ok && !staged) {
+                staged = true;
+                fetch_x();
+            }
+            // the adapters' rows of the tile, from the 16-byte boundary before them
+            if (lane == 0)
+                for (int j = 0; j < ads * pieces && ok; ++j, ++it) {
+                    const int d = ads == 0 ? 0 : j / pieces, r0 = (j - d * pieces) * p.piece;
+                    const int s = it % p.slots, lap = it / p.slots;
+                    ok = lap == 0 || wait(empty0 + 8 * s, (lap - 1) & 1);
+                    if (!ok) break;
+                    const long long n0 = (long long)tl * p.rows + r0, n1 = min(n0 + min(p.piece, p.rows - r0), (long long)p.N);
+                    const long long first = ((long long)s_ad[d] * p.N + n0) * p.R * 2, to = first + max(n1 - n0, 0ll) * p.R * 2;
+                    const long long from = first & ~15ll, whole = min((to + 15) & ~15ll, (long long)p.L * p.N * p.R * 2 & ~15ll);
+                    const uint32_t bytes = n1 > n0 && whole > from ? uint32_t(whole - from) : 0u;
+                    // the array's last bytes, where they fill no 16
+                    if (whole < to && n1 > n0) {
+                        for (long long e = max(whole, from); e < to; e += 2)
+                            *reinterpret_cast<uint16_t *>(smem + s * L.slot + (e - from)) = __ldg(p.b + e / 2);
+                        fence_proxy_async_smem();
+                    }
+                    mbar_arrive_expect_tx(full0 + 8 * s, bytes);
+                    if (bytes) bulk_load_plain(base + s * L.slot, reinterpret_cast<const uint8_t *>(p.b) + from, bytes, full0 + 8 * s);
+                }
             ok = __all_sync(0xffffffffu, ok);
         }
         if (lane == 0) {
@@ -304,8 +355,9 @@ __global__ void __launch_bounds__(tile::kThreads, 1) lora_project(const __grid_c
         if (lane == 0) {
             wait(xbar, 0);
             Pipe pipe = Pipe::make<NC>(tm, 0, stored0, ready0, group);
-            for (int tl = blockIdx.x; tl < p.tiles; tl += p.grid_rows)
-                for (int i = group; i < ns; i += kGroups)
+            int it = 0;
+            for (int tl = blockIdx.x; tl < p.tiles; tl += p.grid_rows, it += ns + ads * pieces)
+                for (int i = first_slot(group, it); i < ns; i += kGroups)
                     multiply_slot<BITS, NC>(wait, pipe, base + L.x + i * SUBS * cell_bytes(NC));
         }
     } else {
@@ -317,25 +369,18 @@ __global__ void __launch_bounds__(tile::kThreads, 1) lora_project(const __grid_c
         grid_launch_dependents();
         wait(xbar, 0);
         int it = 0, tiles = 0;
-        const int align = p.sb.alignment(p.G);
-        for (int tl = blockIdx.x; tl < p.tiles; tl += p.grid_rows, it += ns, ++tiles) {
+        const int align = p.sb.alignment(p.G), inner_pitch = (p.R + 7) & ~7;
+        for (int tl = blockIdx.x; tl < p.tiles; tl += p.grid_rows, it += ns + ads * pieces, ++tiles) {
             const int n = tl * p.rows + row;
             const bool live = row < p.rows && n < p.N;
             Row<BITS, GS, NC> acc;
             acc.start();
             uint32_t last = 0;
-            // the adapters' rows of this tile are on their way to L2 meanwhile
-            if (live)
-                for (int t = group; t < nv; t += kGroups) {
-                    if (s_ad[t] < 0) continue;
-                    const uint16_t *b = p.b + (size_t(s_ad[t]) * p.N + n) * p.R;
-                    for (int r = 0; r < p.R; r += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(b + r));
-                }
             const int buf = tiles % p.sb_buffers;
             wait(sfull0 + 8 * buf, (tiles / p.sb_buffers) & 1);
             const uint32_t sb = base + L.sb + buf * 2 * p.sb.block + min(row, p.rows - 1) * p.sb.pitch + p.sb.offset(n, p.G, g0);
 #pragma unroll 1
-            for (int i = group; i < ns; i += kGroups) {
+            for (int i = first_slot(group, it); i < ns; i += kGroups) {
                 const int s = (it + i) % p.slots, lap = (it + i) / p.slots;
                 wait(full0 + 8 * s, lap & 1);
                 const uint32_t meta = base + L.meta + i * SUBS * meta_bytes(NC);
@@ -345,18 +390,37 @@ __global__ void __launch_bounds__(tile::kThreads, 1) lora_project(const __grid_c
                 acc.slot(wait, pipe, wrow + s * L.slot, aff, meta, last, lane);
                 last = meta + (SUBS - 2 * step_subs(NC)) * meta_bytes(NC);
                 __syncwarp();
-                if (lane == 0) mbar_arrive(empty0 + 8 * s);
+                if (lane == 0) mbar_arrive_many(empty0 + 8 * s, kGroups);
             }
             if (lane == 0) mbar_arrive(sempty0 + 8 * buf);
             acc.finish(wait, pipe, last);
             if (tiles == 0) {
                 // the inner vectors (of vectors without an adapter: whatever is there)
                 grid_dependency_wait();
-                for (int i = tid; i < nv * p.R; i += 32 * kWorkers)
-                    reinterpret_cast<float *>(smem + L.inner)[i] = __ldcg(p.inner + size_t(z) * kPass * p.R + i);
+                for (int i = tid; i < nv * inner_pitch; i += 32 * kWorkers) {
+                    const int t = i / inner_pitch, r = i - t * inner_pitch;
+                    if (r < p.R) reinterpret_cast<float *>(smem + L.inner)[i] = __ldcg(p.inner + (size_t(z) * kPass + t) * p.R + r);
+                }
             }
             float sums[Row<BITS, GS, NC>::kOwn];
-            acc.join(tm + lanes, group, sums);  // its barriers also publish the inner vectors
+            acc.join(tm + lanes, group, it % kGroups, sums);  // its barriers also publish the inner vectors
+            for (int j = 0, at = it + ns; j < ads * pieces; ++j, ++at) {
+                const int d = j / pieces, r0 = (j - d * pieces) * p.piece, s = at % p.slots;
+                wait(full0 + 8 * s, (at / p.slots) & 1);
+                if (live && row >= r0 && row < r0 + p.piece) {
+                    const long long first = ((long long)s_ad[d] * p.N + n - (row - r0)) * p.R * 2;
+                    const uint32_t addr = base + s * L.slot + (uint32_t(first) & 15u) + (row - r0) * p.R * 2;
+                    const float c = __ldg(p.c + s_ad[d]);
+#pragma unroll
+                    for (int i = 0; i < Row<BITS, GS, NC>::kOwn; ++i) {
+                        const int t = group + kGroups * i;
+                        if (t < nv && s_which[t] == d)
+                            sums[i] = __fadd_rn(sums[i], __fmul_rn(c, adapter_dot(addr, reinterpret_cast<const float *>(smem + L.inner) + t * inner_pitch, p.R, row)));
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(empty0 + 8 * s);
+            }
             bool mine = true;
             if (p.nseg > 1) {
                 const size_t plane = size_t(p.N), seg_stride = plane * NC;
@@ -384,10 +448,6 @@ __global__ void __launch_bounds__(tile::kThreads, 1) lora_project(const __grid_c
                 }
             }
             if (!mine || !live) continue;
-            int ads[Row<BITS, GS, NC>::kOwn];
-#pragma unroll
-            for (int i = 0; i < Row<BITS, GS, NC>::kOwn; ++i) ads[i] = group + kGroups * i < nv ? s_ad[group + kGroups * i] : -1;
-            add_adapters(p, ads, reinterpret_cast<const float *>(smem + L.inner) + group * p.R, n, sums);
 #pragma unroll
             for (int i = 0; i < Row<BITS, GS, NC>::kOwn; ++i) {
                 const int t = group + kGroups * i;
@@ -423,7 +483,7 @@ LoraParams plan(int M, int N, int K, int bits, int gs, int R, int sms, Sizes &sz
     p.S = K / 64;
     p.NS = (p.S + slot_subs - 1) / slot_subs;
     p.subs = p.NS * slot_subs;
-    p.nseg = (p.NS * slot_subs + kRangeSubs - 1) / kRangeSubs;
+    p.nseg = (p.NS * slot_subs + range_subs(R) - 1) / range_subs(R);
     p.range = (p.NS + p.nseg - 1) / p.nseg;
     p.nc = M <= 2 ? 2 : M <= 4 ? 4 : M <= 8 ? 8 : 16;
     // tiles of equal height: as many rounds of the grid as 128 rows need
@@ -432,7 +492,15 @@ LoraParams plan(int M, int N, int K, int bits, int gs, int R, int sms, Sizes &sz
     p.rows = ((N + p.grid_rows * rounds - 1) / (p.grid_rows * rounds) + 7) / 8 * 8;
     p.tiles = (N + p.rows - 1) / p.rows;
     if (p.grid_rows > p.tiles) p.grid_rows = p.tiles;
+    // (with room for the bytes before the first where pieces may start off 16 bytes)
+    const int slot = p.rows * tile::kSlotBytes;
+    p.piece = (long long)N * R % 8 == 0 && R * 2 <= tile::kSlotBytes ? p.rows : (slot - 16) / (2 * R);
+    if (p.piece > p.rows) p.piece = p.rows;
+    // (whole rows of up to 96 groups where the ring's three slots still fit beside them)
+    p.slots = tile::kGroups;
+    p.sb_buffers = 1;
     p.sb = tile::Affines::plan(p.G, p.range * slot_subs * 64 / gs, p.rows, 96);
+    if (layout(p, bits, p.nc).total > kSmem) p.sb = tile::Affines::plan(p.G, p.range * slot_subs * 64 / gs, p.rows, 64);
     p.sb_buffers = rounds > 1 ? 2 : 1;
     const size_t passes = (M + kPass - 1) / kPass;
     sz.cells = up256(passes * p.subs * tile::cell_bytes(p.nc));
@@ -465,11 +533,11 @@ cudaError_t launch_lora(const RingMaps &maps, LoraParams &p, cudaStream_t stream
 template <int BITS>
 cudaError_t launch_lora(const RingMaps &maps, LoraParams &p, cudaStream_t stream)
 {
-    // as many slots as fit
-    p.slots = 4;
+    // as many slots as fit, in threes (see qmv_tile.cuh)
+    p.slots = 2 * tile::kGroups;
     if (layout(p, BITS, p.nc).total > kSmem) p.sb_buffers = 1;
     p.slots = kMaxSlotsLora;
-    while (p.slots > 2 && layout(p, BITS, p.nc).total > kSmem) --p.slots;
+    while (p.slots > tile::kGroups && layout(p, BITS, p.nc).total > kSmem) p.slots -= tile::kGroups;
     if (layout(p, BITS, p.nc).total > kSmem) return cudaErrorInvalidConfiguration;
     switch (p.nc) {
         case 2: return launch_lora<BITS, 2>(maps, p, stream);

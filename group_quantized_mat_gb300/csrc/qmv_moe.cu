@@ -594,7 +594,7 @@ __global__ void __launch_bounds__(tile::kThreads, 1)
             run(acc, pipe, p.sba, p.cha, p.NSa, p.Ga, (long long)im.e * 2 * p.I + (row < kHalf ? 0 : p.I - kHalf) + im.tl * kHalf + row);
             constexpr int OWN = Row<BITS, GS, NC, 2>::kOwn;
             float sums[OWN];
-            acc.join(tm + lanes, group, sums);
+            acc.join(tm + lanes, group, 0, sums);
             // rows 64.. (up) hand theirs to rows 0.. (gate), which form h
 #pragma unroll
             for (int i = 0; i < OWN; ++i)
@@ -665,7 +665,7 @@ __global__ void __launch_bounds__(tile::kThreads, 1)
             run(acc, pb, p.sbb, p.chb, p.NSb, p.Gb, (long long)im.e * p.K + n);
             constexpr int OWN = Row<BITS, GS, NC, kTermsH>::kOwn;
             float sums[OWN];
-            acc.join(tm + lanes, group, sums);
+            acc.join(tm + lanes, group, 0, sums);
 #pragma unroll
             for (int i = 0; i < OWN; ++i) {
                 const int j = group + kGroups * i;

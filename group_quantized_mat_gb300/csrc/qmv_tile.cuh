@@ -37,9 +37,14 @@
 // exact there too, 40 for a subgroup) through tcgen05 25, 24 and 21; through
 // mma.sync, whose instruction holds the issue slot for 8 cycles, 27 and 19.
 //
-// Order. Slot i of a row's range of K belongs to worker group i % 3, which adds
-// its subgroups in order; the three groups' sums are added in order. Nothing
-// depends on how many vectors there are.
+// Order. Slots i, i + 3, .. of a row's range of K belong to one worker group,
+// which adds their subgroups in order; the three groups' sums are added in the
+// order of their first slots. Nothing depends on how many vectors there are.
+//
+// The ring has a multiple of three slots and slot s of it always goes to group
+// s % 3. A wait for a slot's next lap by its barrier's parity alone is right only
+// if the lap before has landed; here the waiting group itself has seen it land.
+// (With any number of slots a group could be a lap ahead of a copy that is late.)
 #pragma once
 
 #include "qmv_kernel.cuh"
@@ -107,6 +112,10 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
         : "memory");
 }
+
+// The first of a tile's slots that group `group` takes, `at` being the place in
+// the ring of the tile's first.
+__device__ __forceinline__ int first_slot(int group, int at) { return (group + kGroups - at % kGroups) % kGroups; }
 
 // A place in a ring of `slots`: index and parity of the lap, kept without divisions.
 struct Turn {
@@ -320,6 +329,11 @@ __device__ __forceinline__ uint64_t b_descriptor(uint32_t addr, uint32_t stride)
 {
     return uint64_t((addr >> 4) & 0x3fffu) | uint64_t(1) << 16 | uint64_t(stride >> 4) << 32 | uint64_t(1) << 46 |
            uint64_t(4) << 61;
+}
+
+__device__ __forceinline__ void mbar_arrive_many(uint32_t bar, uint32_t count)
+{
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(count) : "memory");
 }
 
 // An arrival on `bar` when the thread's earlier tensor instructions are done.
@@ -619,9 +633,10 @@ struct Row {
 
     // The three groups' sums of the tile's rows meet in tensor memory (each group
     // its own A columns, `tm` being the first with the warp's lanes): sums[i]
-    // becomes the total of vector group + 3 i, the groups' sums added in order.
+    // becomes the total of vector group + 3 i, added from group `first` on, which
+    // had the tile's first slot.
     static constexpr int kOwn = (NC + kGroups - 1) / kGroups;
-    __device__ __forceinline__ void join(uint32_t tm, int group, float (&sums)[kOwn])
+    __device__ __forceinline__ void join(uint32_t tm, int group, int first, float (&sums)[kOwn])
     {
 #pragma unroll
         for (int c = 0; c < NC / 2; ++c) {
@@ -638,7 +653,8 @@ struct Row {
 #pragma unroll
         for (int i = 0; i < kOwn; ++i)
 #pragma unroll
-            for (int g = 0; g < kGroups; ++g) v[i][g] = tmem_ld1(tm + g * a_columns(NC, TERMS) + min(group + kGroups * i, NC - 1));
+            for (int g = 0; g < kGroups; ++g)
+                v[i][g] = tmem_ld1(tm + (first + g) % kGroups * a_columns(NC, TERMS) + min(group + kGroups * i, NC - 1));
         tmem_wait_ld();
 #pragma unroll
         for (int i = 0; i < kOwn; ++i) {

@@ -152,3 +152,19 @@ def test_capture_in_a_graph():
         torch.cuda.synchronize()
         assert np.array_equal(want, y.float().cpu().numpy())
     assert g.qmv_device_error() == 0
+
+
+def test_few_ring_slots():
+    """The widest range of K with 16 vectors and the highest rank leaves room for
+    two slots of weights: a single vector's call, which has more, gives the same rows."""
+    pr = Problem(16, 17408, 4096, 4, 64, 2, 256, ids=[0, -1, 1, 1] * 4, seed=11)
+    full = pr.run(flags=g.F32_OUT)
+    assert np.isfinite(full).all()
+    for row in (0, 5, 15):
+        assert np.array_equal(pr.run([row], flags=g.F32_OUT)[0], full[row])
+
+
+@pytest.mark.parametrize("N,R", [(19, 3), (23, 1), (130, 27), (77, 254), (1201, 13), (8, 255)])
+def test_adapters_whose_rows_start_anywhere(N, R):
+    """Odd ranks and row counts: pieces of an adapter off 16-byte boundaries, and the array's last bytes."""
+    Problem(6, N, 320, 4, 64, 3, R, ids=[2, 0, 1, 2, -1, 0], seed=N + R).check()
