@@ -58,7 +58,7 @@ struct LoraParams {
     void *y;
     uint8_t *cells;      // [pass][subs][cell_bytes]
     uint8_t *meta;       // [pass][subs][meta_bytes]
-    float *inner;        // [M][R]
+    float *inner;        // [M][inner_pitch(R)]
     float *partials;     // [pass][nseg][nc][N], with nseg > 1
     unsigned *counters;  // [pass][tiles], with nseg > 1
     unsigned *err;
@@ -73,6 +73,9 @@ struct LoraParams {
     int nc, slots, stage_blocks, sb_buffers;
     tile::Affines sb;
 };
+
+// Floats from an inner vector to the next, so that all of a pass's are one bulk copy.
+__host__ __device__ constexpr int inner_pitch(int rank) { return (rank + 7) & ~7; }
 
 template <int BITS, int NC>
 __global__ void __launch_bounds__(kPrepareThreads) lora_prepare(const LoraParams p)
@@ -130,7 +133,7 @@ __global__ void __launch_bounds__(kPrepareThreads) lora_prepare(const LoraParams
     __syncthreads();
     if (tid == 0) {
         for (int j = 1; j < kPrepareThreads / 32; ++j) s = __fadd_rn(s, part[j]);
-        p.inner[size_t(m) * p.R + r] = s;
+        p.inner[size_t(m) * inner_pitch(p.R) + r] = s;
     }
 }
 
@@ -152,7 +155,7 @@ __host__ __device__ inline Layout layout(const LoraParams &p, int bits, int nc)
     l.meta = l.x + subs * tile::cell_bytes(nc);
     l.sb = (l.meta + subs * tile::meta_bytes(nc) + 127) & ~127;
     l.inner = l.sb + p.sb_buffers * 2 * p.sb.block;
-    l.bars = l.inner + nc * ((p.R + 7) & ~7) * 4;
+    l.bars = l.inner + nc * inner_pitch(p.R) * 4;
     l.total = l.bars + (2 * p.slots + 4 * tile::kGroups + 5) * 8;
     return l;
 }
@@ -167,7 +170,7 @@ __device__ __forceinline__ float adapter_dot(uint32_t addr, const float *v, int 
         // that neighbours' reads fall on different banks.
         const int C = R / 8;
         int c = (C >= 8 ? row : row * C >> 3) % C;
-#pragma unroll 2
+#pragma unroll 4
         for (int i = 0; i < C; ++i) {
             float x[8];
             tile::widen8(tile::lds_128(addr + c * 16), x);
@@ -229,7 +232,9 @@ __global__ void __launch_bounds__(tile::kThreads, 1) lora_project(const __grid_c
 {
     using namespace tile;
     extern __shared__ __align__(1024) uint8_t smem[];
-    __shared__ int s_abort, s_last, s_ad[kPass], s_which[kPass], s_ads;
+    __shared__ int s_abort, s_last, s_ad[kPass], s_ads;
+    __shared__ float s_c[kPass];
+    __shared__ uint32_t s_of[kPass];
     __shared__ uint32_t s_tmem;
     constexpr int SUBS = slot_subs(BITS);
     const Layout L = layout(p, BITS, NC);
@@ -242,16 +247,18 @@ __global__ void __launch_bounds__(tile::kThreads, 1) lora_project(const __grid_c
     const int g0 = lo * SUBS * 64 / GS, groups = min(ns * SUBS * 64 / GS, p.G - g0);
     if (warp == 2) {
         // This range's adapters among those of the pass's vectors, each once, in
-        // their order, and each vector's place among them (-1: none here). An
-        // adapter belongs to the range of its number modulo the ranges.
+        // their order, with the vectors that have it. An adapter belongs to the
+        // range of its number modulo the ranges.
         int ad = lane < nv ? __ldg(p.adapter + z * kPass + lane) : -1;
         if (ad < 0 || ad >= p.L || ad % p.nseg != seg) ad = -1;
         const uint32_t same = __match_any_sync(0xffffffffu, ad);
         const bool first = ad >= 0 && __ffs(same) - 1 == lane;
         const uint32_t firsts = __ballot_sync(0xffffffffu, first);
-        const int at = __shfl_sync(0xffffffffu, __popc(firsts & ((1u << lane) - 1u)), __ffs(same) - 1);
-        if (first) s_ad[at] = ad;
-        if (lane < kPass) s_which[lane] = ad >= 0 ? at : -1;
+        if (first) {
+            const int at = __popc(firsts & ((1u << lane) - 1u));
+            s_ad[at] = ad;
+            s_of[at] = same;
+        }
         if (lane == 0) s_ads = __popc(firsts);
     }
     if (tid == 0) {
@@ -279,15 +286,18 @@ __global__ void __launch_bounds__(tile::kThreads, 1) lora_project(const __grid_c
     const Waits wait{&s_abort, p.err};
     const int ads = s_ads, pieces = (p.rows + p.piece - 1) / p.piece;
 
-    // staged x by bulk copies, once the first kernel has ended
+    // staged x and inner vectors by bulk copies, once the first kernel has ended
     auto fetch_x = [&]() {
         grid_dependency_wait();
         asm volatile("fence.proxy.async;" ::: "memory");
         const uint32_t cb = uint32_t(ns) * SUBS * cell_bytes(NC), mb = uint32_t(ns) * SUBS * meta_bytes(NC);
-        mbar_arrive_expect_tx(xbar, cb + mb);
+        const uint32_t ib = uint32_t(nv) * inner_pitch(p.R) * 4;
+        mbar_arrive_expect_tx(xbar, cb + mb + ib);
         const size_t sub = size_t(z) * p.subs + size_t(lo) * SUBS;
         bulk_load_plain(base + L.x, p.cells + sub * cell_bytes(NC), cb, xbar);
         bulk_load_plain(base + L.meta, p.meta + sub * meta_bytes(NC), mb, xbar);
+        // (of vectors without an adapter: whatever is there)
+        bulk_load_plain(base + L.inner, p.inner + size_t(z) * kPass * inner_pitch(p.R), ib, xbar);
     };
 
     if (warp == kThreads / 32 - 1) {
@@ -367,9 +377,10 @@ __global__ void __launch_bounds__(tile::kThreads, 1) lora_project(const __grid_c
         Pipe pipe = Pipe::make<NC>(tm, lanes, stored0, ready0, group);
         const uint32_t wrow = base + row * kSlotBytes + ((row & 7) << 4);
         grid_launch_dependents();
-        wait(xbar, 0);
+        if (tid < ads) s_c[tid] = __ldg(p.c + s_ad[tid]);  // (the first tile's join publishes them)
+        bool landed = false;  // staged x
         int it = 0, tiles = 0;
-        const int align = p.sb.alignment(p.G), inner_pitch = (p.R + 7) & ~7;
+        const int align = p.sb.alignment(p.G);
         for (int tl = blockIdx.x; tl < p.tiles; tl += p.grid_rows, it += ns + ads * pieces, ++tiles) {
             const int n = tl * p.rows + row;
             const bool live = row < p.rows && n < p.N;
@@ -387,6 +398,10 @@ __global__ void __launch_bounds__(tile::kThreads, 1) lora_project(const __grid_c
                 Affine<BITS, GS> aff;
                 aff.read(sb + i * Affine<BITS, GS>::kGroupsPerSlot * 2, p.sb.block, align,
                          groups - i * Affine<BITS, GS>::kGroupsPerSlot);
+                if (!landed) {
+                    wait(xbar, 0);
+                    landed = true;
+                }
                 acc.slot(wait, pipe, wrow + s * L.slot, aff, meta, last, lane);
                 last = meta + (SUBS - 2 * step_subs(NC)) * meta_bytes(NC);
                 __syncwarp();
@@ -394,28 +409,26 @@ __global__ void __launch_bounds__(tile::kThreads, 1) lora_project(const __grid_c
             }
             if (lane == 0) mbar_arrive(sempty0 + 8 * buf);
             acc.finish(wait, pipe, last);
-            if (tiles == 0) {
-                // the inner vectors (of vectors without an adapter: whatever is there)
-                grid_dependency_wait();
-                for (int i = tid; i < nv * inner_pitch; i += 32 * kWorkers) {
-                    const int t = i / inner_pitch, r = i - t * inner_pitch;
-                    if (r < p.R) reinterpret_cast<float *>(smem + L.inner)[i] = __ldcg(p.inner + (size_t(z) * kPass + t) * p.R + r);
-                }
+            if (!landed) {  // (a group without slots needs the inner vectors)
+                wait(xbar, 0);
+                landed = true;
             }
             float sums[Row<BITS, GS, NC>::kOwn];
-            acc.join(tm + lanes, group, it % kGroups, sums);  // its barriers also publish the inner vectors
+            acc.join(tm + lanes, group, it % kGroups, sums);
             for (int j = 0, at = it + ns; j < ads * pieces; ++j, ++at) {
                 const int d = j / pieces, r0 = (j - d * pieces) * p.piece, s = at % p.slots;
                 wait(full0 + 8 * s, (at / p.slots) & 1);
                 if (live && row >= r0 && row < r0 + p.piece) {
                     const long long first = ((long long)s_ad[d] * p.N + n - (row - r0)) * p.R * 2;
                     const uint32_t addr = base + s * L.slot + (uint32_t(first) & 15u) + (row - r0) * p.R * 2;
-                    const float c = __ldg(p.c + s_ad[d]);
+                    // the group's vectors: every third
+#pragma unroll 1
+                    for (uint32_t of = s_of[d] & 0x9249u << group; of; of &= of - 1) {
+                        const int t = __ffs(of) - 1;
+                        const float v = __fmul_rn(s_c[d], adapter_dot(addr, reinterpret_cast<const float *>(smem + L.inner) + t * inner_pitch(p.R), p.R, row));
 #pragma unroll
-                    for (int i = 0; i < Row<BITS, GS, NC>::kOwn; ++i) {
-                        const int t = group + kGroups * i;
-                        if (t < nv && s_which[t] == d)
-                            sums[i] = __fadd_rn(sums[i], __fmul_rn(c, adapter_dot(addr, reinterpret_cast<const float *>(smem + L.inner) + t * inner_pitch, p.R, row)));
+                        for (int k = 0; k < Row<BITS, GS, NC>::kOwn; ++k)
+                            if (t == group + kGroups * k) sums[k] = __fadd_rn(sums[k], v);
                     }
                 }
                 __syncwarp();
@@ -430,13 +443,15 @@ __global__ void __launch_bounds__(tile::kThreads, 1) lora_project(const __grid_c
                     const int t = group + kGroups * i;
                     if (live && t < nv) __stcg(part + seg * seg_stride + t * plane, sums[i]);
                 }
-                __threadfence();
                 named_sync(1, 32 * kWorkers);
-                if (tid == 0) s_last = atomicAdd(p.counters + size_t(z) * p.tiles + tl, 1u) == unsigned(p.nseg - 1);
+                if (tid == 0) {
+                    __threadfence();  // (of what the barrier ordered before it, too)
+                    s_last = atomicAdd(p.counters + size_t(z) * p.tiles + tl, 1u) == unsigned(p.nseg - 1);
+                    __threadfence();
+                }
                 named_sync(1, 32 * kWorkers);
                 mine = s_last != 0;
                 if (mine) {
-                    __threadfence();
 #pragma unroll
                     for (int i = 0; i < Row<BITS, GS, NC>::kOwn; ++i) {
                         const int t = group + kGroups * i;
@@ -505,7 +520,7 @@ LoraParams plan(int M, int N, int K, int bits, int gs, int R, int sms, Sizes &sz
     const size_t passes = (M + kPass - 1) / kPass;
     sz.cells = up256(passes * p.subs * tile::cell_bytes(p.nc));
     sz.meta = up256(passes * p.subs * tile::meta_bytes(p.nc));
-    sz.inner = up256(size_t(M) * R * 4);
+    sz.inner = up256(size_t(M) * inner_pitch(R) * 4);
     sz.counters = p.nseg > 1 ? up256(passes * ((N + 7) / 8) * 4) : 0;
     sz.partials = p.nseg > 1 ? up256(passes * p.nseg * size_t(N) * p.nc * 4) : 0;
     sz.total = sz.cells + sz.meta + sz.inner + sz.counters + sz.partials;
