@@ -49,6 +49,7 @@ constexpr int kMaxK = 1 << 16;
 // vectors, its scales and biases and the inner vectors have to fit at 128 rows.
 __host__ __device__ constexpr int range_subs(int rank) { return rank <= 88 ? 64 : 48; }
 constexpr int kPass = 16;       // vectors that one read of the weights serves
+constexpr int kSms = 152;       // for orders of sums, which depend on no device
 constexpr int kBefore = 3;      // slots of weights asked for before staged x (no more than a ring has)
 
 struct LoraParams {
@@ -78,7 +79,7 @@ struct LoraParams {
 __host__ __device__ constexpr int inner_pitch(int rank) { return (rank + 7) & ~7; }
 
 template <int BITS, int NC>
-__global__ void __launch_bounds__(kPrepareThreads) lora_prepare(const LoraParams p)
+__global__ void __launch_bounds__(kPrepareThreads, 8) lora_prepare(const LoraParams p)
 {
     grid_dependency_wait();
     const int tid = threadIdx.x, passes = (p.M + kPass - 1) / kPass;
@@ -498,7 +499,12 @@ LoraParams plan(int M, int N, int K, int bits, int gs, int R, int sms, Sizes &sz
     p.S = K / 64;
     p.NS = (p.S + slot_subs - 1) / slot_subs;
     p.subs = p.NS * slot_subs;
+    // Ranges of K: as few as fit, and for few rows as many as give each SM of the
+    // card a tile of 128, of three slots at least (one for each worker group).
     p.nseg = (p.NS * slot_subs + range_subs(R) - 1) / range_subs(R);
+    int spread = kSms / ((N + tile::kTileRows - 1) / tile::kTileRows);
+    if (spread > p.NS / tile::kGroups) spread = p.NS / tile::kGroups;
+    if (p.nseg < spread) p.nseg = spread;
     p.range = (p.NS + p.nseg - 1) / p.nseg;
     p.nc = M <= 2 ? 2 : M <= 4 ? 4 : M <= 8 ? 8 : 16;
     // tiles of equal height: as many rounds of the grid as 128 rows need
