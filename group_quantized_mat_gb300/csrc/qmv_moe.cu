@@ -41,9 +41,23 @@ namespace {
 constexpr int kLogitThreads = 256;
 constexpr int kSmemMoe = 227 * 1024 - 1024;
 constexpr int kMaxSlotsMoe = 12;
+// Slots come in threes (see qmv_tile.cuh). Their subgroups' sums are in a ring of
+// their own that is three longer: a group needs those of a slot's last steps until
+// it is done with its next.
+constexpr int kMinSlotsMoe = tile::kGroups;
 constexpr int kHalf = 64;        // rows of a box: an item is two
-constexpr int kChunkGroups = 32; // groups of scales and biases that are fetched at a time
 constexpr int kTermsH = 4;
+constexpr int kSets = 5;         // items whose sums may be on their way
+// One warp brings the weights, four more what is multiplied with them (one warp for
+// all: a slot in 1250 cycles at 6 tokens to an entry, with one gathering warp 1100).
+// Registers move from those and the tensor warps to the workers: 640 x 96 =
+// 384 x 128 + 256 x 48.
+constexpr int kGatherers = 4;
+constexpr int kMoeThreads = tile::kThreads + 32 * kGatherers;
+constexpr int kWorkerRegs = 128, kOtherRegs = 48;
+static_assert(32 * tile::kWorkers * kWorkerRegs + (kMoeThreads - 32 * tile::kWorkers) * kOtherRegs <= kMoeThreads * 96, "registers");
+constexpr int kExchange = tile::kGroups * tile::kGroupColumns, kExchangeSet = tile::kGroups * 8;
+// columns of tensor memory for items' sums on their way to the warps that take them
 
 struct MoeParams {
     const uint16_t *x, *router, *gu_s, *gu_b, *dn_s, *dn_b;
@@ -57,10 +71,11 @@ struct MoeParams {
     float *partials;    // [pair][K]
     unsigned *counters; // CTAs done with A, and with B
     unsigned *err;
-    int M, K, I, E, k, gs, f32_out, gelu, softmax_all;
+    int M, K, I, E, k, gs, nc, f32_out, gelu, softmax_all;
     int Sa, NSa, Ga, Sb, NSb, Gb;  // subgroups, slots and groups of a row of A and of B
-    int tiles_a, tiles_b, words, max_entries, slots, stage_blocks;
+    int tiles_a, tiles_b, max_entries, slots, stage_blocks;
     tile::Affines sba, sbb;
+    int chunk;     // groups of scales and biases that are fetched at a time
     int cha, chb;  // slots whose scales and biases are fetched at a time
     int sb_block;
 };
@@ -124,23 +139,23 @@ __global__ void __launch_bounds__(kLogitThreads) moe_logits(const MoeParams p)
 }
 
 struct MoeLayout {
-    int slot, cells, meta, sb, xs, lists, total;
+    int slot, cells, meta, sb, cell, red, lists, total;
     // within lists
-    int w, ids, pos, tok, base, entry, mask, bars;
+    int w, ids, pos, tok, base, entry, bars;
 };
 
-template <int BITS, int NC>
-__host__ __device__ inline MoeLayout moe_layout(const MoeParams &p)
+__host__ __device__ inline MoeLayout moe_layout(const MoeParams &p, int bits, int nc)
 {
-    constexpr int SUBS = tile::slot_subs(BITS), CB = tile::cell_bytes(NC, kTermsH);
+    const int SUBS = tile::slot_subs(bits), CB = tile::cell_bytes(nc, kTermsH);
     const int pairs = p.M * p.k;
     MoeLayout l;
     l.cells = tile::kTileRows * tile::kSlotBytes;
-    l.meta = l.cells + SUBS * CB;
-    l.slot = (l.meta + SUBS * tile::meta_bytes(NC) + 1023) & ~1023;
-    l.sb = p.slots * l.slot;
-    l.xs = l.sb + 2 * 2 * p.sb_block;
-    l.lists = l.xs + NC * kHalf * 4 + tile::kGroups * 16;
+    l.slot = (l.cells + SUBS * CB + 1023) & ~1023;
+    l.meta = p.slots * l.slot;
+    l.sb = (l.meta + (p.slots + tile::kGroups) * SUBS * tile::meta_bytes(nc) + 127) & ~127;
+    l.cell = (l.sb + 2 * 2 * p.sb_block + 15) & ~15;
+    l.red = l.cell + CB + tile::meta_bytes(nc);
+    l.lists = l.red + 4 * nc * 8;
     l.w = l.lists;
     l.ids = l.w + pairs * 4;
     l.pos = l.ids + ((pairs * 2 + 3) & ~3);
@@ -148,9 +163,7 @@ __host__ __device__ inline MoeLayout moe_layout(const MoeParams &p)
     l.base = l.tok + ((pairs * 2 + 3) & ~3);
     l.entry = l.base + (p.E + 1) * 4;
     l.bars = (l.entry + p.max_entries * 4 + 7) & ~7;
-    // scratch of the routing, in the ring: a row of logits for each warp, the masks
-    l.mask = tile::kThreads / 32 * p.E * 4;
-    l.total = l.bars + (2 * p.slots + 4 * tile::kGroups + 4) * 8;
+    l.total = l.bars + (2 * p.slots + 4 * tile::kGroups + 4 + 2 * kSets) * 8;
     return l;
 }
 
@@ -164,7 +177,7 @@ __device__ __forceinline__ uint32_t order_of(float v)
 // The expert choice of token t by one warp, whose lane holds every 32nd logit:
 // N of them in registers, or for more than 32 N experts in shared memory (l).
 template <int N>
-__device__ __forceinline__ void choose(const MoeParams &p, int t, uint32_t *l, float *w, uint16_t *ids, uint32_t *mask, int lane)
+__device__ __forceinline__ void choose(const MoeParams &p, int t, uint32_t *l, float *w, uint16_t *ids, int lane)
 {
     uint32_t key[N];
     const float *logits = p.logits + size_t(t) * p.E;
@@ -210,10 +223,7 @@ __device__ __forceinline__ void choose(const MoeParams &p, int t, uint32_t *l, f
         for (int i = 0; i < N; ++i)
             if (!many && arg == uint32_t(i * 32 + lane)) key[i] = 0u;
         if (many && lane == int(arg % 32)) l[arg] = 0u;
-        if (lane == 0) {
-            ids[t * p.k + j] = uint16_t(arg);
-            atomicOr(mask + arg * p.words + t / 32, 1u << (t & 31));
-        }
+        if (lane == 0) ids[t * p.k + j] = uint16_t(arg);
     }
     if (lane < p.k) w[t * p.k + lane] = __fdiv_rn(mine, sum);
 }
@@ -228,7 +238,7 @@ __device__ __forceinline__ float activation(float g, bool gelu)
 }
 
 template <int BITS, int GS, int NC>
-__global__ void __launch_bounds__(tile::kThreads, 1)
+__global__ void __launch_bounds__(kMoeThreads, 1)
     moe_experts(const __grid_constant__ CUtensorMap wa, const __grid_constant__ CUtensorMap sa,
                 const __grid_constant__ CUtensorMap ba, const __grid_constant__ CUtensorMap wb,
                 const __grid_constant__ CUtensorMap sbm, const __grid_constant__ CUtensorMap bb, const MoeParams p)
@@ -238,21 +248,21 @@ __global__ void __launch_bounds__(tile::kThreads, 1)
     __shared__ int s_abort, s_entries;
     __shared__ uint32_t s_tmem;
     constexpr int SUBS = slot_subs(BITS), CA = cell_bytes(NC, 2), CB = cell_bytes(NC, kTermsH), MB = meta_bytes(NC);
-    const MoeLayout L = moe_layout<BITS, NC>(p);
+    const MoeLayout L = moe_layout(p, BITS, NC);
     const uint32_t base = smem_u32(smem), full0 = base + L.bars, empty0 = full0 + 8 * p.slots;
     const uint32_t stored0 = empty0 + 8 * p.slots, ready0 = stored0 + 16 * kGroups, sfull0 = ready0 + 16 * kGroups;
-    const uint32_t sempty0 = sfull0 + 16;
+    const uint32_t sempty0 = sfull0 + 16, joined0 = sempty0 + 16, freed0 = joined0 + 8 * kSets;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, grid = gridDim.x;
     float *s_w = reinterpret_cast<float *>(smem + L.w);
     uint16_t *s_ids = reinterpret_cast<uint16_t *>(smem + L.ids), *s_pos = reinterpret_cast<uint16_t *>(smem + L.pos);
     uint16_t *s_tok = reinterpret_cast<uint16_t *>(smem + L.tok);
     int *s_base = reinterpret_cast<int *>(smem + L.base);
-    uint32_t *s_entry = reinterpret_cast<uint32_t *>(smem + L.entry), *s_mask = reinterpret_cast<uint32_t *>(smem + L.mask);
+    uint32_t *s_entry = reinterpret_cast<uint32_t *>(smem + L.entry);
 
     if (tid == 0) {
         for (int i = 0; i < p.slots; ++i) {
-            mbar_init(full0 + 8 * i, 1 + 32);
-            mbar_init(empty0 + 8 * i, 4);
+            mbar_init(full0 + 8 * i, 1 + 32 * kGatherers);
+            mbar_init(empty0 + 8 * i, 4 + 1);  // the group's warps, and its cells read
         }
         for (int i = 0; i < 2 * kGroups; ++i) {
             mbar_init(stored0 + 8 * i, 4);
@@ -262,29 +272,45 @@ __global__ void __launch_bounds__(tile::kThreads, 1)
             mbar_init(sfull0 + 8 * i, 2 * 32);
             mbar_init(sempty0 + 8 * i, kWorkers);
         }
+        for (int i = 0; i < kSets; ++i) {
+            mbar_init(joined0 + 8 * i, kWorkers);
+            mbar_init(freed0 + 8 * i, 4);
+        }
         fence_mbar_init();
         s_abort = 0;
     }
     if (warp == kWorkers) tmem_alloc(smem_u32(&s_tmem), kTmemColumns);
-    for (int i = tid; i < p.E * p.words; i += kThreads) s_mask[i] = 0u;
+    for (int i = tid; i < p.E; i += kMoeThreads) s_base[i] = 0;
     grid_dependency_wait();
     __syncthreads();
 
     // ------------------------------------------------------------- routing
-    for (int t = warp; t < p.M; t += kThreads / 32)
-        choose<4>(p, t, reinterpret_cast<uint32_t *>(smem) + warp * p.E, s_w, s_ids, s_mask, lane);
+    for (int t = warp; t < p.M; t += kMoeThreads / 32)
+        // (a row of logits for each warp in the ring)
+        choose<4>(p, t, reinterpret_cast<uint32_t *>(smem) + warp * p.E, s_w, s_ids, lane);
     __syncthreads();
     if (warp == 0) {
-        // each lane a run of experts: tokens and entries before it
-        const int run = (p.E + 31) / 32, e0 = min(lane * run, p.E), e1 = min(e0 + run, p.E);
-        int pairs = 0, entries = 0;
-        for (int e = e0; e < e1; ++e) {
-            int n = 0;
-            for (int i = 0; i < p.words; ++i) n += __popc(s_mask[e * p.words + i]);
-            pairs += n;
-            entries += (n + NC - 1) / NC;
+        // each choice's place among its expert's, in the order of the tokens
+        const int pairs = p.M * p.k;
+        for (int i0 = 0; i0 < pairs; i0 += 32) {
+            const int i = i0 + lane, e = i < pairs ? s_ids[i] : -1 - lane;
+            const uint32_t same = __match_any_sync(0xffffffffu, e), before = same & ((1u << lane) - 1u);
+            const int n = e >= 0 ? s_base[e] : 0;
+            __syncwarp();
+            if (e >= 0) {
+                s_pos[i] = uint16_t(n + __popc(before));
+                if (!before) s_base[e] = n + __popc(same);
+            }
+            __syncwarp();
         }
-        int pb = pairs, eb = entries;
+        // each lane a run of experts: choices and entries before it
+        const int run = (p.E + 31) / 32, e0 = min(lane * run, p.E), e1 = min(e0 + run, p.E);
+        int choices = 0, entries = 0;
+        for (int e = e0; e < e1; ++e) {
+            choices += s_base[e];
+            entries += (s_base[e] + NC - 1) / NC;
+        }
+        int pb = choices, eb = entries;
 #pragma unroll
         for (int d = 1; d < 32; d *= 2) {
             const int a = __shfl_up_sync(0xffffffffu, pb, d), b = __shfl_up_sync(0xffffffffu, eb, d);
@@ -297,23 +323,20 @@ __global__ void __launch_bounds__(tile::kThreads, 1)
             s_entries = eb;
             s_base[p.E] = pb;
         }
-        pb -= pairs;
+        pb -= choices;
         eb -= entries;
         for (int e = e0; e < e1; ++e) {
-            int n = 0;
-            for (int i = 0; i < p.words; ++i) n += __popc(s_mask[e * p.words + i]);
+            const int n = s_base[e];
             s_base[e] = pb;
             for (int f = 0; f < n; f += NC) s_entry[eb++] = uint32_t(e) | uint32_t(f) << 16;
             pb += n;
         }
     }
     __syncthreads();
-    for (int i = tid; i < p.M * p.k; i += kThreads) {
-        const int t = i / p.k, e = s_ids[i];
-        int before = __popc(s_mask[e * p.words + t / 32] & ((1u << (t & 31)) - 1u));
-        for (int j = 0; j < t / 32; ++j) before += __popc(s_mask[e * p.words + j]);
-        s_pos[i] = uint16_t(s_base[e] + before);
-        s_tok[s_base[e] + before] = uint16_t(t);
+    for (int i = tid; i < p.M * p.k; i += kMoeThreads) {
+        const int e = s_ids[i], at = s_base[e] + s_pos[i];
+        s_pos[i] = uint16_t(at);
+        s_tok[at] = uint16_t(i / p.k);
         if (blockIdx.x == 0 && p.ids_out) p.ids_out[i] = e;
         if (blockIdx.x == 0 && p.weights_out) p.weights_out[i] = s_w[i];
     }
@@ -360,12 +383,12 @@ __global__ void __launch_bounds__(tile::kThreads, 1)
         return it;
     };
 
-    // Waits until all CTAs are done with a part: bounded like every wait.
-    auto meet = [&](const unsigned *counter) {
+    // Waits for a count that other CTAs raise: bounded like every wait.
+    auto meet = [&](const unsigned *counter, int count) {
         for (int i = 0; i < (1 << 21); ++i) {
             unsigned v;
             asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(counter) : "memory");
-            if (v >= unsigned(grid)) return true;
+            if (v >= unsigned(count)) return true;
             if ((i & 63) == 63 && *wait.abort) return false;
         }
         atomicOr(p.err, 1u);
@@ -373,260 +396,178 @@ __global__ void __launch_bounds__(tile::kThreads, 1)
         return false;
     };
 
-    if (warp == kThreads / 32 - 1) {
-        // ---------------------------------------------------------- producer
-        int chunk = 0;
-        Turn turn;
-        bool ok = true;
-        // scales and biases of an item's rows from slot i on: of A the rows r0 of
-        // gate and up, of B 128 rows from r0 (`rows` of them the expert's)
-        auto fetch = [&](bool part_a, const Affines &a, const uint16_t *sc, const uint16_t *bi, const CUtensorMap *sm,
-                         const CUtensorMap *bm, int e, int row, int rows, int G, int i) {
-            const int buf = chunk & 1, round = chunk >> 1;
-            ok = __all_sync(0xffffffffu, round == 0 || wait(sempty0 + 8 * buf, (round - 1) & 1));
-            if (!ok) return;
-            const int g0 = i * SUBS * 64 / GS, groups = min(kChunkGroups, G - g0);  // (of kSbRows)
-            const int off = L.sb + buf * 2 * p.sb_block;
-            const uint32_t bar = sfull0 + 8 * buf;
-            ++chunk;
-            if (a.mode == kSbBoxes) {
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(bar, uint32_t(2 * kTileRows * a.pitch));
-                    if (part_a) {
-                        tma_load_3d(base + off, sm, g0 / 8 * 2, row, 2 * e, bar);
-                        tma_load_3d(base + off + p.sb_block, bm, g0 / 8 * 2, row, 2 * e, bar);
+    // after a wait that ran out: copies in flight end before the CTA does; none is
+    // longer on its way than this
+    auto drain = [&]() {
+        const uint64_t t0 = global_timer_ns();
+        while (global_timer_ns() - t0 < 1000000ull) {}
+    };
+
+    if (warp >= kWorkers) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+        if (warp == kWorkers + kGroups) {
+            // -------------------------------------- the weights' side of the slots
+            int chunk = 0;
+            Turn turn;
+            bool ok = true;
+            // scales and biases of an item's rows from slot i on: of A the rows r0 of
+            // gate and up, of B 128 rows from r0 (`rows` of them the expert's)
+            auto fetch = [&](bool part_a, const Affines &a, const uint16_t *sc, const uint16_t *bi, const CUtensorMap *sm,
+                             const CUtensorMap *bm, int e, int row, int rows, int G, int i) {
+                const int buf = chunk & 1, round = chunk >> 1;
+                ok = __all_sync(0xffffffffu, round == 0 || wait(sempty0 + 8 * buf, (round - 1) & 1));
+                if (!ok) return;
+                const int g0 = i * SUBS * 64 / GS, groups = min(p.chunk, G - g0);  // (of kSbRows)
+                const int off = L.sb + buf * 2 * p.sb_block;
+                const uint32_t bar = sfull0 + 8 * buf;
+                ++chunk;
+                if (a.mode == kSbBoxes) {
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(bar, uint32_t(2 * kTileRows * a.pitch));
+                        if (part_a) {
+                            tma_load_3d(base + off, sm, g0 / 8 * 2, row, 2 * e, bar);
+                            tma_load_3d(base + off + p.sb_block, bm, g0 / 8 * 2, row, 2 * e, bar);
+                        } else {
+                            tma_load_2d(base + off, sm, g0 / 8 * 2, e * p.K + row, bar);
+                            tma_load_2d(base + off + p.sb_block, bm, g0 / 8 * 2, e * p.K + row, bar);
+                        }
                     } else {
-                        tma_load_2d(base + off, sm, g0 / 8 * 2, e * p.K + row, bar);
-                        tma_load_2d(base + off + p.sb_block, bm, g0 / 8 * 2, e * p.K + row, bar);
+                        mbar_arrive(bar);
                     }
-                } else {
                     mbar_arrive(bar);
+                    return;
                 }
-                mbar_arrive(bar);
-                return;
+                Affines b = a;
+                b.block = p.sb_block;
+                const long long r0 = part_a ? (long long)e * 2 * p.I + row : (long long)e * p.K + row, r1 = r0 + (part_a ? p.I : kHalf);
+                const long long all = part_a ? (long long)p.E * 2 * p.I : (long long)p.E * p.K;
+                b.fetch(base + off, smem + off, sc, bi, sm, bm, r0, kHalf, all, G, g0, groups, bar, lane);
+                if (rows > kHalf) b.fetch(base + off + kHalf * a.pitch, smem + off + kHalf * a.pitch, sc, bi, sm, bm, r1, kHalf, all, G, g0, groups, bar, lane);
+                else mbar_arrive(bar);
+            };
+            for (Items is = items_of(p.tiles_a); is.entry < is.entries && ok; advance(is)) {
+                const Item im = item_of(is);
+                int left = 0;  // slots until the next scales and biases
+                for (int i = 0; i < p.NSa && ok; ++i, --left, turn.step(1, p.slots)) {
+                    if (left == 0) {
+                        left = p.cha;
+                        fetch(true, p.sba, p.gu_s, p.gu_b, &sa, &ba, im.e, im.tl * kHalf, kTileRows, p.Ga, i);
+                    }
+                    if (ok && lane == 0) {
+                        ok = turn.lap == 0 || wait(empty0 + 8 * turn.slot, (turn.lap - 1) & 1);
+                        const uint32_t full = full0 + 8 * turn.slot;
+                        if (ok) {
+                            mbar_arrive_expect_tx(full, kTileRows * kSlotBytes);
+                            tma_load_3d(base + turn.slot * L.slot, &wa, i * (kSlotBytes / 8), im.tl * kHalf, 2 * im.e, full);
+                        }
+                    }
+                    ok = __all_sync(0xffffffffu, ok);
+                }
             }
-            Affines b = a;
-            b.block = p.sb_block;
-            const long long r0 = part_a ? (long long)e * 2 * p.I + row : (long long)e * p.K + row, r1 = r0 + (part_a ? p.I : kHalf);
-            const long long all = part_a ? (long long)p.E * 2 * p.I : (long long)p.E * p.K;
-            b.fetch(base + off, smem + off, sc, bi, sm, bm, r0, kHalf, all, G, g0, groups, bar, lane);
-            if (rows > kHalf) b.fetch(base + off + kHalf * a.pitch, smem + off + kHalf * a.pitch, sc, bi, sm, bm, r1, kHalf, all, G, g0, groups, bar, lane);
-            else mbar_arrive(bar);
-        };
-        // the lane's 16 bytes of each token's: subgroup, term and piece
-        const int gsub = lane >> 3, gh = lane >> 2 & 1, gpc = lane & 3;
-        const int msub = lane / 2 % SUBS, mf = lane & 1, mtok = lane / (2 * SUBS);
-        for (Items is = items_of(p.tiles_a); is.entry < is.entries && ok; advance(is)) {
-            const Item im = item_of(is);
-            // where each token's bytes come from, slot by slot
-            const uint8_t *from[NC];
-            const float *mfrom[(NC * SUBS + 15) / 16];
-#pragma unroll
-            for (int j = 0; j < NC; ++j)
-                from[j] = p.rows + size_t(s_tok[im.pair + min(j, im.count - 1)]) * p.NSa * (SUBS * 128) + lane * 16;
-#pragma unroll
-            for (int j = 0; j < (NC * SUBS + 15) / 16; ++j)
-                mfrom[j] = reinterpret_cast<const float *>(
-                               p.xmeta + size_t(s_tok[im.pair + min(j * (16 / SUBS) + mtok, im.count - 1)]) * p.NSa * SUBS + msub) + mf;
-            int left = 0;  // slots until the next scales and biases
-            for (int i = 0; i < p.NSa && ok; ++i, --left) {
-                if (left == 0) {
-                    left = p.cha;
-                    fetch(true, p.sba, p.gu_s, p.gu_b, &sa, &ba, im.e, im.tl * kHalf, kTileRows, p.Ga, i);
-                }
-                if (!ok) break;
-                ok = turn.lap == 0 || wait(empty0 + 8 * turn.slot, (turn.lap - 1) & 1);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-                const uint32_t full = full0 + 8 * turn.slot, dst = base + turn.slot * L.slot;
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(full, kTileRows * kSlotBytes);
-                    tma_load_3d(dst, &wa, i * (kSlotBytes / 8), im.tl * kHalf, 2 * im.e, full);
-                }
-                // the tokens' operand bytes, 512 a time, and their sums
-#pragma unroll
-                for (int j = 0; j < NC; ++j) {
-                    if (j >= im.count) break;
-                    const uint32_t d = dst + L.cells + gsub * CA + operand_offset(operand_index(j, gh), gpc);
-#pragma unroll
-                    for (int s = 0; s < SUBS / 4; ++s)
-                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d + s * 4 * CA), "l"(from[j] + s * 512) : "memory");
-                    from[j] += SUBS * 128;
-                }
-#pragma unroll
-                for (int j = 0; j < (NC * SUBS + 15) / 16; ++j) {
-                    const int tk = j * (16 / SUBS) + mtok;
-                    if (tk < im.count)
-                        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst + L.meta + msub * MB + (tk >> 1) * 16 + (tk & 1) * 4 + mf * 8),
-                                     "l"(mfrom[j])
-                                     : "memory");
-                    mfrom[j] += SUBS * 2;
-                }
-                asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(full) : "memory");
-                turn.step(1, p.slots);
-            }
-        }
-        // B: weights of the first slots before the meeting (as many as are free and
-        // as the two buffers of scales serve), h after it
-        int ahead = 0;
-        const Turn turn0 = turn;
-        auto b_slots = [&](int first, bool weights, bool cells, int most) {
-            int n = 0;
-            Turn at = turn0;
             for (Items is = items_of(p.tiles_b); is.entry < is.entries && ok; advance(is)) {
                 const Item im = item_of(is);
                 const int row = im.tl * kTileRows;
-                const uint8_t *h = p.h + size_t(im.entry) * p.NSb * (SUBS * (CB + MB));
                 int left = 0;
-                for (int i = 0; i < p.NSb && ok; ++i, ++n, --left, h += SUBS * (CB + MB), at.step(1, p.slots)) {
-                    if (n >= most) return n;
-                    const bool fetched = left == 0;
-                    if (fetched) left = p.chb;
-                    if (n < first) continue;
-                    const uint32_t full = full0 + 8 * at.slot, dst = base + at.slot * L.slot;
-                    if (weights) {
-                        if (fetched) fetch(false, p.sbb, p.dn_s, p.dn_b, &sbm, &bb, im.e, row, min(p.K - row, kTileRows), p.Gb, i);
-                        if (!ok) break;
-                        ok = at.lap == 0 || wait(empty0 + 8 * at.slot, (at.lap - 1) & 1);
-                        ok = __all_sync(0xffffffffu, ok);
-                        if (!ok) break;
-                        if (lane == 0) {
-                            mbar_arrive_expect_tx(full, kTileRows * kSlotBytes + SUBS * (CB + MB));
-                            tma_load_2d(dst, &wb, i * (kSlotBytes / 8), im.e * p.K + row, full);
-                            // for the lanes that arrive of their own in A
-                            asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], 32;" ::"r"(full) : "memory");
+                for (int i = 0; i < p.NSb && ok; ++i, --left, turn.step(1, p.slots)) {
+                    if (left == 0) {
+                        left = p.chb;
+                        fetch(false, p.sbb, p.dn_s, p.dn_b, &sbm, &bb, im.e, row, min(p.K - row, kTileRows), p.Gb, i);
+                    }
+                    if (ok && lane == 0) {
+                        ok = turn.lap == 0 || wait(empty0 + 8 * turn.slot, (turn.lap - 1) & 1);
+                        const uint32_t full = full0 + 8 * turn.slot;
+                        if (ok) {
+                            mbar_arrive_expect_tx(full, kTileRows * kSlotBytes);
+                            tma_load_2d(base + turn.slot * L.slot, &wb, i * (kSlotBytes / 8), im.e * p.K + row, full);
                         }
                     }
-                    if (cells && lane == 0) bulk_load_plain(dst + L.cells, h, SUBS * (CB + MB), full);
+                    ok = __all_sync(0xffffffffu, ok);
                 }
             }
-            return n;
-        };
-        if (ok) ahead = b_slots(0, true, false, min(p.slots, p.chb >= p.NSb ? 2 * p.NSb : min(2 * p.chb, p.NSb)));
-        if (ok && lane == 0) {
-            ok = meet(p.counters);
-            asm volatile("fence.proxy.async;" ::: "memory");
-        }
-        ok = __all_sync(0xffffffffu, ok);
-        if (ok) {
-            (void)b_slots(0, false, true, ahead);
-            (void)b_slots(ahead, true, true, 0x7fffffff);
-        }
-        asm volatile("cp.async.wait_all;" ::: "memory");
-        if (!ok && lane == 0) {
-            // copies in flight end before the CTA does; none is longer on its way than this
-            const uint64_t t0 = global_timer_ns();
-            while (global_timer_ns() - t0 < 1000000ull) {}
-        }
-    } else if (warp >= kWorkers) {
-        // ------------------------------------------------------ tensor warps
-        const int group = warp - kWorkers;
-        if (lane == 0) {
-            // turn: of the item's first slot
-            Turn turn;
-            Pipe pipe = Pipe::make<NC, 2>(tm, 0, stored0, ready0, group);
-            for (Items is = items_of(p.tiles_a); is.entry < is.entries; advance(is), turn.step(p.NSa, p.slots)) {
-                Turn at = turn;
-                at.step(group, p.slots);
-                for (int i = group; i < p.NSa; i += kGroups, at.step(kGroups, p.slots))
-                    multiply_slot<BITS, NC, 2, true>(wait, pipe, base + at.slot * L.slot + L.cells);
-            }
-            Pipe pb = Pipe::make<NC, kTermsH>(tm, 0, stored0, ready0, group);
-            pb.steps = pipe.steps;
-            for (Items is = items_of(p.tiles_b); is.entry < is.entries; advance(is), turn.step(p.NSb, p.slots)) {
-                Turn at = turn;
-                at.step(group, p.slots);
-                for (int i = group; i < p.NSb; i += kGroups, at.step(kGroups, p.slots))
-                    multiply_slot<BITS, NC, kTermsH>(wait, pb, base + at.slot * L.slot + L.cells);
-            }
-        }
-    } else {
-        // ----------------------------------------------------------- workers
-        const int group = warp / 4, row = (warp & 3) * 32 + lane;
-        const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
-        const uint32_t wrow = base + row * kSlotBytes + ((row & 7) << 4);
-        Turn turn;  // of the item's first slot
-        int chunk = 0;
-        uint32_t held = 0;  // the barrier of the slot whose last steps are still to be taken
-        // all slots of an item's rows into acc
-        auto run = [&](auto &acc, Pipe &pipe, const Affines &a, int ch, int NS, int G, long long grow) {
-            const int align = a.alignment(G);
-            constexpr int STEP = std::remove_reference_t<decltype(acc)>::kStep;
-            uint32_t last = 0;
-            held = 0;
-            acc.start();
-            Turn at = turn;
-            at.step(group, p.slots);
-            for (int c0 = 0; c0 < NS; c0 += ch, ++chunk) {
-                const int buf = chunk & 1, c1 = min(c0 + ch, NS), g0 = c0 * SUBS * 64 / GS;
-                wait(sfull0 + 8 * buf, (chunk >> 1) & 1);
-                const uint32_t sb = base + L.sb + buf * 2 * p.sb_block + row * a.pitch + a.offset(grow, G, g0);
-#pragma unroll 1
-                for (int i = c0 + (group + kGroups - c0 % kGroups) % kGroups; i < c1; i += kGroups, at.step(kGroups, p.slots)) {
-                    const int s = at.slot;
-                    wait(full0 + 8 * s, at.lap & 1);
-                    Affine<BITS, GS> aff;
-                    constexpr int GP = Affine<BITS, GS>::kGroupsPerSlot;
-                    aff.read(sb + (i - c0) * GP * 2, p.sb_block, align, G - i * GP);
-                    const uint32_t meta = base + s * L.slot + L.meta;
-                    acc.slot(wait, pipe, wrow + s * L.slot, aff, meta, last, lane);
-                    last = meta + (SUBS - 2 * STEP) * MB;
-                    __syncwarp();
-                    if (lane == 0) {
-                        if (held) mbar_arrive(held);
+            if (!ok && lane == 0) drain();
+        } else if (warp > kWorkers + kGroups) {
+            // ------------ the vectors' side of the slots, and what comes of the items' sums
+            Turn turn, mturn, set;
+            bool ok = true;
+            const int which = warp - kWorkers - kGroups - 1, row = which * 32 + lane;
+            const uint32_t ex0 = tm + (uint32_t(which * 32) << 16) + kExchange;
+            constexpr int MINE = (NC + kGatherers - 1) / kGatherers;
+            // the lane's 16 bytes of each token's: subgroup, term and piece
+            const int gsub = lane >> 3, gh = lane >> 2 & 1, gpc = lane & 3;
+            // and the token, subgroup and half of its sums
+            const int msub = lane / 2 % SUBS, mf = lane & 1, mtok = which * (16 / SUBS) + lane / (2 * SUBS);
+            auto gather = [&](const Items &is) {
+                const Item im = item_of(is);
+                // where each token's bytes come from, slot by slot
+                const uint8_t *from[MINE];
+                const float *mfrom;
+#pragma unroll
+                for (int j = 0; j < MINE; ++j)
+                    from[j] = p.rows + size_t(s_tok[im.pair + min(which + j * kGatherers, im.count - 1)]) * p.NSa * (SUBS * 128) + lane * 16;
+                mfrom = reinterpret_cast<const float *>(p.xmeta + size_t(s_tok[im.pair + min(mtok, im.count - 1)]) * p.NSa * SUBS + msub) + mf;
+                for (int i = 0; i < p.NSa; ++i, turn.step(1, p.slots), mturn.step(1, p.slots + kGroups)) {
+                    ok = ok && (turn.lap == 0 || wait(empty0 + 8 * turn.slot, (turn.lap - 1) & 1));
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    const uint32_t full = full0 + 8 * turn.slot, dst = base + turn.slot * L.slot;
+                    const uint32_t sums = base + L.meta + mturn.slot * (SUBS * MB);
+                    // the tokens' operand bytes, 512 a time, and their sums
+#pragma unroll
+                    for (int j = 0; j < MINE; ++j) {
+                        const int tk = which + j * kGatherers;
+                        if (tk >= im.count) break;
+                        const uint32_t d = dst + L.cells + gsub * CA + operand_offset(operand_index(tk, gh), gpc);
+#pragma unroll
+                        for (int s = 0; s < SUBS / 4; ++s)
+                            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d + s * 4 * CA), "l"(from[j] + s * 512) : "memory");
+                        from[j] += SUBS * 128;
                     }
-                    held = empty0 + 8 * s;
+                    if (mtok < im.count)
+                        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(sums + msub * MB + (mtok >> 1) * 16 + (mtok & 1) * 4 + mf * 8),
+                                     "l"(mfrom)
+                                     : "memory");
+                    mfrom += SUBS * 2;
+                    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(full) : "memory");
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(sempty0 + 8 * buf);
-            }
-            acc.finish(wait, pipe, last);
-            __syncwarp();
-            if (lane == 0 && held) mbar_arrive(held);
-            turn.step(NS, p.slots);
-        };
-
-        Pipe pipe = Pipe::make<NC, 2>(tm, lanes, stored0, ready0, group);
-        float *xs = reinterpret_cast<float *>(smem + L.xs), *red = xs + NC * kHalf + group * 4;
-        for (Items is = items_of(p.tiles_a); is.entry < is.entries; advance(is)) {
-            const Item im = item_of(is);
-            Row<BITS, GS, NC, 2> acc;
-            run(acc, pipe, p.sba, p.cha, p.NSa, p.Ga, (long long)im.e * 2 * p.I + (row < kHalf ? 0 : p.I - kHalf) + im.tl * kHalf + row);
-            constexpr int OWN = Row<BITS, GS, NC, 2>::kOwn;
-            float sums[OWN];
-            acc.join(tm + lanes, group, 0, sums);
-            // rows 64.. (up) hand theirs to rows 0.. (gate), which form h
+            };
+            uint8_t *own = smem + L.cell;  // an item's cell of h and its sums
+            float2 *red = reinterpret_cast<float2 *>(smem + L.red);
+            const int half = lane >> 4, r = which * 16 + (lane & 15);  // as in the workers
+            auto form_h = [&](const Items &is) {
+                const Item im = item_of(is);
+                float sums[NC];
+                Row<BITS, GS, NC, 2>::take(wait, ex0 + set.slot * kExchangeSet, joined0 + 8 * set.slot, freed0 + 8 * set.slot, set.lap, lane, sums);
+                set.step(1, kSets);
+                if (row == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the last item's h has left
+                // lanes of gate rows form h of the even tokens, those of up rows of the odd
+                float h[NC / 2];
 #pragma unroll
-            for (int i = 0; i < OWN; ++i)
-                if (row >= kHalf && group + kGroups * i < NC) xs[(group + kGroups * i) * kHalf + row - kHalf] = sums[i];
-            named_sync(2 + group, 128);
-            uint8_t *slot_h = p.h + (size_t(im.entry) * p.NSb + im.tl / SUBS) * (SUBS * (CB + MB));
-            uint8_t *cell = slot_h + im.tl % SUBS * CB, *meta = slot_h + SUBS * CB + im.tl % SUBS * MB;
-            if (row < kHalf) {
+                for (int i = 0; i < NC / 2; ++i) {
+                    const float mine = half ? sums[2 * i + 1] : sums[2 * i];
+                    const float other = __shfl_xor_sync(0xffffffffu, half ? sums[2 * i] : sums[2 * i + 1], 16);
+                    h[i] = __fmul_rn(activation(half ? other : mine, p.gelu), half ? mine : other);
+                }
+                // sum and largest exponent of the 64
 #pragma unroll
-                for (int i = 0; i < OWN; ++i) {
-                    const int j = group + kGroups * i;
-                    if (j >= im.count) break;
-                    float h = __fmul_rn(activation(sums[i], p.gelu), xs[j * kHalf + row]);
-                    // sum and largest exponent of the 64
-                    uint32_t E = max(1u, (__float_as_uint(h) >> 23) & 0xffu);
-                    float sum = h;
-                    E = __reduce_max_sync(0xffffffffu, E);
+                for (int i = 0; i < NC / 2; ++i) {
+                    const uint32_t E = __reduce_max_sync(0xffffu << (lane & 16), max(1u, (__float_as_uint(h[i]) >> 23) & 0xffu));
+                    float sum = h[i];
 #pragma unroll
-                    for (int d = 16; d; d >>= 1) sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, d));
-                    if (lane == 0) {
-                        red[(warp & 1) * 2] = sum;
-                        red[(warp & 1) * 2 + 1] = __uint_as_float(E);
-                    }
-                    named_sync(2 + kGroups + group, 64);
-                    sum = __fadd_rn(red[0], red[2]);
-                    E = max(__float_as_uint(red[1]), __float_as_uint(red[3]));
-                    named_sync(2 + kGroups + group, 64);
-                    const int pw = 134 - int(E);
-                    float v = __fmul_rn(__fmul_rn(h, exp2i(pw / 2)), exp2i(pw - pw / 2));
-                    // the element's byte of its row, in the order of the masks
-                    const int pc = row >> 4, e = row & 15;
-                    const int at = BITS == 4 ? (e >> 3) * 8 + (e & 1) * 4 + ((e & 7) >> 1) : (e & 3) * 4 + (e >> 2);
+                    for (int d = 8; d; d >>= 1) sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, d));
+                    if ((lane & 15) == 0) red[(half * (NC / 2) + i) * 4 + (warp & 3)] = make_float2(sum, __uint_as_float(E));
+                }
+                named_sync(2, 32 * kGatherers);
+                // the element's byte of its row, in the order of the masks
+                const int pc = r >> 4, e = r & 15;
+                const int at = BITS == 4 ? (e >> 3) * 8 + (e & 1) * 4 + ((e & 7) >> 1) : (e & 3) * 4 + (e >> 2);
+#pragma unroll
+                for (int i = 0; i < NC / 2; ++i) {
+                    const int j = 2 * i + half;
+                    const float4 r0 = reinterpret_cast<const float4 *>(red)[(half * (NC / 2) + i) * 2];
+                    const float4 r1 = reinterpret_cast<const float4 *>(red)[(half * (NC / 2) + i) * 2 + 1];
+                    const int E = int(max(max(__float_as_uint(r0.y), __float_as_uint(r0.w)), max(__float_as_uint(r1.y), __float_as_uint(r1.w))));
+                    const int pw = 134 - E;
+                    float v = __fmul_rn(__fmul_rn(h[i], exp2i(pw / 2)), exp2i(pw - pw / 2));
                     if (BITS == 2 && (e & 1)) v = __fmul_rn(v, 0.25f);
 #pragma unroll
                     for (int t = 0; t < kTermsH; ++t) {
@@ -634,52 +575,196 @@ __global__ void __launch_bounds__(tile::kThreads, 1)
                         float back, none;
                         from_e4m3x2(b, back, none);
                         v = __fmul_rn(__fsub_rn(v, back), 32.0f);
-                        cell[operand_offset(operand_index(j, t, kTermsH), pc) + at] = uint8_t(b);
+                        own[operand_offset(operand_index(j, t, kTermsH), pc) + at] = uint8_t(b);
                     }
-                    if (row == 0) {
-                        float *m = reinterpret_cast<float *>(meta + (j >> 1) * 16) + (j & 1);
-                        m[0] = sum;
-                        m[2] = exp2i(min(int(E) - 125, 127));
+                    if (r == 0) {
+                        float *m = reinterpret_cast<float *>(own + CB + i * 16) + half;
+                        m[0] = __fadd_rn(__fadd_rn(r0.x, r0.z), __fadd_rn(r1.x, r1.z));
+                        m[2] = exp2i(min(E - 125, 127));
                     }
+                }
+                uint8_t *slot_h = p.h + (size_t(im.entry) * p.NSb + im.tl / SUBS) * (SUBS * (CB + MB));
+                // subgroups that fill the last slot
+                if (im.tl == p.tiles_a - 1 && p.Sb % SUBS) {
+                    for (int sub = p.Sb % SUBS; sub < SUBS; ++sub) {
+                        uint32_t *c = reinterpret_cast<uint32_t *>(slot_h + sub * CB), *m = reinterpret_cast<uint32_t *>(slot_h + SUBS * CB + sub * MB);
+                        for (int i = row; i < CB / 4; i += 32 * kGatherers) c[i] = 0u;
+                        for (int i = row; i < MB / 4; i += 32 * kGatherers) m[i] = 0u;
+                    }
+                    asm volatile("fence.proxy.async;" ::: "memory");
+                    __threadfence();
+                }
+                fence_proxy_async_smem();
+                named_sync(2, 32 * kGatherers);
+                if (row == 0) {
+                    const uint32_t from = smem_u32(own);
+                    bulk_store(slot_h + im.tl % SUBS * CB, from, CB);
+                    bulk_store(slot_h + SUBS * CB + im.tl % SUBS * MB, from + CB, MB);
+                    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                }
+            };
+            // The sums of an item are taken when the ring has been filled beyond it.
+            // (The four warps meet in every item, also after a wait has run out.)
+            auto behind = [&](int slots) { return min((p.slots + slots - 1) / slots, kSets - 1); };
+            int ahead = 0, most = behind(p.NSa);
+            for (Items is = items_of(p.tiles_a), es = is; es.entry < es.entries;) {
+                if (is.entry < is.entries) {
+                    gather(is);
+                    advance(is);
+                    if (++ahead <= most) continue;
+                }
+                form_h(es);
+                advance(es);
+                --ahead;
+            }
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            // (A count for each entry, raised after each item, let B start on early
+            // entries; but the release of each took thousands of cycles under the
+            // stream of weights: 97 and 181 us for 16 and 48 tokens.)
+            if (row == 0) {
+                asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+                asm volatile("fence.proxy.async;" ::: "memory");
+                asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(p.counters) : "memory");
+                ok = ok && meet(p.counters, grid);
+                asm volatile("fence.proxy.async;" ::: "memory");
+            }
+            ahead = 0;
+            most = behind(p.NSb);
+            for (Items is = items_of(p.tiles_b), es = is; es.entry < es.entries;) {
+                if (is.entry < is.entries) {
+                    const uint8_t *h = p.h + size_t(is.entry) * p.NSb * (SUBS * (CB + MB));
+                    if (row == 0)
+                        for (int i = 0; i < p.NSb && ok; ++i, h += SUBS * (CB + MB), turn.step(1, p.slots), mturn.step(1, p.slots + kGroups)) {
+                            ok = turn.lap == 0 || wait(empty0 + 8 * turn.slot, (turn.lap - 1) & 1);
+                            const uint32_t full = full0 + 8 * turn.slot;
+                            if (!ok) break;
+                            // (one of the lanes' arrivals, and for the others, which arrive of their own in A)
+                            mbar_arrive_expect_tx(full, SUBS * (CB + MB));
+                            mbar_arrive_many(full, 32 * kGatherers - 1);
+                            bulk_load_plain(base + turn.slot * L.slot + L.cells, h, SUBS * CB, full);
+                            bulk_load_plain(base + L.meta + mturn.slot * (SUBS * MB), h + SUBS * CB, SUBS * MB, full);
+                        }
+                    __syncwarp();
+                    advance(is);
+                    if (++ahead <= most) continue;
+                }
+                const Item im = item_of(es);
+                const int n = im.tl * kTileRows + row;
+                float sums[NC];
+                Row<BITS, GS, NC, kTermsH>::take(wait, ex0 + set.slot * kExchangeSet, joined0 + 8 * set.slot, freed0 + 8 * set.slot, set.lap, lane, sums);
+                set.step(1, kSets);
+#pragma unroll
+                for (int j = 0; j < NC; ++j)
+                    if (j < im.count && n < p.K) __stcg(p.partials + size_t(im.pair + j) * p.K + n, sums[j]);
+                advance(es);
+                --ahead;
+            }
+            named_sync(2, 32 * kGatherers);
+            if (row == 0) {
+                __threadfence();  // (of what the barrier ordered before it, too)
+                asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(p.counters + 1) : "memory");
+            }
+            if (!ok && lane == 0) drain();
+        } else if (warp >= kWorkers && warp < kWorkers + kGroups) {
+            // ------------------------------------------------------ tensor warps
+            const int group = warp - kWorkers;
+            if (lane == 0) {
+                // turn: of the item's first slot
+                Turn turn;
+                Pipe pipe = Pipe::make<NC, 2>(tm, 0, stored0, ready0, group);
+                for (Items is = items_of(p.tiles_a); is.entry < is.entries; advance(is), turn.step(p.NSa, p.slots)) {
+                    Turn at = turn;
+                    const int i0 = first_slot(group, turn.slot);
+                    at.step(i0, p.slots);
+                    for (int i = i0; i < p.NSa; i += kGroups, at.step(kGroups, p.slots))
+                        multiply_slot<BITS, NC, 2, true>(wait, pipe, base + at.slot * L.slot + L.cells, empty0 + 8 * at.slot);
+                }
+                Pipe pb = Pipe::make<NC, kTermsH>(tm, 0, stored0, ready0, group);
+                pb.steps = pipe.steps;
+                for (Items is = items_of(p.tiles_b); is.entry < is.entries; advance(is), turn.step(p.NSb, p.slots)) {
+                    Turn at = turn;
+                    const int i0 = first_slot(group, turn.slot);
+                    at.step(i0, p.slots);
+                    for (int i = i0; i < p.NSb; i += kGroups, at.step(kGroups, p.slots))
+                        multiply_slot<BITS, NC, kTermsH>(wait, pb, base + at.slot * L.slot + L.cells, empty0 + 8 * at.slot);
                 }
             }
-            // subgroups that fill the last slot
-            if (im.tl == p.tiles_a - 1)
-                for (int sub = p.Sb % SUBS; sub > 0 && sub < SUBS; ++sub) {
-                    uint32_t *c = reinterpret_cast<uint32_t *>(slot_h + sub * CB), *m = reinterpret_cast<uint32_t *>(slot_h + SUBS * CB + sub * MB);
-                    for (int i = tid; i < CB / 4; i += 32 * kWorkers) c[i] = 0u;
-                    for (int i = tid; i < MB / 4; i += 32 * kWorkers) m[i] = 0u;
-                }
         }
-        asm volatile("fence.proxy.async;" ::: "memory");
-        __threadfence();
-        named_sync(1, 32 * kWorkers);
-        if (tid == 0) asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(p.counters) : "memory");
+    } else {
+        // ----------------------------------------------------------- workers
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kWorkerRegs));
+        const int group = warp / 4, row = (warp & 3) * 32 + lane;
+        const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
+        Turn turn, mturn;  // of the item's first slot
+        int chunk = 0;
+        // all slots of an item's rows into acc
+        auto run = [&](auto &acc, Pipe &pipe, const Affines &a, int ch, int NS, int G, int row, long long grow) {
+            const uint32_t wrow = base + row * kSlotBytes + ((row & 7) << 4);
+            const int align = a.alignment(G);
+            constexpr int STEP = std::remove_reference_t<decltype(acc)>::kStep;
+            uint32_t last = 0;
+            acc.start();
+            Turn at = turn, mat = mturn;
+            const int i0 = first_slot(group, turn.slot);
+            at.step(i0, p.slots);
+            mat.step(i0, p.slots + kGroups);
+            for (int c0 = 0; c0 < NS; c0 += ch, ++chunk) {
+                const int buf = chunk & 1, c1 = min(c0 + ch, NS), g0 = c0 * SUBS * 64 / GS;
+                wait(sfull0 + 8 * buf, (chunk >> 1) & 1);
+                const uint32_t sb = base + L.sb + buf * 2 * p.sb_block + row * a.pitch + a.offset(grow, G, g0);
+#pragma unroll 1
+                for (int i = c0 + (i0 + kGroups - c0 % kGroups) % kGroups; i < c1;
+                     i += kGroups, at.step(kGroups, p.slots), mat.step(kGroups, p.slots + kGroups)) {
+                    const int s = at.slot;
+                    wait(full0 + 8 * s, at.lap & 1);
+                    Affine<BITS, GS> aff;
+                    constexpr int GP = Affine<BITS, GS>::kGroupsPerSlot;
+                    aff.read(sb + (i - c0) * GP * 2, p.sb_block, align, G - i * GP);
+                    const uint32_t meta = base + L.meta + mat.slot * (SUBS * MB);
+                    acc.slot(wait, pipe, wrow + s * L.slot, aff, meta, last, lane);
+                    last = meta + (SUBS - 2 * STEP) * MB;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(empty0 + 8 * s);
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(sempty0 + 8 * buf);
+            }
+            acc.finish(wait, pipe, last);
+            __syncwarp();
+            turn.step(NS, p.slots);
+            mturn.step(NS, p.slots + kGroups);
+        };
 
+        // the sums' set and how many items had it before
+        Turn set;
+        auto give = [&](auto &acc, int c) {
+            acc.give(wait, tm + lanes + kExchange + set.slot * kExchangeSet, c, joined0 + 8 * set.slot, freed0 + 8 * set.slot, set.lap, lane);
+            set.step(1, kSets);
+        };
+        Pipe pipe = Pipe::make<NC, 2>(tm, lanes, stored0, ready0, group);
+        // A warp holds 16 gate rows and the same 16 up rows.
+        const int half = lane >> 4, r = (warp & 3) * 16 + (lane & 15), arow = half * kHalf + r;
+        for (Items is = items_of(p.tiles_a); is.entry < is.entries; advance(is)) {
+            const Item im = item_of(is);
+            const int c = first_slot(group, turn.slot);
+            Row<BITS, GS, NC, 2> acc;
+            run(acc, pipe, p.sba, p.cha, p.NSa, p.Ga, arow, (long long)im.e * 2 * p.I + half * p.I + im.tl * kHalf + r);
+            give(acc, c);
+        }
         Pipe pb = Pipe::make<NC, kTermsH>(tm, lanes, stored0, ready0, group);
         pb.steps = pipe.steps;
         for (Items is = items_of(p.tiles_b); is.entry < is.entries; advance(is)) {
             const Item im = item_of(is);
-            const int n = im.tl * kTileRows + row;
+            const int c = first_slot(group, turn.slot);
             Row<BITS, GS, NC, kTermsH> acc;
-            run(acc, pb, p.sbb, p.chb, p.NSb, p.Gb, (long long)im.e * p.K + n);
-            constexpr int OWN = Row<BITS, GS, NC, kTermsH>::kOwn;
-            float sums[OWN];
-            acc.join(tm + lanes, group, 0, sums);
-#pragma unroll
-            for (int i = 0; i < OWN; ++i) {
-                const int j = group + kGroups * i;
-                if (j < im.count && n < p.K) __stcg(p.partials + size_t(im.pair + j) * p.K + n, sums[i]);
-            }
+            run(acc, pb, p.sbb, p.chb, p.NSb, p.Gb, row, (long long)im.e * p.K + im.tl * kTileRows + row);
+            give(acc, c);
         }
-        __threadfence();
-        named_sync(1, 32 * kWorkers);
         if (tid == 0) {
-            asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(p.counters + 1) : "memory");
-            (void)meet(p.counters + 1);
+            (void)meet(p.counters + 1, grid);
+            __threadfence();
         }
         named_sync(1, 32 * kWorkers);
-        __threadfence();
         // y, four elements at a time (K is a multiple of 64)
         const int quads = p.M * p.K / 4;
         for (int i = blockIdx.x * 32 * kWorkers + tid; i < quads; i += grid * 32 * kWorkers) {
@@ -744,7 +829,23 @@ int columns(int M, int E, int k)
     return M <= 4 || mean <= 1.5 ? 4 : 8;
 }
 
-MoeParams plan_moe(int M, int K, int I, int E, int k, int bits, int gs, int nc, MoeSizes &z)
+// The plan with p.nc tokens to an entry and p.chunk groups to a fetch, if its
+// shared memory fits.
+bool fit(MoeParams &p, int bits)
+{
+    const int subs = tile::slot_subs(bits), pairs = p.M * p.k;
+    p.max_entries = pairs < p.E + pairs / p.nc ? pairs : p.E + pairs / p.nc;
+    p.sba = tile::Affines::plan(p.Ga, p.Ga < p.chunk ? p.Ga : p.chunk, tile::kTileRows, 2 * p.chunk);
+    p.sbb = tile::Affines::plan(p.Gb, p.Gb < p.chunk ? p.Gb : p.chunk, tile::kTileRows, 2 * p.chunk);
+    p.cha = p.sba.mode == tile::kSbWhole ? p.NSa : p.chunk * p.gs / 64 / subs;
+    p.chb = p.sbb.mode == tile::kSbWhole ? p.NSb : p.chunk * p.gs / 64 / subs;
+    p.sb_block = p.sba.block > p.sbb.block ? p.sba.block : p.sbb.block;
+    p.slots = kMaxSlotsMoe;
+    while (p.slots > kMinSlotsMoe && moe_layout(p, bits, p.nc).total > kSmemMoe) p.slots -= tile::kGroups;
+    return moe_layout(p, bits, p.nc).total <= kSmemMoe;
+}
+
+MoeParams plan_moe(int M, int K, int I, int E, int k, int bits, int gs, MoeSizes &z)
 {
     const int subs = tile::slot_subs(bits);
     MoeParams p{};
@@ -753,19 +854,20 @@ MoeParams plan_moe(int M, int K, int I, int E, int k, int bits, int gs, int nc, 
     p.Sb = I / 64; p.NSb = (p.Sb + subs - 1) / subs; p.Gb = I / gs;
     p.tiles_a = I / kHalf;
     p.tiles_b = (K + tile::kTileRows - 1) / tile::kTileRows;
-    p.words = (M + 31) / 32;
+    // scales and biases 32 groups at a time, or 16 where there is no room; fewer
+    // tokens to an entry where there is none still (2-bit weights with 8)
     const int pairs = M * k;
-    p.max_entries = pairs < E + pairs / nc ? pairs : E + pairs / nc;
-    p.sba = tile::Affines::plan(p.Ga, p.Ga < kChunkGroups ? p.Ga : kChunkGroups, tile::kTileRows, 64);
-    p.sbb = tile::Affines::plan(p.Gb, p.Gb < kChunkGroups ? p.Gb : kChunkGroups, tile::kTileRows, 64);
-    p.cha = p.sba.mode == tile::kSbWhole ? p.NSa : kChunkGroups * gs / 64 / subs;
-    p.chb = p.sbb.mode == tile::kSbWhole ? p.NSb : kChunkGroups * gs / 64 / subs;
-    p.sb_block = p.sba.block > p.sbb.block ? p.sba.block : p.sbb.block;
+    for (p.nc = columns(M, E, k);; p.nc /= 2) {
+        p.chunk = 32;
+        if (fit(p, bits)) break;
+        p.chunk = 16;
+        if (fit(p, bits) || p.nc == 2) break;
+    }
     const size_t hs = size_t(p.max_entries) * p.NSb * subs;
     z.logits = up256(size_t(M) * E * 4);
     z.rows = up256(size_t(M) * p.NSa * subs * 128);
     z.xmeta = up256(size_t(M) * p.NSa * subs * 8);
-    z.h = up256(hs * (tile::cell_bytes(nc, kTermsH) + tile::meta_bytes(nc)));
+    z.h = up256(hs * (tile::cell_bytes(p.nc, kTermsH) + tile::meta_bytes(p.nc)));
     z.partials = up256(size_t(pairs) * K * 4);
     z.counters = up256(2 * 4);
     z.total = z.logits + z.rows + z.xmeta + z.h + z.partials + z.counters;
@@ -780,10 +882,7 @@ template <int BITS, int GS, int NC>
 cudaError_t launch_experts(const MoeMaps &m, MoeParams &p, int sms, cudaStream_t stream)
 {
     static std::atomic<int> configured[64] = {};
-    p.slots = kMaxSlotsMoe;
-    // (four at least: a group waits for its next slot while it holds one)
-    while (p.slots > 4 && moe_layout<BITS, NC>(p).total > kSmemMoe) --p.slots;
-    const int smem = moe_layout<BITS, NC>(p).total;
+    const int smem = moe_layout(p, BITS, NC).total;
     if (smem > kSmemMoe) return cudaErrorInvalidConfiguration;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -799,7 +898,7 @@ cudaError_t launch_experts(const MoeMaps &m, MoeParams &p, int sms, cudaStream_t
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(sms);
-    cfg.blockDim = dim3(tile::kThreads);
+    cfg.blockDim = dim3(kMoeThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -812,15 +911,15 @@ cudaError_t launch_experts(const MoeMaps &m, MoeParams &p, int sms, cudaStream_t
 }
 
 template <int BITS, int GS>
-cudaError_t launch_experts_nc(int nc, const MoeMaps &m, MoeParams &p, int sms, cudaStream_t stream)
+cudaError_t launch_experts_nc(const MoeMaps &m, MoeParams &p, int sms, cudaStream_t stream)
 {
-    if (nc == 2) return launch_experts<BITS, GS, 2>(m, p, sms, stream);
-    if (nc == 4) return launch_experts<BITS, GS, 4>(m, p, sms, stream);
+    if (p.nc == 2) return launch_experts<BITS, GS, 2>(m, p, sms, stream);
+    if (p.nc == 4) return launch_experts<BITS, GS, 4>(m, p, sms, stream);
     return launch_experts<BITS, GS, 8>(m, p, sms, stream);
 }
 
 template <int BITS>
-cudaError_t launch_moe(int nc, const MoeMaps &m, MoeParams &p, int sms, cudaStream_t stream)
+cudaError_t launch_moe(const MoeMaps &m, MoeParams &p, int sms, cudaStream_t stream)
 {
     static std::atomic<int> configured[64] = {};
     Launch l;
@@ -830,7 +929,7 @@ cudaError_t launch_moe(int nc, const MoeMaps &m, MoeParams &p, int sms, cudaStre
     l.pdl = true;
     const cudaError_t e = launch_one(moe_logits<BITS>, configured, l, stream, p);
     if (e != cudaSuccess) return e;
-    return p.gs == 64 ? launch_experts_nc<BITS, 64>(nc, m, p, sms, stream) : launch_experts_nc<BITS, 128>(nc, m, p, sms, stream);
+    return p.gs == 64 ? launch_experts_nc<BITS, 64>(m, p, sms, stream) : launch_experts_nc<BITS, 128>(m, p, sms, stream);
 }
 
 }  // namespace
@@ -840,7 +939,7 @@ extern "C" size_t qmv_moe_workspace_size(int M, int K, int inter, int experts, i
 {
     if (qmv::check_moe(M, K, inter, experts, top_k, bits, group_size) != QMV_OK) return 0;
     qmv::MoeSizes z;
-    qmv::plan_moe(M, K, inter, experts, top_k, bits, group_size, qmv::columns(M, experts, top_k), z);
+    qmv::plan_moe(M, K, inter, experts, top_k, bits, group_size, z);
     return z.total;
 }
 
@@ -866,9 +965,8 @@ extern "C" qmv_status qmv_moe_run(const uint16_t *x, const uint16_t *router, con
     DeviceInfo dev;
     st = current_device(&dev);
     if (st != QMV_OK) return st;
-    const int nc = columns(M, experts, top_k);
     MoeSizes z;
-    MoeParams p = plan_moe(M, K, inter, experts, top_k, bits, group_size, nc, z);
+    MoeParams p = plan_moe(M, K, inter, experts, top_k, bits, group_size, z);
     void *ws = nullptr;
     st = scratch(dev, z.total, workspace, workspace_bytes, &ws);
     if (st != QMV_OK) return st;
@@ -904,6 +1002,6 @@ extern "C" qmv_status qmv_moe_run(const uint16_t *x, const uint16_t *router, con
     }
     if (st != QMV_OK) return st;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const cudaError_t e = bits == 4 ? launch_moe<4>(nc, m, p, dev.sms, s) : launch_moe<2>(nc, m, p, dev.sms, s);
+    const cudaError_t e = bits == 4 ? launch_moe<4>(m, p, dev.sms, s) : launch_moe<2>(m, p, dev.sms, s);
     return e == cudaSuccess ? QMV_OK : record_cuda_failure("moe kernel launch", e);
 }

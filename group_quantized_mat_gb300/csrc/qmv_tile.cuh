@@ -73,6 +73,9 @@ __host__ __device__ constexpr int step_subs(int nc, int terms = 2) { return oper
 __host__ __device__ constexpr int a_columns(int nc, int terms = 2) { return 2 * step_subs(nc, terms) * 16; }
 __host__ __device__ constexpr int d_columns(int nc, int terms = 2) { return 2 * step_subs(nc, terms) * acc_columns(nc, terms); }
 constexpr int kTmemColumns = 512;
+// A group's, half for A and half for accumulators whatever the number of vectors
+// and terms, so that groups may be at work with different ones.
+constexpr int kGroupColumns = 128;
 
 __device__ __forceinline__ uint64_t pack2(float lo, float hi)
 {
@@ -266,6 +269,20 @@ __device__ __forceinline__ void tmem_st1(uint32_t a, float v)
 {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(a), "f"(v) : "memory");
 }
+template <int N>
+__device__ __forceinline__ void tmem_st_few(uint32_t a, const float (&v)[N])
+{
+    static_assert(N == 2 || N == 4 || N == 8, "columns");
+    if constexpr (N == 2)
+        asm volatile("tcgen05.st.sync.aligned.32x32b.x2.b32 [%0], {%1,%2};" ::"r"(a), "f"(v[0]), "f"(v[1]) : "memory");
+    else if constexpr (N == 4)
+        asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3])
+                     : "memory");
+    else
+        asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(a), "f"(v[0]), "f"(v[1]), "f"(v[2]),
+                     "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+                     : "memory");
+}
 __device__ __forceinline__ float tmem_ld1(uint32_t a)
 {
     float v;
@@ -275,8 +292,10 @@ __device__ __forceinline__ float tmem_ld1(uint32_t a)
 template <int N>
 __device__ __forceinline__ void tmem_ld(uint32_t a, float (&v)[N])
 {
-    static_assert(N == 4 || N == 8 || N == 16 || N == 32 || N == 64, "columns");
-    if constexpr (N == 4)
+    static_assert(N == 2 || N == 4 || N == 8 || N == 16 || N == 32 || N == 64, "columns");
+    if constexpr (N == 2)
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x2.b32 {%0,%1}, [%2];" : "=f"(v[0]), "=f"(v[1]) : "r"(a));
+    else if constexpr (N == 4)
         asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
                      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
                      : "r"(a));
@@ -334,6 +353,12 @@ __device__ __forceinline__ uint64_t b_descriptor(uint32_t addr, uint32_t stride)
 __device__ __forceinline__ void mbar_arrive_many(uint32_t bar, uint32_t count)
 {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+
+// Bulk store of shared memory; the thread commits and waits for its group.
+__device__ __forceinline__ void bulk_store(void *dst, uint32_t src, uint32_t bytes)
+{
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes) : "memory");
 }
 
 // An arrival on `bar` when the thread's earlier tensor instructions are done.
@@ -508,8 +533,9 @@ struct Pipe {
     template <int NC, int TERMS = 2>
     __device__ __forceinline__ static Pipe make(uint32_t tm, uint32_t lanes, uint32_t stored0, uint32_t ready0, int group)
     {
-        return {stored0 + 16 * group, ready0 + 16 * group, tm + lanes + group * a_columns(NC, TERMS),
-                tm + lanes + kGroups * a_columns(NC, TERMS) + group * d_columns(NC, TERMS), 0u};
+        static_assert(a_columns(NC, TERMS) <= kGroupColumns / 2 && d_columns(NC, TERMS) <= kGroupColumns / 2, "a group's columns");
+        const uint32_t a = tm + lanes + group * kGroupColumns;
+        return {stored0 + 16 * group, ready0 + 16 * group, a, a + kGroupColumns / 2, 0u};
     }
 };
 
@@ -635,6 +661,41 @@ struct Row {
     // its own A columns, `tm` being the first with the warp's lanes): sums[i]
     // becomes the total of vector group + 3 i, added from group `first` on, which
     // had the tile's first slot.
+    // Or one group, the tile's owner, gets all of its sums when it has time, and all
+    // go on to their next tile at once: they leave theirs in columns `ex` (three
+    // sets of 8), free when `freed` says so, and arrive on `joined`. `use` counts the
+    // owner's tiles; c: the group's place in the order of the sums.
+    __device__ __forceinline__ void give(const Waits &wait, uint32_t ex, int c, uint32_t joined, uint32_t freed, int use, int lane) const
+    {
+        if (use > 0) wait(freed, (use - 1) & 1);
+        tmem_fence_after();
+        float v[NC];
+#pragma unroll
+        for (int i = 0; i < NC / 2; ++i) unpack2(y[i], v[2 * i], v[2 * i + 1]);
+        tmem_st_few<NC>(ex + c * 8, v);
+        tmem_wait_st();
+        tmem_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(joined);
+    }
+    static __device__ __forceinline__ void take(const Waits &wait, uint32_t ex, uint32_t joined, uint32_t freed, int use, int lane,
+                                                float (&sums)[NC])
+    {
+        wait(joined, use & 1);
+        tmem_fence_after();
+        float v[kGroups][NC];
+#pragma unroll
+        for (int c = 0; c < kGroups; ++c) tmem_ld<NC>(ex + c * 8, v[c]);
+        tmem_wait_ld();
+#pragma unroll
+        for (int c = 0; c < kGroups; ++c) settle(v[c]);
+#pragma unroll
+        for (int i = 0; i < NC; ++i) sums[i] = __fadd_rn(__fadd_rn(v[0][i], v[1][i]), v[2][i]);
+        tmem_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(freed);
+    }
+
     static constexpr int kOwn = (NC + kGroups - 1) / kGroups;
     __device__ __forceinline__ void join(uint32_t tm, int group, int first, float (&sums)[kOwn])
     {
@@ -642,8 +703,8 @@ struct Row {
         for (int c = 0; c < NC / 2; ++c) {
             float lo, hi;
             unpack2(y[c], lo, hi);
-            tmem_st1(tm + group * a_columns(NC, TERMS) + 2 * c, lo);
-            tmem_st1(tm + group * a_columns(NC, TERMS) + 2 * c + 1, hi);
+            tmem_st1(tm + group * kGroupColumns + 2 * c, lo);
+            tmem_st1(tm + group * kGroupColumns + 2 * c + 1, hi);
         }
         tmem_wait_st();
         tmem_fence_before();
@@ -654,7 +715,7 @@ struct Row {
         for (int i = 0; i < kOwn; ++i)
 #pragma unroll
             for (int g = 0; g < kGroups; ++g)
-                v[i][g] = tmem_ld1(tm + (first + g) % kGroups * a_columns(NC, TERMS) + min(group + kGroups * i, NC - 1));
+                v[i][g] = tmem_ld1(tm + (first + g) % kGroups * kGroupColumns + min(group + kGroups * i, NC - 1));
         tmem_wait_ld();
 #pragma unroll
         for (int i = 0; i < kOwn; ++i) {
@@ -669,9 +730,10 @@ struct Row {
 
 // The tensor warp's part of one slot: waits for each step's A operands and
 // multiplies them with the subgroups' cells. `cell` is the slot's first.
-// FENCE: the cells were written by threads, not by bulk copies.
+// FENCE: the cells were written by threads, not by bulk copies. release: a barrier
+// that gets an arrival when the slot's cells have been read, 0: none.
 template <int BITS, int NC, int TERMS = 2, bool FENCE = false>
-__device__ __forceinline__ void multiply_slot(const Waits &wait, Pipe &p, uint32_t cell)
+__device__ __forceinline__ void multiply_slot(const Waits &wait, Pipe &p, uint32_t cell, uint32_t release = 0)
 {
     constexpr int ND = acc_columns(NC, TERMS), CB = cell_bytes(NC, TERMS), U = step_subs(NC, TERMS);
     constexpr int STEPS = slot_subs(BITS) / U;
@@ -689,6 +751,7 @@ __device__ __forceinline__ void multiply_slot(const Waits &wait, Pipe &p, uint32
         }
         tmem_commit(p.ready + 8 * (j & 1));
     }
+    if (release) tmem_commit(release);
     p.steps += STEPS;
 }
 

@@ -167,3 +167,15 @@ def test_capture_in_a_graph():
         graph.replay()
         torch.cuda.synchronize()
         assert np.array_equal(want, y.float().cpu().numpy())
+
+
+@pytest.mark.parametrize("M,E,k,bits", [(256, 1024, 16, 4), (256, 3, 1, 2), (128, 1024, 32, 4)])
+def test_the_most_choices(M, E, k, bits):
+    """As many choices as a call takes, over few and over the most experts: the lists
+    fill shared memory. Tokens alone and in a small batch give the same rows."""
+    lay = Layer(M, 64, 64, E, k, bits, 64, seed=29)
+    full, ids, _ = lay.run(flags=g.F32_OUT)
+    assert np.isfinite(full).all()
+    for rows in ([0], [M - 1], [M // 2, 1, 7, 64]):
+        got, got_ids, _ = lay.run(rows, flags=g.F32_OUT)
+        assert np.array_equal(got, full[rows]) and np.array_equal(got_ids, ids[rows])
