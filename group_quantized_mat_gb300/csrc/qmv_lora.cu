@@ -25,7 +25,7 @@
 //  - Rows go to CTAs in tiles of equal height (a multiple of 8, at most 128): 104
 //    for 15360 rows on 152 SMs.
 //  - K goes to CTAs in ranges of at most 64 subgroups (4096), whose cells of 16
-//    vectors are 128 KB (48 at ranks above 88). Several ranges meet in the workspace: the CTA that
+//    vectors are 128 KB (48 at ranks above 64). Several ranges meet in the workspace: the CTA that
 //    finishes a tile last adds them in their order.
 // The order of every sum depends on N, K and the rank alone, so a vector's result does not
 // depend on the batch it is in.
@@ -43,12 +43,13 @@ namespace {
 
 constexpr int kPrepareThreads = 256;
 constexpr int kMaxSlotsLora = 12;
-constexpr int kSmem = 227 * 1024 - 1024;
+constexpr int kSmem = 225 * 1024;  // beside 2 KB of static lists
 constexpr int kMaxK = 1 << 16;
 // Subgroups of a range of K at most. The ring's three slots, a range's cells of 16
 // vectors, its scales and biases and the inner vectors have to fit at 128 rows.
-__host__ __device__ constexpr int range_subs(int rank) { return rank <= 88 ? 64 : 48; }
+__host__ __device__ constexpr int range_subs(int rank) { return rank <= 64 ? 64 : 48; }
 constexpr int kPass = 16;       // vectors that one read of the weights serves
+constexpr int kPasses = QMV_MAX_M / kPass;
 constexpr int kSms = 152;       // for orders of sums, which depend on no device
 constexpr int kBefore = 3;      // slots of weights asked for before staged x (no more than a ring has)
 
@@ -71,7 +72,8 @@ struct LoraParams {
     int range;   // slots of the longest range
     int rows, tiles, grid_rows;
     int piece;   // rows of an adapter's B that a ring slot holds
-    int nc, slots, stage_blocks, sb_buffers;
+    int nc, slots, stage_blocks, sb_buffers, inner_buffers;
+    int grid_passes;  // passes that are at work at a time
     tile::Affines sb;
 };
 
@@ -141,7 +143,7 @@ __global__ void __launch_bounds__(kPrepareThreads) lora_prepare(const LoraParams
 }
 
 struct Layout {
-    int slots, slot, x, meta, sb, inner, bars, total;
+    int slots, slot, x, meta, sb, inner, inner_bytes, bars, misc, total;
 };
 
 __host__ __device__ inline Layout layout(const LoraParams &p, int bits, int nc)
@@ -158,23 +160,27 @@ __host__ __device__ inline Layout layout(const LoraParams &p, int bits, int nc)
     l.meta = l.x + subs * tile::cell_bytes(nc);
     l.sb = (l.meta + subs * tile::meta_bytes(nc) + 127) & ~127;
     l.inner = l.sb + p.sb_buffers * 2 * p.sb.block;
-    l.bars = l.inner + nc * inner_pitch(p.R) * 4;
-    l.total = l.bars + (2 * p.slots + 4 * tile::kGroups + 5) * 8;
+    l.inner_bytes = nc * inner_pitch(p.R) * 4;
+    l.bars = l.inner + p.inner_buffers * l.inner_bytes;
+    l.misc = l.bars + (2 * p.slots + 4 * tile::kGroups + 6) * 8;
+    l.total = l.misc + (4 + kPasses) * 4;
     return l;
 }
 
-// The product of a row of an adapter's B (R elements at shared address `addr`)
-// with an inner vector v (padded to a multiple of eight floats).
-__device__ __forceinline__ float adapter_dot(uint32_t addr, const float *v, int R, int row)
+// A third (0, 1, 2) of the product of a row of an adapter's B (R elements at shared
+// address `addr`) with an inner vector v (padded to a multiple of eight floats).
+__device__ __forceinline__ float adapter_dot(uint32_t addr, const float *v, int R, int row, int third)
 {
     float d0 = 0.0f, d1 = 0.0f;
     if (R % 8 == 0) {
         // Rows lie R/8 pieces of 16 bytes apart: each starts at another piece, so
         // that neighbours' reads fall on different banks.
         const int C = R / 8;
-        int c = (C >= 8 ? row : row * C >> 3) % C;
+        const int c0 = C * third / 3, c1 = C * (third + 1) / 3;
+        int c = (C >= 8 ? row : row * C >> 3) % C + c0;
+        if (c >= C) c -= C;
 #pragma unroll 4
-        for (int i = 0; i < C; ++i) {
+        for (int i = c0; i < c1; ++i) {
             float x[8];
             tile::widen8(tile::lds_128(addr + c * 16), x);
             const float4 v0 = *reinterpret_cast<const float4 *>(v + c * 8), v1 = *reinterpret_cast<const float4 *>(v + c * 8 + 4);
@@ -198,10 +204,12 @@ __device__ __forceinline__ float adapter_dot(uint32_t addr, const float *v, int 
             asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w) : "r"(a));
             return w;
         };
-        if (odd) next = lds_32(word);
-        int r = 0;
+        const int fours = R / 4;
+        int r = fours * third / 3 * 4;
+        const int r1 = fours * (third + 1) / 3 * 4;
+        if (odd) next = lds_32(word + 2 * r);
 #pragma unroll 2
-        for (; r + 4 <= R; r += 4) {
+        for (; r < r1; r += 4) {
             uint32_t a, b;
             if (odd) {
                 const uint32_t w1 = lds_32(word + 2 * r + 4), w2 = lds_32(word + 2 * r + 8);
@@ -218,7 +226,7 @@ __device__ __forceinline__ float adapter_dot(uint32_t addr, const float *v, int 
             d0 = __fmaf_rn(__uint_as_float(b << 16), w.z, d0);
             d1 = __fmaf_rn(__uint_as_float(b & 0xffff0000u), w.w, d1);
         }
-        for (; r < R; ++r) {
+        for (; third == 2 && r < R; ++r) {
             uint16_t e;
             asm volatile("ld.shared.u16 %0, [%1];" : "=h"(e) : "r"(addr + 2 * r));
             d0 = __fmaf_rn(__uint_as_float(uint32_t(e) << 16), v[r], d0);
@@ -235,34 +243,36 @@ __global__ void __launch_bounds__(tile::kThreads, 1) lora_project(const __grid_c
 {
     using namespace tile;
     extern __shared__ __align__(1024) uint8_t smem[];
-    __shared__ int s_abort, s_last, s_ad[kPass], s_ads;
-    __shared__ float s_c[kPass];
-    __shared__ uint32_t s_of[kPass];
-    __shared__ uint32_t s_tmem;
+    __shared__ uint16_t s_ad[kPasses][kPass], s_of[kPasses][kPass];
+    __shared__ float s_c[kPasses][kPass];
     constexpr int SUBS = slot_subs(BITS);
     const Layout L = layout(p, BITS, NC);
+    int &s_abort = *reinterpret_cast<int *>(smem + L.misc), &s_last = (&s_abort)[1], *s_ads = &s_abort + 4;
+    uint32_t &s_tmem = *reinterpret_cast<uint32_t *>(smem + L.misc + 8);
     const uint32_t base = smem_u32(smem), full0 = base + L.bars, empty0 = full0 + 8 * p.slots;
     const uint32_t stored0 = empty0 + 8 * p.slots, ready0 = stored0 + 16 * kGroups, xbar = ready0 + 16 * kGroups;
-    const uint32_t sfull0 = xbar + 8, sempty0 = sfull0 + 16;
+    const uint32_t xfree = xbar + 8, sfull0 = xfree + 8, sempty0 = sfull0 + 16;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-    const int seg = blockIdx.y, z = blockIdx.z, nv = min(kPass, p.M - z * kPass);
+    const int seg = blockIdx.y, passes = (p.M + kPass - 1) / kPass;
     const int lo = int((long long)p.NS * seg / p.nseg), ns = int((long long)p.NS * (seg + 1) / p.nseg) - lo;
     const int g0 = lo * SUBS * 64 / GS, groups = min(ns * SUBS * 64 / GS, p.G - g0);
-    if (warp == 2) {
-        // This range's adapters among those of the pass's vectors, each once, in
-        // their order, with the vectors that have it. An adapter belongs to the
-        // range of its number modulo the ranges.
-        int ad = lane < nv ? __ldg(p.adapter + z * kPass + lane) : -1;
+    static_assert(kPasses <= kThreads / 32, "a warp for each pass");
+    if (warp < passes) {
+        // This range's adapters among those of a pass's vectors, each once, in their
+        // order, with the vectors that have it. An adapter belongs to the range of
+        // its number modulo the ranges.
+        const int t = warp * kPass + lane;
+        int ad = lane < kPass && t < p.M ? __ldg(p.adapter + t) : -1;
         if (ad < 0 || ad >= p.L || ad % p.nseg != seg) ad = -1;
         const uint32_t same = __match_any_sync(0xffffffffu, ad);
         const bool first = ad >= 0 && __ffs(same) - 1 == lane;
         const uint32_t firsts = __ballot_sync(0xffffffffu, first);
         if (first) {
             const int at = __popc(firsts & ((1u << lane) - 1u));
-            s_ad[at] = ad;
-            s_of[at] = same;
+            s_ad[warp][at] = uint16_t(ad);
+            s_of[warp][at] = uint16_t(same);
         }
-        if (lane == 0) s_ads = __popc(firsts);
+        if (lane == 0) s_ads[warp] = __popc(firsts);
     }
     if (tid == 0) {
         for (int i = 0; i < p.slots; ++i) {
@@ -274,6 +284,7 @@ __global__ void __launch_bounds__(tile::kThreads, 1) lora_project(const __grid_c
             mbar_init(ready0 + 8 * i, 1);
         }
         mbar_init(xbar, 1);
+        mbar_init(xfree, kWorkers);
         for (int i = 0; i < 2; ++i) {
             mbar_init(sfull0 + 8 * i, 32);
             mbar_init(sempty0 + 8 * i, kWorkers);
@@ -287,12 +298,18 @@ __global__ void __launch_bounds__(tile::kThreads, 1) lora_project(const __grid_c
     tmem_fence_after();
     const uint32_t tm = s_tmem;
     const Waits wait{&s_abort, p.err};
-    const int ads = s_ads, pieces = (p.rows + p.piece - 1) / p.piece;
+    const int pieces = (p.rows + p.piece - 1) / p.piece;
 
-    // staged x and inner vectors by bulk copies, once the first kernel has ended
-    auto fetch_x = [&]() {
-        grid_dependency_wait();
-        asm volatile("fence.proxy.async;" ::: "memory");
+    // staged x and inner vectors of a pass by bulk copies, once the first kernel has
+    // ended and the pass before (`before` passes in all) needs its own no more
+    auto fetch_x = [&](int z, int before) {
+        if (before == 0) {
+            grid_dependency_wait();
+            asm volatile("fence.proxy.async;" ::: "memory");
+        } else {
+            wait(xfree, (before - 1) & 1);
+        }
+        const int nv = min(kPass, p.M - z * kPass);
         const uint32_t cb = uint32_t(ns) * SUBS * cell_bytes(NC), mb = uint32_t(ns) * SUBS * meta_bytes(NC);
         const uint32_t ib = uint32_t(nv) * inner_pitch(p.R) * 4;
         mbar_arrive_expect_tx(xbar, cb + mb + ib);
@@ -300,78 +317,78 @@ __global__ void __launch_bounds__(tile::kThreads, 1) lora_project(const __grid_c
         bulk_load_plain(base + L.x, p.cells + sub * cell_bytes(NC), cb, xbar);
         bulk_load_plain(base + L.meta, p.meta + sub * meta_bytes(NC), mb, xbar);
         // (of vectors without an adapter: whatever is there)
-        bulk_load_plain(base + L.inner, p.inner + size_t(z) * kPass * inner_pitch(p.R), ib, xbar);
+        bulk_load_plain(base + L.inner + (before & 1) * L.inner_bytes, p.inner + size_t(z) * kPass * inner_pitch(p.R), ib, xbar);
     };
 
     if (warp == kThreads / 32 - 1) {
         // ---------------------------------------------------------- producer
-        int it = 0, tiles = 0;
-        bool staged = false, ok = true;
+        int it = 0, tiles = 0, fetched = 0;
+        bool ok = true;
         const uint32_t bytes = uint32_t(p.rows) * kSlotBytes;
-        for (int tl = blockIdx.x; tl < p.tiles && ok; tl += p.grid_rows, ++tiles) {
-            const int buf = tiles % p.sb_buffers, turn = tiles / p.sb_buffers;
-            ok = __all_sync(0xffffffffu, turn == 0 || wait(sempty0 + 8 * buf, (turn - 1) & 1));
-            if (!ok) break;
-            p.sb.fetch(base + L.sb + buf * 2 * p.sb.block, smem + L.sb + buf * 2 * p.sb.block, p.scales, p.biases, &smap, &bmap,
-                       (long long)tl * p.rows, p.rows, p.N, p.G, g0, groups, sfull0 + 8 * buf, lane);
-            if (lane == 0)
-                for (int i = 0; i < ns; ++i, ++it) {
-                    if (!staged && it == min(kBefore, ns)) {
-                        staged = true;
-                        fetch_x();
+        for (int z = blockIdx.z; z < passes && ok; z += gridDim.z) {
+            const int ads = s_ads[z], it0 = it, before = fetched, early = min(fetched == 0 ? kBefore : p.slots, ns);
+            for (int tl = blockIdx.x; tl < p.tiles && ok; tl += p.grid_rows, ++tiles) {
+                const int buf = tiles % p.sb_buffers, turn = tiles / p.sb_buffers;
+                ok = __all_sync(0xffffffffu, turn == 0 || wait(sempty0 + 8 * buf, (turn - 1) & 1));
+                if (!ok) break;
+                p.sb.fetch(base + L.sb + buf * 2 * p.sb.block, smem + L.sb + buf * 2 * p.sb.block, p.scales, p.biases, &smap, &bmap,
+                           (long long)tl * p.rows, p.rows, p.N, p.G, g0, groups, sfull0 + 8 * buf, lane);
+                if (lane == 0)
+                    for (int i = 0; i < ns; ++i, ++it) {
+                        if (fetched == before && it - it0 == early) fetch_x(z, fetched++);
+                        const int s = it % p.slots, lap = it / p.slots;
+                        ok = lap == 0 || wait(empty0 + 8 * s, (lap - 1) & 1);
+                        if (!ok) break;
+                        mbar_arrive_expect_tx(full0 + 8 * s, bytes);
+                        tma_load_2d(base + s * L.slot, &map, (lo + i) * (kSlotBytes / 8), tl * p.rows, full0 + 8 * s);
                     }
-                    const int s = it % p.slots, lap = it / p.slots;
-                    ok = lap == 0 || wait(empty0 + 8 * s, (lap - 1) & 1);
-                    if (!ok) break;
-                    mbar_arrive_expect_tx(full0 + 8 * s, bytes);
-                    tma_load_2d(base + s * L.slot, &map, (lo + i) * (kSlotBytes / 8), tl * p.rows, full0 + 8 * s);
-                }
-            if (lane == 0 && ok && !staged) {
-                staged = true;
-                fetch_x();
+                if (lane == 0 && ok && fetched == before) fetch_x(z, fetched++);
+                // the adapters' rows of the tile, from the 16-byte boundary before them
+                if (lane == 0)
+                    for (int j = 0; j < ads * pieces && ok; ++j, ++it) {
+                        const int d = ads == 0 ? 0 : j / pieces, r0 = (j - d * pieces) * p.piece;
+                        const int s = it % p.slots, lap = it / p.slots;
+                        ok = lap == 0 || wait(empty0 + 8 * s, (lap - 1) & 1);
+                        if (!ok) break;
+                        const long long n0 = (long long)tl * p.rows + r0, n1 = min(n0 + min(p.piece, p.rows - r0), (long long)p.N);
+                        const long long first = ((long long)s_ad[z][d] * p.N + n0) * p.R * 2, to = first + max(n1 - n0, 0ll) * p.R * 2;
+                        const long long from = first & ~15ll, whole = min((to + 15) & ~15ll, (long long)p.L * p.N * p.R * 2 & ~15ll);
+                        const uint32_t bytes = n1 > n0 && whole > from ? uint32_t(whole - from) : 0u;
+                        // the array's last bytes, where they fill no 16
+                        if (whole < to && n1 > n0) {
+                            for (long long e = max(whole, from); e < to; e += 2)
+                                *reinterpret_cast<uint16_t *>(smem + s * L.slot + (e - from)) = __ldg(p.b + e / 2);
+                            fence_proxy_async_smem();
+                        }
+                        mbar_arrive_expect_tx(full0 + 8 * s, bytes);
+                        if (bytes) bulk_load_plain(base + s * L.slot, reinterpret_cast<const uint8_t *>(p.b) + from, bytes, full0 + 8 * s);
+                    }
+                ok = __all_sync(0xffffffffu, ok);
             }
-            // the adapters' rows of the tile, from the 16-byte boundary before them
-            if (lane == 0)
-                for (int j = 0; j < ads * pieces && ok; ++j, ++it) {
-                    const int d = ads == 0 ? 0 : j / pieces, r0 = (j - d * pieces) * p.piece;
-                    const int s = it % p.slots, lap = it / p.slots;
-                    ok = lap == 0 || wait(empty0 + 8 * s, (lap - 1) & 1);
-                    if (!ok) break;
-                    const long long n0 = (long long)tl * p.rows + r0, n1 = min(n0 + min(p.piece, p.rows - r0), (long long)p.N);
-                    const long long first = ((long long)s_ad[d] * p.N + n0) * p.R * 2, to = first + max(n1 - n0, 0ll) * p.R * 2;
-                    const long long from = first & ~15ll, whole = min((to + 15) & ~15ll, (long long)p.L * p.N * p.R * 2 & ~15ll);
-                    const uint32_t bytes = n1 > n0 && whole > from ? uint32_t(whole - from) : 0u;
-                    // the array's last bytes, where they fill no 16
-                    if (whole < to && n1 > n0) {
-                        for (long long e = max(whole, from); e < to; e += 2)
-                            *reinterpret_cast<uint16_t *>(smem + s * L.slot + (e - from)) = __ldg(p.b + e / 2);
-                        fence_proxy_async_smem();
-                    }
-                    mbar_arrive_expect_tx(full0 + 8 * s, bytes);
-                    if (bytes) bulk_load_plain(base + s * L.slot, reinterpret_cast<const uint8_t *>(p.b) + from, bytes, full0 + 8 * s);
-                }
-            ok = __all_sync(0xffffffffu, ok);
+            fetched = __shfl_sync(0xffffffffu, fetched, 0);
         }
         if (lane == 0) {
-            if (!staged) fetch_x();
             if (!ok) {  // copies in flight end before the CTA does
                 for (int j = max(0, it - p.slots); j < it; ++j)
                     (void)mbar_wait_bounded(full0 + 8 * (j % p.slots), (j / p.slots) & 1);
                 for (int j = max(0, tiles - p.sb_buffers); j < tiles; ++j)
                     (void)mbar_wait_bounded(sfull0 + 8 * (j % p.sb_buffers), (j / p.sb_buffers) & 1);
-                (void)mbar_wait_bounded(xbar, 0);
+                if (fetched) (void)mbar_wait_bounded(xbar, (fetched - 1) & 1);
             }
         }
     } else if (warp >= kWorkers) {
         // ------------------------------------------------------ tensor warps
         const int group = warp - kWorkers;
         if (lane == 0) {
-            wait(xbar, 0);
             Pipe pipe = Pipe::make<NC>(tm, 0, stored0, ready0, group);
-            int it = 0;
-            for (int tl = blockIdx.x; tl < p.tiles; tl += p.grid_rows, it += ns + ads * pieces)
-                for (int i = first_slot(group, it); i < ns; i += kGroups)
-                    multiply_slot<BITS, NC>(wait, pipe, base + L.x + i * SUBS * cell_bytes(NC));
+            int it = 0, before = 0;
+            for (int z = blockIdx.z; z < passes; z += gridDim.z, ++before) {
+                const int step = ns + s_ads[z] * pieces;
+                wait(xbar, before & 1);
+                for (int tl = blockIdx.x; tl < p.tiles; tl += p.grid_rows, it += step)
+                    for (int i = first_slot(group, it); i < ns; i += kGroups)
+                        multiply_slot<BITS, NC>(wait, pipe, base + L.x + i * SUBS * cell_bytes(NC));
+            }
         }
     } else {
         // ----------------------------------------------------------- workers
@@ -380,100 +397,135 @@ __global__ void __launch_bounds__(tile::kThreads, 1) lora_project(const __grid_c
         Pipe pipe = Pipe::make<NC>(tm, lanes, stored0, ready0, group);
         const uint32_t wrow = base + row * kSlotBytes + ((row & 7) << 4);
         grid_launch_dependents();
-        if (tid < ads) s_c[tid] = __ldg(p.c + s_ad[tid]);  // (the first tile's join publishes them)
-        bool landed = false;  // staged x
-        int it = 0, tiles = 0;
+        if (tid < kPasses * kPass && tid / kPass < passes && tid % kPass < s_ads[tid / kPass])  // (the next barrier publishes them)
+            s_c[tid / kPass][tid % kPass] = __ldg(p.c + s_ad[tid / kPass][tid % kPass]);
+        int it = 0, tiles = 0, before = 0;
         const int align = p.sb.alignment(p.G);
-        for (int tl = blockIdx.x; tl < p.tiles; tl += p.grid_rows, it += ns + ads * pieces, ++tiles) {
-            const int n = tl * p.rows + row;
-            const bool live = row < p.rows && n < p.N;
-            Row<BITS, GS, NC> acc;
-            acc.start();
-            uint32_t last = 0;
-            const int buf = tiles % p.sb_buffers;
-            wait(sfull0 + 8 * buf, (tiles / p.sb_buffers) & 1);
-            const uint32_t sb = base + L.sb + buf * 2 * p.sb.block + min(row, p.rows - 1) * p.sb.pitch + p.sb.offset(n, p.G, g0);
+        // With several ranges: the tile whose partial sums were left last and, in one
+        // thread, how many ranges had left theirs before. It is looked at after the
+        // next tile, so that nobody waits for the answer.
+        int left_z = 0, left_tl = -1;
+        unsigned others = 0;
+        auto put = [&](int z, int t, int n, float v) {
+            const size_t at = size_t(z * kPass + t) * p.N + n;
+            if (p.f32_out) static_cast<float *>(p.y)[at] = v;
+            else static_cast<__nv_bfloat16 *>(p.y)[at] = __float2bfloat16_rn(v);
+        };
+        // before and after a barrier of all workers
+        auto ask = [&]() {
+            if (tid != 0 || left_tl < 0) return;
+            s_last = others == unsigned(p.nseg - 1);
+            __threadfence();
+        };
+        auto join_ranges = [&]() {
+            if (left_tl < 0 || !s_last) return;
+            const int n = left_tl * p.rows + row, nv = min(kPass, p.M - left_z * kPass);
+            if (row >= p.rows || n >= p.N) return;
+            const float *part = p.partials + size_t(left_z) * p.nseg * NC * p.N + n;
+            float s[Row<BITS, GS, NC>::kOwn];
+            for (int k = 0; k < p.nseg; ++k, part += size_t(NC) * p.N) {
+                float v[Row<BITS, GS, NC>::kOwn];
+#pragma unroll
+                for (int i = 0; i < Row<BITS, GS, NC>::kOwn; ++i) v[i] = group + kGroups * i < nv ? __ldcg(part + size_t(group + kGroups * i) * p.N) : 0.0f;
+#pragma unroll
+                for (int i = 0; i < Row<BITS, GS, NC>::kOwn; ++i) s[i] = k ? __fadd_rn(s[i], v[i]) : v[i];
+            }
+#pragma unroll
+            for (int i = 0; i < Row<BITS, GS, NC>::kOwn; ++i)
+                if (group + kGroups * i < nv) put(left_z, group + kGroups * i, n, s[i]);
+        };
+        for (int z = blockIdx.z; z < passes; z += gridDim.z, ++before) {
+            const int ads = s_ads[z], nv = min(kPass, p.M - z * kPass);
+            const float *inner = reinterpret_cast<const float *>(smem + L.inner + (before & 1 & (p.inner_buffers - 1)) * L.inner_bytes);
+            bool landed = false;  // staged x
+            for (int tl = blockIdx.x; tl < p.tiles; tl += p.grid_rows, it += ns + ads * pieces, ++tiles) {
+                const bool over = tl + p.grid_rows >= p.tiles;  // the pass's last tile here
+                const int n = tl * p.rows + row;
+                const bool live = row < p.rows && n < p.N;
+                Row<BITS, GS, NC> acc;
+                acc.start();
+                uint32_t last = 0;
+                const int buf = tiles % p.sb_buffers;
+                wait(sfull0 + 8 * buf, (tiles / p.sb_buffers) & 1);
+                const uint32_t sb = base + L.sb + buf * 2 * p.sb.block + min(row, p.rows - 1) * p.sb.pitch + p.sb.offset(n, p.G, g0);
 #pragma unroll 1
-            for (int i = first_slot(group, it); i < ns; i += kGroups) {
-                const int s = (it + i) % p.slots, lap = (it + i) / p.slots;
-                wait(full0 + 8 * s, lap & 1);
-                const uint32_t meta = base + L.meta + i * SUBS * meta_bytes(NC);
-                Affine<BITS, GS> aff;
-                aff.read(sb + i * Affine<BITS, GS>::kGroupsPerSlot * 2, p.sb.block, align,
-                         groups - i * Affine<BITS, GS>::kGroupsPerSlot);
-                if (!landed) {
-                    wait(xbar, 0);
+                for (int i = first_slot(group, it); i < ns; i += kGroups) {
+                    const int s = (it + i) % p.slots, lap = (it + i) / p.slots;
+                    wait(full0 + 8 * s, lap & 1);
+                    const uint32_t meta = base + L.meta + i * SUBS * meta_bytes(NC);
+                    Affine<BITS, GS> aff;
+                    aff.read(sb + i * Affine<BITS, GS>::kGroupsPerSlot * 2, p.sb.block, align,
+                             groups - i * Affine<BITS, GS>::kGroupsPerSlot);
+                    if (!landed) {
+                        wait(xbar, before & 1);
+                        landed = true;
+                    }
+                    acc.slot(wait, pipe, wrow + s * L.slot, aff, meta, last, lane);
+                    last = meta + (SUBS - 2 * step_subs(NC)) * meta_bytes(NC);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_many(empty0 + 8 * s, kGroups);
+                }
+                if (lane == 0) mbar_arrive(sempty0 + 8 * buf);
+                acc.finish(wait, pipe, last);
+                if (!landed) {  // (a group without slots needs the inner vectors)
+                    wait(xbar, before & 1);
                     landed = true;
                 }
-                acc.slot(wait, pipe, wrow + s * L.slot, aff, meta, last, lane);
-                last = meta + (SUBS - 2 * step_subs(NC)) * meta_bytes(NC);
                 __syncwarp();
-                if (lane == 0) mbar_arrive_many(empty0 + 8 * s, kGroups);
-            }
-            if (lane == 0) mbar_arrive(sempty0 + 8 * buf);
-            acc.finish(wait, pipe, last);
-            if (!landed) {  // (a group without slots needs the inner vectors)
-                wait(xbar, 0);
-                landed = true;
-            }
-            float sums[Row<BITS, GS, NC>::kOwn];
-            acc.join(tm + lanes, group, it % kGroups, sums);
-            for (int j = 0, at = it + ns; j < ads * pieces; ++j, ++at) {
-                const int d = j / pieces, r0 = (j - d * pieces) * p.piece, s = at % p.slots;
-                wait(full0 + 8 * s, (at / p.slots) & 1);
-                if (live && row >= r0 && row < r0 + p.piece) {
-                    const long long first = ((long long)s_ad[d] * p.N + n - (row - r0)) * p.R * 2;
-                    const uint32_t addr = base + s * L.slot + (uint32_t(first) & 15u) + (row - r0) * p.R * 2;
-                    // the group's vectors: every third
+                if (over && p.inner_buffers == 2 && lane == 0) mbar_arrive(xfree);
+                if (ads) {
+                    // A piece's slot may have held weights of another group: all of them have
+                    // landed once all groups are done with theirs.
+                    named_sync(1, 32 * kWorkers);
+                    const int place = first_slot(group, it);
+                    for (int j = 0, at = it + ns; j < ads * pieces; ++j, ++at) {
+                        const int d = j / pieces, r0 = (j - d * pieces) * p.piece, s = at % p.slots;
+                        wait(full0 + 8 * s, (at / p.slots) & 1);
+                        if (live && row >= r0 && row < r0 + p.piece) {
+                            const long long first = ((long long)s_ad[z][d] * p.N + n - (row - r0)) * p.R * 2;
+                            const uint32_t addr = base + s * L.slot + (uint32_t(first) & 15u) + (row - r0) * p.R * 2;
+                            // each group a third of the rank, by its place in the order of the sums
 #pragma unroll 1
-                    for (uint32_t of = s_of[d] & 0x9249u << group; of; of &= of - 1) {
-                        const int t = __ffs(of) - 1;
-                        const float v = __fmul_rn(s_c[d], adapter_dot(addr, reinterpret_cast<const float *>(smem + L.inner) + t * inner_pitch(p.R), p.R, row));
-#pragma unroll
-                        for (int k = 0; k < Row<BITS, GS, NC>::kOwn; ++k)
-                            if (t == group + kGroups * k) sums[k] = __fadd_rn(sums[k], v);
+                            for (uint32_t of = s_of[z][d]; of; of &= of - 1) {
+                                const int t = __ffs(of) - 1;
+                                const float v = __fmul_rn(s_c[z][d], adapter_dot(addr, inner + t * inner_pitch(p.R), p.R, row, place));
+                                acc.add_one(t, v);
+                            }
+                        }
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(empty0 + 8 * s);
                     }
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(empty0 + 8 * s);
-            }
-            bool mine = true;
-            if (p.nseg > 1) {
-                const size_t plane = size_t(p.N), seg_stride = plane * NC;
-                float *part = p.partials + size_t(z) * p.nseg * seg_stride + n;
+                if (over && p.inner_buffers == 1 && lane == 0) mbar_arrive(xfree);
+                float sums[Row<BITS, GS, NC>::kOwn];
+                acc.join(tm + lanes, group, it % kGroups, sums);
+                if (p.nseg == 1) {
 #pragma unroll
-                for (int i = 0; i < Row<BITS, GS, NC>::kOwn; ++i) {
-                    const int t = group + kGroups * i;
-                    if (live && t < nv) __stcg(part + seg * seg_stride + t * plane, sums[i]);
+                    for (int i = 0; i < Row<BITS, GS, NC>::kOwn; ++i)
+                        if (live && group + kGroups * i < nv) put(z, group + kGroups * i, n, sums[i]);
+                    continue;
                 }
+                float *part = p.partials + (size_t(z) * p.nseg + seg) * NC * p.N + n;
+#pragma unroll
+                for (int i = 0; i < Row<BITS, GS, NC>::kOwn; ++i)
+                    if (live && group + kGroups * i < nv) __stcg(part + size_t(group + kGroups * i) * p.N, sums[i]);
+                ask();
                 named_sync(1, 32 * kWorkers);
+                unsigned had = 0;
                 if (tid == 0) {
                     __threadfence();  // (of what the barrier ordered before it, too)
-                    s_last = atomicAdd(p.counters + size_t(z) * p.tiles + tl, 1u) == unsigned(p.nseg - 1);
-                    __threadfence();
+                    had = atomicAdd(p.counters + size_t(z) * p.tiles + tl, 1u);
                 }
-                named_sync(1, 32 * kWorkers);
-                mine = s_last != 0;
-                if (mine) {
-#pragma unroll
-                    for (int i = 0; i < Row<BITS, GS, NC>::kOwn; ++i) {
-                        const int t = group + kGroups * i;
-                        if (!live || t >= nv) continue;
-                        float s = __ldcg(part + t * plane);
-                        for (int k = 1; k < p.nseg; ++k) s = __fadd_rn(s, __ldcg(part + k * seg_stride + t * plane));
-                        sums[i] = s;
-                    }
-                }
+                join_ranges();
+                others = had;
+                left_z = z;
+                left_tl = tl;
             }
-            if (!mine || !live) continue;
-#pragma unroll
-            for (int i = 0; i < Row<BITS, GS, NC>::kOwn; ++i) {
-                const int t = group + kGroups * i;
-                if (t >= nv) continue;
-                const size_t at = size_t(z * kPass + t) * p.N + n;
-                if (p.f32_out) static_cast<float *>(p.y)[at] = sums[i];
-                else static_cast<__nv_bfloat16 *>(p.y)[at] = __float2bfloat16_rn(sums[i]);
-            }
+        }
+        if (left_tl >= 0) {
+            ask();
+            named_sync(1, 32 * kWorkers);
+            join_ranges();
         }
     }
     __syncwarp();
@@ -521,11 +573,15 @@ LoraParams plan(int M, int N, int K, int bits, int gs, int R, int sms, Sizes &sz
     if (p.piece > p.rows) p.piece = p.rows;
     // (whole rows of up to 96 groups where the ring's three slots still fit beside them)
     p.slots = tile::kGroups;
-    p.sb_buffers = 1;
+    p.sb_buffers = p.inner_buffers = 1;
     p.sb = tile::Affines::plan(p.G, p.range * slot_subs * 64 / gs, p.rows, 96);
     if (layout(p, bits, p.nc).total > kSmem) p.sb = tile::Affines::plan(p.G, p.range * slot_subs * 64 / gs, p.rows, 64);
-    p.sb_buffers = rounds > 1 ? 2 : 1;
     const size_t passes = (M + kPass - 1) / kPass;
+    // passes side by side where one does not fill the card; the others one after the other
+    p.grid_passes = sms / (p.grid_rows * p.nseg);
+    if (p.grid_passes > int(passes)) p.grid_passes = int(passes);
+    if (p.grid_passes < 1) p.grid_passes = 1;
+    p.sb_buffers = rounds > 1 || int(passes) > p.grid_passes ? 2 : 1;
     sz.cells = up256(passes * p.subs * tile::cell_bytes(p.nc));
     sz.meta = up256(passes * p.subs * tile::meta_bytes(p.nc));
     sz.inner = up256(size_t(M) * inner_pitch(R) * 4);
@@ -546,7 +602,7 @@ cudaError_t launch_lora(const RingMaps &maps, LoraParams &p, cudaStream_t stream
     l.pdl = true;
     const cudaError_t e = launch_one(lora_prepare<BITS, NC>, configured[0], l, stream, p);
     if (e != cudaSuccess) return e;
-    l.grid = dim3(p.grid_rows, p.nseg, (p.M + kPass - 1) / kPass);
+    l.grid = dim3(p.grid_rows, p.nseg, p.grid_passes);
     l.threads = tile::kThreads;
     l.smem = size_t(layout(p, BITS, NC).total);
     if (p.gs == 64) return launch_one(lora_project<BITS, 64, NC>, configured[1], l, stream, maps.w, maps.s, maps.b, p);
@@ -558,7 +614,9 @@ cudaError_t launch_lora(const RingMaps &maps, LoraParams &p, cudaStream_t stream
 {
     // as many slots as fit, in threes (see qmv_tile.cuh)
     p.slots = 2 * tile::kGroups;
+    p.inner_buffers = p.M > kPass * p.grid_passes ? 2 : 1;
     if (layout(p, BITS, p.nc).total > kSmem) p.sb_buffers = 1;
+    if (layout(p, BITS, p.nc).total > kSmem) p.inner_buffers = 1;
     p.slots = kMaxSlotsLora;
     while (p.slots > tile::kGroups && layout(p, BITS, p.nc).total > kSmem) p.slots -= tile::kGroups;
     if (layout(p, BITS, p.nc).total > kSmem) return cudaErrorInvalidConfiguration;

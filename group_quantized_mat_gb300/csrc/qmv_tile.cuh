@@ -657,6 +657,19 @@ struct Row {
         }
     }
 
+    // Adds to the sum of vector t.
+    __device__ __forceinline__ void add_one(int t, float v)
+    {
+#pragma unroll
+        for (int i = 0; i < NC / 2; ++i) {
+            float lo, hi;
+            unpack2(y[i], lo, hi);
+            if (t == 2 * i) lo = __fadd_rn(lo, v);
+            if (t == 2 * i + 1) hi = __fadd_rn(hi, v);
+            y[i] = pack2(lo, hi);
+        }
+    }
+
     // The three groups' sums of the tile's rows meet in tensor memory (each group
     // its own A columns, `tm` being the first with the warp's lanes): sums[i]
     // becomes the total of vector group + 3 i, added from group `first` on, which

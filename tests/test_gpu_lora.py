@@ -168,3 +168,15 @@ def test_few_ring_slots():
 def test_adapters_whose_rows_start_anywhere(N, R):
     """Odd ranks and row counts: pieces of an adapter off 16-byte boundaries, and the array's last bytes."""
     Problem(6, N, 320, 4, 64, 3, R, ids=[2, 0, 1, 2, -1, 0], seed=N + R).check()
+
+
+@pytest.mark.parametrize("M,N,K,bits,gs,R", [(40, 20008, 4224, 4, 64, 27), (200, 19992, 1344, 2, 64, 64), (33, 20000, 5120, 2, 128, 200)])
+def test_passes_over_several_tiles(M, N, K, bits, gs, R):
+    """More vectors than a pass and more rows than a round of tiles, over one range of
+    K and several: the same rows as single vectors, and on another run."""
+    pr = Problem(M, N, K, bits, gs, 7, R, seed=12)
+    full = pr.run(flags=g.F32_OUT)
+    assert np.isfinite(full).all()
+    for row in (0, 16, M - 1):
+        assert np.array_equal(pr.run([row], flags=g.F32_OUT)[0], full[row])
+    assert np.array_equal(pr.run(flags=g.F32_OUT), full)
