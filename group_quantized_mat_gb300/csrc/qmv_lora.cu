@@ -167,73 +167,88 @@ __host__ __device__ inline Layout layout(const LoraParams &p, int bits, int nc)
     return l;
 }
 
-// A third (0, 1, 2) of the product of a row of an adapter's B (R elements at shared
-// address `addr`) with an inner vector v (padded to a multiple of eight floats).
-__device__ __forceinline__ float adapter_dot(uint32_t addr, const float *v, int R, int row, int third)
-{
-    float d0 = 0.0f, d1 = 0.0f;
-    if (R % 8 == 0) {
-        // Rows lie R/8 pieces of 16 bytes apart: each starts at another piece, so
-        // that neighbours' reads fall on different banks.
-        const int C = R / 8;
-        const int c0 = C * third / 3, c1 = C * (third + 1) / 3;
-        int c = (C >= 8 ? row : row * C >> 3) % C + c0;
-        if (c >= C) c -= C;
-#pragma unroll 4
-        for (int i = c0; i < c1; ++i) {
-            float x[8];
-            tile::widen8(tile::lds_128(addr + c * 16), x);
-            const float4 v0 = *reinterpret_cast<const float4 *>(v + c * 8), v1 = *reinterpret_cast<const float4 *>(v + c * 8 + 4);
-            d0 = __fmaf_rn(x[0], v0.x, d0);
-            d1 = __fmaf_rn(x[1], v0.y, d1);
-            d0 = __fmaf_rn(x[2], v0.z, d0);
-            d1 = __fmaf_rn(x[3], v0.w, d1);
-            d0 = __fmaf_rn(x[4], v1.x, d0);
-            d1 = __fmaf_rn(x[5], v1.y, d1);
-            d0 = __fmaf_rn(x[6], v1.z, d0);
-            d1 = __fmaf_rn(x[7], v1.w, d1);
-            c = c + 1 == C ? 0 : c + 1;
-        }
-    } else {
-        // words, shifted by an element where the row starts inside one
-        const bool odd = addr & 2;
-        const uint32_t word = addr & ~3u;
-        uint32_t next = 0;
-        auto lds_32 = [](uint32_t a) {
-            uint32_t w;
-            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w) : "r"(a));
-            return w;
-        };
-        const int fours = R / 4;
-        int r = fours * third / 3 * 4;
-        const int r1 = fours * (third + 1) / 3 * 4;
-        if (odd) next = lds_32(word + 2 * r);
-#pragma unroll 2
-        for (; r < r1; r += 4) {
-            uint32_t a, b;
-            if (odd) {
-                const uint32_t w1 = lds_32(word + 2 * r + 4), w2 = lds_32(word + 2 * r + 8);
-                a = __byte_perm(next, w1, 0x5432);
-                b = __byte_perm(w1, w2, 0x5432);
-                next = w2;
-            } else {
-                a = lds_32(word + 2 * r);
-                b = lds_32(word + 2 * r + 4);
-            }
-            const float4 w = *reinterpret_cast<const float4 *>(v + r);
-            d0 = __fmaf_rn(__uint_as_float(a << 16), w.x, d0);
-            d1 = __fmaf_rn(__uint_as_float(a & 0xffff0000u), w.y, d1);
-            d0 = __fmaf_rn(__uint_as_float(b << 16), w.z, d0);
-            d1 = __fmaf_rn(__uint_as_float(b & 0xffff0000u), w.w, d1);
-        }
-        for (; third == 2 && r < R; ++r) {
-            uint16_t e;
-            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(e) : "r"(addr + 2 * r));
-            d0 = __fmaf_rn(__uint_as_float(uint32_t(e) << 16), v[r], d0);
+// A group's third of the products of adapters' rows of B (R elements) with inner
+// vectors (padded to a multiple of eight floats).
+struct Third {
+    int R, C, first, count;  // pieces of eight elements from `first` on, or elements
+
+    __device__ __forceinline__ Third(int rank, int row, int third) : R(rank)
+    {
+        if (R % 8 == 0) {
+            // Rows lie C pieces of 16 bytes apart: each starts at another piece, so
+            // that neighbours' reads fall on different banks.
+            C = R / 8;
+            const int c0 = C * third / 3;
+            count = C * (third + 1) / 3 - c0;
+            first = (C >= 8 ? row : row * C >> 3) % C + c0;
+            if (first >= C) first -= C;
+        } else {
+            C = 0;
+            first = R / 4 * third / 3 * 4;
+            count = third == 2 ? R - first : R / 4 * (third + 1) / 3 * 4 - first;
         }
     }
-    return __fadd_rn(d0, d1);
-}
+    // The row at shared address `addr`.
+    __device__ __forceinline__ float dot(uint32_t addr, const float *v) const
+    {
+        float d0 = 0.0f, d1 = 0.0f;
+        if (C) {
+            int c = first;
+#pragma unroll 2
+            for (int i = 0; i < count; ++i) {
+                float x[8];
+                tile::widen8(tile::lds_128(addr + c * 16), x);
+                const float4 v0 = *reinterpret_cast<const float4 *>(v + c * 8), v1 = *reinterpret_cast<const float4 *>(v + c * 8 + 4);
+                d0 = __fmaf_rn(x[0], v0.x, d0);
+                d1 = __fmaf_rn(x[1], v0.y, d1);
+                d0 = __fmaf_rn(x[2], v0.z, d0);
+                d1 = __fmaf_rn(x[3], v0.w, d1);
+                d0 = __fmaf_rn(x[4], v1.x, d0);
+                d1 = __fmaf_rn(x[5], v1.y, d1);
+                d0 = __fmaf_rn(x[6], v1.z, d0);
+                d1 = __fmaf_rn(x[7], v1.w, d1);
+                c = c + 1 == C ? 0 : c + 1;
+            }
+        } else {
+            // words, shifted by an element where the row starts inside one
+            const bool odd = addr & 2;
+            const uint32_t word = addr & ~3u;
+            uint32_t next = 0;
+            auto lds_32 = [](uint32_t a) {
+                uint32_t w;
+                asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w) : "r"(a));
+                return w;
+            };
+            int r = first;
+            const int end = first + count;
+            if (odd) next = lds_32(word + 2 * r);
+#pragma unroll 2
+            for (; r + 4 <= end; r += 4) {
+                uint32_t a, b;
+                if (odd) {
+                    const uint32_t w1 = lds_32(word + 2 * r + 4), w2 = lds_32(word + 2 * r + 8);
+                    a = __byte_perm(next, w1, 0x5432);
+                    b = __byte_perm(w1, w2, 0x5432);
+                    next = w2;
+                } else {
+                    a = lds_32(word + 2 * r);
+                    b = lds_32(word + 2 * r + 4);
+                }
+                const float4 w = *reinterpret_cast<const float4 *>(v + r);
+                d0 = __fmaf_rn(__uint_as_float(a << 16), w.x, d0);
+                d1 = __fmaf_rn(__uint_as_float(a & 0xffff0000u), w.y, d1);
+                d0 = __fmaf_rn(__uint_as_float(b << 16), w.z, d0);
+                d1 = __fmaf_rn(__uint_as_float(b & 0xffff0000u), w.w, d1);
+            }
+            for (; r < end; ++r) {
+                uint16_t e;
+                asm volatile("ld.shared.u16 %0, [%1];" : "=h"(e) : "r"(addr + 2 * r));
+                d0 = __fmaf_rn(__uint_as_float(uint32_t(e) << 16), v[r], d0);
+            }
+        }
+        return __fadd_rn(d0, d1);
+    }
+};
 
 template <int BITS, int GS, int NC>
 __global__ void __launch_bounds__(tile::kThreads, 1) lora_project(const __grid_constant__ CUtensorMap map,
@@ -400,7 +415,7 @@ __global__ void __launch_bounds__(tile::kThreads, 1) lora_project(const __grid_c
         if (tid < kPasses * kPass && tid / kPass < passes && tid % kPass < s_ads[tid / kPass])  // (the next barrier publishes them)
             s_c[tid / kPass][tid % kPass] = __ldg(p.c + s_ad[tid / kPass][tid % kPass]);
         int it = 0, tiles = 0, before = 0;
-        const int align = p.sb.alignment(p.G);
+        const int align = p.sb.alignment(p.G), pitch = inner_pitch(p.R);
         // With several ranges: the tile whose partial sums were left last and, in one
         // thread, how many ranges had left theirs before. It is looked at after the
         // next tile, so that nobody waits for the answer.
@@ -413,9 +428,9 @@ __global__ void __launch_bounds__(tile::kThreads, 1) lora_project(const __grid_c
         };
         // before and after a barrier of all workers
         auto ask = [&]() {
-            if (tid != 0 || left_tl < 0) return;
+            if (row != 0 || left_tl < 0 || group != (tiles + kGroups - 1) % kGroups) return;
             s_last = others == unsigned(p.nseg - 1);
-            __threadfence();
+            if (s_last) __threadfence();
         };
         auto join_ranges = [&]() {
             if (left_tl < 0 || !s_last) return;
@@ -477,24 +492,26 @@ __global__ void __launch_bounds__(tile::kThreads, 1) lora_project(const __grid_c
                     // A piece's slot may have held weights of another group: all of them have
                     // landed once all groups are done with theirs.
                     named_sync(1, 32 * kWorkers);
-                    const int place = first_slot(group, it);
-                    for (int j = 0, at = it + ns; j < ads * pieces; ++j, ++at) {
-                        const int d = j / pieces, r0 = (j - d * pieces) * p.piece, s = at % p.slots;
-                        wait(full0 + 8 * s, (at / p.slots) & 1);
-                        if (live && row >= r0 && row < r0 + p.piece) {
-                            const long long first = ((long long)s_ad[z][d] * p.N + n - (row - r0)) * p.R * 2;
-                            const uint32_t addr = base + s * L.slot + (uint32_t(first) & 15u) + (row - r0) * p.R * 2;
-                            // each group a third of the rank, by its place in the order of the sums
+                    const Third third(p.R, row, first_slot(group, it));
+                    Turn at;
+                    at.slot = (it + ns) % p.slots;
+                    at.lap = (it + ns) / p.slots;
+                    for (int d = 0; d < ads; ++d)
+                        for (int r0 = 0; r0 < p.rows; r0 += p.piece, at.step(1, p.slots)) {
+                            wait(full0 + 8 * at.slot, at.lap & 1);
+                            if (live && row >= r0 && row < r0 + p.piece) {
+                                // (32 bits are enough for the start's place within 16 bytes)
+                                const uint32_t first = (uint32_t(s_ad[z][d]) * uint32_t(p.N) + uint32_t(tl * p.rows + r0)) * uint32_t(p.R) * 2u;
+                                const uint32_t addr = base + at.slot * L.slot + (first & 15u) + (row - r0) * p.R * 2;
 #pragma unroll 1
-                            for (uint32_t of = s_of[z][d]; of; of &= of - 1) {
-                                const int t = __ffs(of) - 1;
-                                const float v = __fmul_rn(s_c[z][d], adapter_dot(addr, inner + t * inner_pitch(p.R), p.R, row, place));
-                                acc.add_one(t, v);
+                                for (uint32_t of = s_of[z][d]; of; of &= of - 1) {
+                                    const int t = __ffs(of) - 1;
+                                    acc.add_one(t, __fmul_rn(s_c[z][d], third.dot(addr, inner + t * pitch)));
+                                }
                             }
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(empty0 + 8 * at.slot);
                         }
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(empty0 + 8 * s);
-                    }
                 }
                 if (over && p.inner_buffers == 1 && lane == 0) mbar_arrive(xfree);
                 float sums[Row<BITS, GS, NC>::kOwn];
@@ -512,7 +529,7 @@ __global__ void __launch_bounds__(tile::kThreads, 1) lora_project(const __grid_c
                 ask();
                 named_sync(1, 32 * kWorkers);
                 unsigned had = 0;
-                if (tid == 0) {
+                if (row == 0 && group == tiles % kGroups) {
                     __threadfence();  // (of what the barrier ordered before it, too)
                     had = atomicAdd(p.counters + size_t(z) * p.tiles + tl, 1u);
                 }

@@ -657,16 +657,19 @@ struct Row {
         }
     }
 
-    // Adds to the sum of vector t.
-    __device__ __forceinline__ void add_one(int t, float v)
+    // Adds to the sum of vector t, the same in all of a warp: by branches, for it is
+    // rare.
+    __device__ __forceinline__ void add_one(int t, float v) { add_within<0, NC>(t, v); }
+    template <int FROM, int N>
+    __device__ __forceinline__ void add_within(int t, float v)
     {
-#pragma unroll
-        for (int i = 0; i < NC / 2; ++i) {
+        if constexpr (N == 1) {
             float lo, hi;
-            unpack2(y[i], lo, hi);
-            if (t == 2 * i) lo = __fadd_rn(lo, v);
-            if (t == 2 * i + 1) hi = __fadd_rn(hi, v);
-            y[i] = pack2(lo, hi);
+            unpack2(y[FROM / 2], lo, hi);
+            y[FROM / 2] = FROM & 1 ? pack2(lo, __fadd_rn(hi, v)) : pack2(__fadd_rn(lo, v), hi);
+        } else {
+            if (t < FROM + N / 2) add_within<FROM, N / 2>(t, v);
+            else add_within<FROM + N / 2, N / 2>(t, v);
         }
     }
 
