@@ -167,88 +167,68 @@ __host__ __device__ inline Layout layout(const LoraParams &p, int bits, int nc)
     return l;
 }
 
-// A group's third of the products of adapters' rows of B (R elements) with inner
-// vectors (padded to a multiple of eight floats).
-struct Third {
-    int R, C, first, count;  // pieces of eight elements from `first` on, or elements
-
-    __device__ __forceinline__ Third(int rank, int row, int third) : R(rank)
-    {
-        if (R % 8 == 0) {
-            // Rows lie C pieces of 16 bytes apart: each starts at another piece, so
-            // that neighbours' reads fall on different banks.
-            C = R / 8;
-            const int c0 = C * third / 3;
-            count = C * (third + 1) / 3 - c0;
-            first = (C >= 8 ? row : row * C >> 3) % C + c0;
-            if (first >= C) first -= C;
-        } else {
-            C = 0;
-            first = R / 4 * third / 3 * 4;
-            count = third == 2 ? R - first : R / 4 * (third + 1) / 3 * 4 - first;
+// The product of a row of an adapter's B (R elements at shared address `addr`)
+// with an inner vector v (padded to a multiple of eight floats), from 16-byte
+// piece piece0 on where rows are whole pieces.
+__device__ __forceinline__ float adapter_dot(uint32_t addr, const float *v, int R, int piece0)
+{
+    float d0 = 0.0f, d1 = 0.0f;
+    if (R % 8 == 0) {
+        const int C = R / 8;
+        int c = piece0;
+#pragma unroll 4
+        for (int i = 0; i < C; ++i) {
+            float x[8];
+            tile::widen8(tile::lds_128(addr + c * 16), x);
+            const float4 v0 = *reinterpret_cast<const float4 *>(v + c * 8), v1 = *reinterpret_cast<const float4 *>(v + c * 8 + 4);
+            d0 = __fmaf_rn(x[0], v0.x, d0);
+            d1 = __fmaf_rn(x[1], v0.y, d1);
+            d0 = __fmaf_rn(x[2], v0.z, d0);
+            d1 = __fmaf_rn(x[3], v0.w, d1);
+            d0 = __fmaf_rn(x[4], v1.x, d0);
+            d1 = __fmaf_rn(x[5], v1.y, d1);
+            d0 = __fmaf_rn(x[6], v1.z, d0);
+            d1 = __fmaf_rn(x[7], v1.w, d1);
+            c = c + 1 == C ? 0 : c + 1;
+        }
+    } else {
+        // words, shifted by an element where the row starts inside one
+        const bool odd = addr & 2;
+        const uint32_t word = addr & ~3u;
+        uint32_t next = 0;
+        auto lds_32 = [](uint32_t a) {
+            uint32_t w;
+            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w) : "r"(a));
+            return w;
+        };
+        if (odd) next = lds_32(word);
+        int r = 0;
+#pragma unroll 2
+        for (; r + 4 <= R; r += 4) {
+            uint32_t a, b;
+            if (odd) {
+                const uint32_t w1 = lds_32(word + 2 * r + 4), w2 = lds_32(word + 2 * r + 8);
+                a = __byte_perm(next, w1, 0x5432);
+                b = __byte_perm(w1, w2, 0x5432);
+                next = w2;
+            } else {
+                a = lds_32(word + 2 * r);
+                b = lds_32(word + 2 * r + 4);
+            }
+            const float4 w = *reinterpret_cast<const float4 *>(v + r);
+            d0 = __fmaf_rn(__uint_as_float(a << 16), w.x, d0);
+            d1 = __fmaf_rn(__uint_as_float(a & 0xffff0000u), w.y, d1);
+            d0 = __fmaf_rn(__uint_as_float(b << 16), w.z, d0);
+            d1 = __fmaf_rn(__uint_as_float(b & 0xffff0000u), w.w, d1);
+        }
+        for (; r < R; ++r) {
+            uint16_t e;
+            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(e) : "r"(addr + 2 * r));
+            d0 = __fmaf_rn(__uint_as_float(uint32_t(e) << 16), v[r], d0);
         }
     }
-    // The row at shared address `addr`.
-    __device__ __forceinline__ float dot(uint32_t addr, const float *v) const
-    {
-        float d0 = 0.0f, d1 = 0.0f;
-        if (C) {
-            int c = first;
-#pragma unroll 2
-            for (int i = 0; i < count; ++i) {
-                float x[8];
-                tile::widen8(tile::lds_128(addr + c * 16), x);
-                const float4 v0 = *reinterpret_cast<const float4 *>(v + c * 8), v1 = *reinterpret_cast<const float4 *>(v + c * 8 + 4);
-                d0 = __fmaf_rn(x[0], v0.x, d0);
-                d1 = __fmaf_rn(x[1], v0.y, d1);
-                d0 = __fmaf_rn(x[2], v0.z, d0);
-                d1 = __fmaf_rn(x[3], v0.w, d1);
-                d0 = __fmaf_rn(x[4], v1.x, d0);
-                d1 = __fmaf_rn(x[5], v1.y, d1);
-                d0 = __fmaf_rn(x[6], v1.z, d0);
-                d1 = __fmaf_rn(x[7], v1.w, d1);
-                c = c + 1 == C ? 0 : c + 1;
-            }
-        } else {
-            // words, shifted by an element where the row starts inside one
-            const bool odd = addr & 2;
-            const uint32_t word = addr & ~3u;
-            uint32_t next = 0;
-            auto lds_32 = [](uint32_t a) {
-                uint32_t w;
-                asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w) : "r"(a));
-                return w;
-            };
-            int r = first;
-            const int end = first + count;
-            if (odd) next = lds_32(word + 2 * r);
-#pragma unroll 2
-            for (; r + 4 <= end; r += 4) {
-                uint32_t a, b;
-                if (odd) {
-                    const uint32_t w1 = lds_32(word + 2 * r + 4), w2 = lds_32(word + 2 * r + 8);
-                    a = __byte_perm(next, w1, 0x5432);
-                    b = __byte_perm(w1, w2, 0x5432);
-                    next = w2;
-                } else {
-                    a = lds_32(word + 2 * r);
-                    b = lds_32(word + 2 * r + 4);
-                }
-                const float4 w = *reinterpret_cast<const float4 *>(v + r);
-                d0 = __fmaf_rn(__uint_as_float(a << 16), w.x, d0);
-                d1 = __fmaf_rn(__uint_as_float(a & 0xffff0000u), w.y, d1);
-                d0 = __fmaf_rn(__uint_as_float(b << 16), w.z, d0);
-                d1 = __fmaf_rn(__uint_as_float(b & 0xffff0000u), w.w, d1);
-            }
-            for (; r < end; ++r) {
-                uint16_t e;
-                asm volatile("ld.shared.u16 %0, [%1];" : "=h"(e) : "r"(addr + 2 * r));
-                d0 = __fmaf_rn(__uint_as_float(uint32_t(e) << 16), v[r], d0);
-            }
-        }
-        return __fadd_rn(d0, d1);
-    }
-};
+    return __fadd_rn(d0, d1);
+}
 
 template <int BITS, int GS, int NC>
 __global__ void __launch_bounds__(tile::kThreads, 1) lora_project(const __grid_constant__ CUtensorMap map,
@@ -272,11 +252,12 @@ __global__ void __launch_bounds__(tile::kThreads, 1) lora_project(const __grid_c
     const int lo = int((long long)p.NS * seg / p.nseg), ns = int((long long)p.NS * (seg + 1) / p.nseg) - lo;
     const int g0 = lo * SUBS * 64 / GS, groups = min(ns * SUBS * 64 / GS, p.G - g0);
     static_assert(kPasses <= kThreads / 32, "a warp for each pass");
-    if (warp < passes) {
+    const int lists = (warp + kPasses - 2) % kPasses;  // the pass whose lists this warp makes (warp 0 has the barriers to make)
+    if (lists < passes) {
         // This range's adapters among those of a pass's vectors, each once, in their
         // order, with the vectors that have it. An adapter belongs to the range of
         // its number modulo the ranges.
-        const int t = warp * kPass + lane;
+        const int t = lists * kPass + lane;
         int ad = lane < kPass && t < p.M ? __ldg(p.adapter + t) : -1;
         if (ad < 0 || ad >= p.L || ad % p.nseg != seg) ad = -1;
         const uint32_t same = __match_any_sync(0xffffffffu, ad);
@@ -284,10 +265,10 @@ __global__ void __launch_bounds__(tile::kThreads, 1) lora_project(const __grid_c
         const uint32_t firsts = __ballot_sync(0xffffffffu, first);
         if (first) {
             const int at = __popc(firsts & ((1u << lane) - 1u));
-            s_ad[warp][at] = uint16_t(ad);
-            s_of[warp][at] = uint16_t(same);
+            s_ad[lists][at] = uint16_t(ad);
+            s_of[lists][at] = uint16_t(same);
         }
-        if (lane == 0) s_ads[warp] = __popc(firsts);
+        if (lane == 0) s_ads[lists] = __popc(firsts);
     }
     if (tid == 0) {
         for (int i = 0; i < p.slots; ++i) {
@@ -416,6 +397,9 @@ __global__ void __launch_bounds__(tile::kThreads, 1) lora_project(const __grid_c
             s_c[tid / kPass][tid % kPass] = __ldg(p.c + s_ad[tid / kPass][tid % kPass]);
         int it = 0, tiles = 0, before = 0;
         const int align = p.sb.alignment(p.G), pitch = inner_pitch(p.R);
+        // Adapters' rows lie R/8 pieces of 16 bytes apart: each starts at another
+        // piece, so that neighbours' reads fall on different banks.
+        const int piece0 = p.R % 8 ? 0 : (p.R >= 64 ? row : row * (p.R / 8) >> 3) % (p.R / 8);
         // With several ranges: the tile whose partial sums were left last and, in one
         // thread, how many ranges had left theirs before. It is looked at after the
         // next tile, so that nobody waits for the answer.
@@ -488,34 +472,32 @@ __global__ void __launch_bounds__(tile::kThreads, 1) lora_project(const __grid_c
                 }
                 __syncwarp();
                 if (over && p.inner_buffers == 2 && lane == 0) mbar_arrive(xfree);
-                if (ads) {
-                    // A piece's slot may have held weights of another group: all of them have
-                    // landed once all groups are done with theirs.
-                    named_sync(1, 32 * kWorkers);
-                    const Third third(p.R, row, first_slot(group, it));
-                    Turn at;
-                    at.slot = (it + ns) % p.slots;
-                    at.lap = (it + ns) / p.slots;
-                    for (int d = 0; d < ads; ++d)
-                        for (int r0 = 0; r0 < p.rows; r0 += p.piece, at.step(1, p.slots)) {
-                            wait(full0 + 8 * at.slot, at.lap & 1);
-                            if (live && row >= r0 && row < r0 + p.piece) {
-                                // (32 bits are enough for the start's place within 16 bytes)
-                                const uint32_t first = (uint32_t(s_ad[z][d]) * uint32_t(p.N) + uint32_t(tl * p.rows + r0)) * uint32_t(p.R) * 2u;
-                                const uint32_t addr = base + at.slot * L.slot + (first & 15u) + (row - r0) * p.R * 2;
-#pragma unroll 1
-                                for (uint32_t of = s_of[z][d]; of; of &= of - 1) {
-                                    const int t = __ffs(of) - 1;
-                                    acc.add_one(t, __fmul_rn(s_c[z][d], third.dot(addr, inner + t * pitch)));
-                                }
-                            }
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(empty0 + 8 * at.slot);
-                        }
-                }
-                if (over && p.inner_buffers == 1 && lane == 0) mbar_arrive(xfree);
                 float sums[Row<BITS, GS, NC>::kOwn];
                 acc.join(tm + lanes, group, it % kGroups, sums);
+                Turn at;
+                at.slot = (it + ns) % p.slots;
+                at.lap = (it + ns) / p.slots;
+                for (int d = 0; d < ads; ++d)
+                    for (int r0 = 0; r0 < p.rows; r0 += p.piece, at.step(1, p.slots)) {
+                        wait(full0 + 8 * at.slot, at.lap & 1);
+                        if (live && row >= r0 && row < r0 + p.piece) {
+                            // (32 bits are enough for the start's place within 16 bytes)
+                            const uint32_t first = (uint32_t(s_ad[z][d]) * uint32_t(p.N) + uint32_t(tl * p.rows + r0)) * uint32_t(p.R) * 2u;
+                            const uint32_t addr = base + at.slot * L.slot + (first & 15u) + (row - r0) * p.R * 2;
+                            // the group's vectors: every third
+#pragma unroll 1
+                            for (uint32_t of = s_of[z][d] & 0x9249u << group; of; of &= of - 1) {
+                                const int t = __ffs(of) - 1;
+                                const float v = __fmul_rn(s_c[z][d], adapter_dot(addr, inner + t * pitch, p.R, piece0));
+#pragma unroll
+                                for (int k = 0; k < Row<BITS, GS, NC>::kOwn; ++k)
+                                    if (t == group + kGroups * k) sums[k] = __fadd_rn(sums[k], v);
+                            }
+                        }
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(empty0 + 8 * at.slot);
+                    }
+                if (over && p.inner_buffers == 1 && lane == 0) mbar_arrive(xfree);
                 if (p.nseg == 1) {
 #pragma unroll
                     for (int i = 0; i < Row<BITS, GS, NC>::kOwn; ++i)

@@ -657,22 +657,6 @@ struct Row {
         }
     }
 
-    // Adds to the sum of vector t, the same in all of a warp: by branches, for it is
-    // rare.
-    __device__ __forceinline__ void add_one(int t, float v) { add_within<0, NC>(t, v); }
-    template <int FROM, int N>
-    __device__ __forceinline__ void add_within(int t, float v)
-    {
-        if constexpr (N == 1) {
-            float lo, hi;
-            unpack2(y[FROM / 2], lo, hi);
-            y[FROM / 2] = FROM & 1 ? pack2(lo, __fadd_rn(hi, v)) : pack2(__fadd_rn(lo, v), hi);
-        } else {
-            if (t < FROM + N / 2) add_within<FROM, N / 2>(t, v);
-            else add_within<FROM + N / 2, N / 2>(t, v);
-        }
-    }
-
     // The three groups' sums of the tile's rows meet in tensor memory (each group
     // its own A columns, `tm` being the first with the warp's lanes): sums[i]
     // becomes the total of vector group + 3 i, added from group `first` on, which
