@@ -174,58 +174,73 @@ __device__ __forceinline__ uint32_t order_of(float v)
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// The expert choice of token t by one warp, whose lane holds every 32nd logit:
-// N of them in registers, or for more than 32 N experts in shared memory (l).
-template <int N>
+__device__ __forceinline__ float logit_of(uint32_t key) { return __uint_as_float(key & 0x80000000u ? key & 0x7fffffffu : ~key); }
+
+constexpr int kFew = 4;  // 32 times as many experts are chosen from in registers
+
+// The expert choice of token t by one warp, whose lane holds every 32nd logit in
+// registers, or for MANY (more than 32 kFew experts) in shared memory (l). Lane j
+// ends with choice j. (Two instances and no exponential in the loop: the code runs
+// once, from a cold cache, and its length is what takes the time.)
+template <bool MANY>
 __device__ __forceinline__ void choose(const MoeParams &p, int t, uint32_t *l, float *w, uint16_t *ids, int lane)
 {
-    uint32_t key[N];
+    uint32_t key[kFew], first = 0, mine = 0, id = 0;
     const float *logits = p.logits + size_t(t) * p.E;
-    const bool many = p.E > 32 * N;
-#pragma unroll
-    for (int i = 0; i < N; ++i) key[i] = !many && i * 32 + lane < p.E ? order_of(__ldcg(logits + i * 32 + lane)) : 0u;
-    if (many)
+    if (MANY) {
         for (int e = lane; e < p.E; e += 32) l[e] = order_of(__ldcg(logits + e));
-    float top = 0.0f, sum = 0.0f, mine = 0.0f;
-    for (int j = 0; j < p.k; ++j) {
-        uint32_t best = 0;
+    } else {
 #pragma unroll
-        for (int i = 0; i < N; ++i) best = max(best, key[i]);
-        if (many)
-            for (int e = lane; e < p.E; e += 32) best = max(best, l[e]);
-        best = __reduce_max_sync(0xffffffffu, best);
-        uint32_t arg = 0xffffffffu;
-#pragma unroll
-        for (int i = N - 1; i >= 0; --i)
-            if (key[i] == best) arg = i * 32 + lane;
-        if (many)
-            for (int e = lane; e < p.E; e += 32)
-                if (l[e] == best) {
-                    arg = e;
-                    break;
-                }
-        arg = __reduce_min_sync(0xffffffffu, arg);
-        const float v = __uint_as_float(best & 0x80000000u ? best & 0x7fffffffu : ~best);
-        if (j == 0) {
-            top = v;
-            if (p.softmax_all) {
-                // over all experts, each lane's in order, then across the lanes
-                for (int e = lane; e < p.E; e += 32) sum = __fadd_rn(sum, top > -INFINITY ? expf(__fsub_rn(__ldcg(logits + e), top)) : 1.0f);
-#pragma unroll
-                for (int d = 16; d; d >>= 1) sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, d));
-            }
-        }
-        // (all logits -inf: equal weights)
-        const float mass = top > -INFINITY ? expf(__fsub_rn(v, top)) : 1.0f;
-        if (lane == j) mine = mass;
-        if (!p.softmax_all) sum = __fadd_rn(sum, mass);
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-            if (!many && arg == uint32_t(i * 32 + lane)) key[i] = 0u;
-        if (many && lane == int(arg % 32)) l[arg] = 0u;
-        if (lane == 0) ids[t * p.k + j] = uint16_t(arg);
+        for (int i = 0; i < kFew; ++i) key[i] = i * 32 + lane < p.E ? order_of(__ldcg(logits + i * 32 + lane)) : 0u;
     }
-    if (lane < p.k) w[t * p.k + lane] = __fdiv_rn(mine, sum);
+#pragma unroll 1
+    for (int j = 0; j < p.k; ++j) {
+        uint32_t best = 0, arg = 0xffffffffu;
+        if (MANY) {
+            for (int e = lane; e < p.E; e += 32) best = max(best, l[e]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kFew; ++i) best = max(best, key[i]);
+        }
+        best = __reduce_max_sync(0xffffffffu, best);
+        if (MANY) {
+            for (int e = lane; e < p.E && arg == 0xffffffffu; e += 32)
+                if (l[e] == best) arg = e;
+        } else {
+#pragma unroll
+            for (int i = kFew - 1; i >= 0; --i)
+                if (key[i] == best) arg = i * 32 + lane;
+        }
+        arg = __reduce_min_sync(0xffffffffu, arg);
+        if (MANY) {
+            if (lane == int(arg % 32)) l[arg] = 0u;
+        } else {
+#pragma unroll
+            for (int i = 0; i < kFew; ++i)
+                if (arg == uint32_t(i * 32 + lane)) key[i] = 0u;
+        }
+        if (j == 0) first = best;
+        if (lane == j) {
+            mine = best;
+            id = arg;
+        }
+    }
+    // (all logits -inf: equal weights)
+    const float top = logit_of(first);
+    auto mass = [&](float v) { return top > -INFINITY ? expf(__fsub_rn(v, top)) : 1.0f; };
+    const float m = lane < p.k ? mass(logit_of(mine)) : 0.0f;
+    float sum = m;
+    if (p.softmax_all) {
+        // over all experts, each lane's in order, then across the lanes
+        sum = 0.0f;
+        for (int e = lane; e < p.E; e += 32) sum = __fadd_rn(sum, mass(__ldcg(logits + e)));
+    }
+#pragma unroll
+    for (int d = 16; d; d >>= 1) sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, d));
+    if (lane < p.k) {
+        ids[t * p.k + lane] = uint16_t(id);
+        w[t * p.k + lane] = __fdiv_rn(m, sum);
+    }
 }
 
 __device__ __forceinline__ float activation(float g, bool gelu)
@@ -285,9 +300,11 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
     __syncthreads();
 
     // ------------------------------------------------------------- routing
-    for (int t = warp; t < p.M; t += kMoeThreads / 32)
-        // (a row of logits for each warp in the ring)
-        choose<4>(p, t, reinterpret_cast<uint32_t *>(smem) + warp * p.E, s_w, s_ids, lane);
+    // (a row of logits for each warp in the ring)
+    if (p.E > 32 * kFew)
+        for (int t = warp; t < p.M; t += kMoeThreads / 32) choose<true>(p, t, reinterpret_cast<uint32_t *>(smem) + warp * p.E, s_w, s_ids, lane);
+    else
+        for (int t = warp; t < p.M; t += kMoeThreads / 32) choose<false>(p, t, nullptr, s_w, s_ids, lane);
     __syncthreads();
     if (warp == 0) {
         // each choice's place among its expert's, in the order of the tokens
