@@ -21,12 +21,23 @@
 // many vectors have it, and each thread adds their products with the inner
 // vectors to the sums it holds. (Threads reading their rows from global memory,
 // 16 bytes at a time, took 16 of a tile's 47 thousand cycles at 16 vectors of
-// rank 64: 168 us for 64 vectors.)
+// rank 64: 168 us for 64 vectors. A third of every product in each group, before
+// the groups' sums meet: 123 us, and 25.1 for 16 vectors where this takes 23.7.)
 //  - Rows go to CTAs in tiles of equal height (a multiple of 8, at most 128): 104
 //    for 15360 rows on 152 SMs.
 //  - K goes to CTAs in ranges of at most 64 subgroups (4096), whose cells of 16
 //    vectors are 128 KB (48 at ranks above 64). Several ranges meet in the workspace: the CTA that
 //    finishes a tile last adds them in their order.
+//  - Passes of 16 vectors follow one another in a CTA, the next one's x on its way
+//    while the last tile's adapters are added; partial sums of ranges are joined a
+//    tile later, so that nobody waits for a ticket. (A CTA for each pass: 135 us for
+//    64 vectors, 32.9 for 24 of 5120 x 5120.)
+// What bounds it: for few vectors the chain of the two kernels' starts, x, first
+// weights and the join; for 16 the workers' instructions (qmv_tile.cuh) and the
+// adapters' code, which runs from a cold instruction cache. Measured (us; bytes it
+// cannot do without, at 6.8 TB/s): 10.2 for one vector of 1024 x 5120 (0.5), 14.4
+// for 4 of 15360 x 3840 (5.2), 22.5 for 13 of 3840 x 15360 (5.9), 116 for 64 of
+// 17408 x 5120 in 2 bits at rank 64 (9.6), 25.3 for 24 of 5120 x 5120.
 // The order of every sum depends on N, K and the rank alone, so a vector's result does not
 // depend on the batch it is in.
 #include <cuda_bf16.h>

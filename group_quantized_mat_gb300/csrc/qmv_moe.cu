@@ -17,8 +17,14 @@
 //     tile of rows, the last CTA adding its sums, cost 2 us an item.)
 //
 // An expert with no token costs nothing, one with several reads its weights once
-// for up to NC of them. What bounds it is the weights' stream while there are
-// many experts, and for one token the chain logits - experts - meeting - sums.
+// for up to NC of them. What bounds it: for few tokens the chain logits - choice -
+// A - meeting - B - meeting - sums, whose code runs from cold caches; for many the
+// workers, which give a slot 550 to 700 cycles where the memory could bring one
+// every 750, and wait for one another over the ring while sums are taken.
+// Measured (us; bytes a token cannot do without, at 6.8 TB/s): 20.7 for one token
+// and 8 of 64 experts of 2048 x 768 (3.2), 38.4 for 5 and 2 of 8 of 3840 x 1920 in
+// 2 bits (5.6), 79 for 16 and 8 of 128 of 2048 x 768 (32), 163 for 48 and 4 of 32
+// of 5120 x 1280 (49).
 //
 // The inner pipeline is qmv_tile.cuh's. A ring slot holds 128 bytes of 128 rows
 // and the slot's subgroups of the item's tokens. h enters the down product with
@@ -48,16 +54,19 @@ constexpr int kMinSlotsMoe = tile::kGroups;
 constexpr int kHalf = 64;        // rows of a box: an item is two
 constexpr int kTermsH = 4;
 constexpr int kSets = 5;         // items whose sums may be on their way
-// One warp brings the weights, four more what is multiplied with them (one warp for
-// all: a slot in 1250 cycles at 6 tokens to an entry, with one gathering warp 1100).
+// One warp brings the weights; four more gather what is multiplied with them and
+// take the items' sums. (One warp for weights and gathering: a slot in 1250 cycles at
+// 6 tokens to an entry, with one gathering warp 1100. Workers that take the sums
+// themselves: 83 and 165 us for 16 and 48 tokens; four warps more for the sums, and
+// 112 registers for the workers: 82 and 164.)
 // Registers move from those and the tensor warps to the workers: 640 x 96 =
 // 384 x 128 + 256 x 48.
 constexpr int kGatherers = 4;
 constexpr int kMoeThreads = tile::kThreads + 32 * kGatherers;
 constexpr int kWorkerRegs = 128, kOtherRegs = 48;
 static_assert(32 * tile::kWorkers * kWorkerRegs + (kMoeThreads - 32 * tile::kWorkers) * kOtherRegs <= kMoeThreads * 96, "registers");
+// Columns of tensor memory for items' sums on their way to the warps that take them.
 constexpr int kExchange = tile::kGroups * tile::kGroupColumns, kExchangeSet = tile::kGroups * 8;
-// columns of tensor memory for items' sums on their way to the warps that take them
 
 struct MoeParams {
     const uint16_t *x, *router, *gu_s, *gu_b, *dn_s, *dn_b;

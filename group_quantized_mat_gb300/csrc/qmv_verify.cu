@@ -19,6 +19,11 @@
 //     sequence's rows, decides how many tokens are accepted and runs its share of
 //     the race on the one row that matters; the last of a sequence's blocks joins
 //     the winners and writes the results.
+//
+// Measured (us; bytes it cannot do without, at 6.8 TB/s): 13.4 for one sequence of 3
+// drafts and 32000 tokens (0.1: the two kernels' chain), 16.9 for 8 x 4 x 50257 fp32
+// from unaligned rows (2.1), 33.5 for 24 x 12 looked-up drafts of 101001 (10), 80 for
+// 64 x 7 x 131072 (42; its 126 million exponentials alone take the SMs 27 us).
 #include <cuda_bf16.h>
 
 #include <cfloat>

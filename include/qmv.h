@@ -355,9 +355,9 @@ QMV_API qmv_status qmv_lora_run(const uint32_t *w_q, const uint16_t *scales, con
  *                    at most QMV_MAX_CHOICES.
  *  flags             QMV_F32_OUT, QMV_MOE_GELU, QMV_MOE_SOFTMAX_ALL.
  *
- * A NaN router logit counts as -inf. Arithmetic: fp32 sums throughout; h is
- * rounded to the nearest 16 bits of significand between the two products; y is
- * rounded once. A token's result does not depend on the other tokens of the call.
+ * A NaN router logit counts as -inf. Arithmetic: fp32 sums throughout; h keeps
+ * 16 bits of significand between the two products (elements far below the largest
+ * of their 64 fewer, down to 2^-30 of it); y is rounded once. A token's result does not depend on the other tokens of the call.
  *
  * Errors: as for qmv_lora_run; QMV_ERR_SHAPE also when inter is not a multiple of
  * group_size or experts x rows x groups reaches 2^31. */
@@ -431,8 +431,9 @@ QMV_API qmv_status qmv_workspace_init(void *workspace, size_t bytes, qmv_stream_
 
 /* ------------------------------------------------------------ diagnostics */
 
-/* Device-side error word of the current device: the one-vector kernel sets
- * bit 0 when a bounded wait for a weight tile ran out and bit 1 when a launch
+/* Device-side error word of the current device: the one-vector kernel and the
+ * operators of a decode step set bit 0 when a bounded wait (for a weight tile, a
+ * tensor-core result, other CTAs) ran out, the one-vector kernel bit 1 when a launch
  * shape breaks its shared-memory ring protocol (neither happens with the
  * library's own launch plans; the output of that launch is then invalid).
  * Synchronizes the device, stores the word in *word and clears it.
