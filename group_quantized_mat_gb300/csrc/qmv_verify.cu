@@ -21,9 +21,9 @@
 //     the winners and writes the results.
 //
 // Measured (us; bytes it cannot do without, at 6.8 TB/s): 13.4 for one sequence of 3
-// drafts and 32000 tokens (0.1: the two kernels' chain), 16.9 for 8 x 4 x 50257 fp32
-// from unaligned rows (2.1), 33.5 for 24 x 12 looked-up drafts of 101001 (10), 80 for
-// 64 x 7 x 131072 (42; its 126 million exponentials alone take the SMs 27 us).
+// drafts and 32000 tokens (0.1: the two kernels' chain), 17.3 for 8 x 4 x 50257 fp32
+// from unaligned rows (2.1), 30.8 for 24 x 12 looked-up drafts of 101001 (10), 60 for
+// 64 x 7 x 131072 (42: rows at 6 TB/s, then 18 us of race).
 #include <cuda_bf16.h>
 
 #include <cfloat>
@@ -154,20 +154,6 @@ __device__ __forceinline__ float larger(float a, float b)
     return d;
 }
 
-// The block's value of a max (over floats) or sum, in all threads.
-__device__ __forceinline__ float block_max(float v, float *scratch)
-{
-#pragma unroll
-    for (int d = 16; d; d >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
-    __syncthreads();
-    if (threadIdx.x % 32 == 0) scratch[threadIdx.x / 32] = v;
-    __syncthreads();
-    v = scratch[0];
-#pragma unroll
-    for (int w = 1; w < kVerifyWarps; ++w) v = fmaxf(v, scratch[w]);
-    return v;
-}
-
 // 16 bytes that start `bytes` (a multiple of 2) into two aligned 16.
 __device__ __forceinline__ uint4 shifted(uint4 a, uint4 b, int bytes)
 {
@@ -224,31 +210,6 @@ __device__ __forceinline__ void load16(uint4 (&x)[N], const uint8_t *base, long 
     } else {
 #pragma unroll
         for (int k = 0; k < N; ++k) x[k] = load16_apart<F32>(base, v0 + k * step, V);
-    }
-}
-
-// Eight elements of a row from v0 on (a multiple of eight) as they count, those
-// past V as -inf.
-template <bool F32>
-__device__ __forceinline__ void load8(const uint8_t *base, long long v0, int V, int off, float (&x)[8])
-{
-    uint4 a[F32 ? 2 : 1];
-    load16<F32, F32 ? 2 : 1>(a, base, v0, F32 ? 4 : 8, V, off);
-    const uint32_t w[4] = {clean<F32>(a[0].x), clean<F32>(a[0].y), clean<F32>(a[0].z), clean<F32>(a[0].w)};
-    if (F32) {
-        const uint4 &b = a[F32 ? 1 : 0];
-        const uint32_t u[4] = {clean<F32>(b.x), clean<F32>(b.y), clean<F32>(b.z), clean<F32>(b.w)};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            x[i] = __uint_as_float(w[i]);
-            x[4 + i] = __uint_as_float(u[i]);
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            x[2 * i] = __uint_as_float(w[i] << 16);
-            x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-        }
     }
 }
 
@@ -426,10 +387,11 @@ __device__ __forceinline__ void block_best(float &v, int &i, float *sv, int *si)
 }
 
 template <bool F32>
-__global__ void __launch_bounds__(kVerifyThreads, 2) verify_emit(const VerifyParams p)
+__global__ void __launch_bounds__(kVerifyThreads, 3) verify_emit(const VerifyParams p)
 {
     __shared__ float s_max[kMaxRows], s_sum[kMaxRows], sv[kVerifyWarps];
-    __shared__ int s_arg[kMaxRows], s_ok[QMV_MAX_DRAFT + 1], si[kVerifyWarps], s_last;
+    __shared__ int s_arg[kMaxRows], s_ok[QMV_MAX_DRAFT + 1], si[kVerifyWarps], s_last, s_bound;
+    if (threadIdx.x == 0) s_bound = 0;
     const int tid = threadIdx.x, b = blockIdx.x / p.races, race = blockIdx.x - b * p.races;
     // (none of these is written by the first kernel)
     const Mode m = mode_of(p, b);
@@ -493,9 +455,12 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_emit(const VerifyPar
         const int cut = n < m.len && !p.draft ? __ldg(p.draft_tokens + size_t(b) * p.S + n) : -1;
         const float *noise = p.noise + (size_t)b * p.ld_noise;
         // A token enters the race by its exact ratio: two exponentials and two
-        // divisions. Most are ruled out before, by approximations that are good to
-        // 1e-5 of p: the warp's best lower bound of a ratio so far against the
-        // token's upper bound. Eight tokens to a lane at a time.
+        // divisions. Most are ruled out before: at first by p alone against the
+        // noise and the block's best lower bound of a ratio so far (one exponential,
+        // no division; 2e-4 off the bound for the approximations' errors), the rest
+        // by the token's upper bound. Eight tokens to a lane at a time. (Bounds of
+        // both kinds for every token: 46 instructions each and 48 of 80 us at
+        // 64 x 131072.)
         const float c = __fmul_rn(m.inv, 1.4426950408889634f), itotal = __fdiv_rn(1.0f, total);
         const float idsum = dtop > -INFINITY ? __fdiv_rn(1.0f, dsum) : 0.0f, dref = dtop > -INFINITY ? dtop : 0.0f;
         const uint8_t *rowb = static_cast<const uint8_t *>(row), *drowb = static_cast<const uint8_t *>(drow);
@@ -503,48 +468,66 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_emit(const VerifyPar
         const int roff = int(reinterpret_cast<uintptr_t>(rowb) & 15), doff = int(reinterpret_cast<uintptr_t>(drowb) & 15);
         const int noff = int(reinterpret_cast<uintptr_t>(noiseb) & 15), lane = tid % 32;
         float bound = 0.0f;
+        constexpr int LW = F32 ? 2 : 1;
         struct Eight {
-            float l[8], d[8], e[8];
+            uint4 l[LW], d[LW], e[2];
         };
         const auto fetch = [&](Eight &t, int share, bool rest) {
             const long long v0 = (long long)share * 256 + lane * 8;
-            load8<F32>(rowb, v0, p.V, roff, t.l);
-            load8<true>(noiseb, v0, p.V, noff, t.e);
-            if (rest && dtop > -INFINITY) load8<F32>(drowb, v0, p.V, doff, t.d);
+            load16<F32, LW>(t.l, rowb, v0, F32 ? 4 : 8, p.V, roff);
+            load16<true, 2>(t.e, noiseb, v0, 4, p.V, noff);
+            if (rest && dtop > -INFINITY) load16<F32, LW>(t.d, drowb, v0, F32 ? 4 : 8, p.V, doff);
             else
 #pragma unroll
-                for (int k = 0; k < 8; ++k) t.d[k] = -INFINITY;
+                for (int k = 0; k < LW; ++k) t.d[k] = F32 ? make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u) : make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u);
+        };
+        const auto word = [](const uint4 &v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; };
+        const auto value = [&](const uint4 (&v)[LW], int k, bool as_it_counts) {
+            uint32_t w = F32 ? word(v[k / 4 * (LW - 1)], k & 3) : word(v[0], k / 2);
+            if (as_it_counts) w = clean<F32>(w);
+            return F32 ? __uint_as_float(w) : __uint_as_float(k & 1 ? w & 0xffff0000u : w << 16);
         };
         const auto race8 = [&](Eight &t, int share, bool rest) {
             const int v0 = share * 256 + lane * 8;
-            if (rest && (cut & ~7) == v0 && cut >= 0)  // the refused token, its draft being certain, has nothing left
+            bound = fmaxf(bound, __int_as_float(*const_cast<volatile int *>(&s_bound)));
+            const float sure = __fmul_rn(bound, 0.9998f);
+            uint32_t left = 0;  // tokens that are not ruled out (nor is what is NaN)
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    if (v0 + k == cut) t.l[k] = -INFINITY;
+            for (int k = 0; k < 8; ++k) {
+                const float pa = __fmul_rn(ex2(__fmul_rn(__fsub_rn(value(t.l, k, false), top), c)), itotal);
+                if (!(pa < __fmul_rn(sure, __uint_as_float(word(t.e[k / 4], k & 3))))) left |= 1u << k;
+            }
+            if (!__any_sync(0xffffffffu, left)) return;
+            if (rest && (cut & ~7) == v0 && cut >= 0) left &= ~(1u << (cut & 7));  // the refused token, its draft being certain, has nothing left
             float upper[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-                const float pa = __fmul_rn(ex2(__fmul_rn(__fsub_rn(t.l[k], top), c)), itotal);
-                const float qa = __fmul_rn(ex2(__fmul_rn(__fsub_rn(t.d[k], dref), c)), idsum);
+                upper[k] = 0.0f;
+                if (!(left >> k & 1)) continue;
+                const float pa = __fmul_rn(ex2(__fmul_rn(__fsub_rn(value(t.l, k, true), top), c)), itotal);
+                const float qa = __fmul_rn(ex2(__fmul_rn(__fsub_rn(value(t.d, k, true), dref), c)), idsum);
                 const float w = __fsub_rn(pa, qa);
-                t.e[k] = fmaxf(t.e[k], FLT_MIN);
+                const float e = fmaxf(__uint_as_float(clean<true>(word(t.e[k / 4], k & 3))), FLT_MIN);
                 // (a reciprocal of more than 2^126 comes out as 0)
-                const float ea = fminf(t.e[k], 8e37f);
+                const float ea = fminf(e, 8e37f);
                 float r;
                 asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(ea));
                 upper[k] = __fmul_rn(__fmaf_rn(1e-5f, pa, w), __fmul_rn(r, 1.0001f));
                 const float lower = __fmul_rn(__fmaf_rn(-1e-5f, pa, w), __fmul_rn(r, 0.9999f));
-                if (t.e[k] == ea) bound = fmaxf(bound, lower);
+                if (e == ea) bound = fmaxf(bound, lower);
             }
 #pragma unroll
             for (int d = 16; d; d >>= 1) bound = fmaxf(bound, __shfl_xor_sync(0xffffffffu, bound, d));
+            if (lane == 0) atomicMax(&s_bound, __float_as_int(bound));  // (not below 0, so ordered as integers)
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
                 if (!(upper[k] > 0.0f) || upper[k] < bound) continue;
-                float w = __fdiv_rn(expf(__fmul_rn(__fsub_rn(t.l[k], top), m.inv)), total);
-                if (t.d[k] > -INFINITY) w = __fsub_rn(w, __fdiv_rn(expf(__fmul_rn(__fsub_rn(t.d[k], dtop), m.inv)), dsum));
+                const float l = value(t.l, k, true), d = value(t.d, k, true);
+                const float e = fmaxf(__uint_as_float(clean<true>(word(t.e[k / 4], k & 3))), FLT_MIN);
+                float w = __fdiv_rn(expf(__fmul_rn(__fsub_rn(l, top), m.inv)), total);
+                if (d > -INFINITY) w = __fsub_rn(w, __fdiv_rn(expf(__fmul_rn(__fsub_rn(d, dtop), m.inv)), dsum));
                 if (w > 0.0f) {
-                    const float ratio = __fdiv_rn(w, t.e[k]);
+                    const float ratio = __fdiv_rn(w, e);
                     if (better(ratio, v0 + k, best, token)) {
                         best = ratio;
                         token = v0 + k;
@@ -591,6 +574,8 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_emit(const VerifyPar
             // p has nothing that q has not: p itself
             bound = 0.0f;
             best = -1.0f;
+            if (tid == 0) s_bound = 0;
+            __syncthreads();
             run(tid / 32, kVerifyWarps, false);
             block_best(best, token, sv, si);
         }
@@ -608,10 +593,11 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_emit(const VerifyPar
     if (tid == 0) p.accepted[b] = n;
 }
 
-// Parts of a row: at least a piece each. Blocks of the race: at most two for each
+// Parts of a row: at least a piece each. Blocks of the race: at most three for each
 // of 152 SMs (one wave), each at least kRace tokens (every block joins the parts of
-// its sequence's rows for itself: with 4096 blocks for 64 x 131072 the race took
-// 85 us, with 1216 50).
+// its sequence's rows for itself, and its warps start without a bound: for 64 x 131072
+// the whole call took 69 us with at most 304 blocks, 64.5 with 456, 73 with 912; and
+// 60 with 456 whose warps share their bound).
 struct Split {
     int nparts, races;
 };
@@ -623,7 +609,7 @@ Split split(int B, int V, bool f32)
     s.nparts = (V + elems - 1) / elems;
     if (s.nparts > kMaxParts) s.nparts = kMaxParts;
     s.races = (V + kRace - 1) / kRace;
-    const int blocks = B < 304 ? 304 / B : 1;
+    const int blocks = B < 456 ? 456 / B : 1;
     if (s.races > blocks) s.races = blocks;
     return s;
 }
