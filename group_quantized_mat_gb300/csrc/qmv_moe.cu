@@ -54,17 +54,17 @@ constexpr int kMinSlotsMoe = tile::kGroups;
 constexpr int kHalf = 64;        // rows of a box: an item is two
 constexpr int kTermsH = 4;
 constexpr int kSets = 5;         // items whose sums may be on their way
-// One warp brings the weights; four more gather what is multiplied with them and
-// take the items' sums. (One warp for weights and gathering: a slot in 1250 cycles at
-// 6 tokens to an entry, with one gathering warp 1100. Workers that take the sums
-// themselves: 83 and 165 us for 16 and 48 tokens; four warps more for the sums, and
-// 112 registers for the workers: 82 and 164.)
-// Registers move from those and the tensor warps to the workers: 640 x 96 =
-// 384 x 128 + 256 x 48.
-constexpr int kGatherers = 4;
-constexpr int kMoeThreads = tile::kThreads + 32 * kGatherers;
-constexpr int kWorkerRegs = 128, kOtherRegs = 48;
-static_assert(32 * tile::kWorkers * kWorkerRegs + (kMoeThreads - 32 * tile::kWorkers) * kOtherRegs <= kMoeThreads * 96, "registers");
+// Warps: the workers; a tensor warp for each group and one that brings weights;
+// four that gather what is multiplied with them; four that take the items' sums.
+// (One warp for weights and gathering: a slot in 1250 cycles at 6 tokens to an
+// entry. Workers that form h themselves hold up the ring's slots meanwhile, and
+// gatherers that do starve it: 83 and 81 us for 16 tokens.)
+// Registers move to the workers: 768 x 80 = 384 x 112 + 128 x (40 + 40 + 64).
+constexpr int kGatherers = 4, kTakers = 4;
+constexpr int kGather0 = tile::kWorkers + tile::kGroups + 1, kTake0 = kGather0 + kGatherers;
+constexpr int kMoeThreads = 32 * (kTake0 + kTakers);
+constexpr int kWorkerRegs = 112, kOtherRegs = 40, kTakerRegs = 64;
+static_assert(384 * kWorkerRegs + 256 * kOtherRegs + 128 * kTakerRegs <= kMoeThreads * 80, "registers");
 // Columns of tensor memory for items' sums on their way to the warps that take them.
 constexpr int kExchange = tile::kGroups * tile::kGroupColumns, kExchangeSet = tile::kGroups * 8;
 
@@ -78,7 +78,7 @@ struct MoeParams {
     float2 *xmeta;      // [M][subs_a] (sum, f)
     uint8_t *h;         // [entry][slot of B][subgroups' cells, subgroups' meta]
     float *partials;    // [pair][K]
-    unsigned *counters; // CTAs done with A, and with B
+    unsigned *counters; // CTAs done with B, then for each entry its items of A that are done
     unsigned *err;
     int M, K, I, E, k, gs, nc, f32_out, gelu, softmax_all;
     int Sa, NSa, Ga, Sb, NSb, Gb;  // subgroups, slots and groups of a row of A and of B
@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(kLogitThreads) moe_logits(const MoeParams p)
     grid_launch_dependents();
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     if (blockIdx.x == 0)
-        for (int i = tid; i < 2; i += kLogitThreads) p.counters[i] = 0u;
+        for (int i = tid; i < 1 + p.max_entries; i += kLogitThreads) p.counters[i] = 0u;
     if (int(blockIdx.x) < p.stage_blocks) {
         // eight threads for each (token, subgroup)
         const int subs = p.NSa * tile::slot_subs(BITS);
@@ -380,12 +380,15 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
     struct Items {
         int entry, tl, entries, tiles, dentry, dtl;
     };
-    auto items_of = [&](int tiles) {
+    // (`before`: items of the part before, whose round the first ones fill up)
+    auto items_of = [&](int tiles, int before = 0) {
         Items s;
         s.entries = s_entries;
         s.tiles = tiles;
-        s.entry = int(blockIdx.x) / tiles;
-        s.tl = int(blockIdx.x) - s.entry * tiles;
+        int at = int(blockIdx.x) - before % grid;
+        if (at < 0) at += grid;
+        s.entry = at / tiles;
+        s.tl = at - s.entry * tiles;
         s.dentry = grid / tiles;
         s.dtl = grid - s.dentry * tiles;
         return s;
@@ -429,7 +432,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
         while (global_timer_ns() - t0 < 1000000ull) {}
     };
 
-    if (warp >= kWorkers) {
+    if (warp >= kWorkers && warp < kTake0) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         if (warp == kWorkers + kGroups) {
             // -------------------------------------- the weights' side of the slots
@@ -490,7 +493,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
                     ok = __all_sync(0xffffffffu, ok);
                 }
             }
-            for (Items is = items_of(p.tiles_b); is.entry < is.entries && ok; advance(is)) {
+            for (Items is = items_of(p.tiles_b, s_entries * p.tiles_a); is.entry < is.entries && ok; advance(is)) {
                 const Item im = item_of(is);
                 const int row = im.tl * kTileRows;
                 int left = 0;
@@ -511,18 +514,17 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
                 }
             }
             if (!ok && lane == 0) drain();
-        } else if (warp > kWorkers + kGroups) {
-            // ------------ the vectors' side of the slots, and what comes of the items' sums
-            Turn turn, mturn, set;
+        } else if (warp >= kGather0) {
+            // ------------------------------------------------- the vectors' side of the slots
+            Turn turn, mturn;
             bool ok = true;
-            const int which = warp - kWorkers - kGroups - 1, row = which * 32 + lane;
-            const uint32_t ex0 = tm + (uint32_t(which * 32) << 16) + kExchange;
+            const int which = warp - kGather0;
             constexpr int MINE = (NC + kGatherers - 1) / kGatherers;
             // the lane's 16 bytes of each token's: subgroup, term and piece
             const int gsub = lane >> 3, gh = lane >> 2 & 1, gpc = lane & 3;
             // and the token, subgroup and half of its sums
             const int msub = lane / 2 % SUBS, mf = lane & 1, mtok = which * (16 / SUBS) + lane / (2 * SUBS);
-            auto gather = [&](const Items &is) {
+            for (Items is = items_of(p.tiles_a); is.entry < is.entries && ok; advance(is)) {
                 const Item im = item_of(is);
                 // where each token's bytes come from, slot by slot
                 const uint8_t *from[MINE];
@@ -555,140 +557,28 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
                     mfrom += SUBS * 2;
                     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(full) : "memory");
                 }
-            };
-            uint8_t *own = smem + L.cell;  // an item's cell of h and its sums
-            float2 *red = reinterpret_cast<float2 *>(smem + L.red);
-            const int half = lane >> 4, r = which * 16 + (lane & 15);  // as in the workers
-            auto form_h = [&](const Items &is) {
-                const Item im = item_of(is);
-                float sums[NC];
-                Row<BITS, GS, NC, 2>::take(wait, ex0 + set.slot * kExchangeSet, joined0 + 8 * set.slot, freed0 + 8 * set.slot, set.lap, lane, sums);
-                set.step(1, kSets);
-                if (row == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the last item's h has left
-                // lanes of gate rows form h of the even tokens, those of up rows of the odd
-                float h[NC / 2];
-#pragma unroll
-                for (int i = 0; i < NC / 2; ++i) {
-                    const float mine = half ? sums[2 * i + 1] : sums[2 * i];
-                    const float other = __shfl_xor_sync(0xffffffffu, half ? sums[2 * i] : sums[2 * i + 1], 16);
-                    h[i] = __fmul_rn(activation(half ? other : mine, p.gelu), half ? mine : other);
-                }
-                // sum and largest exponent of the 64
-#pragma unroll
-                for (int i = 0; i < NC / 2; ++i) {
-                    const uint32_t E = __reduce_max_sync(0xffffu << (lane & 16), max(1u, (__float_as_uint(h[i]) >> 23) & 0xffu));
-                    float sum = h[i];
-#pragma unroll
-                    for (int d = 8; d; d >>= 1) sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, d));
-                    if ((lane & 15) == 0) red[(half * (NC / 2) + i) * 4 + (warp & 3)] = make_float2(sum, __uint_as_float(E));
-                }
-                named_sync(2, 32 * kGatherers);
-                // the element's byte of its row, in the order of the masks
-                const int pc = r >> 4, e = r & 15;
-                const int at = BITS == 4 ? (e >> 3) * 8 + (e & 1) * 4 + ((e & 7) >> 1) : (e & 3) * 4 + (e >> 2);
-#pragma unroll
-                for (int i = 0; i < NC / 2; ++i) {
-                    const int j = 2 * i + half;
-                    const float4 r0 = reinterpret_cast<const float4 *>(red)[(half * (NC / 2) + i) * 2];
-                    const float4 r1 = reinterpret_cast<const float4 *>(red)[(half * (NC / 2) + i) * 2 + 1];
-                    const int E = int(max(max(__float_as_uint(r0.y), __float_as_uint(r0.w)), max(__float_as_uint(r1.y), __float_as_uint(r1.w))));
-                    const int pw = 134 - E;
-                    float v = __fmul_rn(__fmul_rn(h[i], exp2i(pw / 2)), exp2i(pw - pw / 2));
-                    if (BITS == 2 && (e & 1)) v = __fmul_rn(v, 0.25f);
-#pragma unroll
-                    for (int t = 0; t < kTermsH; ++t) {
-                        const uint32_t b = to_e4m3x2(v, 0.0f);
-                        float back, none;
-                        from_e4m3x2(b, back, none);
-                        v = __fmul_rn(__fsub_rn(v, back), 32.0f);
-                        own[operand_offset(operand_index(j, t, kTermsH), pc) + at] = uint8_t(b);
-                    }
-                    if (r == 0) {
-                        float *m = reinterpret_cast<float *>(own + CB + i * 16) + half;
-                        m[0] = __fadd_rn(__fadd_rn(r0.x, r0.z), __fadd_rn(r1.x, r1.z));
-                        m[2] = exp2i(min(E - 125, 127));
-                    }
-                }
-                uint8_t *slot_h = p.h + (size_t(im.entry) * p.NSb + im.tl / SUBS) * (SUBS * (CB + MB));
-                // subgroups that fill the last slot
-                if (im.tl == p.tiles_a - 1 && p.Sb % SUBS) {
-                    for (int sub = p.Sb % SUBS; sub < SUBS; ++sub) {
-                        uint32_t *c = reinterpret_cast<uint32_t *>(slot_h + sub * CB), *m = reinterpret_cast<uint32_t *>(slot_h + SUBS * CB + sub * MB);
-                        for (int i = row; i < CB / 4; i += 32 * kGatherers) c[i] = 0u;
-                        for (int i = row; i < MB / 4; i += 32 * kGatherers) m[i] = 0u;
-                    }
-                    asm volatile("fence.proxy.async;" ::: "memory");
-                    __threadfence();
-                }
-                fence_proxy_async_smem();
-                named_sync(2, 32 * kGatherers);
-                if (row == 0) {
-                    const uint32_t from = smem_u32(own);
-                    bulk_store(slot_h + im.tl % SUBS * CB, from, CB);
-                    bulk_store(slot_h + SUBS * CB + im.tl % SUBS * MB, from + CB, MB);
-                    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-                }
-            };
-            // The sums of an item are taken when the ring has been filled beyond it.
-            // (The four warps meet in every item, also after a wait has run out.)
-            auto behind = [&](int slots) { return min((p.slots + slots - 1) / slots, kSets - 1); };
-            int ahead = 0, most = behind(p.NSa);
-            for (Items is = items_of(p.tiles_a), es = is; es.entry < es.entries;) {
-                if (is.entry < is.entries) {
-                    gather(is);
-                    advance(is);
-                    if (++ahead <= most) continue;
-                }
-                form_h(es);
-                advance(es);
-                --ahead;
             }
             asm volatile("cp.async.wait_all;" ::: "memory");
-            // (A count for each entry, raised after each item, let B start on early
-            // entries; but the release of each took thousands of cycles under the
-            // stream of weights: 97 and 181 us for 16 and 48 tokens.)
-            if (row == 0) {
-                asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-                asm volatile("fence.proxy.async;" ::: "memory");
-                asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(p.counters) : "memory");
-                ok = ok && meet(p.counters, grid);
-                asm volatile("fence.proxy.async;" ::: "memory");
-            }
-            ahead = 0;
-            most = behind(p.NSb);
-            for (Items is = items_of(p.tiles_b), es = is; es.entry < es.entries;) {
-                if (is.entry < is.entries) {
+            if (ok && which == 0 && lane == 0) {
+                int ready = -1;
+                for (Items is = items_of(p.tiles_b, s_entries * p.tiles_a); is.entry < is.entries && ok; advance(is)) {
                     const uint8_t *h = p.h + size_t(is.entry) * p.NSb * (SUBS * (CB + MB));
-                    if (row == 0)
-                        for (int i = 0; i < p.NSb && ok; ++i, h += SUBS * (CB + MB), turn.step(1, p.slots), mturn.step(1, p.slots + kGroups)) {
-                            ok = turn.lap == 0 || wait(empty0 + 8 * turn.slot, (turn.lap - 1) & 1);
-                            const uint32_t full = full0 + 8 * turn.slot;
-                            if (!ok) break;
-                            // (one of the lanes' arrivals, and for the others, which arrive of their own in A)
-                            mbar_arrive_expect_tx(full, SUBS * (CB + MB));
-                            mbar_arrive_many(full, 32 * kGatherers - 1);
-                            bulk_load_plain(base + turn.slot * L.slot + L.cells, h, SUBS * CB, full);
-                            bulk_load_plain(base + L.meta + mturn.slot * (SUBS * MB), h + SUBS * CB, SUBS * MB, full);
-                        }
-                    __syncwarp();
-                    advance(is);
-                    if (++ahead <= most) continue;
+                    if (ready != is.entry) {
+                        ready = is.entry;
+                        ok = meet(p.counters + 1 + ready, p.tiles_a);
+                        asm volatile("fence.proxy.async;" ::: "memory");
+                    }
+                    for (int i = 0; i < p.NSb && ok; ++i, h += SUBS * (CB + MB), turn.step(1, p.slots), mturn.step(1, p.slots + kGroups)) {
+                        ok = turn.lap == 0 || wait(empty0 + 8 * turn.slot, (turn.lap - 1) & 1);
+                        const uint32_t full = full0 + 8 * turn.slot;
+                        if (!ok) break;
+                        // (one of the lanes' arrivals, and for the others, which arrive of their own in A)
+                        mbar_arrive_expect_tx(full, SUBS * (CB + MB));
+                        mbar_arrive_many(full, 32 * kGatherers - 1);
+                        bulk_load_plain(base + turn.slot * L.slot + L.cells, h, SUBS * CB, full);
+                        bulk_load_plain(base + L.meta + mturn.slot * (SUBS * MB), h + SUBS * CB, SUBS * MB, full);
+                    }
                 }
-                const Item im = item_of(es);
-                const int n = im.tl * kTileRows + row;
-                float sums[NC];
-                Row<BITS, GS, NC, kTermsH>::take(wait, ex0 + set.slot * kExchangeSet, joined0 + 8 * set.slot, freed0 + 8 * set.slot, set.lap, lane, sums);
-                set.step(1, kSets);
-#pragma unroll
-                for (int j = 0; j < NC; ++j)
-                    if (j < im.count && n < p.K) __stcg(p.partials + size_t(im.pair + j) * p.K + n, sums[j]);
-                advance(es);
-                --ahead;
-            }
-            named_sync(2, 32 * kGatherers);
-            if (row == 0) {
-                __threadfence();  // (of what the barrier ordered before it, too)
-                asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(p.counters + 1) : "memory");
             }
             if (!ok && lane == 0) drain();
         } else if (warp >= kWorkers && warp < kWorkers + kGroups) {
@@ -707,7 +597,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
                 }
                 Pipe pb = Pipe::make<NC, kTermsH>(tm, 0, stored0, ready0, group);
                 pb.steps = pipe.steps;
-                for (Items is = items_of(p.tiles_b); is.entry < is.entries; advance(is), turn.step(p.NSb, p.slots)) {
+                for (Items is = items_of(p.tiles_b, s_entries * p.tiles_a); is.entry < is.entries; advance(is), turn.step(p.NSb, p.slots)) {
                     Turn at = turn;
                     const int i0 = first_slot(group, turn.slot);
                     at.step(i0, p.slots);
@@ -715,6 +605,115 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
                         multiply_slot<BITS, NC, kTermsH>(wait, pb, base + at.slot * L.slot + L.cells, empty0 + 8 * at.slot);
                 }
             }
+        }
+    } else if (warp >= kTake0) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTakerRegs));
+        // ------------------------------------------- what comes of the items' sums
+        // (The four warps meet in every item, also after a wait has run out.)
+        Turn set;
+        const int row = (warp - kTake0) * 32 + lane;
+        const uint32_t ex0 = tm + (uint32_t((warp - kTake0) * 32) << 16) + kExchange;
+        uint8_t *own = smem + L.cell;  // an item's cell of h and its sums
+        float2 *red = reinterpret_cast<float2 *>(smem + L.red);
+        const int half = lane >> 4, r = (warp - kTake0) * 16 + (lane & 15);  // as in the workers
+        // B may start on an entry when all its items are counted. (A release takes
+        // thousands of cycles under the stream of weights; by the workers, or by
+        // warps that gather as well, it cost more than it gave.)
+        int written = -1;  // entry of the last item
+        auto publish = [&]() {
+            if (row == 0 && written >= 0) {
+                asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+                asm volatile("fence.proxy.async;" ::: "memory");
+                asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(p.counters + 1 + written) : "memory");
+            }
+            written = -1;
+        };
+        for (Items is = items_of(p.tiles_a); is.entry < is.entries; advance(is)) {
+            const Item im = item_of(is);
+            float sums[NC];
+            Row<BITS, GS, NC, 2>::take(wait, ex0 + set.slot * kExchangeSet, joined0 + 8 * set.slot, freed0 + 8 * set.slot, set.lap, lane, sums);
+            set.step(1, kSets);
+            publish();  // the last item's h, which has long been written
+            // lanes of gate rows form h of the even tokens, those of up rows of the odd
+            float h[NC / 2];
+#pragma unroll
+            for (int i = 0; i < NC / 2; ++i) {
+                const float mine = half ? sums[2 * i + 1] : sums[2 * i];
+                const float other = __shfl_xor_sync(0xffffffffu, half ? sums[2 * i] : sums[2 * i + 1], 16);
+                h[i] = __fmul_rn(activation(half ? other : mine, p.gelu), half ? mine : other);
+            }
+            // sum and largest exponent of the 64
+#pragma unroll
+            for (int i = 0; i < NC / 2; ++i) {
+                const uint32_t E = __reduce_max_sync(0xffffu << (lane & 16), max(1u, (__float_as_uint(h[i]) >> 23) & 0xffu));
+                float sum = h[i];
+#pragma unroll
+                for (int d = 8; d; d >>= 1) sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, d));
+                if ((lane & 15) == 0) red[(half * (NC / 2) + i) * 4 + (warp & 3)] = make_float2(sum, __uint_as_float(E));
+            }
+            named_sync(2, 32 * kTakers);
+            // the element's byte of its row, in the order of the masks
+            const int pc = r >> 4, e = r & 15;
+            const int at = BITS == 4 ? (e >> 3) * 8 + (e & 1) * 4 + ((e & 7) >> 1) : (e & 3) * 4 + (e >> 2);
+#pragma unroll
+            for (int i = 0; i < NC / 2; ++i) {
+                const int j = 2 * i + half;
+                const float4 r0 = reinterpret_cast<const float4 *>(red)[(half * (NC / 2) + i) * 2];
+                const float4 r1 = reinterpret_cast<const float4 *>(red)[(half * (NC / 2) + i) * 2 + 1];
+                const int E = int(max(max(__float_as_uint(r0.y), __float_as_uint(r0.w)), max(__float_as_uint(r1.y), __float_as_uint(r1.w))));
+                const int pw = 134 - E;
+                float v = __fmul_rn(__fmul_rn(h[i], exp2i(pw / 2)), exp2i(pw - pw / 2));
+                if (BITS == 2 && (e & 1)) v = __fmul_rn(v, 0.25f);
+#pragma unroll
+                for (int t = 0; t < kTermsH; ++t) {
+                    const uint32_t b = to_e4m3x2(v, 0.0f);
+                    float back, none;
+                    from_e4m3x2(b, back, none);
+                    v = __fmul_rn(__fsub_rn(v, back), 32.0f);
+                    own[operand_offset(operand_index(j, t, kTermsH), pc) + at] = uint8_t(b);
+                }
+                if (r == 0) {
+                    float *m = reinterpret_cast<float *>(own + CB + i * 16) + half;
+                    m[0] = __fadd_rn(__fadd_rn(r0.x, r0.z), __fadd_rn(r1.x, r1.z));
+                    m[2] = exp2i(min(E - 125, 127));
+                }
+            }
+            uint8_t *slot_h = p.h + (size_t(im.entry) * p.NSb + im.tl / SUBS) * (SUBS * (CB + MB));
+            // subgroups that fill the last slot
+            if (im.tl == p.tiles_a - 1 && p.Sb % SUBS) {
+                for (int sub = p.Sb % SUBS; sub < SUBS; ++sub) {
+                    uint32_t *c = reinterpret_cast<uint32_t *>(slot_h + sub * CB), *m = reinterpret_cast<uint32_t *>(slot_h + SUBS * CB + sub * MB);
+                    for (int i = row; i < CB / 4; i += 32 * kTakers) c[i] = 0u;
+                    for (int i = row; i < MB / 4; i += 32 * kTakers) m[i] = 0u;
+                }
+                asm volatile("fence.proxy.async;" ::: "memory");
+                __threadfence();
+            }
+            fence_proxy_async_smem();
+            named_sync(2, 32 * kTakers);
+            if (row == 0) {
+                const uint32_t from = smem_u32(own);
+                bulk_store(slot_h + im.tl % SUBS * CB, from, CB);
+                bulk_store(slot_h + SUBS * CB + im.tl % SUBS * MB, from + CB, MB);
+                asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+            }
+            written = im.entry;
+        }
+        publish();
+        for (Items is = items_of(p.tiles_b, s_entries * p.tiles_a); is.entry < is.entries; advance(is)) {
+            const Item im = item_of(is);
+            const int n = im.tl * kTileRows + row;
+            float sums[NC];
+            Row<BITS, GS, NC, kTermsH>::take(wait, ex0 + set.slot * kExchangeSet, joined0 + 8 * set.slot, freed0 + 8 * set.slot, set.lap, lane, sums);
+            set.step(1, kSets);
+#pragma unroll
+            for (int j = 0; j < NC; ++j)
+                if (j < im.count && n < p.K) __stcg(p.partials + size_t(im.pair + j) * p.K + n, sums[j]);
+        }
+        named_sync(2, 32 * kTakers);
+        if (row == 0) {
+            __threadfence();  // (of what the barrier ordered before it, too)
+            asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(p.counters) : "memory");
         }
     } else {
         // ----------------------------------------------------------- workers
@@ -779,7 +778,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
         }
         Pipe pb = Pipe::make<NC, kTermsH>(tm, lanes, stored0, ready0, group);
         pb.steps = pipe.steps;
-        for (Items is = items_of(p.tiles_b); is.entry < is.entries; advance(is)) {
+        for (Items is = items_of(p.tiles_b, s_entries * p.tiles_a); is.entry < is.entries; advance(is)) {
             const Item im = item_of(is);
             const int c = first_slot(group, turn.slot);
             Row<BITS, GS, NC, kTermsH> acc;
@@ -787,7 +786,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
             give(acc, c);
         }
         if (tid == 0) {
-            (void)meet(p.counters + 1, grid);
+            (void)meet(p.counters, grid);
             __threadfence();
         }
         named_sync(1, 32 * kWorkers);
@@ -868,7 +867,9 @@ bool fit(MoeParams &p, int bits)
     p.sb_block = p.sba.block > p.sbb.block ? p.sba.block : p.sbb.block;
     p.slots = kMaxSlotsMoe;
     while (p.slots > kMinSlotsMoe && moe_layout(p, bits, p.nc).total > kSmemMoe) p.slots -= tile::kGroups;
-    return moe_layout(p, bits, p.nc).total <= kSmemMoe;
+    // (the routing's rows of logits lie before the lists)
+    const MoeLayout l = moe_layout(p, bits, p.nc);
+    return l.total <= kSmemMoe && l.lists >= kMoeThreads / 32 * p.E * 4;
 }
 
 MoeParams plan_moe(int M, int K, int I, int E, int k, int bits, int gs, MoeSizes &z)
@@ -895,7 +896,7 @@ MoeParams plan_moe(int M, int K, int I, int E, int k, int bits, int gs, MoeSizes
     z.xmeta = up256(size_t(M) * p.NSa * subs * 8);
     z.h = up256(hs * (tile::cell_bytes(p.nc, kTermsH) + tile::meta_bytes(p.nc)));
     z.partials = up256(size_t(pairs) * K * 4);
-    z.counters = up256(2 * 4);
+    z.counters = up256((1 + size_t(p.max_entries)) * 4);
     z.total = z.logits + z.rows + z.xmeta + z.h + z.partials + z.counters;
     return p;
 }
