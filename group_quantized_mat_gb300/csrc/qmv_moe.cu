@@ -11,20 +11,23 @@
 //       A. 64 rows of an expert's gate and the 64 of its up product, for up to NC
 //          of its tokens: activation, and h as operand bytes to the workspace;
 //       B. 128 rows of an expert's down product, sums to the workspace.
-//     Between A and B all CTAs meet (one counter); the weights of the first B
-//     items are on their way to the ring meanwhile. After B they meet again, and
-//     share the sums over each token's choices, in their order. (A ticket for each
-//     tile of rows, the last CTA adding its sums, cost 2 us an item.)
+//     An entry (an expert and up to NC of its tokens) has a count of its items of
+//     A that are done; B takes it when all are, its weights already on their way.
+//     After B all CTAs meet and share the sums over each token's choices, in their
+//     order. (A ticket for each tile of rows, the last CTA adding its sums, cost
+//     2 us an item; a meeting of all CTAs between A and B 163 us for 48 tokens
+//     where this takes 157.)
 //
 // An expert with no token costs nothing, one with several reads its weights once
 // for up to NC of them. What bounds it: for few tokens the chain logits - choice -
-// A - meeting - B - meeting - sums, whose code runs from cold caches; for many the
-// workers, which give a slot 550 to 700 cycles where the memory could bring one
-// every 750, and wait for one another over the ring while sums are taken.
-// Measured (us; bytes a token cannot do without, at 6.8 TB/s): 20.7 for one token
-// and 8 of 64 experts of 2048 x 768 (3.2), 38.4 for 5 and 2 of 8 of 3840 x 1920 in
-// 2 bits (5.6), 79 for 16 and 8 of 128 of 2048 x 768 (32), 163 for 48 and 4 of 32
-// of 5120 x 1280 (49).
+// A - counts - B - meeting - sums, whose code runs from cold caches; for many the
+// ring: 6 slots (9 with 4 tokens to an entry) are all that fits beside the cells,
+// and a slot is taken from its request to the end of its step, 6 to 8 thousand
+// cycles under load.
+// Measured (us; bytes a call cannot do without, at 6.8 TB/s): 20.8 for one token
+// and 8 of 64 experts of 2048 x 768 (3.2), 36.9 for 5 and 2 of 8 of 3840 x 1920 in
+// 2 bits (5.6), 79 for 16 and 8 of 128 of 2048 x 768 (32; A runs at 5.8 TB/s with
+// scales and biases), 157 for 48 and 4 of 32 of 5120 x 1280 (49).
 //
 // The inner pipeline is qmv_tile.cuh's. A ring slot holds 128 bytes of 128 rows
 // and the slot's subgroups of the item's tokens. h enters the down product with
@@ -57,8 +60,9 @@ constexpr int kSets = 5;         // items whose sums may be on their way
 // Warps: the workers; a tensor warp for each group and one that brings weights;
 // four that gather what is multiplied with them; four that take the items' sums.
 // (One warp for weights and gathering: a slot in 1250 cycles at 6 tokens to an
-// entry. Workers that form h themselves hold up the ring's slots meanwhile, and
-// gatherers that do starve it: 83 and 81 us for 16 tokens.)
+// entry. Workers that form h themselves: 83 and 165 us for 16 and 48 tokens;
+// gatherers that do: 79 and 163, as with takers, but these can also afford to count
+// each item, a release of thousands of cycles under the stream of weights.)
 // Registers move to the workers: 768 x 80 = 384 x 112 + 128 x (40 + 40 + 64).
 constexpr int kGatherers = 4, kTakers = 4;
 constexpr int kGather0 = tile::kWorkers + tile::kGroups + 1, kTake0 = kGather0 + kGatherers;
