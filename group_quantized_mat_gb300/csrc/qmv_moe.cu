@@ -25,7 +25,7 @@
 // and a slot is taken from its request to the end of its step, 6 to 8 thousand
 // cycles under load.
 // Measured (us; bytes a call cannot do without, at 6.8 TB/s): 20.8 for one token
-// and 8 of 64 experts of 2048 x 768 (3.2), 36.9 for 5 and 2 of 8 of 3840 x 1920 in
+// and 8 of 64 experts of 2048 x 768 (3.2), 39 for 5 and 2 of 8 of 3840 x 1920 in
 // 2 bits (5.6), 79 for 16 and 8 of 128 of 2048 x 768 (32; A runs at 5.8 TB/s with
 // scales and biases), 157 for 48 and 4 of 32 of 5120 x 1280 (49).
 //
