@@ -47,24 +47,18 @@
 
 #include "qmv.h"
 #include "qmv_launch.cuh"
+#include "qmv_lora_plan.h"
 #include "qmv_tile.cuh"
 
 namespace qmv {
 namespace {
 
+using namespace lora;
+
 constexpr int kPrepareThreads = 256;
-constexpr int kMaxSlotsLora = 12;
-constexpr int kSmem = 225 * 1024;  // beside 2 KB of static lists
-constexpr int kMaxK = 1 << 16;
-// Subgroups of a range of K at most. The ring's three slots, a range's cells of 16
-// vectors, its scales and biases and the inner vectors have to fit at 128 rows.
-__host__ __device__ constexpr int range_subs(int rank) { return rank <= 64 ? 64 : 48; }
-constexpr int kPass = 16;       // vectors that one read of the weights serves
-constexpr int kPasses = QMV_MAX_M / kPass;
-constexpr int kSms = 152;       // for orders of sums, which depend on no device
 constexpr int kBefore = 3;      // slots of weights asked for before staged x (no more than a ring has)
 
-struct LoraParams {
+struct LoraParams : LoraShape {
     const uint16_t *scales, *biases, *x, *a, *b;
     const int32_t *adapter;
     const float *c;
@@ -75,21 +69,8 @@ struct LoraParams {
     float *partials;     // [pass][nseg][nc][N], with nseg > 1
     unsigned *counters;  // [pass][tiles], with nseg > 1
     unsigned *err;
-    int M, N, K, G, gs, L, R, f32_out;
-    int S;       // subgroups of a row
-    int NS;      // slots of a row
-    int subs;    // NS slots' subgroups (those past S are staged as zeros)
-    int nseg;    // ranges of K
-    int range;   // slots of the longest range
-    int rows, tiles, grid_rows;
-    int piece;   // rows of an adapter's B that a ring slot holds
-    int nc, slots, stage_blocks, sb_buffers, inner_buffers;
-    int grid_passes;  // passes that are at work at a time
-    tile::Affines sb;
+    int L, f32_out, stage_blocks;
 };
-
-// Floats from an inner vector to the next, so that all of a pass's are one bulk copy.
-__host__ __device__ constexpr int inner_pitch(int rank) { return (rank + 7) & ~7; }
 
 template <int BITS, int NC>
 __global__ void __launch_bounds__(kPrepareThreads) lora_prepare(const LoraParams p)
@@ -151,31 +132,6 @@ __global__ void __launch_bounds__(kPrepareThreads) lora_prepare(const LoraParams
         for (int j = 1; j < kPrepareThreads / 32; ++j) s = __fadd_rn(s, part[j]);
         p.inner[size_t(m) * inner_pitch(p.R) + r] = s;
     }
-}
-
-struct Layout {
-    int slots, slot, x, meta, sb, inner, inner_bytes, bars, misc, total;
-};
-
-__host__ __device__ inline Layout layout(const LoraParams &p, int bits, int nc)
-{
-    const int subs = p.range * tile::slot_subs(bits);
-    Layout l;
-    l.slots = 0;
-    l.slot = p.rows * tile::kSlotBytes;
-    // a tile of fewer than 128 rows reads on past its slot's end
-    l.x = p.slots * l.slot;
-    if (l.x < (p.slots - 1) * l.slot + tile::kTileRows * tile::kSlotBytes)
-        l.x = (p.slots - 1) * l.slot + tile::kTileRows * tile::kSlotBytes;
-    l.x = (l.x + 1023) & ~1023;
-    l.meta = l.x + subs * tile::cell_bytes(nc);
-    l.sb = (l.meta + subs * tile::meta_bytes(nc) + 127) & ~127;
-    l.inner = l.sb + p.sb_buffers * 2 * p.sb.block;
-    l.inner_bytes = nc * inner_pitch(p.R) * 4;
-    l.bars = l.inner + p.inner_buffers * l.inner_bytes;
-    l.misc = l.bars + (2 * p.slots + 4 * tile::kGroups + 6) * 8;
-    l.total = l.misc + (4 + kPasses) * 4;
-    return l;
 }
 
 // The product of a row of an adapter's B (R elements at shared address `addr`)
@@ -547,60 +503,6 @@ __global__ void __launch_bounds__(tile::kThreads, 1) lora_project(const __grid_c
 
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
-struct Sizes {
-    size_t cells, meta, inner, counters, partials, total;
-};
-
-size_t up256(size_t b) { return (b + 255) & ~size_t(255); }
-
-// What a call needs; `sms` only shapes the grid (tiles), never an order of sums
-// or a size.
-LoraParams plan(int M, int N, int K, int bits, int gs, int R, int sms, Sizes &sz)
-{
-    const int slot_subs = tile::slot_subs(bits);
-    LoraParams p{};
-    p.M = M; p.N = N; p.K = K; p.G = K / gs; p.gs = gs; p.R = R;
-    p.S = K / 64;
-    p.NS = (p.S + slot_subs - 1) / slot_subs;
-    p.subs = p.NS * slot_subs;
-    // Ranges of K: as few as fit, and for few rows as many as give each SM of the
-    // card a tile of 128, of three slots at least (one for each worker group).
-    p.nseg = (p.NS * slot_subs + range_subs(R) - 1) / range_subs(R);
-    int spread = kSms / ((N + tile::kTileRows - 1) / tile::kTileRows);
-    if (spread > p.NS / tile::kGroups) spread = p.NS / tile::kGroups;
-    if (p.nseg < spread) p.nseg = spread;
-    p.range = (p.NS + p.nseg - 1) / p.nseg;
-    p.nc = M <= 2 ? 2 : M <= 4 ? 4 : M <= 8 ? 8 : 16;
-    // tiles of equal height: as many rounds of the grid as 128 rows need
-    p.grid_rows = sms / p.nseg > 0 ? sms / p.nseg : 1;
-    const int rounds = (N + tile::kTileRows * p.grid_rows - 1) / (tile::kTileRows * p.grid_rows);
-    p.rows = ((N + p.grid_rows * rounds - 1) / (p.grid_rows * rounds) + 7) / 8 * 8;
-    p.tiles = (N + p.rows - 1) / p.rows;
-    if (p.grid_rows > p.tiles) p.grid_rows = p.tiles;
-    // (with room for the bytes before the first where pieces may start off 16 bytes)
-    const int slot = p.rows * tile::kSlotBytes;
-    p.piece = (long long)N * R % 8 == 0 && R * 2 <= tile::kSlotBytes ? p.rows : (slot - 16) / (2 * R);
-    if (p.piece > p.rows) p.piece = p.rows;
-    // (whole rows of up to 96 groups where the ring's three slots still fit beside them)
-    p.slots = tile::kGroups;
-    p.sb_buffers = p.inner_buffers = 1;
-    p.sb = tile::Affines::plan(p.G, p.range * slot_subs * 64 / gs, p.rows, 96);
-    if (layout(p, bits, p.nc).total > kSmem) p.sb = tile::Affines::plan(p.G, p.range * slot_subs * 64 / gs, p.rows, 64);
-    const size_t passes = (M + kPass - 1) / kPass;
-    // passes side by side where one does not fill the card; the others one after the other
-    p.grid_passes = sms / (p.grid_rows * p.nseg);
-    if (p.grid_passes > int(passes)) p.grid_passes = int(passes);
-    if (p.grid_passes < 1) p.grid_passes = 1;
-    p.sb_buffers = rounds > 1 || int(passes) > p.grid_passes ? 2 : 1;
-    sz.cells = up256(passes * p.subs * tile::cell_bytes(p.nc));
-    sz.meta = up256(passes * p.subs * tile::meta_bytes(p.nc));
-    sz.inner = up256(size_t(M) * inner_pitch(R) * 4);
-    sz.counters = p.nseg > 1 ? up256(passes * ((N + 7) / 8) * 4) : 0;
-    sz.partials = p.nseg > 1 ? up256(passes * p.nseg * size_t(N) * p.nc * 4) : 0;
-    sz.total = sz.cells + sz.meta + sz.inner + sz.counters + sz.partials;
-    return p;
-}
-
 template <int BITS, int NC>
 cudaError_t launch_lora(const RingMaps &maps, LoraParams &p, cudaStream_t stream)
 {
@@ -622,14 +524,7 @@ cudaError_t launch_lora(const RingMaps &maps, LoraParams &p, cudaStream_t stream
 template <int BITS>
 cudaError_t launch_lora(const RingMaps &maps, LoraParams &p, cudaStream_t stream)
 {
-    // as many slots as fit, in threes (see qmv_tile.cuh)
-    p.slots = 2 * tile::kGroups;
-    p.inner_buffers = p.M > kPass * p.grid_passes ? 2 : 1;
-    if (layout(p, BITS, p.nc).total > kSmem) p.sb_buffers = 1;
-    if (layout(p, BITS, p.nc).total > kSmem) p.inner_buffers = 1;
-    p.slots = kMaxSlotsLora;
-    while (p.slots > tile::kGroups && layout(p, BITS, p.nc).total > kSmem) p.slots -= tile::kGroups;
-    if (layout(p, BITS, p.nc).total > kSmem) return cudaErrorInvalidConfiguration;
+    if (!fit(p, BITS)) return cudaErrorInvalidConfiguration;
     switch (p.nc) {
         case 2: return launch_lora<BITS, 2>(maps, p, stream);
         case 4: return launch_lora<BITS, 4>(maps, p, stream);
@@ -643,10 +538,10 @@ cudaError_t launch_lora(const RingMaps &maps, LoraParams &p, cudaStream_t stream
 
 extern "C" size_t qmv_lora_workspace_size(int M, int N, int K, int bits, int group_size, int rank)
 {
-    if (qmv::check_weights(M, N, K, bits, group_size) != QMV_OK || K > qmv::kMaxK || rank < 1 || rank > QMV_MAX_RANK)
+    if (qmv::check_weights(M, N, K, bits, group_size) != QMV_OK || K > qmv::lora::kMaxK || rank < 1 || rank > QMV_MAX_RANK)
         return 0;
-    qmv::Sizes sz;
-    qmv::plan(M, N, K, bits, group_size, rank, 1, sz);
+    qmv::lora::Sizes sz;
+    qmv::lora::plan(M, N, K, bits, group_size, rank, 1, sz);
     return sz.total;
 }
 
@@ -671,7 +566,8 @@ extern "C" qmv_status qmv_lora_run(const uint32_t *w_q, const uint16_t *scales, 
     st = current_device(&dev);
     if (st != QMV_OK) return st;
     Sizes sz;
-    LoraParams p = plan(M, N, K, bits, group_size, rank, dev.sms, sz);
+    LoraParams p{};
+    static_cast<LoraShape &>(p) = plan(M, N, K, bits, group_size, rank, dev.sms, sz);
     void *ws = nullptr;
     st = scratch(dev, sz.total, workspace, workspace_bytes, &ws);
     if (st != QMV_OK) return st;

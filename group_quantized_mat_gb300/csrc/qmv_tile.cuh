@@ -48,34 +48,10 @@
 #pragma once
 
 #include "qmv_kernel.cuh"
+#include "qmv_tile_plan.h"
 
 namespace qmv {
 namespace tile {
-
-constexpr int kGroups = 3;                   // worker groups of four warps
-constexpr int kWorkers = 4 * kGroups;        // worker warps; then a tensor warp for each group
-constexpr int kThreads = 32 * (kWorkers + kGroups + 1);  // and the producer
-constexpr int kTileRows = 128;
-constexpr int kSlotBytes = 128;              // bytes of a row in a ring slot
-
-__host__ __device__ constexpr int slot_subs(int bits) { return kSlotBytes * 8 / bits / 64; }  // 4 or 8
-// nc vectors of `terms` e4m3 each are the rows of a subgroup's B operand: atoms of
-// 8 rows x 64 bytes. The instruction's N is 16 at least; where there are only 8
-// rows its second eight are the first again.
-__host__ __device__ constexpr int operand_rows(int nc, int terms = 2) { return nc * terms; }
-__host__ __device__ constexpr int cell_bytes(int nc, int terms = 2) { return operand_rows(nc, terms) <= 8 ? 512 : operand_rows(nc, terms) * 64; }
-// Bytes of a subgroup's (sum, sum, f, f), for each pair of vectors.
-__host__ __device__ constexpr int meta_bytes(int nc) { return nc / 2 * 16; }
-// Columns of an accumulator: the instruction's N.
-__host__ __device__ constexpr int acc_columns(int nc, int terms = 2) { return operand_rows(nc, terms) <= 16 ? 16 : operand_rows(nc, terms); }
-// Subgroups of a step, and a group's columns of A (two steps) and of accumulators.
-__host__ __device__ constexpr int step_subs(int nc, int terms = 2) { return operand_rows(nc, terms) <= 16 ? 2 : 1; }
-__host__ __device__ constexpr int a_columns(int nc, int terms = 2) { return 2 * step_subs(nc, terms) * 16; }
-__host__ __device__ constexpr int d_columns(int nc, int terms = 2) { return 2 * step_subs(nc, terms) * acc_columns(nc, terms); }
-constexpr int kTmemColumns = 512;
-// A group's, half for A and half for accumulators whatever the number of vectors
-// and terms, so that groups may be at work with different ones.
-constexpr int kGroupColumns = 128;
 
 __device__ __forceinline__ uint64_t pack2(float lo, float hi)
 {
@@ -394,82 +370,48 @@ struct Waits {
     }
 };
 
-// How a tile's scales and biases come to shared memory, once for its range of K:
-// by tensor map where rows start on 16 bytes (boxes an odd number of 16 bytes
-// wide, so that 32 rows' reads spread over the banks), else whole rows in one
-// piece where that is small, else row by row. What was tried instead: a thread
-// reading its own row's from global memory, up to three slots ahead, waited for
-// microseconds behind the stream of weights; copies of 8 bytes a row and slot by
-// the producer warp kept it busy for twice the time of a slot.
-enum { kSbBoxes, kSbWhole, kSbRows };
-
-struct Affines {
-    int mode, pitch, block;  // bytes from row to row, and of each of the two arrays
-
-    // `whole`: most groups of a row that are fetched as whole rows.
-    __host__ __device__ static Affines plan(int G, int groups, int rows, int whole)
-    {
-        Affines a;
-        a.mode = G % 8 == 0 ? kSbBoxes : G <= whole ? kSbWhole : kSbRows;
-        a.pitch = a.mode == kSbWhole ? 2 * G : (((2 * groups + 30) / 16) | 1) * 16;
-        a.block = (rows * a.pitch + 127) & ~127;
-        return a;
-    }
-    // By the whole producer warp, each lane arriving once on `bar`: rows row0 .. row0 + rows - 1 of `all`, groups g0 ..
-    // g0 + groups - 1 of G, into dst (generic address `gen`). smap, bmap: tensor
-    // maps for kSbBoxes, at row `mrow0` of the map.
-    __device__ __forceinline__ void fetch(uint32_t dst, uint8_t *gen, const uint16_t *sc, const uint16_t *bi,
-                                          const CUtensorMap *smap, const CUtensorMap *bmap, long long row0, int rows,
-                                          long long all, int G, int g0, int groups, uint32_t bar, int lane) const
-    {
-        if (mode == kSbBoxes) {
-            if (lane == 0) {
-                mbar_arrive_expect_tx(bar, uint32_t(2 * rows * pitch));
-                tma_load_2d(dst, smap, g0 / 8 * 2, int(row0), bar);  // eight groups are two elements
-                tma_load_2d(dst + block, bmap, g0 / 8 * 2, int(row0), bar);
-            } else {
-                mbar_arrive(bar);
-            }
-            return;
+__device__ __forceinline__ void Affines::fetch(uint32_t dst, uint8_t *gen, const uint16_t *sc, const uint16_t *bi,
+                                               const CUtensorMap *smap, const CUtensorMap *bmap, long long row0,
+                                               int rows, long long all, int G, int g0, int groups, uint32_t bar,
+                                               int lane) const
+{
+    if (mode == kSbBoxes) {
+        if (lane == 0) {
+            mbar_arrive_expect_tx(bar, uint32_t(2 * rows * pitch));
+            tma_load_2d(dst, smap, g0 / 8 * 2, int(row0), bar);  // eight groups are two elements
+            tma_load_2d(dst + block, bmap, g0 / 8 * 2, int(row0), bar);
+        } else {
+            mbar_arrive(bar);
         }
-        // from the 16-byte boundary before the first; the last bytes of the
-        // arrays, where they fill no 16, go one by one
-        const long long end = all * G * 2;
-        const int step = mode == kSbWhole ? rows : 1;
-        uint32_t total = 0;
-        for (int pass = 0; pass < 2; ++pass) {
-            for (int r = mode == kSbWhole ? (lane == 0 ? 0 : rows) : lane; r < rows; r += mode == kSbWhole ? rows : 32) {
-                const long long n = row0 + r;
-                if (n >= all) break;
-                const long long first = mode == kSbWhole ? n * G * 2 : (n * G + g0) * 2, from = first & ~15ll;
-                const long long to = mode == kSbWhole ? min(first + (long long)step * G * 2, end) : first + 2 * groups;
-                const long long whole = min((to + 15) & ~15ll, end & ~15ll);
-                const uint32_t bytes = whole > from ? uint32_t(whole - from) : 0u, d = uint32_t(r * pitch);
-                if (pass == 0) {
-                    total += 2 * bytes;
-                    for (long long e = max(whole, from); e < to; e += 2) {
-                        *reinterpret_cast<uint16_t *>(gen + d + (e - from)) = __ldg(sc + e / 2);
-                        *reinterpret_cast<uint16_t *>(gen + d + block + (e - from)) = __ldg(bi + e / 2);
-                    }
-                } else if (bytes) {
-                    bulk_load_plain(dst + d, reinterpret_cast<const uint8_t *>(sc) + from, bytes, bar);
-                    bulk_load_plain(dst + d + block, reinterpret_cast<const uint8_t *>(bi) + from, bytes, bar);
+        return;
+    }
+    // from the 16-byte boundary before the first; the last bytes of the
+    // arrays, where they fill no 16, go one by one
+    const long long end = all * G * 2;
+    const int step = mode == kSbWhole ? rows : 1;
+    uint32_t total = 0;
+    for (int pass = 0; pass < 2; ++pass) {
+        for (int r = mode == kSbWhole ? (lane == 0 ? 0 : rows) : lane; r < rows; r += mode == kSbWhole ? rows : 32) {
+            const long long n = row0 + r;
+            if (n >= all) break;
+            const long long first = mode == kSbWhole ? n * G * 2 : (n * G + g0) * 2, from = first & ~15ll;
+            const long long to = mode == kSbWhole ? min(first + (long long)step * G * 2, end) : first + 2 * groups;
+            const long long whole = min((to + 15) & ~15ll, end & ~15ll);
+            const uint32_t bytes = whole > from ? uint32_t(whole - from) : 0u, d = uint32_t(r * pitch);
+            if (pass == 0) {
+                total += 2 * bytes;
+                for (long long e = max(whole, from); e < to; e += 2) {
+                    *reinterpret_cast<uint16_t *>(gen + d + (e - from)) = __ldg(sc + e / 2);
+                    *reinterpret_cast<uint16_t *>(gen + d + block + (e - from)) = __ldg(bi + e / 2);
                 }
+            } else if (bytes) {
+                bulk_load_plain(dst + d, reinterpret_cast<const uint8_t *>(sc) + from, bytes, bar);
+                bulk_load_plain(dst + d + block, reinterpret_cast<const uint8_t *>(bi) + from, bytes, bar);
             }
-            if (pass == 0) mbar_arrive_expect_tx(bar, total);
         }
+        if (pass == 0) mbar_arrive_expect_tx(bar, total);
     }
-    // Offset of group g0 of a row in its bytes there.
-    __device__ __forceinline__ uint32_t offset(long long row, int G, int g0) const
-    {
-        return mode == kSbBoxes ? (g0 & 7) * 2u : mode == kSbWhole ? g0 * 2u : uint32_t((row * G + g0) * 2) & 15u;
-    }
-    // Bytes by which a row's groups of a slot are aligned there, at most 8.
-    __device__ __forceinline__ int alignment(int G) const
-    {
-        return mode == kSbRows ? 2 : mode == kSbBoxes || G % 4 == 0 ? 8 : G % 2 == 0 ? 4 : 2;
-    }
-};
+}
 
 // Scales and biases of a row for the groups of one slot.
 template <int BITS, int GS>
