@@ -280,7 +280,7 @@ __global__ void __launch_bounds__(tile::kThreads, 1) lora_project(const __grid_c
         bulk_load_plain(base + L.x, p.cells + sub * cell_bytes(NC), cb, xbar);
         bulk_load_plain(base + L.meta, p.meta + sub * meta_bytes(NC), mb, xbar);
         // (of vectors without an adapter: whatever is there)
-        bulk_load_plain(base + L.inner + (before & 1) * L.inner_bytes, p.inner + size_t(z) * kPass * inner_pitch(p.R), ib, xbar);
+        bulk_load_plain(base + inner_at(p, L, before), p.inner + size_t(z) * kPass * inner_pitch(p.R), ib, xbar);
     };
 
     if (warp == kThreads / 32 - 1) {
@@ -402,7 +402,7 @@ __global__ void __launch_bounds__(tile::kThreads, 1) lora_project(const __grid_c
         };
         for (int z = blockIdx.z; z < passes; z += gridDim.z, ++before) {
             const int ads = s_ads[z], nv = min(kPass, p.M - z * kPass);
-            const float *inner = reinterpret_cast<const float *>(smem + L.inner + (before & 1 & (p.inner_buffers - 1)) * L.inner_bytes);
+            const float *inner = reinterpret_cast<const float *>(smem + inner_at(p, L, before));
             bool landed = false;  // staged x
             for (int tl = blockIdx.x; tl < p.tiles; tl += p.grid_rows, it += ns + ads * pieces, ++tiles) {
                 const bool over = tl + p.grid_rows >= p.tiles;  // the pass's last tile here

@@ -63,6 +63,13 @@ __host__ __device__ inline Layout layout(const LoraShape &p, int bits, int nc)
     return l;
 }
 
+// Where the inner vectors of a CTA's pass lie, `before` passes of it having gone
+// before: the producer's copy and the workers' reads both ask here.
+__host__ __device__ inline int inner_at(const LoraShape &p, const Layout &l, int before)
+{
+    return l.inner + (before & (p.inner_buffers - 1)) * l.inner_bytes;
+}
+
 struct Sizes {
     size_t cells, meta, inner, counters, partials, total;
 };
@@ -126,7 +133,9 @@ inline bool fit(LoraShape &p, int bits)
     if (layout(p, bits, p.nc).total > kSmem) p.inner_buffers = 1;
     p.slots = kMaxSlots;
     while (p.slots > tile::kGroups && layout(p, bits, p.nc).total > kSmem) p.slots -= tile::kGroups;
-    return layout(p, bits, p.nc).total <= kSmem;
+    // (whatever a pass brings to its inner vectors stays before the barriers)
+    const Layout l = layout(p, bits, p.nc);
+    return l.total <= kSmem && inner_at(p, l, 0) + l.inner_bytes <= l.bars && inner_at(p, l, 1) + l.inner_bytes <= l.bars;
 }
 
 }  // namespace lora
