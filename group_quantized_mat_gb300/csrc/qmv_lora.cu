@@ -347,10 +347,20 @@ __global__ void __launch_bounds__(tile::kThreads, 1) lora_project(const __grid_c
             int it = 0, before = 0;
             for (int z = blockIdx.z; z < passes; z += gridDim.z, ++before) {
                 const int step = ns + s_ads[z] * pieces;
-                wait(xbar, before & 1);
-                for (int tl = blockIdx.x; tl < p.tiles; tl += p.grid_rows, it += step)
-                    for (int i = first_slot(group, it); i < ns; i += kGroups)
+                bool landed = false;
+                for (int tl = blockIdx.x; tl < p.tiles; tl += p.grid_rows, it += step) {
+                    const int i0 = first_slot(group, it);
+                    // A pass waits for this warp only where its group has slots: without
+                    // any it must not wait by a parity that may be two passes old. (Nor
+                    // is the parity enough after such a pass; the workers' arrivals are,
+                    // which have waited for x.)
+                    if (i0 < ns && !landed) {
+                        wait(xbar, before & 1);
+                        landed = true;
+                    }
+                    for (int i = i0; i < ns; i += kGroups)
                         multiply_slot<BITS, NC>(wait, pipe, base + L.x + i * SUBS * cell_bytes(NC));
+                }
             }
         }
     } else {

@@ -10,3 +10,6 @@ PASSES += [(50, 17408, 4096, 4, 64, 200), (48, 20008, 1984, 4, 64, 24), (40, 390
 
 # one pass whose ring has three slots
 THREE_SLOTS = [(16, 15360, 3840, 4, 64, 16), (13, 14336, 4096, 2, 64, 64), (16, 17408, 4096, 4, 64, 64)]
+
+# several passes in a CTA over fewer slots of K than there are worker groups
+FEW_SLOTS = [(100, 20008, 256, 4, 64, 16), (64, 20000, 512, 4, 128, 8), (40, 19500, 128, 2, 64, 27), (200, 19456, 1024, 2, 128, 64)]

@@ -8,7 +8,7 @@ import pytest
 import torch
 
 import group_quantized_mat_gb300 as g
-from lora_shapes import PASSES, THREE_SLOTS
+from lora_shapes import FEW_SLOTS, PASSES, THREE_SLOTS
 from operators_reference import U
 
 pytestmark = pytest.mark.gpu
@@ -69,7 +69,7 @@ def expect(shape, wide, mag, x, a, b, ids, c):
     return y, err
 
 
-@pytest.mark.parametrize("shape", sorted(PASSES, key=lambda s: s[1:]) + THREE_SLOTS, ids=lambda s: "x".join(map(str, s)))
+@pytest.mark.parametrize("shape", sorted(PASSES, key=lambda s: s[1:]) + THREE_SLOTS + FEW_SLOTS, ids=lambda s: "x".join(map(str, s)))
 def test_passes_match_the_formula(shape):
     M, N, K, bits, gs, R = shape
     w, s, b, wide, mag = weights(N, K, bits, gs)

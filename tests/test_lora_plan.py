@@ -9,7 +9,7 @@ import subprocess
 
 import pytest
 
-from lora_shapes import PASSES, THREE_SLOTS
+from lora_shapes import FEW_SLOTS, PASSES, THREE_SLOTS
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
@@ -95,3 +95,6 @@ def test_gpu_shapes_cover_the_plans(plan):
     assert any(p["tiles"] > p["grid_rows"] for p in several)
     for s in THREE_SLOTS:
         assert plan(*s)["slots"] == 3, s
+    for s in FEW_SLOTS:
+        p = plan(*s)
+        assert p["passes"] > 1 and p["nseg"] == 1 and p["subs"] * s[3] < 3 * 16, s
