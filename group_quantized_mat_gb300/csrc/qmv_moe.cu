@@ -649,8 +649,8 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
             // sum and largest exponent of the 64
 #pragma unroll
             for (int i = 0; i < NC / 2; ++i) {
-                const uint32_t E = __reduce_max_sync(0xffffu << (lane & 16), max(1u, (__float_as_uint(h[i]) >> 23) & 0xffu));
-                float sum = h[i];
+                const uint32_t E = __reduce_max_sync(0xffffu << (lane & 16), max(kLeastExponent, (__float_as_uint(h[i]) >> 23) & 0xffu));
+                float sum = __fmul_rn(h[i], kSumScale);
 #pragma unroll
                 for (int d = 8; d; d >>= 1) sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, d));
                 if ((lane & 15) == 0) red[(half * (NC / 2) + i) * 4 + (warp & 3)] = make_float2(sum, __uint_as_float(E));
@@ -664,8 +664,8 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
                 const int j = 2 * i + half;
                 const float4 r0 = reinterpret_cast<const float4 *>(red)[(half * (NC / 2) + i) * 2];
                 const float4 r1 = reinterpret_cast<const float4 *>(red)[(half * (NC / 2) + i) * 2 + 1];
-                const int E = int(max(max(__float_as_uint(r0.y), __float_as_uint(r0.w)), max(__float_as_uint(r1.y), __float_as_uint(r1.w))));
-                const int pw = 134 - E;
+                const uint32_t E = max(max(__float_as_uint(r0.y), __float_as_uint(r0.w)), max(__float_as_uint(r1.y), __float_as_uint(r1.w)));
+                const int pw = scale_power(E);
                 float v = __fmul_rn(__fmul_rn(h[i], exp2i(pw / 2)), exp2i(pw - pw / 2));
                 if (BITS == 2 && (e & 1)) v = __fmul_rn(v, 0.25f);
 #pragma unroll
@@ -679,7 +679,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
                 if (r == 0) {
                     float *m = reinterpret_cast<float *>(own + CB + i * 16) + half;
                     m[0] = __fadd_rn(__fadd_rn(r0.x, r0.z), __fadd_rn(r1.x, r1.z));
-                    m[2] = exp2i(min(E - 125, 127));
+                    m[2] = unscale(E);
                 }
             }
             uint8_t *slot_h = p.h + (size_t(im.entry) * p.NSb + im.tl / SUBS) * (SUBS * (CB + MB));

@@ -21,6 +21,12 @@
 //    operand, their sums two accumulators, joined as (hi + lo/32) * f.
 // The accumulators are fp32 (checked: sums of exact products come out exact).
 //
+// Sums are kept as a 2^10th of what they are until they leave the tile (the staged
+// sum x and f are times 2^-10): f, which undoes x's scaling, would not
+// be a number from |x| of 2^126 on, and q x of the largest x sum to up to 2^138. As
+// powers of two change no rounding, results are those of sums kept as they are,
+// but for results below 2^-116, which are multiples of 2^-139.
+//
 // The tile. A thread owns a row (a lane of tensor memory). For each subgroup it
 // reads its 32 (2-bit: 16) bytes from the ring, masks them into 16 registers,
 // stores those as its 16 columns of the A operand in tensor memory, and two
@@ -134,24 +140,36 @@ __device__ __forceinline__ int operand_index(int tok, int h, int terms = 2) { re
 // Byte of 16-byte piece c of that row in a subgroup's cell (64-byte swizzle).
 __device__ __forceinline__ int operand_offset(int r, int c) { return (r >> 3) * 512 + (r & 7) * 64 + ((c ^ (r >> 1)) & 3) * 16; }
 
+// The scale of sums inside a tile, and back.
+constexpr float kSumScale = 0x1p-10f, kSumUnscale = 0x1p10f;
+
+// By the largest exponent field E of a subgroup: the power of two that brings its
+// elements to 2^7 .. 2^8 at most, and the factor f that undoes it (and the operands'
+// 2^-9) in the scale of sums. From 2^-118 down the power stays what it is there, so
+// that f is a normal number; bf16 elements are exact all the same. An infinity or
+// NaN makes f NaN, and with it everything that the vector gives.
+constexpr uint32_t kLeastExponent = 9;
+__device__ __forceinline__ int scale_power(uint32_t E) { return 134 - int(E); }
+__device__ __forceinline__ float unscale(uint32_t E) { return E == 255 ? __uint_as_float(0x7fc00000u) : exp2i(int(E) - 135); }
+
 // Stages eight elements of a vector: octet o (0..7) of a subgroup, by the eight
 // consecutive threads of a warp that hold its octets. x: elements 8 o .. 8 o + 7;
-// piece(h): where the 16-byte piece o / 2 of term h goes; keep(sum, f) is called
-// by one of the eight.
+// piece(h): where the 16-byte piece o / 2 of term h goes; keep(sum, f), in the scale
+// of sums, is called by one of the eight.
 template <int BITS, typename Piece, typename Keep>
 __device__ __forceinline__ void stage_octet(const float (&x)[8], int o, Piece piece, Keep keep)
 {
     float sum = 0.0f;
-    uint32_t E = 1;
+    uint32_t E = kLeastExponent;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        sum = __fadd_rn(sum, x[i]);
+        sum = __fmaf_rn(x[i], kSumScale, sum);  // (the product is exact)
         E = max(E, (__float_as_uint(x[i]) >> 23) & 0xffu);
     }
     E = __reduce_max_sync(0xffu << (threadIdx.x & 24), E);
 #pragma unroll
     for (int d = 1; d < 8; d *= 2) sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, d));
-    const int p = 134 - int(E);  // the largest |x| becomes 2^7 .. 2^8
+    const int p = scale_power(E);
     const float p1 = exp2i(p / 2), p2 = exp2i(p - p / 2);
     uint32_t hi[4], lo[4];  // elements (2i, 2i + 1) as bytes
 #pragma unroll
@@ -183,7 +201,7 @@ __device__ __forceinline__ void stage_octet(const float (&x)[8], int o, Piece pi
             w[6] = uint16_t(__byte_perm(odd, 0, 0x0031));
         }
     }
-    if (o == 0) keep(sum, exp2i(min(int(E) - 125, 127)));  // 2^9 / 2^p
+    if (o == 0) keep(sum, unscale(E));
 }
 
 // Eight bf16 of a 16-byte load as floats.
@@ -632,7 +650,7 @@ struct Row {
 #pragma unroll
         for (int c = 0; c < kGroups; ++c) settle(v[c]);
 #pragma unroll
-        for (int i = 0; i < NC; ++i) sums[i] = __fadd_rn(__fadd_rn(v[0][i], v[1][i]), v[2][i]);
+        for (int i = 0; i < NC; ++i) sums[i] = __fmul_rn(__fadd_rn(__fadd_rn(v[0][i], v[1][i]), v[2][i]), kSumUnscale);
         tmem_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(freed);
@@ -662,7 +680,7 @@ struct Row {
 #pragma unroll
         for (int i = 0; i < kOwn; ++i) {
             settle(v[i]);
-            sums[i] = __fadd_rn(__fadd_rn(v[i][0], v[i][1]), v[i][2]);
+            sums[i] = __fmul_rn(__fadd_rn(__fadd_rn(v[i][0], v[i][1]), v[i][2]), kSumUnscale);
         }
         tmem_fence_before();
         named_sync(1, 32 * kWorkers);

@@ -315,7 +315,8 @@ QMV_API qmv_status qmv_mxfp4_run(const uint32_t *w_q, const uint8_t *scales, con
  * factored form, as for qmv_run, but summed by the tensor cores in another fixed
  * order), the inner vector A x is kept in fp32, and the sum of the two terms is
  * rounded once. A vector's result does not depend on the other vectors of the
- * call: it is bit-identical to an M = 1 call on that vector.
+ * call: it is bit-identical to an M = 1 call on that vector. A vector that holds
+ * an infinity or NaN gives NaN throughout.
  *
  * Errors: QMV_ERR_NULL, QMV_ERR_BITS, QMV_ERR_GROUP, QMV_ERR_SHAPE,
  * QMV_ERR_M_RANGE, QMV_ERR_COUNT, QMV_ERR_FLAGS, QMV_ERR_ALIGN (also for
@@ -357,7 +358,8 @@ QMV_API qmv_status qmv_lora_run(const uint32_t *w_q, const uint16_t *scales, con
  *
  * A NaN router logit counts as -inf. Arithmetic: fp32 sums throughout; h keeps
  * 16 bits of significand between the two products (elements far below the largest
- * of their 64 fewer, down to 2^-30 of it); y is rounded once. A token's result does not depend on the other tokens of the call.
+ * of their 64 fewer, down to 2^-30 of it); y is rounded once. A token's result does not depend on the other
+ * tokens of the call. An infinity or NaN in x or h makes the token's y NaN.
  *
  * Errors: as for qmv_lora_run; QMV_ERR_SHAPE also when inter is not a multiple of
  * group_size or experts x rows x groups reaches 2^31. */
