@@ -96,7 +96,8 @@ __device__ __forceinline__ Mode mode_of(const VerifyParams &p, int b)
     Mode m;
     const float t = p.temperature ? __ldg(p.temperature + b) : 1.0f;
     m.greedy = !(t > 0.0f);
-    m.inv = m.greedy ? 1.0f : fmaxf(__fdiv_rn(1.0f, t), FLT_MIN);
+    // (a number, and times log2 e still one: 0 at the maximum stays 0)
+    m.inv = m.greedy ? 1.0f : fminf(fmaxf(__fdiv_rn(1.0f, t), FLT_MIN), 2e38f);
     m.len = p.draft_len ? min(max(__ldg(p.draft_len + b), 0), p.S) : p.S;
     return m;
 }

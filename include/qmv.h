@@ -397,7 +397,7 @@ QMV_API qmv_status qmv_moe_run(const uint16_t *x, const uint16_t *router, const 
  *                drafts were not sampled: q_i is then 1 at x_i and 0 elsewhere.
  *  draft_tokens  device, int32 [B, S]. One outside [0, V) is never accepted.
  *  draft_len     device, int32 [B], or NULL (S for all); taken into [0, S].
- *  temperature   device, float [B], or NULL (1 for all).
+ *  temperature   device, float [B], or NULL (1 for all). Above 0 and below 5e-39 it counts as that.
  *  uniform       device, float [B, S], in [0, 1).
  *  noise         device, float [B, ld_noise], positive; below the smallest normal
  *                number it counts as that.
