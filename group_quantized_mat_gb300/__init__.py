@@ -116,12 +116,16 @@ def load(path: str | None = None) -> ctypes.CDLL:
 
 
 def _ptr(a) -> int | None:
-    if a is None:
-        return None
+    if a is None or type(a) is int:
+        return a
     try:
         return a.data_ptr()  # torch.Tensor
     except AttributeError:
-        return a.ctypes.data if isinstance(a, np.ndarray) else int(a)
+        if isinstance(a, np.ndarray):
+            return a.ctypes.data
+        if isinstance(a, int):
+            return int(a)
+        raise  # a float or a text is no address
 
 
 def _stream(s) -> int | None:
