@@ -38,8 +38,9 @@
 // cannot do without, at 6.8 TB/s): 10.2 for one vector of 1024 x 5120 (0.5), 14.4
 // for 4 of 15360 x 3840 (5.2), 22.5 for 13 of 3840 x 15360 (5.9), 116 for 64 of
 // 17408 x 5120 in 2 bits at rank 64 (9.6), 25.3 for 24 of 5120 x 5120.
-// The order of every sum depends on N, K and the rank alone, so a vector's result does not
-// depend on the batch it is in.
+// The order of an output's sums depends on N, K, the rank, its row and its adapter's number
+// (which says with which range of K the adapter is added), so a vector's result depends
+// neither on the batch it is in nor on the card.
 #include <cuda_bf16.h>
 
 #include <cstdint>
@@ -374,9 +375,6 @@ __global__ void __launch_bounds__(tile::kThreads, 1) lora_project(const __grid_c
             s_c[tid / kPass][tid % kPass] = __ldg(p.c + s_ad[tid / kPass][tid % kPass]);
         int it = 0, tiles = 0, before = 0;
         const int align = p.sb.alignment(p.G), pitch = inner_pitch(p.R);
-        // Adapters' rows lie R/8 pieces of 16 bytes apart: each starts at another
-        // piece, so that neighbours' reads fall on different banks.
-        const int piece0 = p.R % 8 ? 0 : (p.R >= 64 ? row : row * (p.R / 8) >> 3) % (p.R / 8);
         // With several ranges: the tile whose partial sums were left last and, in one
         // thread, how many ranges had left theirs before. It is looked at after the
         // next tile, so that nobody waits for the answer.
@@ -418,6 +416,10 @@ __global__ void __launch_bounds__(tile::kThreads, 1) lora_project(const __grid_c
                 const bool over = tl + p.grid_rows >= p.tiles;  // the pass's last tile here
                 const int n = tl * p.rows + row;
                 const bool live = row < p.rows && n < p.N;
+                // Adapters' rows lie R/8 pieces of 16 bytes apart: each starts at another
+                // piece, so that neighbours' reads fall on different banks. (By the row's
+                // place in the matrix: its place in a tile depends on the card.)
+                const int piece0 = p.R % 8 ? 0 : (p.R >= 64 ? n & 127 : (n & 127) * (p.R / 8) >> 3) % (p.R / 8);
                 Row<BITS, GS, NC> acc;
                 acc.start();
                 uint32_t last = 0;

@@ -83,3 +83,15 @@ def test_passes_match_the_formula(shape):
     for m in {0, M // 2, M - 1}:
         x, a, bb, ids, c = p
         assert torch.equal(run((w, s, b), x[m:m + 1].contiguous(), a, bb, ids[m:m + 1].contiguous(), c, (1, *shape[1:]))[0], got[m]), m
+
+
+@pytest.mark.parametrize("R", [16, 24, 72, 128, 200])
+def test_rows_do_not_depend_on_the_tiles_they_are_in(R):
+    """The first rows of a larger matrix, whose tiles are higher, give the same bits."""
+    M, N, K, more = 5, 1000, 1024, 5000
+    w, s, b, _, _ = weights(more, K, 4, 64)
+    x, a, bb, ids, c = problem(M, more, K, 4, 64, R)
+    ids.copy_(torch.arange(M) % 3)
+    large = run((w, s, b), x, a, bb, ids, c, (M, more, K, 4, 64, R))
+    small = run((w[:N].contiguous(), s[:N].contiguous(), b[:N].contiguous()), x, a, bb[:, :N].contiguous(), ids, c, (M, N, K, 4, 64, R))
+    assert torch.equal(large[:, :N], small)

@@ -98,3 +98,13 @@ def test_gpu_shapes_cover_the_plans(plan):
     for s in FEW_SLOTS:
         p = plan(*s)
         assert p["passes"] > 1 and p["nseg"] == 1 and p["subs"] * s[3] < 3 * 16, s
+
+
+def test_sums_do_not_depend_on_the_card(plan):
+    """Ranges of K, which fix the order of sums, are the same whatever the number of SMs;
+    and the GPU test of tiles compares different heights over equal ranges."""
+    for N, K in ((1000, 1024), (15360, 3840), (3840, 15360), (250, 5120), (128256, 4096)):
+        for M in (1, 16, 64):
+            assert len({(p["nseg"], p["subs"]) for p in (plan(M, N, K, 4, 64, 32, sms) for sms in (1, 100, 148, 152))}) == 1
+    a, b = plan(5, 1000, 1024, 4, 64, 72), plan(5, 5000, 1024, 4, 64, 72)
+    assert a["nseg"] == b["nseg"] == 1 and a["rows"] != b["rows"]
