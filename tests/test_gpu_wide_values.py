@@ -132,3 +132,30 @@ def test_tokens_up_to_the_largest_number():
     assert np.array_equal(gi, ids)
     # (of the last token, whose x is small, h falls below the least number)
     assert np.all(np.abs(got - y) <= err + 2.0 ** -130), float(np.max(np.abs(got - y) / (err + 2.0 ** -130)))
+
+
+@pytest.mark.parametrize("bits,gs", [(4, 64), (4, 128), (2, 64), (2, 128)])
+@pytest.mark.parametrize("M", [1, 4, 8, 16])
+def test_sums_of_exact_products_are_exact(M, bits, gs):
+    """Scales 1, biases 0, whole numbers: every sum is a whole number below 2^24, though a
+    group's terms lie up to 2^21 apart, so any bit that an accumulator dropped would show."""
+    K = 256
+    pr = Problem(M, 150, K, bits, gs, 1, 8, ids=[-1] * M, seed=M)
+    rng = np.random.default_rng(M + bits)
+    x = rng.integers(-255, 256, (M, K)).astype(np.float64)
+    for m in range(M):
+        for sub in range(0, K, 64):
+            x[m, sub + 2 * rng.integers(32)] = rng.choice([-1, 1]) * 2.0 ** 17
+    pr.x = ref.to_bf16(x)
+    pr.m.scales, pr.m.biases = np.full_like(pr.m.scales, 0x3f80), np.zeros_like(pr.m.biases)
+    pr.dev = [pr.dev[0], dev(pr.m.scales), dev(pr.m.biases)]
+    want = x @ pr.m.q.astype(np.float64).T
+    assert np.abs(x).max() == 2.0 ** 17 and np.abs(want).max() < 2 ** 24
+    assert np.array_equal(pr.run(flags=g.F32_OUT), want)
+
+
+@pytest.mark.parametrize("M,K,I,E,k,bits,gs,gelu", [(3, 1024, 14336, 2, 1, 4, 64, False), (9, 4096, 2048, 3, 2, 4, 128, True),
+                                                    (2, 65536, 64, 2, 1, 2, 64, False), (2, 64, 65536, 2, 2, 2, 64, True),
+                                                    (40, 128, 14336, 2, 1, 2, 128, False)])
+def test_experts_wider_than_any_other_test(M, K, I, E, k, bits, gs, gelu):
+    Layer(M, K, I, E, k, bits, gs, seed=M + E).check(g.MOE_GELU if gelu else 0)

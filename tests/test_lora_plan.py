@@ -29,12 +29,12 @@ extern "C" int lora_plan(int M, int N, int K, int bits, int gs, int R, int sms, 
         inner_end = end > inner_end ? end : inner_end;
     }
     const int v[] = {p.slots, p.sb_buffers, p.inner_buffers, p.nseg, p.range * tile::slot_subs(bits), p.rows, p.tiles, p.grid_rows,
-                     p.grid_passes, most, p.piece, p.nc, l.slot, l.x, l.meta, l.sb, l.inner, inner_end, l.bars, l.misc, l.total, lora::kSmem, p.sb.block};
+                     p.grid_passes, most, int(sz.total / 256), p.piece, p.nc, l.slot, l.x, l.meta, l.sb, l.inner, inner_end, l.bars, l.misc, l.total, lora::kSmem, p.sb.block};
     for (unsigned i = 0; i < sizeof v / sizeof *v; ++i) out[i] = v[i];
     return ok;
 }
 """
-NAMES = ("slots", "sb_buffers", "inner_buffers", "nseg", "subs", "rows", "tiles", "grid_rows", "grid_passes", "passes", "piece", "nc",
+NAMES = ("slots", "sb_buffers", "inner_buffers", "nseg", "subs", "rows", "tiles", "grid_rows", "grid_passes", "passes", "workspace", "piece", "nc",
          "slot", "x", "meta", "sb", "inner", "inner_end", "bars", "misc", "total", "most", "block")
 
 
@@ -101,10 +101,10 @@ def test_gpu_shapes_cover_the_plans(plan):
 
 
 def test_sums_do_not_depend_on_the_card(plan):
-    """Ranges of K, which fix the order of sums, are the same whatever the number of SMs;
-    and the GPU test of tiles compares different heights over equal ranges."""
+    """Ranges of K, which fix the order of sums, are the same whatever the number of SMs, as
+    the workspace is, whose size is asked for without a card; and the GPU test of tiles compares different heights over equal ranges."""
     for N, K in ((1000, 1024), (15360, 3840), (3840, 15360), (250, 5120), (128256, 4096)):
         for M in (1, 16, 64):
-            assert len({(p["nseg"], p["subs"]) for p in (plan(M, N, K, 4, 64, 32, sms) for sms in (1, 100, 148, 152))}) == 1
+            assert len({(p["nseg"], p["subs"], p["workspace"]) for p in (plan(M, N, K, 4, 64, 32, sms) for sms in (1, 100, 148, 152))}) == 1
     a, b = plan(5, 1000, 1024, 4, 64, 72), plan(5, 5000, 1024, 4, 64, 72)
     assert a["nseg"] == b["nseg"] == 1 and a["rows"] != b["rows"]
