@@ -422,6 +422,7 @@ __device__ __forceinline__ void Affines::fetch(uint32_t dst, uint8_t *gen, const
                     *reinterpret_cast<uint16_t *>(gen + d + (e - from)) = __ldg(sc + e / 2);
                     *reinterpret_cast<uint16_t *>(gen + d + block + (e - from)) = __ldg(bi + e / 2);
                 }
+                if (whole < to) fence_proxy_async_smem();  // (copies come here again)
             } else if (bytes) {
                 bulk_load_plain(dst + d, reinterpret_cast<const uint8_t *>(sc) + from, bytes, bar);
                 bulk_load_plain(dst + d + block, reinterpret_cast<const uint8_t *>(bi) + from, bytes, bar);
