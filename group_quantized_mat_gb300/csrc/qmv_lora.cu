@@ -34,10 +34,11 @@
 //    64 vectors, 32.9 for 24 of 5120 x 5120.)
 // What bounds it: for few vectors the chain of the two kernels' starts, x, first
 // weights and the join; for 16 the workers' instructions (qmv_tile.cuh) and the
-// adapters' code, which runs from a cold instruction cache. Measured (us; bytes it
-// cannot do without, at 6.8 TB/s): 10.2 for one vector of 1024 x 5120 (0.5), 14.4
-// for 4 of 15360 x 3840 (5.2), 22.5 for 13 of 3840 x 15360 (5.9), 116 for 64 of
-// 17408 x 5120 in 2 bits at rank 64 (9.6), 25.3 for 24 of 5120 x 5120.
+// adapters' code, which runs from a cold instruction cache; above 16 every further 16
+// pay for the unpacking again. Measured (us; bytes it cannot do without, at 6.7 TB/s):
+// 10.7 for one vector of 1024 x 5120 (0.5), 14.8 for 4 of 15360 x 3840 (5.2), 23.2 for
+// 13 of 3840 x 15360 (6.0), 117 for 64 of 17408 x 5120 in 2 bits at rank 64 (9.7); of
+// 15360 x 3840 at rank 16, 24.9 for 16 vectors, 40.7 for 32 (5.9) and 73 for 64 (6.1).
 // The order of an output's sums depends on N, K, the rank, its row and its adapter's number
 // (which says with which range of K the adapter is added), so a vector's result depends
 // neither on the batch it is in nor on the card.

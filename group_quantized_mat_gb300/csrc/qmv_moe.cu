@@ -24,14 +24,18 @@
 // ring: 6 slots (9 with 4 tokens to an entry) are all that fits beside the cells,
 // and a slot is taken from its request to the end of its step, 6 to 8 thousand
 // cycles under load.
-// Measured (us; bytes a call cannot do without, at 6.8 TB/s): 20.8 for one token
-// and 8 of 64 experts of 2048 x 768 (3.2), 39 for 5 and 2 of 8 of 3840 x 1920 in
-// 2 bits (5.6), 79 for 16 and 8 of 128 of 2048 x 768 (32; A runs at 5.8 TB/s with
-// scales and biases), 157 for 48 and 4 of 32 of 5120 x 1280 (49).
+// Measured (us; bytes a call cannot do without, at 6.7 TB/s): 22.5 for one token
+// and 8 of 64 experts of 2048 x 768 (3.2), 35 to 41 from card to card for 5 and 2 of
+// 8 of 3840 x 1920 in 2 bits (5.7), 80 for 16 and 8 of 128 of 2048 x 768 (33; A runs at
+// 5.8 TB/s with scales and biases), 157 for 48 and 4 of 32 of 5120 x 1280 (50).
 //
 // The inner pipeline is qmv_tile.cuh's. A ring slot holds 128 bytes of 128 rows
-// and the slot's subgroups of the item's tokens. h enters the down product with
-// four e4m3 terms (17 bits), x with two (its 8 bits).
+// and the slot's subgroups of the item's tokens. x enters with two e4m3 terms, which
+// hold its 8 bits. h, an fp32 number, enters the down product with four, which hold 19:
+// the first has 4 significant bits, each further one 5 more. Five would hold all 24
+// and cost a quarter more in cells, accumulators and reads; with four the results' error
+// against 64 bits is that of an fp32 computation (1.5e-7 to 1e-6 of their norm over 20
+// shapes, 2.7e-7 to 1.4e-6 where everything is fp32).
 //
 // Orders: a token's logits, its sums over K and inter, and the sum over its
 // choices do not depend on the other tokens of the call.

@@ -19,7 +19,8 @@
 //    largest |x| (2^-12 for a 2-bit matrix's odd fields); below that an element
 //    is rounded to 2^-22 (2^-20) of that largest. hi and lo are two rows of the B
 //    operand, their sums two accumulators, joined as (hi + lo/32) * f.
-// The accumulators are fp32 (checked: sums of exact products come out exact).
+// The accumulators are fp32: sums of exact products come out exact, also where terms
+// lie 2^21 apart (tested with whole numbers).
 //
 // Sums are kept as a 2^10th of what they are until they leave the tile (the staged
 // sum x and f are times 2^-10): f, which undoes x's scaling, would not
@@ -618,14 +619,11 @@ struct Row {
         }
     }
 
-    // The three groups' sums of the tile's rows meet in tensor memory (each group
-    // its own A columns, `tm` being the first with the warp's lanes): sums[i]
-    // becomes the total of vector group + 3 i, added from group `first` on, which
-    // had the tile's first slot.
-    // Or one group, the tile's owner, gets all of its sums when it has time, and all
-    // go on to their next tile at once: they leave theirs in columns `ex` (three
-    // sets of 8), free when `freed` says so, and arrive on `joined`. `use` counts the
-    // owner's tiles; c: the group's place in the order of the sums.
+    // How the three groups' sums of a tile's rows meet. Either (give, take) other warps
+    // get them all when they have time, and the groups go on to their next tile at once:
+    // these leave theirs in columns `ex` of tensor memory (three sets of 8), free when
+    // `freed` says so, and arrive on `joined`. `use`: the tiles that had the columns
+    // before; c: the group's place in the order of the sums.
     __device__ __forceinline__ void give(const Waits &wait, uint32_t ex, int c, uint32_t joined, uint32_t freed, int use, int lane) const
     {
         if (use > 0) wait(freed, (use - 1) & 1);
@@ -657,6 +655,10 @@ struct Row {
         if (lane == 0) mbar_arrive(freed);
     }
 
+    // Or (join) the groups wait for one another and share them: through tensor memory
+    // (each group its own A columns, `tm` being the first with the warp's lanes) sums[i]
+    // becomes the total of vector group + 3 i, added from group `first` on, which had
+    // the tile's first slot.
     static constexpr int kOwn = (NC + kGroups - 1) / kGroups;
     __device__ __forceinline__ void join(uint32_t tm, int group, int first, float (&sums)[kOwn])
     {

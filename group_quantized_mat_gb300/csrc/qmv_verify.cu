@@ -20,10 +20,10 @@
 //     the race on the one row that matters; the last of a sequence's blocks joins
 //     the winners and writes the results.
 //
-// Measured (us; bytes it cannot do without, at 6.8 TB/s): 13.4 for one sequence of 3
-// drafts and 32000 tokens (0.1: the two kernels' chain), 17.3 for 8 x 4 x 50257 fp32
-// from unaligned rows (2.1), 30.8 for 24 x 12 looked-up drafts of 101001 (10), 60 for
-// 64 x 7 x 131072 (42: rows at 6 TB/s, then 18 us of race).
+// Measured (us; bytes of the rows that are needed, at 6.7 TB/s): 14.2 for one sequence
+// of 3 drafts and 32000 tokens (0.1: the two kernels' chain), 18 for 8 x 4 x 50257 fp32
+// from unaligned rows (1.5), 31 for 24 x 12 looked-up drafts of 101001 (7), 60 for
+// 64 x 7 x 131072 (31: 41 us of rows, then 18 of race).
 #include <cuda_bf16.h>
 
 #include <cfloat>

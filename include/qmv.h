@@ -311,10 +311,12 @@ QMV_API qmv_status qmv_mxfp4_run(const uint32_t *w_q, const uint8_t *scales, con
  *              rank are padded with zeros).
  *  flags       QMV_F32_OUT.
  *
- * Arithmetic: the products and sums of both terms are fp32 (the group's
- * factored form, as for qmv_run, but summed by the tensor cores in another fixed
- * order), the inner vector A x is kept in fp32, and the sum of the two terms is
- * rounded once. A vector's result does not depend on the other vectors of the
+ * Arithmetic: the sums of both terms are fp32 (the group's factored form, as for
+ * qmv_run, but summed by the tensor cores in another fixed order), the inner vector
+ * A x is kept in fp32, and the sum of the two terms is rounded once. The tensor
+ * cores multiply x exactly down to 2^-14 of the largest of its 64 (2^-12 for 2-bit
+ * weights); an element below that is rounded, by at most 2^-22 (2^-20) of that
+ * largest. A vector's result does not depend on the other vectors of the
  * call: it is bit-identical to an M = 1 call on that vector. A vector that holds
  * an infinity or NaN gives NaN throughout.
  *
@@ -356,10 +358,12 @@ QMV_API qmv_status qmv_lora_run(const uint32_t *w_q, const uint16_t *scales, con
  *                    at most QMV_MAX_CHOICES.
  *  flags             QMV_F32_OUT, QMV_MOE_GELU, QMV_MOE_SOFTMAX_ALL.
  *
- * A NaN router logit counts as -inf. Arithmetic: fp32 sums throughout; h keeps
- * 16 bits of significand between the two products (elements far below the largest
- * of their 64 fewer, down to 2^-30 of it); y is rounded once. A token's result does not depend on the other
- * tokens of the call. An infinity or NaN in x or h makes the token's y NaN.
+ * A NaN router logit counts as -inf. Arithmetic: fp32 sums throughout; x is
+ * multiplied as in qmv_lora_run; h keeps 19 bits of significand between the two
+ * products (elements below 2^-11 of the largest of their 64 fewer, with an error of
+ * at most 2^-30 of it), also with QMV_F32_OUT; y is rounded once. A token's result
+ * does not depend on the other tokens of the call. An infinity or NaN in x or h
+ * makes the token's y NaN.
  *
  * Errors: as for qmv_lora_run; QMV_ERR_SHAPE also when inter is not a multiple of
  * group_size or experts x rows x groups reaches 2^31. */
