@@ -30,6 +30,9 @@ SB_INTERLEAVED = 0x8
 MOE_GELU = 0x10
 MOE_SOFTMAX_ALL = 0x20
 VERIFY_F32_LOGITS = 0x40
+ROPE_F32_IN = 0x80
+ROPE_NEIGHBOURS = 0x100
+ROPE_NORM_PLUS_ONE = 0x200
 
 STATUS = {
     0: "QMV_OK", 1: "QMV_ERR_NULL", 2: "QMV_ERR_BITS", 3: "QMV_ERR_GROUP", 4: "QMV_ERR_SHAPE",
@@ -40,7 +43,8 @@ STATUS = {
 
 EXPORTED = ("qmv_packed_words", "qmv_pack", "qmv_unpack", "qmv_pack_sb", "qmv_split_count", "qmv_workspace_size",
             "qmv_run", "qmv_run_ex", "qmv_run_noalloc", "qmv_mxfp4_run", "qmv_workspace_init", "qmv_lora_workspace_size", "qmv_lora_run",
-            "qmv_moe_workspace_size", "qmv_moe_run", "qmv_verify_workspace_size", "qmv_verify_run", "qmv_device_error", "qmv_last_cuda_error",
+            "qmv_moe_workspace_size", "qmv_moe_run", "qmv_verify_workspace_size", "qmv_verify_run", "qmv_rope_run",
+            "qmv_attend_workspace_size", "qmv_attend_run", "qmv_device_error", "qmv_last_cuda_error",
             "qmv_status_string")
 
 
@@ -102,6 +106,13 @@ def load(path: str | None = None) -> ctypes.CDLL:
         lib.qmv_verify_workspace_size.argtypes = [I] * 3
         lib.qmv_verify_run.restype = I
         lib.qmv_verify_run.argtypes = [P] * 10 + [I] * 3 + [I64] * 3 + [P, SZ, U, P]
+        F = ctypes.c_float
+        lib.qmv_rope_run.restype = I
+        lib.qmv_rope_run.argtypes = [P] * 10 + [I] * 8 + [F] + [I64] * 4 + [U, P]
+        lib.qmv_attend_workspace_size.restype = SZ
+        lib.qmv_attend_workspace_size.argtypes = [I] * 10
+        lib.qmv_attend_run.restype = I
+        lib.qmv_attend_run.argtypes = [P] * 8 + [I] * 9 + [F, I, I] + [I64] * 5 + [P, SZ, U, P]
         lib.qmv_workspace_init.restype = I
         lib.qmv_workspace_init.argtypes = [P, SZ, P]
         lib.qmv_device_error.restype = I
@@ -277,6 +288,49 @@ def qmv_verify_run(target, draft, draft_tokens, draft_len, temperature, uniform,
                                  V if ld_noise is None else ld_noise, _ptr(workspace), workspace_bytes, flags,
                                  _stream(stream))
     _check(code, "qmv_verify_run")
+
+
+# --------------------------------------------- an attention layer's part --
+def qmv_rope_run(qkv, q_norm, k_norm, positions, inv_freq, axis, slots, q, k_cache, v_cache, T: int, heads: int,
+                 kv_heads: int, head_dim: int, rope_dim: int, page_size: int, pages: int, axes: int = 1,
+                 eps: float = 1e-6, ld_qkv: int | None = None, page_stride: int | None = None,
+                 token_stride: int | None = None, head_stride: int | None = None, flags: int = 0, stream=None) -> None:
+    """Norms and rotation of each head's query and key, and the new keys and values put into the paged cache; see
+    include/qmv.h. The strides default to those of whole rows and of a cache [pages, page_size, kv_heads, head_dim]."""
+    code = load().qmv_rope_run(_ptr(qkv), _ptr(q_norm), _ptr(k_norm), _ptr(positions), _ptr(inv_freq), _ptr(axis),
+                               _ptr(slots), _ptr(q), _ptr(k_cache), _ptr(v_cache), T, heads, kv_heads, head_dim,
+                               rope_dim, page_size, pages, axes, eps,
+                               (heads + 2 * kv_heads) * head_dim if ld_qkv is None else ld_qkv,
+                               page_size * kv_heads * head_dim if page_stride is None else page_stride,
+                               kv_heads * head_dim if token_stride is None else token_stride,
+                               head_dim if head_stride is None else head_stride, flags, _stream(stream))
+    _check(code, "qmv_rope_run")
+
+
+def qmv_attend_workspace_size(B: int, T: int, max_new: int, heads: int, kv_heads: int, head_dim: int, page_size: int,
+                              max_pages: int, window: int = 0, sinks: int = 0) -> int:
+    return int(load().qmv_attend_workspace_size(B, T, max_new, heads, kv_heads, head_dim, page_size, max_pages, window,
+                                                sinks))
+
+
+def qmv_attend_run(q, k_cache, v_cache, page_table, q_start, kv_len, out, lse, B: int, T: int, max_new: int, heads: int,
+                   kv_heads: int, head_dim: int, page_size: int, pages: int, max_pages: int, scale: float | None = None,
+                   window: int = 0, sinks: int = 0, ld_q: int | None = None, ld_out: int | None = None,
+                   page_stride: int | None = None, token_stride: int | None = None, head_stride: int | None = None,
+                   workspace=None, workspace_bytes: int = 0, flags: int = 0, stream=None) -> None:
+    """Attention of new tokens over a paged cache; see include/qmv.h. The scale defaults to head_dim ** -0.5, the
+    strides to those of whole rows and of a cache [pages, page_size, kv_heads, head_dim]."""
+    if scale is None:
+        scale = head_dim ** -0.5 if head_dim > 0 else 1.0
+    code = load().qmv_attend_run(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(page_table), _ptr(q_start), _ptr(kv_len),
+                                 _ptr(out), _ptr(lse), B, T, max_new, heads, kv_heads, head_dim, page_size, pages,
+                                 max_pages, scale, window, sinks,
+                                 heads * head_dim if ld_q is None else ld_q, heads * head_dim if ld_out is None else ld_out,
+                                 page_size * kv_heads * head_dim if page_stride is None else page_stride,
+                                 kv_heads * head_dim if token_stride is None else token_stride,
+                                 head_dim if head_stride is None else head_stride, _ptr(workspace), workspace_bytes,
+                                 flags, _stream(stream))
+    _check(code, "qmv_attend_run")
 
 
 def qmv_workspace_init(workspace, nbytes: int, stream=None) -> None:

@@ -754,7 +754,7 @@ extern "C" const char *qmv_status_string(qmv_status s)
         case QMV_ERR_WORKSPACE: return "QMV_ERR_WORKSPACE: workspace smaller than qmv_workspace_size()";
         case QMV_ERR_VALUE: return "QMV_ERR_VALUE: a quantized value does not fit in `bits` bits";
         case QMV_ERR_FLAGS: return "QMV_ERR_FLAGS: unknown flag bits";
-        case QMV_ERR_COUNT: return "QMV_ERR_COUNT: a count (adapters, rank, experts, top_k, batch, drafts) out of range";
+        case QMV_ERR_COUNT: return "QMV_ERR_COUNT: a count (adapters, rank, experts, top_k, batch, drafts, tokens, heads, axes) out of range";
     }
     return "unknown qmv_status";
 }

@@ -60,7 +60,7 @@ typedef enum qmv_status {
     QMV_ERR_VALUE = 9,      /* qmv_pack: an input value does not fit in `bits` bits        */
     QMV_ERR_FLAGS = 10,     /* unknown bits set in `flags`                                 */
     QMV_ERR_COUNT = 11      /* a count (adapters, rank, experts, top_k, batch, drafted
-                               tokens) is outside its range                               */
+                               tokens, tokens, heads, axes) is outside its range          */
 } qmv_status;
 
 /* The CUDA stream type (identical to cudaStream_t; 0 is the legacy default stream). */
@@ -429,6 +429,121 @@ QMV_API qmv_status qmv_verify_run(const void *target, const void *draft, const i
                                   const float *noise, int32_t *tokens, int32_t *accepted, float *logprob, int B,
                                   int S, int V, int64_t ld_target, int64_t ld_draft, int64_t ld_noise,
                                   void *workspace, size_t workspace_bytes, unsigned flags, qmv_stream_t stream);
+
+/* --------------------------------------------- an attention layer's part -- */
+
+/* Between the projections of a layer's queries, keys and values and that of its
+ * output: norms, rotation and the write to a paged cache (qmv_rope_run), and the
+ * attention of new tokens over that cache (qmv_attend_run). Both follow the rules
+ * above (asynchronous, checked on the host, outputs beside inputs).
+ *
+ * A cache is two device arrays, one of keys and one of values, bf16, 16-byte
+ * aligned. The key of kv head g in place o of page p is the head_dim elements from
+ *
+ *   p * page_stride + o * token_stride + g * head_stride
+ *
+ * on, and the value is at the same place of the other array. The strides are in
+ * elements, multiples of 8, and no two rows overlap: [pages, page_size, kv_heads,
+ * head_dim] and [pages, kv_heads, page_size, head_dim] are the usual orders.
+ *  page_size   a multiple of 8 up to 65536.  pages 1 .. 2^31 - 1.
+ *  kv_heads    1 .. QMV_MAX_KV_HEADS; heads a multiple of it, at most
+ *              QMV_MAX_HEAD_GROUP times as many. Query head h goes with kv head
+ *              h / (heads / kv_heads).
+ *  head_dim    64, 128 or 256.  T 1 .. QMV_MAX_TOKENS, T (heads + 2 kv_heads) below 2^31. */
+#define QMV_MAX_KV_HEADS 1024
+#define QMV_MAX_HEAD_GROUP 64
+#define QMV_MAX_TOKENS (1 << 22)
+
+/* Norms of each head's query and key, rotation by position, and the new keys and
+ * values put into the cache, in one pass over a projection's output:
+ *
+ *   x' = x / sqrt(mean(x^2) + eps) * w             for each query and key head, w per element
+ *   (a, b) -> (a cos - b sin, a sin + b cos)       for each pair i of the first rope_dim elements,
+ *                                                  by the angle positions[axis[i], t] * inv_freq[i]
+ *
+ *  qkv         device, bf16 (fp32 with QMV_ROPE_F32_IN) [T, ld_qkv]: a row holds the
+ *              queries' heads, the keys', then the values', 16-byte aligned.
+ *  q_norm,     device, bf16 [head_dim]: w (1 + w is taken with QMV_ROPE_NORM_PLUS_ONE),
+ *  k_norm      16-byte aligned, or NULL: no norm of the queries (the keys).
+ *  positions   device, int32 [axes, T].  inv_freq  device, float [rope_dim / 2], finite.
+ *  axis        device, uint8 [rope_dim / 2]: the axis by whose position a pair turns, or
+ *              NULL (axis 0 for all); a value from axes on counts as axes - 1.
+ *  slots       device, int64 [T]: the place p * page_size + o of a token's key and value;
+ *              outside [0, pages * page_size) the token is not stored. Two tokens of
+ *              one place leave a mixture of their rows there. NULL: nothing is stored,
+ *              k_cache and v_cache may be NULL.
+ *  q           device, bf16 [T, heads, head_dim], 16-byte aligned: the turned queries.
+ *  rope_dim    0, or a multiple of 16 up to head_dim. Pair i is the elements i and
+ *              i + rope_dim / 2, or 2 i and 2 i + 1 with QMV_ROPE_NEIGHBOURS. With 0
+ *              positions and inv_freq may be NULL.
+ *  axes        1 .. QMV_MAX_AXES.  eps >= 0.
+ *  ld_qkv      elements from row to row, at least (heads + 2 kv_heads) head_dim, a multiple of 8.
+ *
+ * Arithmetic: fp32, rounded once. An angle is reduced to a fraction of a turn in 64-bit
+ * fixed point, so that far positions keep their fraction (an error of at most
+ * |position| 2^-50 radians and 2^-24 of a turn). A token's result does not depend on the
+ * other tokens of the call.
+ *
+ * Errors: QMV_ERR_NULL, QMV_ERR_COUNT (T, heads, kv_heads, axes), QMV_ERR_SHAPE (head_dim,
+ * rope_dim, page_size, pages, strides, eps), QMV_ERR_FLAGS, QMV_ERR_ALIGN, QMV_ERR_CUDA. */
+#define QMV_MAX_AXES 4
+#define QMV_ROPE_F32_IN 0x80u
+#define QMV_ROPE_NEIGHBOURS 0x100u
+#define QMV_ROPE_NORM_PLUS_ONE 0x200u
+QMV_API qmv_status qmv_rope_run(const void *qkv, const uint16_t *q_norm, const uint16_t *k_norm,
+                                const int32_t *positions, const float *inv_freq, const uint8_t *axis,
+                                const int64_t *slots, uint16_t *q, uint16_t *k_cache, uint16_t *v_cache, int T,
+                                int heads, int kv_heads, int head_dim, int rope_dim, int page_size, int pages,
+                                int axes, float eps, int64_t ld_qkv, int64_t page_stride, int64_t token_stride,
+                                int64_t head_stride, unsigned flags, qmv_stream_t stream);
+
+/* Attention of new tokens over a paged cache that holds their keys and values
+ * already: for query i of sequence b at position  t = kv_len[b] - n[b] + i,
+ *
+ *   out = sum_j p_j v_j / sum_j p_j,   p_j = exp(scale q . k_j),
+ *
+ * over the keys j <= t, and with a window only those with j > t - window or j < sinks.
+ *
+ *  q           device, bf16 [T, ld_q], 16-byte aligned: a row holds the heads of a token.
+ *  page_table  device, int32 [B, max_pages]: the page of keys page_size * i and on. Only
+ *              entries of pages with a key that some query sees are used; keys of a
+ *              page outside [0, pages) are not seen by any query.
+ *  q_start     device, int32 [B + 1]: sequence b's new tokens are the rows q_start[b] ..
+ *              q_start[b+1] - 1 (n[b] of them, in order; from 0 to max_new). Rows of no
+ *              sequence are left as they are. NULL: max_new rows for each, T = B max_new.
+ *  kv_len      device, int32 [B]: its keys, those of the new tokens among them; taken into
+ *              [0, max_pages * page_size].
+ *  out         device, bf16 [T, ld_out], 16-byte aligned.
+ *  lse         device, float [T, heads], or NULL: log of sum_j p_j.
+ *  B           1 .. QMV_MAX_SEQUENCES.  max_new 1 .. T: new tokens of a sequence at most;
+ *              a sequence with more of them has the first max_new rows computed (at the
+ *              positions that its n[b] gives).
+ *  max_pages   page-table entries of a sequence; max_pages * page_size at most 2^26.
+ *  scale       finite.  window 1 .. 2^30, or 0: none.  sinks 0 .. 2^30, without a window not used.
+ *  ld_q,       elements from row to row, at least heads * head_dim, multiples of 8.
+ *  ld_out
+ *  flags       0.
+ *
+ * A query that sees no key gives zeros, and -inf in lse. What lies in the cache
+ * behind a sequence's keys, or in pages that no query of the sequence sees, has no
+ * influence, whatever it holds. An infinity or NaN in a key or value that some query
+ * of the sequence sees may reach other queries of the sequence in the call.
+ *
+ * Arithmetic: fp32 scores, maxima and sums; out is rounded once.
+ *
+ * Errors: QMV_ERR_NULL, QMV_ERR_COUNT (B, T, max_new, heads, kv_heads), QMV_ERR_SHAPE
+ * (head_dim, page_size, pages, max_pages, scale, window, sinks, strides), QMV_ERR_FLAGS,
+ * QMV_ERR_ALIGN, QMV_ERR_WORKSPACE, QMV_ERR_CUDA. */
+#define QMV_MAX_SEQUENCES 1024
+QMV_API size_t qmv_attend_workspace_size(int B, int T, int max_new, int heads, int kv_heads, int head_dim,
+                                         int page_size, int max_pages, int window, int sinks);
+QMV_API qmv_status qmv_attend_run(const uint16_t *q, const uint16_t *k_cache, const uint16_t *v_cache,
+                                  const int32_t *page_table, const int32_t *q_start, const int32_t *kv_len,
+                                  uint16_t *out, float *lse, int B, int T, int max_new, int heads, int kv_heads,
+                                  int head_dim, int page_size, int pages, int max_pages, float scale, int window,
+                                  int sinks, int64_t ld_q, int64_t ld_out, int64_t page_stride,
+                                  int64_t token_stride, int64_t head_stride, void *workspace,
+                                  size_t workspace_bytes, unsigned flags, qmv_stream_t stream);
 
 /* Zero-fills `bytes` of a caller workspace on `stream` (cudaMemsetAsync). Calls
  * do not need it (a workspace holds no state between calls); kept as a
