@@ -26,7 +26,8 @@ CU_SOURCES = ["qmv_api.cu", "qmv_noalloc.cu", "qmv_mx.cu", "qmv_lora.cu", "qmv_m
               "qmv_inst_b4g64.cu", "qmv_inst_b4g128.cu", "qmv_inst_b2g64.cu", "qmv_inst_b2g128.cu"]
 CXX_SOURCES = ["qmv_codec.cpp"]
 HEADERS = ["qmv_plan.h", "qmv_kernel.cuh", "qmv_launch.cuh", "qmv_launch_decl.h", "qmv_tile.cuh", "qmv_tile_plan.h",
-           "qmv_lora_plan.h", "qmv_cache.h"]
+           "qmv_lora_plan.h", "qmv_cache.h",
+           "qmv_attend_plan.h"]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_103a,code=sm_103a",

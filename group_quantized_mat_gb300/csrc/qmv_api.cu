@@ -525,6 +525,16 @@ qmv_status current_device(DeviceInfo *out)
     return device_error_ptr(out->dev, &out->err);
 }
 
+namespace {
+qmv_status encoded(int r)
+{
+    if (r == 0) return QMV_OK;
+    snprintf(g_last_error, sizeof g_last_error, "cuTensorMapEncodeTiled returned %d%s", r,
+             r < 0 ? " (driver entry point not found)" : "");
+    return QMV_ERR_CUDA;
+}
+}  // namespace
+
 qmv_status encode_rows(CUtensorMap *map, const void *w, long long row_bytes, long long rows, int box_elems,
                        int box_rows, bool swizzle, long long blocks, int box_blocks)
 {
@@ -539,10 +549,26 @@ qmv_status encode_rows(CUtensorMap *map, const void *w, long long row_bytes, lon
                    CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE));
     }
-    if (r == 0) return QMV_OK;
-    snprintf(g_last_error, sizeof g_last_error, "cuTensorMapEncodeTiled returned %d%s", r,
-             r < 0 ? " (driver entry point not found)" : "");
-    return QMV_ERR_CUDA;
+    return encoded(r);
+}
+
+qmv_status encode_bf16(CUtensorMap *map, const void *at, int rank, const int64_t *dims, const int64_t *strides, const int *box)
+{
+    auto fn = encode_fn();
+    int r = -1;
+    if (fn) {
+        cuuint64_t d[4], s[3];
+        cuuint32_t b[4];
+        const cuuint32_t estr[4] = {1, 1, 1, 1};
+        for (int i = 0; i < rank; ++i) {
+            d[i] = cuuint64_t(dims[i]);
+            b[i] = cuuint32_t(box[i]);
+            if (i > 0) s[i - 1] = cuuint64_t(strides[i - 1]) * 2;
+        }
+        r = int(fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, cuuint32_t(rank), const_cast<void *>(at), d, s, b, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE));
+    }
+    return encoded(r);
 }
 
 qmv_status scratch(const DeviceInfo &d, size_t need, void *given, size_t given_bytes, void **out)

@@ -3,40 +3,711 @@
 // The simplest kernel that is right: a warp for each query head of each new token,
 // over the keys that it sees one after the other, with the running maximum and sum
 // of a softmax. Every key is read once for each query head.
+#include <cuda.h>
 #include <cuda_bf16.h>
 
 #include <cmath>
 #include <cstdint>
 
 #include "qmv.h"
+#include "qmv_attend_plan.h"
 #include "qmv_cache.h"
 #include "qmv_launch.cuh"
+#include "qmv_tile.cuh"
 
 namespace qmv {
 namespace {
+
+using namespace attend;
+using tile::named_sync;
+using tile::settle;
+using tile::tmem_commit;
+using tile::tmem_fence_after;
+using tile::tmem_fence_before;
+using tile::tmem_ld;
+using tile::tmem_wait_ld;
+using tile::tmem_wait_st;
+using tile::Waits;
 
 struct AttendParams {
     const uint16_t *q, *k, *v;
     const int32_t *table, *q_start, *kv_len;
     uint16_t *out;
     float *lse;
-    int B, T, max_new, heads, group;
+    int B, T, max_new, heads, kv_heads, group;
     int page_size, pages, max_pages;
+    int box;  // keys of a tensor-map box: all of one page
     float scale;
     int window, sinks;
     int64_t ld_q, ld_out, page_stride, token_stride, head_stride;
+    unsigned *err;
+    // few tokens: the plan, and the workspace's parts
+    int tokens, rows, units, slots;
+    int p_off, q_off, misc_off;
+    int32_t *prefix;
+    float2 *meta;
+    float *parts;
 };
 
-// First row, new tokens and keys of a sequence.
+// First row, new tokens (and those of them that are computed), keys and the first new
+// token's position of a sequence.
 struct Sequence {
-    int row, n, keys;
+    int row, n, done, keys, pos;
+    __device__ __forceinline__ Sequence(const AttendParams &p, const int4 &kept) : row(kept.x), n(kept.y), done(min(n, p.max_new)), keys(kept.z), pos(keys - n) {}
     __device__ __forceinline__ Sequence(const AttendParams &p, int b)
     {
         row = p.q_start ? min(max(__ldg(p.q_start + b), 0), p.T) : b * p.max_new;
         n = p.q_start ? min(max(__ldg(p.q_start + b + 1), row), p.T) - row : p.max_new;
+        done = min(n, p.max_new);
         keys = min(max(__ldg(p.kv_len + b), 0), p.max_pages * p.page_size);
+        pos = keys - n;
     }
 };
+
+// Keys that some of a sequence's queries at positions first .. last see: below `end`, and
+// from `low` on or below `first` (of which none where there is no window).
+struct Seen {
+    int end, low, sinks;
+    __device__ __forceinline__ Seen(const AttendParams &p, int first, int last)
+    {
+        end = max(last + 1, 0);
+        low = p.window ? max(first - p.window + 1, 0) : 0;
+        sinks = p.window ? min(p.sinks, low) : 0;
+    }
+    __device__ __forceinline__ bool operator()(int key) const { return key < end && (key >= low || key < sinks); }
+    // Does it hold for a key of key .. key + n - 1?
+    __device__ __forceinline__ bool any(int key, int n) const { return key < end && (key + n > low || key < sinks); }
+};
+
+__device__ __forceinline__ float exp2_fast(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// 2^e for a whole number e <= 0, exactly (0 below 2^-126).
+__device__ __forceinline__ float power_of_two(float e) { return e < -126.0f ? 0.0f : tile::exp2i(int(e)); }
+
+// The largest of a warp's values, of those that are numbers, for each of N = 16 or 32: a
+// lane ends with that of value lane / (32 / N). Each step halves what a lane keeps.
+template <int N>
+__device__ __forceinline__ float max_scatter(float (&v)[N], int lane)
+{
+#pragma unroll
+    for (int m = 16, n = N / 2; m > 0; m /= 2, n = n > 1 ? n / 2 : n) {
+        if (m < 32 / N) {
+            v[0] = fmaxf(v[0], __shfl_xor_sync(0xffffffffu, v[0], m));
+            continue;
+        }
+        const bool upper = (lane & m) != 0;
+#pragma unroll
+        for (int i = 0; i < n; ++i) {
+            const float keep = upper ? v[n + i] : v[i], send = upper ? v[i] : v[n + i];
+            v[i] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, send, m));
+        }
+    }
+    return v[0];
+}
+
+__device__ __forceinline__ float warp_max(float x)
+{
+#pragma unroll
+    for (int m = 16; m > 0; m /= 2) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, m));
+    return x;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, int x, int y, int z, int w, uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+        : "memory");
+}
+
+// Descriptor of an operand in shared memory: `leading` and `stride` bytes as the layout
+// has them, layout 2 for the 128-byte swizzle and 4 for the 64-byte one.
+__device__ __forceinline__ uint64_t descriptor(uint32_t addr, uint32_t leading, uint32_t stride, uint32_t layout)
+{
+    return uint64_t((addr >> 4) & 0x3fffu) | uint64_t((leading >> 4) & 0x3fffu) << 16 | uint64_t((stride >> 4) & 0x3fffu) << 32 |
+           uint64_t(1) << 46 | uint64_t(layout) << 61;
+}
+
+// Kind of a product of bf16 operands with fp32 sums, 128 x N; a operand whose rows
+// are contiguous instead of its products' index is `rows` major.
+__host__ __device__ constexpr uint32_t mma_kind(int N, bool a_rows, bool b_rows)
+{
+    return 1u << 4 | 1u << 7 | 1u << 10 | uint32_t(a_rows) << 15 | uint32_t(b_rows) << 16 | uint32_t(N >> 3) << 17 | (128u >> 4) << 24;
+}
+
+// D (128 x N fp32, tensor memory) (+)= A (128 x 16) B^T (N x 16), both from shared memory.
+template <uint32_t KIND>
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, bool add)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(KIND), "r"(uint32_t(add))
+        : "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void tmem_st(uint32_t a, const float (&v)[N])
+{
+    static_assert(N == 16, "columns");
+    uint32_t r[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(v[i]);
+    tile::tmem_st(a, r);
+}
+
+// ------------------------------------------------------------ few new tokens --
+//
+// Sequences of up to 16 new tokens. The query rows of one kv head (tokens x group of
+// them) are columns, keys are rows:
+//
+//   S^T (keys x columns)          = K Q^T         K from shared memory as it lies in the cache
+//   P^T = exp2(S^T scale log2(e) - m)             a thread has a key, in registers
+//   O^T (head_dim x columns)     += V^T P^T       V from shared memory as it lies in the cache
+//
+// both by tcgen05, keys and values brought by TMA through a ring of 16 KB slots. The
+// products' cost does not depend on how few columns are in use, and it is hidden: the
+// bytes of K and V are what bounds it. P is kept in two bf16 terms (16 bits of it), as
+// 2 x columns columns of one product, so that the weights' rounding is below that of
+// fp32 sums' order.
+//
+// Order. A work item is a unit of 512 keys, from a multiple of 512 on, in leaves of 256,
+// whose products are added in the order of keys; a column's reference m is a whole
+// number, from the maxima of its leaves so far, so that a change of m scales by powers
+// of two without a rounding. Units are joined by attend_join in an order given by
+// their places. So a row's result depends on its query and the keys that it sees alone:
+// not on the other tokens of the call, nor on how many SMs there are.
+
+struct Item {
+    int b, g, block, unit, index;  // index: of the partial sums
+    int row, tokens, rows;         // first row of q, its tokens and columns
+    int pos, n;                    // position of the first token; of the last: pos + tokens - 1
+    int leaf, leaves;
+    bool whole;                    // the sequence has one unit
+};
+
+// Units of a sequence: those of its first tokens, then those from its window on.
+struct Units {
+    int sinks, low, count;
+    __device__ __forceinline__ Units(const AttendParams &p, const Sequence &s)
+    {
+        const Seen seen(p, s.pos, s.pos + s.done - 1);
+        low = seen.low / kUnit;
+        sinks = min((seen.sinks + kUnit - 1) / kUnit, low);
+        count = seen.end > 0 ? sinks + (seen.end - 1) / kUnit - low + 1 : 1;
+        count = s.done > 0 && s.done <= kFew ? min(count, p.units) : 0;
+    }
+    __device__ __forceinline__ int place(int u) const { return u < sinks ? u : low + u - sinks; }
+};
+
+// The sequences in shared memory: each one's first work item, then row, n and keys.
+struct Sequences {
+    const int32_t *first;  // [B + 1]
+    const int4 *kept;      // [B]
+};
+
+__device__ __forceinline__ Item item_at(const AttendParams &p, const Sequences &all, int index)
+{
+    int lo = 0, hi = p.B;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        (all.first[mid] <= index ? lo : hi) = mid;
+    }
+    const Sequence s(p, all.kept[lo]);
+    const Units units(p, s);
+    const int blocks = (s.done + p.tokens - 1) / p.tokens;
+    Item it;
+    it.b = lo;
+    it.index = index;
+    index -= all.first[lo];
+    it.block = index % blocks;
+    index /= blocks;
+    it.g = index % p.kv_heads;
+    it.unit = units.place(index / p.kv_heads);
+    it.row = s.row + it.block * p.tokens;
+    it.tokens = min(p.tokens, s.done - it.block * p.tokens);
+    it.rows = it.tokens * p.group;
+    it.pos = s.pos + it.block * p.tokens;
+    it.whole = units.count == 1;
+    const Seen seen(p, it.pos, it.pos + it.tokens - 1);
+    int from = it.unit * kUnit;
+    int to = min(from + kUnit, seen.end);
+    if (to <= seen.low) to = min(to, seen.sinks);
+    if (from >= seen.sinks) from = max(from, seen.low);  // (sinks <= low)
+    it.leaf = from / kLeaf;
+    it.leaves = from < to ? (to - 1) / kLeaf - it.leaf + 1 : 0;
+    return it;
+}
+
+// What lies behind the ring, the weights and the queries.
+template <int NC>
+struct FewShared {
+    uint64_t full[16], empty[16], q_full, q_empty, s_ready, p_ready[2], o_done, finished;
+    int abort, changed[NC / 16][2];
+    uint32_t tmem;
+    float top[4][NC], sum[4][NC], ref[NC], use[NC], shift[NC], total[NC];
+    int last[NC], low[NC];  // a column sees keys up to `last` and from `low` on
+    int4 seqs[1];           // [B], then the sequences' first items [B + 1]
+};
+
+// A place in the ring and the parity of its lap.
+struct Place {
+    int slot = 0;
+    uint32_t lap = 0;
+    __device__ __forceinline__ void step(int slots)
+    {
+        if (++slot == slots) {
+            slot = 0;
+            lap ^= 1;
+        }
+    }
+};
+
+__host__ __device__ constexpr int few_threads(int NC) { return NC / 16 * 128 + 64; }
+
+template <int D, int NC>
+__global__ void __launch_bounds__(few_threads(NC), NC < 64 ? 2 : 1)
+    attend_few(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const AttendParams p)
+{
+    constexpr int DB = D / 64, HALVES = D < 128 ? 1 : D / 128;  // blocks of 64 elements; tiles of 128 in V^T's rows
+    constexpr int kChunks = 2 * DB;                              // of a leaf's keys, and of its values
+    constexpr int kColumns = 2 * NC + 2 * NC * HALVES, kAlloc = kColumns <= 64 ? 64 : kColumns <= 128 ? 128 : kColumns <= 256 ? 256 : 512;
+    constexpr int kKeyBytes = NC == 16 ? 64 : 128;  // of a key's weights in a block of P
+    constexpr int kThreads = few_threads(NC), kProducer = kThreads / 32 - 2, kTensor = kProducer + 1;
+    extern __shared__ uint8_t raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+    FewShared<NC> &sh = *reinterpret_cast<FewShared<NC> *>(smem + p.misc_off);
+    int32_t *first = reinterpret_cast<int32_t *>(sh.seqs + p.B);
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid & 31;
+    const uint32_t base = smem_u32(smem), full0 = smem_u32(sh.full), empty0 = smem_u32(sh.empty);
+    const uint32_t q_full = smem_u32(&sh.q_full), q_empty = smem_u32(&sh.q_empty), s_ready = smem_u32(&sh.s_ready);
+    const uint32_t p_ready = smem_u32(sh.p_ready), o_done = smem_u32(&sh.o_done), finished = smem_u32(&sh.finished);
+    const uint32_t P = base + p.p_off, Q = base + p.q_off;
+    if (tid == 0) {
+        for (int i = 0; i < p.slots; ++i) {
+            mbar_init(full0 + 8 * i, 1);
+            mbar_init(empty0 + 8 * i, 1);
+        }
+        for (const uint32_t bar : {q_full, q_empty, s_ready, o_done, finished}) mbar_init(bar, 1);
+        mbar_init(p_ready, NC / 4);  // a warp's arrival
+        mbar_init(p_ready + 8, NC / 4);
+        fence_mbar_init();
+        sh.abort = 0;
+    }
+    if (tid < NC / 16) sh.changed[tid][0] = sh.changed[tid][1] = 0;
+    if (warp == kTensor) tile::tmem_alloc(smem_u32(&sh.tmem), kAlloc);
+    grid_launch_dependents();
+    grid_dependency_wait();
+    for (int b = tid; b < p.B; b += kThreads) {
+        const Sequence s(p, b);
+        sh.seqs[b] = make_int4(s.row, s.n, s.keys, 0);
+        first[b + 1] = Units(p, s).count * ((s.done + p.tokens - 1) / p.tokens) * p.kv_heads;
+    }
+    tmem_fence_before();
+    __syncthreads();
+    tmem_fence_after();
+    if (warp == 0) {
+        int sum = 0;
+        for (int b0 = 0; b0 < p.B; b0 += 32) {
+            int v = b0 + lane < p.B ? first[b0 + lane + 1] : 0;
+#pragma unroll
+            for (int d = 1; d < 32; d *= 2) {
+                const int u = __shfl_up_sync(0xffffffffu, v, d);
+                if (lane >= d) v += u;
+            }
+            if (b0 + lane < p.B) first[b0 + lane + 1] = sum + v;
+            sum += __shfl_sync(0xffffffffu, v, 31);
+        }
+        if (lane == 0) first[0] = 0;
+    }
+    __syncthreads();
+    if (blockIdx.x == 0 && p.units > 1)
+        for (int b = tid; b <= p.B; b += kThreads) p.prefix[b] = first[b];
+    const uint32_t tm = sh.tmem, S = tm, O = tm + 2 * NC;
+    const Sequences all{first, sh.seqs};
+    const int items = first[p.B];
+    const Waits wait{&sh.abort, p.err};
+
+    if (warp == kProducer) {
+        // ------------------------------------------------------------- producer
+        const int per_tile = 128 / p.box, boxes = 2 * per_tile;  // a lane has a box of the leaf's keys
+        Place at;
+        int n = 0, issued = 0;
+        bool ok = true;
+        for (int index = blockIdx.x; index < items && ok; index += gridDim.x) {
+            const Item it = item_at(p, all, index);
+            if (it.leaves == 0) continue;  // (no queries are brought for an item without keys)
+            const Seen seen(p, it.pos, it.pos + it.tokens - 1);
+            const int32_t *table = p.table + int64_t(it.b) * p.max_pages;
+            ok = __all_sync(0xffffffffu, n == 0 || wait(q_empty, (n - 1) & 1));
+            if (!ok) break;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(q_full, uint32_t(p.rows) * D * 2);
+                for (int c = 0; c < DB; ++c) tile::tma_load_3d(Q + c * NC * 128, &qmap, 64 * c, it.g * p.group, it.row, q_full);
+            }
+            ++n;
+            for (int leaf = it.leaf; leaf < it.leaf + it.leaves && ok; ++leaf) {
+                const int key = leaf * kLeaf + lane * p.box;
+                int page = -1, place = 0;
+                if (lane < boxes && seen.any(key, p.box)) {
+                    page = __ldg(table + key / p.page_size);
+                    place = key % p.page_size;
+                }
+                if (unsigned(page) >= unsigned(p.pages)) page = p.pages;  // outside the map: zeros
+#pragma unroll 1
+                for (int i = 0; i < 2 * kChunks; ++i, ++issued, at.step(p.slots)) {
+                    if (issued >= p.slots) ok = wait(empty0 + 8 * at.slot, at.lap ^ 1);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    const uint32_t dst = base + at.slot * kChunk, bar = full0 + 8 * at.slot;
+                    if (lane == 0) mbar_arrive_expect_tx(bar, kChunk);
+                    __syncwarp();
+                    const bool values = i >= kChunks;
+                    const int j = values ? i - kChunks : i;
+                    if (!values || D == 64) {
+                        // 128 keys, 64 elements
+                        const int box = lane - j / DB * per_tile;
+                        if (box >= 0 && box < per_tile)
+                            tma_load_4d(dst + box * p.box * 128, values ? &vmap : &kmap, 64 * (j % DB), place, it.g, page, bar);
+                    } else {
+                        // 64 keys, twice 64 elements
+                        const int box = lane - j / HALVES * per_tile / 2;
+                        if (box >= 0 && box < per_tile / 2)
+                            for (int d = 0; d < 2; ++d)
+                                tma_load_4d(dst + d * 8192 + box * p.box * 128, &vmap, 128 * (j % HALVES) + 64 * d, place, it.g, page, bar);
+                    }
+                }
+            }
+        }
+        if (!ok) {
+            // copies in flight have to land before the block ends
+            for (int i = max(issued - p.slots, 0); i < issued; ++i) mbar_wait_bounded(full0 + 8 * (i % p.slots), (i / p.slots) & 1);
+            if (n > 0) mbar_wait_bounded(q_full, (n - 1) & 1);
+        }
+    } else if (warp == kTensor) {
+        // ---------------------------------------------------------- tensor warp
+        if (lane == 0) {
+            constexpr uint32_t kScores = mma_kind(NC, false, false), kValues = mma_kind(2 * NC, true, true);
+            // (head_dim 64: the tile's second 64 rows repeat the first, and are not read)
+            const uint64_t keys0 = descriptor(base, 16, 1024, 2), queries = descriptor(Q, 16, 1024, 2);
+            const uint64_t values0 = descriptor(base, D == 64 ? 0 : 8192, 1024, 2);
+            const uint64_t weights = NC == 16 ? descriptor(P, 16, 512, 4) : descriptor(P, kLeaf * 128, 1024, 2);
+            Place at;
+            int n = 0, leaf = 0;
+            for (int index = blockIdx.x; index < items; index += gridDim.x) {
+                const Item it = item_at(p, all, index);
+                if (it.leaves == 0) continue;
+                wait(q_full, n & 1);
+                for (int l = 0; l < it.leaves; ++l, ++leaf) {
+#pragma unroll 1
+                    for (int i = 0; i < kChunks; ++i, at.step(p.slots)) {
+                        wait(full0 + 8 * at.slot, at.lap);
+                        const int c = i % DB;
+                        const uint64_t a = keys0 + uint32_t(at.slot * (kChunk >> 4)), b = queries + uint32_t(c * NC * (128 >> 4));
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) mma_ss<kScores>(S + i / DB * NC, a + 2 * k, b + 2 * k, c + k > 0);
+                        tmem_commit(empty0 + 8 * at.slot);
+                    }
+                    tmem_commit(s_ready);
+                    if (l == it.leaves - 1) tmem_commit(q_empty);
+#pragma unroll 1
+                    for (int i = 0; i < kChunks; ++i, at.step(p.slots)) {
+                        if (i % DB == 0) {
+                            wait(p_ready + 8 * (i / DB), leaf & 1);
+                            tmem_fence_after();
+                        }
+                        wait(full0 + 8 * at.slot, at.lap);
+                        constexpr int kKeys = D == 64 ? 128 : 64;
+                        const int c = i % HALVES, key = i / HALVES * kKeys;
+                        const uint64_t a = values0 + uint32_t(at.slot * (kChunk >> 4)), b = weights + uint32_t(key * (kKeyBytes >> 4));
+#pragma unroll
+                        for (int k = 0; k < kKeys / 16; ++k)
+                            mma_ss<kValues>(O + c * 2 * NC, a + k * (2048 >> 4), b + k * (16 * kKeyBytes >> 4), l > 0 || key + k > 0);
+                        tmem_commit(empty0 + 8 * at.slot);
+                    }
+                    tmem_commit(o_done);
+                }
+                ++n;
+            }
+            tmem_commit(finished);
+            mbar_wait_bounded(finished, 0);
+        }
+    } else {
+        // ---------------------------------------------------------------- weights
+        // Four warps have 16 columns. A thread has the key `mine` of each of the leaf's
+        // two tiles, then the element `mine` of the sums (and mine + 128 of head_dim
+        // 256). Its lanes of tensor memory are its warp's. (One body of code for 16 columns, and
+        // masks as bits that a short loop makes: with all columns in a thread the code did
+        // not stay in the instruction cache, and a leaf of 64 columns took 20 us.)
+        const int group = warp / 4, c0 = 16 * group, quarter = warp & 3, mine = tid & 127, meet = 1 + group;
+        const uint32_t lanes = uint32_t(quarter * 32) << 16;
+        const float c2 = __fmul_rn(p.scale, 1.4426950408889634f);
+        int leaf = 0;
+#pragma unroll 1
+        for (int index = blockIdx.x; index < items; index += gridDim.x) {
+            const Item it = item_at(p, all, index);
+            const Seen seen(p, it.pos, it.pos + it.tokens - 1);
+            const int32_t *table = p.table + int64_t(it.b) * p.max_pages;
+            if (mine < 16) {
+                const int r = c0 + mine, pos = it.pos + r / p.group;
+                sh.ref[r] = -INFINITY;
+                sh.last[r] = r < it.rows ? pos : -1;
+                sh.low[r] = p.window ? pos - p.window + 1 : 0;
+            }
+            float sum[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) sum[i] = 0.0f;
+            named_sync(meet, 128);
+#pragma unroll 1
+            for (int l = 0; l < it.leaves; ++l, ++leaf) {
+                const int key0 = (it.leaf + l) * kLeaf + mine;
+                int page[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) page[h] = seen(key0 + 128 * h) ? __ldg(table + (key0 + 128 * h) / p.page_size) : -1;
+                wait(s_ready, leaf & 1);
+                tmem_fence_after();
+                uint32_t see[2] = {0xffffu, 0xffffu};  // which columns see the key
+                const bool there0 = unsigned(page[0]) < unsigned(p.pages), there1 = unsigned(page[1]) < unsigned(p.pages);
+                if (!(there0 && there1 && key0 + 128 <= it.pos && (!p.window || key0 >= it.pos + it.tokens - p.window))) {
+#pragma unroll 1
+                    for (int h = 0; h < 2; ++h) {
+                        const int key = key0 + 128 * h;
+                        uint32_t bits = 0;
+#pragma unroll 4
+                        for (int i = 0; i < 16; ++i)
+                            if (key <= sh.last[c0 + i] && (key >= sh.low[c0 + i] || key < p.sinks)) bits |= 1u << i;
+                        (h ? see[1] : see[0]) = (h ? there1 : there0) ? bits : 0u;
+                    }
+                }
+                float s0[16], s1[16], top[16];
+                tmem_ld<16>(S + lanes + c0, s0);
+                tmem_ld<16>(S + lanes + NC + c0, s1);
+                tmem_wait_ld();
+                settle(s0);
+                settle(s1);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    s0[i] = see[0] >> i & 1 ? __fmul_rn(s0[i], c2) : -INFINITY;
+                    s1[i] = see[1] >> i & 1 ? __fmul_rn(s1[i], c2) : -INFINITY;
+                    top[i] = fmaxf(s0[i], s1[i]);
+                }
+                const float m = max_scatter(top, lane);
+                // (lanes 2 i and 2 i + 1 have the largest of column i)
+                if (!(lane & 1)) sh.top[quarter][c0 + lane / 2] = m;
+                named_sync(meet, 128);
+                if (mine < 16) {
+                    const int r = c0 + mine;
+                    float m = fmaxf(fmaxf(sh.top[0][r], sh.top[1][r]), fmaxf(sh.top[2][r], sh.top[3][r]));
+                    if (r >= it.rows) m = -INFINITY;  // (a column without a query)
+                    const float old = sh.ref[r];
+                    // kept while weights stay below 2^8
+                    const float now = m > __fadd_rn(old, 8.0f) ? ceilf(m) : old;
+                    sh.ref[r] = now;
+                    sh.use[r] = now == -INFINITY ? 0.0f : now;
+                    const bool moved = now != old && old != -INFINITY;
+                    sh.shift[r] = moved ? power_of_two(__fsub_rn(old, now)) : 1.0f;
+                    if (moved) sh.changed[group][leaf & 1] = 1;
+                }
+                if (mine == 127) sh.changed[group][(leaf + 1) & 1] = 0;
+                // the last leaf's products are done: P is free, O stands still
+                if (leaf > 0) wait(o_done, (leaf - 1) & 1);
+                named_sync(meet, 128);
+                if (l > 0 && sh.changed[group][leaf & 1]) {
+                    float f[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        f[i] = sh.shift[c0 + i];
+                        sum[i] = __fmul_rn(sum[i], f[i]);
+                    }
+                    tmem_fence_after();
+#pragma unroll 1
+                    for (int c = 0; c < 2 * HALVES; ++c) {
+                        float o[16];
+                        tmem_ld<16>(O + lanes + c * NC + c0, o);
+                        tmem_wait_ld();
+                        settle(o);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) o[i] = __fmul_rn(o[i], f[i]);
+                        tmem_st<16>(O + lanes + c * NC + c0, o);
+                    }
+                    tmem_wait_st();
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float(&w)[16] = h ? s1 : s0;
+                    const int k = h * 128 + mine;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        w[i] = exp2_fast(__fsub_rn(w[i], sh.use[c0 + i]));
+                        sum[i] = __fadd_rn(sum[i], w[i]);
+                    }
+                    uint32_t hi[8], lo[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        hi[i] = pack_bf16(w[2 * i], w[2 * i + 1]);
+                        lo[i] = pack_bf16(__fsub_rn(w[2 * i], __uint_as_float(hi[i] << 16)),
+                                          __fsub_rn(w[2 * i + 1], __uint_as_float(hi[i] & 0xffff0000u)));
+                    }
+                    const uint32_t row = P + k * kKeyBytes, swizzle = NC == 16 ? (k >> 1) & 3 : k & 7;
+                    const int low_at = NC == 16 ? 2 : NC == 32 ? 4 : 0;  // of 64 columns the second terms are a block of their own
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const uint32_t piece = 2 * group + i;
+                        sts_v4_u32(row + ((piece ^ swizzle) << 4), make_uint4(hi[4 * i], hi[4 * i + 1], hi[4 * i + 2], hi[4 * i + 3]));
+                        sts_v4_u32(row + (NC == 64 ? kLeaf * 128 : 0) + (((piece + low_at) ^ swizzle) << 4),
+                                   make_uint4(lo[4 * i], lo[4 * i + 1], lo[4 * i + 2], lo[4 * i + 3]));
+                    }
+                    // Values of keys that no column sees may be anything, and 0 x NaN is NaN: zeros
+                    // in their place. (A tile's values all fit in the ring, and nothing but the
+                    // products of the tile before has to be done for them to land.)
+                    const bool there = h ? there1 : there0;
+                    if (group == 0 && !__all_sync(0xffffffffu, there)) {
+                        const int from = leaf * 2 * kChunks + kChunks;
+#pragma unroll 1
+                        for (int c = 0; c < DB; ++c) {
+                            // 64 elements of the key: which chunk, where
+                            const int chunk = from + (D == 64 ? h : (h * 2 + mine / 64) * HALVES + c / 2);
+                            const int slot = chunk % p.slots;
+                            wait(full0 + 8 * slot, (chunk / p.slots) & 1);
+                            if (!there) {
+                                const uint32_t at = base + slot * kChunk + (D == 64 ? mine * 128 : (c & 1) * 8192 + (mine & 63) * 128);
+                                for (int i = 0; i < 8; ++i) sts_v4_u32(at + 16 * i, make_uint4(0, 0, 0, 0));
+                            }
+                        }
+                    }
+                    tmem_fence_before();
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(p_ready + 8 * h);
+                }
+            }
+            // ------------------------------------------------ what the item gives
+            const float part = tree_reduce_scatter<16>(sum, lane);
+            if (!(lane & 1)) sh.sum[quarter][c0 + lane / 2] = part;
+            named_sync(meet, 128);
+            if (mine < 16 && c0 + mine < it.rows) {
+                const int r = c0 + mine;
+                const float t = __fadd_rn(__fadd_rn(sh.sum[0][r], sh.sum[1][r]), __fadd_rn(sh.sum[2][r], sh.sum[3][r]));
+                if (it.whole) {
+                    const int row = it.row + r / p.group, head = it.g * p.group + r % p.group;
+                    const bool none = sh.ref[r] == -INFINITY;
+                    sh.total[r] = none ? 0.0f : __fdiv_rn(1.0f, t);
+                    if (p.lse)
+                        p.lse[int64_t(row) * p.heads + head] = none ? -INFINITY : __fmul_rn(0.6931471805599453f, __fadd_rn(sh.ref[r], log2f(t)));
+                } else {
+                    p.meta[int64_t(it.index) * p.rows + r] = make_float2(sh.ref[r], t);
+                }
+            }
+            if (it.leaves > 0) wait(o_done, (leaf - 1) & 1);
+            named_sync(meet, 128);
+            tmem_fence_after();
+#pragma unroll 1
+            for (int half = 0; half < HALVES; ++half) {
+                const int d = half * 128 + mine;
+                float a[16], b[16];
+                tmem_ld<16>(O + lanes + half * 2 * NC + c0, a);
+                tmem_ld<16>(O + lanes + half * 2 * NC + NC + c0, b);
+                tmem_wait_ld();
+                settle(a);
+                settle(b);
+                if (d >= D) continue;
+                float *parts = p.parts + (int64_t(it.index) * p.rows + c0) * D + d;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const int r = c0 + i;
+                    if (r >= it.rows) break;
+                    const float o = it.leaves > 0 ? __fadd_rn(a[i], b[i]) : 0.0f;
+                    if (it.whole) {
+                        const int row = it.row + r / p.group, head = it.g * p.group + r % p.group;
+                        const float f = sh.total[r];
+                        reinterpret_cast<__nv_bfloat16 *>(p.out)[row * p.ld_out + head * D + d] = __float2bfloat16_rn(f == 0.0f ? 0.0f : __fmul_rn(o, f));
+                    } else {
+                        parts[i * D] = o;
+                    }
+                }
+            }
+            tmem_fence_before();
+            named_sync(meet, 128);  // (the columns' lists are for the next item now)
+        }
+    }
+    tmem_fence_before();
+    __syncthreads();
+    tmem_fence_after();
+    if (warp == kTensor) tile::tmem_free(tm, kAlloc);
+}
+
+// Joins a row's units: with M the largest of their references (whole numbers), their
+// sums times 2^(ref - M), those of places u = w, w + 8, .. by warp w in order, then the
+// warps' in order. A block has a row.
+constexpr int kJoinWarps = 8;
+template <int D>
+__global__ void __launch_bounds__(kJoinWarps * 32) attend_join(const AttendParams p)
+{
+    constexpr int E = D / 32;
+    __shared__ float s_sum[kJoinWarps][D], s_total[kJoinWarps], s_top[kJoinWarps];
+    grid_dependency_wait();
+    const int few = min(p.max_new, kFew), b = int(blockIdx.x) / few, i = int(blockIdx.x) % few, h = blockIdx.y;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    const Sequence s(p, b);
+    const Units units(p, s);
+    if (i >= s.done || units.count <= 1) return;
+    const int blocks = (s.done + p.tokens - 1) / p.tokens, step = blocks * p.kv_heads * p.rows;
+    const int64_t first = int64_t(p.prefix[b] + h / p.group * blocks + i / p.tokens) * p.rows + i % p.tokens * p.group + h % p.group;
+    float top = -INFINITY;
+    for (int u = threadIdx.x; u < units.count; u += kJoinWarps * 32) top = fmaxf(top, p.meta[first + int64_t(u) * step].x);
+    top = warp_max(top);
+    if (lane == 0) s_top[warp] = top;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) top = fmaxf(top, s_top[w]);
+    float sum[E], total = 0.0f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) sum[e] = 0.0f;
+    const auto part = [&](int from, int to) {
+        // units whose places are the warp's
+        int u = from + ((warp - units.place(from)) & (kJoinWarps - 1));
+#pragma unroll 4
+        for (; u < to; u += kJoinWarps) {
+            const int64_t at = first + int64_t(u) * step;
+            const float2 m = p.meta[at];
+            const float w = m.x == -INFINITY ? 0.0f : power_of_two(__fsub_rn(m.x, top));
+            total = __fmaf_rn(m.y, w, total);
+#pragma unroll
+            for (int e = 0; e < E; ++e) sum[e] = __fmaf_rn(p.parts[at * D + lane + 32 * e], w, sum[e]);
+        }
+    };
+    part(0, units.sinks);
+    part(units.sinks, units.count);
+#pragma unroll
+    for (int e = 0; e < E; ++e) s_sum[warp][lane + 32 * e] = sum[e];
+    if (lane == 0) s_total[warp] = total;
+    __syncthreads();
+    total = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) total = __fadd_rn(total, s_total[w]);
+    const bool none = top == -INFINITY;
+    const int64_t row = s.row + i;
+    if (threadIdx.x < D) {
+        float o = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kJoinWarps; ++w) o = __fadd_rn(o, s_sum[w][threadIdx.x]);
+        reinterpret_cast<__nv_bfloat16 *>(p.out)[row * p.ld_out + h * D + threadIdx.x] = __float2bfloat16_rn(none ? 0.0f : __fdiv_rn(o, total));
+    }
+    if (p.lse && threadIdx.x == 0)
+        p.lse[row * p.heads + h] = none ? -INFINITY : __fmul_rn(0.6931471805599453f, __fadd_rn(top, log2f(total)));
+}
 
 template <int D>
 __global__ void __launch_bounds__(128) attend_simple(const AttendParams p)
@@ -49,8 +720,8 @@ __global__ void __launch_bounds__(128) attend_simple(const AttendParams p)
     for (int b = 0; b < p.B; ++b) {
         const Sequence s(p, b);
         const int i = t - s.row;
-        if (i < 0 || i >= s.n || i >= p.max_new) continue;
-        const int pos = s.keys - s.n + i;
+        if (i < 0 || i >= s.done || s.done <= kFew) continue;
+        const int pos = s.pos + i;
         float q[E], o[E], m = -INFINITY, l = 0.0f;
         for (int e = 0; e < E; ++e) {
             q[e] = __fmul_rn(bf16_bits_to_f32(p.q[t * p.ld_q + h * D + lane + 32 * e]), p.scale);
@@ -79,10 +750,36 @@ __global__ void __launch_bounds__(128) attend_simple(const AttendParams p)
     }
 }
 
+struct Maps {
+    CUtensorMap q, k, v;
+};
+
+template <int D, int NC>
+cudaError_t launch_few(const AttendParams &p, const Maps &m, const FewPlan &f, int sms, cudaStream_t stream)
+{
+    static std::atomic<int> configured[2][64] = {};
+    Launch l;
+    const int64_t most = int64_t(f.ctas) * sms;
+    l.grid = dim3(unsigned(f.items < most ? f.items : most));
+    l.threads = few_threads(NC);
+    l.smem = size_t(f.smem);
+    l.pdl = true;
+    cudaError_t e = launch_one(attend_few<D, NC>, configured[0], l, stream, m.q, m.k, m.v, p);
+    if (e != cudaSuccess || f.units == 1) return e;
+    l.grid = dim3(unsigned(p.B * (p.max_new < kFew ? p.max_new : kFew)), unsigned(p.heads));
+    l.threads = kJoinWarps * 32;
+    l.smem = 0;
+    return launch_one(attend_join<D>, configured[1], l, stream, p);
+}
+
 template <int D>
-cudaError_t launch_attend(const AttendParams &p, cudaStream_t stream)
+cudaError_t launch_attend(const AttendParams &p, const Maps &m, const FewPlan &f, int sms, cudaStream_t stream)
 {
     static std::atomic<int> configured[64] = {};
+    cudaError_t e = f.columns == 16   ? launch_few<D, 16>(p, m, f, sms, stream)
+                    : f.columns == 32 ? launch_few<D, 32>(p, m, f, sms, stream)
+                                      : launch_few<D, 64>(p, m, f, sms, stream);
+    if (e != cudaSuccess || p.max_new <= kFew) return e;
     Launch l;
     l.grid = dim3(unsigned((int64_t(p.T) * p.heads + 3) / 4));
     l.threads = 128;
@@ -101,7 +798,8 @@ qmv_status check_attend(int B, int T, int max_new, int heads, int kv_heads, int 
     if (page_size < 8 || page_size % 8 != 0 || page_size > 65536 || max_pages < 1 || int64_t(max_pages) * page_size > (1 << 26) ||
         window < 0 || window > (1 << 30) || sinks < 0 || sinks > (1 << 30))
         return QMV_ERR_SHAPE;
-    return QMV_OK;
+    const FewPlan f = few_plan(B, max_new, heads, kv_heads, head_dim, int64_t(max_pages) * page_size, window, sinks);
+    return f.workspace > (size_t(1) << 40) || f.items >= (int64_t(1) << 31) ? QMV_ERR_SHAPE : QMV_OK;
 }
 
 }  // namespace
@@ -111,7 +809,7 @@ extern "C" size_t qmv_attend_workspace_size(int B, int T, int max_new, int heads
                                             int max_pages, int window, int sinks)
 {
     if (qmv::check_attend(B, T, max_new, heads, kv_heads, head_dim, page_size, max_pages, window, sinks) != QMV_OK) return 0;
-    return 16;
+    return qmv::attend::few_plan(B, max_new, heads, kv_heads, head_dim, int64_t(max_pages) * page_size, window, sinks).workspace;
 }
 
 extern "C" qmv_status qmv_attend_run(const uint16_t *q, const uint16_t *k_cache, const uint16_t *v_cache,
@@ -153,7 +851,30 @@ extern "C" qmv_status qmv_attend_run(const uint16_t *q, const uint16_t *k_cache,
     p.scale = scale; p.window = window; p.sinks = sinks;
     p.ld_q = ld_q; p.ld_out = ld_out;
     p.page_stride = page_stride; p.token_stride = token_stride; p.head_stride = head_stride;
+    p.kv_heads = kv_heads;
+    p.err = dev.err;
+    const FewPlan f = few_plan(B, max_new, heads, kv_heads, head_dim, int64_t(max_pages) * page_size, window, sinks);
+    p.tokens = f.tokens; p.rows = f.rows; p.units = f.units; p.slots = f.slots;
+    p.p_off = f.p_off; p.q_off = f.q_off; p.misc_off = f.misc_off;
+    uint8_t *at = static_cast<uint8_t *>(ws);
+    p.prefix = reinterpret_cast<int32_t *>(at + f.prefix_off);
+    p.meta = reinterpret_cast<float2 *>(at + f.meta_off);
+    p.parts = reinterpret_cast<float *>(at + f.parts_off);
+    // keys and values by boxes of 64 elements and as many keys of one page as its size allows
+    p.box = 64;
+    while (page_size % p.box) p.box /= 2;
+    Maps m;
+    const int64_t cache_dims[4] = {head_dim, page_size, kv_heads, pages}, cache_strides[3] = {token_stride, head_stride, page_stride};
+    const int cache_box[4] = {64, p.box, 1, 1};
+    const int64_t q_dims[3] = {head_dim, heads, T}, q_strides[2] = {head_dim, ld_q};
+    const int q_box[3] = {64, p.group, f.tokens};
+    st = encode_bf16(&m.k, k_cache, 4, cache_dims, cache_strides, cache_box);
+    if (st == QMV_OK) st = encode_bf16(&m.v, v_cache, 4, cache_dims, cache_strides, cache_box);
+    if (st == QMV_OK) st = encode_bf16(&m.q, q, 3, q_dims, q_strides, q_box);
+    if (st != QMV_OK) return st;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const cudaError_t e = head_dim == 64 ? launch_attend<64>(p, s) : head_dim == 128 ? launch_attend<128>(p, s) : launch_attend<256>(p, s);
+    const cudaError_t e = head_dim == 64    ? launch_attend<64>(p, m, f, dev.sms, s)
+                          : head_dim == 128 ? launch_attend<128>(p, m, f, dev.sms, s)
+                                            : launch_attend<256>(p, m, f, dev.sms, s);
     return e == cudaSuccess ? QMV_OK : record_cuda_failure("attention kernel launch", e);
 }

@@ -1,0 +1,79 @@
+// The launch plan of qmv_attend_run: tiles, what lies where in shared memory and in
+// the workspace. Host code without a CUDA call, so that plans can be checked without a GPU.
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+
+#include "qmv.h"
+
+namespace qmv {
+namespace attend {
+
+constexpr int kFew = QMV_TILE_M;  // new tokens of a sequence up to which they share one read of its keys
+constexpr int kLeaf = 256;        // keys whose weights are formed at once: two tiles of 128
+constexpr int kUnit = 512;        // keys of one work item, from a multiple of 512 on
+constexpr int kChunk = 16384;     // bytes of a ring slot
+constexpr int kSmemSm = 228 * 1024, kSmemBlock = 227 * 1024, kSmemReserved = 1024;
+
+// Work items of sequences of a few new tokens: query rows of one kv head are the
+// columns of a tile, `tokens` of a sequence at a time.
+struct FewPlan {
+    int columns;  // 16, 32 or 64
+    int tokens;   // new tokens of an item at most
+    int blocks;   // items of one kv head and unit
+    int rows;     // columns in use: tokens * group
+    int slots, ctas;
+    int p_off, q_off, misc_off, smem;
+    int units;    // of a sequence at most
+    int64_t items;
+    size_t prefix_off, meta_off, parts_off, workspace;
+};
+
+inline size_t up256(size_t b) { return (b + 255) & ~size_t(255); }
+
+// Fixed shared memory behind the ring: weights of a leaf (two bf16 terms), queries,
+// then barriers, maxima, sums and the sequences.
+inline void few_smem(FewPlan &f, int D, int B)
+{
+    const int p_bytes = kLeaf * f.columns * 4, q_bytes = f.columns * D * 2;
+    const int misc = 512 + f.columns * 4 * 16 + B * 16 + (B + 1) * 4;
+    const int fixed = p_bytes + q_bytes + ((misc + 1023) & ~1023);
+    const int two = (kSmemSm / 2 - kSmemReserved - 1024 - fixed) / kChunk;
+    // (a tile's values, at most four slots, have to be there at once: see the zeroing of unseen rows)
+    f.ctas = f.columns < 64 && two >= 4 ? 2 : 1;
+    f.slots = f.ctas == 2 ? two : (kSmemBlock - 1024 - fixed) / kChunk;
+    if (f.slots > 11) f.slots = 11;
+    f.p_off = f.slots * kChunk;
+    f.q_off = f.p_off + p_bytes;
+    f.misc_off = f.q_off + q_bytes;
+    f.smem = f.slots * kChunk + fixed + 1024;  // (1024: to align the ring)
+}
+
+inline FewPlan few_plan(int B, int max_new, int heads, int kv_heads, int D, int64_t capacity, int window, int sinks)
+{
+    FewPlan f{};
+    const int group = heads / kv_heads, most = max_new < kFew ? max_new : kFew;
+    const int rows = most * group;
+    f.columns = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+    f.tokens = f.columns / group < most ? f.columns / group : most;
+    f.blocks = (most + f.tokens - 1) / f.tokens;
+    f.rows = f.tokens * group;
+    few_smem(f, D, B);
+    int64_t units = (capacity + kUnit - 1) / kUnit;
+    if (window) {
+        // the units of window + most - 1 keys, and those of the first tokens
+        const int64_t near = (int64_t(window) + most - 1 + kUnit - 2) / kUnit + 1, first = (int64_t(sinks) + kUnit - 1) / kUnit;
+        if (near + first < units) units = near + first;
+    }
+    f.units = int(units);
+    f.items = int64_t(B) * kv_heads * f.blocks * units;
+    f.prefix_off = 0;
+    f.meta_off = up256(size_t(B + 1) * 4);
+    f.parts_off = f.meta_off + up256(size_t(f.items) * f.rows * 8);
+    f.workspace = f.units > 1 ? f.parts_off + up256(size_t(f.items) * f.rows * D * 4) : f.meta_off;
+    return f;
+}
+
+}  // namespace attend
+}  // namespace qmv

@@ -62,6 +62,9 @@ qmv_status current_device(DeviceInfo *out);
 // `box_blocks` of them to a box.
 qmv_status encode_rows(CUtensorMap *map, const void *w, long long row_bytes, long long rows, int box_elems,
                        int box_rows, bool swizzle, long long blocks = 1, int box_blocks = 1);
+// A tensor map of a bf16 tensor of up to four dimensions, the first one contiguous
+// (strides in elements), with the 128-byte swizzle; zeros outside the tensor.
+qmv_status encode_bf16(CUtensorMap *map, const void *at, int rank, const int64_t *dims, const int64_t *strides, const int *box);
 qmv_status scratch(const DeviceInfo &d, size_t need, void *given, size_t given_bytes, void **out);
 
 // One launch for V = 1..16 vectors (qmv_mx.cu).
