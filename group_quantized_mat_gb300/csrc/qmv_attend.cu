@@ -36,7 +36,8 @@ struct AttendParams {
     float *lse;
     int B, T, max_new, heads, kv_heads, group;
     int page_size, pages, max_pages;
-    int box;  // keys of a tensor-map box: all of one page
+    int box;              // keys of a tensor-map box: all of one page
+    uint64_t page_magic;  // ceil(2^42 / page_size)
     float scale;
     int window, sinks;
     int64_t ld_q, ld_out, page_stride, token_stride, head_stride;
@@ -79,6 +80,9 @@ struct Seen {
     __device__ __forceinline__ bool any(int key, int n) const { return key < end && (key + n > low || key < sinks); }
 };
 
+// The page of a key, key / page_size: exact for keys below 2^26 and page sizes up to 2^16.
+__device__ __forceinline__ int page_of(const AttendParams &p, int key) { return int(uint64_t(unsigned(key)) * p.page_magic >> 42); }
+
 __device__ __forceinline__ float exp2_fast(float x)
 {
     float y;
@@ -89,25 +93,25 @@ __device__ __forceinline__ float exp2_fast(float x)
 // 2^e for a whole number e <= 0, exactly (0 below 2^-126).
 __device__ __forceinline__ float power_of_two(float e) { return e < -126.0f ? 0.0f : tile::exp2i(int(e)); }
 
-// The largest of a warp's values, of those that are numbers, for each of N = 16 or 32: a
-// lane ends with that of value lane / (32 / N). Each step halves what a lane keeps.
+// The largest of a warp's values, of those that are numbers, for each of 16: lanes 2 i
+// and 2 i + 1 end with that of value i. Each step halves what a lane keeps.
 template <int N>
-__device__ __forceinline__ float max_scatter(float (&v)[N], int lane)
+__device__ __forceinline__ void max_step(float (&v)[16], int lane)
 {
+    const bool upper = (lane & 2 * N) != 0;
 #pragma unroll
-    for (int m = 16, n = N / 2; m > 0; m /= 2, n = n > 1 ? n / 2 : n) {
-        if (m < 32 / N) {
-            v[0] = fmaxf(v[0], __shfl_xor_sync(0xffffffffu, v[0], m));
-            continue;
-        }
-        const bool upper = (lane & m) != 0;
-#pragma unroll
-        for (int i = 0; i < n; ++i) {
-            const float keep = upper ? v[n + i] : v[i], send = upper ? v[i] : v[n + i];
-            v[i] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, send, m));
-        }
+    for (int i = 0; i < N; ++i) {
+        const float keep = upper ? v[N + i] : v[i], send = upper ? v[i] : v[N + i];
+        v[i] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, send, 2 * N));
     }
-    return v[0];
+}
+__device__ __forceinline__ float max_scatter(float (&v)[16], int lane)
+{
+    max_step<8>(v, lane);
+    max_step<4>(v, lane);
+    max_step<2>(v, lane);
+    max_step<1>(v, lane);
+    return fmaxf(v[0], __shfl_xor_sync(0xffffffffu, v[0], 1));
 }
 
 __device__ __forceinline__ float warp_max(float x)
@@ -218,9 +222,10 @@ struct Sequences {
     const int4 *kept;      // [B]
 };
 
-__device__ __forceinline__ Item item_at(const AttendParams &p, const Sequences &all, int index)
+__device__ __noinline__ Item item_at(const AttendParams &p, const Sequences &all, int index)
 {
     int lo = 0, hi = p.B;
+#pragma unroll 1
     while (hi - lo > 1) {
         const int mid = (lo + hi) / 2;
         (all.first[mid] <= index ? lo : hi) = mid;
@@ -254,11 +259,12 @@ __device__ __forceinline__ Item item_at(const AttendParams &p, const Sequences &
 // What lies behind the ring, the weights and the queries.
 template <int NC>
 struct FewShared {
-    uint64_t full[16], empty[16], q_full, q_empty, s_ready, p_ready[2], o_done, finished;
+    uint64_t full[16], empty[16], q_full[2], q_empty[2], s_ready[2], p_ready[2], o_done, finished;
     int abort, changed[NC / 16][2];
     uint32_t tmem;
     float top[4][NC], sum[4][NC], ref[NC], use[NC], shift[NC], total[NC];
     int last[NC], low[NC];  // a column sees keys up to `last` and from `low` on
+    int64_t out[NC];        // where its sums go
     int4 seqs[1];           // [B], then the sequences' first items [B + 1]
 };
 
@@ -283,7 +289,8 @@ __global__ void __launch_bounds__(few_threads(NC), NC < 64 ? 2 : 1)
 {
     constexpr int DB = D / 64, HALVES = D < 128 ? 1 : D / 128;  // blocks of 64 elements; tiles of 128 in V^T's rows
     constexpr int kChunks = 2 * DB;                              // of a leaf's keys, and of its values
-    constexpr int kColumns = 2 * NC + 2 * NC * HALVES, kAlloc = kColumns <= 64 ? 64 : kColumns <= 128 ? 128 : kColumns <= 256 ? 256 : 512;
+    constexpr int kScores = 2 * NC;  // columns of a leaf's scores, of which there are two
+    constexpr int kColumns = 2 * kScores + 2 * NC * HALVES, kAlloc = kColumns <= 128 ? 128 : kColumns <= 256 ? 256 : 512;
     constexpr int kKeyBytes = NC == 16 ? 64 : 128;  // of a key's weights in a block of P
     constexpr int kThreads = few_threads(NC), kProducer = kThreads / 32 - 2, kTensor = kProducer + 1;
     extern __shared__ uint8_t raw[];
@@ -292,17 +299,23 @@ __global__ void __launch_bounds__(few_threads(NC), NC < 64 ? 2 : 1)
     int32_t *first = reinterpret_cast<int32_t *>(sh.seqs + p.B);
     const int tid = threadIdx.x, warp = tid / 32, lane = tid & 31;
     const uint32_t base = smem_u32(smem), full0 = smem_u32(sh.full), empty0 = smem_u32(sh.empty);
-    const uint32_t q_full = smem_u32(&sh.q_full), q_empty = smem_u32(&sh.q_empty), s_ready = smem_u32(&sh.s_ready);
+    const uint32_t q_full = smem_u32(sh.q_full), q_empty = smem_u32(sh.q_empty), s_ready = smem_u32(sh.s_ready);
     const uint32_t p_ready = smem_u32(sh.p_ready), o_done = smem_u32(&sh.o_done), finished = smem_u32(&sh.finished);
     const uint32_t P = base + p.p_off, Q = base + p.q_off;
     if (tid == 0) {
+#pragma unroll 1
         for (int i = 0; i < p.slots; ++i) {
             mbar_init(full0 + 8 * i, 1);
             mbar_init(empty0 + 8 * i, 1);
         }
-        for (const uint32_t bar : {q_full, q_empty, s_ready, o_done, finished}) mbar_init(bar, 1);
-        mbar_init(p_ready, NC / 4);  // a warp's arrival
-        mbar_init(p_ready + 8, NC / 4);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(q_full + 8 * i, 1);
+            mbar_init(q_empty + 8 * i, 1);
+            mbar_init(s_ready + 8 * i, 1);
+            mbar_init(p_ready + 8 * i, NC / 4);  // a warp's arrival
+        }
+        mbar_init(o_done, 1);
+        mbar_init(finished, 1);
         fence_mbar_init();
         sh.abort = 0;
     }
@@ -310,6 +323,7 @@ __global__ void __launch_bounds__(few_threads(NC), NC < 64 ? 2 : 1)
     if (warp == kTensor) tile::tmem_alloc(smem_u32(&sh.tmem), kAlloc);
     grid_launch_dependents();
     grid_dependency_wait();
+#pragma unroll 1
     for (int b = tid; b < p.B; b += kThreads) {
         const Sequence s(p, b);
         sh.seqs[b] = make_int4(s.row, s.n, s.keys, 0);
@@ -320,6 +334,7 @@ __global__ void __launch_bounds__(few_threads(NC), NC < 64 ? 2 : 1)
     tmem_fence_after();
     if (warp == 0) {
         int sum = 0;
+#pragma unroll 1
         for (int b0 = 0; b0 < p.B; b0 += 32) {
             int v = b0 + lane < p.B ? first[b0 + lane + 1] : 0;
 #pragma unroll
@@ -334,116 +349,157 @@ __global__ void __launch_bounds__(few_threads(NC), NC < 64 ? 2 : 1)
     }
     __syncthreads();
     if (blockIdx.x == 0 && p.units > 1)
+#pragma unroll 1
         for (int b = tid; b <= p.B; b += kThreads) p.prefix[b] = first[b];
-    const uint32_t tm = sh.tmem, S = tm, O = tm + 2 * NC;
+    const uint32_t tm = sh.tmem, S = tm, O = tm + 2 * kScores;
     const Sequences all{first, sh.seqs};
     const int items = first[p.B];
     const Waits wait{&sh.abort, p.err};
 
     if (warp == kProducer) {
         // ------------------------------------------------------------- producer
+        // A leaf's keys, then the values of the leaf before, as the products need them.
         const int per_tile = 128 / p.box, boxes = 2 * per_tile;  // a lane has a box of the leaf's keys
         Place at;
         int n = 0, issued = 0;
         bool ok = true;
+        const auto slot = [&]() {
+            if (issued >= p.slots) ok = wait(empty0 + 8 * at.slot, at.lap ^ 1);
+            ok = __all_sync(0xffffffffu, ok);
+            if (ok && lane == 0) mbar_arrive_expect_tx(full0 + 8 * at.slot, kChunk);
+            __syncwarp();
+            return ok;
+        };
+        struct Boxes {
+            int page, place, g;
+        };
+        const auto bring_keys = [&](const Boxes &x) {
+#pragma unroll 1
+            for (int i = 0; i < kChunks && slot(); ++i, ++issued, at.step(p.slots)) {
+                // 128 keys, 64 elements
+                const int box = lane - i / DB * per_tile;
+                if (box >= 0 && box < per_tile)
+                    tma_load_4d(base + at.slot * kChunk + box * p.box * 128, &kmap, 64 * (i % DB), x.place, x.g, x.page, full0 + 8 * at.slot);
+            }
+        };
+        const auto bring_values = [&](const Boxes &x) {
+#pragma unroll 1
+            for (int i = 0; i < kChunks && slot(); ++i, ++issued, at.step(p.slots)) {
+                // 64 keys, twice 64 elements (128 keys, 64 elements of head_dim 64)
+                const int few = D == 64 ? per_tile : per_tile / 2, box = lane - i / HALVES * few;
+                if (box >= 0 && box < few)
+                    for (int d = 0; d < (D == 64 ? 1 : 2); ++d)
+                        tma_load_4d(base + at.slot * kChunk + d * 8192 + box * p.box * 128, &vmap, 128 * (i % HALVES) + 64 * d, x.place, x.g, x.page,
+                                    full0 + 8 * at.slot);
+            }
+        };
+        Boxes before{-1, 0, 0};
+        bool any = false;
+#pragma unroll 1
         for (int index = blockIdx.x; index < items && ok; index += gridDim.x) {
             const Item it = item_at(p, all, index);
             if (it.leaves == 0) continue;  // (no queries are brought for an item without keys)
             const Seen seen(p, it.pos, it.pos + it.tokens - 1);
             const int32_t *table = p.table + int64_t(it.b) * p.max_pages;
-            ok = __all_sync(0xffffffffu, n == 0 || wait(q_empty, (n - 1) & 1));
+            const uint32_t set = 8 * (n & 1);
+            ok = __all_sync(0xffffffffu, n < 2 || wait(q_empty + set, (n / 2 - 1) & 1));
             if (!ok) break;
             if (lane == 0) {
-                mbar_arrive_expect_tx(q_full, uint32_t(p.rows) * D * 2);
-                for (int c = 0; c < DB; ++c) tile::tma_load_3d(Q + c * NC * 128, &qmap, 64 * c, it.g * p.group, it.row, q_full);
+                mbar_arrive_expect_tx(q_full + set, uint32_t(p.rows) * D * 2);
+                for (int c = 0; c < DB; ++c)
+                    tile::tma_load_3d(Q + ((n & 1) * DB + c) * NC * 128, &qmap, 64 * c, it.g * p.group, it.row, q_full + set);
             }
             ++n;
+#pragma unroll 1
             for (int leaf = it.leaf; leaf < it.leaf + it.leaves && ok; ++leaf) {
                 const int key = leaf * kLeaf + lane * p.box;
-                int page = -1, place = 0;
+                Boxes x{-1, 0, it.g};
                 if (lane < boxes && seen.any(key, p.box)) {
-                    page = __ldg(table + key / p.page_size);
-                    place = key % p.page_size;
+                    x.page = page_of(p, key);
+                    x.place = key - x.page * p.page_size;
+                    x.page = __ldg(table + x.page);
                 }
-                if (unsigned(page) >= unsigned(p.pages)) page = p.pages;  // outside the map: zeros
-#pragma unroll 1
-                for (int i = 0; i < 2 * kChunks; ++i, ++issued, at.step(p.slots)) {
-                    if (issued >= p.slots) ok = wait(empty0 + 8 * at.slot, at.lap ^ 1);
-                    ok = __all_sync(0xffffffffu, ok);
-                    if (!ok) break;
-                    const uint32_t dst = base + at.slot * kChunk, bar = full0 + 8 * at.slot;
-                    if (lane == 0) mbar_arrive_expect_tx(bar, kChunk);
-                    __syncwarp();
-                    const bool values = i >= kChunks;
-                    const int j = values ? i - kChunks : i;
-                    if (!values || D == 64) {
-                        // 128 keys, 64 elements
-                        const int box = lane - j / DB * per_tile;
-                        if (box >= 0 && box < per_tile)
-                            tma_load_4d(dst + box * p.box * 128, values ? &vmap : &kmap, 64 * (j % DB), place, it.g, page, bar);
-                    } else {
-                        // 64 keys, twice 64 elements
-                        const int box = lane - j / HALVES * per_tile / 2;
-                        if (box >= 0 && box < per_tile / 2)
-                            for (int d = 0; d < 2; ++d)
-                                tma_load_4d(dst + d * 8192 + box * p.box * 128, &vmap, 128 * (j % HALVES) + 64 * d, place, it.g, page, bar);
-                    }
-                }
+                if (unsigned(x.page) >= unsigned(p.pages)) x.page = p.pages;  // outside the map: zeros
+                bring_keys(x);
+                if (any && ok) bring_values(before);
+                any = true;
+                before = x;
             }
         }
+        if (any && ok) bring_values(before);
         if (!ok) {
             // copies in flight have to land before the block ends
+#pragma unroll 1
             for (int i = max(issued - p.slots, 0); i < issued; ++i) mbar_wait_bounded(full0 + 8 * (i % p.slots), (i / p.slots) & 1);
-            if (n > 0) mbar_wait_bounded(q_full, (n - 1) & 1);
+#pragma unroll 1
+            for (int i = max(n - 2, 0); i < n; ++i) mbar_wait_bounded(q_full + 8 * (i & 1), (i / 2) & 1);
         }
     } else if (warp == kTensor) {
         // ---------------------------------------------------------- tensor warp
-        if (lane == 0) {
-            constexpr uint32_t kScores = mma_kind(NC, false, false), kValues = mma_kind(2 * NC, true, true);
-            // (head_dim 64: the tile's second 64 rows repeat the first, and are not read)
-            const uint64_t keys0 = descriptor(base, 16, 1024, 2), queries = descriptor(Q, 16, 1024, 2);
-            const uint64_t values0 = descriptor(base, D == 64 ? 0 : 8192, 1024, 2);
-            const uint64_t weights = NC == 16 ? descriptor(P, 16, 512, 4) : descriptor(P, kLeaf * 128, 1024, 2);
-            Place at;
-            int n = 0, leaf = 0;
-            for (int index = blockIdx.x; index < items; index += gridDim.x) {
-                const Item it = item_at(p, all, index);
-                if (it.leaves == 0) continue;
-                wait(q_full, n & 1);
-                for (int l = 0; l < it.leaves; ++l, ++leaf) {
+        // The scores of a leaf, then the sums of the leaf before, whose weights were
+        // formed meanwhile.
+        constexpr uint32_t kScoreKind = mma_kind(NC, false, false), kValueKind = mma_kind(2 * NC, true, true);
+        // (head_dim 64: the tile's second 64 rows repeat the first, and are not read)
+        const uint64_t keys0 = descriptor(base, 16, 1024, 2), queries = descriptor(Q, 16, 1024, 2);
+        const uint64_t values0 = descriptor(base, D == 64 ? 0 : 8192, 1024, 2);
+        const uint64_t weights = NC == 16 ? descriptor(P, 16, 512, 4) : descriptor(P, kLeaf * 128, 1024, 2);
+        Place at;
+        int n = 0, leaf = 0;
+        bool fresh = false;  // the leaf before is an item's first
+        const auto sums = [&](int leaf, bool fresh) {
 #pragma unroll 1
-                    for (int i = 0; i < kChunks; ++i, at.step(p.slots)) {
-                        wait(full0 + 8 * at.slot, at.lap);
-                        const int c = i % DB;
-                        const uint64_t a = keys0 + uint32_t(at.slot * (kChunk >> 4)), b = queries + uint32_t(c * NC * (128 >> 4));
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) mma_ss<kScores>(S + i / DB * NC, a + 2 * k, b + 2 * k, c + k > 0);
-                        tmem_commit(empty0 + 8 * at.slot);
-                    }
-                    tmem_commit(s_ready);
-                    if (l == it.leaves - 1) tmem_commit(q_empty);
-#pragma unroll 1
-                    for (int i = 0; i < kChunks; ++i, at.step(p.slots)) {
-                        if (i % DB == 0) {
-                            wait(p_ready + 8 * (i / DB), leaf & 1);
-                            tmem_fence_after();
-                        }
-                        wait(full0 + 8 * at.slot, at.lap);
-                        constexpr int kKeys = D == 64 ? 128 : 64;
-                        const int c = i % HALVES, key = i / HALVES * kKeys;
-                        const uint64_t a = values0 + uint32_t(at.slot * (kChunk >> 4)), b = weights + uint32_t(key * (kKeyBytes >> 4));
-#pragma unroll
-                        for (int k = 0; k < kKeys / 16; ++k)
-                            mma_ss<kValues>(O + c * 2 * NC, a + k * (2048 >> 4), b + k * (16 * kKeyBytes >> 4), l > 0 || key + k > 0);
-                        tmem_commit(empty0 + 8 * at.slot);
-                    }
-                    tmem_commit(o_done);
+            for (int i = 0; i < kChunks; ++i, at.step(p.slots)) {
+                if (i % DB == 0) {
+                    wait(p_ready + 8 * (i / DB), leaf & 1);
+                    tmem_fence_after();
                 }
-                ++n;
+                wait(full0 + 8 * at.slot, at.lap);
+                constexpr int kKeys = D == 64 ? 128 : 64;
+                const int c = i % HALVES, key = i / HALVES * kKeys;
+                const uint64_t a = values0 + uint32_t(at.slot * (kChunk >> 4)), b = weights + uint32_t(key * (kKeyBytes >> 4));
+                if (lane == 0) {
+#pragma unroll
+                    for (int k = 0; k < kKeys / 16; ++k)
+                        mma_ss<kValueKind>(O + c * 2 * NC, a + k * (2048 >> 4), b + k * (16 * kKeyBytes >> 4), !fresh || key + k > 0);
+                    tmem_commit(empty0 + 8 * at.slot);
+                    if (i == kChunks - 1) tmem_commit(o_done);
+                }
+                __syncwarp();
             }
-            tmem_commit(finished);
-            mbar_wait_bounded(finished, 0);
+        };
+#pragma unroll 1
+        for (int index = blockIdx.x; index < items; index += gridDim.x) {
+            const Item it = item_at(p, all, index);
+            if (it.leaves == 0) continue;
+            const int set = n & 1;
+            wait(q_full + 8 * set, (n / 2) & 1);
+#pragma unroll 1
+            for (int l = 0; l < it.leaves; ++l, ++leaf) {
+#pragma unroll 1
+                for (int i = 0; i < kChunks; ++i, at.step(p.slots)) {
+                    wait(full0 + 8 * at.slot, at.lap);
+                    const int c = i % DB;
+                    const uint32_t d = S + (leaf & 1) * kScores + i / DB * NC;
+                    const uint64_t a = keys0 + uint32_t(at.slot * (kChunk >> 4)), b = queries + uint32_t((set * DB + c) * NC * (128 >> 4));
+                    if (lane == 0) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) mma_ss<kScoreKind>(d, a + 2 * k, b + 2 * k, c + k > 0);
+                        tmem_commit(empty0 + 8 * at.slot);
+                        if (i == kChunks - 1) {
+                            tmem_commit(s_ready + 8 * (leaf & 1));
+                            if (l == it.leaves - 1) tmem_commit(q_empty + 8 * set);
+                        }
+                    }
+                    __syncwarp();
+                }
+                if (leaf > 0) sums(leaf - 1, fresh);
+                fresh = l == 0;
+            }
+            ++n;
         }
+        if (leaf > 0) sums(leaf - 1, fresh);
+        if (lane == 0) tmem_commit(finished);
+        mbar_wait_bounded(finished, 0);
     } else {
         // ---------------------------------------------------------------- weights
         // Four warps have 16 columns. A thread has the key `mine` of each of the leaf's
@@ -465,6 +521,7 @@ __global__ void __launch_bounds__(few_threads(NC), NC < 64 ? 2 : 1)
                 sh.ref[r] = -INFINITY;
                 sh.last[r] = r < it.rows ? pos : -1;
                 sh.low[r] = p.window ? pos - p.window + 1 : 0;
+                sh.out[r] = it.whole ? (it.row + r / p.group) * p.ld_out + (it.g * p.group + r % p.group) * D : (int64_t(it.index) * p.rows + r) * D;
             }
             float sum[16];
 #pragma unroll
@@ -475,8 +532,9 @@ __global__ void __launch_bounds__(few_threads(NC), NC < 64 ? 2 : 1)
                 const int key0 = (it.leaf + l) * kLeaf + mine;
                 int page[2];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) page[h] = seen(key0 + 128 * h) ? __ldg(table + (key0 + 128 * h) / p.page_size) : -1;
-                wait(s_ready, leaf & 1);
+                for (int h = 0; h < 2; ++h) page[h] = seen(key0 + 128 * h) ? __ldg(table + page_of(p, key0 + 128 * h)) : -1;
+                const uint32_t scores = S + (leaf & 1) * kScores + lanes + c0;
+                wait(s_ready + 8 * (leaf & 1), (leaf / 2) & 1);
                 tmem_fence_after();
                 uint32_t see[2] = {0xffffu, 0xffffu};  // which columns see the key
                 const bool there0 = unsigned(page[0]) < unsigned(p.pages), there1 = unsigned(page[1]) < unsigned(p.pages);
@@ -492,8 +550,8 @@ __global__ void __launch_bounds__(few_threads(NC), NC < 64 ? 2 : 1)
                     }
                 }
                 float s0[16], s1[16], top[16];
-                tmem_ld<16>(S + lanes + c0, s0);
-                tmem_ld<16>(S + lanes + NC + c0, s1);
+                tmem_ld<16>(scores, s0);
+                tmem_ld<16>(scores + NC, s1);
                 tmem_wait_ld();
                 settle(s0);
                 settle(s1);
@@ -570,21 +628,28 @@ __global__ void __launch_bounds__(few_threads(NC), NC < 64 ? 2 : 1)
                                    make_uint4(lo[4 * i], lo[4 * i + 1], lo[4 * i + 2], lo[4 * i + 3]));
                     }
                     // Values of keys that no column sees may be anything, and 0 x NaN is NaN: zeros
-                    // in their place. (A tile's values all fit in the ring, and nothing but the
-                    // products of the tile before has to be done for them to land.)
+                    // in their place, once the tile's values have landed. A wait for a slot's lap is
+                    // right only when the lap before has landed and while the lap itself is
+                    // not consumed: what is before the first tile's values in the ring has
+                    // landed with the scores of the leaf behind, what is before the second's
+                    // with the first's. (A tile's values fit in the ring at once, and nothing
+                    // else has to be done for them to land but the products of the tile before.)
                     const bool there = h ? there1 : there0;
-                    if (group == 0 && !__all_sync(0xffffffffu, there)) {
-                        const int from = leaf * 2 * kChunks + kChunks;
+                    if (group == 0 && !__all_sync(0xffffffffu, there0 && there1)) {
+                        bool more = l + 1 < it.leaves;
+#pragma unroll 1
+                        for (int j = index + gridDim.x; !more && j < items; j += gridDim.x) more = item_at(p, all, j).leaves > 0;
+                        if (more) wait(s_ready + 8 * ((leaf + 1) & 1), ((leaf + 1) / 2) & 1);
+                        const int from = (2 * leaf + 1 + more) * kChunks + h * DB;
 #pragma unroll 1
                         for (int c = 0; c < DB; ++c) {
-                            // 64 elements of the key: which chunk, where
-                            const int chunk = from + (D == 64 ? h : (h * 2 + mine / 64) * HALVES + c / 2);
-                            const int slot = chunk % p.slots;
-                            wait(full0 + 8 * slot, (chunk / p.slots) & 1);
-                            if (!there) {
-                                const uint32_t at = base + slot * kChunk + (D == 64 ? mine * 128 : (c & 1) * 8192 + (mine & 63) * 128);
-                                for (int i = 0; i < 8; ++i) sts_v4_u32(at + 16 * i, make_uint4(0, 0, 0, 0));
-                            }
+                            const int slot = (from + c) % p.slots;
+                            wait(full0 + 8 * slot, ((from + c) / p.slots) & 1);
+                            // does the chunk hold 64 elements (of head_dim 64) or 128 of the thread's key?
+                            if (there || (D > 64 && c / HALVES != mine / 64)) continue;
+                            const uint32_t at = base + slot * kChunk + (D == 64 ? mine : mine & 63) * 128;
+#pragma unroll 1
+                            for (int i = 0; i < (D == 64 ? 8 : 16); ++i) sts_v4_u32(at + (i & 7) * 16 + (i >> 3) * 8192, make_uint4(0, 0, 0, 0));
                         }
                     }
                     tmem_fence_before();
@@ -623,18 +688,16 @@ __global__ void __launch_bounds__(few_threads(NC), NC < 64 ? 2 : 1)
                 settle(a);
                 settle(b);
                 if (d >= D) continue;
-                float *parts = p.parts + (int64_t(it.index) * p.rows + c0) * D + d;
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     const int r = c0 + i;
                     if (r >= it.rows) break;
                     const float o = it.leaves > 0 ? __fadd_rn(a[i], b[i]) : 0.0f;
                     if (it.whole) {
-                        const int row = it.row + r / p.group, head = it.g * p.group + r % p.group;
                         const float f = sh.total[r];
-                        reinterpret_cast<__nv_bfloat16 *>(p.out)[row * p.ld_out + head * D + d] = __float2bfloat16_rn(f == 0.0f ? 0.0f : __fmul_rn(o, f));
+                        reinterpret_cast<__nv_bfloat16 *>(p.out)[sh.out[r] + d] = __float2bfloat16_rn(f == 0.0f ? 0.0f : __fmul_rn(o, f));
                     } else {
-                        parts[i * D] = o;
+                        p.parts[sh.out[r] + d] = o;
                     }
                 }
             }
@@ -861,6 +924,7 @@ extern "C" qmv_status qmv_attend_run(const uint16_t *q, const uint16_t *k_cache,
     p.meta = reinterpret_cast<float2 *>(at + f.meta_off);
     p.parts = reinterpret_cast<float *>(at + f.parts_off);
     // keys and values by boxes of 64 elements and as many keys of one page as its size allows
+    p.page_magic = ((uint64_t(1) << 42) + page_size - 1) / page_size;
     p.box = 64;
     while (page_size % p.box) p.box /= 2;
     Maps m;

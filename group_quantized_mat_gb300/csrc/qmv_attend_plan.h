@@ -32,12 +32,12 @@ struct FewPlan {
 
 inline size_t up256(size_t b) { return (b + 255) & ~size_t(255); }
 
-// Fixed shared memory behind the ring: weights of a leaf (two bf16 terms), queries,
+// Fixed shared memory behind the ring: weights of a leaf (two bf16 terms), two items' queries,
 // then barriers, maxima, sums and the sequences.
 inline void few_smem(FewPlan &f, int D, int B)
 {
-    const int p_bytes = kLeaf * f.columns * 4, q_bytes = f.columns * D * 2;
-    const int misc = 512 + f.columns * 4 * 16 + B * 16 + (B + 1) * 4;
+    const int p_bytes = kLeaf * f.columns * 4, q_bytes = 2 * f.columns * D * 2;
+    const int misc = 512 + f.columns * 4 * 18 + B * 16 + (B + 1) * 4;
     const int fixed = p_bytes + q_bytes + ((misc + 1023) & ~1023);
     const int two = (kSmemSm / 2 - kSmemReserved - 1024 - fixed) / kChunk;
     // (a tile's values, at most four slots, have to be there at once: see the zeroing of unseen rows)
