@@ -1,8 +1,9 @@
 // qmv_attend_run: attention of new tokens over a paged cache.
 //
-// The simplest kernel that is right: a warp for each query head of each new token,
-// over the keys that it sees one after the other, with the running maximum and sum
-// of a softmax. Every key is read once for each query head.
+// Two kinds of sequences: those of a few new tokens, whose keys and values are read
+// once for all of them (attend_few, attend_join), and prompts, which are bound by their
+// products (attend_prompt, attend_join_pieces). A call that may hold both launches both; each
+// takes its own.
 #include <cuda.h>
 #include <cuda_bf16.h>
 
@@ -42,8 +43,8 @@ struct AttendParams {
     int window, sinks;
     int64_t ld_q, ld_out, page_stride, token_stride, head_stride;
     unsigned *err;
-    // few tokens: the plan, and the workspace's parts
-    int tokens, rows, units, slots;
+    // the plan, and the workspace's parts
+    int tokens, rows, units, pieces, slots;
     int p_off, q_off, misc_off;
     int32_t *prefix;
     float2 *meta;
@@ -222,6 +223,24 @@ struct Sequences {
     const int4 *kept;      // [B]
 };
 
+// Counts first[1 .. B] become running sums from first[0] = 0 on; by one warp.
+__device__ __forceinline__ void sum_firsts(int32_t *first, int B, int lane)
+{
+    int sum = 0;
+#pragma unroll 1
+    for (int b0 = 0; b0 < B; b0 += 32) {
+        int v = b0 + lane < B ? first[b0 + lane + 1] : 0;
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+            const int u = __shfl_up_sync(0xffffffffu, v, d);
+            if (lane >= d) v += u;
+        }
+        if (b0 + lane < B) first[b0 + lane + 1] = sum + v;
+        sum += __shfl_sync(0xffffffffu, v, 31);
+    }
+    if (lane == 0) first[0] = 0;
+}
+
 __device__ __noinline__ Item item_at(const AttendParams &p, const Sequences &all, int index)
 {
     int lo = 0, hi = p.B;
@@ -332,21 +351,7 @@ __global__ void __launch_bounds__(few_threads(NC), NC < 64 ? 2 : 1)
     tmem_fence_before();
     __syncthreads();
     tmem_fence_after();
-    if (warp == 0) {
-        int sum = 0;
-#pragma unroll 1
-        for (int b0 = 0; b0 < p.B; b0 += 32) {
-            int v = b0 + lane < p.B ? first[b0 + lane + 1] : 0;
-#pragma unroll
-            for (int d = 1; d < 32; d *= 2) {
-                const int u = __shfl_up_sync(0xffffffffu, v, d);
-                if (lane >= d) v += u;
-            }
-            if (b0 + lane < p.B) first[b0 + lane + 1] = sum + v;
-            sum += __shfl_sync(0xffffffffu, v, 31);
-        }
-        if (lane == 0) first[0] = 0;
-    }
+    if (warp == 0) sum_firsts(first, p.B, lane);
     __syncthreads();
     if (blockIdx.x == 0 && p.units > 1)
 #pragma unroll 1
@@ -772,44 +777,573 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attend_join(const AttendParam
         p.lse[row * p.heads + h] = none ? -INFINITY : __fmul_rn(0.6931471805599453f, __fadd_rn(top, log2f(total)));
 }
 
-template <int D>
-__global__ void __launch_bounds__(128) attend_simple(const AttendParams p)
+// ----------------------------------------------------------------- prompts --
+//
+// Sequences of more new tokens than that. Query rows (tokens x heads of one kv head) are rows,
+// 128 to a tile, a thread each:
+//
+//   S (rows x keys)      = Q K^T      from shared memory
+//   P = exp2(S |scale| log2(e) - m)   in registers, then bf16 in tensor memory in S's place
+//   O (rows x head_dim) += P V        V from shared memory as it lies in the cache
+//
+// Two tiles of rows take turns (of head_dim 256, whose sums fill half of tensor
+// memory, two tiles of keys): the tensor cores work on one while the weights of the
+// other are formed. What bounds it is the products, 4 x head_dim operations for each
+// pair of row and key; a tile's exponentials take half as long.
+// m is a whole number again and moves only when a score passes it by 8, so that
+// sums are rarely scaled, and exactly. The weights are rounded to bf16 (2^-8 of each,
+// as an operand next to bf16 values has to be); their total is not.
+//
+// Items go from a sequence's last rows, which see the most keys, to its first. Where there are
+// too few of them the keys are divided into pieces, which attend_join_pieces joins in
+// order; the pieces depend on the call's sizes, and a row's last bits with them.
+
+struct PromptItem {
+    int b, g, index;
+    int row, tok, tokens;  // first row of q, first token of the sequence, tokens
+    int pos;               // of the first token
+    int keys;
+    int sinks, low;        // tiles of the first tokens; first tile of the others
+    int from, to;          // of the list of tiles
+    int pieces;
+    __device__ __forceinline__ int tile(int i) const { return i < sinks ? i : low + i - sinks; }
+};
+
+// Tiles of keys that the rows of tokens [tok, tok + tokens) see.
+struct Tiles {
+    int sinks, low, count;
+    __device__ __forceinline__ Tiles(const AttendParams &p, int first, int last)
+    {
+        const Seen seen(p, first, last);
+        low = seen.low / 128;
+        sinks = min((seen.sinks + 127) / 128, low);
+        count = seen.end > 0 ? sinks + (seen.end - 1) / 128 - low + 1 : 0;
+    }
+};
+
+// Parts of a sequence's items: of eight tiles at least, by its last rows.
+__device__ __forceinline__ int pieces_of(const AttendParams &p, const Sequence &s, int each)
 {
-    constexpr int E = D / 32;
+    const int last = (s.done - 1) / each * each;
+    return max(1, min(p.pieces, Tiles(p, s.pos + last, s.pos + s.done - 1).count / 8));
+}
+
+template <int STREAMS>
+__device__ __noinline__ PromptItem prompt_at(const AttendParams &p, const Sequences &all, int index)
+{
+    int lo = 0, hi = p.B;
+#pragma unroll 1
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        (all.first[mid] <= index ? lo : hi) = mid;
+    }
+    const Sequence s(p, all.kept[lo]);
+    const int each = STREAMS * p.tokens;
+    PromptItem it;
+    it.b = lo;
+    it.index = index;
+    it.pieces = pieces_of(p, s, each);
+    index -= all.first[lo];
+    const int piece = index % it.pieces;
+    index /= it.pieces;
+    it.g = index % p.kv_heads;
+    it.tok = ((s.done - 1) / each - index / p.kv_heads) * each;
+    it.tokens = min(each, s.done - it.tok);
+    it.row = s.row + it.tok;
+    it.pos = s.pos + it.tok;
+    it.keys = s.keys;
+    const Tiles tiles(p, it.pos, it.pos + it.tokens - 1);
+    it.sinks = tiles.sinks;
+    it.low = tiles.low;
+    it.from = int(int64_t(tiles.count) * piece / it.pieces);
+    it.to = int(int64_t(tiles.count) * (piece + 1) / it.pieces);
+    return it;
+}
+
+// The keys that a stream's rows see.
+template <int STREAMS>
+__device__ __forceinline__ Seen stream_sees(const AttendParams &p, const PromptItem &it, int x, int &tokens)
+{
+    tokens = STREAMS == 1 ? it.tokens : max(min(it.tokens - x * p.tokens, p.tokens), 0);
+    const int first = it.pos + x * p.tokens;
+    Seen seen(p, first, first + tokens - 1);
+    if (tokens == 0) seen.end = 0;
+    return seen;
+}
+
+struct PromptShared {
+    uint64_t full[8], empty[8], q_full, q_empty, edge, s_ready[2], p_ready[2], o_done[2], finished;
+    int abort;
+    uint32_t tmem;
+    int4 seqs[1];  // [B], then the sequences' first items [B + 1]
+};
+
+__host__ __device__ constexpr int prompt_threads(int D) { return (D == 256 ? 128 : 256) + 64; }
+
+// D (128 x N fp32) (+)= A (128 x 16, tensor memory) B^T (N x 16, shared memory).
+template <uint32_t KIND>
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, bool add)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(KIND), "r"(uint32_t(add))
+        : "memory");
+}
+
+template <int D>
+__global__ void __launch_bounds__(prompt_threads(D), 1)
+    attend_prompt(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const AttendParams p)
+{
+    constexpr int STREAMS = D == 256 ? 1 : 2, W = D < 128 ? D : 128;  // elements of a chunk
+    constexpr int DB = D / 64, WB = W / 64, CH = D / W, kBytes = 128 * W * 2;
+    constexpr int kThreads = prompt_threads(D), kProducer = kThreads / 32 - 2, kTensor = kProducer + 1;
+    extern __shared__ uint8_t raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+    PromptShared &sh = *reinterpret_cast<PromptShared *>(smem + p.misc_off);
+    int32_t *first = reinterpret_cast<int32_t *>(sh.seqs + p.B);
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid & 31;
+    const uint32_t base = smem_u32(smem), full0 = smem_u32(sh.full), empty0 = smem_u32(sh.empty), Q = base + p.q_off;
+    const uint32_t q_full = smem_u32(&sh.q_full), q_empty = smem_u32(&sh.q_empty), edge = smem_u32(&sh.edge), finished = smem_u32(&sh.finished);
+    const uint32_t s_ready = smem_u32(sh.s_ready), p_ready = smem_u32(sh.p_ready), o_done = smem_u32(sh.o_done);
+    if (tid == 0) {
+#pragma unroll 1
+        for (int i = 0; i < p.slots; ++i) {
+            mbar_init(full0 + 8 * i, 1);
+            mbar_init(empty0 + 8 * i, 1);
+        }
+        mbar_init(q_full, 1);
+        mbar_init(q_empty, 1);
+        mbar_init(edge, 1);
+        mbar_init(finished, 1);
+        for (int x = 0; x < 2; ++x) {
+            mbar_init(s_ready + 8 * x, 1);
+            mbar_init(p_ready + 8 * x, 4);
+            mbar_init(o_done + 8 * x, 1);
+        }
+        fence_mbar_init();
+        sh.abort = 0;
+    }
+    grid_launch_dependents();
     grid_dependency_wait();
-    const int64_t unit = int64_t(blockIdx.x) * 4 + threadIdx.x / 32;
-    const int lane = threadIdx.x & 31, t = int(unit / p.heads), h = int(unit % p.heads);
+    if (warp == kTensor) tile::tmem_alloc(smem_u32(&sh.tmem), 512);
+#pragma unroll 1
+    for (int b = tid; b < p.B; b += kThreads) {
+        const Sequence s(p, b);
+        sh.seqs[b] = make_int4(s.row, s.n, s.keys, 0);
+        const int each = STREAMS * p.tokens;
+        first[b + 1] = s.done > kFew ? (s.done + each - 1) / each * p.kv_heads * pieces_of(p, s, each) : 0;
+    }
+    tmem_fence_before();
+    __syncthreads();
+    tmem_fence_after();
+    if (warp == 0) sum_firsts(first, p.B, lane);
+    __syncthreads();
+    if (blockIdx.x == 0 && p.pieces > 1)
+#pragma unroll 1
+        for (int b = tid; b <= p.B; b += kThreads) p.prefix[b] = first[b];
+    const uint32_t tm = sh.tmem, S = tm, O = tm + 256;
+    const Sequences all{first, sh.seqs};
+    const int items = first[p.B];
+    const Waits wait{&sh.abort, p.err};
+
+    if (warp == kProducer) {
+        // ------------------------------------------------------------- producer
+        // The first tile's keys; then each tile's values, before them (head_dim 256) or
+        // after them the next tile's keys, as the products need them.
+        const int per_tile = 128 / p.box, box = lane % per_tile, block = lane / per_tile;
+        Place at;
+        int n = 0, issued = 0, edges = 0;
+        bool ok = true;
+        // a chunk: 128 keys, W elements from c W on; `rows` of them are kept (values behind a
+        // sequence's keys may be anything, and 0 x NaN is NaN: zeros in their place)
+        const auto bring = [&](const CUtensorMap *map, const PromptItem &it, int page, int place, int c, int rows) {
+            if (issued >= p.slots) ok = wait(empty0 + 8 * at.slot, at.lap ^ 1);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) return;
+            const uint32_t full = full0 + 8 * at.slot, bar = rows < 128 ? edge : full, dst = base + at.slot * kBytes;
+            if (lane == 0) mbar_arrive_expect_tx(bar, kBytes);
+            __syncwarp();
+            if (block < WB) tma_load_4d(dst + block * 16384 + box * p.box * 128, map, c * W + 64 * block, place, it.g, page, bar);
+            if (rows < 128) {
+                ok = __all_sync(0xffffffffu, wait(edge, edges & 1));
+                ++edges;
+#pragma unroll 1
+                for (int i = rows * 8 + lane; i < 128 * 8; i += 32)
+                    for (int d = 0; d < WB; ++d) sts_v4_u32(dst + d * 16384 + i * 16, make_uint4(0, 0, 0, 0));
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(full);
+            }
+            ++issued;
+            at.step(p.slots);
+        };
+#pragma unroll 1
+        for (int index = blockIdx.x; index < items && ok; index += gridDim.x) {
+            const PromptItem it = prompt_at<STREAMS>(p, all, index);
+            if (it.from == it.to) continue;
+            const Seen seen(p, it.pos, it.pos + it.tokens - 1);
+            const int32_t *table = p.table + int64_t(it.b) * p.max_pages;
+            ok = __all_sync(0xffffffffu, n == 0 || wait(q_empty, (n - 1) & 1));
+            if (!ok) break;
+            if (lane == 0) {
+                const int sets = STREAMS == 2 && it.tokens > p.tokens ? 2 : 1;
+                mbar_arrive_expect_tx(q_full, uint32_t(sets * p.tokens * p.group) * D * 2);
+                for (int i = 0; i < sets * DB; ++i)
+                    tile::tma_load_3d(Q + i * 16384, &qmap, i % DB * 64, it.g * p.group, it.row + i / DB * p.tokens, q_full);
+            }
+            ++n;
+            int page = p.pages, place = 0, before = 0, before_place = 0, before_rows = 0;
+#pragma unroll 1
+            for (int i = it.from; i <= it.to && ok; ++i) {
+                int rows = 0;
+                if (i < it.to) {
+                    const int key = it.tile(i) * 128 + box * p.box;
+                    rows = min(it.keys - it.tile(i) * 128, 128);
+                    page = -1;
+                    place = 0;
+                    if (block < WB && seen.any(key, p.box)) {
+                        page = page_of(p, key);
+                        place = key - page * p.page_size;
+                        page = __ldg(table + page);
+                    }
+                    if (unsigned(page) >= unsigned(p.pages)) page = p.pages;  // outside the map: zeros
+                }
+                // (of one stream a tile's scores come before the sums of the tile before; of
+                // two the first stream's sums come before the second tile's first scores)
+#pragma unroll 1
+                for (int half = 0; half < 2; ++half) {
+                    const bool keys = (half == 0) == (STREAMS == 1);
+                    if (keys ? i == it.to : i == it.from) continue;
+#pragma unroll 1
+                    for (int c = 0; c < CH && ok; ++c) {
+                        if (keys)
+                            bring(&kmap, it, page, place, c, 128);
+                        else
+                            bring(&vmap, it, before, before_place, c, before_rows);
+                    }
+                }
+                before = page;
+                before_place = place;
+                before_rows = rows;
+            }
+        }
+        if (!ok) {
+            // copies in flight have to land before the block ends (those of an edge have been waited for)
+#pragma unroll 1
+            for (int i = max(issued - p.slots, 0); i < issued; ++i) mbar_wait_bounded(full0 + 8 * (i % p.slots), (i / p.slots) & 1);
+            if (n > 0) mbar_wait_bounded(q_full, (n - 1) & 1);
+        }
+    } else if (warp == kTensor) {
+        // ---------------------------------------------------------- tensor warp
+        constexpr uint32_t kScoreKind = mma_kind(128, false, false), kValueKind = mma_kind(W, false, true);
+        const uint64_t keys0 = descriptor(base, 16, 1024, 2), queries = descriptor(Q, 16, 1024, 2);
+        const uint64_t values0 = descriptor(base, 16384, 1024, 2);
+        Place at;
+        int n = 0, done[2] = {0, 0};  // tiles of a stream (of a buffer of scores) so far
+        // scores of a tile whose keys are in the chunk at `c`, from element 64 b WB on
+        const auto scores = [&](int buffer, int x, const Place &c, int b) {
+            if (lane == 0) {
+                const uint64_t k0 = keys0 + uint32_t(c.slot * (kBytes >> 4)), q0 = queries + uint32_t((x * DB + b * WB) * (16384 >> 4));
+#pragma unroll
+                for (int k = 0; k < W / 16; ++k)
+                    mma_ss<kScoreKind>(S + buffer * 128, q0 + (k / 4) * (16384 >> 4) + 2 * (k & 3), k0 + (k / 4) * (16384 >> 4) + 2 * (k & 3), b + k > 0);
+            }
+            __syncwarp();
+        };
+        const auto sums = [&](int buffer, int o, const Place &c, bool add) {
+            if (lane == 0) {
+                const uint64_t v0 = values0 + uint32_t(c.slot * (kBytes >> 4));
+#pragma unroll
+                for (int k = 0; k < 8; ++k) mma_ts<kValueKind>(O + o, S + buffer * 128 + 8 * k, v0 + k * (2048 >> 4), add || k > 0);
+            }
+            __syncwarp();
+        };
+        const auto commit = [&](uint32_t bar) {
+            if (lane == 0) tmem_commit(bar);
+            __syncwarp();
+        };
+#pragma unroll 1
+        for (int index = blockIdx.x; index < items; index += gridDim.x) {
+            const PromptItem it = prompt_at<STREAMS>(p, all, index);
+            if (it.from == it.to) continue;
+            wait(q_full, n & 1);
+            ++n;
+            if (STREAMS == 1) {
+                // S(0), S(1), O(0), S(2), O(1), ..
+#pragma unroll 1
+                for (int i = it.from; i <= it.to; ++i) {
+                    if (i < it.to) {
+                        const int buffer = done[0] & 1;
+#pragma unroll 1
+                        for (int c = 0; c < CH; ++c) {
+                            wait(full0 + 8 * at.slot, at.lap);
+                            scores(buffer, 0, at, c);
+                            commit(empty0 + 8 * at.slot);
+                            at.step(p.slots);
+                        }
+                        commit(s_ready + 8 * buffer);
+                        if (i == it.to - 1) commit(q_empty);
+                        ++done[0];
+                    }
+                    if (i > it.from) {
+                        const int tile = done[0] - (i < it.to ? 2 : 1);
+                        wait(p_ready + 8 * (tile & 1), (tile / 2) & 1);
+                        tmem_fence_after();
+#pragma unroll 1
+                        for (int c = 0; c < CH; ++c) {
+                            wait(full0 + 8 * at.slot, at.lap);
+                            sums(tile & 1, c * W, at, i > it.from + 1);
+                            commit(empty0 + 8 * at.slot);
+                            at.step(p.slots);
+                        }
+                        commit(o_done);
+                    }
+                }
+            } else {
+                // S0(0), S1(0), then O0(i), S0(i + 1), O1(i), S1(i + 1); streams that see nothing
+                // of a tile leave it out
+                int tokens;
+                const Seen sees[2] = {stream_sees<STREAMS>(p, it, 0, tokens), stream_sees<STREAMS>(p, it, 1, tokens)};
+                bool add[2] = {false, false};
+                uint32_t active = 0;  // streams at work on tile i - 1
+#pragma unroll 1
+                for (int i = it.from; i <= it.to; ++i) {
+                    const int key = it.tile(i) * 128;
+                    const uint32_t next = i < it.to ? uint32_t(sees[0].any(key, 128)) | uint32_t(sees[1].any(key, 128)) << 1 : 0u;
+                    Place values = at, keys = at;
+                    if (i > it.from) keys.step(p.slots);
+#pragma unroll 1
+                    for (int x = 0; x < 2; ++x) {
+                        if (i > it.from && x == 0) wait(full0 + 8 * values.slot, values.lap);
+                        if (active >> x & 1) {
+                            const int tile = (x ? done[1] : done[0]) - 1;
+                            wait(p_ready + 8 * x, tile & 1);
+                            tmem_fence_after();
+                            sums(x, x * D, values, x ? add[1] : add[0]);
+                            commit(o_done + 8 * x);
+                            (x ? add[1] : add[0]) = true;
+                        }
+                        if (i > it.from && x == 1) commit(empty0 + 8 * values.slot);
+                        if (i < it.to && x == 0) wait(full0 + 8 * keys.slot, keys.lap);
+                        if (next >> x & 1) {
+                            scores(x, x, keys, 0);
+                            commit(s_ready + 8 * x);
+                            ++(x ? done[1] : done[0]);
+                        }
+                        if (i < it.to && x == 1) commit(empty0 + 8 * keys.slot);
+                    }
+                    if (i == it.to - 1) commit(q_empty);
+                    active = next;
+                    if (i > it.from) at.step(p.slots);
+                    if (i < it.to) at.step(p.slots);
+                }
+            }
+        }
+        commit(finished);
+        mbar_wait_bounded(finished, 0);
+    } else {
+        // ---------------------------------------------------------------- weights
+        const int x = STREAMS == 1 ? 0 : warp / 4, r = tid & 127, quarter = warp & 3;
+        const uint32_t lanes = uint32_t(quarter * 32) << 16, mine = O + lanes + x * D;
+        const float c2 = __fmul_rn(p.scale, 1.4426950408889634f);
+        const uint64_t scale2 = tile::pack2(c2, c2);
+        const int per_tile = 128 / p.box;
+        int tiles = 0;  // of the stream so far
+#pragma unroll 1
+        for (int index = blockIdx.x; index < items; index += gridDim.x) {
+            const PromptItem it = prompt_at<STREAMS>(p, all, index);
+            int tokens;
+            const Seen sees = stream_sees<STREAMS>(p, it, x, tokens), seen(p, it.pos, it.pos + it.tokens - 1);
+            const int32_t *table = p.table + int64_t(it.b) * p.max_pages;
+            const int start = it.pos + x * p.tokens;  // position of the stream's first token
+            const bool real = r < tokens * p.group;
+            const int last = real ? start + r / p.group : -1, low = p.window ? last - p.window + 1 : 0;
+            float ref = -INFINITY, use = 0.0f;
+            uint64_t total[2] = {0ull, 0ull};
+            int worked = 0;
+#pragma unroll 1
+            for (int i = it.from; i < it.to; ++i) {
+                const int key0 = it.tile(i) * 128;
+                if (!sees.any(key0, 128)) continue;
+                // boxes of keys whose page is there
+                int page = -1;
+                const int key = key0 + lane * p.box;
+                if (lane < per_tile && seen.any(key, p.box)) page = __ldg(table + page_of(p, key));
+                const int buffer = STREAMS == 1 ? tiles & 1 : x;
+                wait(s_ready + 8 * buffer, (STREAMS == 1 ? tiles / 2 : tiles) & 1);
+                tmem_fence_after();
+                const uint32_t at = S + buffer * 128 + lanes;
+                float s[128];
+#pragma unroll
+                for (int c = 0; c < 128; c += 32) {
+                    float part[32];
+                    tmem_ld<32>(at + c, part);
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) s[c + k] = part[k];
+                }
+                const uint32_t there = __ballot_sync(0xffffffffu, unsigned(page) < unsigned(p.pages));
+                tmem_wait_ld();
+                settle(s);
+                const bool plain = there == (per_tile == 32 ? 0xffffffffu : (1u << per_tile) - 1u) && key0 + 127 <= start &&
+                                   (!p.window || key0 >= start + tokens - p.window);
+                if (!plain) {
+                    // (a score that is not seen becomes one that stays below every other: its weight is set to 0 below)
+                    const int shift = 31 - __clz(p.box);
+#pragma unroll
+                    for (int k = 0; k < 128; ++k) {
+                        const int j = key0 + k;
+                        const bool v = j <= last && (j >= low || j < p.sinks) && (there >> (k >> shift) & 1);
+                        if (!v) s[k] = c2 < 0.0f ? INFINITY : -INFINITY;
+                    }
+                }
+                float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                if (c2 >= 0.0f) {
+#pragma unroll
+                    for (int k = 0; k < 128; k += 2) top[(k / 2) & 3] = fmaxf(top[(k / 2) & 3], fmaxf(s[k], s[k + 1]));
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 128; k += 2) top[(k / 2) & 3] = fmaxf(top[(k / 2) & 3], -fminf(s[k], s[k + 1]));
+                }
+                float m = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+                m = m == -INFINITY ? m : __fmul_rn(m, fabsf(c2));
+                // kept while weights stay below 2^8
+                const bool moves = m > __fadd_rn(ref, 8.0f);
+                const float now = moves ? ceilf(m) : ref;
+                if (__any_sync(0xffffffffu, moves && ref != -INFINITY)) {
+                    const float f = moves && ref != -INFINITY ? power_of_two(__fsub_rn(ref, now)) : 1.0f;
+                    wait(o_done + 8 * x, (tiles - 1) & 1);  // (the tile before's sums are in)
+                    tmem_fence_after();
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 16) {
+                        float o[16];
+                        tmem_ld<16>(mine + c, o);
+                        tmem_wait_ld();
+                        settle(o);
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) o[k] = __fmul_rn(o[k], f);
+                        tmem_st<16>(mine + c, o);
+                    }
+                    tmem_wait_st();
+                    const uint64_t ff = tile::pack2(f, f);
+                    total[0] = tile::mul2(total[0], ff);
+                    total[1] = tile::mul2(total[1], ff);
+                }
+                ref = now;
+                use = ref == -INFINITY ? 0.0f : ref;
+                const uint64_t minus = tile::pack2(-use, -use);
+#pragma unroll
+                for (int c = 0; c < 128; c += 32) {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) {
+                        float a, b;
+                        tile::unpack2(tile::fma2(tile::pack2(s[c + 2 * k], s[c + 2 * k + 1]), scale2, minus), a, b);
+                        a = exp2_fast(a);
+                        b = exp2_fast(b);
+                        if (!plain) {
+                            if (fabsf(s[c + 2 * k]) == INFINITY) a = 0.0f;
+                            if (fabsf(s[c + 2 * k + 1]) == INFINITY) b = 0.0f;
+                        }
+                        total[k & 1] = tile::add2(total[k & 1], tile::pack2(a, b));
+                        w[k] = pack_bf16(a, b);
+                    }
+                    tile::tmem_st(at + c / 2, w);
+                }
+                tmem_wait_st();
+                tmem_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_ready + 8 * buffer);
+                ++tiles;
+                ++worked;
+            }
+            // ------------------------------------------------ what the item gives
+            float t0, t1, t2, t3;
+            tile::unpack2(total[0], t0, t1);
+            tile::unpack2(total[1], t2, t3);
+            const float sum = __fadd_rn(__fadd_rn(t0, t1), __fadd_rn(t2, t3));
+            if (worked) wait(o_done + 8 * x, (tiles - 1) & 1);
+            tmem_fence_after();
+            const bool none = ref == -INFINITY;
+            const int64_t row = it.row + x * p.tokens + r / p.group;
+            const int head = it.g * p.group + r % p.group;
+            const int64_t part = (int64_t(it.index) * STREAMS + x) * 128 + r;
+            const bool whole = it.pieces == 1;
+            const float f = none ? 0.0f : whole ? __fdiv_rn(1.0f, sum) : 1.0f;
+            if (real) {
+                if (!whole)
+                    p.meta[part] = make_float2(ref, sum);
+                else if (p.lse)
+                    p.lse[row * p.heads + head] = none ? -INFINITY : __fmul_rn(0.6931471805599453f, __fadd_rn(ref, log2f(sum)));
+            }
+#pragma unroll 1
+            for (int c = 0; c < D; c += 16) {
+                float o[16];
+                tmem_ld<16>(mine + c, o);
+                tmem_wait_ld();
+                settle(o);
+#pragma unroll
+                for (int k = 0; k < 16; ++k) o[k] = none ? 0.0f : __fmul_rn(o[k], f);
+                if (!real) continue;
+                if (whole) {
+                    uint4 *to = reinterpret_cast<uint4 *>(p.out + row * p.ld_out + head * D + c);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        to[k] = make_uint4(pack_bf16(o[8 * k], o[8 * k + 1]), pack_bf16(o[8 * k + 2], o[8 * k + 3]),
+                                           pack_bf16(o[8 * k + 4], o[8 * k + 5]), pack_bf16(o[8 * k + 6], o[8 * k + 7]));
+                } else {
+                    float4 *to = reinterpret_cast<float4 *>(p.parts + part * D + c);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) to[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                }
+            }
+            tmem_fence_before();
+        }
+    }
+    tmem_fence_before();
+    __syncthreads();
+    tmem_fence_after();
+    if (warp == kTensor) tile::tmem_free(tm, 512);
+}
+
+// Joins a row's pieces in order; a warp has a row.
+template <int D>
+__global__ void __launch_bounds__(256) attend_join_pieces(const AttendParams p)
+{
+    constexpr int E = D / 32, STREAMS = D == 256 ? 1 : 2;
+    grid_dependency_wait();
+    const int64_t unit = int64_t(blockIdx.x) * 8 + threadIdx.x / 32;
+    const int lane = threadIdx.x & 31, t = int(unit / p.heads), h = int(unit % p.heads), each = STREAMS * p.tokens;
     if (t >= p.T) return;
+#pragma unroll 1
     for (int b = 0; b < p.B; ++b) {
         const Sequence s(p, b);
         const int i = t - s.row;
         if (i < 0 || i >= s.done || s.done <= kFew) continue;
-        const int pos = s.pos + i;
-        float q[E], o[E], m = -INFINITY, l = 0.0f;
-        for (int e = 0; e < E; ++e) {
-            q[e] = __fmul_rn(bf16_bits_to_f32(p.q[t * p.ld_q + h * D + lane + 32 * e]), p.scale);
-            o[e] = 0.0f;
+        const int pieces = pieces_of(p, s, each);
+        if (pieces == 1) continue;
+        const int index = ((s.done - 1) / each - i / each) * p.kv_heads + h / p.group;
+        const int64_t first = (int64_t(p.prefix[b] + index * pieces) * STREAMS + i % each / p.tokens) * 128 + i % p.tokens * p.group + h % p.group;
+        float top = -INFINITY, total = 0.0f, sum[E];
+#pragma unroll 1
+        for (int k = 0; k < pieces; ++k) top = fmaxf(top, p.meta[first + int64_t(k) * STREAMS * 128].x);
+#pragma unroll
+        for (int e = 0; e < E; ++e) sum[e] = 0.0f;
+#pragma unroll 2
+        for (int k = 0; k < pieces; ++k) {
+            const int64_t at = first + int64_t(k) * STREAMS * 128;
+            const float2 m = p.meta[at];
+            const float w = m.x == -INFINITY ? 0.0f : power_of_two(__fsub_rn(m.x, top));
+            total = __fmaf_rn(m.y, w, total);
+#pragma unroll
+            for (int e = 0; e < E; ++e) sum[e] = __fmaf_rn(p.parts[at * D + lane + 32 * e], w, sum[e]);
         }
-        const int low = p.window ? max(pos - p.window + 1, 0) : 0;
-        for (int j = p.window && p.sinks > 0 ? 0 : low; j <= pos; ++j) {
-            if (j < low && j >= p.sinks) j = low;
-            const int page = __ldg(p.table + int64_t(b) * p.max_pages + j / p.page_size);
-            if (page < 0 || page >= p.pages) continue;
-            const int64_t at = page * p.page_stride + j % p.page_size * p.token_stride + h / p.group * p.head_stride + lane;
-            float dot = 0.0f;
-            for (int e = 0; e < E; ++e) dot = __fmaf_rn(q[e], bf16_bits_to_f32(p.k[at + 32 * e]), dot);
-            for (int d = 16; d > 0; d /= 2) dot = __fadd_rn(dot, __shfl_xor_sync(0xffffffffu, dot, d));
-            const float top = fmaxf(m, dot);
-            const float keep = top == -INFINITY ? 1.0f : expf(m - top), w = top == -INFINITY ? 0.0f : expf(dot - top);
-            m = top;
-            l = __fmaf_rn(l, keep, w);
-            for (int e = 0; e < E; ++e) o[e] = __fmaf_rn(o[e], keep, __fmul_rn(w, bf16_bits_to_f32(p.v[at + 32 * e])));
-        }
-        for (int e = 0; e < E; ++e) {
-            const float y = l == 0.0f ? 0.0f : __fdiv_rn(o[e], l);
-            reinterpret_cast<__nv_bfloat16 *>(p.out)[t * p.ld_out + h * D + lane + 32 * e] = __float2bfloat16_rn(y);
-        }
-        if (p.lse && lane == 0) p.lse[int64_t(t) * p.heads + h] = l == 0.0f ? -INFINITY : __fadd_rn(m, logf(l));
+        const bool none = top == -INFINITY;
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            reinterpret_cast<__nv_bfloat16 *>(p.out)[t * p.ld_out + h * D + lane + 32 * e] = __float2bfloat16_rn(none ? 0.0f : __fdiv_rn(sum[e], total));
+        if (p.lse && lane == 0)
+            p.lse[int64_t(t) * p.heads + h] = none ? -INFINITY : __fmul_rn(0.6931471805599453f, __fadd_rn(top, log2f(total)));
     }
 }
 
@@ -836,19 +1370,28 @@ cudaError_t launch_few(const AttendParams &p, const Maps &m, const FewPlan &f, i
 }
 
 template <int D>
+cudaError_t launch_prompt(const AttendParams &p, const Maps &m, const PromptPlan &f, int sms, cudaStream_t stream)
+{
+    static std::atomic<int> configured[2][64] = {};
+    Launch l;
+    l.grid = dim3(unsigned(f.items < sms ? f.items : sms));
+    l.threads = prompt_threads(D);
+    l.smem = size_t(f.smem);
+    l.pdl = true;
+    cudaError_t e = launch_one(attend_prompt<D>, configured[0], l, stream, m.q, m.k, m.v, p);
+    if (e != cudaSuccess || f.pieces == 1) return e;
+    l.grid = dim3(unsigned((int64_t(p.T) * p.heads + 7) / 8));
+    l.threads = 256;
+    l.smem = 0;
+    return launch_one(attend_join_pieces<D>, configured[1], l, stream, p);
+}
+
+template <int D>
 cudaError_t launch_attend(const AttendParams &p, const Maps &m, const FewPlan &f, int sms, cudaStream_t stream)
 {
-    static std::atomic<int> configured[64] = {};
-    cudaError_t e = f.columns == 16   ? launch_few<D, 16>(p, m, f, sms, stream)
-                    : f.columns == 32 ? launch_few<D, 32>(p, m, f, sms, stream)
-                                      : launch_few<D, 64>(p, m, f, sms, stream);
-    if (e != cudaSuccess || p.max_new <= kFew) return e;
-    Launch l;
-    l.grid = dim3(unsigned((int64_t(p.T) * p.heads + 3) / 4));
-    l.threads = 128;
-    l.smem = 0;
-    l.pdl = true;
-    return launch_one(attend_simple<D>, configured, l, stream, p);
+    return f.columns == 16   ? launch_few<D, 16>(p, m, f, sms, stream)
+           : f.columns == 32 ? launch_few<D, 32>(p, m, f, sms, stream)
+                             : launch_few<D, 64>(p, m, f, sms, stream);
 }
 
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
@@ -861,8 +1404,10 @@ qmv_status check_attend(int B, int T, int max_new, int heads, int kv_heads, int 
     if (page_size < 8 || page_size % 8 != 0 || page_size > 65536 || max_pages < 1 || int64_t(max_pages) * page_size > (1 << 26) ||
         window < 0 || window > (1 << 30) || sinks < 0 || sinks > (1 << 30))
         return QMV_ERR_SHAPE;
-    const FewPlan f = few_plan(B, max_new, heads, kv_heads, head_dim, int64_t(max_pages) * page_size, window, sinks);
-    return f.workspace > (size_t(1) << 40) || f.items >= (int64_t(1) << 31) ? QMV_ERR_SHAPE : QMV_OK;
+    const int64_t capacity = int64_t(max_pages) * page_size;
+    const FewPlan f = few_plan(B, max_new, heads, kv_heads, head_dim, capacity, window, sinks);
+    const PromptPlan g = prompt_plan(B, T, max_new, heads, kv_heads, head_dim, capacity, window, sinks);
+    return f.workspace + g.workspace > (size_t(1) << 40) || f.items >= (int64_t(1) << 31) || g.items >= (int64_t(1) << 31) ? QMV_ERR_SHAPE : QMV_OK;
 }
 
 }  // namespace
@@ -872,7 +1417,11 @@ extern "C" size_t qmv_attend_workspace_size(int B, int T, int max_new, int heads
                                             int max_pages, int window, int sinks)
 {
     if (qmv::check_attend(B, T, max_new, heads, kv_heads, head_dim, page_size, max_pages, window, sinks) != QMV_OK) return 0;
-    return qmv::attend::few_plan(B, max_new, heads, kv_heads, head_dim, int64_t(max_pages) * page_size, window, sinks).workspace;
+    // (the two kinds of sequences run one after the other, each with the whole of it)
+    const int64_t capacity = int64_t(max_pages) * page_size;
+    const size_t few = qmv::attend::few_plan(B, max_new, heads, kv_heads, head_dim, capacity, window, sinks).workspace;
+    const size_t prompt = qmv::attend::prompt_plan(B, T, max_new, heads, kv_heads, head_dim, capacity, window, sinks).workspace;
+    return few > prompt ? few : prompt;
 }
 
 extern "C" qmv_status qmv_attend_run(const uint16_t *q, const uint16_t *k_cache, const uint16_t *v_cache,
@@ -937,8 +1486,22 @@ extern "C" qmv_status qmv_attend_run(const uint16_t *q, const uint16_t *k_cache,
     if (st == QMV_OK) st = encode_bf16(&m.q, q, 3, q_dims, q_strides, q_box);
     if (st != QMV_OK) return st;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const cudaError_t e = head_dim == 64    ? launch_attend<64>(p, m, f, dev.sms, s)
-                          : head_dim == 128 ? launch_attend<128>(p, m, f, dev.sms, s)
-                                            : launch_attend<256>(p, m, f, dev.sms, s);
+    cudaError_t e = head_dim == 64    ? launch_attend<64>(p, m, f, dev.sms, s)
+                    : head_dim == 128 ? launch_attend<128>(p, m, f, dev.sms, s)
+                                      : launch_attend<256>(p, m, f, dev.sms, s);
+    const PromptPlan g = prompt_plan(B, T, max_new, heads, kv_heads, head_dim, int64_t(max_pages) * page_size, window, sinks);
+    if (e == cudaSuccess && g.items > 0) {
+        p.tokens = g.tokens; p.pieces = g.pieces; p.slots = g.slots;
+        p.q_off = g.q_off; p.misc_off = g.misc_off;
+        p.prefix = reinterpret_cast<int32_t *>(at + g.prefix_off);
+        p.meta = reinterpret_cast<float2 *>(at + g.meta_off);
+        p.parts = reinterpret_cast<float *>(at + g.parts_off);
+        const int tile_box[3] = {64, p.group, g.tokens};
+        st = encode_bf16(&m.q, q, 3, q_dims, q_strides, tile_box);
+        if (st != QMV_OK) return st;
+        e = head_dim == 64    ? launch_prompt<64>(p, m, g, dev.sms, s)
+            : head_dim == 128 ? launch_prompt<128>(p, m, g, dev.sms, s)
+                              : launch_prompt<256>(p, m, g, dev.sms, s);
+    }
     return e == cudaSuccess ? QMV_OK : record_cuda_failure("attention kernel launch", e);
 }

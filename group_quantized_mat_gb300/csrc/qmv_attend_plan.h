@@ -50,6 +50,48 @@ inline void few_smem(FewPlan &f, int D, int B)
     f.smem = f.slots * kChunk + fixed + 1024;  // (1024: to align the ring)
 }
 
+// Work items of longer sequences: two tiles of 128 query rows (one of head_dim 256) over
+// the tiles of 128 keys that they see, or over one of `pieces` parts of them.
+struct PromptPlan {
+    int tokens;  // of a tile: as many as their heads of one kv head fit 128 rows
+    int streams, slots, chunk;
+    int q_off, misc_off, smem;
+    int pieces;
+    int64_t items;
+    size_t prefix_off, meta_off, parts_off, workspace;
+};
+
+inline PromptPlan prompt_plan(int B, int T, int max_new, int heads, int kv_heads, int D, int64_t capacity, int window, int sinks)
+{
+    PromptPlan f{};
+    if (max_new <= kFew) return f;
+    f.tokens = 128 / (heads / kv_heads);
+    f.streams = D == 256 ? 1 : 2;
+    f.chunk = 128 * (D < 128 ? D : 128) * 2;
+    const int q_bytes = f.streams * 128 * D * 2, misc = (512 + B * 16 + (B + 1) * 4 + 1023) & ~1023;
+    f.slots = (kSmemBlock - 1024 - q_bytes - misc) / f.chunk;
+    if (f.slots > 8) f.slots = 8;
+    f.q_off = f.slots * f.chunk;
+    f.misc_off = f.q_off + q_bytes;
+    f.smem = f.misc_off + misc + 1024;
+    // sequences of more than kFew tokens, their last items not whole
+    const int each = f.streams * f.tokens, sequences = T / (kFew + 1) < B ? T / (kFew + 1) : B;
+    const int64_t tiles = int64_t(T / each + sequences) * kv_heads;
+    // enough parts that four rounds of items fill 152 SMs, of 1024 keys at least
+    int64_t keys = capacity;
+    if (window && int64_t(window) + each + sinks < keys) keys = int64_t(window) + each + sinks;
+    int64_t pieces = tiles > 0 ? (4 * 152 + tiles - 1) / tiles : 1;
+    if (pieces > (keys + 1023) / 1024) pieces = (keys + 1023) / 1024;
+    f.pieces = int(pieces < 1 ? 1 : pieces);
+    f.items = tiles * f.pieces;
+    f.prefix_off = 0;
+    f.meta_off = up256(size_t(B + 1) * 4);
+    const size_t rows = f.pieces > 1 ? size_t(f.items) * f.streams * 128 : 0;
+    f.parts_off = f.meta_off + up256(rows * 8);
+    f.workspace = f.parts_off + up256(rows * D * 4);
+    return f;
+}
+
 inline FewPlan few_plan(int B, int max_new, int heads, int kv_heads, int D, int64_t capacity, int window, int sinks)
 {
     FewPlan f{};
