@@ -1097,7 +1097,7 @@ __global__ void __launch_bounds__(prompt_threads(D), 1)
                             commit(empty0 + 8 * at.slot);
                             at.step(p.slots);
                         }
-                        commit(o_done);
+                        commit(o_done + 8 * (tile & 1));
                     }
                 }
             } else {
@@ -1150,6 +1150,15 @@ __global__ void __launch_bounds__(prompt_threads(D), 1)
         const uint64_t scale2 = tile::pack2(c2, c2);
         const int per_tile = 128 / p.box;
         int tiles = 0;  // of the stream so far
+        // The last tile's sums are in. (One stream's scores run ahead of the sums of the tile
+        // before, so that its tiles have a barrier each in turn: with one for all, the wait for
+        // an item's last tile could see the parity of the tile before the one before it.)
+        const auto sums_in = [&]() {
+            if (STREAMS == 1)
+                wait(o_done + 8 * ((tiles - 1) & 1), ((tiles - 1) / 2) & 1);
+            else
+                wait(o_done + 8 * x, (tiles - 1) & 1);
+        };
 #pragma unroll 1
         for (int index = blockIdx.x; index < items; index += gridDim.x) {
             const PromptItem it = prompt_at<STREAMS>(p, all, index);
@@ -1212,7 +1221,7 @@ __global__ void __launch_bounds__(prompt_threads(D), 1)
                 const float now = moves ? ceilf(m) : ref;
                 if (__any_sync(0xffffffffu, moves && ref != -INFINITY)) {
                     const float f = moves && ref != -INFINITY ? power_of_two(__fsub_rn(ref, now)) : 1.0f;
-                    wait(o_done + 8 * x, (tiles - 1) & 1);  // (the tile before's sums are in)
+                    sums_in();
                     tmem_fence_after();
 #pragma unroll 1
                     for (int c = 0; c < D; c += 16) {
@@ -1262,7 +1271,7 @@ __global__ void __launch_bounds__(prompt_threads(D), 1)
             tile::unpack2(total[0], t0, t1);
             tile::unpack2(total[1], t2, t3);
             const float sum = __fadd_rn(__fadd_rn(t0, t1), __fadd_rn(t2, t3));
-            if (worked) wait(o_done + 8 * x, (tiles - 1) & 1);
+            if (worked) sums_in();
             tmem_fence_after();
             const bool none = ref == -INFINITY;
             const int64_t row = it.row + x * p.tokens + r / p.group;

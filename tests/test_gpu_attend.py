@@ -118,6 +118,18 @@ def test_prompts(heads, kv, D, new, keys):
     p.check(p.run())
 
 
+@pytest.mark.parametrize("heads,kv,D", [(24, 8, 256), (4, 4, 256), (16, 2, 128), (6, 2, 64)])
+@pytest.mark.parametrize("new,keys", [([29], [3323]), ([17, 100, 5, 33], [5000, 2100, 3000, 1100])])
+def test_prompts_in_pieces(heads, kv, D, new, keys):
+    """Few rows over many keys: their tiles in several pieces, which end at other tiles each."""
+    p = Problem(new, keys, heads, kv, D, page=16, seed=heads + sum(keys), sharp=2.0)
+    d = p.device()
+    got = p.run(d)
+    p.check(got)
+    for _ in range(3):
+        assert same(p.run(d), got)
+
+
 @pytest.mark.parametrize("page", [8, 16, 24, 40, 64, 96, 128, 200, 256, 1000])
 @pytest.mark.parametrize("order", ["tokens", "heads"])
 def test_pages(page, order):
