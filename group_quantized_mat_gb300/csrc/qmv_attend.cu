@@ -153,13 +153,12 @@ __host__ __device__ constexpr uint32_t mma_kind(int N, bool a_rows, bool b_rows)
 }
 
 // D (128 x N fp32, tensor memory) (+)= A (128 x 16) B^T (N x 16), both from shared memory.
-template <uint32_t KIND>
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, bool add)
+__device__ __forceinline__ void mma_ss(uint32_t kind, uint32_t d, uint64_t a, uint64_t b, bool add)
 {
     asm volatile(
         "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(KIND), "r"(uint32_t(add))
+        "l"(a), "l"(b), "r"(kind), "r"(uint32_t(add))
         : "memory");
 }
 
@@ -465,7 +464,7 @@ __global__ void __launch_bounds__(few_threads(NC), NC < 64 ? 2 : 1)
                 if (lane == 0) {
 #pragma unroll
                     for (int k = 0; k < kKeys / 16; ++k)
-                        mma_ss<kValueKind>(O + c * 2 * NC, a + k * (2048 >> 4), b + k * (16 * kKeyBytes >> 4), !fresh || key + k > 0);
+                        mma_ss(kValueKind, O + c * 2 * NC, a + k * (2048 >> 4), b + k * (16 * kKeyBytes >> 4), !fresh || key + k > 0);
                     tmem_commit(empty0 + 8 * at.slot);
                     if (i == kChunks - 1) tmem_commit(o_done);
                 }
@@ -488,7 +487,7 @@ __global__ void __launch_bounds__(few_threads(NC), NC < 64 ? 2 : 1)
                     const uint64_t a = keys0 + uint32_t(at.slot * (kChunk >> 4)), b = queries + uint32_t((set * DB + c) * NC * (128 >> 4));
                     if (lane == 0) {
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) mma_ss<kScoreKind>(d, a + 2 * k, b + 2 * k, c + k > 0);
+                        for (int k = 0; k < 4; ++k) mma_ss(kScoreKind, d, a + 2 * k, b + 2 * k, c + k > 0);
                         tmem_commit(empty0 + 8 * at.slot);
                         if (i == kChunks - 1) {
                             tmem_commit(s_ready + 8 * (leaf & 1));
@@ -871,6 +870,27 @@ __device__ __forceinline__ Seen stream_sees(const AttendParams &p, const PromptI
     return seen;
 }
 
+// Bits 0 .. n - 1.
+__device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
+
+__device__ __forceinline__ void hide(float (&s)[32], uint32_t see)
+{
+#pragma unroll
+    for (int k = 0; k < 32; ++k)
+        if (!(see >> k & 1)) s[k] = -INFINITY;
+}
+
+__device__ __forceinline__ void tmem_ld32(uint32_t a, float (&v)[32])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+          "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]), "=f"(v[17]),
+          "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]), "=f"(v[25]), "=f"(v[26]),
+          "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+        : "r"(a));
+}
+
 struct PromptShared {
     uint64_t full[8], empty[8], q_full, q_empty, edge, s_ready[2], p_ready[2], o_done[2], finished;
     int abort;
@@ -1036,7 +1056,8 @@ __global__ void __launch_bounds__(prompt_threads(D), 1)
         }
     } else if (warp == kTensor) {
         // ---------------------------------------------------------- tensor warp
-        constexpr uint32_t kScoreKind = mma_kind(128, false, false), kValueKind = mma_kind(W, false, true);
+        constexpr uint32_t kValueKind = mma_kind(W, false, true);
+        const uint32_t score_kind = mma_kind(128, false, false) | (p.scale < 0.0f ? 1u << 13 : 0u);  // (- Q)
         const uint64_t keys0 = descriptor(base, 16, 1024, 2), queries = descriptor(Q, 16, 1024, 2);
         const uint64_t values0 = descriptor(base, 16384, 1024, 2);
         Place at;
@@ -1047,7 +1068,7 @@ __global__ void __launch_bounds__(prompt_threads(D), 1)
                 const uint64_t k0 = keys0 + uint32_t(c.slot * (kBytes >> 4)), q0 = queries + uint32_t((x * DB + b * WB) * (16384 >> 4));
 #pragma unroll
                 for (int k = 0; k < W / 16; ++k)
-                    mma_ss<kScoreKind>(S + buffer * 128, q0 + (k / 4) * (16384 >> 4) + 2 * (k & 3), k0 + (k / 4) * (16384 >> 4) + 2 * (k & 3), b + k > 0);
+                    mma_ss(score_kind, S + buffer * 128, q0 + (k / 4) * (16384 >> 4) + 2 * (k & 3), k0 + (k / 4) * (16384 >> 4) + 2 * (k & 3), b + k > 0);
             }
             __syncwarp();
         };
@@ -1146,9 +1167,10 @@ __global__ void __launch_bounds__(prompt_threads(D), 1)
         // ---------------------------------------------------------------- weights
         const int x = STREAMS == 1 ? 0 : warp / 4, r = tid & 127, quarter = warp & 3;
         const uint32_t lanes = uint32_t(quarter * 32) << 16, mine = O + lanes + x * D;
-        const float c2 = __fmul_rn(p.scale, 1.4426950408889634f);
+        // (the products have the scale's sign already; above 0, so that a hidden score's weight is 0)
+        const float c2 = fmaxf(__fmul_rn(fabsf(p.scale), 1.4426950408889634f), 1.2e-38f);
         const uint64_t scale2 = tile::pack2(c2, c2);
-        const int per_tile = 128 / p.box;
+        const int per_tile = 128 / p.box, box_shift = 31 - __clz(p.box);
         int tiles = 0;  // of the stream so far
         // The last tile's sums are in. (One stream's scores run ahead of the sums of the tile
         // before, so that its tiles have a barrier each in turn: with one for all, the wait for
@@ -1183,39 +1205,37 @@ __global__ void __launch_bounds__(prompt_threads(D), 1)
                 wait(s_ready + 8 * buffer, (STREAMS == 1 ? tiles / 2 : tiles) & 1);
                 tmem_fence_after();
                 const uint32_t at = S + buffer * 128 + lanes;
-                float s[128];
-#pragma unroll
-                for (int c = 0; c < 128; c += 32) {
-                    float part[32];
-                    tmem_ld<32>(at + c, part);
-#pragma unroll
-                    for (int k = 0; k < 32; ++k) s[c + k] = part[k];
-                }
                 const uint32_t there = __ballot_sync(0xffffffffu, unsigned(page) < unsigned(p.pages));
-                tmem_wait_ld();
-                settle(s);
-                const bool plain = there == (per_tile == 32 ? 0xffffffffu : (1u << per_tile) - 1u) && key0 + 127 <= start &&
-                                   (!p.window || key0 >= start + tokens - p.window);
-                if (!plain) {
-                    // (a score that is not seen becomes one that stays below every other: its weight is set to 0 below)
-                    const int shift = 31 - __clz(p.box);
+                const bool plain = there == (1u << per_tile) - 1u && key0 + 127 <= start && (!p.window || key0 >= start + tokens - p.window);
+                // which of the 32 keys from `key` on the row sees
+                const auto see = [&](int c) {
+                    const int key = key0 + c;
+                    uint32_t v = below(p.sinks - key) | ~below(low - key);
+                    v &= below(last + 1 - key);
+                    uint32_t boxes = 0;
 #pragma unroll
-                    for (int k = 0; k < 128; ++k) {
-                        const int j = key0 + k;
-                        const bool v = j <= last && (j >= low || j < p.sinks) && (there >> (k >> shift) & 1);
-                        if (!v) s[k] = c2 < 0.0f ? INFINITY : -INFINITY;
+                    for (int k = 0; k < 32; k += 8) boxes |= (there >> ((c + k) >> box_shift) & 1u) * (0xffu << k);
+                    return v & boxes;
+                };
+                // Scores go by in 32 columns, the next 32 on their way (all 128 in registers, and code
+                // for all of them in a row, did not stay in the instruction cache: 3100 cycles a
+                // tile).
+                float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                float s[2][32];
+                tmem_ld32(at, s[0]);
+#pragma unroll 1
+                for (int c = 0; c < 128; c += 64) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        tmem_wait_ld();
+                        settle(s[h]);
+                        tmem_ld32(at + ((c + 32 * h + 32) & 127), s[1 - h]);  // (at the end the first again)
+                        if (!plain) hide(s[h], see(c + 32 * h));
+#pragma unroll
+                        for (int k = 0; k < 32; k += 2) top[(k / 2) & 3] = fmaxf(top[(k / 2) & 3], fmaxf(s[h][k], s[h][k + 1]));
                     }
                 }
-                float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                if (c2 >= 0.0f) {
-#pragma unroll
-                    for (int k = 0; k < 128; k += 2) top[(k / 2) & 3] = fmaxf(top[(k / 2) & 3], fmaxf(s[k], s[k + 1]));
-                } else {
-#pragma unroll
-                    for (int k = 0; k < 128; k += 2) top[(k / 2) & 3] = fmaxf(top[(k / 2) & 3], -fminf(s[k], s[k + 1]));
-                }
-                float m = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-                m = m == -INFINITY ? m : __fmul_rn(m, fabsf(c2));
+                const float m = __fmul_rn(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])), c2);
                 // kept while weights stay below 2^8
                 const bool moves = m > __fadd_rn(ref, 8.0f);
                 const float now = moves ? ceilf(m) : ref;
@@ -1241,23 +1261,27 @@ __global__ void __launch_bounds__(prompt_threads(D), 1)
                 ref = now;
                 use = ref == -INFINITY ? 0.0f : ref;
                 const uint64_t minus = tile::pack2(-use, -use);
+#pragma unroll 1
+                for (int c = 0; c < 128; c += 64) {
 #pragma unroll
-                for (int c = 0; c < 128; c += 32) {
-                    uint32_t w[16];
+                    for (int h = 0; h < 2; ++h) {
+                        tmem_wait_ld();
+                        settle(s[h]);
+                        if (c + 32 * h < 96) tmem_ld32(at + c + 32 * h + 32, s[1 - h]);
+                        if (!plain) hide(s[h], see(c + 32 * h));
+                        uint32_t w[16];
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) {
-                        float a, b;
-                        tile::unpack2(tile::fma2(tile::pack2(s[c + 2 * k], s[c + 2 * k + 1]), scale2, minus), a, b);
-                        a = exp2_fast(a);
-                        b = exp2_fast(b);
-                        if (!plain) {
-                            if (fabsf(s[c + 2 * k]) == INFINITY) a = 0.0f;
-                            if (fabsf(s[c + 2 * k + 1]) == INFINITY) b = 0.0f;
+                        for (int k = 0; k < 16; ++k) {
+                            float a, b;
+                            tile::unpack2(tile::fma2(tile::pack2(s[h][2 * k], s[h][2 * k + 1]), scale2, minus), a, b);
+                            a = exp2_fast(a);
+                            b = exp2_fast(b);
+                            total[k & 1] = tile::add2(total[k & 1], tile::pack2(a, b));
+                            w[k] = pack_bf16(a, b);
                         }
-                        total[k & 1] = tile::add2(total[k & 1], tile::pack2(a, b));
-                        w[k] = pack_bf16(a, b);
+                        // (columns whose scores have been read)
+                        tile::tmem_st(at + c / 2 + 16 * h, w);
                     }
-                    tile::tmem_st(at + c / 2, w);
                 }
                 tmem_wait_st();
                 tmem_fence_before();
