@@ -91,6 +91,16 @@ __device__ __forceinline__ float exp2_fast(float x)
     return y;
 }
 
+// One lane of a converged warp, for the instructions that a single thread issues. (With a
+// plain lane == 0 the compiler does not know that one thread is left, and a step of four
+// products took some 800 cycles.)
+__device__ __forceinline__ bool one_lane()
+{
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
 // 2^e for a whole number e <= 0, exactly (0 below 2^-126).
 __device__ __forceinline__ float power_of_two(float e) { return e < -126.0f ? 0.0f : tile::exp2i(int(e)); }
 
@@ -461,7 +471,7 @@ __global__ void __launch_bounds__(few_threads(NC), NC < 64 ? 2 : 1)
                 constexpr int kKeys = D == 64 ? 128 : 64;
                 const int c = i % HALVES, key = i / HALVES * kKeys;
                 const uint64_t a = values0 + uint32_t(at.slot * (kChunk >> 4)), b = weights + uint32_t(key * (kKeyBytes >> 4));
-                if (lane == 0) {
+                if (one_lane()) {
 #pragma unroll
                     for (int k = 0; k < kKeys / 16; ++k)
                         mma_ss(kValueKind, O + c * 2 * NC, a + k * (2048 >> 4), b + k * (16 * kKeyBytes >> 4), !fresh || key + k > 0);
@@ -485,7 +495,7 @@ __global__ void __launch_bounds__(few_threads(NC), NC < 64 ? 2 : 1)
                     const int c = i % DB;
                     const uint32_t d = S + (leaf & 1) * kScores + i / DB * NC;
                     const uint64_t a = keys0 + uint32_t(at.slot * (kChunk >> 4)), b = queries + uint32_t((set * DB + c) * NC * (128 >> 4));
-                    if (lane == 0) {
+                    if (one_lane()) {
 #pragma unroll
                         for (int k = 0; k < 4; ++k) mma_ss(kScoreKind, d, a + 2 * k, b + 2 * k, c + k > 0);
                         tmem_commit(empty0 + 8 * at.slot);
@@ -502,7 +512,7 @@ __global__ void __launch_bounds__(few_threads(NC), NC < 64 ? 2 : 1)
             ++n;
         }
         if (leaf > 0) sums(leaf - 1, fresh);
-        if (lane == 0) tmem_commit(finished);
+        if (one_lane()) tmem_commit(finished);
         mbar_wait_bounded(finished, 0);
     } else {
         // ---------------------------------------------------------------- weights
@@ -1064,7 +1074,7 @@ __global__ void __launch_bounds__(prompt_threads(D), 1)
         int n = 0, done[2] = {0, 0};  // tiles of a stream (of a buffer of scores) so far
         // scores of a tile whose keys are in the chunk at `c`, from element 64 b WB on
         const auto scores = [&](int buffer, int x, const Place &c, int b) {
-            if (lane == 0) {
+            if (one_lane()) {
                 const uint64_t k0 = keys0 + uint32_t(c.slot * (kBytes >> 4)), q0 = queries + uint32_t((x * DB + b * WB) * (16384 >> 4));
 #pragma unroll
                 for (int k = 0; k < W / 16; ++k)
@@ -1073,7 +1083,7 @@ __global__ void __launch_bounds__(prompt_threads(D), 1)
             __syncwarp();
         };
         const auto sums = [&](int buffer, int o, const Place &c, bool add) {
-            if (lane == 0) {
+            if (one_lane()) {
                 const uint64_t v0 = values0 + uint32_t(c.slot * (kBytes >> 4));
 #pragma unroll
                 for (int k = 0; k < 8; ++k) mma_ts<kValueKind>(O + o, S + buffer * 128 + 8 * k, v0 + k * (2048 >> 4), add || k > 0);
@@ -1081,7 +1091,7 @@ __global__ void __launch_bounds__(prompt_threads(D), 1)
             __syncwarp();
         };
         const auto commit = [&](uint32_t bar) {
-            if (lane == 0) tmem_commit(bar);
+            if (one_lane()) tmem_commit(bar);
             __syncwarp();
         };
 #pragma unroll 1
