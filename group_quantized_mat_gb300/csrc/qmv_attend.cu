@@ -250,7 +250,7 @@ __device__ __forceinline__ void sum_firsts(int32_t *first, int B, int lane)
     if (lane == 0) first[0] = 0;
 }
 
-__device__ __noinline__ Item item_at(const AttendParams &p, const Sequences &all, int index)
+__device__ __forceinline__ Item item_at(const AttendParams &p, const Sequences &all, int index)
 {
     int lo = 0, hi = p.B;
 #pragma unroll 1
@@ -838,7 +838,7 @@ __device__ __forceinline__ int pieces_of(const AttendParams &p, const Sequence &
 }
 
 template <int STREAMS>
-__device__ __noinline__ PromptItem prompt_at(const AttendParams &p, const Sequences &all, int index)
+__device__ __forceinline__ PromptItem prompt_at(const AttendParams &p, const Sequences &all, int index)
 {
     int lo = 0, hi = p.B;
 #pragma unroll 1
@@ -976,6 +976,9 @@ __global__ void __launch_bounds__(prompt_threads(D), 1)
     const Sequences all{first, sh.seqs};
     const int items = first[p.B];
     const Waits wait{&sh.abort, p.err};
+    // Items get smaller, so that every other round goes the other way (six prompts: the
+    // longest block has 2 % more than the mean, instead of 6).
+    const auto item_of = [](int round) { return round * int(gridDim.x) + int(round & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x); };
 
     if (warp == kProducer) {
         // ------------------------------------------------------------- producer
@@ -1009,7 +1012,7 @@ __global__ void __launch_bounds__(prompt_threads(D), 1)
             at.step(p.slots);
         };
 #pragma unroll 1
-        for (int index = blockIdx.x; index < items && ok; index += gridDim.x) {
+        for (int round = 0, index; ok && (index = item_of(round)) < items; ++round) {
             const PromptItem it = prompt_at<STREAMS>(p, all, index);
             if (it.from == it.to) continue;
             const Seen seen(p, it.pos, it.pos + it.tokens - 1);
@@ -1095,7 +1098,7 @@ __global__ void __launch_bounds__(prompt_threads(D), 1)
             __syncwarp();
         };
 #pragma unroll 1
-        for (int index = blockIdx.x; index < items; index += gridDim.x) {
+        for (int round = 0, index; (index = item_of(round)) < items; ++round) {
             const PromptItem it = prompt_at<STREAMS>(p, all, index);
             if (it.from == it.to) continue;
             wait(q_full, n & 1);
@@ -1136,37 +1139,56 @@ __global__ void __launch_bounds__(prompt_threads(D), 1)
                 // of a tile leave it out
                 int tokens;
                 const Seen sees[2] = {stream_sees<STREAMS>(p, it, 0, tokens), stream_sees<STREAMS>(p, it, 1, tokens)};
-                bool add[2] = {false, false};
-                uint32_t active = 0;  // streams at work on tile i - 1
+                uint32_t active = 0, started = 0;  // streams at work on tile i - 1; with sums of this item
 #pragma unroll 1
                 for (int i = it.from; i <= it.to; ++i) {
                     const int key = it.tile(i) * 128;
                     const uint32_t next = i < it.to ? uint32_t(sees[0].any(key, 128)) | uint32_t(sees[1].any(key, 128)) << 1 : 0u;
-                    Place values = at, keys = at;
-                    if (i > it.from) keys.step(p.slots);
+                    Place keys = at;
+                    const uint32_t vslot = at.slot;
+                    if (i > it.from) {
+                        keys.step(p.slots);
+                        wait(full0 + 8 * vslot, at.lap);
+                    }
 #pragma unroll 1
                     for (int x = 0; x < 2; ++x) {
-                        if (i > it.from && x == 0) wait(full0 + 8 * values.slot, values.lap);
-                        if (active >> x & 1) {
-                            const int tile = (x ? done[1] : done[0]) - 1;
-                            wait(p_ready + 8 * x, tile & 1);
+                        const bool work = active >> x & 1, more = next >> x & 1;
+                        if (work) {
+                            wait(p_ready + 8 * x, ((x ? done[1] : done[0]) - 1) & 1);
                             tmem_fence_after();
-                            sums(x, x * D, values, x ? add[1] : add[0]);
-                            commit(o_done + 8 * x);
-                            (x ? add[1] : add[0]) = true;
+                            if (one_lane()) {
+                                const uint64_t v0 = values0 + vslot * (kBytes >> 4);
+#pragma unroll
+                                for (int k = 0; k < 8; ++k)
+                                    mma_ts<kValueKind>(O + x * D, S + x * 128 + 8 * k, v0 + k * (2048 >> 4), k > 0 || (started >> x & 1));
+                                tmem_commit(o_done + 8 * x);
+                                if (x == 1) tmem_commit(empty0 + 8 * vslot);
+                            }
+                            __syncwarp();
+                        } else if (x == 1 && i > it.from) {
+                            commit(empty0 + 8 * vslot);
                         }
-                        if (i > it.from && x == 1) commit(empty0 + 8 * values.slot);
-                        if (i < it.to && x == 0) wait(full0 + 8 * keys.slot, keys.lap);
-                        if (next >> x & 1) {
-                            scores(x, x, keys, 0);
-                            commit(s_ready + 8 * x);
-                            ++(x ? done[1] : done[0]);
+                        if (x == 0 && i < it.to) wait(full0 + 8 * keys.slot, keys.lap);
+                        if (more) {
+                            if (one_lane()) {
+                                const uint64_t k0 = keys0 + uint32_t(keys.slot * (kBytes >> 4)), q0 = queries + uint32_t(x * DB * (16384 >> 4));
+#pragma unroll
+                                for (int k = 0; k < W / 16; ++k)
+                                    mma_ss(score_kind, S + x * 128, q0 + (k / 4) * (16384 >> 4) + 2 * (k & 3), k0 + (k / 4) * (16384 >> 4) + 2 * (k & 3), k > 0);
+                                tmem_commit(s_ready + 8 * x);
+                                if (x == 1) tmem_commit(empty0 + 8 * keys.slot);
+                            }
+                            __syncwarp();
+                        } else if (x == 1 && i < it.to) {
+                            commit(empty0 + 8 * keys.slot);
                         }
-                        if (i < it.to && x == 1) commit(empty0 + 8 * keys.slot);
                     }
+                    started |= active;
+                    done[0] += next & 1;
+                    done[1] += next >> 1;
                     if (i == it.to - 1) commit(q_empty);
                     active = next;
-                    if (i > it.from) at.step(p.slots);
+                    at = keys;
                     if (i < it.to) at.step(p.slots);
                 }
             }
@@ -1192,7 +1214,7 @@ __global__ void __launch_bounds__(prompt_threads(D), 1)
                 wait(o_done + 8 * x, (tiles - 1) & 1);
         };
 #pragma unroll 1
-        for (int index = blockIdx.x; index < items; index += gridDim.x) {
+        for (int round = 0, index; (index = item_of(round)) < items; ++round) {
             const PromptItem it = prompt_at<STREAMS>(p, all, index);
             int tokens;
             const Seen sees = stream_sees<STREAMS>(p, it, x, tokens), seen(p, it.pos, it.pos + it.tokens - 1);
