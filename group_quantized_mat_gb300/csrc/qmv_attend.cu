@@ -44,7 +44,7 @@ struct AttendParams {
     int64_t ld_q, ld_out, page_stride, token_stride, head_stride;
     unsigned *err;
     // the plan, and the workspace's parts
-    int tokens, rows, units, pieces, slots;
+    int tokens, rows, units, pieces, slots, key_slots, q_sets;
     int p_off, q_off, misc_off;
     int32_t *prefix;
     float2 *meta;
@@ -287,7 +287,7 @@ __device__ __forceinline__ Item item_at(const AttendParams &p, const Sequences &
 // What lies behind the ring, the weights and the queries.
 template <int NC>
 struct FewShared {
-    uint64_t full[16], empty[16], q_full[2], q_empty[2], s_ready[2], p_ready[2], o_done, finished;
+    uint64_t full[16], empty[16], q_full[2], q_empty[2], s_ready[2], p_ready[4], o_done, finished;
     int abort, changed[NC / 16][2];
     uint32_t tmem;
     float top[4][NC], sum[4][NC], ref[NC], use[NC], shift[NC], total[NC];
@@ -296,23 +296,28 @@ struct FewShared {
     int4 seqs[1];           // [B], then the sequences' first items [B + 1]
 };
 
-// A place in the ring and the parity of its lap.
+// A place in a ring of slots [first, end) and the parity of its lap. A ring has one
+// consumer, which takes its slots in order: a wait for a lap's parity is right only when the
+// lap before has landed.
 struct Place {
-    int slot = 0;
+    int first, end, slot;
     uint32_t lap = 0;
-    __device__ __forceinline__ void step(int slots)
+    int issued = 0;  // (by the producer)
+    __device__ __forceinline__ Place(int first, int end) : first(first), end(end), slot(first) {}
+    __device__ __forceinline__ void step()
     {
-        if (++slot == slots) {
-            slot = 0;
+        if (++slot == end) {
+            slot = first;
             lap ^= 1;
         }
     }
+    __device__ __forceinline__ bool full() const { return issued >= end - first; }
 };
 
-__host__ __device__ constexpr int few_threads(int NC) { return NC / 16 * 128 + 64; }
+__host__ __device__ constexpr int few_threads(int NC) { return NC / 16 * 128 + 96; }
 
 template <int D, int NC>
-__global__ void __launch_bounds__(few_threads(NC), NC < 64 ? 2 : 1)
+__global__ void __launch_bounds__(few_threads(NC), D < 256 && NC == 16 ? 2 : 1)
     attend_few(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const AttendParams p)
 {
     constexpr int DB = D / 64, HALVES = D < 128 ? 1 : D / 128;  // blocks of 64 elements; tiles of 128 in V^T's rows
@@ -320,7 +325,7 @@ __global__ void __launch_bounds__(few_threads(NC), NC < 64 ? 2 : 1)
     constexpr int kScores = 2 * NC;  // columns of a leaf's scores, of which there are two
     constexpr int kColumns = 2 * kScores + 2 * NC * HALVES, kAlloc = kColumns <= 128 ? 128 : kColumns <= 256 ? 256 : 512;
     constexpr int kKeyBytes = NC == 16 ? 64 : 128;  // of a key's weights in a block of P
-    constexpr int kThreads = few_threads(NC), kProducer = kThreads / 32 - 2, kTensor = kProducer + 1;
+    constexpr int kThreads = few_threads(NC), kProducer = kThreads / 32 - 3, kTensor = kProducer + 1;
     extern __shared__ uint8_t raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     FewShared<NC> &sh = *reinterpret_cast<FewShared<NC> *>(smem + p.misc_off);
@@ -340,10 +345,11 @@ __global__ void __launch_bounds__(few_threads(NC), NC < 64 ? 2 : 1)
             mbar_init(q_full + 8 * i, 1);
             mbar_init(q_empty + 8 * i, 1);
             mbar_init(s_ready + 8 * i, 1);
-            mbar_init(p_ready + 8 * i, NC / 4);  // a warp's arrival
+            mbar_init(p_ready + 16 * i, NC / 4);  // a warp's arrival
+            mbar_init(p_ready + 16 * i + 8, NC / 4);
         }
         mbar_init(o_done, 1);
-        mbar_init(finished, 1);
+        mbar_init(finished, 2);
         fence_mbar_init();
         sh.abort = 0;
     }
@@ -374,11 +380,11 @@ __global__ void __launch_bounds__(few_threads(NC), NC < 64 ? 2 : 1)
         // ------------------------------------------------------------- producer
         // A leaf's keys, then the values of the leaf before, as the products need them.
         const int per_tile = 128 / p.box, boxes = 2 * per_tile;  // a lane has a box of the leaf's keys
-        Place at;
-        int n = 0, issued = 0;
+        Place keys(0, p.key_slots), values(p.key_slots, p.slots);
+        int n = 0;
         bool ok = true;
-        const auto slot = [&]() {
-            if (issued >= p.slots) ok = wait(empty0 + 8 * at.slot, at.lap ^ 1);
+        const auto slot = [&](Place &at) {
+            if (at.full()) ok = wait(empty0 + 8 * at.slot, at.lap ^ 1);
             ok = __all_sync(0xffffffffu, ok);
             if (ok && lane == 0) mbar_arrive_expect_tx(full0 + 8 * at.slot, kChunk);
             __syncwarp();
@@ -389,22 +395,22 @@ __global__ void __launch_bounds__(few_threads(NC), NC < 64 ? 2 : 1)
         };
         const auto bring_keys = [&](const Boxes &x) {
 #pragma unroll 1
-            for (int i = 0; i < kChunks && slot(); ++i, ++issued, at.step(p.slots)) {
+            for (int i = 0; i < kChunks && slot(keys); ++i, ++keys.issued, keys.step()) {
                 // 128 keys, 64 elements
                 const int box = lane - i / DB * per_tile;
                 if (box >= 0 && box < per_tile)
-                    tma_load_4d(base + at.slot * kChunk + box * p.box * 128, &kmap, 64 * (i % DB), x.place, x.g, x.page, full0 + 8 * at.slot);
+                    tma_load_4d(base + keys.slot * kChunk + box * p.box * 128, &kmap, 64 * (i % DB), x.place, x.g, x.page, full0 + 8 * keys.slot);
             }
         };
         const auto bring_values = [&](const Boxes &x) {
 #pragma unroll 1
-            for (int i = 0; i < kChunks && slot(); ++i, ++issued, at.step(p.slots)) {
+            for (int i = 0; i < kChunks && slot(values); ++i, ++values.issued, values.step()) {
                 // 64 keys, twice 64 elements (128 keys, 64 elements of head_dim 64)
                 const int few = D == 64 ? per_tile : per_tile / 2, box = lane - i / HALVES * few;
                 if (box >= 0 && box < few)
                     for (int d = 0; d < (D == 64 ? 1 : 2); ++d)
-                        tma_load_4d(base + at.slot * kChunk + d * 8192 + box * p.box * 128, &vmap, 128 * (i % HALVES) + 64 * d, x.place, x.g, x.page,
-                                    full0 + 8 * at.slot);
+                        tma_load_4d(base + values.slot * kChunk + d * 8192 + box * p.box * 128, &vmap, 128 * (i % HALVES) + 64 * d, x.place, x.g, x.page,
+                                    full0 + 8 * values.slot);
             }
         };
         Boxes before{-1, 0, 0};
@@ -415,13 +421,13 @@ __global__ void __launch_bounds__(few_threads(NC), NC < 64 ? 2 : 1)
             if (it.leaves == 0) continue;  // (no queries are brought for an item without keys)
             const Seen seen(p, it.pos, it.pos + it.tokens - 1);
             const int32_t *table = p.table + int64_t(it.b) * p.max_pages;
-            const uint32_t set = 8 * (n & 1);
-            ok = __all_sync(0xffffffffu, n < 2 || wait(q_empty + set, (n / 2 - 1) & 1));
+            const int set = n % p.q_sets;
+            ok = __all_sync(0xffffffffu, n < p.q_sets || wait(q_empty + 8 * set, (n / p.q_sets - 1) & 1));
             if (!ok) break;
             if (lane == 0) {
-                mbar_arrive_expect_tx(q_full + set, uint32_t(p.rows) * D * 2);
+                mbar_arrive_expect_tx(q_full + 8 * set, uint32_t(p.rows) * D * 2);
                 for (int c = 0; c < DB; ++c)
-                    tile::tma_load_3d(Q + ((n & 1) * DB + c) * NC * 128, &qmap, 64 * c, it.g * p.group, it.row, q_full + set);
+                    tile::tma_load_3d(Q + (set * DB + c) * NC * 128, &qmap, 64 * c, it.g * p.group, it.row, q_full + 8 * set);
             }
             ++n;
 #pragma unroll 1
@@ -444,34 +450,40 @@ __global__ void __launch_bounds__(few_threads(NC), NC < 64 ? 2 : 1)
         if (!ok) {
             // copies in flight have to land before the block ends
 #pragma unroll 1
-            for (int i = max(issued - p.slots, 0); i < issued; ++i) mbar_wait_bounded(full0 + 8 * (i % p.slots), (i / p.slots) & 1);
+            for (int ring = 0; ring < 2; ++ring) {
+                const Place &at = ring ? values : keys;
+                const int slots = at.end - at.first;
 #pragma unroll 1
-            for (int i = max(n - 2, 0); i < n; ++i) mbar_wait_bounded(q_full + 8 * (i & 1), (i / 2) & 1);
+                for (int i = max(at.issued - slots, 0); i < at.issued; ++i) mbar_wait_bounded(full0 + 8 * (at.first + i % slots), (i / slots) & 1);
+            }
+#pragma unroll 1
+            for (int i = max(n - p.q_sets, 0); i < n; ++i) mbar_wait_bounded(q_full + 8 * (i % p.q_sets), (i / p.q_sets) & 1);
         }
-    } else if (warp == kTensor) {
-        // ---------------------------------------------------------- tensor warp
-        // The scores of a leaf, then the sums of the leaf before, whose weights were
-        // formed meanwhile.
+    } else if (warp >= kTensor) {
+        // --------------------------------------------------------- tensor warps
+        // One for the scores, which run a leaf ahead, one for the sums: a wait for a
+        // barrier takes some 300 cycles while products keep shared memory busy, and the tensor
+        // cores' queue is short, so that one warp's waits leave them idle.
+        const bool first_warp = warp == kTensor;
         constexpr uint32_t kScoreKind = mma_kind(NC, false, false), kValueKind = mma_kind(2 * NC, true, true);
         // (head_dim 64: the tile's second 64 rows repeat the first, and are not read)
         const uint64_t keys0 = descriptor(base, 16, 1024, 2), queries = descriptor(Q, 16, 1024, 2);
         const uint64_t values0 = descriptor(base, D == 64 ? 0 : 8192, 1024, 2);
         const uint64_t weights = NC == 16 ? descriptor(P, 16, 512, 4) : descriptor(P, kLeaf * 128, 1024, 2);
-        Place at;
+        Place at(first_warp ? 0 : p.key_slots, first_warp ? p.key_slots : p.slots);
         int n = 0, leaf = 0;
-        bool fresh = false;  // the leaf before is an item's first
         const auto sums = [&](int leaf, bool fresh) {
 #pragma unroll 1
-            for (int i = 0; i < kChunks; ++i, at.step(p.slots)) {
+            for (int i = 0; i < kChunks; ++i, at.step()) {
                 if (i % DB == 0) {
-                    wait(p_ready + 8 * (i / DB), leaf & 1);
+                    wait(p_ready + 16 * (leaf & 1) + 8 * (i / DB), (leaf / 2) & 1);
                     tmem_fence_after();
                 }
                 wait(full0 + 8 * at.slot, at.lap);
                 constexpr int kKeys = D == 64 ? 128 : 64;
                 const int c = i % HALVES, key = i / HALVES * kKeys;
-                const uint64_t a = values0 + uint32_t(at.slot * (kChunk >> 4)), b = weights + uint32_t(key * (kKeyBytes >> 4));
                 if (one_lane()) {
+                    const uint64_t a = values0 + uint32_t(at.slot * (kChunk >> 4)), b = weights + uint32_t(key * (kKeyBytes >> 4));
 #pragma unroll
                     for (int k = 0; k < kKeys / 16; ++k)
                         mma_ss(kValueKind, O + c * 2 * NC, a + k * (2048 >> 4), b + k * (16 * kKeyBytes >> 4), !fresh || key + k > 0);
@@ -485,34 +497,40 @@ __global__ void __launch_bounds__(few_threads(NC), NC < 64 ? 2 : 1)
         for (int index = blockIdx.x; index < items; index += gridDim.x) {
             const Item it = item_at(p, all, index);
             if (it.leaves == 0) continue;
-            const int set = n & 1;
-            wait(q_full + 8 * set, (n / 2) & 1);
+            const int set = n % p.q_sets, leaves = it.leaves;
+            if (first_warp) wait(q_full + 8 * set, (n / p.q_sets) & 1);
 #pragma unroll 1
-            for (int l = 0; l < it.leaves; ++l, ++leaf) {
-#pragma unroll 1
-                for (int i = 0; i < kChunks; ++i, at.step(p.slots)) {
-                    wait(full0 + 8 * at.slot, at.lap);
-                    const int c = i % DB;
-                    const uint32_t d = S + (leaf & 1) * kScores + i / DB * NC;
-                    const uint64_t a = keys0 + uint32_t(at.slot * (kChunk >> 4)), b = queries + uint32_t((set * DB + c) * NC * (128 >> 4));
-                    if (one_lane()) {
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) mma_ss(kScoreKind, d, a + 2 * k, b + 2 * k, c + k > 0);
-                        tmem_commit(empty0 + 8 * at.slot);
-                        if (i == kChunks - 1) {
-                            tmem_commit(s_ready + 8 * (leaf & 1));
-                            if (l == it.leaves - 1) tmem_commit(q_empty + 8 * set);
-                        }
+            for (int l = 0; l < leaves; ++l, ++leaf) {
+                if (first_warp) {
+                    if (leaf >= 2) {
+                        wait(p_ready + 16 * (leaf & 1) + 8, (leaf / 2 - 1) & 1);  // (its scores of before have been read)
+                        tmem_fence_after();
                     }
-                    __syncwarp();
+#pragma unroll 1
+                    for (int i = 0; i < kChunks; ++i, at.step()) {
+                        wait(full0 + 8 * at.slot, at.lap);
+                        const int c = i % DB;
+                        if (one_lane()) {
+                            const uint32_t d = S + (leaf & 1) * kScores + i / DB * NC;
+                            const uint64_t a = keys0 + uint32_t(at.slot * (kChunk >> 4)), b = queries + uint32_t((set * DB + c) * NC * (128 >> 4));
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) mma_ss(kScoreKind, d, a + 2 * k, b + 2 * k, c + k > 0);
+                            tmem_commit(empty0 + 8 * at.slot);
+                            if (i == kChunks - 1) {
+                                tmem_commit(s_ready + 8 * (leaf & 1));
+                                if (l == leaves - 1) tmem_commit(q_empty + 8 * set);
+                            }
+                        }
+                        __syncwarp();
+                    }
+                } else {
+                    sums(leaf, l == 0);
                 }
-                if (leaf > 0) sums(leaf - 1, fresh);
-                fresh = l == 0;
             }
             ++n;
         }
-        if (leaf > 0) sums(leaf - 1, fresh);
         if (one_lane()) tmem_commit(finished);
+        __syncwarp();
         mbar_wait_bounded(finished, 0);
     } else {
         // ---------------------------------------------------------------- weights
@@ -642,23 +660,17 @@ __global__ void __launch_bounds__(few_threads(NC), NC < 64 ? 2 : 1)
                                    make_uint4(lo[4 * i], lo[4 * i + 1], lo[4 * i + 2], lo[4 * i + 3]));
                     }
                     // Values of keys that no column sees may be anything, and 0 x NaN is NaN: zeros
-                    // in their place, once the tile's values have landed. A wait for a slot's lap is
-                    // right only when the lap before has landed and while the lap itself is
-                    // not consumed: what is before the first tile's values in the ring has
-                    // landed with the scores of the leaf behind, what is before the second's
-                    // with the first's. (A tile's values fit in the ring at once, and nothing
-                    // else has to be done for them to land but the products of the tile before.)
+                    // in their place, once the tile's values have landed. (A wait for a slot's lap is
+                    // right only when the lap before has landed and while the lap itself is not
+                    // consumed: the leaf before's values have been used, the second tile's
+                    // come after the first's. A tile's values fit in the ring at once.)
                     const bool there = h ? there1 : there0;
                     if (group == 0 && !__all_sync(0xffffffffu, there0 && there1)) {
-                        bool more = l + 1 < it.leaves;
-#pragma unroll 1
-                        for (int j = index + gridDim.x; !more && j < items; j += gridDim.x) more = item_at(p, all, j).leaves > 0;
-                        if (more) wait(s_ready + 8 * ((leaf + 1) & 1), ((leaf + 1) / 2) & 1);
-                        const int from = (2 * leaf + 1 + more) * kChunks + h * DB;
+                        const int from = leaf * kChunks + h * DB, slots = p.slots - p.key_slots;
 #pragma unroll 1
                         for (int c = 0; c < DB; ++c) {
-                            const int slot = (from + c) % p.slots;
-                            wait(full0 + 8 * slot, ((from + c) / p.slots) & 1);
+                            const int slot = p.key_slots + (from + c) % slots;
+                            wait(full0 + 8 * slot, ((from + c) / slots) & 1);
                             // does the chunk hold 64 elements (of head_dim 64) or 128 of the thread's key?
                             if (there || (D > 64 && c / HALVES != mine / 64)) continue;
                             const uint32_t at = base + slot * kChunk + (D == 64 ? mine : mine & 63) * 128;
@@ -669,7 +681,7 @@ __global__ void __launch_bounds__(few_threads(NC), NC < 64 ? 2 : 1)
                     tmem_fence_before();
                     fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(p_ready + 8 * h);
+                    if (lane == 0) mbar_arrive(p_ready + 16 * (leaf & 1) + 8 * h);
                 }
             }
             // ------------------------------------------------ what the item gives
@@ -908,7 +920,14 @@ struct PromptShared {
     int4 seqs[1];  // [B], then the sequences' first items [B + 1]
 };
 
-__host__ __device__ constexpr int prompt_threads(int D) { return (D == 256 ? 128 : 256) + 64; }
+// Hardware barriers: at 1 and 2 the 128 threads of a stream arrive, whose weights are
+// there, and the tensor warp that issues waits for them; at 3 that warp and the one that
+// watches the ring meet. (Each barrier has one number of threads for good: one whose
+// number changed from tile to tile would take a warp that is a tile ahead for one of the tile before.)
+constexpr int kMeetWeights = 160, kMeetRing = 64;
+__device__ __forceinline__ void named_arrive(int id, int threads) { asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
+
+__host__ __device__ constexpr int prompt_threads(int D) { return (D == 256 ? 128 : 256) + 96; }
 
 // D (128 x N fp32) (+)= A (128 x 16, tensor memory) B^T (N x 16, shared memory).
 template <uint32_t KIND>
@@ -927,7 +946,7 @@ __global__ void __launch_bounds__(prompt_threads(D), 1)
 {
     constexpr int STREAMS = D == 256 ? 1 : 2, W = D < 128 ? D : 128;  // elements of a chunk
     constexpr int DB = D / 64, WB = W / 64, CH = D / W, kBytes = 128 * W * 2;
-    constexpr int kThreads = prompt_threads(D), kProducer = kThreads / 32 - 2, kTensor = kProducer + 1;
+    constexpr int kThreads = prompt_threads(D), kProducer = kThreads / 32 - 3, kTensor = kProducer + 1;
     extern __shared__ uint8_t raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     PromptShared &sh = *reinterpret_cast<PromptShared *>(smem + p.misc_off);
@@ -945,7 +964,7 @@ __global__ void __launch_bounds__(prompt_threads(D), 1)
         mbar_init(q_full, 1);
         mbar_init(q_empty, 1);
         mbar_init(edge, 1);
-        mbar_init(finished, 1);
+        mbar_init(finished, 2);
         for (int x = 0; x < 2; ++x) {
             mbar_init(s_ready + 8 * x, 1);
             mbar_init(p_ready + 8 * x, 4);
@@ -985,13 +1004,13 @@ __global__ void __launch_bounds__(prompt_threads(D), 1)
         // The first tile's keys; then each tile's values, before them (head_dim 256) or
         // after them the next tile's keys, as the products need them.
         const int per_tile = 128 / p.box, box = lane % per_tile, block = lane / per_tile;
-        Place at;
-        int n = 0, issued = 0, edges = 0;
+        Place first_ring(0, STREAMS == 1 ? p.key_slots : p.slots), second_ring(p.key_slots, p.slots);
+        int n = 0, edges = 0;
         bool ok = true;
         // a chunk: 128 keys, W elements from c W on; `rows` of them are kept (values behind a
         // sequence's keys may be anything, and 0 x NaN is NaN: zeros in their place)
-        const auto bring = [&](const CUtensorMap *map, const PromptItem &it, int page, int place, int c, int rows) {
-            if (issued >= p.slots) ok = wait(empty0 + 8 * at.slot, at.lap ^ 1);
+        const auto bring = [&](Place &at, const CUtensorMap *map, const PromptItem &it, int page, int place, int c, int rows) {
+            if (at.full()) ok = wait(empty0 + 8 * at.slot, at.lap ^ 1);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) return;
             const uint32_t full = full0 + 8 * at.slot, bar = rows < 128 ? edge : full, dst = base + at.slot * kBytes;
@@ -1008,8 +1027,8 @@ __global__ void __launch_bounds__(prompt_threads(D), 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(full);
             }
-            ++issued;
-            at.step(p.slots);
+            ++at.issued;
+            at.step();
         };
 #pragma unroll 1
         for (int round = 0, index; ok && (index = item_of(round)) < items; ++round) {
@@ -1051,9 +1070,9 @@ __global__ void __launch_bounds__(prompt_threads(D), 1)
 #pragma unroll 1
                     for (int c = 0; c < CH && ok; ++c) {
                         if (keys)
-                            bring(&kmap, it, page, place, c, 128);
+                            bring(first_ring, &kmap, it, page, place, c, 128);
                         else
-                            bring(&vmap, it, before, before_place, c, before_rows);
+                            bring(STREAMS == 1 ? second_ring : first_ring, &vmap, it, before, before_place, c, before_rows);
                     }
                 }
                 before = page;
@@ -1064,136 +1083,145 @@ __global__ void __launch_bounds__(prompt_threads(D), 1)
         if (!ok) {
             // copies in flight have to land before the block ends (those of an edge have been waited for)
 #pragma unroll 1
-            for (int i = max(issued - p.slots, 0); i < issued; ++i) mbar_wait_bounded(full0 + 8 * (i % p.slots), (i / p.slots) & 1);
+            for (int ring = 0; ring < 2; ++ring) {
+                const Place &at = ring ? second_ring : first_ring;
+                const int slots = at.end - at.first;
+#pragma unroll 1
+                for (int i = max(at.issued - slots, 0); i < at.issued; ++i) mbar_wait_bounded(full0 + 8 * (at.first + i % slots), (i / slots) & 1);
+            }
             if (n > 0) mbar_wait_bounded(q_full, (n - 1) & 1);
         }
-    } else if (warp == kTensor) {
-        // ---------------------------------------------------------- tensor warp
+    } else if (warp >= kTensor) {
+        // --------------------------------------------------------- tensor warps
+        // A wait for a barrier in shared memory takes some 300 cycles while products read
+        // their operands there, and the tensor cores' queue is short: a warp that waits leaves
+        // them idle. So of two streams the first warp issues products and waits at hardware
+        // barriers alone, where the second comes when what the ring brings is there. (With
+        // a warp for each stream their products slow one another down: 2339 us instead of 2003 for six
+        // prompts.) Of one stream a warp issues the scores and one the sums.
+        const int x = warp - kTensor;
+        Place at(STREAMS == 1 && x ? p.key_slots : 0, STREAMS == 1 && !x ? p.key_slots : p.slots);
         constexpr uint32_t kValueKind = mma_kind(W, false, true);
-        const uint32_t score_kind = mma_kind(128, false, false) | (p.scale < 0.0f ? 1u << 13 : 0u);  // (- Q)
+        const uint32_t score_kind = mma_kind(128, false, false) | (p.scale < 0.0f ? 1u << 13 : 0u);  // (of the scale's sign: - Q)
         const uint64_t keys0 = descriptor(base, 16, 1024, 2), queries = descriptor(Q, 16, 1024, 2);
         const uint64_t values0 = descriptor(base, 16384, 1024, 2);
-        Place at;
-        int n = 0, done[2] = {0, 0};  // tiles of a stream (of a buffer of scores) so far
-        // scores of a tile whose keys are in the chunk at `c`, from element 64 b WB on
-        const auto scores = [&](int buffer, int x, const Place &c, int b) {
+        int n = 0, tiles = 0;
+        const auto scores = [&](int buffer, int set, int b, uint32_t bar, uint32_t more) {
+            wait(full0 + 8 * at.slot, at.lap);
             if (one_lane()) {
-                const uint64_t k0 = keys0 + uint32_t(c.slot * (kBytes >> 4)), q0 = queries + uint32_t((x * DB + b * WB) * (16384 >> 4));
+                const uint64_t k0 = keys0 + uint32_t(at.slot * (kBytes >> 4)), q0 = queries + uint32_t((set * DB + b * WB) * (16384 >> 4));
 #pragma unroll
                 for (int k = 0; k < W / 16; ++k)
                     mma_ss(score_kind, S + buffer * 128, q0 + (k / 4) * (16384 >> 4) + 2 * (k & 3), k0 + (k / 4) * (16384 >> 4) + 2 * (k & 3), b + k > 0);
+                tmem_commit(empty0 + 8 * at.slot);
+                if (bar) tmem_commit(bar);
+                if (more) tmem_commit(more);
             }
             __syncwarp();
+            at.step();
         };
-        const auto sums = [&](int buffer, int o, const Place &c, bool add) {
+        const auto sums = [&](int buffer, int o, bool add, uint32_t bar) {
+            wait(full0 + 8 * at.slot, at.lap);
             if (one_lane()) {
-                const uint64_t v0 = values0 + uint32_t(c.slot * (kBytes >> 4));
+                const uint64_t v0 = values0 + uint32_t(at.slot * (kBytes >> 4));
 #pragma unroll
                 for (int k = 0; k < 8; ++k) mma_ts<kValueKind>(O + o, S + buffer * 128 + 8 * k, v0 + k * (2048 >> 4), add || k > 0);
+                tmem_commit(empty0 + 8 * at.slot);
+                if (bar) tmem_commit(bar);
             }
             __syncwarp();
-        };
-        const auto commit = [&](uint32_t bar) {
-            if (one_lane()) tmem_commit(bar);
-            __syncwarp();
+            at.step();
         };
 #pragma unroll 1
         for (int round = 0, index; (index = item_of(round)) < items; ++round) {
             const PromptItem it = prompt_at<STREAMS>(p, all, index);
-            if (it.from == it.to) continue;
-            wait(q_full, n & 1);
-            ++n;
+            const int from = it.from, to = it.to;
+            if (from == to) continue;
             if (STREAMS == 1) {
-                // S(0), S(1), O(0), S(2), O(1), ..
+                if (x == 0) wait(q_full, n & 1);
 #pragma unroll 1
-                for (int i = it.from; i <= it.to; ++i) {
-                    if (i < it.to) {
-                        const int buffer = done[0] & 1;
-#pragma unroll 1
-                        for (int c = 0; c < CH; ++c) {
-                            wait(full0 + 8 * at.slot, at.lap);
-                            scores(buffer, 0, at, c);
-                            commit(empty0 + 8 * at.slot);
-                            at.step(p.slots);
+                for (int i = from; i < to; ++i, ++tiles) {
+                    const int buffer = tiles & 1;
+                    if (x == 0) {
+                        if (tiles >= 2) {
+                            wait(o_done + 8 * buffer, (tiles / 2 - 1) & 1);  // (the buffer's weights of before are used)
+                            tmem_fence_after();
                         }
-                        commit(s_ready + 8 * buffer);
-                        if (i == it.to - 1) commit(q_empty);
-                        ++done[0];
-                    }
-                    if (i > it.from) {
-                        const int tile = done[0] - (i < it.to ? 2 : 1);
-                        wait(p_ready + 8 * (tile & 1), (tile / 2) & 1);
+#pragma unroll 1
+                        for (int c = 0; c < CH; ++c) scores(buffer, 0, c, c == CH - 1 ? s_ready + 8 * buffer : 0u, c == CH - 1 && i == to - 1 ? q_empty : 0u);
+                    } else {
+                        wait(p_ready + 8 * buffer, (tiles / 2) & 1);
                         tmem_fence_after();
 #pragma unroll 1
-                        for (int c = 0; c < CH; ++c) {
-                            wait(full0 + 8 * at.slot, at.lap);
-                            sums(tile & 1, c * W, at, i > it.from + 1);
-                            commit(empty0 + 8 * at.slot);
-                            at.step(p.slots);
-                        }
-                        commit(o_done + 8 * (tile & 1));
+                        for (int c = 0; c < CH; ++c) sums(buffer, c * W, i > from, c == CH - 1 ? o_done + 8 * buffer : 0u);
                     }
                 }
             } else {
                 // S0(0), S1(0), then O0(i), S0(i + 1), O1(i), S1(i + 1); streams that see nothing
                 // of a tile leave it out
                 int tokens;
-                const Seen sees[2] = {stream_sees<STREAMS>(p, it, 0, tokens), stream_sees<STREAMS>(p, it, 1, tokens)};
+                const Seen see0 = stream_sees<STREAMS>(p, it, 0, tokens), see1 = stream_sees<STREAMS>(p, it, 1, tokens);
                 uint32_t active = 0, started = 0;  // streams at work on tile i - 1; with sums of this item
 #pragma unroll 1
-                for (int i = it.from; i <= it.to; ++i) {
+                for (int i = from; i <= to; ++i) {
                     const int key = it.tile(i) * 128;
-                    const uint32_t next = i < it.to ? uint32_t(sees[0].any(key, 128)) | uint32_t(sees[1].any(key, 128)) << 1 : 0u;
-                    Place keys = at;
-                    const uint32_t vslot = at.slot;
-                    if (i > it.from) {
-                        keys.step(p.slots);
-                        wait(full0 + 8 * vslot, at.lap);
+                    const uint32_t next = i < to ? uint32_t(see0.any(key, 128)) | uint32_t(see1.any(key, 128)) << 1 : 0u;
+                    if (x) {
+                        // the values of tile i - 1 and the keys of tile i (the queries)
+                        if (i == from) {
+                            wait(q_full, n & 1);
+                        } else {
+                            wait(full0 + 8 * at.slot, at.lap);
+                            at.step();
+                        }
+                        if (i < to) {
+                            wait(full0 + 8 * at.slot, at.lap);
+                            at.step();
+                        }
                     }
+                    named_sync(3, kMeetRing);
+                    if (!x) {
+                        const uint32_t vslot = at.slot;
+                        if (i > from) at.step();
+                        const uint32_t kslot = at.slot;
+                        if (i < to) at.step();
 #pragma unroll 1
-                    for (int x = 0; x < 2; ++x) {
-                        const bool work = active >> x & 1, more = next >> x & 1;
-                        if (work) {
-                            wait(p_ready + 8 * x, ((x ? done[1] : done[0]) - 1) & 1);
-                            tmem_fence_after();
+                        for (int s = 0; s < 2; ++s) {
+                            const bool last = s == 1;
+                            if (active >> s & 1) {
+                                named_sync(1 + s, kMeetWeights);
+                                tmem_fence_after();
+                            }
                             if (one_lane()) {
-                                const uint64_t v0 = values0 + vslot * (kBytes >> 4);
+                                if (active >> s & 1) {
+                                    const uint64_t v0 = values0 + vslot * (kBytes >> 4);
 #pragma unroll
-                                for (int k = 0; k < 8; ++k)
-                                    mma_ts<kValueKind>(O + x * D, S + x * 128 + 8 * k, v0 + k * (2048 >> 4), k > 0 || (started >> x & 1));
-                                tmem_commit(o_done + 8 * x);
-                                if (x == 1) tmem_commit(empty0 + 8 * vslot);
+                                    for (int k = 0; k < 8; ++k)
+                                        mma_ts<kValueKind>(O + s * D, S + s * 128 + 8 * k, v0 + k * (2048 >> 4), k > 0 || (started >> s & 1));
+                                    tmem_commit(o_done + 8 * s);
+                                }
+                                if (last && i > from) tmem_commit(empty0 + 8 * vslot);
+                                if (next >> s & 1) {
+                                    const uint64_t k0 = keys0 + kslot * (kBytes >> 4), q0 = queries + uint32_t(s * DB * (16384 >> 4));
+#pragma unroll
+                                    for (int k = 0; k < W / 16; ++k)
+                                        mma_ss(score_kind, S + s * 128, q0 + (k / 4) * (16384 >> 4) + 2 * (k & 3), k0 + (k / 4) * (16384 >> 4) + 2 * (k & 3), k > 0);
+                                    tmem_commit(s_ready + 8 * s);
+                                }
+                                if (last && i < to) tmem_commit(empty0 + 8 * kslot);
+                                if (last && i == to - 1) tmem_commit(q_empty);
                             }
                             __syncwarp();
-                        } else if (x == 1 && i > it.from) {
-                            commit(empty0 + 8 * vslot);
                         }
-                        if (x == 0 && i < it.to) wait(full0 + 8 * keys.slot, keys.lap);
-                        if (more) {
-                            if (one_lane()) {
-                                const uint64_t k0 = keys0 + uint32_t(keys.slot * (kBytes >> 4)), q0 = queries + uint32_t(x * DB * (16384 >> 4));
-#pragma unroll
-                                for (int k = 0; k < W / 16; ++k)
-                                    mma_ss(score_kind, S + x * 128, q0 + (k / 4) * (16384 >> 4) + 2 * (k & 3), k0 + (k / 4) * (16384 >> 4) + 2 * (k & 3), k > 0);
-                                tmem_commit(s_ready + 8 * x);
-                                if (x == 1) tmem_commit(empty0 + 8 * keys.slot);
-                            }
-                            __syncwarp();
-                        } else if (x == 1 && i < it.to) {
-                            commit(empty0 + 8 * keys.slot);
-                        }
+                        started |= active;
                     }
-                    started |= active;
-                    done[0] += next & 1;
-                    done[1] += next >> 1;
-                    if (i == it.to - 1) commit(q_empty);
                     active = next;
-                    at = keys;
-                    if (i < it.to) at.step(p.slots);
                 }
             }
+            ++n;
         }
-        commit(finished);
+        if (one_lane()) tmem_commit(finished);
+        __syncwarp();
         mbar_wait_bounded(finished, 0);
     } else {
         // ---------------------------------------------------------------- weights
@@ -1317,8 +1345,12 @@ __global__ void __launch_bounds__(prompt_threads(D), 1)
                 }
                 tmem_wait_st();
                 tmem_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(p_ready + 8 * buffer);
+                if (STREAMS == 1) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(p_ready + 8 * buffer);
+                } else {
+                    named_arrive(1 + x, kMeetWeights);
+                }
                 ++tiles;
                 ++worked;
             }
@@ -1531,7 +1563,7 @@ extern "C" qmv_status qmv_attend_run(const uint16_t *q, const uint16_t *k_cache,
     p.kv_heads = kv_heads;
     p.err = dev.err;
     const FewPlan f = few_plan(B, max_new, heads, kv_heads, head_dim, int64_t(max_pages) * page_size, window, sinks);
-    p.tokens = f.tokens; p.rows = f.rows; p.units = f.units; p.slots = f.slots;
+    p.tokens = f.tokens; p.rows = f.rows; p.units = f.units; p.slots = f.slots; p.key_slots = f.key_slots; p.q_sets = f.q_sets;
     p.p_off = f.p_off; p.q_off = f.q_off; p.misc_off = f.misc_off;
     uint8_t *at = static_cast<uint8_t *>(ws);
     p.prefix = reinterpret_cast<int32_t *>(at + f.prefix_off);
@@ -1556,7 +1588,7 @@ extern "C" qmv_status qmv_attend_run(const uint16_t *q, const uint16_t *k_cache,
                                       : launch_attend<256>(p, m, f, dev.sms, s);
     const PromptPlan g = prompt_plan(B, T, max_new, heads, kv_heads, head_dim, int64_t(max_pages) * page_size, window, sinks);
     if (e == cudaSuccess && g.items > 0) {
-        p.tokens = g.tokens; p.pieces = g.pieces; p.slots = g.slots;
+        p.tokens = g.tokens; p.pieces = g.pieces; p.slots = g.slots; p.key_slots = g.key_slots;
         p.q_off = g.q_off; p.misc_off = g.misc_off;
         p.prefix = reinterpret_cast<int32_t *>(at + g.prefix_off);
         p.meta = reinterpret_cast<float2 *>(at + g.meta_off);

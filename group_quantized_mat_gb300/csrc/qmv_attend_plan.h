@@ -23,7 +23,8 @@ struct FewPlan {
     int tokens;   // new tokens of an item at most
     int blocks;   // items of one kv head and unit
     int rows;     // columns in use: tokens * group
-    int slots, ctas;
+    int slots, key_slots, ctas;  // ring slots, those of keys; blocks of an SM
+    int q_sets;                  // items whose queries are held
     int p_off, q_off, misc_off, smem;
     int units;    // of a sequence at most
     int64_t items;
@@ -36,14 +37,16 @@ inline size_t up256(size_t b) { return (b + 255) & ~size_t(255); }
 // then barriers, maxima, sums and the sequences.
 inline void few_smem(FewPlan &f, int D, int B)
 {
-    const int p_bytes = kLeaf * f.columns * 4, q_bytes = 2 * f.columns * D * 2;
+    f.q_sets = D == 256 && f.columns == 64 ? 1 : 2;
+    const int p_bytes = kLeaf * f.columns * 4, q_bytes = f.q_sets * f.columns * D * 2;
     const int misc = 512 + f.columns * 4 * 18 + B * 16 + (B + 1) * 4;
     const int fixed = p_bytes + q_bytes + ((misc + 1023) & ~1023);
-    const int two = (kSmemSm / 2 - kSmemReserved - 1024 - fixed) / kChunk;
-    // (a tile's values, at most four slots, have to be there at once: see the zeroing of unseen rows)
-    f.ctas = f.columns < 64 && two >= 4 ? 2 : 1;
+    // (a tile's values, D / 64 slots, have to be there at once: see the zeroing of unseen rows)
+    const int least = D / 64 + 2 > 5 ? D / 64 + 2 : 5, two = (kSmemSm / 2 - kSmemReserved - 1024 - fixed) / kChunk;
+    f.ctas = f.columns == 16 && two >= least ? 2 : 1;
     f.slots = f.ctas == 2 ? two : (kSmemBlock - 1024 - fixed) / kChunk;
     if (f.slots > 11) f.slots = 11;
+    f.key_slots = f.slots / 2 < f.slots - D / 64 ? f.slots / 2 : f.slots - D / 64;
     f.p_off = f.slots * kChunk;
     f.q_off = f.p_off + p_bytes;
     f.misc_off = f.q_off + q_bytes;
@@ -55,6 +58,7 @@ inline void few_smem(FewPlan &f, int D, int B)
 struct PromptPlan {
     int tokens;  // of a tile: as many as their heads of one kv head fit 128 rows
     int streams, slots, chunk;
+    int key_slots;  // of one stream, whose keys and values have rings of their own
     int q_off, misc_off, smem;
     int pieces;
     int64_t items;
@@ -71,6 +75,7 @@ inline PromptPlan prompt_plan(int B, int T, int max_new, int heads, int kv_heads
     const int q_bytes = f.streams * 128 * D * 2, misc = (512 + B * 16 + (B + 1) * 4 + 1023) & ~1023;
     f.slots = (kSmemBlock - 1024 - q_bytes - misc) / f.chunk;
     if (f.slots > 8) f.slots = 8;
+    f.key_slots = (f.slots + 1) / 2;
     f.q_off = f.slots * f.chunk;
     f.misc_off = f.q_off + q_bytes;
     f.smem = f.misc_off + misc + 1024;
