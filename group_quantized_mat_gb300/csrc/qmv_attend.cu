@@ -44,7 +44,7 @@ struct AttendParams {
     int64_t ld_q, ld_out, page_stride, token_stride, head_stride;
     unsigned *err;
     // the plan, and the workspace's parts
-    int tokens, rows, units, pieces, slots, key_slots, q_sets;
+    int tokens, rows, units, unit_shift, pieces, slots, key_slots, q_sets;
     int p_off, q_off, misc_off;
     int32_t *prefix;
     float2 *meta;
@@ -197,7 +197,8 @@ __device__ __forceinline__ void tmem_st(uint32_t a, const float (&v)[N])
 // 2 x columns columns of one product, so that the weights' rounding is below that of
 // fp32 sums' order.
 //
-// Order. A work item is a unit of 512 keys, from a multiple of 512 on, in leaves of 256,
+// Order. A work item is a unit of 512 keys (256 where that many make the call's longest
+// sequence at most 152 items), from a multiple of 512 on, in leaves of 256,
 // whose products are added in the order of keys; a column's reference m is a whole
 // number, from the maxima of its leaves so far, so that a change of m scales by powers
 // of two without a rounding. Units are joined by attend_join in an order given by
@@ -218,9 +219,9 @@ struct Units {
     __device__ __forceinline__ Units(const AttendParams &p, const Sequence &s)
     {
         const Seen seen(p, s.pos, s.pos + s.done - 1);
-        low = seen.low / kUnit;
-        sinks = min((seen.sinks + kUnit - 1) / kUnit, low);
-        count = seen.end > 0 ? sinks + (seen.end - 1) / kUnit - low + 1 : 1;
+        low = seen.low >> p.unit_shift;
+        sinks = min((seen.sinks + (1 << p.unit_shift) - 1) >> p.unit_shift, low);
+        count = seen.end > 0 ? sinks + ((seen.end - 1) >> p.unit_shift) - low + 1 : 1;
         count = s.done > 0 && s.done <= kFew ? min(count, p.units) : 0;
     }
     __device__ __forceinline__ int place(int u) const { return u < sinks ? u : low + u - sinks; }
@@ -258,25 +259,30 @@ __device__ __forceinline__ Item item_at(const AttendParams &p, const Sequences &
         const int mid = (lo + hi) / 2;
         (all.first[mid] <= index ? lo : hi) = mid;
     }
-    const Sequence s(p, all.kept[lo]);
+    const int4 kept = all.kept[lo];
+    const Sequence s(p, kept);
     const Units units(p, s);
-    const int blocks = (s.done + p.tokens - 1) / p.tokens;
+    const unsigned blocks = unsigned(kept.w);
     Item it;
     it.b = lo;
     it.index = index;
     index -= all.first[lo];
-    it.block = index % blocks;
-    index /= blocks;
-    it.g = index % p.kv_heads;
-    it.unit = units.place(index / p.kv_heads);
+    it.block = 0;
+    if (blocks > 1) {
+        it.block = int(unsigned(index) % blocks);
+        index = int(unsigned(index) / blocks);
+    }
+    const int u = int(unsigned(index) / unsigned(p.kv_heads));
+    it.g = index - u * p.kv_heads;
+    it.unit = units.place(u);
     it.row = s.row + it.block * p.tokens;
     it.tokens = min(p.tokens, s.done - it.block * p.tokens);
     it.rows = it.tokens * p.group;
     it.pos = s.pos + it.block * p.tokens;
     it.whole = units.count == 1;
     const Seen seen(p, it.pos, it.pos + it.tokens - 1);
-    int from = it.unit * kUnit;
-    int to = min(from + kUnit, seen.end);
+    int from = it.unit << p.unit_shift;
+    int to = min(from + (1 << p.unit_shift), seen.end);
     if (to <= seen.low) to = min(to, seen.sinks);
     if (from >= seen.sinks) from = max(from, seen.low);  // (sinks <= low)
     it.leaf = from / kLeaf;
@@ -314,7 +320,7 @@ struct Place {
     __device__ __forceinline__ bool full() const { return issued >= end - first; }
 };
 
-__host__ __device__ constexpr int few_threads(int NC) { return NC / 16 * 128 + 96; }
+__host__ __device__ constexpr int few_threads(int NC) { return NC / 16 * 128 + 128; }
 
 template <int D, int NC>
 __global__ void __launch_bounds__(few_threads(NC), D < 256 && NC == 16 ? 2 : 1)
@@ -325,7 +331,7 @@ __global__ void __launch_bounds__(few_threads(NC), D < 256 && NC == 16 ? 2 : 1)
     constexpr int kScores = 2 * NC;  // columns of a leaf's scores, of which there are two
     constexpr int kColumns = 2 * kScores + 2 * NC * HALVES, kAlloc = kColumns <= 128 ? 128 : kColumns <= 256 ? 256 : 512;
     constexpr int kKeyBytes = NC == 16 ? 64 : 128;  // of a key's weights in a block of P
-    constexpr int kThreads = few_threads(NC), kProducer = kThreads / 32 - 3, kTensor = kProducer + 1;
+    constexpr int kThreads = few_threads(NC), kProducer = kThreads / 32 - 4, kTensor = kProducer + 2;
     extern __shared__ uint8_t raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     FewShared<NC> &sh = *reinterpret_cast<FewShared<NC> *>(smem + p.misc_off);
@@ -360,8 +366,9 @@ __global__ void __launch_bounds__(few_threads(NC), D < 256 && NC == 16 ? 2 : 1)
 #pragma unroll 1
     for (int b = tid; b < p.B; b += kThreads) {
         const Sequence s(p, b);
-        sh.seqs[b] = make_int4(s.row, s.n, s.keys, 0);
-        first[b + 1] = Units(p, s).count * ((s.done + p.tokens - 1) / p.tokens) * p.kv_heads;
+        const int blocks = (s.done + p.tokens - 1) / p.tokens;
+        sh.seqs[b] = make_int4(s.row, s.n, s.keys, blocks);
+        first[b + 1] = Units(p, s).count * blocks * p.kv_heads;
     }
     tmem_fence_before();
     __syncthreads();
@@ -376,86 +383,66 @@ __global__ void __launch_bounds__(few_threads(NC), D < 256 && NC == 16 ? 2 : 1)
     const int items = first[p.B];
     const Waits wait{&sh.abort, p.err};
 
-    if (warp == kProducer) {
-        // ------------------------------------------------------------- producer
-        // A leaf's keys, then the values of the leaf before, as the products need them.
+    if (warp >= kProducer && warp < kTensor) {
+        // ------------------------------------------------------------ producers
+        // One brings keys (and queries), one values: neither ring waits for the other.
+        const bool values = warp > kProducer;
+        const CUtensorMap *map = values ? &vmap : &kmap;
         const int per_tile = 128 / p.box, boxes = 2 * per_tile;  // a lane has a box of the leaf's keys
-        Place keys(0, p.key_slots), values(p.key_slots, p.slots);
+        Place at(values ? p.key_slots : 0, values ? p.slots : p.key_slots);
         int n = 0;
         bool ok = true;
-        const auto slot = [&](Place &at) {
-            if (at.full()) ok = wait(empty0 + 8 * at.slot, at.lap ^ 1);
-            ok = __all_sync(0xffffffffu, ok);
-            if (ok && lane == 0) mbar_arrive_expect_tx(full0 + 8 * at.slot, kChunk);
-            __syncwarp();
-            return ok;
-        };
-        struct Boxes {
-            int page, place, g;
-        };
-        const auto bring_keys = [&](const Boxes &x) {
-#pragma unroll 1
-            for (int i = 0; i < kChunks && slot(keys); ++i, ++keys.issued, keys.step()) {
-                // 128 keys, 64 elements
-                const int box = lane - i / DB * per_tile;
-                if (box >= 0 && box < per_tile)
-                    tma_load_4d(base + keys.slot * kChunk + box * p.box * 128, &kmap, 64 * (i % DB), x.place, x.g, x.page, full0 + 8 * keys.slot);
-            }
-        };
-        const auto bring_values = [&](const Boxes &x) {
-#pragma unroll 1
-            for (int i = 0; i < kChunks && slot(values); ++i, ++values.issued, values.step()) {
-                // 64 keys, twice 64 elements (128 keys, 64 elements of head_dim 64)
-                const int few = D == 64 ? per_tile : per_tile / 2, box = lane - i / HALVES * few;
-                if (box >= 0 && box < few)
-                    for (int d = 0; d < (D == 64 ? 1 : 2); ++d)
-                        tma_load_4d(base + values.slot * kChunk + d * 8192 + box * p.box * 128, &vmap, 128 * (i % HALVES) + 64 * d, x.place, x.g, x.page,
-                                    full0 + 8 * values.slot);
-            }
-        };
-        Boxes before{-1, 0, 0};
-        bool any = false;
 #pragma unroll 1
         for (int index = blockIdx.x; index < items && ok; index += gridDim.x) {
             const Item it = item_at(p, all, index);
             if (it.leaves == 0) continue;  // (no queries are brought for an item without keys)
             const Seen seen(p, it.pos, it.pos + it.tokens - 1);
             const int32_t *table = p.table + int64_t(it.b) * p.max_pages;
-            const int set = n % p.q_sets;
-            ok = __all_sync(0xffffffffu, n < p.q_sets || wait(q_empty + 8 * set, (n / p.q_sets - 1) & 1));
-            if (!ok) break;
-            if (lane == 0) {
-                mbar_arrive_expect_tx(q_full + 8 * set, uint32_t(p.rows) * D * 2);
-                for (int c = 0; c < DB; ++c)
-                    tile::tma_load_3d(Q + (set * DB + c) * NC * 128, &qmap, 64 * c, it.g * p.group, it.row, q_full + 8 * set);
-            }
-            ++n;
-#pragma unroll 1
-            for (int leaf = it.leaf; leaf < it.leaf + it.leaves && ok; ++leaf) {
+            const int leaves = it.leaf + it.leaves, g = it.g;
+            for (int leaf = it.leaf; leaf < leaves && ok; ++leaf) {
                 const int key = leaf * kLeaf + lane * p.box;
-                Boxes x{-1, 0, it.g};
+                int page = -1, place = 0;
                 if (lane < boxes && seen.any(key, p.box)) {
-                    x.page = page_of(p, key);
-                    x.place = key - x.page * p.page_size;
-                    x.page = __ldg(table + x.page);
+                    page = page_of(p, key);
+                    place = key - page * p.page_size;
+                    page = __ldg(table + page);
                 }
-                if (unsigned(x.page) >= unsigned(p.pages)) x.page = p.pages;  // outside the map: zeros
-                bring_keys(x);
-                if (any && ok) bring_values(before);
-                any = true;
-                before = x;
+                if (!values && leaf == it.leaf) {
+                    const int set = n % p.q_sets;
+                    ok = __all_sync(0xffffffffu, n < p.q_sets || wait(q_empty + 8 * set, (n / p.q_sets - 1) & 1));
+                    if (!ok) break;
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(q_full + 8 * set, uint32_t(p.rows) * D * 2);
+                        for (int c = 0; c < DB; ++c)
+                            tile::tma_load_3d(Q + (set * DB + c) * NC * 128, &qmap, 64 * c, g * p.group, it.row, q_full + 8 * set);
+                    }
+                    ++n;
+                }
+                if (unsigned(page) >= unsigned(p.pages)) page = p.pages;  // outside the map: zeros
+#pragma unroll 1
+                for (int i = 0; i < kChunks; ++i, ++at.issued, at.step()) {
+                    if (at.full()) ok = wait(empty0 + 8 * at.slot, at.lap ^ 1);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    const uint32_t full = full0 + 8 * at.slot, dst = base + at.slot * kChunk;
+                    if (lane == 0) mbar_arrive_expect_tx(full, kChunk);
+                    __syncwarp();
+                    // keys: 128, 64 elements; values: 64, twice 64 elements (128, 64 elements of head_dim 64)
+                    const bool pairs = values && D > 64;
+                    const int few = pairs ? per_tile / 2 : per_tile, column = pairs ? i % HALVES * 128 : i % DB * 64;
+                    const int box = lane - (pairs ? i / HALVES : i / DB) * few;
+                    if (box >= 0 && box < few) {
+                        tma_load_4d(dst + box * p.box * 128, map, column, place, g, page, full);
+                        if (pairs) tma_load_4d(dst + 8192 + box * p.box * 128, map, column + 64, place, g, page, full);
+                    }
+                }
             }
         }
-        if (any && ok) bring_values(before);
         if (!ok) {
             // copies in flight have to land before the block ends
+            const int slots = at.end - at.first;
 #pragma unroll 1
-            for (int ring = 0; ring < 2; ++ring) {
-                const Place &at = ring ? values : keys;
-                const int slots = at.end - at.first;
-#pragma unroll 1
-                for (int i = max(at.issued - slots, 0); i < at.issued; ++i) mbar_wait_bounded(full0 + 8 * (at.first + i % slots), (i / slots) & 1);
-            }
+            for (int i = max(at.issued - slots, 0); i < at.issued; ++i) mbar_wait_bounded(full0 + 8 * (at.first + i % slots), (i / slots) & 1);
 #pragma unroll 1
             for (int i = max(n - p.q_sets, 0); i < n; ++i) mbar_wait_bounded(q_full + 8 * (i % p.q_sets), (i / p.q_sets) & 1);
         }
@@ -542,6 +529,7 @@ __global__ void __launch_bounds__(few_threads(NC), D < 256 && NC == 16 ? 2 : 1)
         const int group = warp / 4, c0 = 16 * group, quarter = warp & 3, mine = tid & 127, meet = 1 + group;
         const uint32_t lanes = uint32_t(quarter * 32) << 16;
         const float c2 = __fmul_rn(p.scale, 1.4426950408889634f);
+        const int column = c0 + (mine & 15), token = column / p.group, head = column - token * p.group;  // of the first 16 threads
         int leaf = 0;
 #pragma unroll 1
         for (int index = blockIdx.x; index < items; index += gridDim.x) {
@@ -549,11 +537,11 @@ __global__ void __launch_bounds__(few_threads(NC), D < 256 && NC == 16 ? 2 : 1)
             const Seen seen(p, it.pos, it.pos + it.tokens - 1);
             const int32_t *table = p.table + int64_t(it.b) * p.max_pages;
             if (mine < 16) {
-                const int r = c0 + mine, pos = it.pos + r / p.group;
+                const int r = column, pos = it.pos + token;
                 sh.ref[r] = -INFINITY;
                 sh.last[r] = r < it.rows ? pos : -1;
                 sh.low[r] = p.window ? pos - p.window + 1 : 0;
-                sh.out[r] = it.whole ? (it.row + r / p.group) * p.ld_out + (it.g * p.group + r % p.group) * D : (int64_t(it.index) * p.rows + r) * D;
+                sh.out[r] = it.whole ? (it.row + token) * p.ld_out + (it.g * p.group + head) * D : (int64_t(it.index) * p.rows + r) * D;
             }
             float sum[16];
 #pragma unroll
@@ -692,11 +680,10 @@ __global__ void __launch_bounds__(few_threads(NC), D < 256 && NC == 16 ? 2 : 1)
                 const int r = c0 + mine;
                 const float t = __fadd_rn(__fadd_rn(sh.sum[0][r], sh.sum[1][r]), __fadd_rn(sh.sum[2][r], sh.sum[3][r]));
                 if (it.whole) {
-                    const int row = it.row + r / p.group, head = it.g * p.group + r % p.group;
                     const bool none = sh.ref[r] == -INFINITY;
                     sh.total[r] = none ? 0.0f : __fdiv_rn(1.0f, t);
                     if (p.lse)
-                        p.lse[int64_t(row) * p.heads + head] = none ? -INFINITY : __fmul_rn(0.6931471805599453f, __fadd_rn(sh.ref[r], log2f(t)));
+                        p.lse[int64_t(it.row + token) * p.heads + it.g * p.group + head] = none ? -INFINITY : __fmul_rn(0.6931471805599453f, __fadd_rn(sh.ref[r], log2f(t)));
                 } else {
                     p.meta[int64_t(it.index) * p.rows + r] = make_float2(sh.ref[r], t);
                 }
@@ -1563,7 +1550,7 @@ extern "C" qmv_status qmv_attend_run(const uint16_t *q, const uint16_t *k_cache,
     p.kv_heads = kv_heads;
     p.err = dev.err;
     const FewPlan f = few_plan(B, max_new, heads, kv_heads, head_dim, int64_t(max_pages) * page_size, window, sinks);
-    p.tokens = f.tokens; p.rows = f.rows; p.units = f.units; p.slots = f.slots; p.key_slots = f.key_slots; p.q_sets = f.q_sets;
+    p.tokens = f.tokens; p.rows = f.rows; p.units = f.units; p.unit_shift = f.unit == kLeaf ? 8 : 9; p.slots = f.slots; p.key_slots = f.key_slots; p.q_sets = f.q_sets;
     p.p_off = f.p_off; p.q_off = f.q_off; p.misc_off = f.misc_off;
     uint8_t *at = static_cast<uint8_t *>(ws);
     p.prefix = reinterpret_cast<int32_t *>(at + f.prefix_off);

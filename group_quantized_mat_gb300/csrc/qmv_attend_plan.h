@@ -12,7 +12,6 @@ namespace attend {
 
 constexpr int kFew = QMV_TILE_M;  // new tokens of a sequence up to which they share one read of its keys
 constexpr int kLeaf = 256;        // keys whose weights are formed at once: two tiles of 128
-constexpr int kUnit = 512;        // keys of one work item, from a multiple of 512 on
 constexpr int kChunk = 16384;     // bytes of a ring slot
 constexpr int kSmemSm = 228 * 1024, kSmemBlock = 227 * 1024, kSmemReserved = 1024;
 
@@ -26,6 +25,7 @@ struct FewPlan {
     int slots, key_slots, ctas;  // ring slots, those of keys; blocks of an SM
     int q_sets;                  // items whose queries are held
     int p_off, q_off, misc_off, smem;
+    int unit;     // keys of one item, from a multiple of it on
     int units;    // of a sequence at most
     int64_t items;
     size_t prefix_off, meta_off, parts_off, workspace;
@@ -107,10 +107,15 @@ inline FewPlan few_plan(int B, int max_new, int heads, int kv_heads, int D, int6
     f.blocks = (most + f.tokens - 1) / f.tokens;
     f.rows = f.tokens * group;
     few_smem(f, D, B);
-    int64_t units = (capacity + kUnit - 1) / kUnit;
+    // An item is two leaves; one leaf where that makes a sequence no more items than a card has
+    // SMs. By the longest sequence that the call has room for, not by how long they are
+    // nor by how many there are, so that a row's sums keep their order from call to call.
+    const int64_t sees = window && int64_t(window) + sinks + most < capacity ? int64_t(window) + sinks + most : capacity;
+    f.unit = (sees + kLeaf - 1) / kLeaf * kv_heads <= 152 ? kLeaf : 2 * kLeaf;
+    int64_t units = (capacity + f.unit - 1) / f.unit;
     if (window) {
         // the units of window + most - 1 keys, and those of the first tokens
-        const int64_t near = (int64_t(window) + most - 1 + kUnit - 2) / kUnit + 1, first = (int64_t(sinks) + kUnit - 1) / kUnit;
+        const int64_t near = (int64_t(window) + most - 1 + f.unit - 2) / f.unit + 1, first = (int64_t(sinks) + f.unit - 1) / f.unit;
         if (near + first < units) units = near + first;
     }
     f.units = int(units);
