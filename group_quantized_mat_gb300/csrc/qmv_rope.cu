@@ -8,11 +8,10 @@
 // nothing, and no 64-bit floating point is in the loop (152 SMs do it at two
 // operations a cycle).
 //
-// A row (one head of one token) belongs to head_dim / 8 lanes of a warp, 16 bytes of
-// bf16 each; its sum of squares joins by shuffles, and a pair's other element comes
-// from the lane that holds it. A block takes tokens in turn: it computes the
-// token's sines and cosines once, for all of its heads, while the rows' loads are in
-// flight. It is bound by memory from a few hundred tokens on; below that by the
+// A row (one head of one token) belongs to head_dim / 8 lanes of a warp, each with both
+// elements of four pairs; its sum of squares joins by shuffles. A block takes tokens in
+// turn: it computes the token's sines and cosines once, for all of its heads, while the
+// next token's loads are in flight. It is bound by memory from a few hundred tokens on; below that by the
 // latency of a launch, two loads and a store.
 //
 // A thread has four rows of a token in flight, or one where the tokens alone do not
@@ -28,7 +27,7 @@
 namespace qmv {
 namespace {
 
-constexpr int kRopeThreads = 256;
+constexpr int kRopeThreads = 256, kRopeBlocks = 3;  // blocks of an SM
 
 struct RopeParams {
     const void *qkv;
@@ -46,108 +45,119 @@ struct RopeParams {
     int neighbours;
 };
 
-__device__ __forceinline__ void widen(const uint4 &v, float (&x)[8])
+__device__ __forceinline__ void widen(const uint2 &v, float *x)
 {
-    const uint32_t in[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        x[2 * i] = __uint_as_float(in[i] << 16);
-        x[2 * i + 1] = __uint_as_float(in[i] & 0xffff0000u);
-    }
+    x[0] = __uint_as_float(v.x << 16);
+    x[1] = __uint_as_float(v.x & 0xffff0000u);
+    x[2] = __uint_as_float(v.y << 16);
+    x[3] = __uint_as_float(v.y & 0xffff0000u);
 }
 
-__device__ __forceinline__ uint4 narrow(const float (&x)[8])
+__device__ __forceinline__ uint2 narrow(const float *x)
 {
-    uint32_t r[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-        r[i] = *reinterpret_cast<const uint32_t *>(&h);
-    }
-    return make_uint4(r[0], r[1], r[2], r[3]);
+    const __nv_bfloat162 a = __floats2bfloat162_rn(x[0], x[1]), b = __floats2bfloat162_rn(x[2], x[3]);
+    return make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
 }
 
-// Eight elements as they lie in memory.
+// A lane's eight elements as they lie in memory: four from `e0` on, four from `e1` on.
 template <bool F32>
 struct Octet {
-    uint4 v[F32 ? 2 : 1];
-    __device__ __forceinline__ void load(const void *base, int64_t element)
+    uint2 v[F32 ? 4 : 2];
+    __device__ __forceinline__ void load(const void *base, int64_t row, int e0, int e1)
     {
-        const uint8_t *at = static_cast<const uint8_t *>(base) + element * (F32 ? 4 : 2);
         // (read once: not kept in L1)
-#pragma unroll
-        for (int i = 0; i < (F32 ? 2 : 1); ++i) v[i] = __ldcs(reinterpret_cast<const uint4 *>(at) + i);
+        if constexpr (F32) {
+            const float *at = static_cast<const float *>(base) + row;
+            const uint4 a = __ldcs(reinterpret_cast<const uint4 *>(at + e0)), b = __ldcs(reinterpret_cast<const uint4 *>(at + e1));
+            v[0] = make_uint2(a.x, a.y);
+            v[1] = make_uint2(a.z, a.w);
+            v[2] = make_uint2(b.x, b.y);
+            v[3] = make_uint2(b.z, b.w);
+        } else {
+            const uint16_t *at = static_cast<const uint16_t *>(base) + row;
+            v[0] = __ldcs(reinterpret_cast<const uint2 *>(at + e0));
+            v[1] = __ldcs(reinterpret_cast<const uint2 *>(at + e1));
+        }
     }
     __device__ __forceinline__ void get(float (&x)[8]) const
     {
         if constexpr (F32) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                x[4 * i] = __uint_as_float(v[i].x);
-                x[4 * i + 1] = __uint_as_float(v[i].y);
-                x[4 * i + 2] = __uint_as_float(v[i].z);
-                x[4 * i + 3] = __uint_as_float(v[i].w);
+            for (int i = 0; i < 4; ++i) {
+                x[2 * i] = __uint_as_float(v[i].x);
+                x[2 * i + 1] = __uint_as_float(v[i].y);
             }
         } else {
             widen(v[0], x);
+            widen(v[1], x + 4);
         }
     }
 };
 
-template <int D, bool F32, int ROWS>
-__global__ void __launch_bounds__(kRopeThreads) rope_rows(const RopeParams p)
+template <int D, bool F32, bool NEIGHBOURS, int ROWS>
+__global__ void __launch_bounds__(kRopeThreads, ROWS > 1 ? kRopeBlocks : 1) rope_rows(const RopeParams p)
 {
     constexpr int kLanes = D / 8, kPass = kRopeThreads / kLanes;
     __shared__ uint64_t s_turn[D / 2];          // a pair's fraction of a turn for each position, times 2^64
     __shared__ uint8_t s_axis[D / 2];
     __shared__ float s_cos[2][D / 2], s_sin[2][D / 2];  // two tokens': one block-wide meeting for each is enough
+    __shared__ int64_t s_place[2];                      // where the cache takes them, or -1
     const int tid = threadIdx.x, li = tid % kLanes, half = p.rot / 2;
     const int rows = p.heads + 2 * p.kv_heads, row0 = int(blockIdx.y) * ROWS * kPass + tid / kLanes;
     grid_dependency_wait();
-    for (int i = tid; i < half; i += kRopeThreads) {
-        double f = double(__ldg(p.inv_freq + i)) * 0.15915494309189533577;  // 1 / (2 pi)
+    if (tid < half) {  // (at most 128 pairs)
+        double f = double(__ldg(p.inv_freq + tid)) * 0.15915494309189533577;  // 1 / (2 pi)
         f -= floor(f);
-        s_turn[i] = __double2ull_rn(f * 18446744073709551616.0);
-        s_axis[i] = uint8_t(p.axis ? min(int(__ldg(p.axis + i)), p.axes - 1) : 0);
+        s_turn[tid] = __double2ull_rn(f * 18446744073709551616.0);
+        s_axis[tid] = uint8_t(p.axis ? min(int(__ldg(p.axis + tid)), p.axes - 1) : 0);
     }
-    __syncthreads();
-    uint4 wq = make_uint4(0, 0, 0, 0), wk = wq;
-    if (p.q_norm) wq = __ldg(reinterpret_cast<const uint4 *>(p.q_norm) + li);
-    if (p.k_norm) wk = __ldg(reinterpret_cast<const uint4 *>(p.k_norm) + li);
-    // halves: elements 8 li .. are all first or all second of their pairs, the others
-    // of which lie rot / 16 lanes further or before
-    const int lane = tid & 31, hl = p.rot / 16;
-    const bool turns = li < 2 * hl, second = li >= hl;
-    const int partner = p.neighbours || !turns ? lane : second ? lane - hl : lane + hl;
-
+    // of halves a lane has four pairs' first elements and their second ones, else eight in a row
+    const bool turns = li < p.rot / 8, halves = !NEIGHBOURS && turns;
+    const int e0 = halves ? 4 * li : 8 * li, e1 = halves ? half + 4 * li : 8 * li + 4;
+    uint2 wq[2] = {}, wk[2] = {};
+    if (p.q_norm) {
+        wq[0] = __ldg(reinterpret_cast<const uint2 *>(p.q_norm + e0));
+        wq[1] = __ldg(reinterpret_cast<const uint2 *>(p.q_norm + e1));
+    }
+    if (p.k_norm) {
+        wk[0] = __ldg(reinterpret_cast<const uint2 *>(p.k_norm + e0));
+        wk[1] = __ldg(reinterpret_cast<const uint2 *>(p.k_norm + e1));
+    }
+    // the next token's rows, place and position are on their way while a token is worked on
+    Octet<F32> ahead[ROWS];
+    int64_t slot_ahead = -1;
+    int pos_ahead = 0;
+    const auto fetch = [&](int t) {
+        if (t >= p.T) return;
+#pragma unroll
+        for (int k = 0; k < ROWS; ++k)
+            if (row0 + k * kPass < rows) ahead[k].load(p.qkv, t * p.ld_qkv + (row0 + k * kPass) * D, e0, e1);
+        if (tid == kRopeThreads - 1) slot_ahead = p.slots ? __ldg(p.slots + t) : -1;
+        if (tid < half) pos_ahead = __ldg(p.positions + (int64_t)s_axis[tid] * p.T + t);
+    };
+    fetch(blockIdx.x);  // (a thread reads the axis that it wrote)
     for (int t = blockIdx.x, n = 0; t < p.T; t += gridDim.x, ++n) {
         Octet<F32> in[ROWS];
 #pragma unroll
-        for (int k = 0; k < ROWS; ++k)
-            if (row0 + k * kPass < rows) in[k].load(p.qkv, t * p.ld_qkv + (int64_t)(row0 + k * kPass) * D + 8 * li);
-        const int64_t slot = p.slots ? __ldg(p.slots + t) : -1;
+        for (int k = 0; k < ROWS; ++k) in[k] = ahead[k];
         float *cs = s_cos[n & 1], *sn = s_sin[n & 1];
-        for (int i = tid; i < half; i += kRopeThreads) {
-            const int64_t pos = __ldg(p.positions + (int64_t)s_axis[i] * p.T + t);
-            const int turn = int(uint32_t((uint64_t(pos) * s_turn[i]) >> 32));  // in 2^-32 of a turn, from -1/2 on
-            sincospif(__fmul_rn(__int2float_rn(turn), 0x1p-31f), sn + i, cs + i);
+        if (tid < half) {
+            const int turn = int(uint32_t((uint64_t(int64_t(pos_ahead)) * s_turn[tid]) >> 32));  // in 2^-32 of a turn, from -1/2 on
+            sincospif(__fmul_rn(__int2float_rn(turn), 0x1p-31f), sn + tid, cs + tid);
         }
+        if (tid == kRopeThreads - 1) {
+            const int64_t slot = slot_ahead;
+            s_place[n & 1] = slot >= 0 && slot < p.places ? slot / p.page_size * p.page_stride + slot % p.page_size * p.token_stride : -1;
+        }
+        fetch(t + gridDim.x);
         __syncthreads();
-        float c[8], s[8];
-        if (turns) {
+        float c[4], s[4];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int i = p.neighbours ? 4 * li + j / 2 : 8 * (second ? li - hl : li) + j;
-                const bool b = p.neighbours ? j & 1 : second;
-                c[j] = cs[i];
-                s[j] = b ? sn[i] : -sn[i];
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) c[j] = 1.0f, s[j] = 0.0f;
+        for (int j = 0; j < 4; ++j) {
+            c[j] = turns ? cs[4 * li + j] : 1.0f;
+            s[j] = turns ? sn[4 * li + j] : 0.0f;
         }
-        const bool stored = slot >= 0 && slot < p.places;
-        const int64_t place = stored ? slot / p.page_size * p.page_stride + slot % p.page_size * p.token_stride : 0;
+        const int64_t place = s_place[n & 1];
 #pragma unroll
         for (int k = 0; k < ROWS; ++k) {
             const int r = row0 + k * kPass, g = r - p.heads;
@@ -167,51 +177,59 @@ __global__ void __launch_bounds__(kRopeThreads) rope_rows(const RopeParams p)
             for (int d = 1; d < kLanes; d *= 2) sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, d));
             if (!value && norm) {
                 float w[8];
-                widen(g < 0 ? wq : wk, w);
-                const float f = __fdiv_rn(1.0f, __fsqrt_rn(__fmaf_rn(sum, 1.0f / D, p.eps)));
+                widen(g < 0 ? wq[0] : wk[0], w);
+                widen(g < 0 ? wq[1] : wk[1], w + 4);
+                const float f = rsqrtf(__fmaf_rn(sum, 1.0f / D, p.eps));
 #pragma unroll
                 for (int j = 0; j < 8; ++j) x[j] = __fmul_rn(__fmul_rn(x[j], f), __fadd_rn(w[j], p.one));
             }
-            float y[8];
+            if (!value && turns) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float other = p.neighbours ? x[j ^ 1] : __shfl_sync(0xffffffffu, x[j], partner);
-                y[j] = value || !turns ? x[j] : __fmaf_rn(x[j], c[j], __fmul_rn(other, s[j]));
+                for (int j = 0; j < 4; ++j) {
+                    float &a = x[NEIGHBOURS ? 2 * j : j], &b = x[NEIGHBOURS ? 2 * j + 1 : 4 + j];
+                    const float turned = __fmaf_rn(a, c[j], -__fmul_rn(b, s[j]));
+                    b = __fmaf_rn(b, c[j], __fmul_rn(a, s[j]));
+                    a = turned;
+                }
             }
             if (r >= rows) continue;
-            const uint4 out = narrow(y);
-            if (g < 0) {
-                *reinterpret_cast<uint4 *>(p.q + ((int64_t)t * p.heads + r) * D + 8 * li) = out;
-            } else if (stored) {
-                uint16_t *cache = value ? p.v_cache : p.k_cache;
-                *reinterpret_cast<uint4 *>(cache + place + (value ? g - p.kv_heads : g) * p.head_stride + 8 * li) = out;
-            }
+            uint16_t *to;
+            if (g < 0)
+                to = p.q + ((int64_t)t * p.heads + r) * D;
+            else if (place >= 0)
+                to = (value ? p.v_cache : p.k_cache) + place + (value ? g - p.kv_heads : g) * p.head_stride;
+            else
+                continue;
+            *reinterpret_cast<uint2 *>(to + e0) = narrow(x);
+            *reinterpret_cast<uint2 *>(to + e1) = narrow(x + 4);
         }
     }
 }
 
-template <int D, bool F32, int ROWS>
+template <int D, bool F32, bool NEIGHBOURS, int ROWS>
 cudaError_t launch_rope(const RopeParams &p, int sms, cudaStream_t stream)
 {
     static std::atomic<int> configured[64] = {};
     const int rows = p.heads + 2 * p.kv_heads, block_rows = ROWS * kRopeThreads / (D / 8);
     const int y = (rows + block_rows - 1) / block_rows;
-    const int fill = (4 * sms + y - 1) / y;  // four blocks for an SM
+    const int fill = (kRopeBlocks * sms + y - 1) / y;
     Launch l;
     l.grid = dim3(unsigned(p.T < fill ? p.T : fill), unsigned(y));
     l.threads = kRopeThreads;
     l.smem = 0;
     l.pdl = true;
-    return launch_one(rope_rows<D, F32, ROWS>, configured, l, stream, p);
+    return launch_one(rope_rows<D, F32, NEIGHBOURS, ROWS>, configured, l, stream, p);
 }
 
 template <int D, bool F32>
 cudaError_t launch_rope_rows(const RopeParams &p, int sms, cudaStream_t stream)
 {
-    const int rows = p.heads + 2 * p.kv_heads, block_rows = 4 * kRopeThreads / (D / 8);
+    constexpr int kRows = F32 ? 2 : 4;  // 64 bytes in flight for a thread, and as many of the next token
+    const int rows = p.heads + 2 * p.kv_heads, block_rows = kRows * kRopeThreads / (D / 8);
     // one row a thread while that leaves no SM with two blocks more than another's one
-    if ((int64_t)p.T * ((rows + block_rows - 1) / block_rows) < sms) return launch_rope<D, F32, 1>(p, sms, stream);
-    return launch_rope<D, F32, 4>(p, sms, stream);
+    const bool few = (int64_t)p.T * ((rows + block_rows - 1) / block_rows) < sms;
+    if (p.neighbours) return few ? launch_rope<D, F32, true, 1>(p, sms, stream) : launch_rope<D, F32, true, kRows>(p, sms, stream);
+    return few ? launch_rope<D, F32, false, 1>(p, sms, stream) : launch_rope<D, F32, false, kRows>(p, sms, stream);
 }
 
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
