@@ -37,14 +37,14 @@ struct AttendParams {
     float *lse;
     int B, T, max_new, heads, kv_heads, group;
     int page_size, pages, max_pages;
-    int box;              // keys of a tensor-map box: all of one page
     uint64_t page_magic;  // ceil(2^42 / page_size)
+    int map_code;         // of the largest boxes in use
     float scale;
     int window, sinks;
     int64_t ld_q, ld_out, page_stride, token_stride, head_stride;
     unsigned *err;
     // the plan, and the workspace's parts
-    int tokens, rows, units, unit_shift, pieces, slots, key_slots, q_sets;
+    int tokens, blocks, rows, units, unit_shift, pieces, slots, key_slots, q_sets;
     int p_off, q_off, misc_off;
     int32_t *prefix;
     float2 *meta;
@@ -84,13 +84,6 @@ struct Seen {
 // The page of a key, key / page_size: exact for keys below 2^26 and page sizes up to 2^16.
 __device__ __forceinline__ int page_of(const AttendParams &p, int key) { return int(uint64_t(unsigned(key)) * p.page_magic >> 42); }
 
-__device__ __forceinline__ float exp2_fast(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 // One lane of a converged warp, for the instructions that a single thread issues. (With a
 // plain lane == 0 the compiler does not know that one thread is left, and a step of four
 // products took some 800 cycles.)
@@ -99,6 +92,13 @@ __device__ __forceinline__ bool one_lane()
     uint32_t p;
     asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
     return p != 0;
+}
+
+__device__ __forceinline__ float exp2_fast(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
 // 2^e for a whole number e <= 0, exactly (0 below 2^-126).
@@ -146,6 +146,46 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
         : "memory");
 }
+
+// Tensor maps of keys and of values, with boxes of 8, 16, 32 and 64 keys.
+struct CacheMaps {
+    CUtensorMap k[4], v[4];
+};
+
+// A lane's eight keys of 128 or 256 from a multiple of 128 on (lanes past them have none).
+// Keys that lie together, in one page and in one block of 64, come by as few boxes as the
+// binary digits of their number. (A box takes some 100 cycles of the warp that issues it,
+// whatever its size.)
+struct Boxes {
+    int page, place;  // outside the map where there is none (zeros); in the page
+    int code;         // of the box's size
+    bool start;       // does a box start with the lane's keys?
+
+    __device__ __forceinline__ void find(const AttendParams &p, const Seen &seen, const int32_t *table, int first, int lane, int lanes)
+    {
+        const int key = first + 8 * lane, row = page_of(p, key), at = key - row * p.page_size;
+        const int before = min(lane & 7, at / 8), all = before + min(8 - (lane & 7), (p.page_size - at) / 8);
+        code = -1;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            if ((all >> c & 1) && before == (all >> (c + 1)) << (c + 1)) code = c;
+        start = code >= 0 && lane < lanes;
+        page = start && seen.any(key, 8 << code) ? __ldg(table + row) : -1;
+        if (unsigned(page) >= unsigned(p.pages)) page = p.pages;
+        place = at;
+    }
+
+    // The boxes of the keys of lanes from .. from + n - 1, to `dst` on: BLOCKS times 64 elements,
+    // `apart` bytes apart. (The lanes where they start issue them; one lane that goes through
+    // them with shuffles took half as long again.)
+    template <int BLOCKS>
+    __device__ __forceinline__ void bring(const CUtensorMap *maps, uint32_t dst, int lane, int from, int n, int column, int apart, int g, uint32_t bar) const
+    {
+        if (!start || lane < from || lane >= from + n) return;
+#pragma unroll
+        for (int c = 0; c < BLOCKS; ++c) tma_load_4d(dst + (lane - from) * 1024 + c * apart, maps + code, column + 64 * c, place, g, page, bar);
+    }
+};
 
 // Descriptor of an operand in shared memory: `leading` and `stride` bytes as the layout
 // has them, layout 2 for the 128-byte swizzle and 4 for the 64-byte one.
@@ -233,6 +273,12 @@ struct Sequences {
     const int4 *kept;      // [B]
 };
 
+// Where an item's sums lie in the workspace.
+__device__ __forceinline__ int part_of(const AttendParams &p, int b, int u, int block, int g)
+{
+    return ((b * p.units + u) * p.blocks + block) * p.kv_heads + g;
+}
+
 // Counts first[1 .. B] become running sums from first[0] = 0 on; by one warp.
 __device__ __forceinline__ void sum_firsts(int32_t *first, int B, int lane)
 {
@@ -265,7 +311,6 @@ __device__ __forceinline__ Item item_at(const AttendParams &p, const Sequences &
     const unsigned blocks = unsigned(kept.w);
     Item it;
     it.b = lo;
-    it.index = index;
     index -= all.first[lo];
     it.block = 0;
     if (blocks > 1) {
@@ -274,6 +319,7 @@ __device__ __forceinline__ Item item_at(const AttendParams &p, const Sequences &
     }
     const int u = int(unsigned(index) / unsigned(p.kv_heads));
     it.g = index - u * p.kv_heads;
+    it.index = part_of(p, lo, u, it.block, it.g);
     it.unit = units.place(u);
     it.row = s.row + it.block * p.tokens;
     it.tokens = min(p.tokens, s.done - it.block * p.tokens);
@@ -322,9 +368,24 @@ struct Place {
 
 __host__ __device__ constexpr int few_threads(int NC) { return NC / 16 * 128 + 128; }
 
+// What the first loads need, on its way into the caches while the sequences' lengths are.
+__device__ __forceinline__ void prefetch_maps(const CUtensorMap &qmap, const CacheMaps &maps, const AttendParams &p)
+{
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&qmap)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(maps.k + p.map_code)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(maps.v + p.map_code)) : "memory");
+}
+__device__ __forceinline__ void prefetch_table(const AttendParams &p, int tid)
+{
+    // 32 entries a line; a small table, by the blocks together
+    const int64_t lines = (int64_t(p.B) * p.max_pages + 31) / 32;
+    const int64_t line = int64_t(tid) * gridDim.x + blockIdx.x;
+    if (lines <= 2048 && line < lines) asm volatile("prefetch.global.L2 [%0];" ::"l"(p.table + 32 * line) : "memory");
+}
+
 template <int D, int NC>
 __global__ void __launch_bounds__(few_threads(NC), D < 256 && NC == 16 ? 2 : 1)
-    attend_few(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const AttendParams p)
+    attend_few(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CacheMaps maps, const AttendParams p)
 {
     constexpr int DB = D / 64, HALVES = D < 128 ? 1 : D / 128;  // blocks of 64 elements; tiles of 128 in V^T's rows
     constexpr int kChunks = 2 * DB;                              // of a leaf's keys, and of its values
@@ -361,8 +422,10 @@ __global__ void __launch_bounds__(few_threads(NC), D < 256 && NC == 16 ? 2 : 1)
     }
     if (tid < NC / 16) sh.changed[tid][0] = sh.changed[tid][1] = 0;
     if (warp == kTensor) tile::tmem_alloc(smem_u32(&sh.tmem), kAlloc);
-    grid_launch_dependents();
+    if (tid == 0) prefetch_maps(qmap, maps, p);
     grid_dependency_wait();
+    grid_launch_dependents();  // (what comes next may read what was there before this kernel)
+    prefetch_table(p, tid);
 #pragma unroll 1
     for (int b = tid; b < p.B; b += kThreads) {
         const Sequence s(p, b);
@@ -375,9 +438,6 @@ __global__ void __launch_bounds__(few_threads(NC), D < 256 && NC == 16 ? 2 : 1)
     tmem_fence_after();
     if (warp == 0) sum_firsts(first, p.B, lane);
     __syncthreads();
-    if (blockIdx.x == 0 && p.units > 1)
-#pragma unroll 1
-        for (int b = tid; b <= p.B; b += kThreads) p.prefix[b] = first[b];
     const uint32_t tm = sh.tmem, S = tm, O = tm + 2 * kScores;
     const Sequences all{first, sh.seqs};
     const int items = first[p.B];
@@ -387,8 +447,7 @@ __global__ void __launch_bounds__(few_threads(NC), D < 256 && NC == 16 ? 2 : 1)
         // ------------------------------------------------------------ producers
         // One brings keys (and queries), one values: neither ring waits for the other.
         const bool values = warp > kProducer;
-        const CUtensorMap *map = values ? &vmap : &kmap;
-        const int per_tile = 128 / p.box, boxes = 2 * per_tile;  // a lane has a box of the leaf's keys
+        const CUtensorMap *map = values ? maps.v : maps.k;
         Place at(values ? p.key_slots : 0, values ? p.slots : p.key_slots);
         int n = 0;
         bool ok = true;
@@ -400,13 +459,8 @@ __global__ void __launch_bounds__(few_threads(NC), D < 256 && NC == 16 ? 2 : 1)
             const int32_t *table = p.table + int64_t(it.b) * p.max_pages;
             const int leaves = it.leaf + it.leaves, g = it.g;
             for (int leaf = it.leaf; leaf < leaves && ok; ++leaf) {
-                const int key = leaf * kLeaf + lane * p.box;
-                int page = -1, place = 0;
-                if (lane < boxes && seen.any(key, p.box)) {
-                    page = page_of(p, key);
-                    place = key - page * p.page_size;
-                    page = __ldg(table + page);
-                }
+                Boxes boxes;
+                boxes.find(p, seen, table, leaf * kLeaf, lane, 32);
                 if (!values && leaf == it.leaf) {
                     const int set = n % p.q_sets;
                     ok = __all_sync(0xffffffffu, n < p.q_sets || wait(q_empty + 8 * set, (n / p.q_sets - 1) & 1));
@@ -418,7 +472,6 @@ __global__ void __launch_bounds__(few_threads(NC), D < 256 && NC == 16 ? 2 : 1)
                     }
                     ++n;
                 }
-                if (unsigned(page) >= unsigned(p.pages)) page = p.pages;  // outside the map: zeros
 #pragma unroll 1
                 for (int i = 0; i < kChunks; ++i, ++at.issued, at.step()) {
                     if (at.full()) ok = wait(empty0 + 8 * at.slot, at.lap ^ 1);
@@ -428,13 +481,10 @@ __global__ void __launch_bounds__(few_threads(NC), D < 256 && NC == 16 ? 2 : 1)
                     if (lane == 0) mbar_arrive_expect_tx(full, kChunk);
                     __syncwarp();
                     // keys: 128, 64 elements; values: 64, twice 64 elements (128, 64 elements of head_dim 64)
-                    const bool pairs = values && D > 64;
-                    const int few = pairs ? per_tile / 2 : per_tile, column = pairs ? i % HALVES * 128 : i % DB * 64;
-                    const int box = lane - (pairs ? i / HALVES : i / DB) * few;
-                    if (box >= 0 && box < few) {
-                        tma_load_4d(dst + box * p.box * 128, map, column, place, g, page, full);
-                        if (pairs) tma_load_4d(dst + 8192 + box * p.box * 128, map, column + 64, place, g, page, full);
-                    }
+                    if (D > 64 && values)
+                        boxes.bring<2>(map, dst, lane, i / HALVES * 8, 8, i % HALVES * 128, 8192, g, full);
+                    else
+                        boxes.bring<1>(map, dst, lane, i / DB * 16, 16, i % DB * 64, 0, g, full);
                 }
             }
         }
@@ -724,65 +774,68 @@ __global__ void __launch_bounds__(few_threads(NC), D < 256 && NC == 16 ? 2 : 1)
     if (warp == kTensor) tile::tmem_free(tm, kAlloc);
 }
 
-// Joins a row's units: with M the largest of their references (whole numbers), their
-// sums times 2^(ref - M), those of places u = w, w + 8, .. by warp w in order, then the
-// warps' in order. A block has a row.
+// Joins a row's units: their sums times powers of two that bring them to one reference,
+// those of places u = w, w + 8, .. by warp w in order, then the warps' in order. A block
+// has a row.
 constexpr int kJoinWarps = 8;
 template <int D>
 __global__ void __launch_bounds__(kJoinWarps * 32) attend_join(const AttendParams p)
 {
     constexpr int E = D / 32;
     __shared__ float s_sum[kJoinWarps][D], s_total[kJoinWarps], s_top[kJoinWarps];
-    grid_dependency_wait();
-    const int few = min(p.max_new, kFew), b = int(blockIdx.x) / few, i = int(blockIdx.x) % few, h = blockIdx.y;
+    // (what is read here was there before attend_few began)
+    const int few = min(p.max_new, kFew), b = int(blockIdx.x) / few, i = int(blockIdx.x) - b * few, h = blockIdx.y;
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
     const Sequence s(p, b);
     const Units units(p, s);
+    const int g = h / p.group, block = i / p.tokens, row_in = (i - block * p.tokens) * p.group + h - g * p.group;
+    grid_dependency_wait();
     if (i >= s.done || units.count <= 1) return;
-    const int blocks = (s.done + p.tokens - 1) / p.tokens, step = blocks * p.kv_heads * p.rows;
-    const int64_t first = int64_t(p.prefix[b] + h / p.group * blocks + i / p.tokens) * p.rows + i % p.tokens * p.group + h % p.group;
-    float top = -INFINITY;
-    for (int u = threadIdx.x; u < units.count; u += kJoinWarps * 32) top = fmaxf(top, p.meta[first + int64_t(u) * step].x);
-    top = warp_max(top);
-    if (lane == 0) s_top[warp] = top;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) top = fmaxf(top, s_top[w]);
-    float sum[E], total = 0.0f;
+    // units whose places are the warp's, of the first tokens and of the others
+    float top = -INFINITY, total = 0.0f, sum[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) sum[e] = 0.0f;
-    const auto part = [&](int from, int to) {
-        // units whose places are the warp's
+#pragma unroll 1
+    for (int from = 0; from < units.count; from = from < units.sinks ? units.sinks : units.count) {
+        const int to = from < units.sinks ? units.sinks : units.count;
         int u = from + ((warp - units.place(from)) & (kJoinWarps - 1));
 #pragma unroll 4
         for (; u < to; u += kJoinWarps) {
-            const int64_t at = first + int64_t(u) * step;
-            const float2 m = p.meta[at];
-            const float w = m.x == -INFINITY ? 0.0f : power_of_two(__fsub_rn(m.x, top));
-            total = __fmaf_rn(m.y, w, total);
+            const int64_t at = int64_t(part_of(p, b, u, block, g)) * p.rows + row_in;
+            const float2 m = __ldcg(p.meta + at);
+            float v[E];
 #pragma unroll
-            for (int e = 0; e < E; ++e) sum[e] = __fmaf_rn(p.parts[at * D + lane + 32 * e], w, sum[e]);
+            for (int e = 0; e < E; ++e) v[e] = __ldcg(p.parts + at * D + lane + 32 * e);
+            // (powers of two: a reference that moves rounds nothing)
+            const float now = fmaxf(top, m.x), keep = top == -INFINITY ? 0.0f : power_of_two(__fsub_rn(top, now));
+            const float w = m.x == -INFINITY ? 0.0f : power_of_two(__fsub_rn(m.x, now));
+            top = now;
+            total = __fmaf_rn(m.y, w, __fmul_rn(total, keep));
+#pragma unroll
+            for (int e = 0; e < E; ++e) sum[e] = __fmaf_rn(v[e], w, __fmul_rn(sum[e], keep));
         }
-    };
-    part(0, units.sinks);
-    part(units.sinks, units.count);
+    }
+    if (lane == 0) s_top[warp] = top;
 #pragma unroll
     for (int e = 0; e < E; ++e) s_sum[warp][lane + 32 * e] = sum[e];
     if (lane == 0) s_total[warp] = total;
     __syncthreads();
+    float all = -INFINITY, o = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) all = fmaxf(all, s_top[w]);
     total = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) total = __fadd_rn(total, s_total[w]);
-    const bool none = top == -INFINITY;
-    const int64_t row = s.row + i;
-    if (threadIdx.x < D) {
-        float o = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kJoinWarps; ++w) o = __fadd_rn(o, s_sum[w][threadIdx.x]);
-        reinterpret_cast<__nv_bfloat16 *>(p.out)[row * p.ld_out + h * D + threadIdx.x] = __float2bfloat16_rn(none ? 0.0f : __fdiv_rn(o, total));
+    for (int w = 0; w < kJoinWarps; ++w) {
+        const float f = s_top[w] == -INFINITY ? 0.0f : power_of_two(__fsub_rn(s_top[w], all));
+        total = __fmaf_rn(s_total[w], f, total);
+        if (threadIdx.x < D) o = __fmaf_rn(s_sum[w][threadIdx.x], f, o);
     }
+    const bool none = all == -INFINITY;
+    const int64_t row = s.row + i;
+    if (threadIdx.x < D)
+        reinterpret_cast<__nv_bfloat16 *>(p.out)[row * p.ld_out + h * D + threadIdx.x] = __float2bfloat16_rn(none ? 0.0f : __fdiv_rn(o, total));
     if (p.lse && threadIdx.x == 0)
-        p.lse[row * p.heads + h] = none ? -INFINITY : __fmul_rn(0.6931471805599453f, __fadd_rn(top, log2f(total)));
+        p.lse[row * p.heads + h] = none ? -INFINITY : __fmul_rn(0.6931471805599453f, __fadd_rn(all, log2f(total)));
 }
 
 // ----------------------------------------------------------------- prompts --
@@ -929,7 +982,7 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, bool 
 
 template <int D>
 __global__ void __launch_bounds__(prompt_threads(D), 1)
-    attend_prompt(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const AttendParams p)
+    attend_prompt(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CacheMaps maps, const AttendParams p)
 {
     constexpr int STREAMS = D == 256 ? 1 : 2, W = D < 128 ? D : 128;  // elements of a chunk
     constexpr int DB = D / 64, WB = W / 64, CH = D / W, kBytes = 128 * W * 2;
@@ -960,8 +1013,10 @@ __global__ void __launch_bounds__(prompt_threads(D), 1)
         fence_mbar_init();
         sh.abort = 0;
     }
-    grid_launch_dependents();
+    if (tid == 0) prefetch_maps(qmap, maps, p);
     grid_dependency_wait();
+    grid_launch_dependents();
+    prefetch_table(p, tid);
     if (warp == kTensor) tile::tmem_alloc(smem_u32(&sh.tmem), 512);
 #pragma unroll 1
     for (int b = tid; b < p.B; b += kThreads) {
@@ -990,20 +1045,19 @@ __global__ void __launch_bounds__(prompt_threads(D), 1)
         // ------------------------------------------------------------- producer
         // The first tile's keys; then each tile's values, before them (head_dim 256) or
         // after them the next tile's keys, as the products need them.
-        const int per_tile = 128 / p.box, box = lane % per_tile, block = lane / per_tile;
         Place first_ring(0, STREAMS == 1 ? p.key_slots : p.slots), second_ring(p.key_slots, p.slots);
         int n = 0, edges = 0;
         bool ok = true;
         // a chunk: 128 keys, W elements from c W on; `rows` of them are kept (values behind a
         // sequence's keys may be anything, and 0 x NaN is NaN: zeros in their place)
-        const auto bring = [&](Place &at, const CUtensorMap *map, const PromptItem &it, int page, int place, int c, int rows) {
+        const auto bring = [&](Place &at, const CUtensorMap *map, const PromptItem &it, const Boxes &boxes, int c, int rows) {
             if (at.full()) ok = wait(empty0 + 8 * at.slot, at.lap ^ 1);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) return;
             const uint32_t full = full0 + 8 * at.slot, bar = rows < 128 ? edge : full, dst = base + at.slot * kBytes;
             if (lane == 0) mbar_arrive_expect_tx(bar, kBytes);
             __syncwarp();
-            if (block < WB) tma_load_4d(dst + block * 16384 + box * p.box * 128, map, c * W + 64 * block, place, it.g, page, bar);
+            boxes.bring<WB>(map, dst, lane, 0, 16, c * W, 16384, it.g, bar);
             if (rows < 128) {
                 ok = __all_sync(0xffffffffu, wait(edge, edges & 1));
                 ++edges;
@@ -1032,21 +1086,14 @@ __global__ void __launch_bounds__(prompt_threads(D), 1)
                     tile::tma_load_3d(Q + i * 16384, &qmap, i % DB * 64, it.g * p.group, it.row + i / DB * p.tokens, q_full);
             }
             ++n;
-            int page = p.pages, place = 0, before = 0, before_place = 0, before_rows = 0;
+            Boxes boxes{}, before{};
+            int before_rows = 0;
 #pragma unroll 1
             for (int i = it.from; i <= it.to && ok; ++i) {
                 int rows = 0;
                 if (i < it.to) {
-                    const int key = it.tile(i) * 128 + box * p.box;
                     rows = min(it.keys - it.tile(i) * 128, 128);
-                    page = -1;
-                    place = 0;
-                    if (block < WB && seen.any(key, p.box)) {
-                        page = page_of(p, key);
-                        place = key - page * p.page_size;
-                        page = __ldg(table + page);
-                    }
-                    if (unsigned(page) >= unsigned(p.pages)) page = p.pages;  // outside the map: zeros
+                    boxes.find(p, seen, table, it.tile(i) * 128, lane, 16);
                 }
                 // (of one stream a tile's scores come before the sums of the tile before; of
                 // two the first stream's sums come before the second tile's first scores)
@@ -1057,13 +1104,12 @@ __global__ void __launch_bounds__(prompt_threads(D), 1)
 #pragma unroll 1
                     for (int c = 0; c < CH && ok; ++c) {
                         if (keys)
-                            bring(first_ring, &kmap, it, page, place, c, 128);
+                            bring(first_ring, maps.k, it, boxes, c, 128);
                         else
-                            bring(STREAMS == 1 ? second_ring : first_ring, &vmap, it, before, before_place, c, before_rows);
+                            bring(STREAMS == 1 ? second_ring : first_ring, maps.v, it, before, c, before_rows);
                     }
                 }
-                before = page;
-                before_place = place;
+                before = boxes;
                 before_rows = rows;
             }
         }
@@ -1217,7 +1263,6 @@ __global__ void __launch_bounds__(prompt_threads(D), 1)
         // (the products have the scale's sign already; above 0, so that a hidden score's weight is 0)
         const float c2 = fmaxf(__fmul_rn(fabsf(p.scale), 1.4426950408889634f), 1.2e-38f);
         const uint64_t scale2 = tile::pack2(c2, c2);
-        const int per_tile = 128 / p.box, box_shift = 31 - __clz(p.box);
         int tiles = 0;  // of the stream so far
         // The last tile's sums are in. (One stream's scores run ahead of the sums of the tile
         // before, so that its tiles have a barrier each in turn: with one for all, the wait for
@@ -1244,16 +1289,16 @@ __global__ void __launch_bounds__(prompt_threads(D), 1)
             for (int i = it.from; i < it.to; ++i) {
                 const int key0 = it.tile(i) * 128;
                 if (!sees.any(key0, 128)) continue;
-                // boxes of keys whose page is there
+                // eights of keys whose page is there
                 int page = -1;
-                const int key = key0 + lane * p.box;
-                if (lane < per_tile && seen.any(key, p.box)) page = __ldg(table + page_of(p, key));
+                const int key = key0 + lane * 8;
+                if (lane < 16 && seen.any(key, 8)) page = __ldg(table + page_of(p, key));
                 const int buffer = STREAMS == 1 ? tiles & 1 : x;
                 wait(s_ready + 8 * buffer, (STREAMS == 1 ? tiles / 2 : tiles) & 1);
                 tmem_fence_after();
                 const uint32_t at = S + buffer * 128 + lanes;
                 const uint32_t there = __ballot_sync(0xffffffffu, unsigned(page) < unsigned(p.pages));
-                const bool plain = there == (1u << per_tile) - 1u && key0 + 127 <= start && (!p.window || key0 >= start + tokens - p.window);
+                const bool plain = there == 0xffffu && key0 + 127 <= start && (!p.window || key0 >= start + tokens - p.window);
                 // which of the 32 keys from `key` on the row sees
                 const auto see = [&](int c) {
                     const int key = key0 + c;
@@ -1261,7 +1306,7 @@ __global__ void __launch_bounds__(prompt_threads(D), 1)
                     v &= below(last + 1 - key);
                     uint32_t boxes = 0;
 #pragma unroll
-                    for (int k = 0; k < 32; k += 8) boxes |= (there >> ((c + k) >> box_shift) & 1u) * (0xffu << k);
+                    for (int k = 0; k < 32; k += 8) boxes |= (there >> ((c + k) / 8) & 1u) * (0xffu << k);
                     return v & boxes;
                 };
                 // Scores go by in 32 columns, the next 32 on their way (all 128 in registers, and code
@@ -1432,7 +1477,8 @@ __global__ void __launch_bounds__(256) attend_join_pieces(const AttendParams p)
 }
 
 struct Maps {
-    CUtensorMap q, k, v;
+    CUtensorMap q;
+    CacheMaps cache;
 };
 
 template <int D, int NC>
@@ -1445,7 +1491,7 @@ cudaError_t launch_few(const AttendParams &p, const Maps &m, const FewPlan &f, i
     l.threads = few_threads(NC);
     l.smem = size_t(f.smem);
     l.pdl = true;
-    cudaError_t e = launch_one(attend_few<D, NC>, configured[0], l, stream, m.q, m.k, m.v, p);
+    cudaError_t e = launch_one(attend_few<D, NC>, configured[0], l, stream, m.q, m.cache, p);
     if (e != cudaSuccess || f.units == 1) return e;
     l.grid = dim3(unsigned(p.B * (p.max_new < kFew ? p.max_new : kFew)), unsigned(p.heads));
     l.threads = kJoinWarps * 32;
@@ -1462,7 +1508,7 @@ cudaError_t launch_prompt(const AttendParams &p, const Maps &m, const PromptPlan
     l.threads = prompt_threads(D);
     l.smem = size_t(f.smem);
     l.pdl = true;
-    cudaError_t e = launch_one(attend_prompt<D>, configured[0], l, stream, m.q, m.k, m.v, p);
+    cudaError_t e = launch_one(attend_prompt<D>, configured[0], l, stream, m.q, m.cache, p);
     if (e != cudaSuccess || f.pieces == 1) return e;
     l.grid = dim3(unsigned((int64_t(p.T) * p.heads + 7) / 8));
     l.threads = 256;
@@ -1550,23 +1596,26 @@ extern "C" qmv_status qmv_attend_run(const uint16_t *q, const uint16_t *k_cache,
     p.kv_heads = kv_heads;
     p.err = dev.err;
     const FewPlan f = few_plan(B, max_new, heads, kv_heads, head_dim, int64_t(max_pages) * page_size, window, sinks);
-    p.tokens = f.tokens; p.rows = f.rows; p.units = f.units; p.unit_shift = f.unit == kLeaf ? 8 : 9; p.slots = f.slots; p.key_slots = f.key_slots; p.q_sets = f.q_sets;
+    p.tokens = f.tokens; p.blocks = f.blocks; p.rows = f.rows; p.units = f.units; p.unit_shift = f.unit == kLeaf ? 8 : 9; p.slots = f.slots; p.key_slots = f.key_slots; p.q_sets = f.q_sets;
     p.p_off = f.p_off; p.q_off = f.q_off; p.misc_off = f.misc_off;
     uint8_t *at = static_cast<uint8_t *>(ws);
     p.prefix = reinterpret_cast<int32_t *>(at + f.prefix_off);
     p.meta = reinterpret_cast<float2 *>(at + f.meta_off);
     p.parts = reinterpret_cast<float *>(at + f.parts_off);
-    // keys and values by boxes of 64 elements and as many keys of one page as its size allows
     p.page_magic = ((uint64_t(1) << 42) + page_size - 1) / page_size;
-    p.box = 64;
-    while (page_size % p.box) p.box /= 2;
+    // Keys and values by boxes of 64 elements and 64 keys at most: one size where pages are
+    // a power of two or multiples of 64, else all that fit a page.
     Maps m;
     const int64_t cache_dims[4] = {head_dim, page_size, kv_heads, pages}, cache_strides[3] = {token_stride, head_stride, page_stride};
-    const int cache_box[4] = {64, p.box, 1, 1};
+    p.map_code = page_size >= 64 ? 3 : page_size >= 32 ? 2 : page_size >= 16 ? 1 : 0;
+    const bool one_size = page_size % 64 == 0 || (page_size & (page_size - 1)) == 0;
+    for (int c = one_size ? p.map_code : 0; c <= p.map_code && st == QMV_OK; ++c) {
+        const int box[4] = {64, 8 << c, 1, 1};
+        st = encode_bf16(&m.cache.k[c], k_cache, 4, cache_dims, cache_strides, box);
+        if (st == QMV_OK) st = encode_bf16(&m.cache.v[c], v_cache, 4, cache_dims, cache_strides, box);
+    }
     const int64_t q_dims[3] = {head_dim, heads, T}, q_strides[2] = {head_dim, ld_q};
     const int q_box[3] = {64, p.group, f.tokens};
-    st = encode_bf16(&m.k, k_cache, 4, cache_dims, cache_strides, cache_box);
-    if (st == QMV_OK) st = encode_bf16(&m.v, v_cache, 4, cache_dims, cache_strides, cache_box);
     if (st == QMV_OK) st = encode_bf16(&m.q, q, 3, q_dims, q_strides, q_box);
     if (st != QMV_OK) return st;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
