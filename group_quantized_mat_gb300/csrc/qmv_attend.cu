@@ -160,6 +160,7 @@ struct Boxes {
     int page, place;  // outside the map where there is none (zeros); in the page
     int code;         // of the box's size
     bool start;       // does a box start with the lane's keys?
+    uint32_t there;   // bits of the lanes whose keys' page is there
 
     __device__ __forceinline__ void find(const AttendParams &p, const Seen &seen, const int32_t *table, int first, int lane, int lanes)
     {
@@ -171,8 +172,10 @@ struct Boxes {
             if ((all >> c & 1) && before == (all >> (c + 1)) << (c + 1)) code = c;
         start = code >= 0 && lane < lanes;
         page = start && seen.any(key, 8 << code) ? __ldg(table + row) : -1;
-        if (unsigned(page) >= unsigned(p.pages)) page = p.pages;
+        const bool found = unsigned(page) < unsigned(p.pages);
+        if (!found) page = p.pages;
         place = at;
+        there = __reduce_or_sync(0xffffffffu, found ? ((1u << (1 << (code & 3))) - 1u) << lane : 0u);
     }
 
     // The boxes of the keys of lanes from .. from + n - 1, to `dst` on: BLOCKS times 64 elements,
@@ -237,8 +240,8 @@ __device__ __forceinline__ void tmem_st(uint32_t a, const float (&v)[N])
 // 2 x columns columns of one product, so that the weights' rounding is below that of
 // fp32 sums' order.
 //
-// Order. A work item is a unit of 512 keys (256 where that many make the call's longest
-// sequence at most 152 items), from a multiple of 512 on, in leaves of 256,
+// Order. A work item is a unit of 256, 512 or 1024 keys (see few_plan), from a multiple of
+// that on, in leaves of 256,
 // whose products are added in the order of keys; a column's reference m is a whole
 // number, from the maxima of its leaves so far, so that a change of m scales by powers
 // of two without a rounding. Units are joined by attend_join in an order given by
@@ -345,6 +348,7 @@ struct FewShared {
     float top[4][NC], sum[4][NC], ref[NC], use[NC], shift[NC], total[NC];
     int last[NC], low[NC];  // a column sees keys up to `last` and from `low` on
     int64_t out[NC];        // where its sums go
+    uint32_t there[8];      // of the last leaves: which eights of keys have a page
     int4 seqs[1];           // [B], then the sequences' first items [B + 1]
 };
 
@@ -411,7 +415,7 @@ __global__ void __launch_bounds__(few_threads(NC), D < 256 && NC == 16 ? 2 : 1)
         for (int i = 0; i < 2; ++i) {
             mbar_init(q_full + 8 * i, 1);
             mbar_init(q_empty + 8 * i, 1);
-            mbar_init(s_ready + 8 * i, 1);
+            mbar_init(s_ready + 8 * i, 2);  // the scores, and the warp that has seen the keys land
             mbar_init(p_ready + 16 * i, NC / 4);  // a warp's arrival
             mbar_init(p_ready + 16 * i + 8, NC / 4);
         }
@@ -449,7 +453,7 @@ __global__ void __launch_bounds__(few_threads(NC), D < 256 && NC == 16 ? 2 : 1)
         const bool values = warp > kProducer;
         const CUtensorMap *map = values ? maps.v : maps.k;
         Place at(values ? p.key_slots : 0, values ? p.slots : p.key_slots);
-        int n = 0;
+        int n = 0, brought = 0;  // items' queries, leaves
         bool ok = true;
 #pragma unroll 1
         for (int index = blockIdx.x; index < items && ok; index += gridDim.x) {
@@ -461,6 +465,8 @@ __global__ void __launch_bounds__(few_threads(NC), D < 256 && NC == 16 ? 2 : 1)
             for (int leaf = it.leaf; leaf < leaves && ok; ++leaf) {
                 Boxes boxes;
                 boxes.find(p, seen, table, leaf * kLeaf, lane, 32);
+                if (!values && lane == 0) sh.there[brought & 7] = boxes.there;
+                ++brought;
                 if (!values && leaf == it.leaf) {
                     const int set = n % p.q_sets;
                     ok = __all_sync(0xffffffffu, n < p.q_sets || wait(q_empty + 8 * set, (n / p.q_sets - 1) & 1));
@@ -555,6 +561,7 @@ __global__ void __launch_bounds__(few_threads(NC), D < 256 && NC == 16 ? 2 : 1)
                             tmem_commit(empty0 + 8 * at.slot);
                             if (i == kChunks - 1) {
                                 tmem_commit(s_ready + 8 * (leaf & 1));
+                                mbar_arrive(s_ready + 8 * (leaf & 1));
                                 if (l == leaves - 1) tmem_commit(q_empty + 8 * set);
                             }
                         }
@@ -585,13 +592,12 @@ __global__ void __launch_bounds__(few_threads(NC), D < 256 && NC == 16 ? 2 : 1)
         for (int index = blockIdx.x; index < items; index += gridDim.x) {
             const Item it = item_at(p, all, index);
             const Seen seen(p, it.pos, it.pos + it.tokens - 1);
-            const int32_t *table = p.table + int64_t(it.b) * p.max_pages;
             if (mine < 16) {
                 const int r = column, pos = it.pos + token;
                 sh.ref[r] = -INFINITY;
                 sh.last[r] = r < it.rows ? pos : -1;
                 sh.low[r] = p.window ? pos - p.window + 1 : 0;
-                sh.out[r] = it.whole ? (it.row + token) * p.ld_out + (it.g * p.group + head) * D : (int64_t(it.index) * p.rows + r) * D;
+                sh.out[r] = (it.row + token) * p.ld_out + (it.g * p.group + head) * D;
             }
             float sum[16];
 #pragma unroll
@@ -600,14 +606,13 @@ __global__ void __launch_bounds__(few_threads(NC), D < 256 && NC == 16 ? 2 : 1)
 #pragma unroll 1
             for (int l = 0; l < it.leaves; ++l, ++leaf) {
                 const int key0 = (it.leaf + l) * kLeaf + mine;
-                int page[2];
-#pragma unroll
-                for (int h = 0; h < 2; ++h) page[h] = seen(key0 + 128 * h) ? __ldg(table + page_of(p, key0 + 128 * h)) : -1;
                 const uint32_t scores = S + (leaf & 1) * kScores + lanes + c0;
                 wait(s_ready + 8 * (leaf & 1), (leaf / 2) & 1);
                 tmem_fence_after();
                 uint32_t see[2] = {0xffffu, 0xffffu};  // which columns see the key
-                const bool there0 = unsigned(page[0]) < unsigned(p.pages), there1 = unsigned(page[1]) < unsigned(p.pages);
+                // (keys whose page is there, as the producer found it)
+                const uint32_t there = sh.there[leaf & 7];
+                const bool there0 = seen(key0) && (there >> (mine / 8) & 1), there1 = seen(key0 + 128) && (there >> (16 + mine / 8) & 1);
                 if (!(there0 && there1 && key0 + 128 <= it.pos && (!p.window || key0 >= it.pos + it.tokens - p.window))) {
 #pragma unroll 1
                     for (int h = 0; h < 2; ++h) {
@@ -702,7 +707,7 @@ __global__ void __launch_bounds__(few_threads(NC), D < 256 && NC == 16 ? 2 : 1)
                     // right only when the lap before has landed and while the lap itself is not
                     // consumed: the leaf before's values have been used, the second tile's
                     // come after the first's. A tile's values fit in the ring at once.)
-                    const bool there = h ? there1 : there0;
+                    const bool seen_key = h ? there1 : there0;
                     if (group == 0 && !__all_sync(0xffffffffu, there0 && there1)) {
                         const int from = leaf * kChunks + h * DB, slots = p.slots - p.key_slots;
 #pragma unroll 1
@@ -710,7 +715,7 @@ __global__ void __launch_bounds__(few_threads(NC), D < 256 && NC == 16 ? 2 : 1)
                             const int slot = p.key_slots + (from + c) % slots;
                             wait(full0 + 8 * slot, ((from + c) / slots) & 1);
                             // does the chunk hold 64 elements (of head_dim 64) or 128 of the thread's key?
-                            if (there || (D > 64 && c / HALVES != mine / 64)) continue;
+                            if (seen_key || (D > 64 && c / HALVES != mine / 64)) continue;
                             const uint32_t at = base + slot * kChunk + (D == 64 ? mine : mine & 63) * 128;
 #pragma unroll 1
                             for (int i = 0; i < (D == 64 ? 8 : 16); ++i) sts_v4_u32(at + (i & 7) * 16 + (i >> 3) * 8192, make_uint4(0, 0, 0, 0));
@@ -751,17 +756,23 @@ __global__ void __launch_bounds__(few_threads(NC), D < 256 && NC == 16 ? 2 : 1)
                 settle(a);
                 settle(b);
                 if (d >= D) continue;
+                if (it.leaves == 0) {
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int r = c0 + i;
-                    if (r >= it.rows) break;
-                    const float o = it.leaves > 0 ? __fadd_rn(a[i], b[i]) : 0.0f;
-                    if (it.whole) {
-                        const float f = sh.total[r];
-                        reinterpret_cast<__nv_bfloat16 *>(p.out)[sh.out[r] + d] = __float2bfloat16_rn(f == 0.0f ? 0.0f : __fmul_rn(o, f));
-                    } else {
-                        p.parts[sh.out[r] + d] = o;
-                    }
+                    for (int i = 0; i < 16; ++i) a[i] = b[i] = 0.0f;
+                }
+                const int left = it.rows - c0;
+                if (!it.whole) {
+                    float *to = p.parts + (int64_t(it.index) * p.rows + c0) * D + d;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (i < left) to[i * D] = __fadd_rn(a[i], b[i]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (i < left) {
+                            const float f = sh.total[c0 + i];
+                            reinterpret_cast<__nv_bfloat16 *>(p.out)[sh.out[c0 + i] + d] = __float2bfloat16_rn(f == 0.0f ? 0.0f : __fmul_rn(__fadd_rn(a[i], b[i]), f));
+                        }
                 }
             }
             tmem_fence_before();
@@ -956,8 +967,8 @@ __device__ __forceinline__ void tmem_ld32(uint32_t a, float (&v)[32])
 struct PromptShared {
     uint64_t full[8], empty[8], q_full, q_empty, edge, s_ready[2], p_ready[2], o_done[2], finished;
     int abort;
-    uint32_t tmem;
-    int4 seqs[1];  // [B], then the sequences' first items [B + 1]
+    uint32_t tmem, there[8];  // (of the last tiles: which eights of keys have a page)
+    int4 seqs[1];             // [B], then the sequences' first items [B + 1]
 };
 
 // Hardware barriers: at 1 and 2 the 128 threads of a stream arrive, whose weights are
@@ -1006,7 +1017,7 @@ __global__ void __launch_bounds__(prompt_threads(D), 1)
         mbar_init(edge, 1);
         mbar_init(finished, 2);
         for (int x = 0; x < 2; ++x) {
-            mbar_init(s_ready + 8 * x, 1);
+            mbar_init(s_ready + 8 * x, 2);  // the scores, and the warp that has seen the keys land
             mbar_init(p_ready + 8 * x, 4);
             mbar_init(o_done + 8 * x, 1);
         }
@@ -1046,7 +1057,7 @@ __global__ void __launch_bounds__(prompt_threads(D), 1)
         // The first tile's keys; then each tile's values, before them (head_dim 256) or
         // after them the next tile's keys, as the products need them.
         Place first_ring(0, STREAMS == 1 ? p.key_slots : p.slots), second_ring(p.key_slots, p.slots);
-        int n = 0, edges = 0;
+        int n = 0, edges = 0, brought = 0;
         bool ok = true;
         // a chunk: 128 keys, W elements from c W on; `rows` of them are kept (values behind a
         // sequence's keys may be anything, and 0 x NaN is NaN: zeros in their place)
@@ -1094,6 +1105,8 @@ __global__ void __launch_bounds__(prompt_threads(D), 1)
                 if (i < it.to) {
                     rows = min(it.keys - it.tile(i) * 128, 128);
                     boxes.find(p, seen, table, it.tile(i) * 128, lane, 16);
+                    if (lane == 0) sh.there[brought & 7] = boxes.there;
+                    ++brought;
                 }
                 // (of one stream a tile's scores come before the sums of the tile before; of
                 // two the first stream's sums come before the second tile's first scores)
@@ -1147,7 +1160,10 @@ __global__ void __launch_bounds__(prompt_threads(D), 1)
                 for (int k = 0; k < W / 16; ++k)
                     mma_ss(score_kind, S + buffer * 128, q0 + (k / 4) * (16384 >> 4) + 2 * (k & 3), k0 + (k / 4) * (16384 >> 4) + 2 * (k & 3), b + k > 0);
                 tmem_commit(empty0 + 8 * at.slot);
-                if (bar) tmem_commit(bar);
+                if (bar) {
+                    tmem_commit(bar);
+                    mbar_arrive(bar);
+                }
                 if (more) tmem_commit(more);
             }
             __syncwarp();
@@ -1240,6 +1256,7 @@ __global__ void __launch_bounds__(prompt_threads(D), 1)
                                     for (int k = 0; k < W / 16; ++k)
                                         mma_ss(score_kind, S + s * 128, q0 + (k / 4) * (16384 >> 4) + 2 * (k & 3), k0 + (k / 4) * (16384 >> 4) + 2 * (k & 3), k > 0);
                                     tmem_commit(s_ready + 8 * s);
+                                    mbar_arrive(s_ready + 8 * s);
                                 }
                                 if (last && i < to) tmem_commit(empty0 + 8 * kslot);
                                 if (last && i == to - 1) tmem_commit(q_empty);
@@ -1263,7 +1280,7 @@ __global__ void __launch_bounds__(prompt_threads(D), 1)
         // (the products have the scale's sign already; above 0, so that a hidden score's weight is 0)
         const float c2 = fmaxf(__fmul_rn(fabsf(p.scale), 1.4426950408889634f), 1.2e-38f);
         const uint64_t scale2 = tile::pack2(c2, c2);
-        int tiles = 0;  // of the stream so far
+        int tiles = 0, ring_tiles = 0;  // of the stream so far, and of the block's items before this one
         // The last tile's sums are in. (One stream's scores run ahead of the sums of the tile
         // before, so that its tiles have a barrier each in turn: with one for all, the wait for
         // an item's last tile could see the parity of the tile before the one before it.)
@@ -1277,8 +1294,7 @@ __global__ void __launch_bounds__(prompt_threads(D), 1)
         for (int round = 0, index; (index = item_of(round)) < items; ++round) {
             const PromptItem it = prompt_at<STREAMS>(p, all, index);
             int tokens;
-            const Seen sees = stream_sees<STREAMS>(p, it, x, tokens), seen(p, it.pos, it.pos + it.tokens - 1);
-            const int32_t *table = p.table + int64_t(it.b) * p.max_pages;
+            const Seen sees = stream_sees<STREAMS>(p, it, x, tokens);
             const int start = it.pos + x * p.tokens;  // position of the stream's first token
             const bool real = r < tokens * p.group;
             const int last = real ? start + r / p.group : -1, low = p.window ? last - p.window + 1 : 0;
@@ -1289,15 +1305,11 @@ __global__ void __launch_bounds__(prompt_threads(D), 1)
             for (int i = it.from; i < it.to; ++i) {
                 const int key0 = it.tile(i) * 128;
                 if (!sees.any(key0, 128)) continue;
-                // eights of keys whose page is there
-                int page = -1;
-                const int key = key0 + lane * 8;
-                if (lane < 16 && seen.any(key, 8)) page = __ldg(table + page_of(p, key));
                 const int buffer = STREAMS == 1 ? tiles & 1 : x;
                 wait(s_ready + 8 * buffer, (STREAMS == 1 ? tiles / 2 : tiles) & 1);
                 tmem_fence_after();
                 const uint32_t at = S + buffer * 128 + lanes;
-                const uint32_t there = __ballot_sync(0xffffffffu, unsigned(page) < unsigned(p.pages));
+                const uint32_t there = sh.there[(ring_tiles + i - it.from) & 7];  // eights of keys whose page is there, as the producer found them
                 const bool plain = there == 0xffffu && key0 + 127 <= start && (!p.window || key0 >= start + tokens - p.window);
                 // which of the 32 keys from `key` on the row sees
                 const auto see = [&](int c) {
@@ -1386,6 +1398,7 @@ __global__ void __launch_bounds__(prompt_threads(D), 1)
                 ++tiles;
                 ++worked;
             }
+            ring_tiles += it.to - it.from;
             // ------------------------------------------------ what the item gives
             float t0, t1, t2, t3;
             tile::unpack2(total[0], t0, t1);
@@ -1596,7 +1609,7 @@ extern "C" qmv_status qmv_attend_run(const uint16_t *q, const uint16_t *k_cache,
     p.kv_heads = kv_heads;
     p.err = dev.err;
     const FewPlan f = few_plan(B, max_new, heads, kv_heads, head_dim, int64_t(max_pages) * page_size, window, sinks);
-    p.tokens = f.tokens; p.blocks = f.blocks; p.rows = f.rows; p.units = f.units; p.unit_shift = f.unit == kLeaf ? 8 : 9; p.slots = f.slots; p.key_slots = f.key_slots; p.q_sets = f.q_sets;
+    p.tokens = f.tokens; p.blocks = f.blocks; p.rows = f.rows; p.units = f.units; p.unit_shift = f.unit == kLeaf ? 8 : f.unit == 2 * kLeaf ? 9 : 10; p.slots = f.slots; p.key_slots = f.key_slots; p.q_sets = f.q_sets;
     p.p_off = f.p_off; p.q_off = f.q_off; p.misc_off = f.misc_off;
     uint8_t *at = static_cast<uint8_t *>(ws);
     p.prefix = reinterpret_cast<int32_t *>(at + f.prefix_off);

@@ -107,11 +107,13 @@ inline FewPlan few_plan(int B, int max_new, int heads, int kv_heads, int D, int6
     f.blocks = (most + f.tokens - 1) / f.tokens;
     f.rows = f.tokens * group;
     few_smem(f, D, B);
-    // An item is two leaves; one leaf where that makes a sequence no more items than a card has
-    // SMs. By the longest sequence that the call has room for, not by how long they are
-    // nor by how many there are, so that a row's sums keep their order from call to call.
+    // An item is two leaves; one where that makes a sequence no more items than a card has
+    // SMs, four where it makes it eight times as many. By the longest sequence that the call
+    // has room for, not by how long they are nor by how many there are, so that a row's
+    // sums keep their order from call to call.
     const int64_t sees = window && int64_t(window) + sinks + most < capacity ? int64_t(window) + sinks + most : capacity;
-    f.unit = (sees + kLeaf - 1) / kLeaf * kv_heads <= 152 ? kLeaf : 2 * kLeaf;
+    const int64_t leaves = (sees + kLeaf - 1) / kLeaf * kv_heads;
+    f.unit = leaves <= 152 ? kLeaf : leaves <= 8 * 152 ? 2 * kLeaf : 4 * kLeaf;
     int64_t units = (capacity + f.unit - 1) / f.unit;
     if (window) {
         // the units of window + most - 1 keys, and those of the first tokens
