@@ -467,20 +467,9 @@ __global__ void __launch_bounds__(few_threads(NC), D < 256 && NC == 16 ? 2 : 1)
                 boxes.find(p, seen, table, leaf * kLeaf, lane, 32);
                 if (!values && lane == 0) sh.there[brought & 7] = boxes.there;
                 ++brought;
-                if (!values && leaf == it.leaf) {
-                    const int set = n % p.q_sets;
-                    ok = __all_sync(0xffffffffu, n < p.q_sets || wait(q_empty + 8 * set, (n / p.q_sets - 1) & 1));
-                    if (!ok) break;
-                    if (lane == 0) {
-                        mbar_arrive_expect_tx(q_full + 8 * set, uint32_t(p.rows) * D * 2);
-                        for (int c = 0; c < DB; ++c)
-                            tile::tma_load_3d(Q + (set * DB + c) * NC * 128, &qmap, 64 * c, g * p.group, it.row, q_full + 8 * set);
-                    }
-                    ++n;
-                }
 #pragma unroll 1
                 for (int i = 0; i < kChunks; ++i, ++at.issued, at.step()) {
-                    if (at.full()) ok = wait(empty0 + 8 * at.slot, at.lap ^ 1);
+                    if (ok && at.full()) ok = wait(empty0 + 8 * at.slot, at.lap ^ 1);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
                     const uint32_t full = full0 + 8 * at.slot, dst = base + at.slot * kChunk;
@@ -491,6 +480,17 @@ __global__ void __launch_bounds__(few_threads(NC), D < 256 && NC == 16 ? 2 : 1)
                         boxes.bring<2>(map, dst, lane, i / HALVES * 8, 8, i % HALVES * 128, 8192, g, full);
                     else
                         boxes.bring<1>(map, dst, lane, i / DB * 16, 16, i % DB * 64, 0, g, full);
+                    // (an item's queries behind its first keys, which have further to come)
+                    if (!values && leaf == it.leaf && i == 0) {
+                        const int set = n % p.q_sets;
+                        ok = __all_sync(0xffffffffu, n < p.q_sets || wait(q_empty + 8 * set, (n / p.q_sets - 1) & 1));
+                        if (ok && lane == 0) {
+                            mbar_arrive_expect_tx(q_full + 8 * set, uint32_t(p.rows) * D * 2);
+                            for (int c = 0; c < DB; ++c)
+                                tile::tma_load_3d(Q + (set * DB + c) * NC * 128, &qmap, 64 * c, g * p.group, it.row, q_full + 8 * set);
+                        }
+                        n += ok;
+                    }
                 }
             }
         }

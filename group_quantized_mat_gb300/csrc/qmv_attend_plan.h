@@ -35,7 +35,7 @@ inline size_t up256(size_t b) { return (b + 255) & ~size_t(255); }
 
 // Fixed shared memory behind the ring: weights of a leaf (two bf16 terms), two items' queries,
 // then barriers, maxima, sums and the sequences.
-inline void few_smem(FewPlan &f, int D, int B)
+inline void few_smem(FewPlan &f, int D, int B, bool alone)
 {
     f.q_sets = D == 256 && f.columns == 64 ? 1 : 2;
     const int p_bytes = kLeaf * f.columns * 4, q_bytes = f.q_sets * f.columns * D * 2;
@@ -43,7 +43,7 @@ inline void few_smem(FewPlan &f, int D, int B)
     const int fixed = p_bytes + q_bytes + ((misc + 1023) & ~1023);
     // (a tile's values, D / 64 slots, have to be there at once: see the zeroing of unseen rows)
     const int least = D / 64 + 2 > 5 ? D / 64 + 2 : 5, two = (kSmemSm / 2 - kSmemReserved - 1024 - fixed) / kChunk;
-    f.ctas = f.columns == 16 && two >= least ? 2 : 1;
+    f.ctas = f.columns == 16 && two >= least && !alone ? 2 : 1;
     f.slots = f.ctas == 2 ? two : (kSmemBlock - 1024 - fixed) / kChunk;
     if (f.slots > 11) f.slots = 11;
     f.key_slots = f.slots / 2 < f.slots - D / 64 ? f.slots / 2 : f.slots - D / 64;
@@ -106,7 +106,6 @@ inline FewPlan few_plan(int B, int max_new, int heads, int kv_heads, int D, int6
     f.tokens = f.columns / group < most ? f.columns / group : most;
     f.blocks = (most + f.tokens - 1) / f.tokens;
     f.rows = f.tokens * group;
-    few_smem(f, D, B);
     // An item is two leaves; one where that makes a sequence no more items than a card has
     // SMs, four where it makes it eight times as many. By the longest sequence that the call
     // has room for, not by how long they are nor by how many there are, so that a row's
@@ -122,6 +121,8 @@ inline FewPlan few_plan(int B, int max_new, int heads, int kv_heads, int D, int6
     }
     f.units = int(units);
     f.items = int64_t(B) * kv_heads * f.blocks * units;
+    // (a ring that holds a whole leaf where every item has an SM for itself)
+    few_smem(f, D, B, f.items <= 152);
     f.prefix_off = 0;
     f.meta_off = up256(size_t(B + 1) * 4);
     f.parts_off = f.meta_off + up256(size_t(f.items) * f.rows * 8);
