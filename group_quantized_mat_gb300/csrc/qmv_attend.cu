@@ -964,6 +964,18 @@ __device__ __forceinline__ void tmem_ld32(uint32_t a, float (&v)[32])
         : "r"(a));
 }
 
+// Columns of 16 keys' weights in a tile's scores: 32 for its first 64 keys, where theirs
+// were, and 32 for the others.
+__device__ __forceinline__ int weights_at(int k) { return 8 * k + (k >= 4 ? 32 : 0); }
+
+__device__ __forceinline__ float tmem_ld1(uint32_t a)
+{
+    float v[1] = {tile::tmem_ld1(a)};
+    tmem_wait_ld();
+    settle(v);
+    return v[0];
+}
+
 struct PromptShared {
     uint64_t full[8], empty[8], q_full, q_empty, edge, s_ready[2], p_ready[2], o_done[2], finished;
     int abort;
@@ -971,14 +983,14 @@ struct PromptShared {
     int4 seqs[1];             // [B], then the sequences' first items [B + 1]
 };
 
-// Hardware barriers: at 1 and 2 the 128 threads of a stream arrive, whose weights are
+// Hardware barriers: at 1 and 2 the 256 threads of a stream arrive, whose weights are
 // there, and the tensor warp that issues waits for them; at 3 that warp and the one that
-// watches the ring meet. (Each barrier has one number of threads for good: one whose
+// watches the ring meet; at 4 and 5 the two threads of a row exchange its maximum. (Each barrier has one number of threads for good: one whose
 // number changed from tile to tile would take a warp that is a tile ahead for one of the tile before.)
-constexpr int kMeetWeights = 160, kMeetRing = 64;
+constexpr int kMeetWeights = 288, kMeetRing = 64, kMeetRows = 256;
 __device__ __forceinline__ void named_arrive(int id, int threads) { asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
 
-__host__ __device__ constexpr int prompt_threads(int D) { return (D == 256 ? 128 : 256) + 96; }
+__host__ __device__ constexpr int prompt_threads(int D) { return (D == 256 ? 256 : 512) + 96; }
 
 // D (128 x N fp32) (+)= A (128 x 16, tensor memory) B^T (N x 16, shared memory).
 template <uint32_t KIND>
@@ -1018,7 +1030,7 @@ __global__ void __launch_bounds__(prompt_threads(D), 1)
         mbar_init(finished, 2);
         for (int x = 0; x < 2; ++x) {
             mbar_init(s_ready + 8 * x, 2);  // the scores, and the warp that has seen the keys land
-            mbar_init(p_ready + 8 * x, 4);
+            mbar_init(p_ready + 8 * x, 8);
             mbar_init(o_done + 8 * x, 1);
         }
         fence_mbar_init();
@@ -1174,7 +1186,7 @@ __global__ void __launch_bounds__(prompt_threads(D), 1)
             if (one_lane()) {
                 const uint64_t v0 = values0 + uint32_t(at.slot * (kBytes >> 4));
 #pragma unroll
-                for (int k = 0; k < 8; ++k) mma_ts<kValueKind>(O + o, S + buffer * 128 + 8 * k, v0 + k * (2048 >> 4), add || k > 0);
+                for (int k = 0; k < 8; ++k) mma_ts<kValueKind>(O + o, S + buffer * 128 + weights_at(k), v0 + k * (2048 >> 4), add || k > 0);
                 tmem_commit(empty0 + 8 * at.slot);
                 if (bar) tmem_commit(bar);
             }
@@ -1246,7 +1258,7 @@ __global__ void __launch_bounds__(prompt_threads(D), 1)
                                     const uint64_t v0 = values0 + vslot * (kBytes >> 4);
 #pragma unroll
                                     for (int k = 0; k < 8; ++k)
-                                        mma_ts<kValueKind>(O + s * D, S + s * 128 + 8 * k, v0 + k * (2048 >> 4), k > 0 || (started >> s & 1));
+                                        mma_ts<kValueKind>(O + s * D, S + s * 128 + weights_at(k), v0 + k * (2048 >> 4), k > 0 || (started >> s & 1));
                                     tmem_commit(o_done + 8 * s);
                                 }
                                 if (last && i > from) tmem_commit(empty0 + 8 * vslot);
@@ -1275,8 +1287,9 @@ __global__ void __launch_bounds__(prompt_threads(D), 1)
         mbar_wait_bounded(finished, 0);
     } else {
         // ---------------------------------------------------------------- weights
-        const int x = STREAMS == 1 ? 0 : warp / 4, r = tid & 127, quarter = warp & 3;
-        const uint32_t lanes = uint32_t(quarter * 32) << 16, mine = O + lanes + x * D;
+        // Two threads have a row, each 64 keys of a tile and then half of the sums.
+        const int x = warp / 8, half = warp / 4 & 1, r = tid & 127, quarter = warp & 3;
+        const uint32_t lanes = uint32_t(quarter * 32) << 16, mine = O + lanes + x * D + half * (D / 2);
         // (the products have the scale's sign already; above 0, so that a hidden score's weight is 0)
         const float c2 = fmaxf(__fmul_rn(fabsf(p.scale), 1.4426950408889634f), 1.2e-38f);
         const uint64_t scale2 = tile::pack2(c2, c2);
@@ -1308,38 +1321,38 @@ __global__ void __launch_bounds__(prompt_threads(D), 1)
                 const int buffer = STREAMS == 1 ? tiles & 1 : x;
                 wait(s_ready + 8 * buffer, (STREAMS == 1 ? tiles / 2 : tiles) & 1);
                 tmem_fence_after();
-                const uint32_t at = S + buffer * 128 + lanes;
+                const uint32_t at = S + buffer * 128 + half * 64 + lanes, other = S + buffer * 128 + (1 - half) * 64 + lanes;
                 const uint32_t there = sh.there[(ring_tiles + i - it.from) & 7];  // eights of keys whose page is there, as the producer found them
                 const bool plain = there == 0xffffu && key0 + 127 <= start && (!p.window || key0 >= start + tokens - p.window);
-                // which of the 32 keys from `key` on the row sees
-                const auto see = [&](int c) {
-                    const int key = key0 + c;
-                    uint32_t v = below(p.sinks - key) | ~below(low - key);
-                    v &= below(last + 1 - key);
-                    uint32_t boxes = 0;
-#pragma unroll
-                    for (int k = 0; k < 32; k += 8) boxes |= (there >> ((c + k) / 8) & 1u) * (0xffu << k);
-                    return v & boxes;
-                };
-                // Scores go by in 32 columns, the next 32 on their way (all 128 in registers, and code
-                // for all of them in a row, did not stay in the instruction cache: 3100 cycles a
-                // tile).
-                float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
                 float s[2][32];
-                tmem_ld32(at, s[0]);
-#pragma unroll 1
-                for (int c = 0; c < 128; c += 64) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) tmem_ld32(at + 32 * h, s[h]);
+                tmem_wait_ld();
+#pragma unroll
+                for (int h = 0; h < 2; ++h) settle(s[h]);
+                if (!plain) {
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        tmem_wait_ld();
-                        settle(s[h]);
-                        tmem_ld32(at + ((c + 32 * h + 32) & 127), s[1 - h]);  // (at the end the first again)
-                        if (!plain) hide(s[h], see(c + 32 * h));
+                        // which of the 32 keys from `key` on the row sees
+                        const int from = half * 64 + 32 * h, key = key0 + from;
+                        uint32_t see = (below(p.sinks - key) | ~below(low - key)) & below(last + 1 - key), eights = 0;
 #pragma unroll
-                        for (int k = 0; k < 32; k += 2) top[(k / 2) & 3] = fmaxf(top[(k / 2) & 3], fmaxf(s[h][k], s[h][k + 1]));
+                        for (int e = 0; e < 4; ++e) eights |= (there >> (from / 8 + e) & 1u) * (0xffu << 8 * e);
+                        hide(s[h], see & eights);
                     }
                 }
-                const float m = __fmul_rn(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])), c2);
+                float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int k = 0; k < 64; k += 2) top[(k / 2) & 3] = fmaxf(top[(k / 2) & 3], fmaxf(s[k / 32][k & 31], s[k / 32][(k & 31) + 1]));
+                float m = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+                // the row's other half, by the last column of either half's scores
+                tile::tmem_st1(at + 63, m);
+                tmem_wait_st();
+                tmem_fence_before();
+                named_sync(4 + x, kMeetRows);
+                tmem_fence_after();
+                m = fmaxf(m, tmem_ld1(other + 63));
+                m = __fmul_rn(m, c2);
                 // kept while weights stay below 2^8
                 const bool moves = m > __fadd_rn(ref, 8.0f);
                 const float now = moves ? ceilf(m) : ref;
@@ -1348,7 +1361,7 @@ __global__ void __launch_bounds__(prompt_threads(D), 1)
                     sums_in();
                     tmem_fence_after();
 #pragma unroll 1
-                    for (int c = 0; c < D; c += 16) {
+                    for (int c = 0; c < D / 2; c += 16) {
                         float o[16];
                         tmem_ld<16>(mine + c, o);
                         tmem_wait_ld();
@@ -1365,27 +1378,19 @@ __global__ void __launch_bounds__(prompt_threads(D), 1)
                 ref = now;
                 use = ref == -INFINITY ? 0.0f : ref;
                 const uint64_t minus = tile::pack2(-use, -use);
-#pragma unroll 1
-                for (int c = 0; c < 128; c += 64) {
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        tmem_wait_ld();
-                        settle(s[h]);
-                        if (c + 32 * h < 96) tmem_ld32(at + c + 32 * h + 32, s[1 - h]);
-                        if (!plain) hide(s[h], see(c + 32 * h));
-                        uint32_t w[16];
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t w[16];
 #pragma unroll
-                        for (int k = 0; k < 16; ++k) {
-                            float a, b;
-                            tile::unpack2(tile::fma2(tile::pack2(s[h][2 * k], s[h][2 * k + 1]), scale2, minus), a, b);
-                            a = exp2_fast(a);
-                            b = exp2_fast(b);
-                            total[k & 1] = tile::add2(total[k & 1], tile::pack2(a, b));
-                            w[k] = pack_bf16(a, b);
-                        }
-                        // (columns whose scores have been read)
-                        tile::tmem_st(at + c / 2 + 16 * h, w);
+                    for (int k = 0; k < 16; ++k) {
+                        float a, b;
+                        tile::unpack2(tile::fma2(tile::pack2(s[h][2 * k], s[h][2 * k + 1]), scale2, minus), a, b);
+                        a = exp2_fast(a);
+                        b = exp2_fast(b);
+                        total[k & 1] = tile::add2(total[k & 1], tile::pack2(a, b));
+                        w[k] = pack_bf16(a, b);
                     }
+                    tile::tmem_st(at + 16 * h, w);  // (in the place of the half's own scores)
                 }
                 tmem_wait_st();
                 tmem_fence_before();
@@ -1403,38 +1408,51 @@ __global__ void __launch_bounds__(prompt_threads(D), 1)
             float t0, t1, t2, t3;
             tile::unpack2(total[0], t0, t1);
             tile::unpack2(total[1], t2, t3);
-            const float sum = __fadd_rn(__fadd_rn(t0, t1), __fadd_rn(t2, t3));
+            float sum = __fadd_rn(__fadd_rn(t0, t1), __fadd_rn(t2, t3));
             if (worked) sums_in();
             tmem_fence_after();
+            // The other half's total, by the first column of either half's sums, which is kept
+            // meanwhile. (The scores' place may have the next item's already.)
+            const float kept = tmem_ld1(mine);
+            tile::tmem_st1(mine, sum);
+            tmem_wait_st();
+            tmem_fence_before();
+            named_sync(4 + x, kMeetRows);
+            tmem_fence_after();
+            {
+                const float theirs = tmem_ld1(O + lanes + x * D + (1 - half) * (D / 2));
+                sum = half ? __fadd_rn(theirs, sum) : __fadd_rn(sum, theirs);
+            }
             const bool none = ref == -INFINITY;
             const int64_t row = it.row + x * p.tokens + r / p.group;
             const int head = it.g * p.group + r % p.group;
             const int64_t part = (int64_t(it.index) * STREAMS + x) * 128 + r;
             const bool whole = it.pieces == 1;
             const float f = none ? 0.0f : whole ? __fdiv_rn(1.0f, sum) : 1.0f;
-            if (real) {
+            if (real && half == 0) {
                 if (!whole)
                     p.meta[part] = make_float2(ref, sum);
                 else if (p.lse)
                     p.lse[row * p.heads + head] = none ? -INFINITY : __fmul_rn(0.6931471805599453f, __fadd_rn(ref, log2f(sum)));
             }
 #pragma unroll 1
-            for (int c = 0; c < D; c += 16) {
+            for (int c = 0; c < D / 2; c += 16) {
                 float o[16];
                 tmem_ld<16>(mine + c, o);
                 tmem_wait_ld();
                 settle(o);
+                if (c == 0) o[0] = kept;
 #pragma unroll
                 for (int k = 0; k < 16; ++k) o[k] = none ? 0.0f : __fmul_rn(o[k], f);
                 if (!real) continue;
                 if (whole) {
-                    uint4 *to = reinterpret_cast<uint4 *>(p.out + row * p.ld_out + head * D + c);
+                    uint4 *to = reinterpret_cast<uint4 *>(p.out + row * p.ld_out + head * D + half * (D / 2) + c);
 #pragma unroll
                     for (int k = 0; k < 2; ++k)
                         to[k] = make_uint4(pack_bf16(o[8 * k], o[8 * k + 1]), pack_bf16(o[8 * k + 2], o[8 * k + 3]),
                                            pack_bf16(o[8 * k + 4], o[8 * k + 5]), pack_bf16(o[8 * k + 6], o[8 * k + 7]));
                 } else {
-                    float4 *to = reinterpret_cast<float4 *>(p.parts + part * D + c);
+                    float4 *to = reinterpret_cast<float4 *>(p.parts + part * D + half * (D / 2) + c);
 #pragma unroll
                     for (int k = 0; k < 4; ++k) to[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
                 }
