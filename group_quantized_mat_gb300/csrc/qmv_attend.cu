@@ -990,7 +990,7 @@ struct PromptShared {
 constexpr int kMeetWeights = 288, kMeetRing = 64, kMeetRows = 256;
 __device__ __forceinline__ void named_arrive(int id, int threads) { asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
 
-__host__ __device__ constexpr int prompt_threads(int D) { return (D == 256 ? 256 : 512) + 96; }
+__host__ __device__ constexpr int prompt_threads(int D) { return (D == 256 ? 256 : 512) + 128; }
 
 // D (128 x N fp32) (+)= A (128 x 16, tensor memory) B^T (N x 16, shared memory).
 template <uint32_t KIND>
@@ -1009,7 +1009,7 @@ __global__ void __launch_bounds__(prompt_threads(D), 1)
 {
     constexpr int STREAMS = D == 256 ? 1 : 2, W = D < 128 ? D : 128;  // elements of a chunk
     constexpr int DB = D / 64, WB = W / 64, CH = D / W, kBytes = 128 * W * 2;
-    constexpr int kThreads = prompt_threads(D), kProducer = kThreads / 32 - 3, kTensor = kProducer + 1;
+    constexpr int kThreads = prompt_threads(D), kProducer = kThreads / 32 - 4, kTensor = kProducer + 2;
     extern __shared__ uint8_t raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     PromptShared &sh = *reinterpret_cast<PromptShared *>(smem + p.misc_off);
@@ -1064,89 +1064,68 @@ __global__ void __launch_bounds__(prompt_threads(D), 1)
     // longest block has 2 % more than the mean, instead of 6).
     const auto item_of = [](int round) { return round * int(gridDim.x) + int(round & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x); };
 
-    if (warp == kProducer) {
-        // ------------------------------------------------------------- producer
-        // The first tile's keys; then each tile's values, before them (head_dim 256) or
-        // after them the next tile's keys, as the products need them.
-        Place first_ring(0, STREAMS == 1 ? p.key_slots : p.slots), second_ring(p.key_slots, p.slots);
+    if (warp >= kProducer && warp < kTensor) {
+        // ------------------------------------------------------------ producers
+        // One brings keys (and queries), one values.
+        const bool values = warp > kProducer;
+        const CUtensorMap *map = values ? maps.v : maps.k;
+        Place at(values ? p.key_slots : 0, values ? p.slots : p.key_slots);
         int n = 0, edges = 0, brought = 0;
         bool ok = true;
-        // a chunk: 128 keys, W elements from c W on; `rows` of them are kept (values behind a
-        // sequence's keys may be anything, and 0 x NaN is NaN: zeros in their place)
-        const auto bring = [&](Place &at, const CUtensorMap *map, const PromptItem &it, const Boxes &boxes, int c, int rows) {
-            if (at.full()) ok = wait(empty0 + 8 * at.slot, at.lap ^ 1);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) return;
-            const uint32_t full = full0 + 8 * at.slot, bar = rows < 128 ? edge : full, dst = base + at.slot * kBytes;
-            if (lane == 0) mbar_arrive_expect_tx(bar, kBytes);
-            __syncwarp();
-            boxes.bring<WB>(map, dst, lane, 0, 16, c * W, 16384, it.g, bar);
-            if (rows < 128) {
-                ok = __all_sync(0xffffffffu, wait(edge, edges & 1));
-                ++edges;
-#pragma unroll 1
-                for (int i = rows * 8 + lane; i < 128 * 8; i += 32)
-                    for (int d = 0; d < WB; ++d) sts_v4_u32(dst + d * 16384 + i * 16, make_uint4(0, 0, 0, 0));
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(full);
-            }
-            ++at.issued;
-            at.step();
-        };
 #pragma unroll 1
         for (int round = 0, index; ok && (index = item_of(round)) < items; ++round) {
             const PromptItem it = prompt_at<STREAMS>(p, all, index);
-            if (it.from == it.to) continue;
+            const int from = it.from, to = it.to, g = it.g;
+            if (from == to) continue;
             const Seen seen(p, it.pos, it.pos + it.tokens - 1);
             const int32_t *table = p.table + int64_t(it.b) * p.max_pages;
-            ok = __all_sync(0xffffffffu, n == 0 || wait(q_empty, (n - 1) & 1));
-            if (!ok) break;
-            if (lane == 0) {
-                const int sets = STREAMS == 2 && it.tokens > p.tokens ? 2 : 1;
-                mbar_arrive_expect_tx(q_full, uint32_t(sets * p.tokens * p.group) * D * 2);
-                for (int i = 0; i < sets * DB; ++i)
-                    tile::tma_load_3d(Q + i * 16384, &qmap, i % DB * 64, it.g * p.group, it.row + i / DB * p.tokens, q_full);
-            }
-            ++n;
-            Boxes boxes{}, before{};
-            int before_rows = 0;
-#pragma unroll 1
-            for (int i = it.from; i <= it.to && ok; ++i) {
-                int rows = 0;
-                if (i < it.to) {
-                    rows = min(it.keys - it.tile(i) * 128, 128);
-                    boxes.find(p, seen, table, it.tile(i) * 128, lane, 16);
-                    if (lane == 0) sh.there[brought & 7] = boxes.there;
-                    ++brought;
+            if (!values) {
+                ok = __all_sync(0xffffffffu, n == 0 || wait(q_empty, (n - 1) & 1));
+                if (!ok) break;
+                if (lane == 0) {
+                    const int sets = STREAMS == 2 && it.tokens > p.tokens ? 2 : 1;
+                    mbar_arrive_expect_tx(q_full, uint32_t(sets * p.tokens * p.group) * D * 2);
+                    for (int i = 0; i < sets * DB; ++i)
+                        tile::tma_load_3d(Q + i * 16384, &qmap, i % DB * 64, g * p.group, it.row + i / DB * p.tokens, q_full);
                 }
-                // (of one stream a tile's scores come before the sums of the tile before; of
-                // two the first stream's sums come before the second tile's first scores)
+                ++n;
+            }
 #pragma unroll 1
-                for (int half = 0; half < 2; ++half) {
-                    const bool keys = (half == 0) == (STREAMS == 1);
-                    if (keys ? i == it.to : i == it.from) continue;
+            for (int i = from; i < to && ok; ++i, ++brought) {
+                Boxes boxes;
+                boxes.find(p, seen, table, it.tile(i) * 128, lane, 16);
+                if (!values && lane == 0) sh.there[brought & 7] = boxes.there;
+                // values behind a sequence's keys may be anything, and 0 x NaN is NaN: zeros in their place
+                const int rows = values ? min(it.keys - it.tile(i) * 128, 128) : 128;
 #pragma unroll 1
-                    for (int c = 0; c < CH && ok; ++c) {
-                        if (keys)
-                            bring(first_ring, maps.k, it, boxes, c, 128);
-                        else
-                            bring(STREAMS == 1 ? second_ring : first_ring, maps.v, it, before, c, before_rows);
+                for (int c = 0; c < CH; ++c, ++at.issued, at.step()) {
+                    // a chunk: 128 keys, W elements from c W on
+                    if (at.full()) ok = wait(empty0 + 8 * at.slot, at.lap ^ 1);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    const uint32_t full = full0 + 8 * at.slot, bar = rows < 128 ? edge : full, dst = base + at.slot * kBytes;
+                    if (lane == 0) mbar_arrive_expect_tx(bar, kBytes);
+                    __syncwarp();
+                    boxes.bring<WB>(map, dst, lane, 0, 16, c * W, 16384, g, bar);
+                    if (rows < 128) {
+                        __syncwarp();
+                        ok = __all_sync(0xffffffffu, wait(edge, edges & 1));
+                        ++edges;
+#pragma unroll 1
+                        for (int e = rows * 8 + lane; e < 128 * 8; e += 32)
+                            for (int d = 0; d < WB; ++d) sts_v4_u32(dst + d * 16384 + e * 16, make_uint4(0, 0, 0, 0));
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(full);
                     }
                 }
-                before = boxes;
-                before_rows = rows;
             }
         }
         if (!ok) {
             // copies in flight have to land before the block ends (those of an edge have been waited for)
+            const int slots = at.end - at.first;
 #pragma unroll 1
-            for (int ring = 0; ring < 2; ++ring) {
-                const Place &at = ring ? second_ring : first_ring;
-                const int slots = at.end - at.first;
-#pragma unroll 1
-                for (int i = max(at.issued - slots, 0); i < at.issued; ++i) mbar_wait_bounded(full0 + 8 * (at.first + i % slots), (i / slots) & 1);
-            }
+            for (int i = max(at.issued - slots, 0); i < at.issued; ++i) mbar_wait_bounded(full0 + 8 * (at.first + i % slots), (i / slots) & 1);
             if (n > 0) mbar_wait_bounded(q_full, (n - 1) & 1);
         }
     } else if (warp >= kTensor) {
@@ -1158,20 +1137,20 @@ __global__ void __launch_bounds__(prompt_threads(D), 1)
         // a warp for each stream their products slow one another down: 2339 us instead of 2003 for six
         // prompts.) Of one stream a warp issues the scores and one the sums.
         const int x = warp - kTensor;
-        Place at(STREAMS == 1 && x ? p.key_slots : 0, STREAMS == 1 && !x ? p.key_slots : p.slots);
+        Place keys(0, p.key_slots), values(p.key_slots, p.slots);
         constexpr uint32_t kValueKind = mma_kind(W, false, true);
         const uint32_t score_kind = mma_kind(128, false, false) | (p.scale < 0.0f ? 1u << 13 : 0u);  // (of the scale's sign: - Q)
         const uint64_t keys0 = descriptor(base, 16, 1024, 2), queries = descriptor(Q, 16, 1024, 2);
         const uint64_t values0 = descriptor(base, 16384, 1024, 2);
         int n = 0, tiles = 0;
         const auto scores = [&](int buffer, int set, int b, uint32_t bar, uint32_t more) {
-            wait(full0 + 8 * at.slot, at.lap);
+            wait(full0 + 8 * keys.slot, keys.lap);
             if (one_lane()) {
-                const uint64_t k0 = keys0 + uint32_t(at.slot * (kBytes >> 4)), q0 = queries + uint32_t((set * DB + b * WB) * (16384 >> 4));
+                const uint64_t k0 = keys0 + uint32_t(keys.slot * (kBytes >> 4)), q0 = queries + uint32_t((set * DB + b * WB) * (16384 >> 4));
 #pragma unroll
                 for (int k = 0; k < W / 16; ++k)
                     mma_ss(score_kind, S + buffer * 128, q0 + (k / 4) * (16384 >> 4) + 2 * (k & 3), k0 + (k / 4) * (16384 >> 4) + 2 * (k & 3), b + k > 0);
-                tmem_commit(empty0 + 8 * at.slot);
+                tmem_commit(empty0 + 8 * keys.slot);
                 if (bar) {
                     tmem_commit(bar);
                     mbar_arrive(bar);
@@ -1179,19 +1158,19 @@ __global__ void __launch_bounds__(prompt_threads(D), 1)
                 if (more) tmem_commit(more);
             }
             __syncwarp();
-            at.step();
+            keys.step();
         };
         const auto sums = [&](int buffer, int o, bool add, uint32_t bar) {
-            wait(full0 + 8 * at.slot, at.lap);
+            wait(full0 + 8 * values.slot, values.lap);
             if (one_lane()) {
-                const uint64_t v0 = values0 + uint32_t(at.slot * (kBytes >> 4));
+                const uint64_t v0 = values0 + uint32_t(values.slot * (kBytes >> 4));
 #pragma unroll
                 for (int k = 0; k < 8; ++k) mma_ts<kValueKind>(O + o, S + buffer * 128 + weights_at(k), v0 + k * (2048 >> 4), add || k > 0);
-                tmem_commit(empty0 + 8 * at.slot);
+                tmem_commit(empty0 + 8 * values.slot);
                 if (bar) tmem_commit(bar);
             }
             __syncwarp();
-            at.step();
+            values.step();
         };
 #pragma unroll 1
         for (int round = 0, index; (index = item_of(round)) < items; ++round) {
@@ -1232,20 +1211,19 @@ __global__ void __launch_bounds__(prompt_threads(D), 1)
                         if (i == from) {
                             wait(q_full, n & 1);
                         } else {
-                            wait(full0 + 8 * at.slot, at.lap);
-                            at.step();
+                            wait(full0 + 8 * values.slot, values.lap);
+                            values.step();
                         }
                         if (i < to) {
-                            wait(full0 + 8 * at.slot, at.lap);
-                            at.step();
+                            wait(full0 + 8 * keys.slot, keys.lap);
+                            keys.step();
                         }
                     }
                     named_sync(3, kMeetRing);
                     if (!x) {
-                        const uint32_t vslot = at.slot;
-                        if (i > from) at.step();
-                        const uint32_t kslot = at.slot;
-                        if (i < to) at.step();
+                        const uint32_t vslot = values.slot, kslot = keys.slot;
+                        if (i > from) values.step();
+                        if (i < to) keys.step();
 #pragma unroll 1
                         for (int s = 0; s < 2; ++s) {
                             const bool last = s == 1;

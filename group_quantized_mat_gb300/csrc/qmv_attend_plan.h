@@ -58,7 +58,7 @@ inline void few_smem(FewPlan &f, int D, int B, bool alone)
 struct PromptPlan {
     int tokens;  // of a tile: as many as their heads of one kv head fit 128 rows
     int streams, slots, chunk;
-    int key_slots;  // of one stream, whose keys and values have rings of their own
+    int key_slots;  // those of keys
     int q_off, misc_off, smem;
     int pieces;
     int64_t items;
