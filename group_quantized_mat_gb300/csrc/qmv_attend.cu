@@ -44,6 +44,7 @@ struct AttendParams {
     int64_t ld_q, ld_out, page_stride, token_stride, head_stride;
     unsigned *err;
     // the plan, and the workspace's parts
+    int items;  // that have a place in the workspace
     int tokens, blocks, rows, units, unit_shift, pieces, slots, key_slots, q_sets;
     int p_off, q_off, misc_off;
     int32_t *prefix;
@@ -243,8 +244,8 @@ __device__ __forceinline__ void tmem_st(uint32_t a, const float (&v)[N])
 // Order. A work item is a unit of 256, 512 or 1024 keys (see few_plan), from a multiple of
 // that on, in leaves of 256,
 // whose products are added in the order of keys; a column's reference m is a whole
-// number, from the maxima of its leaves so far, so that a change of m scales by powers
-// of two without a rounding. Units are joined by attend_join in an order given by
+// number, 8 above the largest score when it is set, and moves only when a score passes it:
+// a change of m scales by powers of two without a rounding, weights are at most 1. Units are joined by attend_join in an order given by
 // their places. So a row's result depends on its query and the keys that it sees alone:
 // not on the other tokens of the call, nor on how many SMs there are.
 
@@ -282,19 +283,21 @@ __device__ __forceinline__ int part_of(const AttendParams &p, int b, int u, int 
     return ((b * p.units + u) * p.blocks + block) * p.kv_heads + g;
 }
 
-// Counts first[1 .. B] become running sums from first[0] = 0 on; by one warp.
-__device__ __forceinline__ void sum_firsts(int32_t *first, int B, int lane)
+// Counts first[1 .. B] become running sums from first[0] = 0 on, at most `most` (that
+// many items have a place; more are there only if rows belong to several sequences); by one
+// warp.
+__device__ __forceinline__ void sum_firsts(int32_t *first, int B, int most, int lane)
 {
-    int sum = 0;
+    int64_t sum = 0;
 #pragma unroll 1
     for (int b0 = 0; b0 < B; b0 += 32) {
-        int v = b0 + lane < B ? first[b0 + lane + 1] : 0;
+        int64_t v = b0 + lane < B ? first[b0 + lane + 1] : 0;
 #pragma unroll
         for (int d = 1; d < 32; d *= 2) {
-            const int u = __shfl_up_sync(0xffffffffu, v, d);
+            const int64_t u = __shfl_up_sync(0xffffffffu, v, d);
             if (lane >= d) v += u;
         }
-        if (b0 + lane < B) first[b0 + lane + 1] = sum + v;
+        if (b0 + lane < B) first[b0 + lane + 1] = int32_t(sum + v < most ? sum + v : most);
         sum += __shfl_sync(0xffffffffu, v, 31);
     }
     if (lane == 0) first[0] = 0;
@@ -440,7 +443,7 @@ __global__ void __launch_bounds__(few_threads(NC), D < 256 && NC == 16 ? 2 : 1)
     tmem_fence_before();
     __syncthreads();
     tmem_fence_after();
-    if (warp == 0) sum_firsts(first, p.B, lane);
+    if (warp == 0) sum_firsts(first, p.B, p.items, lane);
     __syncthreads();
     const uint32_t tm = sh.tmem, S = tm, O = tm + 2 * kScores;
     const Sequences all{first, sh.seqs};
@@ -645,8 +648,8 @@ __global__ void __launch_bounds__(few_threads(NC), D < 256 && NC == 16 ? 2 : 1)
                     float m = fmaxf(fmaxf(sh.top[0][r], sh.top[1][r]), fmaxf(sh.top[2][r], sh.top[3][r]));
                     if (r >= it.rows) m = -INFINITY;  // (a column without a query)
                     const float old = sh.ref[r];
-                    // kept while weights stay below 2^8
-                    const float now = m > __fadd_rn(old, 8.0f) ? ceilf(m) : old;
+                    // above the largest score, and kept while it is
+                    const float now = m > old ? __fadd_rn(ceilf(m), 8.0f) : old;
                     sh.ref[r] = now;
                     sh.use[r] = now == -INFINITY ? 0.0f : now;
                     const bool moved = now != old && old != -INFINITY;
@@ -862,8 +865,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attend_join(const AttendParam
 // memory, two tiles of keys): the tensor cores work on one while the weights of the
 // other are formed. What bounds it is the products, 4 x head_dim operations for each
 // pair of row and key; a tile's exponentials take half as long.
-// m is a whole number again and moves only when a score passes it by 8, so that
-// sums are rarely scaled, and exactly. The weights are rounded to bf16 (2^-8 of each,
+// m is a whole number as above, so that sums are rarely scaled, and exactly. The weights are rounded to bf16 (2^-8 of each,
 // as an operand next to bf16 values has to be); their total is not.
 //
 // Items go from a sequence's last rows, which see the most keys, to its first. Where there are
@@ -876,6 +878,7 @@ struct PromptItem {
     int pos;               // of the first token
     int keys;
     int sinks, low;        // tiles of the first tokens; first tile of the others
+    int low_all;           // the first key that the sequence's queries see behind the first tokens
     int from, to;          // of the list of tiles
     int pieces;
     __device__ __forceinline__ int tile(int i) const { return i < sinks ? i : low + i - sinks; }
@@ -927,6 +930,7 @@ __device__ __forceinline__ PromptItem prompt_at(const AttendParams &p, const Seq
     const Tiles tiles(p, it.pos, it.pos + it.tokens - 1);
     it.sinks = tiles.sinks;
     it.low = tiles.low;
+    it.low_all = Seen(p, s.pos, s.pos).low;
     it.from = int(int64_t(tiles.count) * piece / it.pieces);
     it.to = int(int64_t(tiles.count) * (piece + 1) / it.pieces);
     return it;
@@ -1046,12 +1050,13 @@ __global__ void __launch_bounds__(prompt_threads(D), 1)
         const Sequence s(p, b);
         sh.seqs[b] = make_int4(s.row, s.n, s.keys, 0);
         const int each = STREAMS * p.tokens;
-        first[b + 1] = s.done > kFew ? (s.done + each - 1) / each * p.kv_heads * pieces_of(p, s, each) : 0;
+        const int64_t count = s.done > kFew ? int64_t((s.done + each - 1) / each) * p.kv_heads * pieces_of(p, s, each) : 0;
+        first[b + 1] = int32_t(count < p.items ? count : p.items);
     }
     tmem_fence_before();
     __syncthreads();
     tmem_fence_after();
-    if (warp == 0) sum_firsts(first, p.B, lane);
+    if (warp == 0) sum_firsts(first, p.B, p.items, lane);
     __syncthreads();
     if (blockIdx.x == 0 && p.pieces > 1)
 #pragma unroll 1
@@ -1095,25 +1100,30 @@ __global__ void __launch_bounds__(prompt_threads(D), 1)
                 Boxes boxes;
                 boxes.find(p, seen, table, it.tile(i) * 128, lane, 16);
                 if (!values && lane == 0) sh.there[brought & 7] = boxes.there;
-                // values behind a sequence's keys may be anything, and 0 x NaN is NaN: zeros in their place
-                const int rows = values ? min(it.keys - it.tile(i) * 128, 128) : 128;
+                // Values that no query of the sequence sees may be anything, and 0 x NaN is NaN:
+                // zeros in their place, behind its keys, before its window and behind its first tokens.
+                const int key0 = it.tile(i) * 128;
+                const bool zeros = values && (key0 + 128 > it.keys || (key0 < it.low_all && key0 + 128 > min(p.sinks, it.low_all)));
 #pragma unroll 1
                 for (int c = 0; c < CH; ++c, ++at.issued, at.step()) {
                     // a chunk: 128 keys, W elements from c W on
                     if (at.full()) ok = wait(empty0 + 8 * at.slot, at.lap ^ 1);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
-                    const uint32_t full = full0 + 8 * at.slot, bar = rows < 128 ? edge : full, dst = base + at.slot * kBytes;
+                    const uint32_t full = full0 + 8 * at.slot, bar = zeros ? edge : full, dst = base + at.slot * kBytes;
                     if (lane == 0) mbar_arrive_expect_tx(bar, kBytes);
                     __syncwarp();
                     boxes.bring<WB>(map, dst, lane, 0, 16, c * W, 16384, g, bar);
-                    if (rows < 128) {
+                    if (zeros) {
                         __syncwarp();
                         ok = __all_sync(0xffffffffu, wait(edge, edges & 1));
                         ++edges;
 #pragma unroll 1
-                        for (int e = rows * 8 + lane; e < 128 * 8; e += 32)
+                        for (int e = lane; e < 128 * 8; e += 32) {
+                            const int key = key0 + e / 8;
+                            if (key < it.keys && (key >= it.low_all || key < p.sinks)) continue;
                             for (int d = 0; d < WB; ++d) sts_v4_u32(dst + d * 16384 + e * 16, make_uint4(0, 0, 0, 0));
+                        }
                         fence_proxy_async_smem();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(full);
@@ -1331,9 +1341,9 @@ __global__ void __launch_bounds__(prompt_threads(D), 1)
                 tmem_fence_after();
                 m = fmaxf(m, tmem_ld1(other + 63));
                 m = __fmul_rn(m, c2);
-                // kept while weights stay below 2^8
-                const bool moves = m > __fadd_rn(ref, 8.0f);
-                const float now = moves ? ceilf(m) : ref;
+                // above the largest score, and kept while it is
+                const bool moves = m > ref;
+                const float now = moves ? __fadd_rn(ceilf(m), 8.0f) : ref;
                 if (__any_sync(0xffffffffu, moves && ref != -INFINITY)) {
                     const float f = moves && ref != -INFINITY ? power_of_two(__fsub_rn(ref, now)) : 1.0f;
                     sums_in();
@@ -1461,6 +1471,7 @@ __global__ void __launch_bounds__(256) attend_join_pieces(const AttendParams p)
         const int pieces = pieces_of(p, s, each);
         if (pieces == 1) continue;
         const int index = ((s.done - 1) / each - i / each) * p.kv_heads + h / p.group;
+        if (int64_t(p.prefix[b]) + int64_t(index + 1) * pieces > p.items) continue;
         const int64_t first = (int64_t(p.prefix[b] + index * pieces) * STREAMS + i % each / p.tokens) * 128 + i % p.tokens * p.group + h % p.group;
         float top = -INFINITY, total = 0.0f, sum[E];
 #pragma unroll 1
@@ -1605,6 +1616,7 @@ extern "C" qmv_status qmv_attend_run(const uint16_t *q, const uint16_t *k_cache,
     p.kv_heads = kv_heads;
     p.err = dev.err;
     const FewPlan f = few_plan(B, max_new, heads, kv_heads, head_dim, int64_t(max_pages) * page_size, window, sinks);
+    p.items = int(f.items);
     p.tokens = f.tokens; p.blocks = f.blocks; p.rows = f.rows; p.units = f.units; p.unit_shift = f.unit == kLeaf ? 8 : f.unit == 2 * kLeaf ? 9 : 10; p.slots = f.slots; p.key_slots = f.key_slots; p.q_sets = f.q_sets;
     p.p_off = f.p_off; p.q_off = f.q_off; p.misc_off = f.misc_off;
     uint8_t *at = static_cast<uint8_t *>(ws);
@@ -1633,6 +1645,7 @@ extern "C" qmv_status qmv_attend_run(const uint16_t *q, const uint16_t *k_cache,
                                       : launch_attend<256>(p, m, f, dev.sms, s);
     const PromptPlan g = prompt_plan(B, T, max_new, heads, kv_heads, head_dim, int64_t(max_pages) * page_size, window, sinks);
     if (e == cudaSuccess && g.items > 0) {
+        p.items = int(g.items);
         p.tokens = g.tokens; p.pieces = g.pieces; p.slots = g.slots; p.key_slots = g.key_slots;
         p.q_off = g.q_off; p.misc_off = g.misc_off;
         p.prefix = reinterpret_cast<int32_t *>(at + g.prefix_off);

@@ -450,7 +450,7 @@ QMV_API qmv_status qmv_verify_run(const void *target, const void *draft, const i
  *              QMV_MAX_HEAD_GROUP times as many. Query head h goes with kv head
  *              h / (heads / kv_heads).
  *  head_dim    64, 128 or 256.  T 1 .. QMV_MAX_TOKENS, T (heads + 2 kv_heads) below 2^31. */
-#define QMV_MAX_KV_HEADS 1024
+#define QMV_MAX_KV_HEADS 256
 #define QMV_MAX_HEAD_GROUP 64
 #define QMV_MAX_TOKENS (1 << 22)
 
@@ -529,7 +529,16 @@ QMV_API qmv_status qmv_rope_run(const void *qkv, const uint16_t *q_norm, const u
  * influence, whatever it holds. An infinity or NaN in a key or value that some query
  * of the sequence sees may reach other queries of the sequence in the call.
  *
- * Arithmetic: fp32 scores, maxima and sums; out is rounded once.
+ * Arithmetic: fp32 scores, maxima and sums; out is rounded once. Of a sequence of up to
+ * QMV_TILE_M new tokens the weights p keep 16 bits, and a token's result does not depend
+ * on what else is in the call: with the same heads, head_dim, page_size, max_pages,
+ * scale, window and sinks it is bit-identical to that of a call for this token alone (the
+ * basis of exact verification, as in qmv_run). Of longer ones (prompts) the weights are
+ * rounded to bf16 (their sum is not), and the order of a row's sums may depend on T,
+ * B and max_new as well. Calls repeat bit for bit.
+ *
+ * The workspace holds sums of parts of the keys: about 4 heads head_dim / 512 bytes of
+ * them for each key that max_pages (or the window) allows and each new token.
  *
  * Errors: QMV_ERR_NULL, QMV_ERR_COUNT (B, T, max_new, heads, kv_heads), QMV_ERR_SHAPE
  * (head_dim, page_size, pages, max_pages, scale, window, sinks, strides), QMV_ERR_FLAGS,

@@ -25,8 +25,8 @@ def rope(lib, kw):  # noqa: F811
 
 @pytest.mark.parametrize("kw,code", [
     *[({p: None}, 1) for p in ("qkv", "positions", "inv_freq", "q", "k_cache", "v_cache")],
-    (dict(T=0), 11), (dict(T=(1 << 22) + 1), 11), (dict(heads=0), 11), (dict(heads=9), 11), (dict(kv_heads=0), 11), (dict(kv_heads=1025, heads=1025), 11),
-    (dict(heads=130, kv_heads=2), 11), (dict(T=1 << 22, heads=1024, kv_heads=1024), 11), (dict(axes=0), 11), (dict(axes=5), 11),
+    (dict(T=0), 11), (dict(T=(1 << 22) + 1), 11), (dict(heads=0), 11), (dict(heads=9), 11), (dict(kv_heads=0), 11), (dict(kv_heads=257, heads=257), 11),
+    (dict(heads=130, kv_heads=2), 11), (dict(T=1 << 22, heads=512, kv_heads=256), 11), (dict(axes=0), 11), (dict(axes=5), 11),
     (dict(head_dim=96), 4), (dict(head_dim=0), 4), (dict(rope_dim=-16), 4), (dict(rope_dim=144), 4), (dict(rope_dim=24), 4),
     (dict(eps=-1.0), 4), (dict(eps=math.nan), 4), (dict(eps=math.inf), 4), (dict(ld_qkv=12 * 128 - 8), 4), (dict(ld_qkv=12 * 128 + 4), 4),
     (dict(page_size=0), 4), (dict(page_size=4), 4), (dict(page_size=12), 4), (dict(page_size=65544), 4), (dict(pages=0), 4),
