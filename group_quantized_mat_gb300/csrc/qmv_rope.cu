@@ -101,6 +101,7 @@ __global__ void __launch_bounds__(kRopeThreads, ROWS > 1 ? kRopeBlocks : 1) rope
     __shared__ uint64_t s_turn[D / 2];          // a pair's fraction of a turn for each position, times 2^64
     __shared__ uint8_t s_axis[D / 2];
     __shared__ float s_cos[2][D / 2], s_sin[2][D / 2];  // two tokens': one block-wide meeting for each is enough
+    __shared__ __align__(16) float s_weight[2][D];
     __shared__ int64_t s_place[2];                      // where the cache takes them, or -1
     const int tid = threadIdx.x, li = tid % kLanes, half = p.rot / 2;
     const int rows = p.heads + 2 * p.kv_heads, row0 = int(blockIdx.y) * ROWS * kPass + tid / kLanes;
@@ -111,18 +112,26 @@ __global__ void __launch_bounds__(kRopeThreads, ROWS > 1 ? kRopeBlocks : 1) rope
         s_turn[tid] = __double2ull_rn(f * 18446744073709551616.0);
         s_axis[tid] = uint8_t(p.axis ? min(int(__ldg(p.axis + tid)), p.axes - 1) : 0);
     }
+    // norm weights as they are multiplied with, a lane's eight together
+    for (int i = tid; i < D; i += kRopeThreads) {
+        const int l = i / 8, j = i % 8, e = !NEIGHBOURS && l < p.rot / 8 ? (j < 4 ? 4 * l + j : half + 4 * l + j - 4) : i;
+        s_weight[0][i] = p.q_norm ? __fadd_rn(bf16_bits_to_f32(__ldg(p.q_norm + e)), p.one) : 1.0f;
+        s_weight[1][i] = p.k_norm ? __fadd_rn(bf16_bits_to_f32(__ldg(p.k_norm + e)), p.one) : 1.0f;
+    }
     // of halves a lane has four pairs' first elements and their second ones, else eight in a row
     const bool turns = li < p.rot / 8, halves = !NEIGHBOURS && turns;
     const int e0 = halves ? 4 * li : 8 * li, e1 = halves ? half + 4 * li : 8 * li + 4;
-    uint2 wq[2] = {}, wk[2] = {};
-    if (p.q_norm) {
-        wq[0] = __ldg(reinterpret_cast<const uint2 *>(p.q_norm + e0));
-        wq[1] = __ldg(reinterpret_cast<const uint2 *>(p.q_norm + e1));
+    // a row's place beside that of its token, and what is done with it: a query, a key or a value
+    int64_t to[ROWS];
+    uint32_t kinds = 0;  // two bits each: 0 query, 1 key, 2 value, 3 no row
+#pragma unroll
+    for (int k = 0; k < ROWS; ++k) {
+        const int r = row0 + k * kPass, g = r - p.heads;
+        const uint32_t kind = r >= rows ? 3u : g < 0 ? 0u : g < p.kv_heads ? 1u : 2u;
+        kinds |= kind << 2 * k;
+        to[k] = kind == 0 ? int64_t(r) * D : (kind == 2 ? g - p.kv_heads : g) * p.head_stride;
     }
-    if (p.k_norm) {
-        wk[0] = __ldg(reinterpret_cast<const uint2 *>(p.k_norm + e0));
-        wk[1] = __ldg(reinterpret_cast<const uint2 *>(p.k_norm + e1));
-    }
+    const uint8_t *from = static_cast<const uint8_t *>(p.qkv) + int64_t(row0) * D * (F32 ? 4 : 2);
     // the next token's rows, place and position are on their way while a token is worked on
     Octet<F32> ahead[ROWS];
     int64_t slot_ahead = -1;
@@ -131,11 +140,14 @@ __global__ void __launch_bounds__(kRopeThreads, ROWS > 1 ? kRopeBlocks : 1) rope
         if (t >= p.T) return;
 #pragma unroll
         for (int k = 0; k < ROWS; ++k)
-            if (row0 + k * kPass < rows) ahead[k].load(p.qkv, t * p.ld_qkv + (row0 + k * kPass) * D, e0, e1);
+            if ((kinds >> 2 * k & 3) != 3) ahead[k].load(from + t * p.ld_qkv * (F32 ? 4 : 2), k * kPass * D, e0, e1);
         if (tid == kRopeThreads - 1) slot_ahead = p.slots ? __ldg(p.slots + t) : -1;
         if (tid < half) pos_ahead = __ldg(p.positions + (int64_t)s_axis[tid] * p.T + t);
     };
     fetch(blockIdx.x);  // (a thread reads the axis that it wrote)
+    // the lanes of a row, which go one way at each branch on its kind
+    const uint32_t row_lanes = (kLanes == 32 ? 0xffffffffu : (1u << kLanes) - 1u) << (tid & 31 & ~(kLanes - 1));
+    const uint32_t normed = (p.q_norm ? 1u : 0u) | (p.k_norm ? 2u : 0u);
     for (int t = blockIdx.x, n = 0; t < p.T; t += gridDim.x, ++n) {
         Octet<F32> in[ROWS];
 #pragma unroll
@@ -157,51 +169,38 @@ __global__ void __launch_bounds__(kRopeThreads, ROWS > 1 ? kRopeBlocks : 1) rope
             c[j] = turns ? cs[4 * li + j] : 1.0f;
             s[j] = turns ? sn[4 * li + j] : 0.0f;
         }
-        const int64_t place = s_place[n & 1];
+        const int64_t place = s_place[n & 1], token = int64_t(t) * p.heads * D;
 #pragma unroll
         for (int k = 0; k < ROWS; ++k) {
-            const int r = row0 + k * kPass, g = r - p.heads;
-            // (every lane of a warp takes part in the shuffles)
+            const uint32_t kind = kinds >> 2 * k & 3;
             float x[8];
-            if (r < rows)
-                in[k].get(x);
-            else
+            in[k].get(x);
+            if (kind < 2) {
+                // (a row without a norm is multiplied with 1 twice)
+                float sum = 0.0f;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) x[j] = 0.0f;
-            const bool value = g >= p.kv_heads;
-            const uint16_t *norm = g < 0 ? p.q_norm : p.k_norm;
-            float sum = 0.0f;
+                for (int j = 0; j < 8; ++j) sum = __fmaf_rn(x[j], x[j], sum);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) sum = __fmaf_rn(x[j], x[j], sum);
+                for (int d = 1; d < kLanes; d *= 2) sum = __fadd_rn(sum, __shfl_xor_sync(row_lanes, sum, d));
+                const float f = normed >> kind & 1 ? rsqrtf(__fmaf_rn(sum, 1.0f / D, p.eps)) : 1.0f;
+                const float4 w0 = *reinterpret_cast<const float4 *>(&s_weight[kind][8 * li]), w1 = *reinterpret_cast<const float4 *>(&s_weight[kind][8 * li + 4]);
+                const float w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
-            for (int d = 1; d < kLanes; d *= 2) sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, d));
-            if (!value && norm) {
-                float w[8];
-                widen(g < 0 ? wq[0] : wk[0], w);
-                widen(g < 0 ? wq[1] : wk[1], w + 4);
-                const float f = rsqrtf(__fmaf_rn(sum, 1.0f / D, p.eps));
+                for (int j = 0; j < 8; ++j) x[j] = __fmul_rn(__fmul_rn(x[j], f), w[j]);
+                if (turns) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) x[j] = __fmul_rn(__fmul_rn(x[j], f), __fadd_rn(w[j], p.one));
-            }
-            if (!value && turns) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    float &a = x[NEIGHBOURS ? 2 * j : j], &b = x[NEIGHBOURS ? 2 * j + 1 : 4 + j];
-                    const float turned = __fmaf_rn(a, c[j], -__fmul_rn(b, s[j]));
-                    b = __fmaf_rn(b, c[j], __fmul_rn(a, s[j]));
-                    a = turned;
+                    for (int j = 0; j < 4; ++j) {
+                        float &a = x[NEIGHBOURS ? 2 * j : j], &b = x[NEIGHBOURS ? 2 * j + 1 : 4 + j];
+                        const float turned = __fmaf_rn(a, c[j], -__fmul_rn(b, s[j]));
+                        b = __fmaf_rn(b, c[j], __fmul_rn(a, s[j]));
+                        a = turned;
+                    }
                 }
             }
-            if (r >= rows) continue;
-            uint16_t *to;
-            if (g < 0)
-                to = p.q + ((int64_t)t * p.heads + r) * D;
-            else if (place >= 0)
-                to = (value ? p.v_cache : p.k_cache) + place + (value ? g - p.kv_heads : g) * p.head_stride;
-            else
-                continue;
-            *reinterpret_cast<uint2 *>(to + e0) = narrow(x);
-            *reinterpret_cast<uint2 *>(to + e1) = narrow(x + 4);
+            if (kind == 3 || (kind != 0 && place < 0)) continue;
+            uint16_t *at = (kind == 0 ? p.q + token : (kind == 1 ? p.k_cache : p.v_cache) + place) + to[k];
+            *reinterpret_cast<uint2 *>(at + e0) = narrow(x);
+            *reinterpret_cast<uint2 *>(at + e1) = narrow(x + 4);
         }
     }
 }
