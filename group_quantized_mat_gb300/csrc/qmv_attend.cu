@@ -126,13 +126,6 @@ __device__ __forceinline__ float max_scatter(float (&v)[16], int lane)
     return fmaxf(v[0], __shfl_xor_sync(0xffffffffu, v[0], 1));
 }
 
-__device__ __forceinline__ float warp_max(float x)
-{
-#pragma unroll
-    for (int m = 16; m > 0; m /= 2) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, m));
-    return x;
-}
-
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
 {
     uint32_t r;
@@ -981,14 +974,14 @@ __device__ __forceinline__ float tmem_ld1(uint32_t a)
 }
 
 struct PromptShared {
-    uint64_t full[8], empty[8], q_full, q_empty, edge, s_ready[2], p_ready[2], o_done[2], finished;
+    uint64_t full[12], empty[12], q_full, q_empty, edge, s_ready[2], o_done[2], finished;
     int abort;
     uint32_t tmem, there[8];  // (of the last tiles: which eights of keys have a page)
     int4 seqs[1];             // [B], then the sequences' first items [B + 1]
 };
 
-// Hardware barriers: at 1 and 2 the 256 threads of a stream arrive, whose weights are
-// there, and the tensor warp that issues waits for them; at 3 that warp and the one that
+// Hardware barriers: at 1 and 2 the 256 threads of a stream (of one stream: of the even and
+// of the odd tiles) arrive, whose weights are there, and the tensor warp that issues waits for them; at 3 that warp and the one that
 // watches the ring meet; at 4 and 5 the two threads of a row exchange its maximum. (Each barrier has one number of threads for good: one whose
 // number changed from tile to tile would take a warp that is a tile ahead for one of the tile before.)
 constexpr int kMeetWeights = 288, kMeetRing = 64, kMeetRows = 256;
@@ -1011,8 +1004,12 @@ template <int D>
 __global__ void __launch_bounds__(prompt_threads(D), 1)
     attend_prompt(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CacheMaps maps, const AttendParams p)
 {
-    constexpr int STREAMS = D == 256 ? 1 : 2, W = D < 128 ? D : 128;  // elements of a chunk
-    constexpr int DB = D / 64, WB = W / 64, CH = D / W, kBytes = 128 * W * 2;
+    // A chunk of keys is 128 of them, KW elements; one of values VK keys, all elements. (Of
+    // 32 KB each where they can be: with 16 KB of head_dim 256 the tensor warps wait twice as
+    // often, and a prompt with a window took 199 us instead of 163.)
+    constexpr int STREAMS = D == 256 ? 1 : 2, KW = D == 64 ? 64 : 128, VK = D == 256 ? 64 : 128;
+    constexpr int DB = D / 64, kBytes = 128 * KW * 2, KC = D / KW, VC = 128 / VK;  // chunks of a tile
+    static_assert(kBytes == VK * D * 2, "a ring slot holds either");
     constexpr int kThreads = prompt_threads(D), kProducer = kThreads / 32 - 4, kTensor = kProducer + 2;
     extern __shared__ uint8_t raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
@@ -1021,7 +1018,7 @@ __global__ void __launch_bounds__(prompt_threads(D), 1)
     const int tid = threadIdx.x, warp = tid / 32, lane = tid & 31;
     const uint32_t base = smem_u32(smem), full0 = smem_u32(sh.full), empty0 = smem_u32(sh.empty), Q = base + p.q_off;
     const uint32_t q_full = smem_u32(&sh.q_full), q_empty = smem_u32(&sh.q_empty), edge = smem_u32(&sh.edge), finished = smem_u32(&sh.finished);
-    const uint32_t s_ready = smem_u32(sh.s_ready), p_ready = smem_u32(sh.p_ready), o_done = smem_u32(sh.o_done);
+    const uint32_t s_ready = smem_u32(sh.s_ready), o_done = smem_u32(sh.o_done);
     if (tid == 0) {
 #pragma unroll 1
         for (int i = 0; i < p.slots; ++i) {
@@ -1034,7 +1031,6 @@ __global__ void __launch_bounds__(prompt_threads(D), 1)
         mbar_init(finished, 2);
         for (int x = 0; x < 2; ++x) {
             mbar_init(s_ready + 8 * x, 2);  // the scores, and the warp that has seen the keys land
-            mbar_init(p_ready + 8 * x, 8);
             mbar_init(o_done + 8 * x, 1);
         }
         fence_mbar_init();
@@ -1084,17 +1080,6 @@ __global__ void __launch_bounds__(prompt_threads(D), 1)
             if (from == to) continue;
             const Seen seen(p, it.pos, it.pos + it.tokens - 1);
             const int32_t *table = p.table + int64_t(it.b) * p.max_pages;
-            if (!values) {
-                ok = __all_sync(0xffffffffu, n == 0 || wait(q_empty, (n - 1) & 1));
-                if (!ok) break;
-                if (lane == 0) {
-                    const int sets = STREAMS == 2 && it.tokens > p.tokens ? 2 : 1;
-                    mbar_arrive_expect_tx(q_full, uint32_t(sets * p.tokens * p.group) * D * 2);
-                    for (int i = 0; i < sets * DB; ++i)
-                        tile::tma_load_3d(Q + i * 16384, &qmap, i % DB * 64, g * p.group, it.row + i / DB * p.tokens, q_full);
-                }
-                ++n;
-            }
 #pragma unroll 1
             for (int i = from; i < to && ok; ++i, ++brought) {
                 Boxes boxes;
@@ -1102,27 +1087,41 @@ __global__ void __launch_bounds__(prompt_threads(D), 1)
                 if (!values && lane == 0) sh.there[brought & 7] = boxes.there;
                 // Values that no query of the sequence sees may be anything, and 0 x NaN is NaN:
                 // zeros in their place, behind its keys, before its window and behind its first tokens.
-                const int key0 = it.tile(i) * 128;
-                const bool zeros = values && (key0 + 128 > it.keys || (key0 < it.low_all && key0 + 128 > min(p.sinks, it.low_all)));
+                const int chunks = values ? VC : KC;
 #pragma unroll 1
-                for (int c = 0; c < CH; ++c, ++at.issued, at.step()) {
-                    // a chunk: 128 keys, W elements from c W on
-                    if (at.full()) ok = wait(empty0 + 8 * at.slot, at.lap ^ 1);
+                for (int c = 0; c < chunks; ++c, ++at.issued, at.step()) {
+                    const int key0 = it.tile(i) * 128 + c * VK;
+                    const bool zeros = values && (key0 + VK > it.keys || (key0 < it.low_all && key0 + VK > min(p.sinks, it.low_all)));
+                    if (ok && at.full()) ok = wait(empty0 + 8 * at.slot, at.lap ^ 1);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
                     const uint32_t full = full0 + 8 * at.slot, bar = zeros ? edge : full, dst = base + at.slot * kBytes;
                     if (lane == 0) mbar_arrive_expect_tx(bar, kBytes);
                     __syncwarp();
-                    boxes.bring<WB>(map, dst, lane, 0, 16, c * W, 16384, g, bar);
+                    if (values)
+                        boxes.bring<DB>(map, dst, lane, c * (VK / 8), VK / 8, 0, VK * 128, g, bar);
+                    else
+                        boxes.bring<KW / 64>(map, dst, lane, 0, 16, c * KW, 16384, g, bar);
+                    // (an item's queries behind its first keys, which have further to come)
+                    if (!values && i == from && c == 0) {
+                        ok = __all_sync(0xffffffffu, n == 0 || wait(q_empty, (n - 1) & 1));
+                        if (ok && lane == 0) {
+                            const int sets = STREAMS == 2 && it.tokens > p.tokens ? 2 : 1;
+                            mbar_arrive_expect_tx(q_full, uint32_t(sets * p.tokens * p.group) * D * 2);
+                            for (int q = 0; q < sets * DB; ++q)
+                                tile::tma_load_3d(Q + q * 16384, &qmap, q % DB * 64, g * p.group, it.row + q / DB * p.tokens, q_full);
+                        }
+                        n += ok;
+                    }
                     if (zeros) {
                         __syncwarp();
                         ok = __all_sync(0xffffffffu, wait(edge, edges & 1));
                         ++edges;
 #pragma unroll 1
-                        for (int e = lane; e < 128 * 8; e += 32) {
+                        for (int e = lane; e < VK * 8; e += 32) {
                             const int key = key0 + e / 8;
                             if (key < it.keys && (key >= it.low_all || key < p.sinks)) continue;
-                            for (int d = 0; d < WB; ++d) sts_v4_u32(dst + d * 16384 + e * 16, make_uint4(0, 0, 0, 0));
+                            for (int d = 0; d < DB; ++d) sts_v4_u32(dst + d * VK * 128 + e * 16, make_uint4(0, 0, 0, 0));
                         }
                         fence_proxy_async_smem();
                         __syncwarp();
@@ -1142,45 +1141,21 @@ __global__ void __launch_bounds__(prompt_threads(D), 1)
         // --------------------------------------------------------- tensor warps
         // A wait for a barrier in shared memory takes some 300 cycles while products read
         // their operands there, and the tensor cores' queue is short: a warp that waits leaves
-        // them idle. So of two streams the first warp issues products and waits at hardware
-        // barriers alone, where the second comes when what the ring brings is there. (With
-        // a warp for each stream their products slow one another down: 2339 us instead of 2003 for six
-        // prompts.) Of one stream a warp issues the scores and one the sums.
+        // them idle. So the first warp issues products and waits at hardware barriers alone,
+        // where the second comes when what the rings bring is there. (With a warp for
+        // each of two streams their products slow one another down: 2339 us instead of 2003 for six
+        // prompts; of one stream a warp for the scores and one for the sums took 163 us for one
+        // with a window.)
         const int x = warp - kTensor;
         Place keys(0, p.key_slots), values(p.key_slots, p.slots);
-        constexpr uint32_t kValueKind = mma_kind(W, false, true);
+        constexpr uint32_t kValueKind = mma_kind(D, false, true);
         const uint32_t score_kind = mma_kind(128, false, false) | (p.scale < 0.0f ? 1u << 13 : 0u);  // (of the scale's sign: - Q)
         const uint64_t keys0 = descriptor(base, 16, 1024, 2), queries = descriptor(Q, 16, 1024, 2);
-        const uint64_t values0 = descriptor(base, 16384, 1024, 2);
+        const uint64_t values0 = descriptor(base, VK * 128, 1024, 2);
         int n = 0, tiles = 0;
-        const auto scores = [&](int buffer, int set, int b, uint32_t bar, uint32_t more) {
-            wait(full0 + 8 * keys.slot, keys.lap);
-            if (one_lane()) {
-                const uint64_t k0 = keys0 + uint32_t(keys.slot * (kBytes >> 4)), q0 = queries + uint32_t((set * DB + b * WB) * (16384 >> 4));
-#pragma unroll
-                for (int k = 0; k < W / 16; ++k)
-                    mma_ss(score_kind, S + buffer * 128, q0 + (k / 4) * (16384 >> 4) + 2 * (k & 3), k0 + (k / 4) * (16384 >> 4) + 2 * (k & 3), b + k > 0);
-                tmem_commit(empty0 + 8 * keys.slot);
-                if (bar) {
-                    tmem_commit(bar);
-                    mbar_arrive(bar);
-                }
-                if (more) tmem_commit(more);
-            }
-            __syncwarp();
-            keys.step();
-        };
-        const auto sums = [&](int buffer, int o, bool add, uint32_t bar) {
-            wait(full0 + 8 * values.slot, values.lap);
-            if (one_lane()) {
-                const uint64_t v0 = values0 + uint32_t(values.slot * (kBytes >> 4));
-#pragma unroll
-                for (int k = 0; k < 8; ++k) mma_ts<kValueKind>(O + o, S + buffer * 128 + weights_at(k), v0 + k * (2048 >> 4), add || k > 0);
-                tmem_commit(empty0 + 8 * values.slot);
-                if (bar) tmem_commit(bar);
-            }
-            __syncwarp();
-            values.step();
+        const auto landed = [&](Place &at, int chunks) {
+#pragma unroll 1
+            for (int c = 0; c < chunks; ++c, at.step()) wait(full0 + 8 * at.slot, at.lap);
         };
 #pragma unroll 1
         for (int round = 0, index; (index = item_of(round)) < items; ++round) {
@@ -1188,22 +1163,59 @@ __global__ void __launch_bounds__(prompt_threads(D), 1)
             const int from = it.from, to = it.to;
             if (from == to) continue;
             if (STREAMS == 1) {
-                if (x == 0) wait(q_full, n & 1);
+                // S(0), then S(i + 1), O(i)
 #pragma unroll 1
-                for (int i = from; i < to; ++i, ++tiles) {
-                    const int buffer = tiles & 1;
-                    if (x == 0) {
-                        if (tiles >= 2) {
-                            wait(o_done + 8 * buffer, (tiles / 2 - 1) & 1);  // (the buffer's weights of before are used)
-                            tmem_fence_after();
+                for (int i = from; i <= to; ++i) {
+                    if (x) {
+                        if (i == from) wait(q_full, n & 1);
+                        if (i < to) {
+                            landed(keys, KC);
+                            named_sync(3, kMeetRing);
                         }
+                        if (i > from) {
+                            landed(values, VC);
+                            named_sync(3, kMeetRing);
+                        }
+                        continue;
+                    }
+                    if (i < to) {
+                        const int buffer = tiles & 1;
+                        named_sync(3, kMeetRing);
 #pragma unroll 1
-                        for (int c = 0; c < CH; ++c) scores(buffer, 0, c, c == CH - 1 ? s_ready + 8 * buffer : 0u, c == CH - 1 && i == to - 1 ? q_empty : 0u);
-                    } else {
-                        wait(p_ready + 8 * buffer, (tiles / 2) & 1);
+                        for (int c = 0; c < KC; ++c, keys.step()) {
+                            if (one_lane()) {
+                                const uint64_t k0 = keys0 + uint32_t(keys.slot * (kBytes >> 4)), q0 = queries + uint32_t(c * (KW / 64) * (16384 >> 4));
+#pragma unroll
+                                for (int k = 0; k < KW / 16; ++k)
+                                    mma_ss(score_kind, S + buffer * 128, q0 + (k / 4) * (16384 >> 4) + 2 * (k & 3), k0 + (k / 4) * (16384 >> 4) + 2 * (k & 3), c + k > 0);
+                                tmem_commit(empty0 + 8 * keys.slot);
+                                if (c == KC - 1) {
+                                    tmem_commit(s_ready + 8 * buffer);
+                                    mbar_arrive(s_ready + 8 * buffer);
+                                    if (i == to - 1) tmem_commit(q_empty);
+                                }
+                            }
+                            __syncwarp();
+                        }
+                        ++tiles;
+                    }
+                    if (i > from) {
+                        const int buffer = (tiles - (i < to ? 2 : 1)) & 1;
+                        named_sync(1 + buffer, kMeetWeights);
+                        named_sync(3, kMeetRing);
                         tmem_fence_after();
 #pragma unroll 1
-                        for (int c = 0; c < CH; ++c) sums(buffer, c * W, i > from, c == CH - 1 ? o_done + 8 * buffer : 0u);
+                        for (int c = 0; c < VC; ++c, values.step()) {
+                            if (one_lane()) {
+                                const uint64_t v0 = values0 + uint32_t(values.slot * (kBytes >> 4));
+#pragma unroll
+                                for (int k = 0; k < VK / 16; ++k)
+                                    mma_ts<kValueKind>(O, S + buffer * 128 + weights_at(c * (VK / 16) + k), v0 + k * (2048 >> 4), i > from + 1 || c + k > 0);
+                                tmem_commit(empty0 + 8 * values.slot);
+                                if (c == VC - 1) tmem_commit(o_done + 8 * buffer);
+                            }
+                            __syncwarp();
+                        }
                     }
                 }
             } else {
@@ -1253,7 +1265,7 @@ __global__ void __launch_bounds__(prompt_threads(D), 1)
                                 if (next >> s & 1) {
                                     const uint64_t k0 = keys0 + kslot * (kBytes >> 4), q0 = queries + uint32_t(s * DB * (16384 >> 4));
 #pragma unroll
-                                    for (int k = 0; k < W / 16; ++k)
+                                    for (int k = 0; k < KW / 16; ++k)
                                         mma_ss(score_kind, S + s * 128, q0 + (k / 4) * (16384 >> 4) + 2 * (k & 3), k0 + (k / 4) * (16384 >> 4) + 2 * (k & 3), k > 0);
                                     tmem_commit(s_ready + 8 * s);
                                     mbar_arrive(s_ready + 8 * s);
@@ -1382,12 +1394,7 @@ __global__ void __launch_bounds__(prompt_threads(D), 1)
                 }
                 tmem_wait_st();
                 tmem_fence_before();
-                if (STREAMS == 1) {
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(p_ready + 8 * buffer);
-                } else {
-                    named_arrive(1 + x, kMeetWeights);
-                }
+                named_arrive(1 + buffer, kMeetWeights);
                 ++tiles;
                 ++worked;
             }

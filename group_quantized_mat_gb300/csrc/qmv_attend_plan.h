@@ -71,10 +71,11 @@ inline PromptPlan prompt_plan(int B, int T, int max_new, int heads, int kv_heads
     if (max_new <= kFew) return f;
     f.tokens = 128 / (heads / kv_heads);
     f.streams = D == 256 ? 1 : 2;
-    f.chunk = 128 * (D < 128 ? D : 128) * 2;
+    f.chunk = D == 64 ? 16384 : 32768;
     const int q_bytes = f.streams * 128 * D * 2, misc = (512 + B * 16 + (B + 1) * 4 + 1023) & ~1023;
     f.slots = (kSmemBlock - 1024 - q_bytes - misc) / f.chunk;
-    if (f.slots > 8) f.slots = 8;
+    // (keys run four tiles ahead at most, and PromptShared knows of the last eight tiles)
+    if (f.slots > (D == 64 ? 8 : 12)) f.slots = D == 64 ? 8 : 12;
     f.key_slots = (f.slots + 1) / 2;
     f.q_off = f.slots * f.chunk;
     f.misc_off = f.q_off + q_bytes;
