@@ -8,6 +8,7 @@
 #include <cuda_bf16.h>
 
 #include <cmath>
+#include <cstddef>
 #include <cstdint>
 
 #include "qmv.h"
@@ -31,7 +32,6 @@ using tile::tmem_wait_st;
 using tile::Waits;
 
 struct AttendParams {
-    const uint16_t *q, *k, *v;
     const int32_t *table, *q_start, *kv_len;
     uint16_t *out;
     float *lse;
@@ -41,7 +41,7 @@ struct AttendParams {
     int map_code;         // of the largest boxes in use
     float scale;
     int window, sinks;
-    int64_t ld_q, ld_out, page_stride, token_stride, head_stride;
+    int64_t ld_out;
     unsigned *err;
     // the plan, and the workspace's parts
     int items;  // that have a place in the workspace
@@ -245,7 +245,7 @@ __device__ __forceinline__ void tmem_st(uint32_t a, const float (&v)[N])
 struct Item {
     int b, g, block, unit, index;  // index: of the partial sums
     int row, tokens, rows;         // first row of q, its tokens and columns
-    int pos, n;                    // position of the first token; of the last: pos + tokens - 1
+    int pos;                       // position of the first token; of the last: pos + tokens - 1
     int leaf, leaves;
     bool whole;                    // the sequence has one unit
 };
@@ -366,6 +366,8 @@ struct Place {
     __device__ __forceinline__ bool full() const { return issued >= end - first; }
 };
 
+static_assert(offsetof(FewShared<16>, seqs) <= few_misc(16) && offsetof(FewShared<32>, seqs) <= few_misc(32) && offsetof(FewShared<64>, seqs) <= few_misc(64), "the plan's room for it");
+
 __host__ __device__ constexpr int few_threads(int NC) { return NC / 16 * 128 + 128; }
 
 // What the first loads need, on its way into the caches while the sequences' lengths are.
@@ -424,7 +426,6 @@ __global__ void __launch_bounds__(few_threads(NC), D < 256 && NC == 16 ? 2 : 1)
     if (warp == kTensor) tile::tmem_alloc(smem_u32(&sh.tmem), kAlloc);
     if (tid == 0) prefetch_maps(qmap, maps, p);
     grid_dependency_wait();
-    grid_launch_dependents();  // (what comes next may read what was there before this kernel)
     prefetch_table(p, tid);
 #pragma unroll 1
     for (int b = tid; b < p.B; b += kThreads) {
@@ -436,6 +437,9 @@ __global__ void __launch_bounds__(few_threads(NC), D < 256 && NC == 16 ? 2 : 1)
     tmem_fence_before();
     __syncthreads();
     tmem_fence_after();
+    // What comes next may read what was there before this kernel. (And not before the block has
+    // its tensor memory: a block of the next kernel that took it would wait for this one.)
+    grid_launch_dependents();
     if (warp == 0) sum_firsts(first, p.B, p.items, lane);
     __syncthreads();
     const uint32_t tm = sh.tmem, S = tm, O = tm + 2 * kScores;
@@ -731,7 +735,7 @@ __global__ void __launch_bounds__(few_threads(NC), D < 256 && NC == 16 ? 2 : 1)
                 const int r = c0 + mine;
                 const float t = __fadd_rn(__fadd_rn(sh.sum[0][r], sh.sum[1][r]), __fadd_rn(sh.sum[2][r], sh.sum[3][r]));
                 if (it.whole) {
-                    const bool none = sh.ref[r] == -INFINITY;
+                    const bool none = t == 0.0f;  // (not one whose scores are NaN, which stay it)
                     sh.total[r] = none ? 0.0f : __fdiv_rn(1.0f, t);
                     if (p.lse)
                         p.lse[int64_t(it.row + token) * p.heads + it.g * p.group + head] = none ? -INFINITY : __fmul_rn(0.6931471805599453f, __fadd_rn(sh.ref[r], log2f(t)));
@@ -837,7 +841,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attend_join(const AttendParam
         total = __fmaf_rn(s_total[w], f, total);
         if (threadIdx.x < D) o = __fmaf_rn(s_sum[w][threadIdx.x], f, o);
     }
-    const bool none = all == -INFINITY;
+    const bool none = total == 0.0f;
     const int64_t row = s.row + i;
     if (threadIdx.x < D)
         reinterpret_cast<__nv_bfloat16 *>(p.out)[row * p.ld_out + h * D + threadIdx.x] = __float2bfloat16_rn(none ? 0.0f : __fdiv_rn(o, total));
@@ -979,6 +983,7 @@ struct PromptShared {
     uint32_t tmem, there[8];  // (of the last tiles: which eights of keys have a page)
     int4 seqs[1];             // [B], then the sequences' first items [B + 1]
 };
+static_assert(offsetof(PromptShared, seqs) <= kPromptMisc, "the plan's room for it");
 
 // Hardware barriers: at 1 and 2 the 256 threads of a stream (of one stream: of the even and
 // of the odd tiles) arrive, whose weights are there, and the tensor warp that issues waits for them; at 3 that warp and the one that
@@ -1036,11 +1041,10 @@ __global__ void __launch_bounds__(prompt_threads(D), 1)
         fence_mbar_init();
         sh.abort = 0;
     }
+    if (warp == kTensor) tile::tmem_alloc(smem_u32(&sh.tmem), 512);
     if (tid == 0) prefetch_maps(qmap, maps, p);
     grid_dependency_wait();
-    grid_launch_dependents();
     prefetch_table(p, tid);
-    if (warp == kTensor) tile::tmem_alloc(smem_u32(&sh.tmem), 512);
 #pragma unroll 1
     for (int b = tid; b < p.B; b += kThreads) {
         const Sequence s(p, b);
@@ -1052,6 +1056,7 @@ __global__ void __launch_bounds__(prompt_threads(D), 1)
     tmem_fence_before();
     __syncthreads();
     tmem_fence_after();
+    grid_launch_dependents();  // (behind the allocation, as in attend_few)
     if (warp == 0) sum_firsts(first, p.B, p.items, lane);
     __syncthreads();
     if (blockIdx.x == 0 && p.pieces > 1)
@@ -1418,7 +1423,7 @@ __global__ void __launch_bounds__(prompt_threads(D), 1)
                 const float theirs = tmem_ld1(O + lanes + x * D + (1 - half) * (D / 2));
                 sum = half ? __fadd_rn(theirs, sum) : __fadd_rn(sum, theirs);
             }
-            const bool none = ref == -INFINITY;
+            const bool none = sum == 0.0f;  // (not one whose scores are NaN, which stay it)
             const int64_t row = it.row + x * p.tokens + r / p.group;
             const int head = it.g * p.group + r % p.group;
             const int64_t part = (int64_t(it.index) * STREAMS + x) * 128 + r;
@@ -1494,7 +1499,7 @@ __global__ void __launch_bounds__(256) attend_join_pieces(const AttendParams p)
 #pragma unroll
             for (int e = 0; e < E; ++e) sum[e] = __fmaf_rn(p.parts[at * D + lane + 32 * e], w, sum[e]);
         }
-        const bool none = top == -INFINITY;
+        const bool none = total == 0.0f;
 #pragma unroll
         for (int e = 0; e < E; ++e)
             reinterpret_cast<__nv_bfloat16 *>(p.out)[t * p.ld_out + h * D + lane + 32 * e] = __float2bfloat16_rn(none ? 0.0f : __fdiv_rn(sum[e], total));
@@ -1613,21 +1618,21 @@ extern "C" qmv_status qmv_attend_run(const uint16_t *q, const uint16_t *k_cache,
     if (st != QMV_OK) return st;
 
     AttendParams p{};
-    p.q = q; p.k = k_cache; p.v = v_cache; p.table = page_table; p.q_start = q_start; p.kv_len = kv_len;
+    p.table = page_table; p.q_start = q_start; p.kv_len = kv_len;
     p.out = out; p.lse = lse;
     p.B = B; p.T = T; p.max_new = max_new; p.heads = heads; p.group = heads / kv_heads;
     p.page_size = page_size; p.pages = pages; p.max_pages = max_pages;
     p.scale = scale; p.window = window; p.sinks = sinks;
-    p.ld_q = ld_q; p.ld_out = ld_out;
-    p.page_stride = page_stride; p.token_stride = token_stride; p.head_stride = head_stride;
+    p.ld_out = ld_out;
     p.kv_heads = kv_heads;
     p.err = dev.err;
     const FewPlan f = few_plan(B, max_new, heads, kv_heads, head_dim, int64_t(max_pages) * page_size, window, sinks);
     p.items = int(f.items);
-    p.tokens = f.tokens; p.blocks = f.blocks; p.rows = f.rows; p.units = f.units; p.unit_shift = f.unit == kLeaf ? 8 : f.unit == 2 * kLeaf ? 9 : 10; p.slots = f.slots; p.key_slots = f.key_slots; p.q_sets = f.q_sets;
+    p.tokens = f.tokens; p.blocks = f.blocks; p.rows = f.rows; p.units = f.units;
+    p.unit_shift = f.unit == kLeaf ? 8 : f.unit == 2 * kLeaf ? 9 : 10;
+    p.slots = f.slots; p.key_slots = f.key_slots; p.q_sets = f.q_sets;
     p.p_off = f.p_off; p.q_off = f.q_off; p.misc_off = f.misc_off;
     uint8_t *at = static_cast<uint8_t *>(ws);
-    p.prefix = reinterpret_cast<int32_t *>(at + f.prefix_off);
     p.meta = reinterpret_cast<float2 *>(at + f.meta_off);
     p.parts = reinterpret_cast<float *>(at + f.parts_off);
     p.page_magic = ((uint64_t(1) << 42) + page_size - 1) / page_size;

@@ -28,10 +28,14 @@ struct FewPlan {
     int unit;     // keys of one item, from a multiple of it on
     int units;    // of a sequence at most
     int64_t items;
-    size_t prefix_off, meta_off, parts_off, workspace;
+    size_t meta_off, parts_off, workspace;
 };
 
 inline size_t up256(size_t b) { return (b + 255) & ~size_t(255); }
+
+// What lies before the sequences in shared memory: barriers, columns' maxima, sums and places.
+constexpr int few_misc(int columns) { return 512 + columns * 4 * 18; }
+constexpr int kPromptMisc = 512;
 
 // Fixed shared memory behind the ring: weights of a leaf (two bf16 terms), two items' queries,
 // then barriers, maxima, sums and the sequences.
@@ -39,7 +43,7 @@ inline void few_smem(FewPlan &f, int D, int B, bool alone)
 {
     f.q_sets = D == 256 && f.columns == 64 ? 1 : 2;
     const int p_bytes = kLeaf * f.columns * 4, q_bytes = f.q_sets * f.columns * D * 2;
-    const int misc = 512 + f.columns * 4 * 18 + B * 16 + (B + 1) * 4;
+    const int misc = few_misc(f.columns) + B * 16 + (B + 1) * 4;
     const int fixed = p_bytes + q_bytes + ((misc + 1023) & ~1023);
     // (a tile's values, D / 64 slots, have to be there at once: see the zeroing of unseen rows)
     const int least = D / 64 + 2 > 5 ? D / 64 + 2 : 5, two = (kSmemSm / 2 - kSmemReserved - 1024 - fixed) / kChunk;
@@ -72,7 +76,7 @@ inline PromptPlan prompt_plan(int B, int T, int max_new, int heads, int kv_heads
     f.tokens = 128 / (heads / kv_heads);
     f.streams = D == 256 ? 1 : 2;
     f.chunk = D == 64 ? 16384 : 32768;
-    const int q_bytes = f.streams * 128 * D * 2, misc = (512 + B * 16 + (B + 1) * 4 + 1023) & ~1023;
+    const int q_bytes = f.streams * 128 * D * 2, misc = (kPromptMisc + B * 16 + (B + 1) * 4 + 1023) & ~1023;
     f.slots = (kSmemBlock - 1024 - q_bytes - misc) / f.chunk;
     // (keys run four tiles ahead at most, and PromptShared knows of the last eight tiles)
     if (f.slots > (D == 64 ? 8 : 12)) f.slots = D == 64 ? 8 : 12;
@@ -125,10 +129,9 @@ inline FewPlan few_plan(int B, int max_new, int heads, int kv_heads, int D, int6
     f.items = int64_t(B) * kv_heads * f.blocks * units;
     // (a ring that holds a whole leaf where every item has an SM for itself)
     few_smem(f, D, B, f.items <= 152);
-    f.prefix_off = 0;
-    f.meta_off = up256(size_t(B + 1) * 4);
-    f.parts_off = f.meta_off + up256(size_t(f.items) * f.rows * 8);
-    f.workspace = f.units > 1 ? f.parts_off + up256(size_t(f.items) * f.rows * D * 4) : f.meta_off;
+    f.meta_off = 0;
+    f.parts_off = up256(size_t(f.items) * f.rows * 8);
+    f.workspace = f.units > 1 ? f.parts_off + up256(size_t(f.items) * f.rows * D * 4) : 256;  // (0 would be a refusal)
     return f;
 }
 

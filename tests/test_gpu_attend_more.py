@@ -72,6 +72,19 @@ def test_unseen_keys_of_pages_that_are_seen(new, window, sinks):
     b.check(b.run(window=window, sinks=sinks), window=window, sinks=sinks)
 
 
+@pytest.mark.parametrize("heads,kv,D", [(8, 2, 128), (4, 4, 64), (10, 2, 256)])
+@pytest.mark.parametrize("new,keys", [([1, 3], [5, 700]), ([2, 16], [2, 6000]), ([40, 300], [700, 300]), ([33], [9000])])
+def test_queries_that_are_not_numbers(heads, kv, D, new, keys):
+    """A query with a NaN has NaN as its result, and leaves the others' as they are."""
+    a, b = (Problem(new, keys, heads, kv, D, seed=27) for _ in range(2))
+    bad = torch.zeros(a.T, heads, dtype=torch.bool)
+    bad[::3, 1] = bad[1::4, heads - 1] = True
+    a.q[bad] = math.nan
+    got, want = a.run(), b.run()
+    assert all(torch.isnan(x[bad]).all() for x in got)
+    assert same([x[~bad] for x in got], [x[~bad] for x in want])
+
+
 def test_lists_that_make_no_sense():
     """Rows, lengths and pages out of range or of several sequences: what comes out means nothing, but nothing else is touched."""
     gen = torch.Generator().manual_seed(26)
