@@ -95,6 +95,19 @@ __device__ __forceinline__ bool one_lane()
     return p != 0;
 }
 
+// Has the phase of that parity ended? (Asked ahead of a wait, whose answer takes some 300 cycles
+// while products read shared memory.)
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity)
+{
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return done != 0;
+}
+
 __device__ __forceinline__ float exp2_fast(float x)
 {
     float y;
@@ -228,19 +241,25 @@ __device__ __forceinline__ void tmem_st(uint32_t a, const float (&v)[N])
 //   P^T = exp2(S^T scale log2(e) - m)             a thread has a key, in registers
 //   O^T (head_dim x columns)     += V^T P^T       V from shared memory as it lies in the cache
 //
-// both by tcgen05, keys and values brought by TMA through a ring of 16 KB slots. The
-// products' cost does not depend on how few columns are in use, and it is hidden: the
-// bytes of K and V are what bounds it. P is kept in two bf16 terms (16 bits of it), as
-// 2 x columns columns of one product, so that the weights' rounding is below that of
-// fp32 sums' order.
+// both by tcgen05, keys and values brought by TMA through a ring of 16 KB slots. Keys as
+// rows, because a product's time hardly depends on how few columns there are (128 rows and 16
+// columns 52 cycles, 128 columns 66), and K and V go into it as they lie. P is kept in two bf16
+// terms (16 bits of it), as 2 x columns columns of one product, so that the weights' rounding
+// is below that of fp32 sums' order.
+//
+// What bounds it: with 16 columns the bytes of K and V (64 sequences of 8192 keys, 8 kv heads of
+// 128: 246 us, 98 % of the rate of a copy; the tensor cores are busy for 7 %), of a few thousand
+// keys the chain of two launches, the first loads and the join (4100 keys: 14 us, of which the
+// bytes are 2.5), with 64 columns the weights (13 tokens of 8 heads over 131000 keys: 104 us, the
+// bytes 40: 64 x 256 exponentials, each split in two terms, a leaf of 128 KB).
 //
 // Order. A work item is a unit of 256, 512 or 1024 keys (see few_plan), from a multiple of
-// that on, in leaves of 256,
-// whose products are added in the order of keys; a column's reference m is a whole
-// number, 8 above the largest score when it is set, and moves only when a score passes it:
-// a change of m scales by powers of two without a rounding, weights are at most 1. Units are joined by attend_join in an order given by
-// their places. So a row's result depends on its query and the keys that it sees alone:
-// not on the other tokens of the call, nor on how many SMs there are.
+// that on, in leaves of 256, whose products are added in the order of keys. A column's reference
+// m is a whole number, 8 above the largest score when it is set, and moves only when a score
+// passes it: a change of m scales by powers of two without a rounding, and weights are at most
+// 1. Units are joined by attend_join in an order given by their places. So a row's result
+// depends on its query and the keys that it sees alone: not on the other tokens of the call, nor
+// on how many SMs there are.
 
 struct Item {
     int b, g, block, unit, index;  // index: of the partial sums
@@ -339,9 +358,10 @@ __device__ __forceinline__ Item item_at(const AttendParams &p, const Sequences &
 template <int NC>
 struct FewShared {
     uint64_t full[16], empty[16], q_full[2], q_empty[2], s_ready[2], p_ready[4], o_done, finished;
-    int abort, changed[NC / 16][2];
+    int abort;
     uint32_t tmem;
-    float top[4][NC], sum[4][NC], ref[NC], use[NC], shift[NC], total[NC];
+    float4 top[2][NC];  // a column's largest score in each of four warps, of a leaf and the next
+    float sum[4][NC], total[NC];
     int last[NC], low[NC];  // a column sees keys up to `last` and from `low` on
     int64_t out[NC];        // where its sums go
     uint32_t there[8];      // of the last leaves: which eights of keys have a page
@@ -422,7 +442,6 @@ __global__ void __launch_bounds__(few_threads(NC), D < 256 && NC == 16 ? 2 : 1)
         fence_mbar_init();
         sh.abort = 0;
     }
-    if (tid < NC / 16) sh.changed[tid][0] = sh.changed[tid][1] = 0;
     if (warp == kTensor) tile::tmem_alloc(smem_u32(&sh.tmem), kAlloc);
     if (tid == 0) prefetch_maps(qmap, maps, p);
     grid_dependency_wait();
@@ -519,10 +538,13 @@ __global__ void __launch_bounds__(few_threads(NC), D < 256 && NC == 16 ? 2 : 1)
 #pragma unroll 1
             for (int i = 0; i < kChunks; ++i, at.step()) {
                 if (i % DB == 0) {
+                    // (a tile's values first: they come before its weights)
+                    Place next = at;
+#pragma unroll 1
+                    for (int c = 0; c < DB; ++c, next.step()) wait(full0 + 8 * next.slot, next.lap);
                     wait(p_ready + 16 * (leaf & 1) + 8 * (i / DB), (leaf / 2) & 1);
                     tmem_fence_after();
                 }
-                wait(full0 + 8 * at.slot, at.lap);
                 constexpr int kKeys = D == 64 ? 128 : 64;
                 const int c = i % HALVES, key = i / HALVES * kKeys;
                 if (one_lane()) {
@@ -594,20 +616,20 @@ __global__ void __launch_bounds__(few_threads(NC), D < 256 && NC == 16 ? 2 : 1)
             const Seen seen(p, it.pos, it.pos + it.tokens - 1);
             if (mine < 16) {
                 const int r = column, pos = it.pos + token;
-                sh.ref[r] = -INFINITY;
                 sh.last[r] = r < it.rows ? pos : -1;
                 sh.low[r] = p.window ? pos - p.window + 1 : 0;
                 sh.out[r] = (it.row + token) * p.ld_out + (it.g * p.group + head) * D;
             }
-            float sum[16];
+            float sum[16], ref = -INFINITY;  // ref: of column c0 + lane % 16, in each warp
 #pragma unroll
             for (int i = 0; i < 16; ++i) sum[i] = 0.0f;
             named_sync(meet, 128);
+            bool scored = false;  // are the next leaf's scores there already?
 #pragma unroll 1
             for (int l = 0; l < it.leaves; ++l, ++leaf) {
                 const int key0 = (it.leaf + l) * kLeaf + mine;
                 const uint32_t scores = S + (leaf & 1) * kScores + lanes + c0;
-                wait(s_ready + 8 * (leaf & 1), (leaf / 2) & 1);
+                if (!scored) wait(s_ready + 8 * (leaf & 1), (leaf / 2) & 1);
                 tmem_fence_after();
                 uint32_t see[2] = {0xffffu, 0xffffu};  // which columns see the key
                 // (keys whose page is there, as the producer found it)
@@ -636,34 +658,30 @@ __global__ void __launch_bounds__(few_threads(NC), D < 256 && NC == 16 ? 2 : 1)
                     s1[i] = see[1] >> i & 1 ? __fmul_rn(s1[i], c2) : -INFINITY;
                     top[i] = fmaxf(s0[i], s1[i]);
                 }
-                const float m = max_scatter(top, lane);
                 // (lanes 2 i and 2 i + 1 have the largest of column i)
-                if (!(lane & 1)) sh.top[quarter][c0 + lane / 2] = m;
+                const float most = max_scatter(top, lane);
+                if (!(lane & 1)) (&sh.top[leaf & 1][c0 + lane / 2].x)[quarter] = most;
+                const bool summed = leaf == 0 || mbar_test(o_done, (leaf - 1) & 1);
                 named_sync(meet, 128);
-                if (mine < 16) {
-                    const int r = c0 + mine;
-                    float m = fmaxf(fmaxf(sh.top[0][r], sh.top[1][r]), fmaxf(sh.top[2][r], sh.top[3][r]));
-                    if (r >= it.rows) m = -INFINITY;  // (a column without a query)
-                    const float old = sh.ref[r];
-                    // above the largest score, and kept while it is
-                    const float now = m > old ? __fadd_rn(ceilf(m), 8.0f) : old;
-                    sh.ref[r] = now;
-                    sh.use[r] = now == -INFINITY ? 0.0f : now;
-                    const bool moved = now != old && old != -INFINITY;
-                    sh.shift[r] = moved ? power_of_two(__fsub_rn(old, now)) : 1.0f;
-                    if (moved) sh.changed[group][leaf & 1] = 1;
-                }
-                if (mine == 127) sh.changed[group][(leaf + 1) & 1] = 0;
-                // the last leaf's products are done: P is free, O stands still
-                if (leaf > 0) wait(o_done, (leaf - 1) & 1);
-                named_sync(meet, 128);
-                if (l > 0 && sh.changed[group][leaf & 1]) {
-                    float f[16];
+                const float4 four = sh.top[leaf & 1][c0 + (lane & 15)];
+                // (a column without a query has none)
+                const float m = c0 + (lane & 15) < it.rows ? fmaxf(fmaxf(four.x, four.y), fmaxf(four.z, four.w)) : -INFINITY;
+                // above the largest score, and kept while it is
+                const float now = m > ref ? __fadd_rn(ceilf(m), 8.0f) : ref;
+                const bool moved = now != ref && ref != -INFINITY;
+                const float shift = moved ? power_of_two(__fsub_rn(ref, now)) : 1.0f;
+                ref = now;
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        f[i] = sh.shift[c0 + i];
-                        sum[i] = __fmul_rn(sum[i], f[i]);
-                    }
+                for (int i = 0; i < 16; ++i) {
+                    const float use = __shfl_sync(0xffffffffu, now == -INFINITY ? 0.0f : now, i);
+                    s0[i] = __fsub_rn(s0[i], use);
+                    s1[i] = __fsub_rn(s1[i], use);
+                }
+                // the last leaf's products are done: P is free, O stands still
+                if (!summed) wait(o_done, (leaf - 1) & 1);
+                if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) sum[i] = __fmul_rn(sum[i], __shfl_sync(0xffffffffu, shift, i));
                     tmem_fence_after();
 #pragma unroll 1
                     for (int c = 0; c < 2 * HALVES; ++c) {
@@ -672,18 +690,19 @@ __global__ void __launch_bounds__(few_threads(NC), D < 256 && NC == 16 ? 2 : 1)
                         tmem_wait_ld();
                         settle(o);
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) o[i] = __fmul_rn(o[i], f[i]);
+                        for (int i = 0; i < 16; ++i) o[i] = __fmul_rn(o[i], __shfl_sync(0xffffffffu, shift, i));
                         tmem_st<16>(O + lanes + c * NC + c0, o);
                     }
                     tmem_wait_st();
                 }
+                scored = l + 1 < it.leaves && mbar_test(s_ready + 8 * ((leaf + 1) & 1), ((leaf + 1) / 2) & 1);
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     float(&w)[16] = h ? s1 : s0;
                     const int k = h * 128 + mine;
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
-                        w[i] = exp2_fast(__fsub_rn(w[i], sh.use[c0 + i]));
+                        w[i] = exp2_fast(w[i]);
                         sum[i] = __fadd_rn(sum[i], w[i]);
                     }
                     uint32_t hi[8], lo[8];
@@ -738,9 +757,9 @@ __global__ void __launch_bounds__(few_threads(NC), D < 256 && NC == 16 ? 2 : 1)
                     const bool none = t == 0.0f;  // (not one whose scores are NaN, which stay it)
                     sh.total[r] = none ? 0.0f : __fdiv_rn(1.0f, t);
                     if (p.lse)
-                        p.lse[int64_t(it.row + token) * p.heads + it.g * p.group + head] = none ? -INFINITY : __fmul_rn(0.6931471805599453f, __fadd_rn(sh.ref[r], log2f(t)));
+                        p.lse[int64_t(it.row + token) * p.heads + it.g * p.group + head] = none ? -INFINITY : __fmul_rn(0.6931471805599453f, __fadd_rn(ref, log2f(t)));
                 } else {
-                    p.meta[int64_t(it.index) * p.rows + r] = make_float2(sh.ref[r], t);
+                    p.meta[int64_t(it.index) * p.rows + r] = make_float2(ref, t);
                 }
             }
             if (it.leaves > 0) wait(o_done, (leaf - 1) & 1);
@@ -787,7 +806,7 @@ __global__ void __launch_bounds__(few_threads(NC), D < 256 && NC == 16 ? 2 : 1)
 
 // Joins a row's units: their sums times powers of two that bring them to one reference,
 // those of places u = w, w + 8, .. by warp w in order, then the warps' in order. A block
-// has a row.
+// has a row. (It starts under attend_few, and reads what that left in L2.)
 constexpr int kJoinWarps = 8;
 template <int D>
 __global__ void __launch_bounds__(kJoinWarps * 32) attend_join(const AttendParams p)
@@ -852,7 +871,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attend_join(const AttendParam
 // ----------------------------------------------------------------- prompts --
 //
 // Sequences of more new tokens than that. Query rows (tokens x heads of one kv head) are rows,
-// 128 to a tile, a thread each:
+// 128 to a tile, two threads each:
 //
 //   S (rows x keys)      = Q K^T      from shared memory
 //   P = exp2(S |scale| log2(e) - m)   in registers, then bf16 in tensor memory in S's place
@@ -860,10 +879,15 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attend_join(const AttendParam
 //
 // Two tiles of rows take turns (of head_dim 256, whose sums fill half of tensor
 // memory, two tiles of keys): the tensor cores work on one while the weights of the
-// other are formed. What bounds it is the products, 4 x head_dim operations for each
-// pair of row and key; a tile's exponentials take half as long.
-// m is a whole number as above, so that sums are rarely scaled, and exactly. The weights are rounded to bf16 (2^-8 of each,
-// as an operand next to bf16 values has to be); their total is not.
+// other are formed. What bounds it is the products, 4 x head_dim operations for each pair of
+// row and key, and the loads of scores from tensor memory, which wait for them (64 columns: 650
+// to 880 cycles while products run). Six prompts of 8192 tokens, 40 heads of 128: 1918 us, 64 % of
+// the measured rate of bf16 products, counting the pairs that are seen alone; 8000 tokens of 16
+// heads of 256 with a window of 1024: 157 us. (One thread for a row took 2 to 7 % longer. Some
+// of the exponentials by polynomials: slower, the exponentials' unit is busy for 28 %.)
+//
+// m is a whole number as above, so that sums are rarely scaled, and exactly. The weights are
+// rounded to bf16 (2^-8 of each, as an operand next to bf16 values has to be); their total is not.
 //
 // Items go from a sequence's last rows, which see the most keys, to its first. Where there are
 // too few of them the keys are divided into pieces, which attend_join_pieces joins in
@@ -985,10 +1009,11 @@ struct PromptShared {
 };
 static_assert(offsetof(PromptShared, seqs) <= kPromptMisc, "the plan's room for it");
 
-// Hardware barriers: at 1 and 2 the 256 threads of a stream (of one stream: of the even and
-// of the odd tiles) arrive, whose weights are there, and the tensor warp that issues waits for them; at 3 that warp and the one that
-// watches the ring meet; at 4 and 5 the two threads of a row exchange its maximum. (Each barrier has one number of threads for good: one whose
-// number changed from tile to tile would take a warp that is a tile ahead for one of the tile before.)
+// Hardware barriers: at 1 and 2 the 256 threads of a stream (of one stream: of the even and of
+// the odd tiles) arrive, whose weights are there, and the tensor warp that issues waits for them;
+// at 3 that warp and the one that watches the ring meet; at 4 and 5 the two threads of a row
+// exchange its maximum. (Each barrier has one number of threads for good: one whose number
+// changed from tile to tile would take a warp that is a tile ahead for one of the tile before.)
 constexpr int kMeetWeights = 288, kMeetRing = 64, kMeetRows = 256;
 __device__ __forceinline__ void named_arrive(int id, int threads) { asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
 
@@ -1466,7 +1491,9 @@ __global__ void __launch_bounds__(prompt_threads(D), 1)
     if (warp == kTensor) tile::tmem_free(tm, 512);
 }
 
-// Joins a row's pieces in order; a warp has a row.
+// Joins a row's pieces in order; a warp has a row. (Two chunks of 512 tokens over 16500 keys,
+// 40 heads and 8 kv heads, are 176 items, too few for 152 SMs to share evenly; in four pieces
+// each they are not.)
 template <int D>
 __global__ void __launch_bounds__(256) attend_join_pieces(const AttendParams p)
 {
