@@ -85,6 +85,9 @@ struct Seen {
 // The page of a key, key / page_size: exact for keys below 2^26 and page sizes up to 2^16.
 __device__ __forceinline__ int page_of(const AttendParams &p, int key) { return int(uint64_t(unsigned(key)) * p.page_magic >> 42); }
 
+// Bits 0 .. n - 1.
+__device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
+
 // One lane of a converged warp, for the instructions that a single thread issues. (With a
 // plain lane == 0 the compiler does not know that one thread is left, and a step of four
 // products took some 800 cycles.)
@@ -362,7 +365,6 @@ struct FewShared {
     uint32_t tmem;
     float4 top[2][NC];  // a column's largest score in each of four warps, of a leaf and the next
     float sum[4][NC], total[NC];
-    int last[NC], low[NC];  // a column sees keys up to `last` and from `low` on
     int64_t out[NC];        // where its sums go
     uint32_t there[8];      // of the last leaves: which eights of keys have a page
     int4 seqs[1];           // [B], then the sequences' first items [B + 1]
@@ -615,9 +617,7 @@ __global__ void __launch_bounds__(few_threads(NC), D < 256 && NC == 16 ? 2 : 1)
             const Item it = item_at(p, all, index);
             const Seen seen(p, it.pos, it.pos + it.tokens - 1);
             if (mine < 16) {
-                const int r = column, pos = it.pos + token;
-                sh.last[r] = r < it.rows ? pos : -1;
-                sh.low[r] = p.window ? pos - p.window + 1 : 0;
+                const int r = column;
                 sh.out[r] = (it.row + token) * p.ld_out + (it.g * p.group + head) * D;
             }
             float sum[16], ref = -INFINITY;  // ref: of column c0 + lane % 16, in each warp
@@ -638,12 +638,10 @@ __global__ void __launch_bounds__(few_threads(NC), D < 256 && NC == 16 ? 2 : 1)
                 if (!(there0 && there1 && key0 + 128 <= it.pos && (!p.window || key0 >= it.pos + it.tokens - p.window))) {
 #pragma unroll 1
                     for (int h = 0; h < 2; ++h) {
-                        const int key = key0 + 128 * h;
-                        uint32_t bits = 0;
-#pragma unroll 4
-                        for (int i = 0; i < 16; ++i)
-                            if (key <= sh.last[c0 + i] && (key >= sh.low[c0 + i] || key < p.sinks)) bits |= 1u << i;
-                        (h ? see[1] : see[0]) = (h ? there1 : there0) ? bits : 0u;
+                        // of tokens from `from` to below `to`, whose columns lie side by side
+                        const int key = key0 + 128 * h, from = min(max(key - it.pos, 0), it.tokens);
+                        const int to = p.window && key >= p.sinks ? max(min(key - it.pos + p.window, it.tokens), 0) : it.tokens;
+                        (h ? see[1] : see[0]) = (h ? there1 : there0) ? below(to * p.group - c0) & ~below(from * p.group - c0) : 0u;
                     }
                 }
                 float s0[16], s1[16], top[16];
@@ -726,18 +724,22 @@ __global__ void __launch_bounds__(few_threads(NC), D < 256 && NC == 16 ? 2 : 1)
                     // right only when the lap before has landed and while the lap itself is not
                     // consumed: the leaf before's values have been used, the second tile's
                     // come after the first's. A tile's values fit in the ring at once.)
-                    const bool seen_key = h ? there1 : there0;
+                    const uint32_t unseen = __ballot_sync(0xffffffffu, !(h ? there1 : there0));  // of the warp's keys
                     if (group == 0 && !__all_sync(0xffffffffu, there0 && there1)) {
                         const int from = leaf * kChunks + h * DB, slots = p.slots - p.key_slots;
 #pragma unroll 1
                         for (int c = 0; c < DB; ++c) {
                             const int slot = p.key_slots + (from + c) % slots;
                             wait(full0 + 8 * slot, ((from + c) / slots) & 1);
-                            // does the chunk hold 64 elements (of head_dim 64) or 128 of the thread's key?
-                            if (seen_key || (D > 64 && c / HALVES != mine / 64)) continue;
-                            const uint32_t at = base + slot * kChunk + (D == 64 ? mine : mine & 63) * 128;
+                            // does the chunk hold 64 elements (of head_dim 64) or 128 of the warp's keys?
+                            if (unseen == 0 || (D > 64 && c / HALVES != mine / 64)) continue;
+                            // (the warp's 32 rows, four at a time: a row by each lane has bank conflicts, and a
+                            // window's first leaf took 5500 cycles)
+                            const uint32_t at = base + slot * kChunk + (quarter & (D == 64 ? 3 : 1)) * 4096 + lane * 16;
 #pragma unroll 1
-                            for (int i = 0; i < (D == 64 ? 8 : 16); ++i) sts_v4_u32(at + (i & 7) * 16 + (i >> 3) * 8192, make_uint4(0, 0, 0, 0));
+                            for (int i = 0; i < 8; ++i)
+                                if (unseen >> (4 * i + lane / 8) & 1)
+                                    for (int d = 0; d < (D == 64 ? 1 : 2); ++d) sts_v4_u32(at + i * 512 + d * 8192, make_uint4(0, 0, 0, 0));
                         }
                     }
                     tmem_fence_before();
@@ -967,9 +969,6 @@ __device__ __forceinline__ Seen stream_sees(const AttendParams &p, const PromptI
     if (tokens == 0) seen.end = 0;
     return seen;
 }
-
-// Bits 0 .. n - 1.
-__device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
 
 __device__ __forceinline__ void hide(float (&s)[32], uint32_t see)
 {

@@ -34,7 +34,7 @@ struct FewPlan {
 inline size_t up256(size_t b) { return (b + 255) & ~size_t(255); }
 
 // What lies before the sequences in shared memory: barriers, columns' maxima, sums and places.
-constexpr int few_misc(int columns) { return 512 + columns * 4 * 18; }
+constexpr int few_misc(int columns) { return 512 + columns * 64; }
 constexpr int kPromptMisc = 512;
 
 // Fixed shared memory behind the ring: weights of a leaf (two bf16 terms), two items' queries,
