@@ -251,10 +251,13 @@ __device__ __forceinline__ void tmem_st(uint32_t a, const float (&v)[N])
 // is below that of fp32 sums' order.
 //
 // What bounds it: with 16 columns the bytes of K and V (64 sequences of 8192 keys, 8 kv heads of
-// 128: 246 us, 98 % of the rate of a copy; the tensor cores are busy for 7 %), of a few thousand
-// keys the chain of two launches, the first loads and the join (4100 keys: 14 us, of which the
-// bytes are 2.5), with 64 columns the weights (13 tokens of 8 heads over 131000 keys: 104 us, the
-// bytes 40: 64 x 256 exponentials, each split in two terms, a leaf of 128 KB).
+// 128: 245 us, 97 % of the rate of a copy; the tensor cores are busy for 7 %), of a few thousand
+// keys the chain of two launches, the first loads and the join (4100 keys: 11.7 us, of which the
+// bytes are 2.5), with 64 columns shared memory (13 tokens of 8 heads over 131000 keys: 95 us, the
+// bytes 40: of a leaf products read 224 KB there, 128 arrive and weights are 64, 3300 of its
+// 5000 cycles at 128 bytes each). What the chain of a leaf costs was mostly waits and meetings:
+// every warp forms the references for itself (one meeting a leaf instead of two), barriers are
+// asked ahead of their waits (104 us to 95; one token 13.9 to 11.7 with the masks below).
 //
 // Order. A work item is a unit of 256, 512 or 1024 keys (see few_plan), from a multiple of
 // that on, in leaves of 256, whose products are added in the order of keys. A column's reference
@@ -883,7 +886,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attend_join(const AttendParam
 // memory, two tiles of keys): the tensor cores work on one while the weights of the
 // other are formed. What bounds it is the products, 4 x head_dim operations for each pair of
 // row and key, and the loads of scores from tensor memory, which wait for them (64 columns: 650
-// to 880 cycles while products run). Six prompts of 8192 tokens, 40 heads of 128: 1918 us, 64 % of
+// to 880 cycles while products run). Six prompts of up to 8192 tokens, 40 heads of 128: 1910 us, 64 % of
 // the measured rate of bf16 products, counting the pairs that are seen alone; 8000 tokens of 16
 // heads of 256 with a window of 1024: 157 us. (One thread for a row took 2 to 7 % longer. Some
 // of the exponentials by polynomials: slower, the exponentials' unit is busy for 28 %.)

@@ -112,8 +112,8 @@ inline FewPlan few_plan(int B, int max_new, int heads, int kv_heads, int D, int6
     f.blocks = (most + f.tokens - 1) / f.tokens;
     f.rows = f.tokens * group;
     // An item is two leaves; one where that makes a sequence no more items than a card has
-    // SMs (one token over 4100 keys: 14.4 us with two, 13.8 with one), four where it makes
-    // it eight times as many (13 tokens over 131000 keys: 142 us with two, 104 with four). By
+    // SMs (one token over 4100 keys: 12.2 us with two, 11.7 with one), four where it makes
+    // it eight times as many (13 tokens over 131000 keys: 119 us with two, 95 with four). By
     // the longest sequence that the call has room for, not by how long they are nor by how
     // many there are, so that a row's sums keep their order from call to call.
     const int64_t sees = window && int64_t(window) + sinks + kFew < capacity ? int64_t(window) + sinks + kFew : capacity;
