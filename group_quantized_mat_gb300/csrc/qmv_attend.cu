@@ -252,7 +252,7 @@ __device__ __forceinline__ void tmem_st(uint32_t a, const float (&v)[N])
 //
 // What bounds it: with 16 columns the bytes of K and V (64 sequences of 8192 keys, 8 kv heads of
 // 128: 245 us, 97 % of the rate of a copy; the tensor cores are busy for 7 %), of a few thousand
-// keys the chain of two launches, the first loads and the join (4100 keys: 11.7 us, of which the
+// keys the chain of two launches, the first loads and the join (4100 keys: 11.2 us, of which the
 // bytes are 2.5), with 64 columns shared memory (13 tokens of 8 heads over 131000 keys: 95 us, the
 // bytes 40: of a leaf products read 224 KB there, 128 arrive and weights are 64, 3300 of its
 // 5000 cycles at 128 bytes each). What the chain of a leaf costs was mostly waits and meetings:
@@ -818,6 +818,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attend_join(const AttendParam
 {
     constexpr int E = D / 32;
     __shared__ float s_sum[kJoinWarps][D], s_total[kJoinWarps], s_top[kJoinWarps];
+    grid_launch_dependents();  // (what comes next waits for this kernel's end, and so for attend_few's)
     // (what is read here was there before attend_few began)
     const int few = min(p.max_new, kFew), b = int(blockIdx.x) / few, i = int(blockIdx.x) - b * few, h = blockIdx.y;
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
@@ -1500,6 +1501,7 @@ template <int D>
 __global__ void __launch_bounds__(256) attend_join_pieces(const AttendParams p)
 {
     constexpr int E = D / 32, STREAMS = D == 256 ? 1 : 2;
+    grid_launch_dependents();
     grid_dependency_wait();
     const int64_t unit = int64_t(blockIdx.x) * 8 + threadIdx.x / 32;
     const int lane = threadIdx.x & 31, t = int(unit / p.heads), h = int(unit % p.heads), each = STREAMS * p.tokens;
