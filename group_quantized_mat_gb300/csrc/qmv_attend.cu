@@ -868,8 +868,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attend_join(const AttendParam
     }
     const bool none = total == 0.0f;
     const int64_t row = s.row + i;
+    // (times the reciprocal, as attend_few does where a row has one unit: a token that has one alone
+    // has two with drafts behind it, and its bits are to be the same)
     if (threadIdx.x < D)
-        reinterpret_cast<__nv_bfloat16 *>(p.out)[row * p.ld_out + h * D + threadIdx.x] = __float2bfloat16_rn(none ? 0.0f : __fdiv_rn(o, total));
+        reinterpret_cast<__nv_bfloat16 *>(p.out)[row * p.ld_out + h * D + threadIdx.x] = __float2bfloat16_rn(none ? 0.0f : __fmul_rn(o, __fdiv_rn(1.0f, total)));
     if (p.lse && threadIdx.x == 0)
         p.lse[row * p.heads + h] = none ? -INFINITY : __fmul_rn(0.6931471805599453f, __fadd_rn(all, log2f(total)));
 }

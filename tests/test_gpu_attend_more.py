@@ -72,6 +72,19 @@ def test_unseen_keys_of_pages_that_are_seen(new, window, sinks):
     b.check(b.run(window=window, sinks=sinks), window=window, sinks=sinks)
 
 
+@pytest.mark.parametrize("drafts", [1, 5])
+def test_drafts_that_begin_a_part_of_their_own(drafts):
+    """A token whose keys are one part of the work by themselves, and two with the drafts behind it: the same bits, also
+    where a result is close to the middle of two bf16 (2 million of them: a last bit of fp32 shows in some)."""
+    B, heads = 512, 32
+    p = Problem([1 + drafts] * B, [256 + drafts] * B, heads, 1, 128, page=16, seed=28)
+    out, lse = p.run()
+    one = Problem([1] * B, [256] * B, heads, 1, 128, page=16, seed=0)
+    one.k, one.v, one.pages, one.most, one.table = p.k, p.v, p.pages, p.most, p.table
+    one.q = p.q[::1 + drafts].contiguous()
+    assert same((out[::1 + drafts], lse[::1 + drafts]), one.run())
+
+
 @pytest.mark.parametrize("heads,kv,D", [(8, 2, 128), (4, 4, 64), (10, 2, 256)])
 @pytest.mark.parametrize("new,keys", [([1, 3], [5, 700]), ([2, 16], [2, 6000]), ([40, 300], [700, 300]), ([33], [9000])])
 def test_queries_that_are_not_numbers(heads, kv, D, new, keys):
