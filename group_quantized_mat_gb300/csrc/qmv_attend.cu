@@ -37,7 +37,7 @@ struct AttendParams {
     float *lse;
     int B, T, max_new, heads, kv_heads, group;
     int page_size, pages, max_pages;
-    uint64_t page_magic;  // ceil(2^42 / page_size)
+    uint64_t magic;       // of page_size: see page_of
     int map_code;         // of the largest boxes in use
     float scale;
     int window, sinks;
@@ -81,9 +81,6 @@ struct Seen {
     // Does it hold for a key of key .. key + n - 1?
     __device__ __forceinline__ bool any(int key, int n) const { return key < end && (key + n > low || key < sinks); }
 };
-
-// The page of a key, key / page_size: exact for keys below 2^26 and page sizes up to 2^16.
-__device__ __forceinline__ int page_of(const AttendParams &p, int key) { return int(uint64_t(unsigned(key)) * p.page_magic >> 42); }
 
 // Bits 0 .. n - 1.
 __device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
@@ -174,7 +171,7 @@ struct Boxes {
 
     __device__ __forceinline__ void find(const AttendParams &p, const Seen &seen, const int32_t *table, int first, int lane, int lanes)
     {
-        const int key = first + 8 * lane, row = page_of(p, key), at = key - row * p.page_size;
+        const int key = first + 8 * lane, row = page_of(p.magic, key), at = key - row * p.page_size;
         const int before = min(lane & 7, at / 8), all = before + min(8 - (lane & 7), (p.page_size - at) / 8);
         code = -1;
 #pragma unroll
@@ -1668,7 +1665,7 @@ extern "C" qmv_status qmv_attend_run(const uint16_t *q, const uint16_t *k_cache,
     uint8_t *at = static_cast<uint8_t *>(ws);
     p.meta = reinterpret_cast<float2 *>(at + f.meta_off);
     p.parts = reinterpret_cast<float *>(at + f.parts_off);
-    p.page_magic = ((uint64_t(1) << 42) + page_size - 1) / page_size;
+    p.magic = page_magic(page_size);
     // Keys and values by boxes of 64 elements and 64 keys at most: one size where pages are
     // a power of two or multiples of 64, else all that fit a page.
     Maps m;

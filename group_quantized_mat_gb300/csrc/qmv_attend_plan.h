@@ -1,5 +1,6 @@
 // The launch plan of qmv_attend_run: tiles, what lies where in shared memory and in
-// the workspace. Host code without a CUDA call, so that plans can be checked without a GPU.
+// the workspace, and the division of keys into pages. Code without a CUDA call, so that
+// it can be checked without a GPU.
 #pragma once
 
 #include <cstddef>
@@ -7,8 +8,26 @@
 
 #include "qmv.h"
 
+#ifdef __CUDACC__
+#define QMV_BOTH __host__ __device__ __forceinline__
+#else
+#define QMV_BOTH inline
+#endif
+
 namespace qmv {
 namespace attend {
+
+// The page of a key, key / page_size, for keys that are multiples of 8. Page sizes are multiples
+// of 8 too, so eighths are divided: with e = page_size / 8 up to 2^13 the magic number is
+// (2^37 + r) / e, r < e, and n r < 2^37 for n eighths below 2^24, so that r adds less than 1 / e to
+// the quotient; the product stays below 2^62. (That of whole keys and a magic number for them
+// passes 64 bits from key 2^25 on, with pages of 8.)
+inline uint64_t page_magic(int page_size)
+{
+    const uint64_t e = uint64_t(page_size) / 8;
+    return ((uint64_t(1) << 37) + e - 1) / e;
+}
+QMV_BOTH int page_of(uint64_t magic, int key) { return int(uint64_t(unsigned(key) >> 3) * magic >> 37); }
 
 constexpr int kFew = QMV_TILE_M;  // new tokens of a sequence up to which they share one read of its keys
 constexpr int kLeaf = 256;        // keys whose weights are formed at once: two tiles of 128
