@@ -1439,14 +1439,18 @@ __global__ void __launch_bounds__(prompt_threads(D), 1)
             if (worked) sums_in();
             tmem_fence_after();
             // The other half's total, by the first column of either half's sums, which is kept
-            // meanwhile. (The scores' place may have the next item's already.)
-            const float kept = tmem_ld1(mine);
-            tile::tmem_st1(mine, sum);
-            tmem_wait_st();
-            tmem_fence_before();
-            named_sync(4 + x, kMeetRows);
-            tmem_fence_after();
-            {
+            // meanwhile. (The scores' place may have the next item's already.) Both halves have one
+            // only of an item with a tile for the stream, which all of its threads agree on. A half
+            // may store the next item's total only when the other has loaded this one: between
+            // the two lies a meeting at a tile's maxima, so an item without a tile must not store.
+            float kept = 0.0f;
+            if (worked) {
+                kept = tmem_ld1(mine);
+                tile::tmem_st1(mine, sum);
+                tmem_wait_st();
+                tmem_fence_before();
+                named_sync(4 + x, kMeetRows);
+                tmem_fence_after();
                 const float theirs = tmem_ld1(O + lanes + x * D + (1 - half) * (D / 2));
                 sum = half ? __fadd_rn(theirs, sum) : __fadd_rn(sum, theirs);
             }
