@@ -44,8 +44,10 @@ struct AttendParams {
     int64_t ld_out;
     unsigned *err;
     // the plan, and the workspace's parts
-    int items;  // that have a place in the workspace
-    int tokens, blocks, rows, units, unit_shift, pieces, slots, key_slots, q_sets;
+    int items;  // at most
+    bool by_row;
+    int kept;   // rows whose sums have a place
+    int tokens, rows, units, unit_shift, pieces, slots, key_slots, q_sets;
     int p_off, q_off, misc_off;
     int32_t *prefix;
     float2 *meta;
@@ -265,7 +267,8 @@ __device__ __forceinline__ void tmem_st(uint32_t a, const float (&v)[N])
 // on how many SMs there are.
 
 struct Item {
-    int b, g, block, unit, index;  // index: of the partial sums
+    int b, g, block, unit;
+    uint32_t part;                 // of its first row's sums
     int row, tokens, rows;         // first row of q, its tokens and columns
     int pos;                       // position of the first token; of the last: pos + tokens - 1
     int leaf, leaves;
@@ -292,15 +295,17 @@ struct Sequences {
     const int4 *kept;      // [B]
 };
 
-// Where an item's sums lie in the workspace.
-__device__ __forceinline__ int part_of(const AttendParams &p, int b, int u, int block, int g)
+// Where the sums of token i of sequence b, at the given row of q, lie in the workspace, in groups of
+// heads: units, then kv heads, then rows, so that an item's columns lie together. (By rows of q
+// there are T places; where 16 for each sequence are fewer, those. Fewer than 2^32 in all, as
+// a workspace of at most 2^40 bytes has 264 or more for each.)
+__device__ __forceinline__ uint32_t part_of(const AttendParams &p, int b, int row, int i, int u, int g)
 {
-    return ((b * p.units + u) * p.blocks + block) * p.kv_heads + g;
+    return uint32_t(u * p.kv_heads + g) * uint32_t(p.kept) + uint32_t(p.by_row ? row : b * min(p.max_new, kFew) + i);
 }
 
-// Counts first[1 .. B] become running sums from first[0] = 0 on, at most `most` (that
-// many items have a place; more are there only if rows belong to several sequences); by one
-// warp.
+// Counts first[1 .. B] become running sums from first[0] = 0 on, at most `most` (more are there
+// only if rows belong to several sequences; of prompts that many have a place); by one warp.
 __device__ __forceinline__ void sum_firsts(int32_t *first, int B, int most, int lane)
 {
     int64_t sum = 0;
@@ -340,9 +345,9 @@ __device__ __forceinline__ Item item_at(const AttendParams &p, const Sequences &
     }
     const int u = int(unsigned(index) / unsigned(p.kv_heads));
     it.g = index - u * p.kv_heads;
-    it.index = part_of(p, lo, u, it.block, it.g);
     it.unit = units.place(u);
     it.row = s.row + it.block * p.tokens;
+    it.part = part_of(p, lo, it.row, it.block * p.tokens, u, it.g);
     it.tokens = min(p.tokens, s.done - it.block * p.tokens);
     it.rows = it.tokens * p.group;
     it.pos = s.pos + it.block * p.tokens;
@@ -761,7 +766,7 @@ __global__ void __launch_bounds__(few_threads(NC), D < 256 && NC == 16 ? 2 : 1)
                     if (p.lse)
                         p.lse[int64_t(it.row + token) * p.heads + it.g * p.group + head] = none ? -INFINITY : __fmul_rn(0.6931471805599453f, __fadd_rn(ref, log2f(t)));
                 } else {
-                    p.meta[int64_t(it.index) * p.rows + r] = make_float2(ref, t);
+                    p.meta[int64_t(it.part) * p.group + r] = make_float2(ref, t);
                 }
             }
             if (it.leaves > 0) wait(o_done, (leaf - 1) & 1);
@@ -783,7 +788,7 @@ __global__ void __launch_bounds__(few_threads(NC), D < 256 && NC == 16 ? 2 : 1)
                 }
                 const int left = it.rows - c0;
                 if (!it.whole) {
-                    float *to = p.parts + (int64_t(it.index) * p.rows + c0) * D + d;
+                    float *to = p.parts + (int64_t(it.part) * p.group + c0) * D + d;
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
                         if (i < left) to[i * D] = __fadd_rn(a[i], b[i]);
@@ -821,7 +826,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attend_join(const AttendParam
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
     const Sequence s(p, b);
     const Units units(p, s);
-    const int g = h / p.group, block = i / p.tokens, row_in = (i - block * p.tokens) * p.group + h - g * p.group;
+    const int g = h / p.group, head = h - g * p.group;
     grid_dependency_wait();
     if (i >= s.done || units.count <= 1) return;
     // units whose places are the warp's, of the first tokens and of the others
@@ -834,7 +839,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attend_join(const AttendParam
         int u = from + ((warp - units.place(from)) & (kJoinWarps - 1));
 #pragma unroll 4
         for (; u < to; u += kJoinWarps) {
-            const int64_t at = int64_t(part_of(p, b, u, block, g)) * p.rows + row_in;
+            const int64_t at = int64_t(part_of(p, b, s.row + i, i, u, g)) * p.group + head;
             const float2 m = __ldcg(p.meta + at);
             float v[E];
 #pragma unroll
@@ -1601,7 +1606,7 @@ qmv_status check_attend(int B, int T, int max_new, int heads, int kv_heads, int 
         window < 0 || window > (1 << 30) || sinks < 0 || sinks > (1 << 30))
         return QMV_ERR_SHAPE;
     const int64_t capacity = int64_t(max_pages) * page_size;
-    const FewPlan f = few_plan(B, max_new, heads, kv_heads, head_dim, capacity, window, sinks);
+    const FewPlan f = few_plan(B, T, max_new, heads, kv_heads, head_dim, capacity, window, sinks);
     const PromptPlan g = prompt_plan(B, T, max_new, heads, kv_heads, head_dim, capacity, window, sinks);
     return f.workspace + g.workspace > (size_t(1) << 40) || f.items >= (int64_t(1) << 31) || g.items >= (int64_t(1) << 31) ? QMV_ERR_SHAPE : QMV_OK;
 }
@@ -1615,7 +1620,7 @@ extern "C" size_t qmv_attend_workspace_size(int B, int T, int max_new, int heads
     if (qmv::check_attend(B, T, max_new, heads, kv_heads, head_dim, page_size, max_pages, window, sinks) != QMV_OK) return 0;
     // (the two kinds of sequences run one after the other, each with the whole of it)
     const int64_t capacity = int64_t(max_pages) * page_size;
-    const size_t few = qmv::attend::few_plan(B, max_new, heads, kv_heads, head_dim, capacity, window, sinks).workspace;
+    const size_t few = qmv::attend::few_plan(B, T, max_new, heads, kv_heads, head_dim, capacity, window, sinks).workspace;
     const size_t prompt = qmv::attend::prompt_plan(B, T, max_new, heads, kv_heads, head_dim, capacity, window, sinks).workspace;
     return few > prompt ? few : prompt;
 }
@@ -1660,9 +1665,11 @@ extern "C" qmv_status qmv_attend_run(const uint16_t *q, const uint16_t *k_cache,
     p.ld_out = ld_out;
     p.kv_heads = kv_heads;
     p.err = dev.err;
-    const FewPlan f = few_plan(B, max_new, heads, kv_heads, head_dim, int64_t(max_pages) * page_size, window, sinks);
+    const FewPlan f = few_plan(B, T, max_new, heads, kv_heads, head_dim, int64_t(max_pages) * page_size, window, sinks);
     p.items = int(f.items);
-    p.tokens = f.tokens; p.blocks = f.blocks; p.rows = f.rows; p.units = f.units;
+    p.by_row = f.by_row;
+    p.kept = f.kept;
+    p.tokens = f.tokens; p.rows = f.rows; p.units = f.units;
     p.unit_shift = f.unit == kLeaf ? 8 : f.unit == 2 * kLeaf ? 9 : 10;
     p.slots = f.slots; p.key_slots = f.key_slots; p.q_sets = f.q_sets;
     p.p_off = f.p_off; p.q_off = f.q_off; p.misc_off = f.misc_off;

@@ -47,6 +47,8 @@ struct FewPlan {
     int unit;     // keys of one item, from a multiple of it on
     int units;    // of a sequence at most
     int64_t items;
+    bool by_row;  // where a token's sums lie: by its row of q, or by its sequence's place
+    int kept;     // tokens whose sums the workspace has room for
     size_t meta_off, parts_off, workspace;
 };
 
@@ -121,6 +123,17 @@ inline PromptPlan prompt_plan(int B, int T, int max_new, int heads, int kv_heads
     return f;
 }
 
+// The workspace of `rows` tokens: sums of each token, unit and head.
+inline void few_sums(FewPlan &f, int64_t rows, int heads, int D)
+{
+    const size_t sums = size_t(rows) * f.units * heads;
+    f.kept = int(rows);
+    f.meta_off = 0;
+    f.parts_off = up256(sums * 8);
+    f.workspace = f.units > 1 ? f.parts_off + up256(sums * D * 4) : 256;  // (0 would be a refusal)
+}
+
+// (whatever T is)
 inline FewPlan few_plan(int B, int max_new, int heads, int kv_heads, int D, int64_t capacity, int window, int sinks)
 {
     FewPlan f{};
@@ -148,9 +161,20 @@ inline FewPlan few_plan(int B, int max_new, int heads, int kv_heads, int D, int6
     f.items = int64_t(B) * kv_heads * f.blocks * units;
     // (a ring that holds a whole leaf where every item has an SM for itself)
     few_smem(f, D, B, f.items <= 152);
-    f.meta_off = 0;
-    f.parts_off = up256(size_t(f.items) * f.rows * 8);
-    f.workspace = f.units > 1 ? f.parts_off + up256(size_t(f.items) * f.rows * D * 4) : 256;  // (0 would be a refusal)
+    f.by_row = false;
+    few_sums(f, int64_t(B) * f.blocks * f.tokens, heads, D);
+    return f;
+}
+
+// The plan of a call of T rows. Their number bounds what sequences of few tokens have, and kFew for
+// each sequence does: 255 sequences of one token and a prompt of 512 rows are 767 rows and not
+// 4096 (keys for 131072 of them, 40 heads of 128: 2.0 GB of sums, not 16).
+inline FewPlan few_plan(int B, int T, int max_new, int heads, int kv_heads, int D, int64_t capacity, int window, int sinks)
+{
+    FewPlan f = few_plan(B, max_new, heads, kv_heads, D, capacity, window, sinks);
+    const int64_t most = int64_t(B) * (max_new < kFew ? max_new : kFew);
+    f.by_row = T <= most;
+    few_sums(f, f.by_row ? T : most, heads, D);
     return f;
 }
 

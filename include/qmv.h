@@ -537,8 +537,11 @@ QMV_API qmv_status qmv_rope_run(const void *qkv, const uint16_t *q_norm, const u
  * rounded to bf16 (their sum is not), and the order of a row's sums may depend on T,
  * B and max_new as well. Calls repeat bit for bit.
  *
- * The workspace holds sums of parts of the keys: about 4 heads head_dim / 512 bytes of
- * them for each key that max_pages (or the window) allows and each new token.
+ * The workspace holds sums of parts of the keys, 4 head_dim + 8 bytes for each head of a row
+ * and part. Of few new tokens it has room for T rows, or for min(max_new, 16) of each
+ * sequence where those are fewer, and for each unit of 256, 512 or 1024 keys that max_pages (or
+ * the window) allows; of prompts for up to 1216 parts of 256 rows of one head (128 of head_dim
+ * 256). The two share it.
  *
  * Errors: QMV_ERR_NULL, QMV_ERR_COUNT (B, T, max_new, heads, kv_heads), QMV_ERR_SHAPE
  * (head_dim, page_size, pages, max_pages, scale, window, sinks, strides), QMV_ERR_FLAGS,
