@@ -907,7 +907,7 @@ struct PromptItem {
     int b, g, index;
     int row, tok, tokens;  // first row of q, first token of the sequence, tokens
     int pos;               // of the first token
-    int keys;
+    int end;               // behind the last key that the sequence's computed queries see
     int sinks, low;        // tiles of the first tokens; first tile of the others
     int low_all;           // the first key that the sequence's queries see behind the first tokens
     int from, to;          // of the list of tiles
@@ -957,7 +957,7 @@ __device__ __forceinline__ PromptItem prompt_at(const AttendParams &p, const Seq
     it.tokens = min(each, s.done - it.tok);
     it.row = s.row + it.tok;
     it.pos = s.pos + it.tok;
-    it.keys = s.keys;
+    it.end = s.pos + s.done;
     const Tiles tiles(p, it.pos, it.pos + it.tokens - 1);
     it.sinks = tiles.sinks;
     it.low = tiles.low;
@@ -1123,12 +1123,12 @@ __global__ void __launch_bounds__(prompt_threads(D), 1)
                 boxes.find(p, seen, table, it.tile(i) * 128, lane, 16);
                 if (!values && lane == 0) sh.there[brought & 7] = boxes.there;
                 // Values that no query of the sequence sees may be anything, and 0 x NaN is NaN:
-                // zeros in their place, behind its keys, before its window and behind its first tokens.
+                // zeros in their place, behind the last one seen, before its window and behind its first tokens.
                 const int chunks = values ? VC : KC;
 #pragma unroll 1
                 for (int c = 0; c < chunks; ++c, ++at.issued, at.step()) {
                     const int key0 = it.tile(i) * 128 + c * VK;
-                    const bool zeros = values && (key0 + VK > it.keys || (key0 < it.low_all && key0 + VK > min(p.sinks, it.low_all)));
+                    const bool zeros = values && (key0 + VK > it.end || (key0 < it.low_all && key0 + VK > min(p.sinks, it.low_all)));
                     if (ok && at.full()) ok = wait(empty0 + 8 * at.slot, at.lap ^ 1);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
@@ -1157,7 +1157,7 @@ __global__ void __launch_bounds__(prompt_threads(D), 1)
 #pragma unroll 1
                         for (int e = lane; e < VK * 8; e += 32) {
                             const int key = key0 + e / 8;
-                            if (key < it.keys && (key >= it.low_all || key < p.sinks)) continue;
+                            if (key < it.end && (key >= it.low_all || key < p.sinks)) continue;
                             for (int d = 0; d < DB; ++d) sts_v4_u32(dst + d * VK * 128 + e * 16, make_uint4(0, 0, 0, 0));
                         }
                         fence_proxy_async_smem();

@@ -45,3 +45,19 @@ def test_parts_without_keys(heads, kv, D):
     check_rows(p, got, 1, 0, 17)
     for _ in range(10):
         assert same(p.run(d), got)
+
+
+@pytest.mark.parametrize("heads,kv,D", [(4, 2, 128), (4, 1, 64), (2, 2, 256)])
+@pytest.mark.parametrize("new,keys,most", [([5, 2], [100, 50], 3), ([40, 2], [100, 50], 20), ([300, 31], [900, 400], 150)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (60, 3)])
+def test_keys_of_rows_that_are_not_computed(heads, kv, D, new, keys, most, window, sinks):
+    """Of a sequence with more rows than max_new the last rows' own keys are seen by no query: whatever they hold, it has no
+    influence."""
+    a, b = (Problem(new, keys, heads, kv, D, page=48, seed=43) for _ in range(2))
+    for s, n in enumerate(new):
+        for j in range(keys[s] - n + min(n, most), keys[s]):
+            for c in (a.k, a.v):
+                c[a.table[s, j // 48], j % 48] = math.nan if j % 2 else -math.inf
+    got = a.run(max_new=most, window=window, sinks=sinks)
+    assert same(got, b.run(max_new=most, window=window, sinks=sinks))
+    b.check(got, max_new=most, window=window, sinks=sinks)
