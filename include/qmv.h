@@ -481,8 +481,10 @@ QMV_API qmv_status qmv_verify_run(const void *target, const void *draft, const i
  *
  * Arithmetic: fp32, rounded once. An angle is reduced to a fraction of a turn in 64-bit
  * fixed point, so that far positions keep their fraction (an error of at most
- * |position| 2^-50 radians and 2^-24 of a turn). A token's result does not depend on the
- * other tokens of the call.
+ * |position| max(1, |inv_freq|) 2^-50 radians and 2^-24 of a turn). A token's result does
+ * not depend on the other tokens of the call. The squares of a norm and their mean are fp32 as
+ * well: where they leave its range (elements past 1e18, or below 1e-19 without an eps)
+ * the norm is that of an infinity or of 0.
  *
  * Errors: QMV_ERR_NULL, QMV_ERR_COUNT (T, heads, kv_heads, axes), QMV_ERR_SHAPE (head_dim,
  * rope_dim, page_size, pages, strides, eps), QMV_ERR_FLAGS, QMV_ERR_ALIGN, QMV_ERR_CUDA. */
