@@ -12,7 +12,9 @@ keys stay in the cache behind the sequence's length, where nothing reads them un
 are written over. The step is captured in a CUDA graph.
 
 The emitted tokens are those of decoding one token at a time, bit for bit: no operator's
-result for a token depends on the tokens drafted with it.
+result for a token depends on the tokens drafted with it. That holds for up to 16 tokens
+of a sequence in a step, the last one and 15 drafted ones, and for caches with room for as
+many keys (qmv_attend_run); a step takes 256 rows in all (qmv_run).
 """
 
 import argparse
@@ -52,8 +54,12 @@ class Decoder:
     """`batch` sequences of up to `room` tokens, `drafts` drafted ones a step."""
 
     def __init__(self, model, batch, room, drafts, page=16):
+        if not 0 <= drafts < g.QMV_TILE_M:
+            raise ValueError(f"{drafts} drafted tokens: 0 to {g.QMV_TILE_M - 1}, as those of more are not bit for bit those of single tokens")
+        if not 1 <= batch * (drafts + 1) <= g.QMV_MAX_M:
+            raise ValueError(f"{batch} sequences of {drafts + 1} tokens a step: 1 to {g.QMV_MAX_M} rows")
         self.model, self.B, self.S, self.page = model, batch, drafts, page
-        self.per = -(-(room + drafts + 1) // page)
+        self.per = -(-(room + g.QMV_TILE_M) // page)  # (whatever `drafts` is: sums are divided by the room)
         self.pages = batch * self.per
         shape = (self.pages, page, model.kv_heads, model.head_dim)
         self.k, self.v = (torch.empty(shape, dtype=torch.bfloat16, device="cuda") for _ in range(2))
@@ -137,7 +143,7 @@ def main():
     model = Model(window=a.window, sinks=a.sinks)
     tokens = torch.randint(0, model.vocab, (a.batch, a.prompt), generator=torch.Generator().manual_seed(1), dtype=torch.int32).cuda()
     for drafts in (0, a.drafts):
-        d = Decoder(model, a.batch, a.prompt + (drafts + 1) * a.tokens, drafts)
+        d = Decoder(model, a.batch, a.prompt + (a.drafts + 1) * a.tokens, drafts)
         d.prompt(tokens)
         torch.cuda.synchronize()
         t0 = time.perf_counter()
