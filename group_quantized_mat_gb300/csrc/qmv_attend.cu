@@ -1393,27 +1393,39 @@ __global__ void __launch_bounds__(prompt_threads(D), 1)
                 // above the largest score, and kept while it is
                 const bool moves = m > ref;
                 const float now = moves ? __fadd_rn(ceilf(m), 8.0f) : ref;
-                if (__any_sync(0xffffffffu, moves && ref != -INFINITY)) {
-                    const float f = moves && ref != -INFINITY ? power_of_two(__fsub_rn(ref, now)) : 1.0f;
-                    sums_in();
-                    tmem_fence_after();
-#pragma unroll 1
-                    for (int c = 0; c < D / 2; c += 16) {
-                        float o[16];
-                        tmem_ld<16>(mine + c, o);
-                        tmem_wait_ld();
-                        settle(o);
+                use = now == -INFINITY ? 0.0f : now;
+                // A row whose scores reach 2^29 rounds them as its maximum is rounded: the exact products may
+                // lie further from it than an exponential can hold. (Each row by itself: what a row
+                // without a query has here is left over from before.)
+                const bool huge = real && fabsf(m) >= 0x1p29f && m != -INFINITY, rescale = moves && ref != -INFINITY;
+                if (__any_sync(0xffffffffu, rescale || huge)) {
+                    if (huge) {
 #pragma unroll
-                        for (int k = 0; k < 16; ++k) o[k] = __fmul_rn(o[k], f);
-                        tmem_st<16>(mine + c, o);
+                        for (int k = 0; k < 64; ++k) s[k / 32][k & 31] = __fmul_rn(__fsub_rn(__fmul_rn(s[k / 32][k & 31], c2), use), __frcp_rn(c2));
+                        use = 0.0f;
                     }
-                    tmem_wait_st();
-                    const uint64_t ff = tile::pack2(f, f);
-                    total[0] = tile::mul2(total[0], ff);
-                    total[1] = tile::mul2(total[1], ff);
+                    __syncwarp();
+                    if (__any_sync(0xffffffffu, rescale)) {
+                        const float f = rescale ? power_of_two(__fsub_rn(ref, now)) : 1.0f;
+                        sums_in();
+                        tmem_fence_after();
+#pragma unroll 1
+                        for (int c = 0; c < D / 2; c += 16) {
+                            float o[16];
+                            tmem_ld<16>(mine + c, o);
+                            tmem_wait_ld();
+                            settle(o);
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) o[k] = __fmul_rn(o[k], f);
+                            tmem_st<16>(mine + c, o);
+                        }
+                        tmem_wait_st();
+                        const uint64_t ff = tile::pack2(f, f);
+                        total[0] = tile::mul2(total[0], ff);
+                        total[1] = tile::mul2(total[1], ff);
+                    }
                 }
                 ref = now;
-                use = ref == -INFINITY ? 0.0f : ref;
                 const uint64_t minus = tile::pack2(-use, -use);
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {

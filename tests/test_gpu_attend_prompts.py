@@ -61,3 +61,42 @@ def test_keys_of_rows_that_are_not_computed(heads, kv, D, new, keys, most, windo
     got = a.run(max_new=most, window=window, sinks=sinks)
     assert same(got, b.run(max_new=most, window=window, sinks=sinks))
     b.check(got, max_new=most, window=window, sinks=sinks)
+
+
+@pytest.mark.parametrize("heads,kv,D", [(4, 2, 128), (4, 1, 64), (2, 2, 256)])
+@pytest.mark.parametrize("new,keys", [([5], [700]), ([40], [700]), ([300, 20], [300, 2100])])
+@pytest.mark.parametrize("size,scale", [(2.0 ** 13, None), (2.0 ** 15, 1.0), (2.0 ** 17, 1.0), (2.0 ** 17, -1.0), (2.0 ** 30, 0.5)])
+def test_scores_of_any_size(heads, kv, D, new, keys, size, scale):
+    """Queries of which some are so large that the softmax is a choice of the largest score: that key's value, whatever the size; the
+    others as ever."""
+    p = Problem(new, keys, heads, kv, D, seed=44)
+    p.k = torch.where(torch.isnan(p.k), p.k, (p.k.float() * size).bfloat16())
+    p.q[::2] = (p.q[::2].float() * size).bfloat16()
+    p.q[1::2] = (p.q[1::2].float() / size).bfloat16()
+    d = p.device()
+    out, lse = p.run(d, scale=scale)
+    assert torch.isfinite(out).all() and torch.isfinite(lse).all()
+    s = scale if scale is not None else D ** -0.5
+    chosen = 0
+    for b, n in enumerate(new):
+        for i in range(n):
+            t, L = p.start[b] + i, keys[b] - n + i + 1
+            j = torch.arange(L)
+            at = p.table[b].long()[j // p.page], j % p.page
+            k, v = (c[at].double().repeat_interleave(heads // kv, 1) for c in (p.k, p.v))
+            q = p.q[t].double()
+            z, S = torch.einsum("hd,lhd->lh", q, k) * s, (torch.einsum("hd,lhd->lh", q.abs(), k.abs()) * abs(s)).amax(0)
+            top, where = z.sort(0, descending=True)
+            for h in range(heads):
+                # a score is within (D + 16) steps of an accumulator of S; weights below 2^-200 are none
+                if t % 2 == 0 and L > 1 and float(top[0, h] - top[1, h]) > 2 * (D + 16) * 2.0 ** -23 * float(S[h]) + 200:
+                    chosen += 1
+                    # (one weight, rounded to bf16 in prompts while the total is not, then the result: (1 + 2^-8)^2)
+                    assert ((out[t, h].double() - v[where[0, h], h]).abs() <= (2.0 ** -7 + 2.0 ** -15) * v[where[0, h], h].abs()).all()
+                    assert abs(float(lse[t, h]) - float(top[0, h])) <= 2 * (D + 16) * 2.0 ** -23 * float(S[h])
+    assert chosen > 0.5 * heads * sum(n // 2 for n in new) or size < 2.0 ** 14
+    # the ordinary rows, by the formula
+    if size <= 2.0 ** 17:
+        y, z, oe, le = p.want(scale=scale)
+        rows = torch.arange(p.T) % 2 == 1
+        assert ((out.double() - y).abs()[rows] <= oe[rows] + 1e-30).all() and ((lse.double() - z).abs()[rows] <= le[rows]).all()
