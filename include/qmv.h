@@ -527,8 +527,8 @@ QMV_API qmv_status qmv_rope_run(const void *qkv, const uint16_t *q_norm, const u
  *  flags       0.
  *
  * A query that sees no key gives zeros, and -inf in lse. What lies in the cache
- * behind a sequence's keys, or in pages that no query of the sequence sees, has no
- * influence, whatever it holds. An infinity or NaN in a key or value that some query
+ * behind a sequence's keys, or that no query of the sequence sees, has no influence,
+ * whatever it holds. An infinity or NaN in a key or value that some query
  * of the sequence sees may reach other queries of the sequence in the call.
  *
  * Arithmetic: fp32 scores, maxima and sums; out is rounded once. Of a sequence of up to
@@ -537,7 +537,9 @@ QMV_API qmv_status qmv_rope_run(const void *qkv, const uint16_t *q_norm, const u
  * scale, window and sinks it is bit-identical to that of a call for this token alone (the
  * basis of exact verification, as in qmv_run). Of longer ones (prompts) the weights are
  * rounded to bf16 (their sum is not), and the order of a row's sums may depend on T,
- * B and max_new as well. Calls repeat bit for bit.
+ * B and max_new as well. Calls repeat bit for bit. Weighted values are summed before the
+ * division, with weights of at most 1: values past 3.4e38 over the number of keys seen
+ * may end as infinities.
  *
  * The workspace holds sums of parts of the keys, 4 head_dim + 8 bytes for each head of a row
  * and part. Of few new tokens it has room for T rows, or for min(max_new, 16) of each
@@ -567,10 +569,10 @@ QMV_API qmv_status qmv_workspace_init(void *workspace, size_t bytes, qmv_stream_
 /* ------------------------------------------------------------ diagnostics */
 
 /* Device-side error word of the current device: the one-vector kernel and the
- * operators of a decode step set bit 0 when a bounded wait (for a weight tile, a
- * tensor-core result, other CTAs) ran out, the one-vector kernel bit 1 when a launch
- * shape breaks its shared-memory ring protocol (neither happens with the
- * library's own launch plans; the output of that launch is then invalid).
+ * operators of a decode step and attention set bit 0 when a bounded wait (for a tile of
+ * weights, keys or values, a tensor-core result, other CTAs) ran out, the one-vector
+ * kernel bit 1 when a launch shape breaks its shared-memory ring protocol (neither
+ * happens with the library's own launch plans; the output of that launch is then invalid).
  * Synchronizes the device, stores the word in *word and clears it.
  * Errors: QMV_ERR_NULL, QMV_ERR_CUDA. */
 QMV_API qmv_status qmv_device_error(unsigned *word);
