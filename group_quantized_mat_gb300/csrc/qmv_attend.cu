@@ -896,8 +896,12 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attend_join(const AttendParam
 // heads of 256 with a window of 1024: 157 us. (One thread for a row took 2 to 7 % longer. Some
 // of the exponentials by polynomials: slower, the exponentials' unit is busy for 28 %.)
 //
-// m is a whole number as above, so that sums are rarely scaled, and exactly. The weights are
-// rounded to bf16 (2^-8 of each, as an operand next to bf16 values has to be); their total is not.
+// m is 8 above the largest score when it is set and moves when one passes it, so that sums are
+// rarely scaled. The weights are rounded to bf16 (2^-8 of each, as an operand next to bf16 values
+// has to be); their total is not. So m is not a whole number as above: the largest weight
+// of the tile that sets it is 2^-8, which bf16 has, and a key that a row sees nearly alone (a first
+// token that all look at, a row's only key) has no rounding: the error against 64 bits is then
+// that of the result's rounding, as in fp32 (0.0016 of the norm; 0.0023 with a whole number).
 //
 // Items go from a sequence's last rows, which see the most keys, to its first. Where there are
 // too few of them the keys are divided into pieces, which attend_join_pieces joins in
@@ -1390,9 +1394,9 @@ __global__ void __launch_bounds__(prompt_threads(D), 1)
                 tmem_fence_after();
                 m = fmaxf(m, tmem_ld1(other + 63));
                 m = __fmul_rn(m, c2);
-                // above the largest score, and kept while it is
+                // 8 above the largest score, and kept while it is above
                 const bool moves = m > ref;
-                const float now = moves ? __fadd_rn(ceilf(m), 8.0f) : ref;
+                const float now = moves ? __fadd_rn(m, 8.0f) : ref;
                 use = now == -INFINITY ? 0.0f : now;
                 // A row whose scores reach 2^29 rounds them as its maximum is rounded: the exact products may
                 // lie further from it than an exponential can hold. (Each row by itself: what a row
@@ -1406,7 +1410,7 @@ __global__ void __launch_bounds__(prompt_threads(D), 1)
                     }
                     __syncwarp();
                     if (__any_sync(0xffffffffu, rescale)) {
-                        const float f = rescale ? power_of_two(__fsub_rn(ref, now)) : 1.0f;
+                        const float f = rescale ? exp2_fast(__fsub_rn(ref, now)) : 1.0f;
                         sums_in();
                         tmem_fence_after();
 #pragma unroll 1
@@ -1545,7 +1549,7 @@ __global__ void __launch_bounds__(256) attend_join_pieces(const AttendParams p)
         for (int k = 0; k < pieces; ++k) {
             const int64_t at = first + int64_t(k) * STREAMS * 128;
             const float2 m = p.meta[at];
-            const float w = m.x == -INFINITY ? 0.0f : power_of_two(__fsub_rn(m.x, top));
+            const float w = m.x == -INFINITY ? 0.0f : exp2_fast(__fsub_rn(m.x, top));
             total = __fmaf_rn(m.y, w, total);
 #pragma unroll
             for (int e = 0; e < E; ++e) sum[e] = __fmaf_rn(p.parts[at * D + lane + 32 * e], w, sum[e]);

@@ -100,3 +100,34 @@ def test_scores_of_any_size(heads, kv, D, new, keys, size, scale):
         y, z, oe, le = p.want(scale=scale)
         rows = torch.arange(p.T) % 2 == 1
         assert ((out.double() - y).abs()[rows] <= oe[rows] + 1e-30).all() and ((lse.double() - z).abs()[rows] <= le[rows]).all()
+
+
+@pytest.mark.parametrize("heads,kv,D", [(4, 2, 128), (4, 1, 64), (2, 2, 256)])
+@pytest.mark.parametrize("new,keys", [([100], [128]), ([17, 128, 40], [17, 128, 120])])
+@pytest.mark.parametrize("sharp", [0.5, 3.0, 10.0])
+def test_the_largest_weight_has_no_rounding(heads, kv, D, new, keys, sharp):
+    """Rows whose keys lie in one tile: what the weights' rounding (2^-8 of each) may change is what the other keys than the
+    largest give; of a row with one key it is nothing."""
+    p = Problem(new, keys, heads, kv, D, seed=45, sharp=sharp)
+    out, lse = p.run()
+    p.check((out, lse))
+    for b, n in enumerate(new):
+        for i in range(n):
+            t, L = p.start[b] + i, keys[b] - n + i + 1
+            j = torch.arange(L)
+            at = p.table[b].long()[j // p.page], j % p.page
+            k, v = (c[at].double().repeat_interleave(heads // kv, 1) for c in (p.k, p.v))
+            q = p.q[t].double()
+            z, S = torch.einsum("hd,lhd->lh", q, k) * D ** -0.5, (torch.einsum("hd,lhd->lh", q.abs(), k.abs()) * D ** -0.5).amax(0)
+            w = torch.softmax(z, 0)
+            y, A = torch.einsum("lh,lhd->hd", w, v), torch.einsum("lh,lhd->hd", w, v.abs())
+            e = (D + 16) * 2.0 ** -23 * S + 16 * 2.0 ** -24
+            # (where two scores are so close that either may be the largest in 32 bits, no weight counts as it)
+            top = z.topk(min(L, 2), 0).values
+            clear = top[0] - top[-1] > 2 * e if L > 1 else torch.ones(heads, dtype=torch.bool)
+            least = w.masked_fill(clear & (torch.arange(L)[:, None] == w.argmax(0)), 0.0)
+            rest = torch.einsum("lh,lhd->hd", least, v.abs())
+            bound = 2.0 ** -8 * y.abs() + 2.0 ** -8 * rest + ((2 * e + (L + 64) * 2.0 ** -23)[:, None] * A) * (1 + 2.0 ** -7)
+            assert ((out[t].double() - y).abs() <= (1 + 2.0 ** -8) * bound + 1e-30).all()
+            if L == 1:
+                assert torch.equal(out[t].double(), v[0])
