@@ -250,11 +250,11 @@ __device__ __forceinline__ void tmem_st(uint32_t a, const float (&v)[N])
 // is below that of fp32 sums' order.
 //
 // What bounds it: with 16 columns the bytes of K and V (64 sequences of 8192 keys, 8 kv heads of
-// 128: 245 us, 97 % of the rate of a copy; the tensor cores are busy for 7 %), of a few thousand
-// keys the chain of two launches, the first loads and the join (4100 keys: 11.2 us, of which the
-// bytes are 2.5), with 64 columns shared memory (13 tokens of 8 heads over 131000 keys: 95 us, the
-// bytes 40: of a leaf products read 224 KB there, 128 arrive and weights are 64, 3300 of its
-// 5000 cycles at 128 bytes each). What the chain of a leaf costs was mostly waits and meetings:
+// 128: 247 us, 97 % of the rate of a copy; the tensor cores are busy for 7 %), of a few thousand
+// keys the chain of two launches, the first loads and the join (4100 keys: 11.3 us, of which the
+// bytes are 2.5), with 64 columns mostly shared memory (13 tokens of 8 heads over 131000 keys: 95 us,
+// the bytes 40: of a leaf products read 224 KB there, 128 arrive and weights are 64, 3300 of its
+// 5000 cycles at 128 bytes each; what the others go to is not known). What the chain of a leaf costs was mostly waits and meetings:
 // every warp forms the references for itself (one meeting a leaf instead of two), barriers are
 // asked ahead of their waits (104 us to 95; one token 13.9 to 11.7 with the masks below).
 //
@@ -891,9 +891,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attend_join(const AttendParam
 // memory, two tiles of keys): the tensor cores work on one while the weights of the
 // other are formed. What bounds it is the products, 4 x head_dim operations for each pair of
 // row and key, and the loads of scores from tensor memory, which wait for them (64 columns: 650
-// to 880 cycles while products run). Six prompts of up to 8192 tokens, 40 heads of 128: 1910 us, 64 % of
+// to 880 cycles while products run). Six prompts of up to 8192 tokens, 40 heads of 128: 1883 us, 65 % of
 // the measured rate of bf16 products, counting the pairs that are seen alone; 8000 tokens of 16
-// heads of 256 with a window of 1024: 157 us. (One thread for a row took 2 to 7 % longer. Some
+// heads of 256 with a window of 1024: 159 us; six prompts of 32 heads of 64: 1362 us, 36 %, as a
+// pair of row and key has as many exponentials and half the products. (One thread for a row took 2 to 7 % longer. Some
 // of the exponentials by polynomials: slower, the exponentials' unit is busy for 28 %.)
 //
 // m is 8 above the largest score when it is set and moves when one passes it, so that sums are
@@ -901,7 +902,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attend_join(const AttendParam
 // has to be); their total is not. So m is not a whole number as above: the largest weight
 // of the tile that sets it is 2^-8, which bf16 has, and a key that a row sees nearly alone (a first
 // token that all look at, a row's only key) has no rounding: the error against 64 bits is then
-// that of the result's rounding, as in fp32 (0.0016 of the norm; 0.0023 with a whole number).
+// that of the result's rounding, as in fp32 (0.0016 to 0.0017 of the norm; 0.0023 with a whole number).
 //
 // Items go from a sequence's last rows, which see the most keys, to its first. Where there are
 // too few of them the keys are divided into pieces, which attend_join_pieces joins in

@@ -15,9 +15,9 @@
 // is done with it, its norm's weights) stands before the loop over tokens.
 //
 // What bounds it: memory from a few thousand tokens on (16384 tokens of 40 + 16 heads of 128: 82
-// us, 86 % of the rate of a copy; before rows' places left the loop the instructions did, at
-// three a cycle), below that the latency of a launch, two loads and a store (one token: 2.5 us
-// in a graph, 6.5 with the host's call; 1155 tokens with three axes: 7.5 us, the bytes 3.6).
+// us, 86 % of the rate of a copy, from fp32 112 us, 94 %; before rows' places left the loop the instructions did, at
+// three a cycle), below that the latency of a launch, two loads and a store (one token: 2.1 us
+// in a graph, 6.5 with the host's call; 1155 tokens with three axes: 8.0 us, the bytes 3.6).
 //
 // A thread has four rows of a token in flight (two of fp32), or one where the tokens alone do
 // not fill the SMs (see launch_rope_rows).
